@@ -19,7 +19,8 @@ import torch
 
 from . import _build
 
-__all__ = ["sdpa_bwd", "sdpa_fwd", "workspace_size", "nvfp4_fake_quant", "sdpa_fwd_nvfp4_qat",
+__all__ = ["sdpa_bwd", "sdpa_fwd", "mask_plan", "MaskPlan", "rope_fwd", "rope_bwd", "rope_inv_freq",
+           "workspace_size", "nvfp4_fake_quant", "sdpa_fwd_nvfp4_qat",
            "sdpa_bwd_nvfp4_qat", "nvfp4_qat_workspace_size", "check_device_status", "debug_relay",
            "profile_enable", "profile_read", "library_path", "load", "SdpaError", "KERNEL_NAMES"]
 
@@ -74,6 +75,19 @@ def load(build_if_missing: bool = False):
     lib.sdpa_bwd_typed.restype = i
     lib.sdpa_fwd_typed.argtypes = [i] + list(lib.sdpa_fwd.argtypes[:-1]) + [vp, i, i, vp]
     lib.sdpa_fwd_typed.restype = i
+    lib.sdpa_fwd_scored.argtypes = [i] + list(lib.sdpa_fwd.argtypes[:-1]) + [ctypes.c_float, vp, vp, vp]
+    lib.sdpa_fwd_scored.restype = i
+    lib.sdpa_bwd_scored.argtypes = [i] + list(lib.sdpa_bwd.argtypes[:-1]) + [vp, vp, ctypes.c_float, vp, vp, vp]
+    lib.sdpa_bwd_scored.restype = i
+    lib.sdpa_mask_plan_size.argtypes = [i, i, i]
+    lib.sdpa_mask_plan_size.restype = sz
+    lib.sdpa_mask_plan_rows.argtypes = [vp, vp, i, i, i, vp, sz, vp]
+    lib.sdpa_mask_plan_rows.restype = i
+    lib.sdpa_mask_plan_docs.argtypes = [vp, vp, i, i, i, i, vp, sz, vp]
+    lib.sdpa_mask_plan_docs.restype = i
+    lib.sdpa_rope.argtypes = [i, vp, vp, vp, vp, i, i, i, i, i, ctypes.POINTER(ctypes.c_longlong), vp, i,
+                              ctypes.c_float, vp, i, i, i, i, vp]
+    lib.sdpa_rope.restype = i
     lib.sdpa_nvfp4_fake_quant.argtypes = [vp, vp, ctypes.c_longlong, vp]
     lib.sdpa_nvfp4_fake_quant.restype = i
     lib.sdpa_bwd_nvfp4_qat_workspace_size.argtypes = [i, i, i, i, i, i, i]
@@ -166,12 +180,12 @@ def _check_sink(sink, dsink, Hq):
     return dsink
 
 
-def _check_same_device(ref: torch.Tensor, **tensors) -> None:
+def _check_same_device(ref: torch.Tensor, _ref: str = "q", **tensors) -> None:
     """Every tensor argument lives on ref's device (the library takes raw pointers
     and launches on one device)."""
     for name, t in tensors.items():
         if t is not None and t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device} but q is on {ref.device}: "
+            raise ValueError(f"{name} is on {t.device} but {_ref} is on {ref.device}: "
                              "all tensors must be on one device")
 
 
@@ -201,7 +215,8 @@ def sdpa_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
              workspace: Optional[torch.Tensor] = None, sink: Optional[torch.Tensor] = None,
              dsink: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
              dbias: Optional[torch.Tensor] = None, bias_grad: bool = True,
-             dbias_dtype: torch.dtype = torch.float32,
+             dbias_dtype: torch.dtype = torch.float32, softcap: float = 0.0,
+             alibi_slopes: Optional[torch.Tensor] = None, mask_plan: Optional["MaskPlan"] = None,
              stream: Optional[torch.cuda.Stream] = None):
     """dQ, dK, dV of scaled-dot-product attention (see include/sdpa_bwd.h).
 
@@ -215,6 +230,9 @@ def sdpa_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
     unless ``bias_grad`` is False, appends the fp32 dBias (shaped like ``bias``) to
     the returned tuple (``dbias_dtype`` float32, or bfloat16 / float16 for the
     io-type dBias of the general entry point).
+    With ``softcap`` (> 0), ``alibi_slopes`` (fp32 (Hq,) CUDA) or ``mask_plan`` the call
+    goes through sdpa_bwd_scored: the gradient of sdpa_fwd with the same three (not
+    together with ``bias``).
     """
     lib = load()
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
@@ -243,12 +261,20 @@ def sdpa_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
                        seq_kv_lens=seq_kv_lens, dq=dq, dk=dk, dv=dv, workspace=workspace,
                        sink=sink, dsink=dsink if sink is not None else None, bias=bias,
                        dbias=dbias if bias is not None and bias_grad else None)
+    scored = _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias)
     _check_launch_device(q)
     sc = 0.0 if scale is None else float(scale)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq), _ptr(dk),
             _ptr(dv), B, Hq, Hkv, Sq, Skv, Dqk, Dv, sc, int(causal), int(bottom_right),
             int(window_left), int(window_right), int(deterministic), _ptr(seq_q_lens),
             _ptr(seq_kv_lens), _ptr(workspace), ws_bytes)
+    if scored:
+        rc = lib.sdpa_bwd_scored(_IO_CODES[io], *args, _ptr(sink), _ptr(dsink if sink is not None else None),
+                                 float(softcap), _ptr(alibi_slopes), _plan_ptr(mask_plan),
+                                 _stream_handle(stream))
+        if rc != 0:
+            raise SdpaError(rc, "sdpa_bwd_scored")
+        return (dq, dk, dv) + ((dsink,) if sink is not None else ())
     if io == torch.float16 or (bias is not None and bias_grad and dbias_dtype != torch.float32):
         # the general typed entry: fp16 io, or an io-type dBias (sink and bias optional)
         bias_dtype, bias_batch = 0, 0
@@ -316,17 +342,240 @@ def _check_bias(bias, B, Hq, Sq, Skv) -> int:
     return {torch.float32: DTYPE_F32, torch.float16: DTYPE_F16}.get(bias.dtype, DTYPE_BF16)
 
 
+class MaskPlan:
+    """The key range of every query row of a batch, with the tile summaries that the
+    kernels take their loop bounds from; made by mask_plan()."""
+
+    def __init__(self, B: int, Sq: int, Skv: int, buffer: torch.Tensor):
+        self.B, self.Sq, self.Skv, self.buffer = B, Sq, Skv, buffer
+
+    def __repr__(self) -> str:
+        return f"MaskPlan(B={self.B}, Sq={self.Sq}, Skv={self.Skv}, device={self.buffer.device})"
+
+
+def _plan_ptr(plan: Optional[MaskPlan]):
+    return None if plan is None else _ptr(plan.buffer)
+
+
+def _check_int32(name, t, shapes):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() \
+            or tuple(t.shape) not in shapes:
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of shape "
+                         + " or ".join(str(s) for s in shapes))
+
+
+def mask_plan(B: int, Sq: int, Skv: int, *, doc_ids: Optional[torch.Tensor] = None,
+              prefix_lens: Optional[torch.Tensor] = None, causal: bool = False,
+              row_lo: Optional[torch.Tensor] = None, row_hi: Optional[torch.Tensor] = None,
+              device: Optional[torch.device] = None, plan: Optional[MaskPlan] = None,
+              stream: Optional[torch.cuda.Stream] = None) -> MaskPlan:
+    """The mask plan that sdpa_fwd and sdpa_bwd take as ``mask_plan``, made once per
+    batch for every layer and both directions.
+
+    Packed documents and prefixes (Sq = Skv): ``doc_ids`` int32 (B, Sq), a document being
+    a maximal run of equal consecutive ids; a row sees its own document, with ``causal``
+    the part up to itself. ``prefix_lens`` int32 (B,), or (B, Sq) for a length at each
+    position, lets every row of a document see its first keys too (needs ``causal``).
+    The attention call then takes causal=False: the plan holds the causal side.
+    Or any ranges: row i of batch row b sees keys [row_lo[b, i], row_hi[b, i]), int32
+    (B, Sq) both. ``plan``: one of the same sizes to write into again.
+    """
+    lib = load()
+    B, Sq, Skv = int(B), int(Sq), int(Skv)
+    rows = row_lo is not None or row_hi is not None
+    if rows and (row_lo is None or row_hi is None or doc_ids is not None or prefix_lens is not None or causal):
+        raise ValueError("row_lo and row_hi come together, without doc_ids, prefix_lens or causal")
+    if not rows and Sq != Skv:
+        raise ValueError("documents and prefixes need Sq = Skv: pass row_lo and row_hi")
+    if prefix_lens is not None and not causal:
+        raise ValueError("prefix_lens widen a causal mask: pass causal=True")
+    tensors = {"row_lo": row_lo, "row_hi": row_hi, "doc_ids": doc_ids, "prefix_lens": prefix_lens}
+    for name, t in tensors.items():
+        if t is not None:
+            _check_int32(name, t, ((B,), (B, Sq)) if name == "prefix_lens" else ((B, Sq),))
+    size = int(lib.sdpa_mask_plan_size(B, Sq, Skv))
+    if size == 0:
+        raise SdpaError(1, "sdpa_mask_plan_size")
+    if plan is None:
+        given = next((t for t in tensors.values() if t is not None), None)
+        dev = given.device if given is not None else torch.device("cuda" if device is None else device)
+        plan = MaskPlan(B, Sq, Skv, torch.empty(size, dtype=torch.uint8, device=dev))
+    elif (plan.B, plan.Sq, plan.Skv) != (B, Sq, Skv):
+        raise ValueError(f"plan was made for {plan!r}, not for B={B}, Sq={Sq}, Skv={Skv}")
+    _check_same_device(plan.buffer, _ref="the plan", **tensors)
+    _check_launch_device(plan.buffer)
+    if rows:
+        rc = lib.sdpa_mask_plan_rows(_ptr(row_lo), _ptr(row_hi), B, Sq, Skv, _ptr(plan.buffer), size,
+                                     _stream_handle(stream))
+    else:
+        rc = lib.sdpa_mask_plan_docs(_ptr(doc_ids), _ptr(prefix_lens),
+                                     int(prefix_lens is not None and prefix_lens.dim() == 2), int(causal), B, Sq,
+                                     _ptr(plan.buffer), size, _stream_handle(stream))
+    if rc != 0:
+        raise SdpaError(rc, "sdpa_mask_plan_rows" if rows else "sdpa_mask_plan_docs")
+    return plan
+
+
+def _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias) -> bool:
+    """Whether the call modifies its scores (and then that it may)."""
+    softcap = float(softcap)
+    if not (0.0 <= softcap < math.inf):
+        raise ValueError("softcap must be 0 (none) or a positive finite number")
+    if softcap == 0.0 and alibi_slopes is None and mask_plan is None:
+        return False
+    if bias is not None:
+        raise ValueError("softcap, alibi_slopes and mask_plan do not combine with bias")
+    if alibi_slopes is not None and (
+            not isinstance(alibi_slopes, torch.Tensor) or alibi_slopes.dtype != torch.float32
+            or not alibi_slopes.is_cuda or not alibi_slopes.is_contiguous() or tuple(alibi_slopes.shape) != (Hq,)):
+        raise ValueError("alibi_slopes must be a contiguous fp32 CUDA tensor of shape (Hq,)")
+    if mask_plan is not None:
+        if not isinstance(mask_plan, MaskPlan):
+            raise TypeError("mask_plan must be a MaskPlan (made by mask_plan())")
+        if (mask_plan.B, mask_plan.Sq, mask_plan.Skv) != (B, Sq, Skv):
+            raise ValueError(f"mask_plan was made for {mask_plan!r}, not for B={B}, Sq={Sq}, Skv={Skv}")
+    _check_same_device(q, alibi_slopes=alibi_slopes, mask_plan=None if mask_plan is None else mask_plan.buffer)
+    return True
+
+
+def rope_inv_freq(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+                  original_len: int = 0, low: float = 1.0, high: float = 32.0,
+                  device=None) -> torch.Tensor:
+    """The fp64 (rot_dim / 2,) frequencies (radians per position) that rope_fwd takes:
+    f[i] = base^(-2 i / rot_dim), and for contexts longer than the trained one by ``factor``
+
+      "linear"  f / factor (every position interpolated),
+      "ntk"     the same with base * factor^(rot_dim / (rot_dim - 2)) (the lowest
+                frequency interpolated by ``factor``, the highest kept),
+      "bands"   by how often a frequency turns over ``original_len`` positions,
+                r = original_len * f / (2 pi): kept where r >= high, interpolated where
+                r <= low, a linear mix between (the ramp of the YaRN paper, Peng et al.
+                2023; its factor on the scores is rope_fwd's mult =
+                0.1 ln(factor) + 1 on both queries and keys).
+    """
+    if rot_dim <= 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and positive")
+    if not (base > 0.0 and math.isfinite(base)) or not (factor > 0.0 and math.isfinite(factor)):
+        raise ValueError("base and factor must be positive finite numbers")
+    if scaling not in ("none", "linear", "ntk", "bands"):
+        raise ValueError("scaling must be none, linear, ntk or bands")
+    if scaling == "ntk":
+        if rot_dim < 4:
+            raise ValueError("ntk scaling needs rot_dim >= 4")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = float(base) ** (-2.0 * torch.arange(rot_dim // 2, dtype=torch.float64) / rot_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "bands":
+        if original_len <= 0 or not low < high:
+            raise ValueError("bands scaling needs original_len > 0 and low < high")
+        keep = ((original_len * f / (2.0 * math.pi) - low) / (high - low)).clamp(0.0, 1.0)
+        f = f * (keep + (1.0 - keep) / factor)
+    return f.to(torch.device("cuda") if device is None else device)
+
+
+def _check_rope_tensor(name, t, shape, io):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != io or not t.is_cuda:
+        raise ValueError(f"{name} must be a {io} CUDA tensor")
+    if t.dim() != 4 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.stride(3) != 1 and t.shape[3] > 1:
+        raise ValueError(f"{name} must have contiguous columns (stride 1 in its last dimension)")
+
+
+def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, k_out, stream):
+    lib = load()
+    io = _io_dtype(q)
+    if q.dim() != 4:
+        raise ValueError("q must be (B, H, S, D)")
+    B, Hq, S, D = q.shape
+    _check_rope_tensor("q", q, (B, Hq, S, D), io)
+    Hkv = 0
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k must be a (B, H, S, D) tensor")
+        Hkv = k.shape[1]
+        _check_rope_tensor("k", k, (B, Hkv, S, D), io)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float64 or not inv_freq.is_cuda \
+            or not inv_freq.is_contiguous() or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a contiguous fp64 CUDA vector (rope_inv_freq)")
+    rot = 2 * inv_freq.numel()
+    if rot == 0 or rot > D:
+        raise ValueError(f"inv_freq rotates {rot} columns of {D}")
+    per_batch = 0
+    if positions is not None:
+        _check_int32("positions", positions, ((S,), (B, S)))
+        per_batch = int(positions.dim() == 2)
+        if offset != 0:
+            raise ValueError("offset counts from position 0 where no positions are given")
+    if q_out is None:
+        q_out = torch.empty((B, Hq, S, D), dtype=io, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty((B, Hkv, S, D), dtype=io, device=q.device)
+    _check_rope_tensor("q_out", q_out, (B, Hq, S, D), io)
+    if k is not None:
+        _check_rope_tensor("k_out", k_out, (B, Hkv, S, D), io)
+    _check_same_device(q, k=k, inv_freq=inv_freq, positions=positions, q_out=q_out, k_out=k_out)
+    _check_launch_device(q)
+    strides = []
+    for t in (q, q_out, k, k_out):
+        strides += [0, 0, 0] if t is None else [t.stride(0), t.stride(1), t.stride(2)]
+    if q.numel() > 0:
+        rc = lib.sdpa_rope(_IO_CODES[io], _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), B, Hq, Hkv, S, D,
+                           (ctypes.c_longlong * 12)(*strides), _ptr(inv_freq), rot, float(mult), _ptr(positions),
+                           per_batch, int(offset), int(interleaved), int(inverse), _stream_handle(stream))
+        if rc != 0:
+            raise SdpaError(rc, "sdpa_rope")
+    return q_out, k_out
+
+
+def rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: torch.Tensor, *, mult: float = 1.0,
+             positions: Optional[torch.Tensor] = None, offset: int = 0, interleaved: bool = False,
+             q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None):
+    """Rotary embedding of q (B,Hq,S,D) and k (B,Hkv,S,D) (or of q alone, k None): the
+    first 2 * inv_freq.numel() columns turn pair by pair by position * inv_freq and are
+    multiplied by ``mult``, the others are copied (sdpa_rope in include/sdpa_bwd.h).
+
+    bf16 or fp16, any strides of batch, head and position with contiguous columns: a
+    projection's (B,S,H,D) output goes in as a transposed view and comes out contiguous
+    (B,H,S,D) for sdpa_fwd. ``inv_freq``: fp64 CUDA vector (rope_inv_freq).
+    ``positions``: int32 (S,) or (B,S), else offset .. offset + S - 1. Pairs are columns
+    (i, i + rot/2), or (2i, 2i+1) when ``interleaved``. Returns (q_out, k_out); the
+    outputs may be the inputs (in place).
+    """
+    return _rope(q, k, inv_freq, mult, positions, offset, interleaved, False, q_out, k_out, stream)
+
+
+def rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], inv_freq: torch.Tensor, *, mult: float = 1.0,
+             positions: Optional[torch.Tensor] = None, offset: int = 0, interleaved: bool = False,
+             q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+             stream: Optional[torch.cuda.Stream] = None):
+    """The gradients of rope_fwd's inputs from those of its outputs (dq, dk of sdpa_bwd):
+    the transposed rotation, with rope_fwd's other arguments."""
+    return _rope(dq, dk, inv_freq, mult, positions, offset, interleaved, True, q_out, k_out, stream)
+
+
 def sdpa_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale: Optional[float] = None,
              causal: bool = False, bottom_right: bool = False, window_left: int = -1,
              window_right: int = -1, seq_q_lens: Optional[torch.Tensor] = None,
              seq_kv_lens: Optional[torch.Tensor] = None, sink: Optional[torch.Tensor] = None,
              bias: Optional[torch.Tensor] = None,
              o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+             softcap: float = 0.0, alibi_slopes: Optional[torch.Tensor] = None,
+             mask_plan: Optional["MaskPlan"] = None,
              stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """O (bf16, (B,Hq,Sq,Dv)) and natural-log LSE (fp32, (B,Hq,Sq)) of the masked
     softmax attention (see include/sdpa_bwd.h); the inputs of sdpa_bwd. ``bias``
     ((1|B, Hq, Sq, Skv) bf16, fp16 or fp32 CUDA, contiguous) is added to the scaled
-    scores (sdpa_fwd_bias)."""
+    scores (sdpa_fwd_bias). ``softcap`` (> 0) caps the scaled scores at
+    softcap * tanh(. / softcap); ``alibi_slopes`` (fp32 (Hq,) CUDA) subtracts slope[h] *
+    |q + diag - k|; ``mask_plan`` (see mask_plan()) limits each row to its range of
+    keys, for document and prefix masks (sdpa_fwd_scored; not together with ``bias``)."""
     lib = load()
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
         raise ValueError("q, k, v must be (B, H, S, D)")
@@ -347,11 +596,18 @@ def sdpa_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale: Option
     _check_lse(lse, B, Hq, Sq)
     _check_same_device(q, k=k, v=v, o=o, lse=lse, seq_q_lens=seq_q_lens, seq_kv_lens=seq_kv_lens,
                        sink=sink, bias=bias)
+    scored = _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias)
     _check_launch_device(q)
     sc = 0.0 if scale is None else float(scale)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Sq, Skv, Dqk, Dv, sc,
             int(causal), int(bottom_right), int(window_left), int(window_right),
             _ptr(seq_q_lens), _ptr(seq_kv_lens), _ptr(sink))
+    if scored:
+        rc = lib.sdpa_fwd_scored(_IO_CODES[io], *args, float(softcap), _ptr(alibi_slopes),
+                                 _plan_ptr(mask_plan), _stream_handle(stream))
+        if rc != 0:
+            raise SdpaError(rc, "sdpa_fwd_scored")
+        return o, lse
     if io == torch.float16:
         bias_dtype = _check_bias(bias, B, Hq, Sq, Skv) if bias is not None else 0
         rc = lib.sdpa_fwd_typed(_IO_CODES[io], *args, _ptr(bias), bias_dtype,

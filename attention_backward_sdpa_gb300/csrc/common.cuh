@@ -10,6 +10,8 @@
 
 #include <utility>
 
+#include "score.cuh"
+
 namespace sdpa {
 
 // Tile sizes of the KV-stationary main kernel: one CTA owns BN keys of one
@@ -98,6 +100,8 @@ struct ChainParams {
   uint8_t* ds_ws;
   uint8_t* zero_tile;
 
+  ScoreMods mods;       // capped / distance-biased scores and row ranges (MOD kernels)
+
   int* status;          // per-device status word
   // Ordered relay (deterministic mode, D_qk up to 128 but not 128): how long a
   // key tile waits for its turn before it gives up and reports a timeout, and a
@@ -130,6 +134,42 @@ __host__ __device__ inline void visited_query_tiles(int kt, int Lq, int Lk, int 
   if (q_min > q_max) return;
   qt_lo = (int)(q_min / BQ);
   qt_hi = (int)(q_max / BQ);
+}
+
+// The same under a mask plan: narrowed to the query tiles whose row ranges meet
+// the key tile. The plan's interval is a hull, so tiles inside it may still see
+// no key; the kernels mask those per row.
+__device__ inline void planned_query_tiles(const ScoreMods& m, int b, int kt, int n_kt, int& qt_lo, int& qt_hi) {
+  if (m.k_sum == nullptr) return;
+  const int2 s = m.k_sum[(long long)b * n_kt + kt];
+  qt_lo = max(qt_lo, s.x);
+  qt_hi = min(qt_hi, s.y);
+}
+
+// The replay state (score.cuh) of a thread that holds key k of the key tile at k0
+// against the 64-row query tile qt of batch row b, query head h.
+__device__ __forceinline__ ModTile mod_tile(const ChainParams& p, int b, int h, int qt, int k0, int k, int Lk, int diag,
+                                            bool edge, long long q_lo_vis, long long q_hi_vis) {
+  ModTile m;
+  const int q0 = qt * BQ;
+  m.cap_in = p.mods.cap_in;
+  m.cap_log2 = p.mods.cap_log2;
+  m.scale_log2 = p.scale_log2;
+  m.slope2 = p.mods.slopes != nullptr ? p.mods.slopes[h] * 1.4426950408889634f : 0.f;
+  m.dist = (float)((long long)q0 + diag - k);
+  m.q_lo = (int)min(max(q_lo_vis - q0, 0ll), (long long)BQ);
+  m.q_hi = k < Lk ? (int)min(max(q_hi_vis - q0, -1ll), (long long)BQ) : -1;
+  m.k = k;
+  m.ranges = nullptr;
+  m.masked = edge;
+  if (p.mods.ranges != nullptr) {
+    const int4 s = p.mods.q_sum[(long long)b * p.n_qt + qt];
+    if (s.z > k0 || s.w < min(k0 + BN, Lk)) {  // some row does not see the whole key tile
+      m.ranges = p.mods.ranges + ((long long)b * p.n_qt + qt) * BQ;
+      m.masked = true;
+    }
+  }
+  return m;
 }
 
 // Debug-bounds build (compiled with -DSDPA_DEBUG_BOUNDS): the kernels check
@@ -217,6 +257,7 @@ struct FwdParams {
   int bias_f16;               // 16-bit bias elements are fp16 (else bf16)
   long long bias_bstride;
   int bias_vec;               // rows allow 16-byte loads (S_kv * size % 16 == 0, base aligned)
+  ScoreMods mods;             // capped / distance-biased scores and row ranges (MOD kernels)
   float* lse;                 // (B, Hq, Sq) output
   void* o;                    // (B, Hq, Sq, Dv) output (io type), also behind FwdMaps::o
   int* status;                // device status word
@@ -258,6 +299,33 @@ cudaError_t main_f16_kernel_setup();
 cudaError_t main_bias_kernel_setup();
 cudaError_t launch_main_qat(const MainMaps& maps, const ChainParams& p, cudaStream_t s);
 cudaError_t main_qat_kernel_setup();
+cudaError_t launch_main_mod(const MainMaps& maps, const ChainParams& p, cudaStream_t s);
+cudaError_t main_mod_kernel_setup();
+// A mask plan (score.cuh) from row ranges (row_lo, row_hi) or from documents.
+struct MaskPlanArgs {
+  int B, Sq, Skv;
+  const int32_t* row_lo;       // (B, Sq), or null: the document form
+  const int32_t* row_hi;
+  const int32_t* doc_ids;      // (B, S), or null: one document per batch row
+  const int32_t* prefix_lens;  // (B,), or (B, S) when prefix_per_row, or null
+  int prefix_per_row, causal;
+};
+cudaError_t launch_mask_plan(const MaskPlanArgs& a, void* plan, cudaStream_t s);
+// The rotary embedding (sdpa_rope.cu) of up to two tensors (queries and keys) of
+// H[i] heads; strides of batch, head and position in elements, columns contiguous.
+struct RopeArgs {
+  const void* x[2];
+  void* y[2];
+  int H[2];
+  long long xs[6], ys[6];
+  const double* freq;
+  const int32_t* positions;  // or null: offset + s
+  long long pos_bstride;
+  int offset, B, S, D, rot;
+  int f16, interleaved, inverse;
+  float mult;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s, int num_sms);
 // NVFP4 fake quantization of n_blocks blocks of 16 consecutive bf16 values.
 cudaError_t launch_nvfp4_fake_quant(const void* x, void* y, long long n_blocks, int num_sms,
                                     cudaStream_t s);

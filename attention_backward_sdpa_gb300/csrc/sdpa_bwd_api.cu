@@ -338,6 +338,41 @@ struct BiasArgs {
   int dbias_dtype = SDPA_DTYPE_F32;
 };
 
+// Modified scores of the scored entry points; nothing set for the other calls.
+struct ModArgs {
+  float softcap = 0.f;            // 0: none
+  const float* slopes = nullptr;  // (H_q,) or null
+  const void* plan = nullptr;     // mask plan of (B, S_q, S_kv), or null
+  bool on() const { return softcap != 0.f || slopes != nullptr || plan != nullptr; }
+};
+
+// Checks the modifiers against the scale that the call will use and fills the
+// kernels' view of them.
+int fill_mods(const ModArgs& ma, float scale, int B, int S_q, int S_kv, ScoreMods& m) {
+  m = ScoreMods{};
+  if (!ma.on()) return SDPA_OK;
+  if (!(ma.softcap >= 0.f) || !std::isfinite(ma.softcap)) return SDPA_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(ma.slopes) % 4 != 0) return SDPA_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(ma.plan) % 256 != 0) return SDPA_ERR_ALIGN;
+  m.on = 1;
+  m.slopes = ma.slopes;
+  if (ma.softcap > 0.f) {
+    m.cap_in = scale / ma.softcap;
+    m.cap_log2 = ma.softcap * 1.4426950408889634f;
+    // A cap so far from the scale that their ratio leaves the normal fp32 range
+    // would turn the capped scores into zeros or NaN.
+    if (!std::isnormal(m.cap_in) || !std::isfinite(m.cap_log2)) return SDPA_ERR_INVALID;
+  }
+  if (ma.plan) {
+    const MaskPlanLayout l = mask_plan_layout(B, ceil_div(S_q, BQ), ceil_div(S_kv, BN));
+    const char* base = static_cast<const char*>(ma.plan);
+    m.ranges = reinterpret_cast<const int2*>(base + l.ranges);
+    m.q_sum = reinterpret_cast<const int4*>(base + l.q_sum);
+    m.k_sum = reinterpret_cast<const int2*>(base + l.k_sum);
+  }
+  return SDPA_OK;
+}
+
 // The whole chain; sink/dsink are null for sdpa_bwd().
 int run_chain(const void* q, const void* k, const void* v, const void* o, const void* d_o,
               const float* lse, void* dq, void* dk, void* dv, int B, int H_q, int H_kv, int S_q,
@@ -345,7 +380,7 @@ int run_chain(const void* q, const void* k, const void* v, const void* o, const 
               int window_left, int window_right, int deterministic, const int32_t* seq_q_lens,
               const int32_t* seq_kv_lens, void* workspace, size_t workspace_bytes,
               const float* sink, float* dsink, const BiasArgs& ba, void* stream_,
-              bool qat = false, bool f16 = false) {
+              bool qat = false, bool f16 = false, const ModArgs& ma = ModArgs{}) {
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   int rc = basic_checks(B, H_q, H_kv, S_q, S_kv, D_qk, D_v);
   if (rc != SDPA_OK) return rc;
@@ -375,6 +410,12 @@ int run_chain(const void* q, const void* k, const void* v, const void* o, const 
     if (reinterpret_cast<uintptr_t>(ptr) % 4 != 0) return SDPA_ERR_ALIGN;
   if (window_right >= 0 && !causal) return SDPA_ERR_UNSUPPORTED;
   if (!(scale > 0.f) || !std::isfinite(scale)) scale = 1.0f / std::sqrt((float)D_qk);
+  ScoreMods mods;
+  rc = fill_mods(ma, scale, B, S_q, S_kv, mods);
+  if (rc != SDPA_OK) return rc;
+  // The ordered relay counts on every key tile between a query tile's first and
+  // last to visit it, which row ranges do not give.
+  if (ma.plan && deterministic && choose_route(deterministic, D_qk) == Route::kReduce) return SDPA_ERR_UNSUPPORTED;
 
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return SDPA_ERR_CUDA;
@@ -469,6 +510,7 @@ int run_chain(const void* q, const void* k, const void* v, const void* o, const 
   p.dk_ws = p.n_part > 1 ? reinterpret_cast<__nv_bfloat16*>(ws + cv.dk_ws) : nullptr;
   p.dv_ws = p.n_part > 1 ? reinterpret_cast<__nv_bfloat16*>(ws + cv.dv_ws) : nullptr;
   p.status = status;
+  p.mods = mods;
   {
     std::lock_guard<std::mutex> lock(g_mu);
     p.relay_wait_ns = g_relay_wait_ns;
@@ -576,11 +618,40 @@ int sdpa_bwd(const void* q, const void* k, const void* v, const void* o, const v
 
 namespace {
 
+int plan_checks(int B, int S_q, int S_kv) {
+  if (B <= 0 || S_q <= 0 || S_kv <= 0) return SDPA_ERR_INVALID;
+  const long long limit = 1ll << 30;  // rows, tiles and (position + prefix) stay 32-bit
+  if ((long long)B * (S_q + (long long)BQ) >= limit || (long long)B * (S_kv + (long long)BN) >= limit)
+    return SDPA_ERR_INVALID;
+  return SDPA_OK;
+}
+
+int run_mask_plan(const MaskPlanArgs& a, void* plan, size_t plan_bytes, void* stream) {
+  int rc = plan_checks(a.B, a.Sq, a.Skv);
+  if (rc != SDPA_OK) return rc;
+  if (!plan) return SDPA_ERR_INVALID;
+  for (const void* ptr : {(const void*)a.row_lo, (const void*)a.row_hi, (const void*)a.doc_ids,
+                          (const void*)a.prefix_lens})
+    if (reinterpret_cast<uintptr_t>(ptr) % 4 != 0) return SDPA_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(plan) % 256 != 0) return SDPA_ERR_ALIGN;
+  if (plan_bytes < mask_plan_layout(a.B, ceil_div(a.Sq, BQ), ceil_div(a.Skv, BN)).bytes) return SDPA_ERR_WORKSPACE;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SDPA_ERR_CUDA;
+  int* status = nullptr;
+  int sms = 0;
+  rc = device_state(dev, &status, &sms);
+  if (rc != SDPA_OK) return rc;
+  nvtxRangePushA("sdpa_mask_plan");
+  const cudaError_t e = launch_mask_plan(a, plan, static_cast<cudaStream_t>(stream));
+  nvtxRangePop();
+  return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
 int run_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H_q,
             int H_kv, int S_q, int S_kv, int D_qk, int D_v, float scale, int causal,
             int bottom_right, int window_left, int window_right, const int32_t* seq_q_lens,
             const int32_t* seq_kv_lens, const float* sink, const BiasArgs& ba, void* stream_,
-            bool f16 = false) {
+            bool f16 = false, const ModArgs& ma = ModArgs{}) {
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   int rc = basic_checks(B, H_q, H_kv, S_q, S_kv, D_qk, D_v);
   if (rc != SDPA_OK) return rc;
@@ -600,6 +671,9 @@ int run_fwd(const void* q, const void* k, const void* v, void* o, float* lse, in
   }
   if (window_right >= 0 && !causal) return SDPA_ERR_UNSUPPORTED;
   if (!(scale > 0.f) || !std::isfinite(scale)) scale = 1.0f / std::sqrt((float)D_qk);
+  ScoreMods mods;
+  rc = fill_mods(ma, scale, B, S_q, S_kv, mods);
+  if (rc != SDPA_OK) return rc;
   if (S_q == 0) return SDPA_OK;  // no rows
 
   int dev = 0;
@@ -633,6 +707,7 @@ int run_fwd(const void* q, const void* k, const void* v, void* o, float* lse, in
   p.lse = lse;
   p.o = o;
   p.status = status;
+  p.mods = mods;
   FwdMaps maps;
   const long long BHq = (long long)B * H_q, BHkv = (long long)B * H_kv;
   // An empty key axis still needs valid K/V maps: point them at Q (never read).
@@ -735,6 +810,119 @@ int sdpa_bwd_nvfp4_qat(const void* q, const void* k, const void* v, const void* 
   return run_chain(q, k, v, o_hp, d_o, lse, dq, dk, dv, B, H_q, H_kv, S_q, S_kv, D_qk, D_v, scale,
                    causal, bottom_right, window_left, window_right, 0, seq_q_lens, seq_kv_lens,
                    workspace, workspace_bytes, nullptr, nullptr, BiasArgs{}, stream, true);
+}
+
+int sdpa_fwd_scored(int io_dtype, const void* q, const void* k, const void* v, void* o, float* lse,
+                    int B, int H_q, int H_kv, int S_q, int S_kv, int D_qk, int D_v, float scale,
+                    int causal, int bottom_right, int window_left, int window_right,
+                    const int32_t* seq_q_lens, const int32_t* seq_kv_lens, const float* sink,
+                    float softcap, const float* alibi_slopes, const void* mask_plan, void* stream) {
+  if (io_dtype != SDPA_DTYPE_BF16 && io_dtype != SDPA_DTYPE_F16) return SDPA_ERR_INVALID;
+  const ModArgs ma{softcap, alibi_slopes, mask_plan};
+  return run_fwd(q, k, v, o, lse, B, H_q, H_kv, S_q, S_kv, D_qk, D_v, scale, causal, bottom_right,
+                 window_left, window_right, seq_q_lens, seq_kv_lens, sink, BiasArgs{}, stream,
+                 io_dtype == SDPA_DTYPE_F16, ma);
+}
+
+int sdpa_bwd_scored(int io_dtype, const void* q, const void* k, const void* v, const void* o,
+                    const void* d_o, const float* lse, void* dq, void* dk, void* dv, int B, int H_q,
+                    int H_kv, int S_q, int S_kv, int D_qk, int D_v, float scale, int causal,
+                    int bottom_right, int window_left, int window_right, int deterministic,
+                    const int32_t* seq_q_lens, const int32_t* seq_kv_lens, void* workspace,
+                    size_t workspace_bytes, const float* sink, float* dsink, float softcap,
+                    const float* alibi_slopes, const void* mask_plan, void* stream) {
+  if (io_dtype != SDPA_DTYPE_BF16 && io_dtype != SDPA_DTYPE_F16) return SDPA_ERR_INVALID;
+  if (dsink && !sink) return SDPA_ERR_INVALID;
+  const ModArgs ma{softcap, alibi_slopes, mask_plan};
+  return run_chain(q, k, v, o, d_o, lse, dq, dk, dv, B, H_q, H_kv, S_q, S_kv, D_qk, D_v, scale,
+                   causal, bottom_right, window_left, window_right, deterministic, seq_q_lens,
+                   seq_kv_lens, workspace, workspace_bytes, dsink ? sink : nullptr, dsink, BiasArgs{},
+                   stream, false, io_dtype == SDPA_DTYPE_F16, ma);
+}
+
+size_t sdpa_mask_plan_size(int B, int S_q, int S_kv) {
+  if (plan_checks(B, S_q, S_kv) != SDPA_OK) return 0;
+  return mask_plan_layout(B, ceil_div(S_q, BQ), ceil_div(S_kv, BN)).bytes;
+}
+
+int sdpa_mask_plan_rows(const int32_t* row_lo, const int32_t* row_hi, int B, int S_q, int S_kv,
+                        void* plan, size_t plan_bytes, void* stream) {
+  if (!row_lo || !row_hi) return SDPA_ERR_INVALID;
+  return run_mask_plan(MaskPlanArgs{B, S_q, S_kv, row_lo, row_hi, nullptr, nullptr, 0, 0}, plan, plan_bytes, stream);
+}
+
+int sdpa_mask_plan_docs(const int32_t* doc_ids, const int32_t* prefix_lens, int prefix_per_row,
+                        int causal, int B, int S, void* plan, size_t plan_bytes, void* stream) {
+  if (prefix_lens && !causal) return SDPA_ERR_INVALID;  // a prefix widens a causal mask
+  return run_mask_plan(MaskPlanArgs{B, S, S, nullptr, nullptr, doc_ids, prefix_lens, prefix_per_row ? 1 : 0,
+                                    causal ? 1 : 0},
+                       plan, plan_bytes, stream);
+}
+
+int sdpa_rope(int io_dtype, const void* q, const void* k, void* q_out, void* k_out, int B, int H_q,
+              int H_kv, int S, int D, const long long* strides, const double* inv_freq, int rot_dim,
+              float mult, const int32_t* positions, int positions_per_batch, int offset,
+              int interleaved, int inverse, void* stream) {
+  if (io_dtype != SDPA_DTYPE_BF16 && io_dtype != SDPA_DTYPE_F16) return SDPA_ERR_INVALID;
+  if (B <= 0 || H_q <= 0 || H_kv < 0 || S < 0 || D <= 0 || !strides || !std::isfinite(mult)) return SDPA_ERR_INVALID;
+  if (!q || !q_out || !inv_freq || (H_kv > 0 && (!k || !k_out))) return SDPA_ERR_INVALID;
+  if (rot_dim <= 0 || rot_dim % 2 != 0 || rot_dim > D) return SDPA_ERR_INVALID;
+  if (rot_dim > 512) return SDPA_ERR_UNSUPPORTED;
+  if ((long long)B * S * (H_q + (long long)H_kv) >= 1ll << 31) return SDPA_ERR_INVALID;
+  RopeArgs a{};
+  const void* xs[2] = {q, k};
+  void* ys[2] = {q_out, k_out};
+  const int Hs[2] = {H_q, H_kv}, dims[3] = {B, 0, S};
+  for (int i = 0; i < 2; ++i) {
+    a.x[i] = xs[i];
+    a.y[i] = ys[i];
+    a.H[i] = Hs[i];
+    if (Hs[i] == 0) continue;
+    if (reinterpret_cast<uintptr_t>(xs[i]) % 2 != 0 || reinterpret_cast<uintptr_t>(ys[i]) % 2 != 0) return SDPA_ERR_ALIGN;
+    for (int j = 0; j < 3; ++j) {
+      a.xs[3 * i + j] = strides[6 * i + j];
+      a.ys[3 * i + j] = strides[6 * i + 3 + j];
+      if ((j == 1 ? Hs[i] : dims[j]) > 1 && a.xs[3 * i + j] < 0) return SDPA_ERR_INVALID;
+    }
+    // Two output rows that share a place would race: taken by ascending stride,
+    // each dimension has to step over everything that the smaller ones span.
+    long long span = D, ext[3] = {B, Hs[i], S}, st[3] = {a.ys[3 * i], a.ys[3 * i + 1], a.ys[3 * i + 2]};
+    for (int pass = 0; pass < 3; ++pass) {
+      int low = -1;
+      for (int j = 0; j < 3; ++j)
+        if (ext[j] > 1 && (low < 0 || st[j] < st[low])) low = j;
+      if (low < 0) break;
+      if (st[low] < span || st[low] > (1ll << 40)) return SDPA_ERR_INVALID;
+      span += st[low] * (ext[low] - 1);
+      ext[low] = 1;
+    }
+  }
+  if (reinterpret_cast<uintptr_t>(inv_freq) % 8 != 0 || reinterpret_cast<uintptr_t>(positions) % 4 != 0)
+    return SDPA_ERR_ALIGN;
+  if (S == 0) return SDPA_OK;
+  if (!positions && (offset < 0 || (long long)offset + S > 1ll << 31)) return SDPA_ERR_INVALID;
+  a.freq = inv_freq;
+  a.positions = positions;
+  a.pos_bstride = positions_per_batch ? S : 0;
+  a.offset = offset;
+  a.B = B;
+  a.S = S;
+  a.D = D;
+  a.rot = rot_dim;
+  a.f16 = io_dtype == SDPA_DTYPE_F16 ? 1 : 0;
+  a.interleaved = interleaved ? 1 : 0;
+  a.inverse = inverse ? 1 : 0;
+  a.mult = mult;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SDPA_ERR_CUDA;
+  int* status = nullptr;
+  int sms = 0;
+  const int rc = device_state(dev, &status, &sms);
+  if (rc != SDPA_OK) return rc;
+  nvtxRangePushA("sdpa_rope");
+  const cudaError_t e = launch_rope(a, static_cast<cudaStream_t>(stream), sms);
+  nvtxRangePop();
+  return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
 }
 
 int sdpa_nvfp4_fake_quant(const void* x, void* y, long long n, void* stream) {

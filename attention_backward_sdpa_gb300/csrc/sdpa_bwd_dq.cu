@@ -87,13 +87,30 @@ __device__ __forceinline__ DqUnit dq_unit(const ChainParams& p, int u) {
     const int diag = p.bottom_right ? w.Lk - w.Lq : 0;
     kt_start = (int)max(0ll, floor_div((long long)w.qt0 * BQ + diag - p.window_left, BN) - 1);
   }
-  for (int kt = kt_start; kt < p.n_kt; ++kt) {
+  // Under a mask plan only the key tiles that meet the hull of either query
+  // tile's row ranges can hold anything, and the visited ones among them need
+  // not be contiguous (a tile between them that the main kernel did not visit
+  // reads as zeros).
+  int kt_end = p.n_kt;
+  const bool planned = p.mods.q_sum != nullptr;
+  if (planned) {
+    const int4* qs = p.mods.q_sum + (long long)w.b * p.n_qt + w.qt0;
+    int4 s = qs[0];
+    if (w.qt1 < p.n_qt) {
+      s.x = min(s.x, qs[1].x);
+      s.y = max(s.y, qs[1].y);
+    }
+    kt_start = max(kt_start, s.x / BN);
+    kt_end = min(kt_end, ceil_div(s.y, BN));
+  }
+  for (int kt = kt_start; kt < kt_end; ++kt) {
     int lo, hi;
     visited_query_tiles(kt, w.Lq, w.Lk, p.causal, p.bottom_right, p.window_left, p.window_right, lo, hi);
+    if (planned) planned_query_tiles(p.mods, w.b, kt, p.n_kt, lo, hi);
     if ((lo <= w.qt0 && w.qt0 <= hi) || (w.qt1 < p.n_qt && lo <= w.qt1 && w.qt1 <= hi)) {
       first = min(first, kt);
       last = kt;
-    } else if (last >= 0) {
+    } else if (last >= 0 && !planned) {
       break;
     }
   }
@@ -206,9 +223,11 @@ __global__ void __launch_bounds__(DQ_THREADS, 1)
           mbar_arrive_expect_tx(&dsfull[st], L::TILE_DS);
           int lo, hi;
           visited_query_tiles(kt, w.Lq, w.Lk, p.causal, p.bottom_right, p.window_left, p.window_right, lo, hi);
-          // Without length arrays the band is the visited range itself.
+          // Without length arrays the band is the visited range itself (before
+          // a mask plan narrows it).
           int band_lo = lo, band_hi = hi;
           if (p.seq_q_lens != nullptr || p.seq_kv_lens != nullptr) ds_band_range(p, kt, band_lo, band_hi);
+          planned_query_tiles(p.mods, w.b, kt, p.n_kt, lo, hi);
           for (int half = 0; half < 2; ++half) {
             const int qt = w.qt0 + half;
             const bool stored = qt < p.n_qt && lo <= qt && qt <= hi;

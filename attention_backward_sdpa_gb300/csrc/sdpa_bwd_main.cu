@@ -9,10 +9,12 @@ cudaError_t main_kernel_setup() {
   if (e == cudaSuccess) e = main_bias_kernel_setup();
   if (e == cudaSuccess) e = main_qat_kernel_setup();
   if (e == cudaSuccess) e = main_f16_kernel_setup();
+  if (e == cudaSuccess) e = main_mod_kernel_setup();
   return e;
 }
 
 cudaError_t launch_main(const MainMaps& maps, const ChainParams& p, cudaStream_t s) {
+  if (p.mods.on) return launch_main_mod(maps, p, s);
   if (p.bias != nullptr) return launch_main_bias(maps, p, s);
   if (p.f16) return launch_main_f16(maps, p, s);
   return launch_main_variant<false>(maps, p, s);

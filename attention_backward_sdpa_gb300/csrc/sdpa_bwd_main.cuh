@@ -198,8 +198,9 @@ __device__ __forceinline__ uint32_t fake_nvfp4_p_pair(float p0, float p1, float 
 // reduction, every dS^T tile is stored to the workspace for the dQ kernel.
 // BIAS adds the additive bias to the replay and writes dBias (when p.dbias).
 // QAT writes G3's P^T fake-quantized to NVFP4. F16: fp16 io tensors (and
-// fp16 P^T / dS^T MMA operands) instead of bf16.
-template <int D, bool DS_OUT, bool BIAS, bool QAT = false, bool F16 = false>
+// fp16 P^T / dS^T MMA operands) instead of bf16. MOD: capped and distance-biased
+// scores and row ranges (score.cuh).
+template <int D, bool DS_OUT, bool BIAS, bool QAT = false, bool F16 = false, bool MOD = false>
 __global__ void __launch_bounds__(MAIN_THREADS, 1)
     sdpa_bwd_main(const __grid_constant__ MainMaps maps, const ChainParams p) {
   using L = MainLayout<D, DS_OUT>;
@@ -221,8 +222,11 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
     batch_lengths(p, b0, Lq0, Lk0);
     visited_query_tiles(kt0, Lq0, Lk0, p.causal, p.bottom_right, p.window_left, p.window_right, lo0,
                         hi0);
+    if constexpr (MOD) planned_query_tiles(p.mods, b0, kt0, p.n_kt, lo0, hi0);
     if (hi0 < lo0) {
-      if (!row_has_visible_pair(Lq0, Lk0))
+      // (Row ranges can leave every key tile of a row empty, so that no other
+      // CTA would be there to write the zeros: each empty tile writes its own.)
+      if (MOD || !row_has_visible_pair(Lq0, Lk0))
         zero_key_tile_rows(p, p.dk_ws ? (long long)gi0 : (long long)(gi0 / p.n_part), kt0 * BN);
       if (BIAS && p.dbias != nullptr && !p.dbias_red) {
         const int hk0 = (gi0 / p.n_part) % p.Hkv;
@@ -315,6 +319,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
   int qt_lo, qt_hi;
   visited_query_tiles(kt, Lq, Lk, p.causal, p.bottom_right, p.window_left, p.window_right, qt_lo,
                       qt_hi);
+  if constexpr (MOD) planned_query_tiles(p.mods, b, kt, p.n_kt, qt_lo, qt_hi);
   // Tiles t = 0 .. n-1 walk the visible query tiles (descending) of the group's
   // heads in turn: head bh0 + t / n1, query tile qt_hi - t % n1.
   const int n1 = qt_hi >= qt_lo ? qt_hi - qt_lo + 1 : 0;  // query tiles per head
@@ -487,7 +492,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
     } else if (!DS_OUT && warp == 15) {
       // Idle on this route: this CTA's share of the group's empty key tiles,
       // and the dBias blocks of its key tile that no CTA computes.
-      if (!p.deterministic) zero_group_share_of_empty_key_tiles(p, out_head, kt, Lq, Lk, lane);
+      if (!MOD && !p.deterministic) zero_group_share_of_empty_key_tiles(p, out_head, kt, Lq, Lk, lane);
       if (BIAS && p.dbias != nullptr && !p.dbias_red)
         zero_unvisited_dbias_blocks(p, b, bh0, p.gsz, kt, qt_lo, qt_hi, lane, 32);
     } else if (DS_OUT && warp == 15) {
@@ -519,7 +524,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
     regs_decrease<REGS_DQ>();
     // Idle on the two-kernel route: warp 9 writes this CTA's share of the
     // group's empty key tiles.
-    if (DS_OUT && warp == 9 && !p.deterministic)
+    if (!MOD && DS_OUT && warp == 9 && !p.deterministic)
       zero_group_share_of_empty_key_tiles(p, out_head, kt, Lq, Lk, lane);
     // ... and the dBias blocks of this key tile that no CTA computes.
     if (BIAS && DS_OUT && p.dbias != nullptr && !p.dbias_red)
@@ -677,6 +682,9 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
                              (p.causal && (long long)q0 < (long long)(k0 + BN - 1) - diag - Rp) ||
                              (has_window && (long long)(q0 + BQ - 1) > (long long)k0 - diag + p.window_left);
       const long long bias_off = BIAS ? bias_tile_off(t) : 0;
+      ModTile mt;
+      if constexpr (MOD)
+        mt = mod_tile(p, b, bh0 + t / n1 - b * p.Hq, qt, k0, k, Lk, diag, need_mask, q_lo_vis, q_hi_vis);
 
       // ---- softmax replay: P^T from S^T. The row statistics were written by
       // TMA, so this thread waits on the stage's transaction barrier itself.
@@ -684,6 +692,20 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
           !mbar_wait(&bars[BAR_SFULL + slot], j & 1, abort_flag, WAIT_LIMIT_NS)) { ok = false; break; }
       __syncwarp();
       tc_fence_after();
+      if constexpr (MOD) {
+        // Modified scores: P^T formed, masked and written out half by half.
+        uint32_t ra[32], rb[32], w[16];
+        tmem_ld32(t_lane + L::col_s(slot), ra);
+        tmem_ld32(t_lane + L::col_s(slot) + 32, rb);
+        tmem_ld_wait(ra);
+        tmem_ld_wait(rb);
+        mod_replay_half<F16, 0>(mt, qs, ra, P, w);
+        __syncwarp();
+        tmem_st16(t_lane + L::col_s(slot), w);
+        mod_replay_half<F16, 1>(mt, qs, rb, P, w);
+        __syncwarp();
+        tmem_st16(t_lane + L::col_s(slot) + 16, w);
+      } else {
       {
         uint32_t ra[32], rb[32];
         tmem_ld32(t_lane + L::col_s(slot), ra);
@@ -732,6 +754,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
           for (int i = 0; i < 16; ++i) w[i] = pack_io2<F16>(P[c16 * 32 + 2 * i], P[c16 * 32 + 2 * i + 1]);
         }
         tmem_st16(t_lane + L::col_s(slot) + c16 * 16, w);
+      }
       }
       tmem_st_wait();
       tc_fence_before();
@@ -879,34 +902,34 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
   }
 }
 
-template <int D, bool DS_OUT, bool BIAS, bool QAT = false, bool F16 = false>
+template <int D, bool DS_OUT, bool BIAS, bool QAT = false, bool F16 = false, bool MOD = false>
 static cudaError_t set_main_smem() {
-  return cudaFuncSetAttribute(sdpa_bwd_main<D, DS_OUT, BIAS, QAT, F16>,
+  return cudaFuncSetAttribute(sdpa_bwd_main<D, DS_OUT, BIAS, QAT, F16, MOD>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, MainLayout<D, DS_OUT>::BYTES);
 }
 
 // One CTA per (key tile, head group) work unit.
-template <bool BIAS, bool F16 = false>
+template <bool BIAS, bool F16 = false, bool MOD = false>
 static cudaError_t launch_main_variant(const MainMaps& maps, const ChainParams& p, cudaStream_t s) {
   const dim3 grid((unsigned)(p.n_kt * p.B * p.Hkv * p.n_part));
   const dim3 block(MAIN_THREADS);
   // D_qk = D_v up to 64 runs on the 64-column kernels, up to 128 on the 128-column
   // ones: TMA zero-fills the columns past D on loads and drops them on stores.
   if (p.Dqk <= 64)
-    return launch_kernel(sdpa_bwd_main<64, false, BIAS, false, F16>, grid, block,
+    return launch_kernel(sdpa_bwd_main<64, false, BIAS, false, F16, MOD>, grid, block,
                          MainLayout<64, false>::BYTES, s, true, maps, p);
   if (p.ds_route)
-    return launch_kernel(sdpa_bwd_main<128, true, BIAS, false, F16>, grid, block,
+    return launch_kernel(sdpa_bwd_main<128, true, BIAS, false, F16, MOD>, grid, block,
                          MainLayout<128, true>::BYTES, s, true, maps, p);
-  return launch_kernel(sdpa_bwd_main<128, false, BIAS, false, F16>, grid, block,
+  return launch_kernel(sdpa_bwd_main<128, false, BIAS, false, F16, MOD>, grid, block,
                        MainLayout<128, false>::BYTES, s, true, maps, p);
 }
 
-template <bool BIAS, bool F16 = false>
+template <bool BIAS, bool F16 = false, bool MOD = false>
 static cudaError_t main_variant_setup() {
-  cudaError_t e = set_main_smem<64, false, BIAS, false, F16>();
-  if (e == cudaSuccess) e = set_main_smem<128, false, BIAS, false, F16>();
-  if (e == cudaSuccess) e = set_main_smem<128, true, BIAS, false, F16>();
+  cudaError_t e = set_main_smem<64, false, BIAS, false, F16, MOD>();
+  if (e == cudaSuccess) e = set_main_smem<128, false, BIAS, false, F16, MOD>();
+  if (e == cudaSuccess) e = set_main_smem<128, true, BIAS, false, F16, MOD>();
   return e;
 }
 

@@ -113,7 +113,8 @@ struct Layout {
 // D_qk 64/128 kernel (bias.cuh): loads of the next tile's bias column issued
 // right after dS, dS' stored as dBias, and the dBias blocks no CTA computes
 // zeroed by an idle warp (or by an empty unit's whole CTA).
-template <int DQK, int DV, bool BIAS, bool F16 = false, int SPLIT = 1>
+// MOD: capped and distance-biased scores and row ranges (score.cuh).
+template <int DQK, int DV, bool BIAS, bool F16 = false, int SPLIT = 1, bool MOD = false>
 __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
     sdpa_bwd_main_ds(const __grid_constant__ MainMaps maps, const ChainParams p) {
   using namespace ds_kernel;
@@ -146,10 +147,13 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
     batch_lengths(p, b0, Lq0, Lk0);
     visited_query_tiles(kt0, Lq0, Lk0, p.causal, p.bottom_right, p.window_left, p.window_right, lo0,
                         hi0);
+    if constexpr (MOD) planned_query_tiles(p.mods, b0, kt0, p.n_kt, lo0, hi0);
     if (hi0 < lo0) {
       if (blockIdx.x % SPLIT != 0) return;  // the first half-unit writes the zeros
       // gsz = 1: the partial set of a query head is its bh index.
-      if (!row_has_visible_pair(Lq0, Lk0))
+      // (Under row ranges each empty tile writes its own zeros: they can leave
+      // every key tile of a row empty.)
+      if (MOD || !row_has_visible_pair(Lq0, Lk0))
         zero_key_tile_rows(p, p.dk_ws ? (long long)bh0 : (long long)b0 * p.Hkv + (bh0 % p.Hq) / p.G,
                                     kt0 * BN);
       if (BIAS && p.dbias != nullptr && !p.dbias_red)
@@ -206,6 +210,7 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
   int qt_lo, qt_hi;
   visited_query_tiles(kt, Lq, Lk, p.causal, p.bottom_right, p.window_left, p.window_right, qt_lo,
                       qt_hi);
+  if constexpr (MOD) planned_query_tiles(p.mods, b, kt, p.n_kt, qt_lo, qt_hi);
   const int n = qt_hi - qt_lo + 1;
 
   constexpr uint32_t ID_G1 = idesc_io(128, BQ, false, false, F16);
@@ -370,7 +375,7 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
       }
       bulk_wait_group_read0();
     }
-  } else if (warp == 13 && lead) {
+  } else if (!MOD && warp == 13 && lead) {
     // This CTA's share of the head's empty key tiles (gsz = 1: the partial
     // set of a query head is its bh index).
     zero_group_share_of_empty_key_tiles(p, p.dk_ws ? (long long)bh : (long long)b * p.Hkv + hk,
@@ -416,10 +421,13 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
       const bool need_mask = (k0 + BN > Lk) ||
                              (p.causal && (long long)q0 < (long long)(k0 + BN - 1) - diag - Rp) ||
                              (has_window && (long long)(q0 + BQ - 1) > (long long)k0 - diag + p.window_left);
+      ModTile mt;
+      if constexpr (MOD) mt = mod_tile(p, b, h, qt, k0, k, Lk, diag, need_mask, q_lo_vis, q_hi_vis);
       if (!mbar_wait(&bars[BAR_QFULL + st], (t / NQ) & 1, abort_flag, WAIT_LIMIT_NS) ||
           !mbar_wait(&bars[BAR_SFULL + slot], j & 1, abort_flag, WAIT_LIMIT_NS)) { ok = false; break; }
       __syncwarp();
       tc_fence_after();
+      uint32_t pw[MOD ? 2 : 1][16];  // MOD: the packed probabilities of both halves
       {
         uint32_t ra[32], rb[32];
         tmem_ld32(t_lane + L::col_s(slot), ra);
@@ -428,6 +436,10 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
         tmem_ld_wait(rb);
         tc_fence_before();
         mbar_arrive(&bars[BAR_SREAD + slot]);  // the S^T columns may be overwritten
+        if constexpr (MOD) {
+          mod_replay_half<F16, 0>(mt, qs, ra, P, pw[0]);
+          mod_replay_half<F16, 1>(mt, qs, rb, P, pw[1]);
+        } else {
         const float4* lse4 = reinterpret_cast<const float4*>(qs);
 #pragma unroll
         for (int i4 = 0; i4 < BQ / 4; ++i4) {
@@ -445,8 +457,9 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) P[i4 * 4 + e] = ex2_approx(x[e]);
         }
+        }
       }
-      if (need_mask) {
+      if (!MOD && need_mask) {
 #pragma unroll
         for (int i = 0; i < BQ; ++i) {
           const long long q = q0 + i;
@@ -458,10 +471,14 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
       __syncwarp();
 #pragma unroll
       for (int c16 = 0; c16 < 2; ++c16) {
-        uint32_t w[16];
+        if constexpr (MOD) {
+          tmem_st16(t_lane + L::col_p(slot) + c16 * 16, pw[c16]);
+        } else {
+          uint32_t w[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = pack_io2<F16>(P[c16 * 32 + 2 * i], P[c16 * 32 + 2 * i + 1]);
-        tmem_st16(t_lane + L::col_p(slot) + c16 * 16, w);
+          for (int i = 0; i < 16; ++i) w[i] = pack_io2<F16>(P[c16 * 32 + 2 * i], P[c16 * 32 + 2 * i + 1]);
+          tmem_st16(t_lane + L::col_p(slot) + c16 * 16, w);
+        }
       }
       tmem_st_wait();
       tc_fence_before();
@@ -603,9 +620,9 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
   }
 }
 
-template <int DQK, int DV, bool BIAS, bool F16, int SPLIT>
+template <int DQK, int DV, bool BIAS, bool F16, int SPLIT, bool MOD = false>
 static cudaError_t set_ds_smem() {
-  return cudaFuncSetAttribute(sdpa_bwd_main_ds<DQK, DV, BIAS, F16, SPLIT>,
+  return cudaFuncSetAttribute(sdpa_bwd_main_ds<DQK, DV, BIAS, F16, SPLIT, MOD>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
                               ds_kernel::Layout<DQK, DV, SPLIT>::BYTES);
 }
@@ -616,6 +633,8 @@ static cudaError_t set_ds_smem_all() {
   if (e == cudaSuccess) e = set_ds_smem<DQK, DV, true, false, SPLIT>();
   if (e == cudaSuccess) e = set_ds_smem<DQK, DV, false, true, SPLIT>();
   if (e == cudaSuccess) e = set_ds_smem<DQK, DV, true, true, SPLIT>();
+  if (e == cudaSuccess) e = set_ds_smem<DQK, DV, false, false, SPLIT, true>();
+  if (e == cudaSuccess) e = set_ds_smem<DQK, DV, false, true, SPLIT, true>();
   return e;
 }
 
@@ -631,6 +650,10 @@ static cudaError_t launch_main_ds_dims(const MainMaps& maps, const ChainParams& 
   const dim3 grid((unsigned)(p.n_kt * p.B * p.Hq * SPLIT));
   const dim3 block(ds_kernel::THREADS);
   constexpr int bytes = ds_kernel::Layout<DQK, DV, SPLIT>::BYTES;
+  if (p.mods.on && p.f16)
+    return launch_kernel(sdpa_bwd_main_ds<DQK, DV, false, true, SPLIT, true>, grid, block, bytes, s, true, maps, p);
+  if (p.mods.on)
+    return launch_kernel(sdpa_bwd_main_ds<DQK, DV, false, false, SPLIT, true>, grid, block, bytes, s, true, maps, p);
   if (p.bias != nullptr && p.f16)
     return launch_kernel(sdpa_bwd_main_ds<DQK, DV, true, true, SPLIT>, grid, block, bytes, s, true, maps, p);
   if (p.bias != nullptr)

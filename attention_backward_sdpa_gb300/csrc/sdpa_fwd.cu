@@ -115,7 +115,8 @@ __device__ int g_fwd_done[FWD_SLOTS];
 // CTA per SM takes items from the launch's ticket, and the K/V ring, the S/P
 // slots and their barrier phases run on from one item to the next; otherwise
 // one item per CTA (blockIdx.x).
-template <int DQK, int DV, bool BIAS, bool F16 = false, bool PERSIST = false>
+// MOD: capped and distance-biased scores and row ranges (score.cuh).
+template <int DQK, int DV, bool BIAS, bool F16 = false, bool PERSIST = false, bool MOD = false>
 __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
     sdpa_fwd_kernel(const __grid_constant__ FwdMaps maps, const FwdParams p, const int ticket_slot) {
   using namespace fwd_kernel;
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
             it = e == 0 ? (int)blockIdx.x : -1;
           }
           if (it < 0) break;
-          const FwdItem w = fwd_item(p, it);
+          const FwdItem w = fwd_item<MOD>(p, it);
           if (w.n <= 0) continue;
           // The item's first key tiles only wait for stages that earlier items
           // release, so they load before its Q, which waits for the previous
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
       for (int e = 0; e < E_MAX && ok; ++e) {
         const int it = next_item(e);
         if (it < 0) break;
-        const FwdItem w = fwd_item(p, it);
+        const FwdItem w = fwd_item<MOD>(p, it);
         if (w.n <= 0) continue;
         if (warp == 9) {
           ok = mbar_wait(&bars[BAR_QFULL], ni & 1, abort_flag, WAIT_LIMIT_NS);
@@ -322,7 +323,9 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
     const int i0 = half * 64;  // this half's first key within a tile
     // With a bias the scores are rewritten in place as x = s * c + bias * log2e,
     // and everything below reads them with the factor cs = 1 instead of c.
-    const float cs = BIAS ? 1.f : c;
+    // (The same for capped or distance-biased scores.)
+    const bool modified = MOD && (p.mods.cap_in != 0.f || p.mods.slopes != nullptr);
+    const float cs = (BIAS || modified) ? 1.f : c;
     uint16_t* const o_base = static_cast<uint16_t*>(p.o);
     const size_t o_bytes = (size_t)p.B * p.Hq * p.Sq * p.Dv * 2;
     // O rows go out in 32-byte stores when every 16-column piece is 32-byte
@@ -353,7 +356,7 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         it = next_item(e);
       }
       if (it < 0) break;
-      const FwdItem w = fwd_item(p, it);
+      const FwdItem w = fwd_item<MOD>(p, it);
       const int q = w.q0 + row;
       const long long orow = (long long)w.bh * p.Sq + q;  // O / LSE row
       if (w.n <= 0) {
@@ -373,8 +376,10 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         m = p.sink[w.h] * 1.4426950408889634f;
         l = 1.f;
       }
-      const long long k_vis_hi = p.causal ? (long long)q + w.diag + Rp : (1ll << 40);
-      const long long k_vis_lo = has_window ? (long long)q + w.diag - p.window_left : -(1ll << 40);
+      long long k_vis_hi = p.causal ? (long long)q + w.diag + Rp : (1ll << 40);
+      long long k_vis_lo = has_window ? (long long)q + w.diag - p.window_left : -(1ll << 40);
+      float slope2 = 0.f;
+      if constexpr (MOD) mod_row(p, w, q, live, k_vis_lo, k_vis_hi, slope2);
       const long long bias_row =
           BIAS ? (long long)(w.bh / p.Hq) * p.bias_bstride + ((long long)w.h * p.Sq + q) * p.Skv : 0;
       for (int j = 0; j < w.n; ++j, ++g) {
@@ -401,6 +406,9 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         tmem_ld_wait(sr[0]);
         tmem_ld_wait(sr[1]);
         if constexpr (BIAS) add_bias_row(p, c, braw, bpacked, sr);
+        if constexpr (MOD) {
+          if (modified) modify_score_row(p.mods, c, slope2, (float)(q + w.diag - (k0 + i0)), sr);
+        }
         // Visible keys of this row within the tile: [v_lo, v_hi] relative to k0.
         int v_lo = 0, v_hi = BK - 1;
         if (!live) {
@@ -608,16 +616,16 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
   }
 }
 
-template <int DQK, int DV, bool BIAS, bool F16>
+template <int DQK, int DV, bool BIAS, bool F16, bool MOD>
 static cudaError_t set_fwd_smem() {
-  return cudaFuncSetAttribute(sdpa_fwd_kernel<DQK, DV, BIAS, F16, true>,
+  return cudaFuncSetAttribute(sdpa_fwd_kernel<DQK, DV, BIAS, F16, true, MOD>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, fwd_kernel::Layout<DQK, DV>::BYTES);
 }
 
-template <bool BIAS, bool F16>
+template <bool BIAS, bool F16, bool MOD = false>
 static cudaError_t fwd_setup_variant() {
-  cudaError_t e = set_fwd_smem<64, 64, BIAS, F16>();
-  if (e == cudaSuccess) e = set_fwd_smem<128, 128, BIAS, F16>();
+  cudaError_t e = set_fwd_smem<64, 64, BIAS, F16, MOD>();
+  if (e == cudaSuccess) e = set_fwd_smem<128, 128, BIAS, F16, MOD>();
   return e;
 }
 
@@ -626,12 +634,14 @@ cudaError_t fwd_kernel_setup() {
   if (e == cudaSuccess) e = fwd_setup_variant<true, false>();
   if (e == cudaSuccess) e = fwd_setup_variant<false, true>();
   if (e == cudaSuccess) e = fwd_setup_variant<true, true>();
+  if (e == cudaSuccess) e = fwd_setup_variant<false, false, true>();
+  if (e == cudaSuccess) e = fwd_setup_variant<false, true, true>();
   if (e == cudaSuccess) e = fwd_shared_setup();
   if (e == cudaSuccess) e = fwd_wide_setup();
   return e;
 }
 
-template <bool BIAS, bool F16>
+template <bool BIAS, bool F16, bool MOD = false>
 static cudaError_t launch_fwd_variant(const FwdMaps& maps, const FwdParams& p, cudaStream_t s, int sms,
                                       int slot) {
   // Persistent: one CTA per SM (more than half its shared memory each) taking
@@ -643,10 +653,10 @@ static cudaError_t launch_fwd_variant(const FwdMaps& maps, const FwdParams& p, c
   // D_qk = D_v up to 64 runs on the 64-column kernel, up to 128 on the 128-column
   // one: TMA zero-fills the columns past D on loads and drops them on stores.
   if (p.Dqk <= 64 && p.Dv == p.Dqk)
-    return launch_kernel(sdpa_fwd_kernel<64, 64, BIAS, F16, PERSIST>, grid, block,
+    return launch_kernel(sdpa_fwd_kernel<64, 64, BIAS, F16, PERSIST, MOD>, grid, block,
                          fwd_kernel::Layout<64, 64>::BYTES, s, false, maps, p, slot);
   if (p.Dqk <= 128 && p.Dv == p.Dqk)
-    return launch_kernel(sdpa_fwd_kernel<128, 128, BIAS, F16, PERSIST>, grid, block,
+    return launch_kernel(sdpa_fwd_kernel<128, 128, BIAS, F16, PERSIST, MOD>, grid, block,
                          fwd_kernel::Layout<128, 128>::BYTES, s, false, maps, p, slot);
   return cudaErrorInvalidValue;
 }
@@ -663,6 +673,9 @@ cudaError_t launch_fwd(const FwdMaps& maps, const FwdParams& p, cudaStream_t s) 
   // (sdpa_fwd_wide.cu).
   if (p.Dqk == 192 && p.Dv == 128) return launch_fwd_shared(maps, p, s, sms, slot);
   if (p.Dqk == 256 && p.Dv == 256) return launch_fwd_wide(maps, p, s, sms, slot);
+  if (p.mods.on)
+    return p.f16 ? launch_fwd_variant<false, true, true>(maps, p, s, sms, slot)
+                 : launch_fwd_variant<false, false, true>(maps, p, s, sms, slot);
   if (p.bias)
     return p.f16 ? launch_fwd_variant<true, true>(maps, p, s, sms, slot)
                  : launch_fwd_variant<true, false>(maps, p, s, sms, slot);

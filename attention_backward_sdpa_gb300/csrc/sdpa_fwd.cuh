@@ -118,6 +118,39 @@ __device__ __forceinline__ void add_bias_row(const FwdParams& p, float c, const 
   }
 }
 
+// A thread's 64 scores of a tile rewritten as the modified scores times log2(e)
+// (score.cuh): scores S of its row and keys kb .. kb + 63, `slope2` the head's slope
+// times log2(e) (0 without slopes) and `dist` = q + diag - kb. The cap's branch and
+// the slopes' are uniform across the launch; the polynomial alone serves a warp
+// whose 64 x 32 scores all stay within its range, which they do unless scores come
+// near the cap.
+__device__ __forceinline__ void modify_score_row(const ScoreMods& m, float c, float slope2, float dist,
+                                                 uint32_t (&sr)[2][32]) {
+  if (m.cap_in != 0.f) {
+    float big = 0.f;
+#pragma unroll
+    for (int i = 0; i < 64; ++i) big = fmaxf(big, fabsf(__uint_as_float(sr[i >> 5][i & 31])));
+    if (__all_sync(0xffffffffu, big * m.cap_in <= TANH_SMALL)) {
+#pragma unroll
+      for (int i = 0; i < 64; ++i)
+        sr[i >> 5][i & 31] = __float_as_uint(m.cap_log2 * tanh_small(__uint_as_float(sr[i >> 5][i & 31]) * m.cap_in));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 64; ++i)
+        sr[i >> 5][i & 31] = __float_as_uint(m.cap_log2 * tanh_any(__uint_as_float(sr[i >> 5][i & 31]) * m.cap_in));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 64; ++i) sr[i >> 5][i & 31] = __float_as_uint(__uint_as_float(sr[i >> 5][i & 31]) * c);
+  }
+  if (m.slopes != nullptr) {
+#pragma unroll
+    for (int i = 0; i < 64; ++i)
+      sr[i >> 5][i & 31] =
+          __float_as_uint(fmaf(-slope2, fabsf(dist - (float)i), __uint_as_float(sr[i >> 5][i & 31])));
+  }
+}
+
 // One work item: 128 query rows (query tile qt, descending so that under a
 // causal mask the longest items come first) of one (batch, query head), and the
 // range [kt_lo, kt_lo + n) of 128-key tiles that any of its live rows sees.
@@ -126,6 +159,7 @@ struct FwdItem {
   long long diag;
 };
 
+template <bool MOD = false>
 __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int it) {
   FwdItem w;
   const int BH = p.B * p.Hq;
@@ -147,6 +181,20 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int it) {
     long long k_hi = w.Lk - 1, k_lo = 0;
     if (p.causal) k_hi = min(k_hi, q_last + w.diag + Rp);
     if (p.window_left >= 0) k_lo = max(0ll, (long long)w.q0 + w.diag - p.window_left);
+    if constexpr (MOD) {
+      if (p.mods.q_sum != nullptr) {  // the hull of the rows' ranges (two 64-row tiles)
+        const int n64 = ceil_div(p.Sq, BQ);
+        const int4* qs = p.mods.q_sum + (long long)b * n64 + 2 * w.qt;
+        int4 s = qs[0];
+        if (2 * w.qt + 1 < n64) {
+          const int4 s1 = qs[1];
+          s.x = min(s.x, s1.x);
+          s.y = max(s.y, s1.y);
+        }
+        k_lo = max(k_lo, (long long)s.x);
+        k_hi = min(k_hi, (long long)s.y - 1);
+      }
+    }
     if (k_lo <= k_hi) {
       kt_lo = (int)(k_lo / fwd_shared::BK);
       kt_hi = (int)(k_hi / fwd_shared::BK);
@@ -155,6 +203,18 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int it) {
   w.kt_lo = kt_lo;
   w.n = kt_hi - kt_lo + 1;  // may be 0
   return w;
+}
+
+// What the modified scores add to row q's state of item w: its key range (a mask
+// plan) joins the visible bounds [lo, hi], and the head's distance slope in log2 units.
+__device__ __forceinline__ void mod_row(const FwdParams& p, const FwdItem& w, int q, bool live, long long& lo,
+                                        long long& hi, float& slope2) {
+  if (p.mods.ranges != nullptr && live) {
+    const int2 r = p.mods.ranges[(long long)(w.bh / p.Hq) * ceil_div(p.Sq, BQ) * BQ + q];
+    lo = max(lo, (long long)r.x);
+    hi = min(hi, (long long)r.y - 1);
+  }
+  if (p.mods.slopes != nullptr) slope2 = p.mods.slopes[w.h] * 1.4426950408889634f;
 }
 
 // One 32-byte global store of two 16-byte halves (the address 32-byte aligned):

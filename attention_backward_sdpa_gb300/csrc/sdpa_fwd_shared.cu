@@ -127,7 +127,8 @@ __device__ int g_fwd_sh_done[FWD_SLOTS];
 // CTA per SM takes items from the launch's ticket, and the K/V ring, the S/P
 // slots and their barrier phases run on from one item to the next; otherwise
 // one item per CTA (blockIdx.x).
-template <int DQK, int DV, bool BIAS, bool F16 = false, bool PERSIST = false>
+// MOD: capped and distance-biased scores and row ranges (score.cuh).
+template <int DQK, int DV, bool BIAS, bool F16 = false, bool PERSIST = false, bool MOD = false>
 __global__ void __launch_bounds__(fwd_sh::THREADS, 1)
     sdpa_fwd_shared_kernel(const __grid_constant__ FwdMaps maps, const FwdParams p, const int ticket_slot) {
   using namespace fwd_sh;
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(fwd_sh::THREADS, 1)
             it = e == 0 ? (int)blockIdx.x : -1;
           }
           if (it < 0) break;
-          const FwdItem w = fwd_item(p, it);
+          const FwdItem w = fwd_item<MOD>(p, it);
           if (w.n <= 0) continue;
           // The item's first key tiles only wait for stages that earlier items
           // release, so they load before its Q, which waits for the previous
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(fwd_sh::THREADS, 1)
         for (int e = 0; e < E_MAX && ok; ++e) {
           const int it = ring_take(e);
           if (it < 0) break;
-          const FwdItem w = fwd_item(p, it);
+          const FwdItem w = fwd_item<MOD>(p, it);
           for (int j = 0; j < w.n && ok; ++j, ++g) {
             const int st = g % NS;
             if (g >= NS) ok = mbar_wait(&bars[BAR_VEMPTY + st], ((g / NS) - 1) & 1, abort_flag, WAIT_LIMIT_NS);
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(fwd_sh::THREADS, 1)
       for (int e = 0; e < E_MAX && ok; ++e) {
         const int it = next_item(e);
         if (it < 0) break;
-        const FwdItem w = fwd_item(p, it);
+        const FwdItem w = fwd_item<MOD>(p, it);
         if (w.n <= 0) continue;
         if (warp == 9) {
           ok = mbar_wait(&bars[BAR_QFULL], ni & 1, abort_flag, WAIT_LIMIT_NS);
@@ -361,7 +362,9 @@ __global__ void __launch_bounds__(fwd_sh::THREADS, 1)
     const int i0 = half * 64;  // this warpgroup's first key within a tile
     // With a bias the scores are rewritten in place as x = s * c + bias * log2e,
     // and everything below reads them with the factor cs = 1 instead of c.
-    const float cs = BIAS ? 1.f : c;
+    // (The same for capped or distance-biased scores.)
+    const bool modified = MOD && (p.mods.cap_in != 0.f || p.mods.slopes != nullptr);
+    const float cs = (BIAS || modified) ? 1.f : c;
     uint16_t* const o_base = static_cast<uint16_t*>(p.o);
     const size_t o_bytes = (size_t)p.B * p.Hq * p.Sq * p.Dv * 2;
     // O rows go out in 32-byte stores when every 16-column piece is 32-byte
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(fwd_sh::THREADS, 1)
         it = next_item(e);
       }
       if (it < 0) break;
-      const FwdItem w = fwd_item(p, it);
+      const FwdItem w = fwd_item<MOD>(p, it);
       const int q = w.q0 + row;
       const long long orow = (long long)w.bh * p.Sq + q;  // O / LSE row
       if (w.n <= 0) {
@@ -414,8 +417,10 @@ __global__ void __launch_bounds__(fwd_sh::THREADS, 1)
         m = p.sink[w.h] * 1.4426950408889634f;
         l = half == 0 ? 1.f : 0.f;
       }
-      const long long k_vis_hi = p.causal ? (long long)q + w.diag + Rp : (1ll << 40);
-      const long long k_vis_lo = has_window ? (long long)q + w.diag - p.window_left : -(1ll << 40);
+      long long k_vis_hi = p.causal ? (long long)q + w.diag + Rp : (1ll << 40);
+      long long k_vis_lo = has_window ? (long long)q + w.diag - p.window_left : -(1ll << 40);
+      float slope2 = 0.f;
+      if constexpr (MOD) mod_row(p, w, q, live, k_vis_lo, k_vis_hi, slope2);
       const long long bias_row =
           BIAS ? (long long)(w.bh / p.Hq) * p.bias_bstride + ((long long)w.h * p.Sq + q) * p.Skv : 0;
       for (int j = 0; j < w.n; ++j, ++g) {
@@ -449,6 +454,9 @@ __global__ void __launch_bounds__(fwd_sh::THREADS, 1)
           tmem_ld_wait(sr[0]);
           tmem_ld_wait(sr[1]);
           if constexpr (BIAS) add_bias_row(p, c, braw, bpacked, sr);
+          if constexpr (MOD) {
+            if (modified) modify_score_row(p.mods, c, slope2, (float)(q + w.diag - (k0 + i0)), sr);
+          }
           // Visible keys of this row within the tile: [v_lo, v_hi] relative to k0.
           if (live) {
             v_hi = (int)min((long long)BK - 1, min((long long)w.Lk - 1, k_vis_hi) - k0);
@@ -658,9 +666,9 @@ __global__ void __launch_bounds__(fwd_sh::THREADS, 1)
   }
 }
 
-template <bool BIAS, bool F16>
+template <bool BIAS, bool F16, bool MOD = false>
 static cudaError_t set_fwd_shared_smem() {
-  return cudaFuncSetAttribute(sdpa_fwd_shared_kernel<192, 128, BIAS, F16, true>,
+  return cudaFuncSetAttribute(sdpa_fwd_shared_kernel<192, 128, BIAS, F16, true, MOD>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, fwd_sh::Layout<192, 128>::BYTES);
 }
 
@@ -669,21 +677,26 @@ cudaError_t fwd_shared_setup() {
   if (e == cudaSuccess) e = set_fwd_shared_smem<true, false>();
   if (e == cudaSuccess) e = set_fwd_shared_smem<false, true>();
   if (e == cudaSuccess) e = set_fwd_shared_smem<true, true>();
+  if (e == cudaSuccess) e = set_fwd_shared_smem<false, false, true>();
+  if (e == cudaSuccess) e = set_fwd_shared_smem<false, true, true>();
   return e;
 }
 
-template <bool BIAS, bool F16>
+template <bool BIAS, bool F16, bool MOD = false>
 static cudaError_t launch_shared_variant(const FwdMaps& maps, const FwdParams& p, cudaStream_t s, int sms,
                                          int slot) {
   const long long items = (long long)p.n_qt * p.B * p.Hq;
   const dim3 grid((unsigned)(items < sms ? items : sms));
-  return launch_kernel(sdpa_fwd_shared_kernel<192, 128, BIAS, F16, true>, grid, dim3(fwd_sh::THREADS),
+  return launch_kernel(sdpa_fwd_shared_kernel<192, 128, BIAS, F16, true, MOD>, grid, dim3(fwd_sh::THREADS),
                        fwd_sh::Layout<192, 128>::BYTES, s, false, maps, p, slot);
 }
 
 cudaError_t launch_fwd_shared(const FwdMaps& maps, const FwdParams& p, cudaStream_t s, int sms, int slot) {
   if (p.Dqk != 192 || p.Dv != 128 || sms <= 0 || slot < 0 || slot >= fwd_shared::FWD_SLOTS)
     return cudaErrorInvalidValue;
+  if (p.mods.on)
+    return p.f16 ? launch_shared_variant<false, true, true>(maps, p, s, sms, slot)
+                 : launch_shared_variant<false, false, true>(maps, p, s, sms, slot);
   if (p.bias)
     return p.f16 ? launch_shared_variant<true, true>(maps, p, s, sms, slot)
                  : launch_shared_variant<true, false>(maps, p, s, sms, slot);

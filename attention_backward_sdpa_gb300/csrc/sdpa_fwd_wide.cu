@@ -102,7 +102,8 @@ __device__ int g_fwd_wide_done[fwd_shared::FWD_SLOTS];
 
 // BIAS adds the additive bias (FwdParams::bias) to the scaled scores. F16: fp16
 // io tensors (and fp16 P for the PV GEMM) instead of bf16.
-template <bool BIAS, bool F16>
+// MOD: capped and distance-biased scores and row ranges (score.cuh).
+template <bool BIAS, bool F16, bool MOD = false>
 __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
     sdpa_fwd_wide_kernel(const __grid_constant__ FwdMaps maps, const FwdParams p, const int ticket_slot) {
   using namespace fwd_wide;
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
         ring[r] = it;
         mbar_arrive(&bars[BAR_RFULL + r]);
         if (it < 0) break;
-        const FwdItem w = fwd_item(p, it);
+        const FwdItem w = fwd_item<MOD>(p, it);
         if (w.n <= 0) continue;
         for (int j = 0; j < w.n && ok; ++j, ++g) {
           // Block b of K(g) replaces that of K(g - 1) once G1(g - 1)'s MMAs over
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
       for (int e = 0; ok; ++e) {
         const int it = ring_take(e);
         if (it < 0) break;
-        const FwdItem w = fwd_item(p, it);
+        const FwdItem w = fwd_item<MOD>(p, it);
         for (int j = 0; j < w.n && ok; ++j, ++g) {
           // Keys 32 r .. 32 r + 31 of V(g) replace those of V(g - 1) once G2(g - 1)'s
           // MMAs over them have completed: four 32-row boxes, one per 64-column
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
       for (int e = 0; ok; ++e) {
         const int it = ring_take(e);
         if (it < 0) break;
-        const FwdItem w = fwd_item(p, it);
+        const FwdItem w = fwd_item<MOD>(p, it);
         if (w.n <= 0) continue;
         ok = mbar_wait(&bars[BAR_QFULL], ni & 1, abort_flag, WAIT_LIMIT_NS);
         for (int j = 0; j < w.n && ok; ++j, ++g) {
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
       for (int e = 0; ok; ++e) {
         const int it = ring_take(e);
         if (it < 0) break;
-        const FwdItem w = fwd_item(p, it);
+        const FwdItem w = fwd_item<MOD>(p, it);
         for (int u = 0; u < w.n && ok; ++u, ++g) {
           const int s = g & 1;
           // (The previous item's epilogue has read O before any P of this item
@@ -305,7 +306,9 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
     const int i0 = half * 64;  // this warpgroup's first key within a tile
     // With a bias the scores are rewritten in place as x = s * c + bias * log2e,
     // and everything below reads them with the factor cs = 1 instead of c.
-    const float cs = BIAS ? 1.f : c;
+    // (The same for capped or distance-biased scores.)
+    const bool modified = MOD && (p.mods.cap_in != 0.f || p.mods.slopes != nullptr);
+    const float cs = (BIAS || modified) ? 1.f : c;
     uint16_t* const o_base = static_cast<uint16_t*>(p.o);
     const size_t o_bytes = (size_t)p.B * p.Hq * p.Sq * D * 2;
     // O rows go out in 32-byte stores when every 16-column piece is 32-byte
@@ -328,7 +331,7 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
       have_next = false;
       const int it = sitem[e & 1];
       if (it < 0) break;
-      const FwdItem w = fwd_item(p, it);
+      const FwdItem w = fwd_item<MOD>(p, it);
       const int q = w.q0 + row;
       const long long orow = (long long)w.bh * p.Sq + q;  // O / LSE row
       if (w.n <= 0) {
@@ -349,8 +352,10 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
         m = p.sink[w.h] * 1.4426950408889634f;
         l = half == 0 ? 1.f : 0.f;
       }
-      const long long k_vis_hi = p.causal ? (long long)q + w.diag + Rp : (1ll << 40);
-      const long long k_vis_lo = has_window ? (long long)q + w.diag - p.window_left : -(1ll << 40);
+      long long k_vis_hi = p.causal ? (long long)q + w.diag + Rp : (1ll << 40);
+      long long k_vis_lo = has_window ? (long long)q + w.diag - p.window_left : -(1ll << 40);
+      float slope2 = 0.f;
+      if constexpr (MOD) mod_row(p, w, q, live, k_vis_lo, k_vis_hi, slope2);
       const long long bias_row =
           BIAS ? (long long)(w.bh / p.Hq) * p.bias_bstride + ((long long)w.h * p.Sq + q) * p.Skv : 0;
       for (int j = 0; j < w.n; ++j, ++g) {
@@ -383,6 +388,9 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
           tmem_ld_wait(sr[0]);
           tmem_ld_wait(sr[1]);
           if constexpr (BIAS) add_bias_row(p, c, braw, bpacked, sr);
+          if constexpr (MOD) {
+            if (modified) modify_score_row(p.mods, c, slope2, (float)(q + w.diag - (k0 + i0)), sr);
+          }
           // Visible keys of this row within the tile: [v_lo, v_hi] relative to k0.
           if (live) {
             v_hi = (int)min((long long)BK - 1, min((long long)w.Lk - 1, k_vis_hi) - k0);
@@ -576,9 +584,9 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
   }
 }
 
-template <bool BIAS, bool F16>
+template <bool BIAS, bool F16, bool MOD = false>
 static cudaError_t set_fwd_wide_smem() {
-  return cudaFuncSetAttribute(sdpa_fwd_wide_kernel<BIAS, F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(sdpa_fwd_wide_kernel<BIAS, F16, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               fwd_wide::BYTES);
 }
 
@@ -587,21 +595,26 @@ cudaError_t fwd_wide_setup() {
   if (e == cudaSuccess) e = set_fwd_wide_smem<true, false>();
   if (e == cudaSuccess) e = set_fwd_wide_smem<false, true>();
   if (e == cudaSuccess) e = set_fwd_wide_smem<true, true>();
+  if (e == cudaSuccess) e = set_fwd_wide_smem<false, false, true>();
+  if (e == cudaSuccess) e = set_fwd_wide_smem<false, true, true>();
   return e;
 }
 
-template <bool BIAS, bool F16>
+template <bool BIAS, bool F16, bool MOD = false>
 static cudaError_t launch_wide_variant(const FwdMaps& maps, const FwdParams& p, cudaStream_t s, int sms,
                                        int slot) {
   const long long items = (long long)p.n_qt * p.B * p.Hq;
   const dim3 grid((unsigned)(items < sms ? items : sms));
-  return launch_kernel(sdpa_fwd_wide_kernel<BIAS, F16>, grid, dim3(fwd_wide::THREADS), fwd_wide::BYTES, s,
+  return launch_kernel(sdpa_fwd_wide_kernel<BIAS, F16, MOD>, grid, dim3(fwd_wide::THREADS), fwd_wide::BYTES, s,
                        false, maps, p, slot);
 }
 
 cudaError_t launch_fwd_wide(const FwdMaps& maps, const FwdParams& p, cudaStream_t s, int sms, int slot) {
   if (p.Dqk != fwd_wide::D || p.Dv != fwd_wide::D || sms <= 0 || slot < 0 || slot >= fwd_shared::FWD_SLOTS)
     return cudaErrorInvalidValue;
+  if (p.mods.on)
+    return p.f16 ? launch_wide_variant<false, true, true>(maps, p, s, sms, slot)
+                 : launch_wide_variant<false, false, true>(maps, p, s, sms, slot);
   if (p.bias)
     return p.f16 ? launch_wide_variant<true, true>(maps, p, s, sms, slot)
                  : launch_wide_variant<true, false>(maps, p, s, sms, slot);

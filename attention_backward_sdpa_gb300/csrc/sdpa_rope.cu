@@ -1,0 +1,258 @@
+// sdpa_rope.cu -- the rotary embedding of queries and keys, and its gradient.
+//
+// Column pairs (a, b) of the first rot_dim columns of a row at position t turn by
+// the angle t * f[i] (i the pair's index, f in radians per position):
+//   a' = mult * (a cos - b sin),   b' = mult * (b cos + a sin);
+// the pair is columns (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved,
+// and the columns past rot_dim pass through. The gradient is the transposed
+// rotation: the same with -sin.
+//
+// Angles. A position times a frequency in fp32 loses the angle itself far into
+// a context (at position 10^6 an fp32 angle is off by 0.03). Here each frequency
+// becomes a 64-bit fraction of a turn, f / (2 pi) * 2^64 (taken from the fp64
+// frequency: 53 bits), and the position multiplies it in wrapping 64-bit
+// integers: the product's upper 32 bits are the angle in turns modulo 1, off by
+// t * 2^-54 turns of f's own rounding and 2^-33 of the cut. They convert to fp32 in
+// [-1/2, 1/2) turns (rounded once, 2^-25 relative) and go through sincospif.
+//
+// Cost. Every element is read once and written once; the angle work of a
+// (token, pair) is shared by the heads a thread walks. So the bound is memory,
+// 4 bytes an element.
+//
+// Layout. A thread owns one token's 16 columns: eight pairs, two 16-byte loads and
+// two 16-byte stores per head, and keeps their sines and cosines in registers while
+// it walks HEADS heads, whose loads it issues together. Consecutive threads take
+// consecutive column groups, then tokens. Tensors come with any strides of batch,
+// head and position (the projection's (B, S, H, D) as a transposed view, say), so
+// that no separate transposition is needed before or after.
+#include <cuda.h>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace sdpa {
+
+namespace {
+
+constexpr int THREADS = 256;
+
+struct RopeTensor {
+  const uint16_t* x;
+  uint16_t* y;
+  long long xs[3], ys[3];  // element strides of batch, head, position
+  int H;
+};
+
+struct RopeParams {
+  RopeTensor t[2];         // queries, keys (t[1].H may be 0)
+  const double* freq;      // (rot / 2,) radians per position
+  const int32_t* positions;  // or null: offset + s
+  long long pos_bstride;   // 0: one row of positions for every batch row
+  int offset;
+  int B, S, D, rot;
+  int sign;                // +1, or -1 for the gradient
+  float mult;
+};
+
+// 2^64 * f / (2 pi) modulo 2^64, for any finite f.
+__device__ __forceinline__ uint64_t turn_fraction(double f) {
+  double t = f * 0.15915494309189533577;
+  t -= floor(t);
+  // [0, 1] in two 32-bit pieces (a product by 2^64 may round to 2^64).
+  const double hi = floor(t * 4294967296.0);
+  const double lo = (t * 4294967296.0 - hi) * 4294967296.0;
+  return ((uint64_t)hi << 32) + (uint64_t)lo;
+}
+
+__device__ __forceinline__ void angle_sin_cos(uint64_t turn, int pos, float& sn, float& cs) {
+  const uint64_t a = turn * (uint64_t)(int64_t)pos;
+  sincospif((float)(int32_t)(a >> 32) * 4.6566128730773926e-10f, &sn, &cs);  // 2^-31: half turns
+}
+
+template <bool F16>
+__device__ __forceinline__ float io_f32(uint16_t v) {
+  return F16 ? __half2float(__ushort_as_half(v)) : __uint_as_float((uint32_t)v << 16);
+}
+
+// Head h of the call's H0 + H1 heads: its tensor and the head's index there.
+__device__ __forceinline__ const RopeTensor& rope_head(const RopeParams& p, int h, int& hh) {
+  const bool second = h >= p.t[0].H;
+  hh = second ? h - p.t[0].H : h;
+  return p.t[second ? 1 : 0];
+}
+
+__device__ __forceinline__ uint32_t (&as_words(uint4& v))[4] { return reinterpret_cast<uint32_t(&)[4]>(v); }
+
+// 16-byte form: rot and D multiples of 16 (8 pairs a thread) for the rotated part,
+// pass-through columns in the same 16-column groups. A work item is (token, column
+// group); blockIdx.y selects a group of `heads` consecutive heads.
+template <bool F16, bool INTER, int UNROLL>
+__global__ void __launch_bounds__(THREADS) rope_vec(const RopeParams p, int heads, long long n_items) {
+  __shared__ uint64_t turns[256];  // rot <= 512
+  const int half = p.rot / 2;
+  for (int i = threadIdx.x; i < half; i += THREADS) turns[i] = turn_fraction(p.freq[i]);
+  __syncthreads();
+  const int groups = p.D / 16, rot_groups = p.rot / 16;
+  const int H = p.t[0].H + p.t[1].H;
+  const int h0 = blockIdx.y * heads, h1 = min(h0 + heads, H);
+  for (long long it = (long long)blockIdx.x * THREADS + threadIdx.x; it < n_items;
+       it += (long long)gridDim.x * THREADS) {
+    const int c = (int)(it % groups);
+    const long long tok = it / groups;
+    const int s = (int)(tok % p.S), b = (int)(tok / p.S);
+    // This thread's two 8-column pieces: the pairs' first and second halves, or
+    // two neighbouring pieces (interleaved, and past the rotated part).
+    const bool rotated = c < rot_groups;
+    const int c0 = (rotated && !INTER) ? c * 8 : c * 16;
+    const int c1 = (rotated && !INTER) ? half + c * 8 : c * 16 + 8;
+    float sn[8], cs[8];
+    if (rotated) {
+      const int pos = p.positions ? p.positions[b * p.pos_bstride + s] : p.offset + s;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        angle_sin_cos(turns[c * 8 + i], pos, sn[i], cs[i]);
+        sn[i] *= p.sign > 0 ? p.mult : -p.mult;
+        cs[i] *= p.mult;
+      }
+    }
+    for (int h = h0; h < h1; h += UNROLL) {
+      uint4 u[UNROLL], w[UNROLL];
+#pragma unroll
+      for (int j = 0; j < UNROLL; ++j) {
+        if (h + j >= h1) continue;
+        int hh;
+        const RopeTensor& t = rope_head(p, h + j, hh);
+        const uint16_t* x = t.x + b * t.xs[0] + hh * t.xs[1] + s * t.xs[2];
+        u[j] = *reinterpret_cast<const uint4*>(x + c0);
+        w[j] = *reinterpret_cast<const uint4*>(x + c1);
+      }
+#pragma unroll
+      for (int j = 0; j < UNROLL; ++j) {
+        if (h + j >= h1) continue;
+        int hh;
+        const RopeTensor& t = rope_head(p, h + j, hh);
+        uint16_t* y = t.y + b * t.ys[0] + hh * t.ys[1] + s * t.ys[2];
+        if (rotated) {
+          uint32_t(&a)[4] = as_words(u[j]);
+          uint32_t(&z)[4] = as_words(w[j]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (INTER) {  // a word is a pair
+              const float a0 = io_lo<F16>(a[i]), b0 = io_hi<F16>(a[i]);
+              const float a1 = io_lo<F16>(z[i]), b1 = io_hi<F16>(z[i]);
+              a[i] = pack_io2<F16>(a0 * cs[i] - b0 * sn[i], b0 * cs[i] + a0 * sn[i]);
+              z[i] = pack_io2<F16>(a1 * cs[4 + i] - b1 * sn[4 + i], b1 * cs[4 + i] + a1 * sn[4 + i]);
+            } else {
+              const float a0 = io_lo<F16>(a[i]), a1 = io_hi<F16>(a[i]);
+              const float b0 = io_lo<F16>(z[i]), b1 = io_hi<F16>(z[i]);
+              const int e = 2 * i;
+              a[i] = pack_io2<F16>(a0 * cs[e] - b0 * sn[e], a1 * cs[e + 1] - b1 * sn[e + 1]);
+              z[i] = pack_io2<F16>(b0 * cs[e] + a0 * sn[e], b1 * cs[e + 1] + a1 * sn[e + 1]);
+            }
+          }
+        }
+        *reinterpret_cast<uint4*>(y + c0) = u[j];
+        *reinterpret_cast<uint4*>(y + c1) = w[j];
+      }
+    }
+  }
+}
+
+// Any even rot, any D and any alignment: one pair (or two pass-through columns) a
+// thread, element loads.
+template <bool F16>
+__global__ void __launch_bounds__(THREADS) rope_pairs(const RopeParams p, int interleaved, int heads,
+                                                      long long n_items) {
+  __shared__ uint64_t turns[256];
+  const int half = p.rot / 2;
+  for (int i = threadIdx.x; i < half; i += THREADS) turns[i] = turn_fraction(p.freq[i]);
+  __syncthreads();
+  const int per_row = half + (p.D - p.rot + 1) / 2;
+  const int H = p.t[0].H + p.t[1].H;
+  const int h0 = blockIdx.y * heads, h1 = min(h0 + heads, H);
+  for (long long it = (long long)blockIdx.x * THREADS + threadIdx.x; it < n_items;
+       it += (long long)gridDim.x * THREADS) {
+    const int c = (int)(it % per_row);
+    const long long tok = it / per_row;
+    const int s = (int)(tok % p.S), b = (int)(tok / p.S);
+    const bool rotated = c < half;
+    const int c0 = rotated ? (interleaved ? 2 * c : c) : p.rot + 2 * (c - half);
+    const int c1 = rotated ? (interleaved ? 2 * c + 1 : c + half) : c0 + 1;
+    float sn = 0.f, cs = 0.f;
+    if (rotated) {
+      const int pos = p.positions ? p.positions[b * p.pos_bstride + s] : p.offset + s;
+      angle_sin_cos(turns[c], pos, sn, cs);
+      sn *= p.sign > 0 ? p.mult : -p.mult;
+      cs *= p.mult;
+    }
+    for (int h = h0; h < h1; ++h) {
+      int hh;
+      const RopeTensor& t = rope_head(p, h, hh);
+      const uint16_t* x = t.x + b * t.xs[0] + hh * t.xs[1] + s * t.xs[2];
+      uint16_t* y = t.y + b * t.ys[0] + hh * t.ys[1] + s * t.ys[2];
+      if (rotated) {
+        const float a = io_f32<F16>(x[c0]), z = io_f32<F16>(x[c1]);
+        const uint32_t w = pack_io2<F16>(a * cs - z * sn, z * cs + a * sn);
+        y[c0] = (uint16_t)(w & 0xFFFFu);
+        y[c1] = (uint16_t)(w >> 16);
+      } else {
+        const uint16_t a = x[c0], z = c1 < p.D ? x[c1] : (uint16_t)0;
+        y[c0] = a;
+        if (c1 < p.D) y[c1] = z;
+      }
+    }
+  }
+}
+
+// Whether every row of the tensor starts on a 16-byte boundary.
+bool rows_aligned16(const void* base, const long long (&st)[3]) {
+  return reinterpret_cast<uintptr_t>(base) % 16 == 0 && st[0] % 8 == 0 && st[1] % 8 == 0 && st[2] % 8 == 0;
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream, int num_sms) {
+  RopeParams p{};
+  bool vec = a.D % 16 == 0 && a.rot % 16 == 0;
+  for (int i = 0; i < 2; ++i) {
+    RopeTensor& t = p.t[i];
+    t.H = a.H[i];
+    if (t.H == 0) continue;
+    t.x = static_cast<const uint16_t*>(a.x[i]);
+    t.y = static_cast<uint16_t*>(a.y[i]);
+    for (int j = 0; j < 3; ++j) {
+      t.xs[j] = a.xs[3 * i + j];
+      t.ys[j] = a.ys[3 * i + j];
+    }
+    vec = vec && rows_aligned16(t.x, t.xs) && rows_aligned16(t.y, t.ys);
+  }
+  p.freq = a.freq;
+  p.positions = a.positions;
+  p.pos_bstride = a.pos_bstride;
+  p.offset = a.offset;
+  p.B = a.B;
+  p.S = a.S;
+  p.D = a.D;
+  p.rot = a.rot;
+  p.sign = a.inverse ? -1 : 1;
+  p.mult = a.mult;
+  const int H = a.H[0] + a.H[1];
+  const long long tokens = (long long)a.B * a.S;
+  const long long items = tokens * (vec ? a.D / 16 : a.rot / 2 + (a.D - a.rot + 1) / 2);
+  const long long blocks = (items + THREADS - 1) / THREADS;
+  const int heads = 8;
+  const dim3 grid((unsigned)(blocks < num_sms * 64ll ? blocks : num_sms * 64ll), (unsigned)ceil_div(H, heads));
+  if (!vec) {
+    if (a.f16) rope_pairs<true><<<grid, THREADS, 0, stream>>>(p, a.interleaved, heads, items);
+    else rope_pairs<false><<<grid, THREADS, 0, stream>>>(p, a.interleaved, heads, items);
+  } else if (a.f16) {
+    if (a.interleaved) rope_vec<true, true, 4><<<grid, THREADS, 0, stream>>>(p, heads, items);
+    else rope_vec<true, false, 4><<<grid, THREADS, 0, stream>>>(p, heads, items);
+  } else {
+    if (a.interleaved) rope_vec<false, true, 4><<<grid, THREADS, 0, stream>>>(p, heads, items);
+    else rope_vec<false, false, 4><<<grid, THREADS, 0, stream>>>(p, heads, items);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace sdpa

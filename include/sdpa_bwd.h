@@ -291,6 +291,121 @@ int sdpa_fwd_typed(int io_dtype, const void* q, const void* k, const void* v, vo
                    const void* bias, int bias_dtype, int bias_batch, void* stream);
 
 /*
+ * Modified scores. Language models change the score between Q K^T and the
+ * softmax; the scored entry points serve three such changes, alone or together:
+ *     y = scale * (q . k)
+ *     x = softcap * tanh(y / softcap)          (softcap > 0; else x = y)
+ *     x = x - alibi_slopes[h] * |q + diag - k| (alibi_slopes given; diag as for `causal`)
+ *     and row q sees only the keys of its range in `mask_plan`, besides the
+ *     causal, window and length masks of the call (a pair is visible when all
+ *     of them allow it),
+ * with O, LSE and the gradients of sdpa_fwd() / sdpa_bwd() on the scores x:
+ *     P = exp(x - LSE),  dS = P * (dP - delta) * (1 - tanh(y / softcap)^2).
+ * Every row may lose all its keys (O = 0, LSE = -inf or the sink, zero
+ * gradients). Values of masked keys must still be finite: a masked weight is an
+ * exact 0, and 0 times an infinity or NaN of V, K or dO is NaN.
+ * tanh is exact to a few fp32 roundings for every score and cap. A distance
+ * bias is one fp32 product and sum: |slope * distance| * 2^-24 is lost.
+ */
+
+/* Bytes of a mask plan for B batch rows of S_q queries over S_kv keys (0 for sizes that
+ * the plan calls reject: all must be positive and B * (S + 128) below 2^30). */
+size_t sdpa_mask_plan_size(int B, int S_q, int S_kv);
+
+/*
+ * A mask plan from explicit row ranges: query row i of batch row b sees the keys
+ * [row_lo[b, i], row_hi[b, i]) (int32 (B, S_q), clamped to [0, S_kv]; none when
+ * lo >= hi). Made once per batch; every layer and both directions read it, and it
+ * must stay unchanged until their work has run.
+ *   plan   device buffer of >= sdpa_mask_plan_size() bytes, 256-byte aligned.
+ * Returns SDPA_ERR_INVALID for NULL pointers or bad sizes, SDPA_ERR_ALIGN,
+ * SDPA_ERR_WORKSPACE for a short buffer; enqueued on `stream`.
+ */
+int sdpa_mask_plan_rows(const int32_t* row_lo, const int32_t* row_hi, int B, int S_q, int S_kv,
+                        void* plan, size_t plan_bytes, void* stream);
+
+/*
+ * A mask plan of packed documents and prefixes over B rows of S positions
+ * (queries and keys at the same positions). A document is a maximal run of equal
+ * consecutive ids in doc_ids (int32 (B, S); NULL: each batch row is one document).
+ * A row sees its own document's keys; with `causal` those up to itself and the first
+ * `prefix` keys of the document, whichever reaches further (a prefix that its rows
+ * see in both directions). Use it with causal = 0 in the attention calls: the plan
+ * holds the causal side.
+ *   prefix_lens      int32: (B,), one prefix length for each document of the batch
+ *                    row, or with prefix_per_row (B, S), the length at each position;
+ *                    NULL: none. Lengths below 0 count as 0. Requires causal.
+ * Returns as sdpa_mask_plan_rows(), and SDPA_ERR_INVALID for a prefix without causal.
+ */
+int sdpa_mask_plan_docs(const int32_t* doc_ids, const int32_t* prefix_lens, int prefix_per_row,
+                        int causal, int B, int S, void* plan, size_t plan_bytes, void* stream);
+
+/*
+ * SDPA forward with modified scores. Arguments of sdpa_fwd_typed() without a bias, then
+ *   softcap       cap of the scores, 0 for none. Negative, infinite or NaN caps, and
+ *                 caps whose ratio to the scale leaves the normal fp32 range, return
+ *                 SDPA_ERR_INVALID.
+ *   alibi_slopes  device fp32 (H_q,) finite slopes of any sign, or NULL.
+ *   mask_plan     a plan for (B, S_q, S_kv), 256-byte aligned, or NULL.
+ * Served for every head-dim pair of sdpa_fwd(). With none of the three it is
+ * sdpa_fwd_typed().
+ */
+int sdpa_fwd_scored(int io_dtype, const void* q, const void* k, const void* v, void* o, float* lse,
+                    int B, int H_q, int H_kv, int S_q, int S_kv, int D_qk, int D_v, float scale,
+                    int causal, int bottom_right, int window_left, int window_right,
+                    const int32_t* seq_q_lens, const int32_t* seq_kv_lens, const float* sink,
+                    float softcap, const float* alibi_slopes, const void* mask_plan, void* stream);
+
+/*
+ * SDPA backward with modified scores, with the O and LSE of sdpa_fwd_scored() for the
+ * same arguments. Arguments of sdpa_bwd_typed() without a bias (sink and dsink
+ * optional), then softcap, alibi_slopes and mask_plan as sdpa_fwd_scored(). The
+ * slopes are constants: they have no gradient here. Workspace as
+ * sdpa_bwd_workspace_size() for the same mask arguments. Served for every head-dim
+ * pair of sdpa_bwd(); a mask plan in deterministic mode only where dQ comes from
+ * stored dS (D_qk 128, 192, 256), else SDPA_ERR_UNSUPPORTED.
+ */
+int sdpa_bwd_scored(int io_dtype, const void* q, const void* k, const void* v, const void* o,
+                    const void* d_o, const float* lse, void* dq, void* dk, void* dv, int B, int H_q,
+                    int H_kv, int S_q, int S_kv, int D_qk, int D_v, float scale, int causal,
+                    int bottom_right, int window_left, int window_right, int deterministic,
+                    const int32_t* seq_q_lens, const int32_t* seq_kv_lens, void* workspace,
+                    size_t workspace_bytes, const float* sink, float* dsink, float softcap,
+                    const float* alibi_slopes, const void* mask_plan, void* stream);
+
+/*
+ * Rotary embedding of queries and keys (or of their gradients, `inverse`). In the
+ * first rot_dim columns of a row at position t the column pair i turns by the angle
+ * t * inv_freq[i]:
+ *     (a, b) -> mult * (a cos - b sin, b cos + a sin),
+ * the pair being columns (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved; the
+ * columns past rot_dim are copied. With `inverse` the sine changes sign: the transposed
+ * map, which takes the gradient of the outputs to the gradient of the inputs.
+ * Scalings for long contexts are frequencies (and mult): the caller's inv_freq.
+ *   q, k, q_out, k_out  device 16-bit tensors of H_q and H_kv heads, any strides of batch,
+ *               head and position, columns contiguous; 2-byte aligned (16-byte loads are
+ *               used when D and rot_dim are multiples of 16 and every row of every tensor
+ *               is 16-byte aligned). H_kv = 0: q alone. An output may be its own input
+ *               (same pointer and strides); any other overlap is undefined.
+ *   strides     host array of 12: batch, head, position strides in elements of q, q_out, k,
+ *               k_out in this order. Input strides must not be negative; output rows must
+ *               not overlap (SDPA_ERR_INVALID).
+ *   inv_freq    device fp64 (rot_dim / 2,) finite frequencies in radians per position.
+ *   rot_dim     even, at most D and 512.
+ *   mult        factor on the rotated columns.
+ *   positions   device int32 (S,), or with positions_per_batch (B, S), of any sign; NULL:
+ *               offset + s.
+ *   offset      first position when positions is NULL (>= 0, offset + S <= 2^31).
+ * Angles are exact products of 64-bit fractions of a turn, at every position.
+ * Returns SDPA_ERR_INVALID, SDPA_ERR_UNSUPPORTED (rot_dim above 512) or SDPA_ERR_ALIGN
+ * before anything is enqueued on `stream`.
+ */
+int sdpa_rope(int io_dtype, const void* q, const void* k, void* q_out, void* k_out, int B, int H_q,
+              int H_kv, int S, int D, const long long* strides, const double* inv_freq, int rot_dim,
+              float mult, const int32_t* positions, int positions_per_batch, int offset,
+              int interleaved, int inverse, void* stream);
+
+/*
  * NVFP4 fake quantization ("NVFP4 Attention QAT Backward" page, Overview):
  * y = fake_nvfp4(x) for n contiguous bf16 values, in blocks of 16 consecutive
  * values. A block's local scale is s = E4M3(amax / 6), amax its largest
