@@ -124,8 +124,25 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream_handle(stream: Optional[torch.cuda.Stream]):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    # (torch.cuda.current_stream() builds a Stream object: 2.9 us a call on the Arm
+    # host against 0.1 us for the handle itself)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
+def _is(t, dtype, dev: int, shape) -> bool:
+    """Whether t is a contiguous tensor of this type, device index and shape: the checks
+    of a call in one test. A call whose tensors fail it goes through the checks
+    that name what is wrong; small calls spend most of their time on the host."""
+    return type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == dev and t.shape == shape \
+        and t.is_contiguous()
+
+
+def _optional(t, dtype, dev: int, numel: int) -> bool:
+    """The same for an optional tensor of numel elements in any shape."""
+    return t is None or (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == dev
+                         and t.numel() == numel and t.is_contiguous())
 
 
 def workspace_size(B, Hq, Hkv, Sq, Skv, Dqk, Dv, deterministic=False, *, causal=False,
@@ -241,26 +258,32 @@ def sdpa_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
     B, Hq, Sq, Dqk = q.shape
     Hkv, Skv = k.shape[1], k.shape[2]
     Dv = v.shape[3]
-    _check_bf16("q", q, (B, Hq, Sq, Dqk), io)
-    _check_bf16("k", k, (B, Hkv, Skv, Dqk), io)
-    _check_bf16("v", v, (B, Hkv, Skv, Dv), io)
-    _check_bf16("o", o, (B, Hq, Sq, Dv), io)
-    _check_bf16("do", do, (B, Hq, Sq, Dv), io)
-    _check_lse(lse, B, Hq, Sq)
-    _check_lens(B, seq_q_lens, seq_kv_lens)
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
-    _check_bf16("dq", dq, q.shape, io)
-    _check_bf16("dk", dk, k.shape, io)
-    _check_bf16("dv", dv, v.shape, io)
     ws_bytes = _check_workspace(workspace)
     if sink is not None:
         dsink = _check_sink(sink, dsink, Hq)
-    _check_same_device(q, k=k, v=v, o=o, do=do, lse=lse, seq_q_lens=seq_q_lens,
-                       seq_kv_lens=seq_kv_lens, dq=dq, dk=dk, dv=dv, workspace=workspace,
-                       sink=sink, dsink=dsink if sink is not None else None, bias=bias,
-                       dbias=dbias if bias is not None and bias_grad else None)
+    dev, q_shape, k_shape, o_shape = q.get_device(), (B, Hq, Sq, Dqk), (B, Hkv, Skv, Dqk), (B, Hq, Sq, Dv)
+    if not (q.is_cuda and _is(q, io, dev, q_shape) and _is(k, io, dev, k_shape) and _is(v, io, dev, (B, Hkv, Skv, Dv))
+            and _is(o, io, dev, o_shape) and _is(do, io, dev, o_shape) and _is(dq, io, dev, q_shape)
+            and _is(dk, io, dev, k_shape) and _is(dv, io, dev, (B, Hkv, Skv, Dv))
+            and _optional(lse, torch.float32, dev, B * Hq * Sq) and _optional(seq_q_lens, torch.int32, dev, B)
+            and _optional(seq_kv_lens, torch.int32, dev, B) and workspace is None and sink is None and bias is None):
+        _check_bf16("q", q, q_shape, io)
+        _check_bf16("k", k, k_shape, io)
+        _check_bf16("v", v, (B, Hkv, Skv, Dv), io)
+        _check_bf16("o", o, o_shape, io)
+        _check_bf16("do", do, o_shape, io)
+        _check_lse(lse, B, Hq, Sq)
+        _check_lens(B, seq_q_lens, seq_kv_lens)
+        _check_bf16("dq", dq, q.shape, io)
+        _check_bf16("dk", dk, k.shape, io)
+        _check_bf16("dv", dv, v.shape, io)
+        _check_same_device(q, k=k, v=v, o=o, do=do, lse=lse, seq_q_lens=seq_q_lens,
+                           seq_kv_lens=seq_kv_lens, dq=dq, dk=dk, dv=dv, workspace=workspace,
+                           sink=sink, dsink=dsink if sink is not None else None, bias=bias,
+                           dbias=dbias if bias is not None and bias_grad else None)
     scored = _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias)
     _check_launch_device(q)
     sc = 0.0 if scale is None else float(scale)
@@ -434,7 +457,9 @@ def _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias)
             raise TypeError("mask_plan must be a MaskPlan (made by mask_plan())")
         if (mask_plan.B, mask_plan.Sq, mask_plan.Skv) != (B, Sq, Skv):
             raise ValueError(f"mask_plan was made for {mask_plan!r}, not for B={B}, Sq={Sq}, Skv={Skv}")
-    _check_same_device(q, alibi_slopes=alibi_slopes, mask_plan=None if mask_plan is None else mask_plan.buffer)
+    for name, t in (("alibi_slopes", alibi_slopes), ("mask_plan", None if mask_plan is None else mask_plan.buffer)):
+        if t is not None and t.get_device() != q.get_device():
+            _check_same_device(q, **{name: t})
     return True
 
 
@@ -474,60 +499,82 @@ def rope_inv_freq(rot_dim: int, base: float = 10000.0, *, scaling: str = "none",
     return f.to(torch.device("cuda") if device is None else device)
 
 
-def _check_rope_tensor(name, t, shape, io):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != io or not t.is_cuda:
-        raise ValueError(f"{name} must be a {io} CUDA tensor")
-    if t.dim() != 4 or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.stride(3) != 1 and t.shape[3] > 1:
-        raise ValueError(f"{name} must have contiguous columns (stride 1 in its last dimension)")
-
-
-def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, k_out, stream):
-    lib = load()
+def _check_rope_args(q, k, inv_freq, positions, offset, q_out, k_out):
+    """Names what is wrong with a rope call's arguments."""
     io = _io_dtype(q)
     if q.dim() != 4:
         raise ValueError("q must be (B, H, S, D)")
-    B, Hq, S, D = q.shape
-    _check_rope_tensor("q", q, (B, Hq, S, D), io)
-    Hkv = 0
-    if k is not None:
-        if not isinstance(k, torch.Tensor) or k.dim() != 4:
-            raise ValueError("k must be a (B, H, S, D) tensor")
-        Hkv = k.shape[1]
-        _check_rope_tensor("k", k, (B, Hkv, S, D), io)
-    elif k_out is not None:
+    B, _, S, D = q.shape
+    if k is None and k_out is not None:
         raise ValueError("k_out without k")
+    if k is not None and (not isinstance(k, torch.Tensor) or k.dim() != 4):
+        raise ValueError("k must be a (B, H, S, D) tensor")
+    for name, t, like in (("q", q, q), ("k", k, k), ("q_out", q_out, q), ("k_out", k_out, k)):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != io or not t.is_cuda:
+            raise ValueError(f"{name} must be a {io} CUDA tensor")
+        shape = (B, like.shape[1], S, D)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+        if t.stride(3) != 1 and D > 1:
+            raise ValueError(f"{name} must have contiguous columns (stride 1 in its last dimension)")
     if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float64 or not inv_freq.is_cuda \
             or not inv_freq.is_contiguous() or inv_freq.dim() != 1:
         raise ValueError("inv_freq must be a contiguous fp64 CUDA vector (rope_inv_freq)")
     rot = 2 * inv_freq.numel()
     if rot == 0 or rot > D:
         raise ValueError(f"inv_freq rotates {rot} columns of {D}")
-    per_batch = 0
     if positions is not None:
         _check_int32("positions", positions, ((S,), (B, S)))
-        per_batch = int(positions.dim() == 2)
         if offset != 0:
             raise ValueError("offset counts from position 0 where no positions are given")
-    if q_out is None:
-        q_out = torch.empty((B, Hq, S, D), dtype=io, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty((B, Hkv, S, D), dtype=io, device=q.device)
-    _check_rope_tensor("q_out", q_out, (B, Hq, S, D), io)
-    if k is not None:
-        _check_rope_tensor("k_out", k_out, (B, Hkv, S, D), io)
     _check_same_device(q, k=k, inv_freq=inv_freq, positions=positions, q_out=q_out, k_out=k_out)
+
+
+_Strides = ctypes.c_longlong * 12
+
+
+def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, k_out, stream):
+    lib = _lib or load()
+    if q_out is None and isinstance(q, torch.Tensor):
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None and isinstance(k, torch.Tensor):
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    try:
+        shape, sq, so = q.shape, q.stride(), q_out.stride()
+        B, Hq, S, D = shape
+        io, dev, Hkv, sk, sl = q.dtype, q.get_device(), 0, sq, so
+        good = q.is_cuda and io in _IO_CODES and q_out.dtype is io and q_out.get_device() == dev \
+            and q_out.shape == shape and sq[3] == 1 and so[3] == 1
+        if k is not None:
+            sk, sl, Hkv = k.stride(), k_out.stride(), k.shape[1]
+            good = good and k.dtype is io and k_out.dtype is io and k.get_device() == dev \
+                and k_out.get_device() == dev and k.shape == (B, Hkv, S, D) and k_out.shape == k.shape \
+                and sk[3] == 1 and sl[3] == 1
+        rot = 2 * inv_freq.shape[0]
+        good = good and _is(inv_freq, torch.float64, dev, (rot // 2,)) and 0 < rot <= D \
+            and (k_out is None or k is not None) \
+            and (positions is None or offset == 0 and (_is(positions, torch.int32, dev, (B, S))
+                                                       or _is(positions, torch.int32, dev, (S,))))
+    except (AttributeError, IndexError, ValueError):  # not tensors, or of other dimensions
+        good = False
+    if not good:
+        _check_rope_args(q, k, inv_freq, positions, offset, q_out, k_out)
+        B, Hq, S, D = q.shape
+        sq, so, Hkv, rot = q.stride(), q_out.stride(), 0, 2 * inv_freq.numel()
+        sk, sl = sq, so
+        if k is not None:
+            sk, sl, Hkv = k.stride(), k_out.stride(), k.shape[1]
     _check_launch_device(q)
-    strides = []
-    for t in (q, q_out, k, k_out):
-        strides += [0, 0, 0] if t is None else [t.stride(0), t.stride(1), t.stride(2)]
-    if q.numel() > 0:
-        rc = lib.sdpa_rope(_IO_CODES[io], _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), B, Hq, Hkv, S, D,
-                           (ctypes.c_longlong * 12)(*strides), _ptr(inv_freq), rot, float(mult), _ptr(positions),
-                           per_batch, int(offset), int(interleaved), int(inverse), _stream_handle(stream))
+    if B > 0 and Hq > 0:
+        rc = lib.sdpa_rope(_IO_CODES[q.dtype], q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), B, Hq, Hkv, S, D,
+                           _Strides(sq[0], sq[1], sq[2], so[0], so[1], so[2], sk[0], sk[1], sk[2], sl[0], sl[1], sl[2]),
+                           inv_freq.data_ptr(), rot, mult, _ptr(positions),
+                           0 if positions is None else positions.dim() - 1, offset, interleaved, inverse,
+                           _stream_handle(stream))
         if rc != 0:
             raise SdpaError(rc, "sdpa_rope")
     return q_out, k_out
@@ -583,19 +630,25 @@ def sdpa_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale: Option
     B, Hq, Sq, Dqk = q.shape
     Hkv, Skv = k.shape[1], k.shape[2]
     Dv = v.shape[3]
-    _check_bf16("q", q, (B, Hq, Sq, Dqk), io)
-    _check_bf16("k", k, (B, Hkv, Skv, Dqk), io)
-    _check_bf16("v", v, (B, Hkv, Skv, Dv), io)
-    _check_lens(B, seq_q_lens, seq_kv_lens)
-    if sink is not None and (sink.dtype != torch.float32 or not sink.is_cuda
-                             or not sink.is_contiguous() or sink.numel() != Hq):
-        raise ValueError("sink must be a contiguous fp32 CUDA tensor of Hq elements")
     o = torch.empty((B, Hq, Sq, Dv), dtype=io, device=q.device) if o is None else o
     lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device) if lse is None else lse
-    _check_bf16("o", o, (B, Hq, Sq, Dv), io)
-    _check_lse(lse, B, Hq, Sq)
-    _check_same_device(q, k=k, v=v, o=o, lse=lse, seq_q_lens=seq_q_lens, seq_kv_lens=seq_kv_lens,
-                       sink=sink, bias=bias)
+    dev = q.get_device()
+    if not (q.is_cuda and _is(q, io, dev, (B, Hq, Sq, Dqk)) and _is(k, io, dev, (B, Hkv, Skv, Dqk))
+            and _is(v, io, dev, (B, Hkv, Skv, Dv)) and _is(o, io, dev, (B, Hq, Sq, Dv))
+            and _optional(lse, torch.float32, dev, B * Hq * Sq) and _optional(seq_q_lens, torch.int32, dev, B)
+            and _optional(seq_kv_lens, torch.int32, dev, B) and _optional(sink, torch.float32, dev, Hq)
+            and bias is None):
+        _check_bf16("q", q, (B, Hq, Sq, Dqk), io)
+        _check_bf16("k", k, (B, Hkv, Skv, Dqk), io)
+        _check_bf16("v", v, (B, Hkv, Skv, Dv), io)
+        _check_lens(B, seq_q_lens, seq_kv_lens)
+        if sink is not None and (sink.dtype != torch.float32 or not sink.is_cuda
+                                 or not sink.is_contiguous() or sink.numel() != Hq):
+            raise ValueError("sink must be a contiguous fp32 CUDA tensor of Hq elements")
+        _check_bf16("o", o, (B, Hq, Sq, Dv), io)
+        _check_lse(lse, B, Hq, Sq)
+        _check_same_device(q, k=k, v=v, o=o, lse=lse, seq_q_lens=seq_q_lens, seq_kv_lens=seq_kv_lens,
+                           sink=sink, bias=bias)
     scored = _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias)
     _check_launch_device(q)
     sc = 0.0 if scale is None else float(scale)

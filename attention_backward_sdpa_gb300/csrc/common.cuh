@@ -154,6 +154,8 @@ __device__ __forceinline__ ModTile mod_tile(const ChainParams& p, int b, int h, 
   const int q0 = qt * BQ;
   m.cap_in = p.mods.cap_in;
   m.cap_log2 = p.mods.cap_log2;
+  m.cap_small = p.mods.cap_small;
+  m.cap_c = &p.mods.cap_c;
   m.scale_log2 = p.scale_log2;
   m.slope2 = p.mods.slopes != nullptr ? p.mods.slopes[h] * 1.4426950408889634f : 0.f;
   m.dist = (float)((long long)q0 + diag - k);

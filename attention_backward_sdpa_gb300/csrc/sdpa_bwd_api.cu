@@ -362,6 +362,14 @@ int fill_mods(const ModArgs& ma, float scale, int B, int S_q, int S_kv, ScoreMod
     // A cap so far from the scale that their ratio leaves the normal fp32 range
     // would turn the capped scores into zeros or NaN.
     if (!std::isnormal(m.cap_in) || !std::isfinite(m.cap_log2)) return SDPA_ERR_INVALID;
+    // The polynomial with the powers of cap_in in its coefficients, where those (and
+    // the squared scores up to its bound) stay finite.
+    double power = m.cap_in;
+    m.cap_small = (float)std::fmin(TANH_SMALL / (double)m.cap_in, 1e18);
+    for (int i = 0; i < 6; ++i, power *= (double)m.cap_in * m.cap_in) {
+      m.cap_c[i] = (float)(TANH_C[i] * power);
+      if (!std::isfinite(m.cap_c[i] * m.cap_log2)) m.cap_small = -1.f;  // the quotient serves every score
+    }
   }
   if (ma.plan) {
     const MaskPlanLayout l = mask_plan_layout(B, ceil_div(S_q, BQ), ceil_div(S_kv, BN));

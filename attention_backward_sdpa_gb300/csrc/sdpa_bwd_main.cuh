@@ -784,7 +784,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
           const int i = (chunk & 3) * 8;
           const float4 d0 = delta4[chunk * 2], d1 = delta4[chunk * 2 + 1];
           const int c = chunk * 8;
-          const float ds[8] = {P[c + 0] * (__uint_as_float(r[i + 0]) - d0.x),
+          float ds[8] = {P[c + 0] * (__uint_as_float(r[i + 0]) - d0.x),
                                P[c + 1] * (__uint_as_float(r[i + 1]) - d0.y),
                                P[c + 2] * (__uint_as_float(r[i + 2]) - d0.z),
                                P[c + 3] * (__uint_as_float(r[i + 3]) - d0.w),
@@ -792,6 +792,13 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
                                P[c + 5] * (__uint_as_float(r[i + 5]) - d1.y),
                                P[c + 6] * (__uint_as_float(r[i + 6]) - d1.z),
                                P[c + 7] * (__uint_as_float(r[i + 7]) - d1.w)};
+          if constexpr (MOD) {
+            // A masked pair's dP may have overflowed: its dS is 0, not 0 * inf.
+            if (mt.masked) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) ds[e] = P[c + e] == 0.f ? 0.f : ds[e];
+            }
+          }
           const uint32_t w0 = pack_io2<F16>(ds[0], ds[1]);
           const uint32_t w1 = pack_io2<F16>(ds[2], ds[3]);
           const uint32_t w2 = pack_io2<F16>(ds[4], ds[5]);

@@ -120,35 +120,78 @@ __device__ __forceinline__ void add_bias_row(const FwdParams& p, float c, const 
 
 // A thread's 64 scores of a tile rewritten as the modified scores times log2(e)
 // (score.cuh): scores S of its row and keys kb .. kb + 63, `slope2` the head's slope
-// times log2(e) (0 without slopes) and `dist` = q + diag - kb. The cap's branch and
-// the slopes' are uniform across the launch; the polynomial alone serves a warp
-// whose 64 x 32 scores all stay within its range, which they do unless scores come
-// near the cap.
-__device__ __forceinline__ void modify_score_row(const ScoreMods& m, float c, float slope2, float dist,
-                                                 uint32_t (&sr)[2][32]) {
+// times log2(e) (0 without slopes) and `dist` = q + diag - kb; `coef` the cap's
+// polynomial in log2 units. The branches on the cap and the slopes are uniform across
+// the launch, the one on the scores' size across the warp.
+__device__ __forceinline__ void modify_score_row(const ScoreMods& m, const CapCoef& coef, float c, float slope2,
+                                                 float dist, uint32_t (&sr)[2][32]) {
   if (m.cap_in != 0.f) {
-    float big = 0.f;
+    float big[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 64; ++i) big = fmaxf(big, fabsf(__uint_as_float(sr[i >> 5][i & 31])));
-    if (__all_sync(0xffffffffu, big * m.cap_in <= TANH_SMALL)) {
+    for (int i = 0; i < 64; i += 2)
+      big[(i >> 1) & 3] = max3(big[(i >> 1) & 3], fabsf(__uint_as_float(sr[i >> 5][i & 31])),
+                               fabsf(__uint_as_float(sr[i >> 5][(i & 31) + 1])));
+    if (__all_sync(0xffffffffu, max3(big[0], big[1], fmaxf(big[2], big[3])) <= m.cap_small)) {
 #pragma unroll
-      for (int i = 0; i < 64; ++i)
-        sr[i >> 5][i & 31] = __float_as_uint(m.cap_log2 * tanh_small(__uint_as_float(sr[i >> 5][i & 31]) * m.cap_in));
+      for (int i = 0; i < 64; i += 2) {
+        uint32_t* s = &sr[i >> 5][i & 31];
+        float x0, x1;
+        f2_unpack(tanh2_small(f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1])), coef), x0, x1);
+        s[0] = __float_as_uint(x0);
+        s[1] = __float_as_uint(x1);
+      }
     } else {
+      const uint64_t mult = f2_pack(m.cap_log2, m.cap_log2);
+#pragma unroll
+      for (int i = 0; i < 64; i += 2) {
+        uint32_t* s = &sr[i >> 5][i & 31];
+        float x0, x1;
+        f2_unpack(f2_mul(tanh2_any(__uint_as_float(s[0]), __uint_as_float(s[1]), m.cap_in), mult), x0, x1);
+        s[0] = __float_as_uint(x0);
+        s[1] = __float_as_uint(x1);
+      }
+    }
+    if (m.slopes != nullptr) {
 #pragma unroll
       for (int i = 0; i < 64; ++i)
-        sr[i >> 5][i & 31] = __float_as_uint(m.cap_log2 * tanh_any(__uint_as_float(sr[i >> 5][i & 31]) * m.cap_in));
+        sr[i >> 5][i & 31] =
+            __float_as_uint(fmaf(-slope2, fabsf(dist - (float)i), __uint_as_float(sr[i >> 5][i & 31])));
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 64; ++i) sr[i >> 5][i & 31] = __float_as_uint(__uint_as_float(sr[i >> 5][i & 31]) * c);
-  }
-  if (m.slopes != nullptr) {
+  } else if (m.slopes != nullptr) {
 #pragma unroll
     for (int i = 0; i < 64; ++i)
       sr[i >> 5][i & 31] =
-          __float_as_uint(fmaf(-slope2, fabsf(dist - (float)i), __uint_as_float(sr[i >> 5][i & 31])));
+          __float_as_uint(fmaf(__uint_as_float(sr[i >> 5][i & 31]), c, -slope2 * fabsf(dist - (float)i)));
   }
+}
+
+// The largest of a thread's 64 scores, and their exponentials ex2(x * cs + neg_m) as io
+// pairs with the row sum's partials, in pair instructions: the MOD kernels' forms of the
+// loops that the other instantiations spell out.
+__device__ __forceinline__ float max_score_row(const uint32_t (&sr)[2][32]) {
+  float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < 64; i += 2)
+    mp[(i >> 1) & 3] = max3(mp[(i >> 1) & 3], __uint_as_float(sr[i >> 5][i & 31]), __uint_as_float(sr[i >> 5][(i & 31) + 1]));
+  return max3(mp[0], mp[1], fmaxf(mp[2], mp[3]));
+}
+template <bool F16>
+__device__ __forceinline__ void exp_score_pairs(const uint32_t (&s)[32], float cs, float neg_m, float (&rs)[8],
+                                                uint32_t (&w)[16]) {
+  const uint64_t c2 = f2_pack(cs, cs), m2 = f2_pack(neg_m, neg_m);
+  uint64_t sum[4];
+#pragma unroll
+  for (int a = 0; a < 4; ++a) sum[a] = f2_pack(rs[2 * a], rs[2 * a + 1]);
+#pragma unroll
+  for (int i2 = 0; i2 < 16; ++i2) {
+    float x0, x1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i2]), __uint_as_float(s[2 * i2 + 1])), c2, m2), x0, x1);
+    const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+    sum[i2 & 3] = f2_add(sum[i2 & 3], f2_pack(p0, p1));
+    w[i2] = pack_io2<F16>(p0, p1);
+  }
+#pragma unroll
+  for (int a = 0; a < 4; ++a) f2_unpack(sum[a], rs[2 * a], rs[2 * a + 1]);
 }
 
 // One work item: 128 query rows (query tile qt, descending so that under a

@@ -309,6 +309,8 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
     // (The same for capped or distance-biased scores.)
     const bool modified = MOD && (p.mods.cap_in != 0.f || p.mods.slopes != nullptr);
     const float cs = (BIAS || modified) ? 1.f : c;
+    CapCoef coef;
+    if constexpr (MOD) coef = cap_coef(p.mods.cap_c, p.mods.cap_log2);
     uint16_t* const o_base = static_cast<uint16_t*>(p.o);
     const size_t o_bytes = (size_t)p.B * p.Hq * p.Sq * D * 2;
     // O rows go out in 32-byte stores when every 16-column piece is 32-byte
@@ -389,7 +391,7 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
           tmem_ld_wait(sr[1]);
           if constexpr (BIAS) add_bias_row(p, c, braw, bpacked, sr);
           if constexpr (MOD) {
-            if (modified) modify_score_row(p.mods, c, slope2, (float)(q + w.diag - (k0 + i0)), sr);
+            if (modified) modify_score_row(p.mods, coef, c, slope2, (float)(q + w.diag - (k0 + i0)), sr);
           }
           // Visible keys of this row within the tile: [v_lo, v_hi] relative to k0.
           if (live) {
@@ -402,7 +404,9 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
           float mp[8];
 #pragma unroll
           for (int a = 0; a < 8; ++a) mp[a] = -INFINITY;
-          if (full) {
+          if (MOD && full) {
+            mp[0] = max_score_row(sr);
+          } else if (full) {
 #pragma unroll
             for (int i = 0; i < 64; ++i) mp[i & 7] = fmaxf(mp[i & 7], __uint_as_float(sr[i >> 5][i & 31]));
           } else {
@@ -473,7 +477,9 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
 #pragma unroll
         for (int c16 = 0; c16 < 2; ++c16) {
           uint32_t wv[16];
-          if (full) {
+          if (MOD && full) {
+            exp_score_pairs<F16>(sr[c16], cs, neg_m, rs, wv);
+          } else if (full) {
 #pragma unroll
             for (int i2 = 0; i2 < 16; ++i2) {
               const float p0 = ex2_approx(fmaf(__uint_as_float(sr[c16][2 * i2]), cs, neg_m));
