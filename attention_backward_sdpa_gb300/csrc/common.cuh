@@ -146,10 +146,23 @@ __device__ inline void planned_query_tiles(const ScoreMods& m, int b, int kt, in
   qt_hi = min(qt_hi, s.y);
 }
 
+// Narrows the rows [lo, hi] that see key k by a mask plan whose rows are neighbours;
+// returns whether the plan's are not (then the tiles' row ranges decide).
+__device__ __forceinline__ bool key_rows(const ChainParams& p, int b, int k, long long& lo, long long& hi) {
+  if (p.mods.k_rows == nullptr) return false;
+  if (p.mods.k_exact[b] == 0) return true;
+  const int2 r = p.mods.k_rows[(long long)b * p.n_kt * BN + k];
+  lo = max(lo, (long long)r.x);
+  hi = min(hi, (long long)r.y);
+  return false;
+}
+
 // The replay state (score.cuh) of a thread that holds key k of the key tile at k0
-// against the 64-row query tile qt of batch row b, query head h.
+// against the 64-row query tile qt of batch row b, query head h. q_lo_vis and q_hi_vis
+// bound the rows that see the key (key_rows() included); `row_ranges`: the plan's rows
+// are not neighbours and each tile's own ranges decide.
 __device__ __forceinline__ ModTile mod_tile(const ChainParams& p, int b, int h, int qt, int k0, int k, int Lk, int diag,
-                                            bool edge, long long q_lo_vis, long long q_hi_vis) {
+                                            bool edge, bool row_ranges, long long q_lo_vis, long long q_hi_vis) {
   ModTile m;
   const int q0 = qt * BQ;
   m.cap_in = p.mods.cap_in;
@@ -164,12 +177,14 @@ __device__ __forceinline__ ModTile mod_tile(const ChainParams& p, int b, int h, 
   m.k = k;
   m.ranges = nullptr;
   m.masked = edge;
-  if (p.mods.ranges != nullptr) {
+  if (row_ranges) {
     const int4 s = p.mods.q_sum[(long long)b * p.n_qt + qt];
     if (s.z > k0 || s.w < min(k0 + BN, Lk)) {  // some row does not see the whole key tile
       m.ranges = p.mods.ranges + ((long long)b * p.n_qt + qt) * BQ;
       m.masked = true;
     }
+  } else if (p.mods.k_rows != nullptr) {  // the bounds come from key_rows(): this warp's 32 keys
+    m.masked = __any_sync(0xffffffffu, m.q_lo > 0 || m.q_hi < BQ - 1);
   }
   return m;
 }

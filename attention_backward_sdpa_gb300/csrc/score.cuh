@@ -35,6 +35,8 @@ struct ScoreMods {
   const int2* ranges;  // [B][n_qt * 64] {lo, hi}; rows past S_q hold {0, 0}
   const int4* q_sum;   // [B][n_qt] {min lo, max hi, max lo, min hi} of the tile's rows (below)
   const int2* k_sum;   // [B][n_kt] {first, last} 64-row query tile that sees the 128-key tile
+  const int2* k_rows;  // [B][n_kt * 128] {first, last} query row that sees the key, where `k_exact`
+  const int* k_exact;  // [B] whether every key of the batch row is seen by exactly the rows of k_rows
 };
 
 // Regions of a mask plan of n_qt 64-row and n_kt 128-key tiles, as byte offsets.
@@ -42,15 +44,22 @@ struct ScoreMods {
 // has one); max lo and min hi over all rows below S_q, where a row with no key
 // counts as lo = INT_MAX, so that a tile is only taken as unmasked when every
 // row sees all of it.
+// k_rows, k_exact: where lo and hi of a batch row never decrease from row to row (every
+// document and prefix mask), the rows that see a key are neighbours: those up to the
+// last with lo <= key, from the first with hi > key. The backward, whose threads own a
+// key, then masks by two bounds in registers; for other ranges it reads the 64 row
+// ranges of every tile that needs a mask.
 struct MaskPlanLayout {
-  size_t ranges, q_sum, k_sum, bytes;
+  size_t ranges, q_sum, k_sum, k_rows, k_exact, bytes;
 };
 __host__ __device__ inline MaskPlanLayout mask_plan_layout(int B, int n_qt, int n_kt) {
   MaskPlanLayout l;
   l.ranges = 0;
   l.q_sum = (l.ranges + (size_t)B * n_qt * 64 * sizeof(int2) + 255) & ~(size_t)255;
   l.k_sum = (l.q_sum + (size_t)B * n_qt * sizeof(int4) + 255) & ~(size_t)255;
-  l.bytes = (l.k_sum + (size_t)B * n_kt * sizeof(int2) + 255) & ~(size_t)255;
+  l.k_rows = (l.k_sum + (size_t)B * n_kt * sizeof(int2) + 255) & ~(size_t)255;
+  l.k_exact = l.k_rows + (size_t)B * n_kt * 128 * sizeof(int2);
+  l.bytes = (l.k_exact + (size_t)B * sizeof(int) + 255) & ~(size_t)255;
   return l;
 }
 

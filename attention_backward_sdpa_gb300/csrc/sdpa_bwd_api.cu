@@ -377,6 +377,8 @@ int fill_mods(const ModArgs& ma, float scale, int B, int S_q, int S_kv, ScoreMod
     m.ranges = reinterpret_cast<const int2*>(base + l.ranges);
     m.q_sum = reinterpret_cast<const int4*>(base + l.q_sum);
     m.k_sum = reinterpret_cast<const int2*>(base + l.k_sum);
+    m.k_rows = reinterpret_cast<const int2*>(base + l.k_rows);
+    m.k_exact = reinterpret_cast<const int*>(base + l.k_exact);
   }
   return SDPA_OK;
 }

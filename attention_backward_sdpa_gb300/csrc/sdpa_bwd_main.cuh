@@ -650,8 +650,10 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
     const int k = k0 + row;            // this thread's key (S^T / dP^T lane)
     const bool row_dead = k >= Lk;
-    const long long q_lo_vis = p.causal ? (long long)k - diag - Rp : -(1ll << 40);
-    const long long q_hi_vis = has_window ? (long long)k - diag + p.window_left : (1ll << 40);
+    long long q_lo_vis = p.causal ? (long long)k - diag - Rp : -(1ll << 40);
+    long long q_hi_vis = has_window ? (long long)k - diag + p.window_left : (1ll << 40);
+    bool row_ranges = false;
+    if constexpr (MOD) row_ranges = key_rows(p, b, k, q_lo_vis, q_hi_vis);
     const float scale_log2 = p.scale_log2;
     uint8_t* ds_row = sDS + slot * L::TILE_DS + row * 128;
     float P[BQ];
@@ -684,7 +686,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
       const long long bias_off = BIAS ? bias_tile_off(t) : 0;
       ModTile mt;
       if constexpr (MOD)
-        mt = mod_tile(p, b, bh0 + t / n1 - b * p.Hq, qt, k0, k, Lk, diag, need_mask, q_lo_vis, q_hi_vis);
+        mt = mod_tile(p, b, bh0 + t / n1 - b * p.Hq, qt, k0, k, Lk, diag, need_mask, row_ranges, q_lo_vis, q_hi_vis);
 
       // ---- softmax replay: P^T from S^T. The row statistics were written by
       // TMA, so this thread waits on the stage's transaction barrier itself.

@@ -394,8 +394,10 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
     const int k = k0 + row;
     const bool row_dead = k >= Lk;
-    const long long q_lo_vis = p.causal ? (long long)k - diag - Rp : -(1ll << 40);
-    const long long q_hi_vis = has_window ? (long long)k - diag + p.window_left : (1ll << 40);
+    long long q_lo_vis = p.causal ? (long long)k - diag - Rp : -(1ll << 40);
+    long long q_hi_vis = has_window ? (long long)k - diag + p.window_left : (1ll << 40);
+    bool row_ranges = false;
+    if constexpr (MOD) row_ranges = key_rows(p, b, k, q_lo_vis, q_hi_vis);
     uint8_t* ds_row = sDS + slot * L::TILE_DS + row * 128;
     float P[BQ];
     bool ok = true;
@@ -422,7 +424,7 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
                              (p.causal && (long long)q0 < (long long)(k0 + BN - 1) - diag - Rp) ||
                              (has_window && (long long)(q0 + BQ - 1) > (long long)k0 - diag + p.window_left);
       ModTile mt;
-      if constexpr (MOD) mt = mod_tile(p, b, h, qt, k0, k, Lk, diag, need_mask, q_lo_vis, q_hi_vis);
+      if constexpr (MOD) mt = mod_tile(p, b, h, qt, k0, k, Lk, diag, need_mask, row_ranges, q_lo_vis, q_hi_vis);
       if (!mbar_wait(&bars[BAR_QFULL + st], (t / NQ) & 1, abort_flag, WAIT_LIMIT_NS) ||
           !mbar_wait(&bars[BAR_SFULL + slot], j & 1, abort_flag, WAIT_LIMIT_NS)) { ok = false; break; }
       __syncwarp();

@@ -13,7 +13,10 @@
 //   q_summary    one warp per 64-row tile (two rows a lane, warp reductions).
 //   k_summary    one warp per 128-key tile: the first and last query tile whose
 //                [min lo, max hi) meets it.
-// All four move a few bytes per row (B 8, S 4096: 400 KB) and are bound by
+//   k_exact      one block per batch row: whether lo and hi never decrease.
+//   k_rows       per key, where they never do: the first row with hi above the key and
+//                the last with lo at or below it, by bisection.
+// All move a few bytes per row (B 8, S 4096: 400 KB) and are bound by
 // their launches and the scan's passes over one batch row.
 #include <climits>
 
@@ -160,6 +163,45 @@ __global__ void __launch_bounds__(128) mask_k_summary(const int4* q_sum, int n_q
   if (lane == 0) k_sum[tile] = make_int2(first == INT_MAX ? 0 : first, last);
 }
 
+__global__ void __launch_bounds__(SCAN_THREADS) mask_k_exact(const int2* ranges, int Sq, int rows_pad, int* k_exact) {
+  const int2* r = ranges + (long long)blockIdx.x * rows_pad;
+  bool up = true;
+  for (int i = threadIdx.x + 1; i < Sq; i += SCAN_THREADS) {
+    const int2 a = r[i - 1], c = r[i];
+    up = up && a.x <= c.x && a.y <= c.y;
+  }
+  const int all = __syncthreads_and(up);
+  if (threadIdx.x == 0) k_exact[blockIdx.x] = all;
+}
+
+__global__ void __launch_bounds__(128) mask_k_rows(const int2* ranges, const int* k_exact, int Sq, int rows_pad,
+                                                   int n_kt, int2* k_rows) {
+  const int b = blockIdx.x / n_kt, k = (blockIdx.x % n_kt) * BN + threadIdx.x;
+  const int2* r = ranges + (long long)b * rows_pad;
+  int first = 0, past = Sq;  // the first row with hi > k, and the first with lo > k
+  if (k_exact[b]) {
+    for (int lo = 0, hi = Sq;;) {
+      if (lo == hi) {
+        first = lo;
+        break;
+      }
+      const int mid = (lo + hi) / 2;
+      if (r[mid].y > k) hi = mid;
+      else lo = mid + 1;
+    }
+    for (int lo = 0, hi = Sq;;) {
+      if (lo == hi) {
+        past = lo;
+        break;
+      }
+      const int mid = (lo + hi) / 2;
+      if (r[mid].x > k) hi = mid;
+      else lo = mid + 1;
+    }
+  }
+  k_rows[((long long)b * n_kt) * BN + k] = make_int2(first, past - 1);
+}
+
 }  // namespace
 
 cudaError_t launch_mask_plan(const MaskPlanArgs& a, void* plan, cudaStream_t s) {
@@ -177,6 +219,10 @@ cudaError_t launch_mask_plan(const MaskPlanArgs& a, void* plan, cudaStream_t s) 
                                                                  a.causal, a.Sq, rows_pad, ranges);
   mask_q_summary<<<(unsigned)ceil_div(a.B * n_qt, 4), 128, 0, s>>>(ranges, a.Sq, n_qt, a.B * n_qt, q_sum);
   mask_k_summary<<<(unsigned)ceil_div(a.B * n_kt, 4), 128, 0, s>>>(q_sum, n_qt, n_kt, a.B * n_kt, k_sum);
+  int2* k_rows = reinterpret_cast<int2*>(base + l.k_rows);
+  int* k_exact = reinterpret_cast<int*>(base + l.k_exact);
+  mask_k_exact<<<(unsigned)a.B, SCAN_THREADS, 0, s>>>(ranges, a.Sq, rows_pad, k_exact);
+  mask_k_rows<<<(unsigned)(a.B * n_kt), BN, 0, s>>>(ranges, k_exact, a.Sq, rows_pad, n_kt, k_rows);
   return cudaGetLastError();
 }
 

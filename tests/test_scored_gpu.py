@@ -223,6 +223,21 @@ def test_plan_ranges(B, S, prefix):
         for t in range(n_kt):
             meet = [i for i in range(n_qt) if q_sum[b, i, 0] < 128 * (t + 1) and q_sum[b, i, 1] > 128 * t]
             assert k_sum[b, t].tolist() == ([meet[0], meet[-1]] if meet else [0, -1])
+    # The rows that see each key, where they are neighbours (a prefix length that changes
+    # within a document need not leave them so).
+    at = up(at + B * n_kt * 2)
+    k_rows = words[at: at + B * n_kt * 128 * 2].view(B, n_kt * 128, 2)
+    k_exact = words[at + B * n_kt * 128 * 2:][:B]
+    for b in range(B):
+        lo, hi = rows[b, :, 0], rows[b, :, 1]
+        up_to = bool((lo[1:] >= lo[:-1]).all() and (hi[1:] >= hi[:-1]).all())
+        assert k_exact[b] == int(up_to)
+        if up_to:
+            for k in range(0, S, 1 if S < 2000 else 17):
+                see = ((lo <= k) & (hi > k)).nonzero().flatten()
+                assert see.numel() and k_rows[b, k].tolist() == [see[0].item(), see[-1].item()]
+                assert see.numel() == see[-1] - see[0] + 1
+    assert prefix == "row" or k_exact.all()
 
 
 def test_repeated_calls_are_bitwise_equal():
