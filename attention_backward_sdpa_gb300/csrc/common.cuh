@@ -166,12 +166,12 @@ __device__ __forceinline__ ModTile mod_tile(const ChainParams& p, int b, int h, 
   ModTile m;
   const int q0 = qt * BQ;
   m.cap_in = p.mods.cap_in;
-  m.cap_log2 = p.mods.cap_log2;
   m.cap_small = p.mods.cap_small;
-  m.cap_c = &p.mods.cap_c;
-  m.scale_log2 = p.scale_log2;
+  const float c = p.mods.cap_in != 0.f ? p.mods.cap_log2 : p.scale_log2;
+  m.c2 = f2_pack(c, c);
   m.slope2 = p.mods.slopes != nullptr ? p.mods.slopes[h] * 1.4426950408889634f : 0.f;
   m.dist = (float)((long long)q0 + diag - k);
+  m.ahead = __all_sync(0xffffffffu, m.dist >= 0.f);
   m.q_lo = (int)min(max(q_lo_vis - q0, 0ll), (long long)BQ);
   m.q_hi = k < Lk ? (int)min(max(q_hi_vis - q0, -1ll), (long long)BQ) : -1;
   m.k = k;
@@ -318,6 +318,8 @@ cudaError_t launch_main_qat(const MainMaps& maps, const ChainParams& p, cudaStre
 cudaError_t main_qat_kernel_setup();
 cudaError_t launch_main_mod(const MainMaps& maps, const ChainParams& p, cudaStream_t s);
 cudaError_t main_mod_kernel_setup();
+cudaError_t launch_main_cap(const MainMaps& maps, const ChainParams& p, cudaStream_t s);
+cudaError_t main_cap_kernel_setup();
 // A mask plan (score.cuh) from row ranges (row_lo, row_hi) or from documents.
 struct MaskPlanArgs {
   int B, Sq, Skv;

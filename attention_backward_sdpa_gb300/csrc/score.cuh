@@ -1,6 +1,7 @@
 // score.cuh -- scores that are modified between the score GEMM and the softmax,
-// for the forward and backward kernels instantiated with MOD: a tanh cap, a
-// bias that falls with distance, and a range of visible keys per query row.
+// for the forward and backward kernels instantiated with MOD (MOD_ROWS without a cap,
+// MOD_CAP with one): a tanh cap, a bias that falls with distance, and a range of
+// visible keys per query row.
 //
 //   y = scale * (q . k)                          the scaled score
 //   x = cap * tanh(y / cap)                      with a cap, else x = y
@@ -24,8 +25,10 @@
 
 namespace sdpa {
 
+enum : int { MOD_NONE = 0, MOD_ROWS = 1, MOD_CAP = 2 };
+
 struct ScoreMods {
-  int on;              // run the MOD instantiations
+  int on;              // MOD_NONE, MOD_ROWS or MOD_CAP: which instantiation runs
   float cap_in;        // scale / cap: tanh argument per unit of q . k (0: no cap)
   float cap_log2;      // cap * log2(e)
   float cap_small;     // |q . k| up to which the polynomial below serves (may be 0)
@@ -91,15 +94,21 @@ __device__ __forceinline__ CapCoef cap_coef(const float (&c)[6], float mult) {
   for (int i = 0; i < 6; ++i) k.c[i] = f2_pack(c[i] * mult, c[i] * mult);
   return k;
 }
-// A pair of scores s: mult * tanh(s * cap_in), |s| <= cap_small.
-__device__ __forceinline__ uint64_t tanh2_small(uint64_t s, const CapCoef& k) {
-  const uint64_t u = f2_mul(s, s);
-  uint64_t r = f2_fma(u, k.c[5], k.c[4]);
-  r = f2_fma(u, r, k.c[3]);
-  r = f2_fma(u, r, k.c[2]);
-  r = f2_fma(u, r, k.c[1]);
-  r = f2_fma(u, r, k.c[0]);
-  return f2_mul(s, r);
+// N pairs of scores s, |s| <= cap_small, step by step side by side (left to itself the
+// compiler takes one pair's eight dependent steps after another's, 1,550 cycles for a
+// thread's 64 scores with their exponentials against TANH_SIDE_BY_SIDE): r[i] = the
+// polynomial's value, so that mult * tanh(s * cap_in) = s * r.
+template <int N>
+__device__ __forceinline__ void tanh2_poly(const uint64_t (&s)[N], const CapCoef& k, uint64_t (&r)[N]) {
+  uint64_t u[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) u[i] = f2_mul(s[i], s[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = f2_fma(u[i], k.c[5], k.c[4]);
+#pragma unroll
+  for (int c = 3; c >= 0; --c)
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] = f2_fma(u[i], r[i], k.c[c]);
 }
 // x within [-lim, lim], a NaN kept (a visible score that is not a number has to show).
 __device__ __forceinline__ float clamp_nan(float x, float lim) {
@@ -107,125 +116,205 @@ __device__ __forceinline__ float clamp_nan(float x, float lim) {
   asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}" : "=f"(r) : "f"(x), "f"(-lim), "f"(lim));
   return r;
 }
-// A pair of any scores: tanh(s * cap_in).
-__device__ __forceinline__ uint64_t tanh2_any(float s0, float s1, float cap_in) {
-  constexpr float N[5] = {9.999999936e-01f, 1.344449871e-01f, 3.571599056e-03f, 2.189467996e-05f, 1.523044372e-08f};
-  constexpr float D[5] = {1.0f, 4.677782538e-01f, 2.616444638e-02f, 3.411293732e-04f, 8.522456963e-07f};
-  const float y0 = clamp_nan(s0 * cap_in, TANH_CLAMP), y1 = clamp_nan(s1 * cap_in, TANH_CLAMP);
-  const uint64_t y = f2_pack(y0, y1), u = f2_mul(y, y);
-  uint64_t n = f2_fma(u, f2_pack(N[4], N[4]), f2_pack(N[3], N[3]));
-  uint64_t d = f2_fma(u, f2_pack(D[4], D[4]), f2_pack(D[3], D[3]));
+// N pairs of any scores, in place: tanh(s * cap_in).
+template <int N>
+__device__ __forceinline__ void tanh2_any(uint64_t (&s)[N], float cap_in) {
+  constexpr float NU[5] = {9.999999936e-01f, 1.344449871e-01f, 3.571599056e-03f, 2.189467996e-05f, 1.523044372e-08f};
+  constexpr float DE[5] = {1.0f, 4.677782538e-01f, 2.616444638e-02f, 3.411293732e-04f, 8.522456963e-07f};
+  uint64_t u[N], n[N], d[N];
 #pragma unroll
-  for (int i = 2; i >= 0; --i) {
-    n = f2_fma(u, n, f2_pack(N[i], N[i]));
-    d = f2_fma(u, d, f2_pack(D[i], D[i]));
+  for (int i = 0; i < N; ++i) {
+    float y0, y1;
+    f2_unpack(s[i], y0, y1);
+    s[i] = f2_pack(clamp_nan(y0 * cap_in, TANH_CLAMP), clamp_nan(y1 * cap_in, TANH_CLAMP));
   }
-  float d0, d1, r0, r1;
-  f2_unpack(d, d0, d1);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d0));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d1));
-  return f2_mul(f2_mul(y, n), f2_pack(r0, r1));
+#pragma unroll
+  for (int i = 0; i < N; ++i) u[i] = f2_mul(s[i], s[i]);
+#pragma unroll
+  for (int i = 0; i < N; ++i) n[i] = f2_fma(u[i], f2_pack(NU[4], NU[4]), f2_pack(NU[3], NU[3]));
+#pragma unroll
+  for (int i = 0; i < N; ++i) d[i] = f2_fma(u[i], f2_pack(DE[4], DE[4]), f2_pack(DE[3], DE[3]));
+#pragma unroll
+  for (int c = 2; c >= 0; --c) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) n[i] = f2_fma(u[i], n[i], f2_pack(NU[c], NU[c]));
+#pragma unroll
+    for (int i = 0; i < N; ++i) d[i] = f2_fma(u[i], d[i], f2_pack(DE[c], DE[c]));
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float d0, d1, r0, r1;
+    f2_unpack(d[i], d0, d1);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(d0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(d1));
+    s[i] = f2_mul(f2_mul(s[i], n[i]), f2_pack(r0, r1));
+  }
 }
+// Pairs a step takes side by side.
+constexpr int SIDE = 8;
 
 // The backward's replay of one tile for one thread (its key k against 64 query
 // rows): what the modified scores and the masks need besides S^T.
+//
+// In these kernels everything runs on pairs of neighbouring query rows, and the row
+// statistics (preprocess) come negated, so that no step needs a sign of its own: n_lse =
+// -(LSE * log2(e) + slope2 * i), i the row within its tile, and n_delta = -delta. With a
+// cap, P is then multiplied by t^2 - 1 instead of 1 - t^2, so dS comes out negated, and
+// the host hands these kernels -scale for dQ and dK.
 struct ModTile {
-  float cap_in, cap_log2, cap_small, scale_log2;
-  const float (*cap_c)[6];
+  float cap_in, cap_small;
+  uint64_t c2;         // log2(e) times the cap, or times the scale: the exponent per tanh or per score
   float slope2;        // the head's slope * log2(e) (0 without slopes)
   float dist;          // q0 + diag - k: the distance of row i is |dist + i|
-  int q_lo, q_hi;      // rows (relative to the tile) inside the causal / window / length bounds
+  int q_lo, q_hi;      // rows (relative to the tile) inside the causal / window / length / plan bounds
   int k;
-  const int2* ranges;  // the tile's row ranges, or null when every row sees the whole key tile
+  const int2* ranges;  // the tile's row ranges where those decide, or null
   bool masked;         // the tile needs a mask (uniform across the warp)
+  bool ahead;          // every row of the tile is at or past the warp's keys: no |.| needed
 };
 
 // Half H (rows 32 H .. 32 H + 31) of a tile's replay. r: S^T on entry. P gets the
-// masked probabilities times the cap's derivative, which is all that the dS step
-// reads; w gets the probabilities themselves as io pairs for the dV product.
-// (The two are formed together so that no thread holds 64 derivatives.)
-template <bool F16, int H>
-__device__ __forceinline__ void mod_replay_half(const ModTile& m, const float* lse, uint32_t (&r)[32], float (&P)[64],
-                                                uint32_t (&w)[16]) {
-  const float4* lse4 = reinterpret_cast<const float4*>(lse) + H * 8;
-  if (m.cap_in != 0.f) {
-    // r becomes the tanh.
-    float big = 0.f;
+// masked probabilities (with a cap times t^2 - 1), which is all that the dS step reads; w
+// the probabilities themselves as io pairs for the dV product. (The two are formed
+// together so that no thread holds 64 derivatives.)
+//
+// A warp whose half needs no mask, no |.| and no quotient takes one straight pass, in
+// which the exponentials (a quarter of the FMA rate) run under the polynomials of the
+// neighbouring pairs; the general pass goes step by step.
+template <int MOD, bool F16, int H>
+__device__ __forceinline__ void mod_replay_half(const ModTile& m, const CapCoef& coef, const float* n_lse,
+                                                uint32_t (&r)[32], uint64_t (&P)[32], uint32_t (&w)[16]) {
+  bool small = true;
+  if constexpr (MOD == MOD_CAP) {
+    float big[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) big = max3(big, fabsf(__uint_as_float(r[i])), fabsf(__uint_as_float(r[i + 1])));
-    if (__all_sync(0xffffffffu, big <= m.cap_small)) {
-      const CapCoef k = cap_coef(*m.cap_c, 1.f);
+    for (int i = 0; i < 32; i += 2)
+      big[(i >> 1) & 3] = max3(big[(i >> 1) & 3], fabsf(__uint_as_float(r[i])), fabsf(__uint_as_float(r[i + 1])));
+    small = __all_sync(0xffffffffu, max3(big[0], big[1], fmaxf(big[2], big[3])) <= m.cap_small);
+  }
+  const ulonglong2* l2 = reinterpret_cast<const ulonglong2*>(n_lse) + H * 8;  // two pairs a load
+  const float bias = -m.slope2 * m.dist;  // -slope2 (dist + i): the i part is in the row statistics
+  const uint64_t bias2 = f2_pack(bias, bias), minus_one = f2_pack(-1.f, -1.f);
+  uint64_t* const Ph = P + H * 16;
+  if (small && !m.masked && m.ahead) {
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        float t0, t1;
-        f2_unpack(tanh2_small(f2_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), k), t0, t1);
-        r[i] = __float_as_uint(t0);
-        r[i + 1] = __float_as_uint(t1);
+    for (int blk = 0; blk < 16 / SIDE; ++blk) {
+      uint64_t t[SIDE], x[SIDE];
+#pragma unroll
+      for (int i = 0; i < SIDE; ++i) t[i] = f2_pack(r[2 * (blk * SIDE + i)], r[2 * (blk * SIDE + i) + 1]);
+      if constexpr (MOD == MOD_CAP) {
+        tanh2_poly(t, coef, x);
+#pragma unroll
+        for (int i = 0; i < SIDE; ++i) t[i] = f2_mul(t[i], x[i]);
       }
-    } else {
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        float t0, t1;
-        f2_unpack(tanh2_any(__uint_as_float(r[i]), __uint_as_float(r[i + 1]), m.cap_in), t0, t1);
-        r[i] = __float_as_uint(t0);
-        r[i + 1] = __float_as_uint(t1);
+      for (int i = 0; i < SIDE; i += 2) {
+        const ulonglong2 l = l2[(blk * SIDE + i) / 2];
+        x[i] = f2_fma(t[i], m.c2, f2_add(l.x, bias2));
+        x[i + 1] = f2_fma(t[i + 1], m.c2, f2_add(l.y, bias2));
+      }
+#pragma unroll
+      for (int i = 0; i < SIDE; ++i) {
+        float x0, x1;
+        f2_unpack(x[i], x0, x1);
+        x[i] = f2_pack(ex2_approx(x0), ex2_approx(x1));
+        if constexpr (MOD == MOD_CAP) t[i] = f2_fma(t[i], t[i], minus_one);
+      }
+#pragma unroll
+      for (int i = 0; i < SIDE; ++i) {
+        float p0, p1;
+        f2_unpack(x[i], p0, p1);
+        w[blk * SIDE + i] = pack_io2<F16>(p0, p1);
+        Ph[blk * SIDE + i] = MOD == MOD_CAP ? f2_mul(x[i], t[i]) : x[i];
       }
     }
+    return;
   }
-  const float c1 = m.cap_in != 0.f ? m.cap_log2 : m.scale_log2;
-  const uint64_t c2 = f2_pack(c1, c1);
-  float x[32];
+  if constexpr (MOD == MOD_CAP) {
+    // r becomes the tanh.
+#pragma unroll
+    for (int blk = 0; blk < 16 / SIDE; ++blk) {
+      uint64_t t[SIDE], x[SIDE];
+#pragma unroll
+      for (int i = 0; i < SIDE; ++i) t[i] = f2_pack(r[2 * (blk * SIDE + i)], r[2 * (blk * SIDE + i) + 1]);
+      if (small) {
+        tanh2_poly(t, coef, x);
+#pragma unroll
+        for (int i = 0; i < SIDE; ++i) t[i] = f2_mul(t[i], x[i]);
+      } else {
+        tanh2_any(t, m.cap_in);
+      }
+#pragma unroll
+      for (int i = 0; i < SIDE; ++i) f2_unpack(t[i], r[2 * (blk * SIDE + i)], r[2 * (blk * SIDE + i) + 1]);
+    }
+  }
 #pragma unroll
   for (int i4 = 0; i4 < 8; ++i4) {
-    const float4 l = lse4[i4];
-    const int i = i4 * 4;
-    f2_unpack(f2_fma(f2_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), c2, f2_pack(-l.x, -l.y)), x[i], x[i + 1]);
-    f2_unpack(f2_fma(f2_pack(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])), c2, f2_pack(-l.z, -l.w)), x[i + 2],
-              x[i + 3]);
+    const ulonglong2 l = l2[i4];
+    Ph[2 * i4] = f2_fma(f2_pack(r[4 * i4], r[4 * i4 + 1]), m.c2, l.x);
+    Ph[2 * i4 + 1] = f2_fma(f2_pack(r[4 * i4 + 2], r[4 * i4 + 3]), m.c2, l.y);
   }
   if (m.slope2 != 0.f) {
+    // -slope2 |dist + i| with the row statistics' -slope2 i taken back.
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = fmaf(-m.slope2, fabsf(m.dist + (float)(H * 32 + i)), x[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < 32; ++i) P[H * 32 + i] = ex2_approx(x[i]);
-  if (m.masked) {
-    // (r as well: a masked score may be an overflow or NaN, and 0 times that is NaN.)
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (H * 32 + i < m.q_lo || H * 32 + i > m.q_hi) {
-        P[H * 32 + i] = 0.f;
-        r[i] = 0u;
-      }
-    if (m.ranges != nullptr) {
-      // Two rows per 16-byte load, the same address for the whole warp.
-      const int4* rg = reinterpret_cast<const int4*>(m.ranges) + H * 16;
-#pragma unroll
-      for (int i2 = 0; i2 < 16; ++i2) {
-        const int4 v = __ldg(rg + i2);
-        if (m.k < v.x || m.k >= v.y) {
-          P[H * 32 + 2 * i2] = 0.f;
-          r[2 * i2] = 0u;
-        }
-        if (m.k < v.z || m.k >= v.w) {
-          P[H * 32 + 2 * i2 + 1] = 0.f;
-          r[2 * i2 + 1] = 0u;
-        }
-      }
+    for (int i2 = 0; i2 < 16; ++i2) {
+      const float i = (float)(H * 32 + 2 * i2);
+      float x0, x1;
+      f2_unpack(Ph[i2], x0, x1);
+      x0 = fmaf(m.slope2, i - fabsf(m.dist + i), x0);
+      x1 = fmaf(m.slope2, (i + 1.f) - fabsf(m.dist + (i + 1.f)), x1);
+      Ph[i2] = f2_pack(x0, x1);
     }
   }
+  const int4* rg = reinterpret_cast<const int4*>(m.ranges) + H * 16;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) w[i] = pack_io2<F16>(P[H * 32 + 2 * i], P[H * 32 + 2 * i + 1]);
-  if (m.cap_in != 0.f) {
-    // P times the derivative 1 - t^2.
-    const uint64_t one = f2_pack(1.f, 1.f);
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const float t0 = __uint_as_float(r[i]), t1 = __uint_as_float(r[i + 1]);
-      const uint64_t f = f2_fma(f2_pack(-t0, -t1), f2_pack(t0, t1), one);
-      f2_unpack(f2_mul(f, f2_pack(P[H * 32 + i], P[H * 32 + i + 1])), P[H * 32 + i], P[H * 32 + i + 1]);
+  for (int i2 = 0; i2 < 16; ++i2) {
+    const int i = H * 32 + 2 * i2;
+    bool see0 = i >= m.q_lo && i <= m.q_hi, see1 = i + 1 >= m.q_lo && i + 1 <= m.q_hi;
+    if (m.ranges != nullptr) {  // two rows per 16-byte load, the same address for the whole warp
+      const int4 v = __ldg(rg + i2);
+      see0 = see0 && m.k >= v.x && m.k < v.y;
+      see1 = see1 && m.k >= v.z && m.k < v.w;
+    }
+    float p0, p1;
+    f2_unpack(Ph[i2], p0, p1);
+    p0 = see0 ? ex2_approx(p0) : 0.f;
+    p1 = see1 ? ex2_approx(p1) : 0.f;
+    w[i2] = pack_io2<F16>(p0, p1);
+    Ph[i2] = f2_pack(p0, p1);
+    if constexpr (MOD == MOD_CAP) {
+      // (A masked score may be an overflow or NaN, and 0 times that is NaN: its tanh is
+      // taken as 0.)
+      const uint64_t t = f2_pack(see0 ? r[2 * i2] : 0u, see1 ? r[2 * i2 + 1] : 0u);
+      Ph[i2] = f2_mul(Ph[i2], f2_fma(t, t, minus_one));
     }
   }
+}
+
+// dS of 8 query rows (chunk c of the tile) as io pairs: P (dP - delta); r holds dP^T of a
+// 32-row half, c its chunk there (0 .. 3).
+template <bool F16>
+__device__ __forceinline__ uint4 mod_ds_chunk(const ModTile& m, const uint64_t (&P)[32], const float* n_delta,
+                                              const uint32_t (&r)[32], int chunk) {
+  const ulonglong2* d2 = reinterpret_cast<const ulonglong2*>(n_delta) + chunk * 2;
+  const ulonglong2 da = d2[0], db = d2[1];
+  const uint64_t d[4] = {da.x, da.y, db.x, db.y};
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int i = (chunk & 3) * 8 + 2 * e;
+    const uint64_t p = P[chunk * 4 + e];
+    float s0, s1;
+    f2_unpack(f2_mul(p, f2_add(f2_pack(r[i], r[i + 1]), d[e])), s0, s1);
+    if (m.masked) {  // a masked pair's dP may have overflowed: its dS is 0, not 0 * inf
+      float p0, p1;
+      f2_unpack(p, p0, p1);
+      s0 = p0 == 0.f ? 0.f : s0;
+      s1 = p1 == 0.f ? 0.f : s1;
+    }
+    w[e] = pack_io2<F16>(s0, s1);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 }  // namespace sdpa

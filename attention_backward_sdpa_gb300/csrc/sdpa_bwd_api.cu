@@ -354,7 +354,7 @@ int fill_mods(const ModArgs& ma, float scale, int B, int S_q, int S_kv, ScoreMod
   if (!(ma.softcap >= 0.f) || !std::isfinite(ma.softcap)) return SDPA_ERR_INVALID;
   if (reinterpret_cast<uintptr_t>(ma.slopes) % 4 != 0) return SDPA_ERR_ALIGN;
   if (reinterpret_cast<uintptr_t>(ma.plan) % 256 != 0) return SDPA_ERR_ALIGN;
-  m.on = 1;
+  m.on = ma.softcap > 0.f ? MOD_CAP : MOD_ROWS;
   m.slopes = ma.slopes;
   if (ma.softcap > 0.f) {
     m.cap_in = scale / ma.softcap;
@@ -486,7 +486,7 @@ int run_chain(const void* q, const void* k, const void* v, const void* o, const 
   p.n_part = p.G / p.gsz;
   p.n_qt = ceil_div(S_q, BQ);
   p.n_kt = ceil_div(S_kv, BN);
-  p.scale = scale;
+  p.scale = mods.on == MOD_CAP ? -scale : scale;  // (those kernels form -dS: score.cuh)
   p.scale_log2 = scale * 1.4426950408889634f;
   p.causal = causal ? 1 : 0;
   p.bottom_right = bottom_right ? 1 : 0;

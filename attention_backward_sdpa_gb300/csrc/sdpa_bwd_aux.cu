@@ -196,8 +196,14 @@ __global__ void __launch_bounds__(PRE_THREADS, 2) sdpa_bwd_preprocess(const Chai
           delta = dot;
         }
         if (qs_ok) {
-          qs[qi] = lse2;
-          qs[BQ + qi] = delta;
+          if (p.mods.on) {  // negated, with the distance bias of the row within its tile (score.cuh)
+            const float s2 = p.mods.slopes ? p.mods.slopes[bh % (unsigned)p.Hq] * LOG2E : 0.f;
+            qs[qi] = -(lse2 + s2 * (float)qi);
+            qs[BQ + qi] = -delta;
+          } else {
+            qs[qi] = lse2;
+            qs[BQ + qi] = delta;
+          }
         }
         // Sink term of this row: exp(sink - LSE) * delta (0 for a row past the
         // length, whose delta is 0, or with LSE = -inf, whose lse2 is +inf).

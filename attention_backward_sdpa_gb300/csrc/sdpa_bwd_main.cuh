@@ -198,9 +198,9 @@ __device__ __forceinline__ uint32_t fake_nvfp4_p_pair(float p0, float p1, float 
 // reduction, every dS^T tile is stored to the workspace for the dQ kernel.
 // BIAS adds the additive bias to the replay and writes dBias (when p.dbias).
 // QAT writes G3's P^T fake-quantized to NVFP4. F16: fp16 io tensors (and
-// fp16 P^T / dS^T MMA operands) instead of bf16. MOD: capped and distance-biased
-// scores and row ranges (score.cuh).
-template <int D, bool DS_OUT, bool BIAS, bool QAT = false, bool F16 = false, bool MOD = false>
+// fp16 P^T / dS^T MMA operands) instead of bf16. MOD (MOD_ROWS,
+// MOD_CAP): modified scores (score.cuh).
+template <int D, bool DS_OUT, bool BIAS, bool QAT = false, bool F16 = false, int MOD = MOD_NONE>
 __global__ void __launch_bounds__(MAIN_THREADS, 1)
     sdpa_bwd_main(const __grid_constant__ MainMaps maps, const ChainParams p) {
   using L = MainLayout<D, DS_OUT>;
@@ -255,7 +255,10 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
                                i == BAR_DSREADY + 1 || i == BAR_DQEMPTY || i == BAR_DQEMPTY + 1 ||
                                i == BAR_STAGEREADY || i == BAR_STAGEREADY + 1 || i == BAR_DPREAD ||
                                i == BAR_DPREAD + 1);
-      mbar_init(&bars[i], threads128 ? 128 : 1);
+      // MOD: G3 has an issuer of its own, so a stage is free, and the last MMA done,
+      // when both gradient issuers say so.
+      const bool two = MOD && ((i >= BAR_QEMPTY && i < BAR_QEMPTY + 4) || i == BAR_MMADONE);
+      mbar_init(&bars[i], threads128 ? 128 : two ? 2 : 1);
     }
     fence_mbar_init();
   }
@@ -324,6 +327,40 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
   // heads in turn: head bh0 + t / n1, query tile qt_hi - t % n1.
   const int n1 = qt_hi >= qt_lo ? qt_hi - qt_lo + 1 : 0;  // query tiles per head
   const int n = p.gsz * n1;
+
+  // MOD: G3 of every tile on a warp of its own. Behind one issuer G3 of a tile waits for
+  // the other warpgroup's dS (G4 of the tile before), and with it the slot's next score
+  // GEMM; the longer replay of modified scores made that wait the tile's pace (main kernel
+  // of bwd_capped_gqa 372 us before, 339 us after).
+  auto issue_g3 = [&]() {
+    if constexpr (MOD) {
+      pdl_wait_prior_grid();
+      constexpr uint32_t ID_G3 = idesc_io(128, D, false, true, F16);
+      constexpr uint64_t T_MN = sdesc_sw128_template(L::BLK_Q, 1024);
+      for (int u = 0; u < n; ++u) {
+        const int su = u & 1, stu = u % NSTAGE, ju = u >> 1;
+        const uint32_t aDO = smem_u32(sDO + stu * L::TILE_Q);
+        // P(u) written implies that its G1 ran, so Q and dO of the stage have landed; the
+        // wait on the stage makes dO's arrival explicit for this warp.
+        if (!mbar_wait(&bars[BAR_PREADY + su], ju & 1, abort_flag, WAIT_LIMIT_NS) ||
+            !mbar_wait(&bars[BAR_QFULL + stu], (u / NSTAGE) & 1, abort_flag, WAIT_LIMIT_NS))
+          break;
+        __syncwarp();
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < BQ / 16; ++k)
+            mma_ts(tmem + L::COL_DV, tmem + L::col_s(su) + 8 * k, sdesc_at(T_MN, aDO + k * 2048), ID_G3,
+                   (u > 0 || k > 0));
+          mma_commit(&bars[BAR_SFREE + su]);
+          if (u + NSTAGE < n) mma_commit(&bars[BAR_QEMPTY + stu]);
+        }
+        __syncwarp();
+      }
+      if (n > 0 && elect_one()) mma_commit(&bars[BAR_MMADONE]);
+      __syncwarp();
+    }
+  };
 
   if (warp >= 12) {
     regs_decrease<REGS_CTRL>();
@@ -449,18 +486,20 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
           const uint32_t aQ = smem_u32(sQ + stu * L::TILE_Q);
           const uint32_t aDO = smem_u32(sDO + stu * L::TILE_Q);
           const uint32_t aDS = smem_u32(sDS + su * L::TILE_DS);
-          if (!mbar_wait(&bars[BAR_PREADY + su], ju & 1, abort_flag, WAIT_LIMIT_NS)) break;
-          __syncwarp();
-          tc_fence_after();
-          if (elect_one()) {
-            // G3: dV[key, d] += sum_q P^T[key, q] dO[q, d]; P^T pairs in columns [0,32) of the slot.
+          if constexpr (!MOD) {
+            if (!mbar_wait(&bars[BAR_PREADY + su], ju & 1, abort_flag, WAIT_LIMIT_NS)) break;
+            __syncwarp();
+            tc_fence_after();
+            if (elect_one()) {
+              // G3: dV[key, d] += sum_q P^T[key, q] dO[q, d]; P^T pairs in columns [0,32) of the slot.
 #pragma unroll
-            for (int k = 0; k < BQ / 16; ++k)
-              mma_ts(tmem + L::COL_DV, tmem + L::col_s(su) + 8 * k, sdesc_at(T_MN_Q, aDO + k * 2048),
-                     ID_G34, (u > 0 || k > 0));
-            mma_commit(&bars[BAR_SFREE + su]);
+              for (int k = 0; k < BQ / 16; ++k)
+                mma_ts(tmem + L::COL_DV, tmem + L::col_s(su) + 8 * k, sdesc_at(T_MN_Q, aDO + k * 2048),
+                       ID_G34, (u > 0 || k > 0));
+              mma_commit(&bars[BAR_SFREE + su]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
           if (!mbar_wait(&bars[BAR_DSREADY + su], ju & 1, abort_flag, WAIT_LIMIT_NS)) break;
           __syncwarp();
           tc_fence_after();
@@ -489,6 +528,8 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
         if (n > 0 && elect_one()) mma_commit(&bars[BAR_MMADONE]);
         __syncwarp();
       }
+    } else if (MOD && !DS_OUT && warp == 15) {
+      issue_g3();
     } else if (!DS_OUT && warp == 15) {
       // Idle on this route: this CTA's share of the group's empty key tiles,
       // and the dBias blocks of its key tile that no CTA computes.
@@ -530,6 +571,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
     if (BIAS && DS_OUT && p.dbias != nullptr && !p.dbias_red)
       zero_unvisited_dbias_blocks(p, b, bh0, p.gsz, kt, qt_lo, qt_hi, threadIdx.x - 256, 128);
     pdl_wait_prior_grid();
+    if (MOD && DS_OUT && warp == 8) issue_g3();  // (this warpgroup has nothing else to do on this route)
     const int quarter = warp & 3;
     const int d = quarter * 32 + lane;                 // dQ^T lane = head-dim column
     const bool has_rows = quarter * 32 < D;            // warp-uniform
@@ -656,7 +698,10 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
     if constexpr (MOD) row_ranges = key_rows(p, b, k, q_lo_vis, q_hi_vis);
     const float scale_log2 = p.scale_log2;
     uint8_t* ds_row = sDS + slot * L::TILE_DS + row * 128;
-    float P[BQ];
+    float P[MOD ? 1 : BQ];
+    uint64_t P2[MOD ? BQ / 2 : 1];  // MOD: pairs of query rows
+    CapCoef coef;
+    if constexpr (MOD == MOD_CAP) coef = cap_coef(p.mods.cap_c, 1.f);
     bool ok = true;
     constexpr float LOG2E_F = 1.4426950408889634f;
     const bool key_in = k < p.Skv;
@@ -701,10 +746,10 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
         tmem_ld32(t_lane + L::col_s(slot) + 32, rb);
         tmem_ld_wait(ra);
         tmem_ld_wait(rb);
-        mod_replay_half<F16, 0>(mt, qs, ra, P, w);
+        mod_replay_half<MOD, F16, 0>(mt, coef, qs, ra, P2, w);
         __syncwarp();
         tmem_st16(t_lane + L::col_s(slot), w);
-        mod_replay_half<F16, 1>(mt, qs, rb, P, w);
+        mod_replay_half<MOD, F16, 1>(mt, coef, qs, rb, P2, w);
         __syncwarp();
         tmem_st16(t_lane + L::col_s(slot) + 16, w);
       } else {
@@ -782,11 +827,15 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
         const float4* delta4 = reinterpret_cast<const float4*>(qs + BQ);
 #pragma unroll
         for (int chunk = 0; chunk < 8; ++chunk) {  // 8 queries = 16 bytes of dS^T per chunk
+          if constexpr (MOD) {
+            *reinterpret_cast<uint4*>(ds_row + ((chunk ^ (row & 7)) << 4)) =
+                mod_ds_chunk<F16>(mt, P2, qs + BQ, chunk < 4 ? ra : rb, chunk);
+          } else {
           const uint32_t* r = chunk < 4 ? ra : rb;
           const int i = (chunk & 3) * 8;
           const float4 d0 = delta4[chunk * 2], d1 = delta4[chunk * 2 + 1];
           const int c = chunk * 8;
-          float ds[8] = {P[c + 0] * (__uint_as_float(r[i + 0]) - d0.x),
+          const float ds[8] = {P[c + 0] * (__uint_as_float(r[i + 0]) - d0.x),
                                P[c + 1] * (__uint_as_float(r[i + 1]) - d0.y),
                                P[c + 2] * (__uint_as_float(r[i + 2]) - d0.z),
                                P[c + 3] * (__uint_as_float(r[i + 3]) - d0.w),
@@ -794,13 +843,6 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
                                P[c + 5] * (__uint_as_float(r[i + 5]) - d1.y),
                                P[c + 6] * (__uint_as_float(r[i + 6]) - d1.z),
                                P[c + 7] * (__uint_as_float(r[i + 7]) - d1.w)};
-          if constexpr (MOD) {
-            // A masked pair's dP may have overflowed: its dS is 0, not 0 * inf.
-            if (mt.masked) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) ds[e] = P[c + e] == 0.f ? 0.f : ds[e];
-            }
-          }
           const uint32_t w0 = pack_io2<F16>(ds[0], ds[1]);
           const uint32_t w1 = pack_io2<F16>(ds[2], ds[3]);
           const uint32_t w2 = pack_io2<F16>(ds[4], ds[5]);
@@ -829,6 +871,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
                   if (e < rows_in) __stcs(dst + (long long)e * p.Skv, f32_to_16(ds[e], f16));
               }
             }
+          }
           }
         }
       }
@@ -911,30 +954,34 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
   }
 }
 
-template <int D, bool DS_OUT, bool BIAS, bool QAT = false, bool F16 = false, bool MOD = false>
+template <int D, bool DS_OUT, bool BIAS, bool QAT = false, bool F16 = false, int MOD = MOD_NONE>
 static cudaError_t set_main_smem() {
   return cudaFuncSetAttribute(sdpa_bwd_main<D, DS_OUT, BIAS, QAT, F16, MOD>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, MainLayout<D, DS_OUT>::BYTES);
 }
 
 // One CTA per (key tile, head group) work unit.
-template <bool BIAS, bool F16 = false, bool MOD = false>
+template <bool BIAS, bool F16 = false, int MOD = MOD_NONE>
 static cudaError_t launch_main_variant(const MainMaps& maps, const ChainParams& p, cudaStream_t s) {
   const dim3 grid((unsigned)(p.n_kt * p.B * p.Hkv * p.n_part));
   const dim3 block(MAIN_THREADS);
+  // Launched while the preprocess drains, except with modified scores: there the early
+  // start made the chain slower (bwd_capped_gqa 524 us against 483, bwd_packed_docs 247
+  // against 215; without MOD the two are equal).
+  constexpr bool pdl = MOD == MOD_NONE;
   // D_qk = D_v up to 64 runs on the 64-column kernels, up to 128 on the 128-column
   // ones: TMA zero-fills the columns past D on loads and drops them on stores.
   if (p.Dqk <= 64)
     return launch_kernel(sdpa_bwd_main<64, false, BIAS, false, F16, MOD>, grid, block,
-                         MainLayout<64, false>::BYTES, s, true, maps, p);
+                         MainLayout<64, false>::BYTES, s, pdl, maps, p);
   if (p.ds_route)
     return launch_kernel(sdpa_bwd_main<128, true, BIAS, false, F16, MOD>, grid, block,
-                         MainLayout<128, true>::BYTES, s, true, maps, p);
+                         MainLayout<128, true>::BYTES, s, pdl, maps, p);
   return launch_kernel(sdpa_bwd_main<128, false, BIAS, false, F16, MOD>, grid, block,
-                       MainLayout<128, false>::BYTES, s, true, maps, p);
+                       MainLayout<128, false>::BYTES, s, pdl, maps, p);
 }
 
-template <bool BIAS, bool F16 = false, bool MOD = false>
+template <bool BIAS, bool F16 = false, int MOD = MOD_NONE>
 static cudaError_t main_variant_setup() {
   cudaError_t e = set_main_smem<64, false, BIAS, false, F16, MOD>();
   if (e == cudaSuccess) e = set_main_smem<128, false, BIAS, false, F16, MOD>();

@@ -113,8 +113,8 @@ struct Layout {
 // D_qk 64/128 kernel (bias.cuh): loads of the next tile's bias column issued
 // right after dS, dS' stored as dBias, and the dBias blocks no CTA computes
 // zeroed by an idle warp (or by an empty unit's whole CTA).
-// MOD: capped and distance-biased scores and row ranges (score.cuh).
-template <int DQK, int DV, bool BIAS, bool F16 = false, int SPLIT = 1, bool MOD = false>
+// MOD (MOD_ROWS, MOD_CAP): modified scores (score.cuh).
+template <int DQK, int DV, bool BIAS, bool F16 = false, int SPLIT = 1, int MOD = MOD_NONE>
 __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
     sdpa_bwd_main_ds(const __grid_constant__ MainMaps maps, const ChainParams p) {
   using namespace ds_kernel;
@@ -399,7 +399,10 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
     bool row_ranges = false;
     if constexpr (MOD) row_ranges = key_rows(p, b, k, q_lo_vis, q_hi_vis);
     uint8_t* ds_row = sDS + slot * L::TILE_DS + row * 128;
-    float P[BQ];
+    float P[MOD ? 1 : BQ];
+    uint64_t P2[MOD ? BQ / 2 : 1];  // MOD: pairs of query rows
+    CapCoef coef;
+    if constexpr (MOD == MOD_CAP) coef = cap_coef(p.mods.cap_c, 1.f);
     bool ok = true;
     constexpr float LOG2E_F = 1.4426950408889634f;
     const bool key_in = k < p.Skv;
@@ -439,8 +442,8 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
         tc_fence_before();
         mbar_arrive(&bars[BAR_SREAD + slot]);  // the S^T columns may be overwritten
         if constexpr (MOD) {
-          mod_replay_half<F16, 0>(mt, qs, ra, P, pw[0]);
-          mod_replay_half<F16, 1>(mt, qs, rb, P, pw[1]);
+          mod_replay_half<MOD, F16, 0>(mt, coef, qs, ra, P2, pw[0]);
+          mod_replay_half<MOD, F16, 1>(mt, coef, qs, rb, P2, pw[1]);
         } else {
         const float4* lse4 = reinterpret_cast<const float4*>(qs);
 #pragma unroll
@@ -461,11 +464,13 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
         }
         }
       }
-      if (!MOD && need_mask) {
+      if constexpr (!MOD) {
+        if (need_mask) {
 #pragma unroll
-        for (int i = 0; i < BQ; ++i) {
-          const long long q = q0 + i;
-          if (row_dead || q < q_lo_vis || q > q_hi_vis) P[i] = 0.f;
+          for (int i = 0; i < BQ; ++i) {
+            const long long q = q0 + i;
+            if (row_dead || q < q_lo_vis || q > q_hi_vis) P[i] = 0.f;
+          }
         }
       }
       // P^T columns of this slot are read by G3 of tile t-2 until it completes.
@@ -506,11 +511,15 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
         const float4* delta4 = reinterpret_cast<const float4*>(qs + BQ);
 #pragma unroll
         for (int chunk = 0; chunk < 8; ++chunk) {  // 8 queries = 16 bytes of dS^T per chunk
+          if constexpr (MOD) {
+            *reinterpret_cast<uint4*>(ds_row + ((chunk ^ (row & 7)) << 4)) =
+                mod_ds_chunk<F16>(mt, P2, qs + BQ, chunk < 4 ? ra : rb, chunk);
+          } else {
           const uint32_t* r = chunk < 4 ? ra : rb;
           const int i = (chunk & 3) * 8;
           const float4 d0 = delta4[chunk * 2], d1 = delta4[chunk * 2 + 1];
           const int c = chunk * 8;
-          float ds[8] = {P[c + 0] * (__uint_as_float(r[i + 0]) - d0.x),
+          const float ds[8] = {P[c + 0] * (__uint_as_float(r[i + 0]) - d0.x),
                                P[c + 1] * (__uint_as_float(r[i + 1]) - d0.y),
                                P[c + 2] * (__uint_as_float(r[i + 2]) - d0.z),
                                P[c + 3] * (__uint_as_float(r[i + 3]) - d0.w),
@@ -518,13 +527,6 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
                                P[c + 5] * (__uint_as_float(r[i + 5]) - d1.y),
                                P[c + 6] * (__uint_as_float(r[i + 6]) - d1.z),
                                P[c + 7] * (__uint_as_float(r[i + 7]) - d1.w)};
-          if constexpr (MOD) {
-            // A masked pair's dP may have overflowed: its dS is 0, not 0 * inf.
-            if (mt.masked) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) ds[e] = P[c + e] == 0.f ? 0.f : ds[e];
-            }
-          }
           const uint32_t w0 = pack_io2<F16>(ds[0], ds[1]);
           const uint32_t w1 = pack_io2<F16>(ds[2], ds[3]);
           const uint32_t w2 = pack_io2<F16>(ds[4], ds[5]);
@@ -552,6 +554,7 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
                   if (e < rows_in) __stcs(dst + (long long)e * p.Skv, f32_to_16(ds[e], f16));
               }
             }
+          }
           }
         }
       }
@@ -629,7 +632,7 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
   }
 }
 
-template <int DQK, int DV, bool BIAS, bool F16, int SPLIT, bool MOD = false>
+template <int DQK, int DV, bool BIAS, bool F16, int SPLIT, int MOD = MOD_NONE>
 static cudaError_t set_ds_smem() {
   return cudaFuncSetAttribute(sdpa_bwd_main_ds<DQK, DV, BIAS, F16, SPLIT, MOD>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -642,8 +645,10 @@ static cudaError_t set_ds_smem_all() {
   if (e == cudaSuccess) e = set_ds_smem<DQK, DV, true, false, SPLIT>();
   if (e == cudaSuccess) e = set_ds_smem<DQK, DV, false, true, SPLIT>();
   if (e == cudaSuccess) e = set_ds_smem<DQK, DV, true, true, SPLIT>();
-  if (e == cudaSuccess) e = set_ds_smem<DQK, DV, false, false, SPLIT, true>();
-  if (e == cudaSuccess) e = set_ds_smem<DQK, DV, false, true, SPLIT, true>();
+  if (e == cudaSuccess) e = set_ds_smem<DQK, DV, false, false, SPLIT, MOD_ROWS>();
+  if (e == cudaSuccess) e = set_ds_smem<DQK, DV, false, true, SPLIT, MOD_ROWS>();
+  if (e == cudaSuccess) e = set_ds_smem<DQK, DV, false, false, SPLIT, MOD_CAP>();
+  if (e == cudaSuccess) e = set_ds_smem<DQK, DV, false, true, SPLIT, MOD_CAP>();
   return e;
 }
 
@@ -659,10 +664,12 @@ static cudaError_t launch_main_ds_dims(const MainMaps& maps, const ChainParams& 
   const dim3 grid((unsigned)(p.n_kt * p.B * p.Hq * SPLIT));
   const dim3 block(ds_kernel::THREADS);
   constexpr int bytes = ds_kernel::Layout<DQK, DV, SPLIT>::BYTES;
-  if (p.mods.on && p.f16)
-    return launch_kernel(sdpa_bwd_main_ds<DQK, DV, false, true, SPLIT, true>, grid, block, bytes, s, true, maps, p);
+  if (p.mods.on == MOD_CAP)
+    return p.f16 ? launch_kernel(sdpa_bwd_main_ds<DQK, DV, false, true, SPLIT, MOD_CAP>, grid, block, bytes, s, true, maps, p)
+                 : launch_kernel(sdpa_bwd_main_ds<DQK, DV, false, false, SPLIT, MOD_CAP>, grid, block, bytes, s, true, maps, p);
   if (p.mods.on)
-    return launch_kernel(sdpa_bwd_main_ds<DQK, DV, false, false, SPLIT, true>, grid, block, bytes, s, true, maps, p);
+    return p.f16 ? launch_kernel(sdpa_bwd_main_ds<DQK, DV, false, true, SPLIT, MOD_ROWS>, grid, block, bytes, s, true, maps, p)
+                 : launch_kernel(sdpa_bwd_main_ds<DQK, DV, false, false, SPLIT, MOD_ROWS>, grid, block, bytes, s, true, maps, p);
   if (p.bias != nullptr && p.f16)
     return launch_kernel(sdpa_bwd_main_ds<DQK, DV, true, true, SPLIT>, grid, block, bytes, s, true, maps, p);
   if (p.bias != nullptr)

@@ -115,8 +115,8 @@ __device__ int g_fwd_done[FWD_SLOTS];
 // CTA per SM takes items from the launch's ticket, and the K/V ring, the S/P
 // slots and their barrier phases run on from one item to the next; otherwise
 // one item per CTA (blockIdx.x).
-// MOD: capped and distance-biased scores and row ranges (score.cuh).
-template <int DQK, int DV, bool BIAS, bool F16 = false, bool PERSIST = false, bool MOD = false>
+// MOD (MOD_ROWS, MOD_CAP): modified scores (score.cuh).
+template <int DQK, int DV, bool BIAS, bool F16 = false, bool PERSIST = false, int MOD = MOD_NONE>
 __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
     sdpa_fwd_kernel(const __grid_constant__ FwdMaps maps, const FwdParams p, const int ticket_slot) {
   using namespace fwd_kernel;
@@ -324,10 +324,10 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
     // With a bias the scores are rewritten in place as x = s * c + bias * log2e,
     // and everything below reads them with the factor cs = 1 instead of c.
     // (The same for capped or distance-biased scores.)
-    const bool modified = MOD && (p.mods.cap_in != 0.f || p.mods.slopes != nullptr);
+    const bool modified = MOD == MOD_CAP || (MOD && p.mods.slopes != nullptr);
     const float cs = (BIAS || modified) ? 1.f : c;
     CapCoef coef;
-    if constexpr (MOD) coef = cap_coef(p.mods.cap_c, p.mods.cap_log2);
+    if constexpr (MOD == MOD_CAP) coef = cap_coef(p.mods.cap_c, p.mods.cap_log2);
     uint16_t* const o_base = static_cast<uint16_t*>(p.o);
     const size_t o_bytes = (size_t)p.B * p.Hq * p.Sq * p.Dv * 2;
     // O rows go out in 32-byte stores when every 16-column piece is 32-byte
@@ -408,9 +408,6 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         tmem_ld_wait(sr[0]);
         tmem_ld_wait(sr[1]);
         if constexpr (BIAS) add_bias_row(p, c, braw, bpacked, sr);
-        if constexpr (MOD) {
-          if (modified) modify_score_row(p.mods, coef, c, slope2, (float)(q + w.diag - (k0 + i0)), sr);
-        }
         // Visible keys of this row within the tile: [v_lo, v_hi] relative to k0.
         int v_lo = 0, v_hi = BK - 1;
         if (!live) {
@@ -424,11 +421,16 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         // stores below are .sync.aligned, and a warp split between the two paths
         // would reach them diverged.
         const bool full = __all_sync(0xffffffffu, v_lo <= i0 && v_hi >= i0 + 63);
+        bool capped = false;  // the scores are still to be capped (exp_score_pairs)
+        if constexpr (MOD) {
+          if (modified) capped = modify_score_row<MOD>(p.mods, coef, c, slope2, (float)(q + w.diag - (k0 + i0)), full, sr);
+        }
         float mp[8];
 #pragma unroll
         for (int a = 0; a < 8; ++a) mp[a] = -INFINITY;
         if (MOD && full) {
           mp[0] = max_score_row(sr);
+          if (MOD == MOD_CAP && capped) mp[0] = cap_score(mp[0], coef);
         } else if (full) {
 #pragma unroll
           for (int i = 0; i < 64; ++i) mp[i & 7] = fmaxf(mp[i & 7], __uint_as_float(sr[i >> 5][i & 31]));
@@ -489,7 +491,8 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         for (int c16 = 0; c16 < 2; ++c16) {
           uint32_t wv[16];
           if (MOD && full) {
-            exp_score_pairs<F16>(sr[c16], cs, neg_m, rs, wv);
+            if (MOD == MOD_CAP && capped) exp_score_pairs<F16, true>(sr[c16], coef, cs, neg_m, rs, wv);
+            else exp_score_pairs<F16, false>(sr[c16], coef, cs, neg_m, rs, wv);
           } else if (full) {
 #pragma unroll
             for (int i2 = 0; i2 < 16; ++i2) {
@@ -622,13 +625,13 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
   }
 }
 
-template <int DQK, int DV, bool BIAS, bool F16, bool MOD>
+template <int DQK, int DV, bool BIAS, bool F16, int MOD>
 static cudaError_t set_fwd_smem() {
   return cudaFuncSetAttribute(sdpa_fwd_kernel<DQK, DV, BIAS, F16, true, MOD>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, fwd_kernel::Layout<DQK, DV>::BYTES);
 }
 
-template <bool BIAS, bool F16, bool MOD = false>
+template <bool BIAS, bool F16, int MOD = MOD_NONE>
 static cudaError_t fwd_setup_variant() {
   cudaError_t e = set_fwd_smem<64, 64, BIAS, F16, MOD>();
   if (e == cudaSuccess) e = set_fwd_smem<128, 128, BIAS, F16, MOD>();
@@ -640,14 +643,16 @@ cudaError_t fwd_kernel_setup() {
   if (e == cudaSuccess) e = fwd_setup_variant<true, false>();
   if (e == cudaSuccess) e = fwd_setup_variant<false, true>();
   if (e == cudaSuccess) e = fwd_setup_variant<true, true>();
-  if (e == cudaSuccess) e = fwd_setup_variant<false, false, true>();
-  if (e == cudaSuccess) e = fwd_setup_variant<false, true, true>();
+  if (e == cudaSuccess) e = fwd_setup_variant<false, false, MOD_ROWS>();
+  if (e == cudaSuccess) e = fwd_setup_variant<false, true, MOD_ROWS>();
+  if (e == cudaSuccess) e = fwd_setup_variant<false, false, MOD_CAP>();
+  if (e == cudaSuccess) e = fwd_setup_variant<false, true, MOD_CAP>();
   if (e == cudaSuccess) e = fwd_shared_setup();
   if (e == cudaSuccess) e = fwd_wide_setup();
   return e;
 }
 
-template <bool BIAS, bool F16, bool MOD = false>
+template <bool BIAS, bool F16, int MOD = MOD_NONE>
 static cudaError_t launch_fwd_variant(const FwdMaps& maps, const FwdParams& p, cudaStream_t s, int sms,
                                       int slot) {
   // Persistent: one CTA per SM (more than half its shared memory each) taking
@@ -679,9 +684,12 @@ cudaError_t launch_fwd(const FwdMaps& maps, const FwdParams& p, cudaStream_t s) 
   // (sdpa_fwd_wide.cu).
   if (p.Dqk == 192 && p.Dv == 128) return launch_fwd_shared(maps, p, s, sms, slot);
   if (p.Dqk == 256 && p.Dv == 256) return launch_fwd_wide(maps, p, s, sms, slot);
+  if (p.mods.on == MOD_CAP)
+    return p.f16 ? launch_fwd_variant<false, true, MOD_CAP>(maps, p, s, sms, slot)
+                 : launch_fwd_variant<false, false, MOD_CAP>(maps, p, s, sms, slot);
   if (p.mods.on)
-    return p.f16 ? launch_fwd_variant<false, true, true>(maps, p, s, sms, slot)
-                 : launch_fwd_variant<false, false, true>(maps, p, s, sms, slot);
+    return p.f16 ? launch_fwd_variant<false, true, MOD_ROWS>(maps, p, s, sms, slot)
+                 : launch_fwd_variant<false, false, MOD_ROWS>(maps, p, s, sms, slot);
   if (p.bias)
     return p.f16 ? launch_fwd_variant<true, true>(maps, p, s, sms, slot)
                  : launch_fwd_variant<true, false>(maps, p, s, sms, slot);

@@ -87,7 +87,7 @@ __device__ __forceinline__ void load_fwd_bias_row(const FwdParams& p, long long 
   }
 }
 
-// A thread's 64 scores of a tile rewritten as x = s * c + bias * log2e, the bias
+// A thread's scores of a tile rewritten as x = s * c + bias * log2e, the bias
 // widened from 16-bit pairs (`packed`; fp16 when p.bias_f16, else bf16) or taken
 // as fp32 words. One loop per element form (the choice is uniform across the
 // warp), so that widening an element is a fixed instruction or two: a
@@ -118,80 +118,131 @@ __device__ __forceinline__ void add_bias_row(const FwdParams& p, float c, const 
   }
 }
 
-// A thread's 64 scores of a tile rewritten as the modified scores times log2(e)
-// (score.cuh): scores S of its row and keys kb .. kb + 63, `slope2` the head's slope
+// A thread's scores of a tile rewritten as the modified scores times log2(e)
+// (score.cuh): scores S of its row and keys from kb, `slope2` the head's slope
 // times log2(e) (0 without slopes) and `dist` = q + diag - kb; `coef` the cap's
-// polynomial in log2 units. The branches on the cap and the slopes are uniform across
-// the launch, the one on the scores' size across the warp.
-__device__ __forceinline__ void modify_score_row(const ScoreMods& m, const CapCoef& coef, float c, float slope2,
-                                                 float dist, uint32_t (&sr)[2][32]) {
-  if (m.cap_in != 0.f) {
+// polynomial in log2 units. The branch on the slopes is uniform across the launch, those
+// on the scores' size and on the distances' sign across the warp. Returns true where the
+// scores are left as they are for exp_score_pairs<CAPPED>: a cap alone, every score within the
+// polynomial, every key visible.
+template <int MOD, int NC>
+__device__ __forceinline__ bool modify_score_row(const ScoreMods& m, const CapCoef& coef, float c, float slope2,
+                                                 float dist, bool full, uint32_t (&sr)[NC][32]) {
+  constexpr int N = NC * 32;  // keys kb .. kb + N - 1
+  bool small = false;
+  if constexpr (MOD == MOD_CAP) {
     float big[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < 64; i += 2)
+    for (int i = 0; i < N; i += 2)
       big[(i >> 1) & 3] = max3(big[(i >> 1) & 3], fabsf(__uint_as_float(sr[i >> 5][i & 31])),
                                fabsf(__uint_as_float(sr[i >> 5][(i & 31) + 1])));
-    if (__all_sync(0xffffffffu, max3(big[0], big[1], fmaxf(big[2], big[3])) <= m.cap_small)) {
+    small = __all_sync(0xffffffffu, max3(big[0], big[1], fmaxf(big[2], big[3])) <= m.cap_small);
+  }
+  const bool biased = m.slopes != nullptr;
+  if (MOD == MOD_CAP && small && full && !biased) return true;
+  // Every key at or before its row: the bias is -slope2 (dist - i), one multiply-add a
+  // score without |.|.
+  const bool ahead = __all_sync(0xffffffffu, dist >= (float)(N - 1));
+  const float base = -slope2 * dist;
+  const uint64_t c2 = f2_pack(c, c), log2_cap = f2_pack(m.cap_log2, m.cap_log2);
 #pragma unroll
-      for (int i = 0; i < 64; i += 2) {
-        uint32_t* s = &sr[i >> 5][i & 31];
-        float x0, x1;
-        f2_unpack(tanh2_small(f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1])), coef), x0, x1);
-        s[0] = __float_as_uint(x0);
-        s[1] = __float_as_uint(x1);
+  for (int blk = 0; blk < N / 2 / SIDE; ++blk) {
+    uint64_t x[SIDE], b[SIDE];
+    uint32_t* const s = &sr[blk * SIDE / 16][(blk * SIDE % 16) * 2];
+#pragma unroll
+    for (int i = 0; i < SIDE; ++i) x[i] = f2_pack(s[2 * i], s[2 * i + 1]);
+    if (biased) {
+#pragma unroll
+      for (int i = 0; i < SIDE; ++i) {
+        const float i0 = (float)(2 * (blk * SIDE + i)), i1 = i0 + 1.f;
+        b[i] = ahead ? f2_pack(fmaf(slope2, i0, base), fmaf(slope2, i1, base))
+                     : f2_pack(-slope2 * fabsf(dist - i0), -slope2 * fabsf(dist - i1));
       }
     } else {
-      const uint64_t mult = f2_pack(m.cap_log2, m.cap_log2);
 #pragma unroll
-      for (int i = 0; i < 64; i += 2) {
-        uint32_t* s = &sr[i >> 5][i & 31];
-        float x0, x1;
-        f2_unpack(f2_mul(tanh2_any(__uint_as_float(s[0]), __uint_as_float(s[1]), m.cap_in), mult), x0, x1);
-        s[0] = __float_as_uint(x0);
-        s[1] = __float_as_uint(x1);
+      for (int i = 0; i < SIDE; ++i) b[i] = 0ull;
+    }
+    if constexpr (MOD == MOD_CAP) {
+      if (small) {
+        uint64_t r[SIDE];
+        tanh2_poly(x, coef, r);
+#pragma unroll
+        for (int i = 0; i < SIDE; ++i) x[i] = f2_fma(x[i], r[i], b[i]);
+      } else {
+        tanh2_any(x, m.cap_in);
+#pragma unroll
+        for (int i = 0; i < SIDE; ++i) x[i] = f2_fma(x[i], log2_cap, b[i]);
       }
-    }
-    if (m.slopes != nullptr) {
+    } else {
 #pragma unroll
-      for (int i = 0; i < 64; ++i)
-        sr[i >> 5][i & 31] =
-            __float_as_uint(fmaf(-slope2, fabsf(dist - (float)i), __uint_as_float(sr[i >> 5][i & 31])));
+      for (int i = 0; i < SIDE; ++i) x[i] = f2_fma(x[i], c2, b[i]);
     }
-  } else if (m.slopes != nullptr) {
 #pragma unroll
-    for (int i = 0; i < 64; ++i)
-      sr[i >> 5][i & 31] =
-          __float_as_uint(fmaf(__uint_as_float(sr[i >> 5][i & 31]), c, -slope2 * fabsf(dist - (float)i)));
+    for (int i = 0; i < SIDE; ++i) f2_unpack(x[i], s[2 * i], s[2 * i + 1]);
   }
+  return false;
 }
 
-// The largest of a thread's 64 scores, and their exponentials ex2(x * cs + neg_m) as io
+// The largest of a thread's scores, and their exponentials ex2(x * cs + neg_m) as io
 // pairs with the row sum's partials, in pair instructions: the MOD kernels' forms of the
 // loops that the other instantiations spell out.
-__device__ __forceinline__ float max_score_row(const uint32_t (&sr)[2][32]) {
+template <int NC>
+__device__ __forceinline__ float max_score_row(const uint32_t (&sr)[NC][32]) {
   float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int i = 0; i < 64; i += 2)
+  for (int i = 0; i < NC * 32; i += 2)
     mp[(i >> 1) & 3] = max3(mp[(i >> 1) & 3], __uint_as_float(sr[i >> 5][i & 31]), __uint_as_float(sr[i >> 5][(i & 31) + 1]));
   return max3(mp[0], mp[1], fmaxf(mp[2], mp[3]));
 }
-template <bool F16>
-__device__ __forceinline__ void exp_score_pairs(const uint32_t (&s)[32], float cs, float neg_m, float (&rs)[8],
-                                                uint32_t (&w)[16]) {
+// CAPPED: from scores that modify_score_row() left as they are, ex2(cap * tanh(s) + neg_m)
+// (the row maximum is taken of the scores before: the cap keeps their order).
+template <bool F16, bool CAPPED>
+__device__ __forceinline__ void exp_score_pairs(const uint32_t (&s)[32], const CapCoef& coef, float cs, float neg_m,
+                                                float (&rs)[8], uint32_t (&w)[16]) {
   const uint64_t c2 = f2_pack(cs, cs), m2 = f2_pack(neg_m, neg_m);
   uint64_t sum[4];
 #pragma unroll
   for (int a = 0; a < 4; ++a) sum[a] = f2_pack(rs[2 * a], rs[2 * a + 1]);
 #pragma unroll
-  for (int i2 = 0; i2 < 16; ++i2) {
-    float x0, x1;
-    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i2]), __uint_as_float(s[2 * i2 + 1])), c2, m2), x0, x1);
-    const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-    sum[i2 & 3] = f2_add(sum[i2 & 3], f2_pack(p0, p1));
-    w[i2] = pack_io2<F16>(p0, p1);
+  for (int blk = 0; blk < 16 / SIDE; ++blk) {
+    uint64_t x[SIDE];
+#pragma unroll
+    for (int i = 0; i < SIDE; ++i) x[i] = f2_pack(s[2 * (blk * SIDE + i)], s[2 * (blk * SIDE + i) + 1]);
+    if constexpr (CAPPED) {
+      uint64_t r[SIDE];
+      tanh2_poly(x, coef, r);
+#pragma unroll
+      for (int i = 0; i < SIDE; ++i) x[i] = f2_fma(x[i], r[i], m2);
+    } else {
+#pragma unroll
+      for (int i = 0; i < SIDE; ++i) x[i] = f2_fma(x[i], c2, m2);
+    }
+#pragma unroll
+    for (int i = 0; i < SIDE; ++i) {
+      float x0, x1;
+      f2_unpack(x[i], x0, x1);
+      x[i] = f2_pack(ex2_approx(x0), ex2_approx(x1));
+    }
+#pragma unroll
+    for (int i = 0; i < SIDE; ++i) {
+      float p0, p1;
+      f2_unpack(x[i], p0, p1);
+      sum[i & 3] = f2_add(sum[i & 3], x[i]);
+      w[blk * SIDE + i] = pack_io2<F16>(p0, p1);
+    }
   }
 #pragma unroll
   for (int a = 0; a < 4; ++a) f2_unpack(sum[a], rs[2 * a], rs[2 * a + 1]);
+}
+
+// One capped score in log2 units.
+__device__ __forceinline__ float cap_score(float s, const CapCoef& coef) {
+  const uint64_t x[1] = {f2_pack(s, s)};
+  uint64_t r[1];
+  tanh2_poly(x, coef, r);
+  float y, z;
+  f2_unpack(f2_mul(x[0], r[0]), y, z);
+  return y;
 }
 
 // One work item: 128 query rows (query tile qt, descending so that under a
@@ -202,8 +253,38 @@ struct FwdItem {
   long long diag;
 };
 
-template <bool MOD = false>
-__device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int it) {
+// What an item's bounds read from memory (the batch row's lengths, and under a mask plan
+// the summaries of its two 64-row tiles), so that a caller can have the loads in flight.
+struct FwdItemLoads {
+  int Lq, Lk;
+  int2 s;  // first key and end
+};
+template <int MOD>
+__device__ __forceinline__ FwdItemLoads fwd_item_loads(const FwdParams& p, int it) {
+  FwdItemLoads l;
+  const int BH = p.B * p.Hq, qt = p.n_qt - 1 - it / BH, b = (it % BH) / p.Hq;
+  l.Lq = p.Sq;
+  l.Lk = p.Skv;
+  if (p.seq_q_lens) l.Lq = min(max(p.seq_q_lens[b], 0), p.Sq);
+  if (p.seq_kv_lens) l.Lk = min(max(p.seq_kv_lens[b], 0), p.Skv);
+  l.s = make_int2(0, p.Skv);
+  if constexpr (MOD) {
+    if (p.mods.q_sum != nullptr) {  // the hull of the rows' ranges
+      const int n64 = ceil_div(p.Sq, BQ);
+      const int4* qs = p.mods.q_sum + (long long)b * n64 + 2 * qt;
+      const int4 s0 = qs[0];
+      l.s = make_int2(s0.x, s0.y);
+      if (2 * qt + 1 < n64) {
+        const int4 s1 = qs[1];
+        l.s = make_int2(min(s0.x, s1.x), max(s0.y, s1.y));
+      }
+    }
+  }
+  return l;
+}
+
+template <int MOD = MOD_NONE>
+__device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int it, const FwdItemLoads& l) {
   FwdItem w;
   const int BH = p.B * p.Hq;
   w.qt = p.n_qt - 1 - it / BH;
@@ -212,10 +293,8 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int it) {
   w.h = w.bh % p.Hq;
   w.kvh = b * p.Hkv + w.h / p.G;
   w.q0 = w.qt * fwd_shared::BM;
-  w.Lq = p.Sq;
-  w.Lk = p.Skv;
-  if (p.seq_q_lens) w.Lq = min(max(p.seq_q_lens[b], 0), p.Sq);
-  if (p.seq_kv_lens) w.Lk = min(max(p.seq_kv_lens[b], 0), p.Skv);
+  w.Lq = l.Lq;
+  w.Lk = l.Lk;
   w.diag = p.bottom_right ? (long long)w.Lk - w.Lq : 0;
   const long long Rp = p.window_right > 0 ? p.window_right : 0;
   int kt_lo = 0, kt_hi = -1;
@@ -225,18 +304,8 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int it) {
     if (p.causal) k_hi = min(k_hi, q_last + w.diag + Rp);
     if (p.window_left >= 0) k_lo = max(0ll, (long long)w.q0 + w.diag - p.window_left);
     if constexpr (MOD) {
-      if (p.mods.q_sum != nullptr) {  // the hull of the rows' ranges (two 64-row tiles)
-        const int n64 = ceil_div(p.Sq, BQ);
-        const int4* qs = p.mods.q_sum + (long long)b * n64 + 2 * w.qt;
-        int4 s = qs[0];
-        if (2 * w.qt + 1 < n64) {
-          const int4 s1 = qs[1];
-          s.x = min(s.x, s1.x);
-          s.y = max(s.y, s1.y);
-        }
-        k_lo = max(k_lo, (long long)s.x);
-        k_hi = min(k_hi, (long long)s.y - 1);
-      }
+      k_lo = max(k_lo, (long long)l.s.x);
+      k_hi = min(k_hi, (long long)l.s.y - 1);
     }
     if (k_lo <= k_hi) {
       kt_lo = (int)(k_lo / fwd_shared::BK);
@@ -246,6 +315,10 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int it) {
   w.kt_lo = kt_lo;
   w.n = kt_hi - kt_lo + 1;  // may be 0
   return w;
+}
+template <int MOD = MOD_NONE>
+__device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int it) {
+  return fwd_item<MOD>(p, it, fwd_item_loads<MOD>(p, it));
 }
 
 // What the modified scores add to row q's state of item w: its key range (a mask

@@ -102,8 +102,8 @@ __device__ int g_fwd_wide_done[fwd_shared::FWD_SLOTS];
 
 // BIAS adds the additive bias (FwdParams::bias) to the scaled scores. F16: fp16
 // io tensors (and fp16 P for the PV GEMM) instead of bf16.
-// MOD: capped and distance-biased scores and row ranges (score.cuh).
-template <bool BIAS, bool F16, bool MOD = false>
+// MOD (MOD_ROWS, MOD_CAP): modified scores (score.cuh).
+template <bool BIAS, bool F16, int MOD = MOD_NONE>
 __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
     sdpa_fwd_wide_kernel(const __grid_constant__ FwdMaps maps, const FwdParams p, const int ticket_slot) {
   using namespace fwd_wide;
@@ -307,10 +307,10 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
     // With a bias the scores are rewritten in place as x = s * c + bias * log2e,
     // and everything below reads them with the factor cs = 1 instead of c.
     // (The same for capped or distance-biased scores.)
-    const bool modified = MOD && (p.mods.cap_in != 0.f || p.mods.slopes != nullptr);
+    const bool modified = MOD == MOD_CAP || (MOD && p.mods.slopes != nullptr);
     const float cs = (BIAS || modified) ? 1.f : c;
     CapCoef coef;
-    if constexpr (MOD) coef = cap_coef(p.mods.cap_c, p.mods.cap_log2);
+    if constexpr (MOD == MOD_CAP) coef = cap_coef(p.mods.cap_c, p.mods.cap_log2);
     uint16_t* const o_base = static_cast<uint16_t*>(p.o);
     const size_t o_bytes = (size_t)p.B * p.Hq * p.Sq * D * 2;
     // O rows go out in 32-byte stores when every 16-column piece is 32-byte
@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
         float mt_h = -INFINITY;
         int v_lo = 0, v_hi = -1;
         bool full = false;
+        bool capped = false;  // the scores are still to be capped (exp_score_pairs)
         if (wok) {
           tc_fence_after();
           tmem_ld32(t_lane + 128u * s + i0, sr[0]);
@@ -390,9 +391,6 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
           tmem_ld_wait(sr[0]);
           tmem_ld_wait(sr[1]);
           if constexpr (BIAS) add_bias_row(p, c, braw, bpacked, sr);
-          if constexpr (MOD) {
-            if (modified) modify_score_row(p.mods, coef, c, slope2, (float)(q + w.diag - (k0 + i0)), sr);
-          }
           // Visible keys of this row within the tile: [v_lo, v_hi] relative to k0.
           if (live) {
             v_hi = (int)min((long long)BK - 1, min((long long)w.Lk - 1, k_vis_hi) - k0);
@@ -401,11 +399,15 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
           // Unmasked path when this warpgroup's 64 keys are visible to the whole
           // warp (warp-uniform: the tensor-memory stores below are .sync.aligned).
           full = __all_sync(0xffffffffu, v_lo <= i0 && v_hi >= i0 + 63);
+          if constexpr (MOD) {
+            if (modified) capped = modify_score_row<MOD>(p.mods, coef, c, slope2, (float)(q + w.diag - (k0 + i0)), full, sr);
+          }
           float mp[8];
 #pragma unroll
           for (int a = 0; a < 8; ++a) mp[a] = -INFINITY;
           if (MOD && full) {
             mp[0] = max_score_row(sr);
+            if (MOD == MOD_CAP && capped) mp[0] = cap_score(mp[0], coef);
           } else if (full) {
 #pragma unroll
             for (int i = 0; i < 64; ++i) mp[i & 7] = fmaxf(mp[i & 7], __uint_as_float(sr[i >> 5][i & 31]));
@@ -478,7 +480,8 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
         for (int c16 = 0; c16 < 2; ++c16) {
           uint32_t wv[16];
           if (MOD && full) {
-            exp_score_pairs<F16>(sr[c16], cs, neg_m, rs, wv);
+            if (MOD == MOD_CAP && capped) exp_score_pairs<F16, true>(sr[c16], coef, cs, neg_m, rs, wv);
+            else exp_score_pairs<F16, false>(sr[c16], coef, cs, neg_m, rs, wv);
           } else if (full) {
 #pragma unroll
             for (int i2 = 0; i2 < 16; ++i2) {
@@ -590,7 +593,7 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
   }
 }
 
-template <bool BIAS, bool F16, bool MOD = false>
+template <bool BIAS, bool F16, int MOD = MOD_NONE>
 static cudaError_t set_fwd_wide_smem() {
   return cudaFuncSetAttribute(sdpa_fwd_wide_kernel<BIAS, F16, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               fwd_wide::BYTES);
@@ -601,12 +604,14 @@ cudaError_t fwd_wide_setup() {
   if (e == cudaSuccess) e = set_fwd_wide_smem<true, false>();
   if (e == cudaSuccess) e = set_fwd_wide_smem<false, true>();
   if (e == cudaSuccess) e = set_fwd_wide_smem<true, true>();
-  if (e == cudaSuccess) e = set_fwd_wide_smem<false, false, true>();
-  if (e == cudaSuccess) e = set_fwd_wide_smem<false, true, true>();
+  if (e == cudaSuccess) e = set_fwd_wide_smem<false, false, MOD_ROWS>();
+  if (e == cudaSuccess) e = set_fwd_wide_smem<false, true, MOD_ROWS>();
+  if (e == cudaSuccess) e = set_fwd_wide_smem<false, false, MOD_CAP>();
+  if (e == cudaSuccess) e = set_fwd_wide_smem<false, true, MOD_CAP>();
   return e;
 }
 
-template <bool BIAS, bool F16, bool MOD = false>
+template <bool BIAS, bool F16, int MOD = MOD_NONE>
 static cudaError_t launch_wide_variant(const FwdMaps& maps, const FwdParams& p, cudaStream_t s, int sms,
                                        int slot) {
   const long long items = (long long)p.n_qt * p.B * p.Hq;
@@ -618,9 +623,12 @@ static cudaError_t launch_wide_variant(const FwdMaps& maps, const FwdParams& p, 
 cudaError_t launch_fwd_wide(const FwdMaps& maps, const FwdParams& p, cudaStream_t s, int sms, int slot) {
   if (p.Dqk != fwd_wide::D || p.Dv != fwd_wide::D || sms <= 0 || slot < 0 || slot >= fwd_shared::FWD_SLOTS)
     return cudaErrorInvalidValue;
+  if (p.mods.on == MOD_CAP)
+    return p.f16 ? launch_wide_variant<false, true, MOD_CAP>(maps, p, s, sms, slot)
+                 : launch_wide_variant<false, false, MOD_CAP>(maps, p, s, sms, slot);
   if (p.mods.on)
-    return p.f16 ? launch_wide_variant<false, true, true>(maps, p, s, sms, slot)
-                 : launch_wide_variant<false, false, true>(maps, p, s, sms, slot);
+    return p.f16 ? launch_wide_variant<false, true, MOD_ROWS>(maps, p, s, sms, slot)
+                 : launch_wide_variant<false, false, MOD_ROWS>(maps, p, s, sms, slot);
   if (p.bias)
     return p.f16 ? launch_wide_variant<true, true>(maps, p, s, sms, slot)
                  : launch_wide_variant<true, false>(maps, p, s, sms, slot);
