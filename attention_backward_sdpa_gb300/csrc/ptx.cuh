@@ -418,6 +418,12 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// The smallest of three (a NaN operand is ignored, as by fminf).
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // The largest of three (a NaN operand is ignored, as by fmaxf).
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;

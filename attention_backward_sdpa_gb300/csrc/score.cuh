@@ -32,7 +32,7 @@ struct ScoreMods {
   float cap_in;        // scale / cap: tanh argument per unit of q . k (0: no cap)
   float cap_log2;      // cap * log2(e)
   float cap_small;     // |q . k| up to which the polynomial below serves (may be 0)
-  float cap_c[6];      // its coefficients in powers of q . k: TANH_C[i] * cap_in^(2 i + 1)
+  float cap_c[5];      // its coefficients in powers of q . k: TANH_C[i] * cap_in^(2 i + 1)
   const float* slopes; // (Hq,) distance slopes, or null
   // Mask plan regions, or null. lo/hi are keys, clamped to [0, S_kv].
   const int2* ranges;  // [B][n_qt * 64] {lo, hi}; rows past S_q hold {0, 0}
@@ -68,9 +68,9 @@ __host__ __device__ inline MaskPlanLayout mask_plan_layout(int B, int n_qt, int 
 
 // tanh(y), y = s * cap_in. Two forms, both accurate relative to the value (a large cap
 // multiplies whatever absolute error small values have):
-//   |y| <= 0.8   an odd polynomial of degree 11 (least-maximum fit of tanh(y) / y in
-//                y^2, 5.8e-8 before its roundings), with the powers of cap_in taken
-//                into its coefficients: 7 multiply-adds, no division;
+//   |y| <= 0.65  an odd polynomial of degree 9 (least-maximum fit of tanh(y) / y in
+//                y^2, 1.5e-7 before its roundings), with the powers of cap_in taken
+//                into its coefficients: 6 multiply-adds, no division;
 //   any y        y N(y^2) / D(y^2), N and D of degree 4, fitted on [0, 8] (6.4e-9,
 //                3.1e-7 with the fp32 roundings), y clamped to [-8, 8] (1 - tanh(8) =
 //                2.3e-7): 12 multiply-adds and a reciprocal.
@@ -78,35 +78,34 @@ __host__ __device__ inline MaskPlanLayout mask_plan_layout(int B, int n_qt, int 
 // scores come near the cap. (The quotient 1 - 2 / (1 + e^2y) would take two
 // special-function results a score where the softmax's exponential already fills that
 // unit, and rounds small values to multiples of 2^-24.)
-constexpr float TANH_SMALL = 0.8f;
-constexpr float TANH_C[6] = {9.999999421e-01f,  -3.333267492e-01f, 1.332104826e-01f,
-                             -5.311431475e-02f, 1.909329914e-02f,  -4.355298764e-03f};
+constexpr float TANH_SMALL = 0.65f;
+constexpr float TANH_C[5] = {9.999998465e-01f, -3.333150019e-01f, 1.329787373e-01f, -5.151791598e-02f,
+                             1.462508501e-02f};
 constexpr float TANH_CLAMP = 8.0f;
 
 // The polynomial's coefficients as pairs, times `mult` (1: tanh; cap * log2(e): the
 // capped score in log2 units).
 struct CapCoef {
-  uint64_t c[6];
+  uint64_t c[5];
 };
-__device__ __forceinline__ CapCoef cap_coef(const float (&c)[6], float mult) {
+__device__ __forceinline__ CapCoef cap_coef(const float (&c)[5], float mult) {
   CapCoef k;
 #pragma unroll
-  for (int i = 0; i < 6; ++i) k.c[i] = f2_pack(c[i] * mult, c[i] * mult);
+  for (int i = 0; i < 5; ++i) k.c[i] = f2_pack(c[i] * mult, c[i] * mult);
   return k;
 }
 // N pairs of scores s, |s| <= cap_small, step by step side by side (left to itself the
-// compiler takes one pair's eight dependent steps after another's, 1,550 cycles for a
-// thread's 64 scores with their exponentials against TANH_SIDE_BY_SIDE): r[i] = the
-// polynomial's value, so that mult * tanh(s * cap_in) = s * r.
+// compiler may take one pair's dependent steps after another's): r[i] = the polynomial's
+// value, so that mult * tanh(s * cap_in) = s * r.
 template <int N>
 __device__ __forceinline__ void tanh2_poly(const uint64_t (&s)[N], const CapCoef& k, uint64_t (&r)[N]) {
   uint64_t u[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) u[i] = f2_mul(s[i], s[i]);
 #pragma unroll
-  for (int i = 0; i < N; ++i) r[i] = f2_fma(u[i], k.c[5], k.c[4]);
+  for (int i = 0; i < N; ++i) r[i] = f2_fma(u[i], k.c[4], k.c[3]);
 #pragma unroll
-  for (int c = 3; c >= 0; --c)
+  for (int c = 2; c >= 0; --c)
 #pragma unroll
     for (int i = 0; i < N; ++i) r[i] = f2_fma(u[i], r[i], k.c[c]);
 }

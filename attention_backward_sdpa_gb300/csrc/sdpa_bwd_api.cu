@@ -366,7 +366,7 @@ int fill_mods(const ModArgs& ma, float scale, int B, int S_q, int S_kv, ScoreMod
     // the squared scores up to its bound) stay finite.
     double power = m.cap_in;
     m.cap_small = (float)std::fmin(TANH_SMALL / (double)m.cap_in, 1e18);
-    for (int i = 0; i < 6; ++i, power *= (double)m.cap_in * m.cap_in) {
+    for (int i = 0; i < 5; ++i, power *= (double)m.cap_in * m.cap_in) {
       m.cap_c[i] = (float)(TANH_C[i] * power);
       if (!std::isfinite(m.cap_c[i] * m.cap_log2)) m.cap_small = -1.f;  // the quotient serves every score
     }

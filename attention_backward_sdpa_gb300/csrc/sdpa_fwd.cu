@@ -421,16 +421,13 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         // stores below are .sync.aligned, and a warp split between the two paths
         // would reach them diverged.
         const bool full = __all_sync(0xffffffffu, v_lo <= i0 && v_hi >= i0 + 63);
-        bool capped = false;  // the scores are still to be capped (exp_score_pairs)
-        if constexpr (MOD) {
-          if (modified) capped = modify_score_row<MOD>(p.mods, coef, c, slope2, (float)(q + w.diag - (k0 + i0)), full, sr);
-        }
+        ModChunks ch;  // MOD: what the warp sees of its two chunks
         float mp[8];
 #pragma unroll
         for (int a = 0; a < 8; ++a) mp[a] = -INFINITY;
-        if (MOD && full) {
-          mp[0] = max_score_row(sr);
-          if (MOD == MOD_CAP && capped) mp[0] = cap_score(mp[0], coef);
+        if constexpr (MOD) {
+          mp[0] = mod_scores<MOD>(p.mods, coef, c, cs, modified, slope2, (float)(q + w.diag - (k0 + i0)), v_lo - i0,
+                                  v_hi - i0, sr, ch);
         } else if (full) {
 #pragma unroll
           for (int i = 0; i < 64; ++i) mp[i & 7] = fmaxf(mp[i & 7], __uint_as_float(sr[i >> 5][i & 31]));
@@ -440,7 +437,8 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
             if (i0 + i >= v_lo && i0 + i <= v_hi) mp[i & 7] = fmaxf(mp[i & 7], __uint_as_float(sr[i >> 5][i & 31]));
         }
         const float mt = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
-                               fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7]))) * cs;  // cs > 0
+                               fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7]))) *
+                         (MOD ? 1.f : cs);  // cs > 0 (mod_scores has multiplied)
         // Raise the reference when the tile's maximum exceeds it by more than the
         // threshold (or when it is the row's first visible key).
         const bool raise = mt > m + RESCALE_THRESHOLD || (m == -INFINITY && mt > -INFINITY);
@@ -490,9 +488,8 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
 #pragma unroll
         for (int c16 = 0; c16 < 2; ++c16) {
           uint32_t wv[16];
-          if (MOD && full) {
-            if (MOD == MOD_CAP && capped) exp_score_pairs<F16, true>(sr[c16], coef, cs, neg_m, rs, wv);
-            else exp_score_pairs<F16, false>(sr[c16], coef, cs, neg_m, rs, wv);
+          if constexpr (MOD) {
+            mod_exp_chunk<F16, MOD>(sr[c16], ch, c16, coef, cs, neg_m, rs, wv);
           } else if (full) {
 #pragma unroll
             for (int i2 = 0; i2 < 16; ++i2) {

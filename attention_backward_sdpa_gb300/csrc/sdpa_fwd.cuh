@@ -118,39 +118,30 @@ __device__ __forceinline__ void add_bias_row(const FwdParams& p, float c, const 
   }
 }
 
-// A thread's scores of a tile rewritten as the modified scores times log2(e)
-// (score.cuh): scores S of its row and keys from kb, `slope2` the head's slope
-// times log2(e) (0 without slopes) and `dist` = q + diag - kb; `coef` the cap's
-// polynomial in log2 units. The branch on the slopes is uniform across the launch, those
-// on the scores' size and on the distances' sign across the warp. Returns true where the
-// scores are left as they are for exp_score_pairs<CAPPED>: a cap alone, every score within the
-// polynomial, every key visible.
-template <int MOD, int NC>
-__device__ __forceinline__ bool modify_score_row(const ScoreMods& m, const CapCoef& coef, float c, float slope2,
-                                                 float dist, bool full, uint32_t (&sr)[NC][32]) {
-  constexpr int N = NC * 32;  // keys kb .. kb + N - 1
-  bool small = false;
-  if constexpr (MOD == MOD_CAP) {
-    float big[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < N; i += 2)
-      big[(i >> 1) & 3] = max3(big[(i >> 1) & 3], fabsf(__uint_as_float(sr[i >> 5][i & 31])),
-                               fabsf(__uint_as_float(sr[i >> 5][(i & 31) + 1])));
-    small = __all_sync(0xffffffffu, max3(big[0], big[1], fmaxf(big[2], big[3])) <= m.cap_small);
-  }
-  const bool biased = m.slopes != nullptr;
-  if (MOD == MOD_CAP && small && full && !biased) return true;
+// ---- Modified scores (MOD): a thread's 64 keys of a tile in two chunks of 32. Which
+// chunks a warp sees in full, in part or not at all is decided for the warp, so that a
+// mask's edge costs the one chunk that it crosses, and a chunk that no row sees costs
+// nothing but its zeros.
+struct ModChunks {
+  bool any[2];      // some row of the warp sees a key of the chunk
+  bool deferred[2]; // the scores are left to be capped with the exponentials
+};
+
+// The chunk's scores as modified scores times log2(e): keys from kb, `dist` = q + diag - kb.
+template <int MOD>
+__device__ __forceinline__ void modify_chunk(const ScoreMods& m, const CapCoef& coef, float c, float slope2, float dist,
+                                             bool small, uint32_t (&s)[32]) {
   // Every key at or before its row: the bias is -slope2 (dist - i), one multiply-add a
   // score without |.|.
-  const bool ahead = __all_sync(0xffffffffu, dist >= (float)(N - 1));
+  const bool biased = m.slopes != nullptr, ahead = __all_sync(0xffffffffu, dist >= 31.f);
   const float base = -slope2 * dist;
   const uint64_t c2 = f2_pack(c, c), log2_cap = f2_pack(m.cap_log2, m.cap_log2);
 #pragma unroll
-  for (int blk = 0; blk < N / 2 / SIDE; ++blk) {
+  for (int blk = 0; blk < 16 / SIDE; ++blk) {
     uint64_t x[SIDE], b[SIDE];
-    uint32_t* const s = &sr[blk * SIDE / 16][(blk * SIDE % 16) * 2];
+    uint32_t* const sb = s + blk * SIDE * 2;
 #pragma unroll
-    for (int i = 0; i < SIDE; ++i) x[i] = f2_pack(s[2 * i], s[2 * i + 1]);
+    for (int i = 0; i < SIDE; ++i) x[i] = f2_pack(sb[2 * i], sb[2 * i + 1]);
     if (biased) {
 #pragma unroll
       for (int i = 0; i < SIDE; ++i) {
@@ -178,27 +169,83 @@ __device__ __forceinline__ bool modify_score_row(const ScoreMods& m, const CapCo
       for (int i = 0; i < SIDE; ++i) x[i] = f2_fma(x[i], c2, b[i]);
     }
 #pragma unroll
-    for (int i = 0; i < SIDE; ++i) f2_unpack(x[i], s[2 * i], s[2 * i + 1]);
+    for (int i = 0; i < SIDE; ++i) f2_unpack(x[i], sb[2 * i], sb[2 * i + 1]);
   }
-  return false;
 }
 
-// The largest of a thread's scores, and their exponentials ex2(x * cs + neg_m) as io
-// pairs with the row sum's partials, in pair instructions: the MOD kernels' forms of the
-// loops that the other instantiations spell out.
-template <int NC>
-__device__ __forceinline__ float max_score_row(const uint32_t (&sr)[NC][32]) {
-  float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int i = 0; i < NC * 32; i += 2)
-    mp[(i >> 1) & 3] = max3(mp[(i >> 1) & 3], __uint_as_float(sr[i >> 5][i & 31]), __uint_as_float(sr[i >> 5][(i & 31) + 1]));
-  return max3(mp[0], mp[1], fmaxf(mp[2], mp[3]));
+// One capped score in log2 units.
+__device__ __forceinline__ float cap_score(float s, const CapCoef& coef) {
+  const uint64_t x[1] = {f2_pack(s, s)};
+  uint64_t r[1];
+  tanh2_poly(x, coef, r);
+  float y, z;
+  f2_unpack(f2_mul(x[0], r[0]), y, z);
+  return y;
 }
-// CAPPED: from scores that modify_score_row() left as they are, ex2(cap * tanh(s) + neg_m)
-// (the row maximum is taken of the scores before: the cap keeps their order).
+
+// A tile's scores prepared for the exponentials: modified where `modified` (capped or
+// biased; else they stay, and the exponent takes them times cs), -inf where masked.
+// Keys [lo, hi] of the thread's 64 are visible to its row; `dist` = q + diag - its first
+// key. Returns the row's maximum in log2 units (-inf when it sees none).
+template <int MOD>
+__device__ __forceinline__ float mod_scores(const ScoreMods& m, const CapCoef& coef, float c, float cs, bool modified,
+                                            float slope2, float dist, int lo, int hi, uint32_t (&sr)[2][32],
+                                            ModChunks& ch) {
+  bool full[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int l = lo - 32 * k, h = hi - 32 * k;
+    full[k] = __all_sync(0xffffffffu, l <= 0 && h >= 31);
+    ch.any[k] = full[k] || __any_sync(0xffffffffu, l <= h && l <= 31 && h >= 0);
+    ch.deferred[k] = false;
+  }
+  float big[2] = {-INFINITY, -INFINITY};  // the chunks' largest scores as they are
+  bool small = false;
+  if constexpr (MOD == MOD_CAP) {
+    float least = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (!ch.any[k]) continue;
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, mn[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        const float s0 = __uint_as_float(sr[k][i]), s1 = __uint_as_float(sr[k][i + 1]);
+        mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], s0, s1);
+        mn[(i >> 1) & 3] = min3(mn[(i >> 1) & 3], s0, s1);
+      }
+      big[k] = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+      least = min3(least, fminf(mn[0], mn[1]), fminf(mn[2], mn[3]));
+    }
+    small = __all_sync(0xffffffffu, max3(big[0], big[1], -least) <= m.cap_small);
+  }
+  float mt = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (!ch.any[k]) continue;
+    if (MOD == MOD_CAP && small && full[k] && m.slopes == nullptr) {
+      ch.deferred[k] = true;
+      mt = fmaxf(mt, cap_score(big[k], coef));
+      continue;
+    }
+    if (modified) modify_chunk<MOD>(m, coef, c, slope2, dist - (float)(32 * k), small, sr[k]);
+    if (!full[k]) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < lo - 32 * k || i > hi - 32 * k) sr[k][i] = 0xFF800000u;  // -inf
+    }
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+      mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(sr[k][i]), __uint_as_float(sr[k][i + 1]));
+    mt = fmaxf(mt, max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * cs);  // cs > 0
+  }
+  return mt;
+}
+
+// The chunk's P = ex2(x * cs + neg_m) as io pairs, added to the row sum's partials.
 template <bool F16, bool CAPPED>
-__device__ __forceinline__ void exp_score_pairs(const uint32_t (&s)[32], const CapCoef& coef, float cs, float neg_m,
-                                                float (&rs)[8], uint32_t (&w)[16]) {
+__device__ __forceinline__ void exp_chunk(const uint32_t (&s)[32], const CapCoef& coef, float cs, float neg_m,
+                                          float (&rs)[8], uint32_t (&w)[16]) {
   const uint64_t c2 = f2_pack(cs, cs), m2 = f2_pack(neg_m, neg_m);
   uint64_t sum[4];
 #pragma unroll
@@ -234,15 +281,17 @@ __device__ __forceinline__ void exp_score_pairs(const uint32_t (&s)[32], const C
 #pragma unroll
   for (int a = 0; a < 4; ++a) f2_unpack(sum[a], rs[2 * a], rs[2 * a + 1]);
 }
-
-// One capped score in log2 units.
-__device__ __forceinline__ float cap_score(float s, const CapCoef& coef) {
-  const uint64_t x[1] = {f2_pack(s, s)};
-  uint64_t r[1];
-  tanh2_poly(x, coef, r);
-  float y, z;
-  f2_unpack(f2_mul(x[0], r[0]), y, z);
-  return y;
+template <bool F16, int MOD>
+__device__ __forceinline__ void mod_exp_chunk(const uint32_t (&s)[32], const ModChunks& ch, int k, const CapCoef& coef,
+                                              float cs, float neg_m, float (&rs)[8], uint32_t (&w)[16]) {
+  if (!ch.any[k]) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = 0u;
+  } else if (MOD == MOD_CAP && ch.deferred[k]) {
+    exp_chunk<F16, true>(s, coef, cs, neg_m, rs, w);
+  } else {
+    exp_chunk<F16, false>(s, coef, cs, neg_m, rs, w);
+  }
 }
 
 // One work item: 128 query rows (query tile qt, descending so that under a
