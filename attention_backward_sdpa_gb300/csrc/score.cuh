@@ -149,8 +149,9 @@ __device__ __forceinline__ void tanh2_any(uint64_t (&s)[N], float cap_in) {
     s[i] = f2_mul(f2_mul(s[i], n[i]), f2_pack(r0, r1));
   }
 }
-// Pairs a step takes side by side.
-constexpr int SIDE = 8;
+// Pairs a step takes side by side: 16 where the registers allow it (a thread's 64 scores
+// 484 cycles against 598 with 8), 8 in the backward.
+constexpr int SIDE = 8, FWD_SIDE = 16;
 
 // The backward's replay of one tile for one thread (its key k against 64 query
 // rows): what the modified scores and the masks need besides S^T.

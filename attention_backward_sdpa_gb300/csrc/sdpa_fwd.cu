@@ -79,7 +79,7 @@ struct Layout {
   static constexpr int TILE_K = BK * DQK * 2;
   static constexpr int TILE_V = BK * DV * 2;
   static constexpr int STAGE = TILE_K + TILE_V;
-  static constexpr int NS_FIT = (232448 - TILE_Q - NUM_BARS * 8 - 2 * 256 * 4 - 64) / STAGE;
+  static constexpr int NS_FIT = (232448 - TILE_Q - NUM_BARS * 8 - 2 * 256 * 4 - 64 - (RING + 2) * MSG_INTS * 4) / STAGE;
   static constexpr int NS = NS_FIT > 4 ? 4 : NS_FIT;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = TILE_Q;
@@ -88,7 +88,7 @@ struct Layout {
   static constexpr int OFF_MISC = OFF_XCH + 2 * 256 * 4;
   // More than half an SM's shared memory keeps one CTA per SM, so the 512
   // tensor-memory columns are never contended.
-  static constexpr int BYTES_RAW = OFF_MISC + 64;
+  static constexpr int BYTES_RAW = OFF_MISC + 64 + (RING + 2) * MSG_INTS * 4;
   static constexpr int BYTES = BYTES_RAW > 120 * 1024 ? BYTES_RAW : 120 * 1024;
   // Two O accumulators, one per half of the keys: O_h at COL_O + 128 h.
   static constexpr uint32_t COL_O = 128 * NSLOT;
@@ -135,6 +135,9 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   volatile int* ring = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 16);  // [RING] items
   volatile int* sitem = ring + RING;  // [2] the softmax warpgroups' current item, by parity
+  // MOD: the same two as messages with the items' bounds.
+  volatile int* ring_msg = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 64);
+  volatile int* smsg = ring_msg + RING * MSG_INTS;
   const int n_items = p.n_qt * p.B * p.Hq;
   // Items a CTA walks at most: one without PERSIST, so that the compiler sees
   // a single pass and keeps no state across items.
@@ -153,6 +156,20 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
       }
     }
     return __shfl_sync(0xffffffffu, it, 0);
+  };
+
+  auto next_msg = [&](int e) -> FwdItemMsg {  // MOD
+    FwdItemMsg m{-1, 0, 0, 0, 0};
+    if (lane == 0) {
+      const int r = e % RING;
+      if (mbar_wait(&bars[BAR_RFULL + r], (e / RING) & 1, abort_flag, WAIT_LIMIT_NS)) {
+        m = get_msg(ring_msg + r * MSG_INTS);
+        mbar_arrive(&bars[BAR_REMPTY + r]);
+      }
+    }
+    m.it = __shfl_sync(0xffffffffu, m.it, 0);
+    m.n = __shfl_sync(0xffffffffu, m.n, 0);  // (the issuers need no more; lane 0 has the rest)
+    return m;
   };
 
   if (tid == 0) {
@@ -205,6 +222,7 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         };
         for (int e = 0; e < E_MAX && ok; ++e) {
           int it;
+          FwdItem w;
           if constexpr (PERSIST) {
             // Take the next item and publish it to the other roles.
             const int r = e % RING;
@@ -212,13 +230,22 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
               break;
             it = atomicAdd(&g_fwd_ticket[ticket_slot], 1);
             if (it >= n_items) it = -1;
-            ring[r] = it;
+            if constexpr (MOD) {
+              FwdItemMsg m{it, 0, 0, 0, 0};
+              if (it >= 0) {
+                w = fwd_item<MOD>(p, it);
+                m = FwdItemMsg{it, w.kt_lo, w.n, w.Lq, w.Lk};
+              }
+              put_msg(ring_msg + r * MSG_INTS, m);
+            } else {
+              ring[r] = it;
+            }
             mbar_arrive(&bars[BAR_RFULL + r]);
           } else {
             it = e == 0 ? (int)blockIdx.x : -1;
           }
           if (it < 0) break;
-          const FwdItem w = fwd_item<MOD>(p, it);
+          if constexpr (!MOD) w = fwd_item<MOD>(p, it);
           if (w.n <= 0) continue;
           // The item's first key tiles only wait for stages that earlier items
           // release, so they load before its Q, which waits for the previous
@@ -249,9 +276,16 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
       bool ok = true;
       const uint32_t aQ = smem_u32(sQ);
       for (int e = 0; e < E_MAX && ok; ++e) {
-        const int it = next_item(e);
-        if (it < 0) break;
-        const FwdItem w = fwd_item<MOD>(p, it);
+        FwdItem w;
+        if constexpr (MOD) {
+          const FwdItemMsg m = next_msg(e);
+          if (m.it < 0) break;
+          w.n = m.n;
+        } else {
+          const int it = next_item(e);
+          if (it < 0) break;
+          w = fwd_item<MOD>(p, it);
+        }
         if (w.n <= 0) continue;
         if (warp == 9) {
           ok = mbar_wait(&bars[BAR_QFULL], ni & 1, abort_flag, WAIT_LIMIT_NS);
@@ -336,6 +370,20 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
     int g = 0;
     bool ok = true;
     bool have_next = false;  // the item for this e was taken during the previous epilogue
+    // MOD: that item, and what this thread's row of it reads from memory, on its way while
+    // the epilogue goes on.
+    int next_it = -1;
+    FwdItem next_w{};
+    ModRowLoads next_loads{};
+    auto take_next = [&](int e) {
+      if constexpr (MOD) {
+        const FwdItemMsg t = get_msg(smsg + (e & 1) * MSG_INTS);
+        next_it = t.it;
+        if (t.it < 0) return;
+        next_w = fwd_item(p, t);
+        next_loads = mod_row_loads(p, next_w, next_w.q0 + row);
+      }
+    };
     for (int e = 0; e < E_MAX && ok; ++e) {
       // Warp 0 takes the item for all eight warps, so that they never disagree
       // on it (a wait that gives up can do so in one reader and not in another)
@@ -344,7 +392,20 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
       // own. Double-buffered by parity: a slot is rewritten only after a later
       // barrier that every reader of it has passed.
       int it;
-      if constexpr (PERSIST) {
+      FwdItem w;
+      if constexpr (MOD) {
+        if (!have_next) {
+          if (warp == 0) {
+            const FwdItemMsg t = next_msg(e);
+            if (lane == 0) put_msg(smsg + (e & 1) * MSG_INTS, t);
+          }
+          named_bar_sync(3, 256);
+          take_next(e);
+        }
+        have_next = false;
+        it = next_it;
+        w = next_w;
+      } else if constexpr (PERSIST) {
         if (!have_next) {
           if (warp == 0) {
             const int t = next_item(e);
@@ -358,7 +419,8 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         it = next_item(e);
       }
       if (it < 0) break;
-      const FwdItem w = fwd_item<MOD>(p, it);
+      if constexpr (!MOD) w = fwd_item<MOD>(p, it);
+      const ModRowLoads loads = next_loads;
       const int q = w.q0 + row;
       const long long orow = (long long)w.bh * p.Sq + q;  // O / LSE row
       if (w.n <= 0) {
@@ -368,20 +430,20 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
           uint4* o = reinterpret_cast<uint4*>(o_base + orow * p.Dv);
           if (in_bounds(p.status, o, (size_t)p.Dv * 2, p.o, o_bytes))
             for (int i = 0; i < p.Dv / 8; ++i) o[i] = make_uint4(0u, 0u, 0u, 0u);
-          p.lse[orow] = p.sink ? p.sink[w.h] : -INFINITY;
+          p.lse[orow] = p.sink ? (MOD ? loads.sink : p.sink[w.h]) : -INFINITY;
         }
         continue;
       }
       const bool live = q < w.Lq;
       float m = -INFINITY, l = 0.f;  // this half's reference and sum (the sink goes to half 0)
       if (p.sink && half == 0) {
-        m = p.sink[w.h] * 1.4426950408889634f;
+        m = (MOD ? loads.sink : p.sink[w.h]) * 1.4426950408889634f;
         l = 1.f;
       }
-      long long k_vis_hi = p.causal ? (long long)q + w.diag + Rp : (1ll << 40);
-      long long k_vis_lo = has_window ? (long long)q + w.diag - p.window_left : -(1ll << 40);
-      float slope2 = 0.f;
-      if constexpr (MOD) mod_row(p, w, q, live, k_vis_lo, k_vis_hi, slope2);
+      const long long k_vis_hi = p.causal ? (long long)q + w.diag + Rp : (1ll << 40);
+      const long long k_vis_lo = has_window ? (long long)q + w.diag - p.window_left : -(1ll << 40);
+      ModRow mr;
+      if constexpr (MOD) mr = mod_row(p, w, q, live, loads);
       const long long bias_row =
           BIAS ? (long long)(w.bh / p.Hq) * p.bias_bstride + ((long long)w.h * p.Sq + q) * p.Skv : 0;
       for (int j = 0; j < w.n; ++j, ++g) {
@@ -409,8 +471,9 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         tmem_ld_wait(sr[1]);
         if constexpr (BIAS) add_bias_row(p, c, braw, bpacked, sr);
         // Visible keys of this row within the tile: [v_lo, v_hi] relative to k0.
-        int v_lo = 0, v_hi = BK - 1;
-        if (!live) {
+        int v_lo = 0, v_hi = BK - 1;  // (MOD: mod_chunks)
+        if (MOD) {
+        } else if (!live) {
           v_hi = -1;
         } else {
           v_hi = (int)min((long long)BK - 1, min((long long)w.Lk - 1, k_vis_hi) - k0);
@@ -420,14 +483,16 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         // tile but the mask edges). The choice is warp-uniform: the tensor-memory
         // stores below are .sync.aligned, and a warp split between the two paths
         // would reach them diverged.
-        const bool full = __all_sync(0xffffffffu, v_lo <= i0 && v_hi >= i0 + 63);
-        ModChunks ch;  // MOD: what the warp sees of its two chunks
+        const bool full = !MOD && __all_sync(0xffffffffu, v_lo <= i0 && v_hi >= i0 + 63);
+        ModChunks ch;            // MOD: what the warp sees of its two chunks
+        bool as_before = false;  // MOD: no row of the warp raises its reference
         float mp[8];
 #pragma unroll
         for (int a = 0; a < 8; ++a) mp[a] = -INFINITY;
         if constexpr (MOD) {
-          mp[0] = mod_scores<MOD>(p.mods, coef, c, cs, modified, slope2, (float)(q + w.diag - (k0 + i0)), v_lo - i0,
-                                  v_hi - i0, sr, ch);
+          mod_chunks(mr, k0 + i0, ch);
+          as_before = MOD == MOD_CAP && mod_tile_as_before(p.mods, mr, sr, ch);
+          if (!as_before) mp[0] = mod_scores<MOD>(p.mods, coef, c, cs, modified, mr, k0 + i0, sr, ch);
         } else if (full) {
 #pragma unroll
           for (int i = 0; i < 64; ++i) mp[i & 7] = fmaxf(mp[i & 7], __uint_as_float(sr[i >> 5][i & 31]));
@@ -441,14 +506,14 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
                          (MOD ? 1.f : cs);  // cs > 0 (mod_scores has multiplied)
         // Raise the reference when the tile's maximum exceeds it by more than the
         // threshold (or when it is the row's first visible key).
-        const bool raise = mt > m + RESCALE_THRESHOLD || (m == -INFINITY && mt > -INFINITY);
+        const bool raise = !as_before && (mt > m + RESCALE_THRESHOLD || (m == -INFINITY && mt > -INFINITY));
         const float m_new = raise ? mt : m;
         const float alpha = raise ? ex2_approx(m - m_new) : 1.f;  // 0 when m was -inf
         // O_half holds contributions of this item's earlier tiles once m is
         // finite and j > 0. It is rescaled once G2(g-1) has completed (G2(g)
         // waits for this tile's P_READY).
         const bool rescale_o = raise && j > 0 && m > -INFINITY;
-        if (__any_sync(0xffffffffu, rescale_o)) {
+        if (!as_before && __any_sync(0xffffffffu, rescale_o)) {
           if (!mbar_wait(&bars[BAR_PVDONE + (g - 1) % NSLOT], ((g - 1) / NSLOT) & 1, abort_flag,
                          WAIT_LIMIT_NS)) {
             ok = false;
@@ -475,6 +540,10 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         }
         l *= alpha;
         m = m_new;
+        if constexpr (MOD == MOD_CAP) {
+          if (!as_before && ch.deferred[0] && ch.deferred[1])
+            mr.raw_ok = raise ? ch.big + RESCALE_THRESHOLD / c : fmaxf(mr.raw_ok, ch.big);
+        }
         // P = exp2(x - m) on visible keys, as bf16 pairs into the slot's columns
         // [64 half, 64 half + 32): inside this half's own S columns, which this
         // warp has already read. (Writing into the other half's S columns raced
@@ -538,8 +607,13 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
       if constexpr (PERSIST) {
         // The next item, handed to every softmax warp by the barrier below.
         if (warp == 0) {
-          const int t = next_item(e + 1);
-          if (lane == 0) sitem[(e + 1) & 1] = t;
+          if constexpr (MOD) {
+            const FwdItemMsg t = next_msg(e + 1);
+            if (lane == 0) put_msg(smsg + ((e + 1) & 1) * MSG_INTS, t);
+          } else {
+            const int t = next_item(e + 1);
+            if (lane == 0) sitem[(e + 1) & 1] = t;
+          }
         }
         have_next = true;
       }
@@ -548,6 +622,7 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
       const bool any_fail = named_bar_sync_or(1, 256, !warp_ok);
       const float m0 = xch[row], m1 = xch[128 + row];
       const float l0 = xch[256 + row], l1 = xch[384 + row];
+      if constexpr (MOD) take_next(e + 1);
       named_bar_sync(1, 256);  // the exchange area is free for the next item
       const float M = fmaxf(m0, m1);
       const float a0 = (m0 == -INFINITY) ? 0.f : ex2_approx(m0 - M);

@@ -119,12 +119,26 @@ __device__ __forceinline__ void add_bias_row(const FwdParams& p, float c, const 
 }
 
 // ---- Modified scores (MOD): a thread's 64 keys of a tile in two chunks of 32. Which
-// chunks a warp sees in full, in part or not at all is decided for the warp, so that a
+// chunks are seen in full, in part or not at all is decided for a whole warp, so that a
 // mask's edge costs the one chunk that it crosses, and a chunk that no row sees costs
 // nothing but its zeros.
 struct ModChunks {
-  bool any[2];      // some row of the warp sees a key of the chunk
+  bool full[2];     // every row of the warp sees the whole chunk
+  bool any[2];      // some row may see a key of it
   bool deferred[2]; // the scores are left to be capped with the exponentials
+  float big;        // the largest score of the deferred chunks as it is
+};
+
+// A row's state under modified scores, for one item.
+struct ModRow {
+  int lo, hi;                          // its visible keys [lo, hi] (hi < lo: none)
+  int lo_max, hi_min, lo_min, hi_max;  // the same over the warp's rows: what all and what any of them see
+  int place;                           // q + diag
+  float slope2;                        // the head's distance slope * log2(e)
+  // Scores up to this one need no raise of the softmax reference (a cap alone): the cap
+  // never widens a difference, so a score c x higher than the reference's is at most x
+  // higher capped.
+  float raw_ok;
 };
 
 // The chunk's scores as modified scores times log2(e): keys from kb, `dist` = q + diag - kb.
@@ -137,39 +151,39 @@ __device__ __forceinline__ void modify_chunk(const ScoreMods& m, const CapCoef& 
   const float base = -slope2 * dist;
   const uint64_t c2 = f2_pack(c, c), log2_cap = f2_pack(m.cap_log2, m.cap_log2);
 #pragma unroll
-  for (int blk = 0; blk < 16 / SIDE; ++blk) {
-    uint64_t x[SIDE], b[SIDE];
-    uint32_t* const sb = s + blk * SIDE * 2;
+  for (int blk = 0; blk < 16 / FWD_SIDE; ++blk) {
+    uint64_t x[FWD_SIDE], b[FWD_SIDE];
+    uint32_t* const sb = s + blk * FWD_SIDE * 2;
 #pragma unroll
-    for (int i = 0; i < SIDE; ++i) x[i] = f2_pack(sb[2 * i], sb[2 * i + 1]);
+    for (int i = 0; i < FWD_SIDE; ++i) x[i] = f2_pack(sb[2 * i], sb[2 * i + 1]);
     if (biased) {
 #pragma unroll
-      for (int i = 0; i < SIDE; ++i) {
-        const float i0 = (float)(2 * (blk * SIDE + i)), i1 = i0 + 1.f;
+      for (int i = 0; i < FWD_SIDE; ++i) {
+        const float i0 = (float)(2 * (blk * FWD_SIDE + i)), i1 = i0 + 1.f;
         b[i] = ahead ? f2_pack(fmaf(slope2, i0, base), fmaf(slope2, i1, base))
                      : f2_pack(-slope2 * fabsf(dist - i0), -slope2 * fabsf(dist - i1));
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < SIDE; ++i) b[i] = 0ull;
+      for (int i = 0; i < FWD_SIDE; ++i) b[i] = 0ull;
     }
     if constexpr (MOD == MOD_CAP) {
       if (small) {
-        uint64_t r[SIDE];
+        uint64_t r[FWD_SIDE];
         tanh2_poly(x, coef, r);
 #pragma unroll
-        for (int i = 0; i < SIDE; ++i) x[i] = f2_fma(x[i], r[i], b[i]);
+        for (int i = 0; i < FWD_SIDE; ++i) x[i] = f2_fma(x[i], r[i], b[i]);
       } else {
         tanh2_any(x, m.cap_in);
 #pragma unroll
-        for (int i = 0; i < SIDE; ++i) x[i] = f2_fma(x[i], log2_cap, b[i]);
+        for (int i = 0; i < FWD_SIDE; ++i) x[i] = f2_fma(x[i], log2_cap, b[i]);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < SIDE; ++i) x[i] = f2_fma(x[i], c2, b[i]);
+      for (int i = 0; i < FWD_SIDE; ++i) x[i] = f2_fma(x[i], c2, b[i]);
     }
 #pragma unroll
-    for (int i = 0; i < SIDE; ++i) f2_unpack(x[i], sb[2 * i], sb[2 * i + 1]);
+    for (int i = 0; i < FWD_SIDE; ++i) f2_unpack(x[i], sb[2 * i], sb[2 * i + 1]);
   }
 }
 
@@ -183,55 +197,77 @@ __device__ __forceinline__ float cap_score(float s, const CapCoef& coef) {
   return y;
 }
 
-// A tile's scores prepared for the exponentials: modified where `modified` (capped or
-// biased; else they stay, and the exponent takes them times cs), -inf where masked.
-// Keys [lo, hi] of the thread's 64 are visible to its row; `dist` = q + diag - its first
-// key. Returns the row's maximum in log2 units (-inf when it sees none).
-template <int MOD>
-__device__ __forceinline__ float mod_scores(const ScoreMods& m, const CapCoef& coef, float c, float cs, bool modified,
-                                            float slope2, float dist, int lo, int hi, uint32_t (&sr)[2][32],
-                                            ModChunks& ch) {
-  bool full[2];
+// Which chunks of the 64 keys from kb the warp sees: from the item's bounds, no votes.
+__device__ __forceinline__ void mod_chunks(const ModRow& r, int kb, ModChunks& ch) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const int l = lo - 32 * k, h = hi - 32 * k;
-    full[k] = __all_sync(0xffffffffu, l <= 0 && h >= 31);
-    ch.any[k] = full[k] || __any_sync(0xffffffffu, l <= h && l <= 31 && h >= 0);
+    const int c0 = kb + 32 * k;
+    ch.full[k] = c0 >= r.lo_max && c0 + 31 <= r.hi_min;
+    ch.any[k] = c0 + 31 >= r.lo_min && c0 <= r.hi_max;
     ch.deferred[k] = false;
   }
+  ch.big = -INFINITY;
+}
+
+// The largest score of a chunk and, in `least`, the smallest or 0.
+__device__ __forceinline__ float chunk_extremes(const uint32_t (&s)[32], float& least) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, mn[4] = {least, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float s0 = __uint_as_float(s[i]), s1 = __uint_as_float(s[i + 1]);
+    mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], s0, s1);
+    mn[(i >> 1) & 3] = min3(mn[(i >> 1) & 3], s0, s1);
+  }
+  least = min3(mn[0], mn[1], fminf(mn[2], mn[3]));
+  return max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+}
+
+// The common tile under a cap alone: both chunks visible to the whole warp, every score
+// within the polynomial and none that would raise its row's reference. One pass and one
+// vote; the scores stay as they are for exp_chunk<CAPPED>.
+__device__ __forceinline__ bool mod_tile_as_before(const ScoreMods& m, const ModRow& r, const uint32_t (&sr)[2][32],
+                                                   ModChunks& ch) {
+  if (!ch.full[0] || !ch.full[1] || m.slopes != nullptr) return false;
+  float least = 0.f;
+  const float b0 = chunk_extremes(sr[0], least);
+  const float b1 = chunk_extremes(sr[1], least);
+  const float big = fmaxf(b0, b1);
+  if (!__all_sync(0xffffffffu, fmaxf(big, -least) <= m.cap_small && big <= r.raw_ok)) return false;
+  ch.deferred[0] = ch.deferred[1] = true;
+  return true;
+}
+
+// A tile's scores prepared for the exponentials: modified where `modified` (capped or
+// biased; else they stay, and the exponent takes them times cs), -inf where masked. The
+// thread's 64 keys start at kb. Returns the row's maximum in log2 units (-inf when it
+// sees none).
+template <int MOD>
+__device__ __forceinline__ float mod_scores(const ScoreMods& m, const CapCoef& coef, float c, float cs, bool modified,
+                                            const ModRow& r, int kb, uint32_t (&sr)[2][32], ModChunks& ch) {
   float big[2] = {-INFINITY, -INFINITY};  // the chunks' largest scores as they are
   bool small = false;
   if constexpr (MOD == MOD_CAP) {
     float least = 0.f;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (!ch.any[k]) continue;
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, mn[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        const float s0 = __uint_as_float(sr[k][i]), s1 = __uint_as_float(sr[k][i + 1]);
-        mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], s0, s1);
-        mn[(i >> 1) & 3] = min3(mn[(i >> 1) & 3], s0, s1);
-      }
-      big[k] = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-      least = min3(least, fminf(mn[0], mn[1]), fminf(mn[2], mn[3]));
-    }
+    for (int k = 0; k < 2; ++k)
+      if (ch.any[k]) big[k] = chunk_extremes(sr[k], least);
     small = __all_sync(0xffffffffu, max3(big[0], big[1], -least) <= m.cap_small);
   }
   float mt = -INFINITY;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (!ch.any[k]) continue;
-    if (MOD == MOD_CAP && small && full[k] && m.slopes == nullptr) {
+    if (MOD == MOD_CAP && small && ch.full[k] && m.slopes == nullptr) {
       ch.deferred[k] = true;
-      mt = fmaxf(mt, cap_score(big[k], coef));
+      ch.big = fmaxf(ch.big, big[k]);
       continue;
     }
-    if (modified) modify_chunk<MOD>(m, coef, c, slope2, dist - (float)(32 * k), small, sr[k]);
-    if (!full[k]) {
+    const int c0 = kb + 32 * k;
+    if (modified) modify_chunk<MOD>(m, coef, c, r.slope2, (float)(r.place - c0), small, sr[k]);
+    if (!ch.full[k]) {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        if (i < lo - 32 * k || i > hi - 32 * k) sr[k][i] = 0xFF800000u;  // -inf
+        if (i < r.lo - c0 || i > r.hi - c0) sr[k][i] = 0xFF800000u;  // -inf
     }
     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -239,6 +275,7 @@ __device__ __forceinline__ float mod_scores(const ScoreMods& m, const CapCoef& c
       mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], __uint_as_float(sr[k][i]), __uint_as_float(sr[k][i + 1]));
     mt = fmaxf(mt, max3(mx[0], mx[1], fmaxf(mx[2], mx[3])) * cs);  // cs > 0
   }
+  if (MOD == MOD_CAP && (ch.deferred[0] || ch.deferred[1])) mt = fmaxf(mt, cap_score(ch.big, coef));
   return mt;
 }
 
@@ -251,31 +288,31 @@ __device__ __forceinline__ void exp_chunk(const uint32_t (&s)[32], const CapCoef
 #pragma unroll
   for (int a = 0; a < 4; ++a) sum[a] = f2_pack(rs[2 * a], rs[2 * a + 1]);
 #pragma unroll
-  for (int blk = 0; blk < 16 / SIDE; ++blk) {
-    uint64_t x[SIDE];
+  for (int blk = 0; blk < 16 / FWD_SIDE; ++blk) {
+    uint64_t x[FWD_SIDE];
 #pragma unroll
-    for (int i = 0; i < SIDE; ++i) x[i] = f2_pack(s[2 * (blk * SIDE + i)], s[2 * (blk * SIDE + i) + 1]);
+    for (int i = 0; i < FWD_SIDE; ++i) x[i] = f2_pack(s[2 * (blk * FWD_SIDE + i)], s[2 * (blk * FWD_SIDE + i) + 1]);
     if constexpr (CAPPED) {
-      uint64_t r[SIDE];
+      uint64_t r[FWD_SIDE];
       tanh2_poly(x, coef, r);
 #pragma unroll
-      for (int i = 0; i < SIDE; ++i) x[i] = f2_fma(x[i], r[i], m2);
+      for (int i = 0; i < FWD_SIDE; ++i) x[i] = f2_fma(x[i], r[i], m2);
     } else {
 #pragma unroll
-      for (int i = 0; i < SIDE; ++i) x[i] = f2_fma(x[i], c2, m2);
+      for (int i = 0; i < FWD_SIDE; ++i) x[i] = f2_fma(x[i], c2, m2);
     }
 #pragma unroll
-    for (int i = 0; i < SIDE; ++i) {
+    for (int i = 0; i < FWD_SIDE; ++i) {
       float x0, x1;
       f2_unpack(x[i], x0, x1);
       x[i] = f2_pack(ex2_approx(x0), ex2_approx(x1));
     }
 #pragma unroll
-    for (int i = 0; i < SIDE; ++i) {
+    for (int i = 0; i < FWD_SIDE; ++i) {
       float p0, p1;
       f2_unpack(x[i], p0, p1);
       sum[i & 3] = f2_add(sum[i & 3], x[i]);
-      w[blk * SIDE + i] = pack_io2<F16>(p0, p1);
+      w[blk * FWD_SIDE + i] = pack_io2<F16>(p0, p1);
     }
   }
 #pragma unroll
@@ -370,16 +407,72 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int it) {
   return fwd_item<MOD>(p, it, fwd_item_loads<MOD>(p, it));
 }
 
-// What the modified scores add to row q's state of item w: its key range (a mask
-// plan) joins the visible bounds [lo, hi], and the head's distance slope in log2 units.
-__device__ __forceinline__ void mod_row(const FwdParams& p, const FwdItem& w, int q, bool live, long long& lo,
-                                        long long& hi, float& slope2) {
-  if (p.mods.ranges != nullptr && live) {
-    const int2 r = p.mods.ranges[(long long)(w.bh / p.Hq) * ceil_div(p.Sq, BQ) * BQ + q];
-    lo = max(lo, (long long)r.x);
-    hi = min(hi, (long long)r.y - 1);
-  }
-  if (p.mods.slopes != nullptr) slope2 = p.mods.slopes[w.h] * 1.4426950408889634f;
+// An item as the producer publishes it under modified scores, with the bounds that it has
+// read already, so that no other role waits for memory to know its item.
+struct FwdItemMsg {
+  int it, kt_lo, n, Lq, Lk;
+};
+constexpr int MSG_INTS = 5;
+__device__ __forceinline__ void put_msg(volatile int* at, const FwdItemMsg& m) {
+  at[0] = m.it;
+  at[1] = m.kt_lo;
+  at[2] = m.n;
+  at[3] = m.Lq;
+  at[4] = m.Lk;
+}
+__device__ __forceinline__ FwdItemMsg get_msg(const volatile int* at) {
+  return FwdItemMsg{at[0], at[1], at[2], at[3], at[4]};
+}
+__device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, const FwdItemMsg& m) {
+  FwdItem w;
+  const int BH = p.B * p.Hq;
+  w.qt = p.n_qt - 1 - m.it / BH;
+  w.bh = m.it % BH;
+  w.h = w.bh % p.Hq;
+  w.kvh = w.bh / p.Hq * p.Hkv + w.h / p.G;
+  w.q0 = w.qt * fwd_shared::BM;
+  w.Lq = m.Lq;
+  w.Lk = m.Lk;
+  w.diag = p.bottom_right ? (long long)m.Lk - m.Lq : 0;
+  w.kt_lo = m.kt_lo;
+  w.n = m.n;
+  return w;
+}
+
+// What row q of an item reads from memory under modified scores.
+struct ModRowLoads {
+  int2 range;
+  float slope, sink;
+};
+__device__ __forceinline__ ModRowLoads mod_row_loads(const FwdParams& p, const FwdItem& w, int q) {
+  ModRowLoads l;
+  l.range = make_int2(0, p.Skv);
+  if (p.mods.ranges != nullptr && q < p.Sq)
+    l.range = p.mods.ranges[(long long)(w.bh / p.Hq) * ceil_div(p.Sq, BQ) * BQ + q];
+  l.slope = p.mods.slopes != nullptr ? p.mods.slopes[w.h] : 0.f;
+  l.sink = p.sink != nullptr ? p.sink[w.h] : 0.f;
+  return l;
+}
+
+// Row q's state under modified scores in item w: its visible keys by the causal, window,
+// length and plan bounds.
+__device__ __forceinline__ ModRow mod_row(const FwdParams& p, const FwdItem& w, int q, bool live, const ModRowLoads& l) {
+  ModRow r;
+  r.place = (int)(q + w.diag);
+  long long lo = 0, hi = w.Lk - 1;
+  if (p.causal) hi = min(hi, (long long)r.place + max(p.window_right, 0));
+  if (p.window_left >= 0) lo = max(lo, (long long)r.place - p.window_left);
+  lo = max(lo, (long long)l.range.x);
+  hi = min(hi, (long long)l.range.y - 1);
+  r.lo = (int)min(lo, (long long)w.Lk);
+  r.hi = live ? (int)max(hi, -1ll) : -1;
+  r.lo_max = __reduce_max_sync(0xffffffffu, r.lo);
+  r.hi_min = __reduce_min_sync(0xffffffffu, r.hi);
+  r.lo_min = __reduce_min_sync(0xffffffffu, r.lo);
+  r.hi_max = __reduce_max_sync(0xffffffffu, r.hi);
+  r.slope2 = l.slope * 1.4426950408889634f;
+  r.raw_ok = -INFINITY;
+  return r;
 }
 
 // One 32-byte global store of two 16-byte halves (the address 32-byte aligned):

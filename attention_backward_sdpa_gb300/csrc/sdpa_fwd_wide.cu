@@ -354,10 +354,10 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
         m = p.sink[w.h] * 1.4426950408889634f;
         l = half == 0 ? 1.f : 0.f;
       }
-      long long k_vis_hi = p.causal ? (long long)q + w.diag + Rp : (1ll << 40);
-      long long k_vis_lo = has_window ? (long long)q + w.diag - p.window_left : -(1ll << 40);
-      float slope2 = 0.f;
-      if constexpr (MOD) mod_row(p, w, q, live, k_vis_lo, k_vis_hi, slope2);
+      const long long k_vis_hi = p.causal ? (long long)q + w.diag + Rp : (1ll << 40);
+      const long long k_vis_lo = has_window ? (long long)q + w.diag - p.window_left : -(1ll << 40);
+      ModRow mr;
+      if constexpr (MOD) mr = mod_row(p, w, q, live, mod_row_loads(p, w, q));
       const long long bias_row =
           BIAS ? (long long)(w.bh / p.Hq) * p.bias_bstride + ((long long)w.h * p.Sq + q) * p.Skv : 0;
       for (int j = 0; j < w.n; ++j, ++g) {
@@ -403,8 +403,8 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
 #pragma unroll
           for (int a = 0; a < 8; ++a) mp[a] = -INFINITY;
           if constexpr (MOD) {
-            mp[0] = mod_scores<MOD>(p.mods, coef, c, cs, modified, slope2, (float)(q + w.diag - (k0 + i0)), v_lo - i0,
-                                    v_hi - i0, sr, ch);
+            mod_chunks(mr, k0 + i0, ch);
+            mp[0] = mod_scores<MOD>(p.mods, coef, c, cs, modified, mr, k0 + i0, sr, ch);
           } else if (full) {
 #pragma unroll
             for (int i = 0; i < 64; ++i) mp[i & 7] = fmaxf(mp[i & 7], __uint_as_float(sr[i >> 5][i & 31]));
