@@ -79,6 +79,8 @@ def load(build_if_missing: bool = False):
     lib.sdpa_fwd_scored.restype = i
     lib.sdpa_bwd_scored.argtypes = [i] + list(lib.sdpa_bwd.argtypes[:-1]) + [vp, vp, ctypes.c_float, vp, vp, vp]
     lib.sdpa_bwd_scored.restype = i
+    lib.sdpa_bwd_scored_workspace_size.argtypes = [i] * 13
+    lib.sdpa_bwd_scored_workspace_size.restype = sz
     lib.sdpa_mask_plan_size.argtypes = [i, i, i]
     lib.sdpa_mask_plan_size.restype = sz
     lib.sdpa_mask_plan_rows.argtypes = [vp, vp, i, i, i, vp, sz, vp]
@@ -146,13 +148,15 @@ def _optional(t, dtype, dev: int, numel: int) -> bool:
 
 
 def workspace_size(B, Hq, Hkv, Sq, Skv, Dqk, Dv, deterministic=False, *, causal=False,
-                   bottom_right=False, window_left=-1, window_right=-1, padded=False) -> int:
+                   bottom_right=False, window_left=-1, window_right=-1, padded=False,
+                   scored=False) -> int:
     """Workspace bytes of sdpa_bwd for this shape and mask (``padded``: length
-    arrays will be passed). The defaults (no mask) give the largest size for the
-    shape, which serves every mask."""
-    return int(load().sdpa_bwd_workspace_size(B, Hq, Hkv, Sq, Skv, Dqk, Dv, int(causal),
-                                              int(bottom_right), int(window_left),
-                                              int(window_right), int(deterministic), int(padded)))
+    arrays will be passed; ``scored``: softcap, alibi_slopes or a mask_plan will be).
+    The defaults (no mask) give the largest size for the shape, which serves every mask."""
+    lib = load()
+    size = lib.sdpa_bwd_scored_workspace_size if scored else lib.sdpa_bwd_workspace_size
+    return int(size(B, Hq, Hkv, Sq, Skv, Dqk, Dv, int(causal), int(bottom_right), int(window_left),
+                    int(window_right), int(deterministic), int(padded)))
 
 
 def _check_bf16(name, t, shape, dtype=torch.bfloat16):

@@ -61,6 +61,7 @@ struct ChainParams {
   int* ticket;          // work-unit ticket
   __nv_bfloat16* dk_ws; // n_part > 1: [B][Hkv][n_part][Skv][Dqk] partials, else null
   __nv_bfloat16* dv_ws; // n_part > 1: [B][Hkv][n_part][Skv][Dv]
+  int part_f32;         // the partials are fp32 (modified scores) instead of the io type
   int n_counters;       // B*Hq*n_qt + 1 (counters plus ticket)
 
   // Sink tokens (optional): the forward's LSE already folds the sink logits in,
@@ -102,6 +103,7 @@ struct ChainParams {
 
   ScoreMods mods;       // capped / distance-biased scores and row ranges (MOD kernels)
 
+  int sms;              // SMs of the device
   int* status;          // per-device status word
   // Ordered relay (deterministic mode, D_qk up to 128 but not 128): how long a
   // key tile waits for its turn before it gives up and reports a timeout, and a
@@ -219,7 +221,7 @@ __host__ __device__ inline size_t io_q_bytes(const ChainParams& p, int D) {  // 
   return (size_t)p.B * p.Hq * p.Sq * D * 2;
 }
 __host__ __device__ inline size_t kv_out_bytes(const ChainParams& p, int D, bool partials) {  // dK / dV (or partial sets)
-  return (size_t)p.B * (partials ? p.Hq : p.Hkv) * p.Skv * D * 2;
+  return (size_t)p.B * (partials ? p.Hq : p.Hkv) * p.Skv * D * (partials && p.part_f32 ? 4 : 2);
 }
 
 // Band of query tiles [lo, hi] of key tile kt in the dS workspace (see ChainParams).
@@ -451,15 +453,31 @@ __device__ inline void zero_group_share_of_empty_key_tiles(const ChainParams& p,
 __device__ inline void zero_key_tile_rows(const ChainParams& p, long long head, int k0) {
   const int rows = min(BN, p.Skv - k0);
   const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-  uint4* dk = reinterpret_cast<uint4*>((p.dk_ws ? p.dk_ws : p.dk) + (head * p.Skv + k0) * p.Dqk);
-  uint4* dv = reinterpret_cast<uint4*>((p.dv_ws ? p.dv_ws : p.dv) + (head * p.Skv + k0) * p.Dv);
-  if (!in_bounds(p.status, dk, (size_t)rows * p.Dqk * 2, p.dk_ws ? p.dk_ws : p.dk,
-                 kv_out_bytes(p, p.Dqk, p.dk_ws != nullptr)) ||
-      !in_bounds(p.status, dv, (size_t)rows * p.Dv * 2, p.dv_ws ? p.dv_ws : p.dv,
-                 kv_out_bytes(p, p.Dv, p.dv_ws != nullptr)))
+  const int esz = p.dk_ws && p.part_f32 ? 4 : 2;
+  char* const dk_base = reinterpret_cast<char*>(p.dk_ws ? p.dk_ws : p.dk);
+  char* const dv_base = reinterpret_cast<char*>(p.dv_ws ? p.dv_ws : p.dv);
+  uint4* dk = reinterpret_cast<uint4*>(dk_base + (head * p.Skv + k0) * p.Dqk * esz);
+  uint4* dv = reinterpret_cast<uint4*>(dv_base + (head * p.Skv + k0) * p.Dv * esz);
+  if (!in_bounds(p.status, dk, (size_t)rows * p.Dqk * esz, dk_base, kv_out_bytes(p, p.Dqk, p.dk_ws != nullptr)) ||
+      !in_bounds(p.status, dv, (size_t)rows * p.Dv * esz, dv_base, kv_out_bytes(p, p.Dv, p.dv_ws != nullptr)))
     return;
-  for (int i = threadIdx.x; i < rows * (p.Dqk / 8); i += blockDim.x) dk[i] = z;
-  for (int i = threadIdx.x; i < rows * (p.Dv / 8); i += blockDim.x) dv[i] = z;
+  for (int i = threadIdx.x; i < rows * (p.Dqk * esz / 16); i += blockDim.x) dk[i] = z;
+  for (int i = threadIdx.x; i < rows * (p.Dv * esz / 16); i += blockDim.x) dv[i] = z;
+}
+
+// 32 columns [c0, c0 + 32) of a key's row of an fp32 partial set (D columns; those past
+// them are dropped), from a thread's accumulator registers times `mult`.
+__device__ __forceinline__ void store_partial_f32(const ChainParams& p, const __nv_bfloat16* set, long long head,
+                                                  int key, int D, int c0, const uint32_t (&r)[32], float mult) {
+  if (key >= p.Skv || c0 >= D) return;
+  float* row = reinterpret_cast<float*>(const_cast<__nv_bfloat16*>(set)) + (head * p.Skv + key) * D + c0;
+  if (!in_bounds(p.status, row, (size_t)min(32, D - c0) * 4, set, kv_out_bytes(p, D, true))) return;
+#pragma unroll
+  for (int i = 0; i < 32; i += 4)
+    if (c0 + i < D)
+      *reinterpret_cast<float4*>(row + i) =
+          make_float4(__uint_as_float(r[i]) * mult, __uint_as_float(r[i + 1]) * mult, __uint_as_float(r[i + 2]) * mult,
+                      __uint_as_float(r[i + 3]) * mult);
 }
 
 }  // namespace sdpa

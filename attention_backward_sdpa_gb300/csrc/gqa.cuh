@@ -72,6 +72,44 @@ __device__ __forceinline__ void gqa_reduce_rows(const ChainParams& p, const __nv
   }
 }
 
+// The same over fp32 partial sets.
+template <bool F16>
+__device__ __forceinline__ void gqa_reduce_rows_f32(const ChainParams& p, const __nv_bfloat16* ws, __nv_bfloat16* out,
+                                                    int D, unsigned row_begin, unsigned row_end, unsigned thread,
+                                                    unsigned nthreads) {
+  const unsigned CPR = (unsigned)D / 8;
+  const unsigned items = (row_end > row_begin ? row_end - row_begin : 0) * CPR;
+  const long long set_stride = (long long)p.Skv * D;
+  const float* base = reinterpret_cast<const float*>(ws);
+  for (unsigned it = thread; it < items; it += nthreads) {
+    const unsigned row = row_begin + it / CPR, c8 = it % CPR;
+    const unsigned bhk = row / (unsigned)p.Skv, k = row - bhk * (unsigned)p.Skv;
+    const float* src = base + (long long)bhk * p.n_part * set_stride + (long long)k * D + c8 * 8;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < p.n_part; j0 += 4) {  // four sets' loads together, added in ascending order
+      float4 v[4][2];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j0 + j < p.n_part) {
+          v[j][0] = *reinterpret_cast<const float4*>(src + (j0 + j) * set_stride);
+          v[j][1] = *reinterpret_cast<const float4*>(src + (j0 + j) * set_stride + 4);
+        }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j0 + j < p.n_part) {
+          acc[0] += v[j][0].x; acc[1] += v[j][0].y; acc[2] += v[j][0].z; acc[3] += v[j][0].w;
+          acc[4] += v[j][1].x; acc[5] += v[j][1].y; acc[6] += v[j][1].z; acc[7] += v[j][1].w;
+        }
+    }
+    uint4 o;
+    o.x = pack_io2<F16>(acc[0], acc[1]);
+    o.y = pack_io2<F16>(acc[2], acc[3]);
+    o.z = pack_io2<F16>(acc[4], acc[5]);
+    o.w = pack_io2<F16>(acc[6], acc[7]);
+    *reinterpret_cast<uint4*>(out + (long long)row * D + c8 * 8) = o;
+  }
+}
+
 // Piece `piece` of `n_pieces` of the slice of output rows assigned to CTA
 // `cta` of `n_ctas` (both outputs). Pieces let a kernel spread the work.
 template <bool F16 = false>
@@ -86,6 +124,11 @@ __device__ __forceinline__ void gqa_reduce_slice(const ChainParams& p, unsigned 
   const unsigned pp = (hi - lo + n_pieces - 1) / n_pieces;
   const unsigned plo = lo + piece * pp, phi = (plo + pp < hi) ? plo + pp : hi;
   if (plo >= phi) return;
+  if (p.part_f32) {
+    gqa_reduce_rows_f32<F16>(p, p.dk_ws, p.dk, p.Dqk, plo, phi, thread, nthreads);
+    gqa_reduce_rows_f32<F16>(p, p.dv_ws, p.dv, p.Dv, plo, phi, thread, nthreads);
+    return;
+  }
   gqa_reduce_rows<F16>(p, p.dk_ws, p.dk, p.Dqk, plo, phi, thread, nthreads);
   gqa_reduce_rows<F16>(p, p.dv_ws, p.dv, p.Dv, plo, phi, thread, nthreads);
 }

@@ -94,7 +94,8 @@ struct Carve {
   size_t total;
 };
 
-Carve carve(const Shape& sh, Route route, bool qat = false) {
+// `scored`: modified scores, whose per-head dK/dV partials are fp32.
+Carve carve(const Shape& sh, Route route, bool qat = false, bool scored = false) {
   const int B = sh.B, Hq = sh.Hq, Hkv = sh.Hkv, Sq = sh.Sq, Skv = sh.Skv, Dqk = sh.Dqk, Dv = sh.Dv;
   const size_t n_qt = (size_t)ceil_div(Sq, BQ);
   const size_t bh = (size_t)B * Hq;
@@ -120,9 +121,9 @@ Carve carve(const Shape& sh, Route route, bool qat = false) {
   off = align256(off + bh * n_qt * sizeof(float));
   if (Hkv < Hq) {
     c.dk_ws = off;
-    off = align256(off + bh * (size_t)Skv * Dqk * 2);
+    off = align256(off + bh * (size_t)Skv * Dqk * (scored ? 4 : 2));
     c.dv_ws = off;
-    off = align256(off + bh * (size_t)Skv * Dv * 2);
+    off = align256(off + bh * (size_t)Skv * Dv * (scored ? 4 : 2));
   } else {
     c.dk_ws = c.dv_ws = SIZE_MAX;
   }
@@ -271,6 +272,16 @@ size_t sdpa_bwd_workspace_size(int B, int H_q, int H_kv, int S_q, int S_kv, int 
   const Shape sh{B, H_q, H_kv, S_q, S_kv, D_qk, D_v, causal, bottom_right, window_left, window_right,
                  padded};
   return carve(sh, choose_route(deterministic, D_qk)).total;
+}
+
+size_t sdpa_bwd_scored_workspace_size(int B, int H_q, int H_kv, int S_q, int S_kv, int D_qk, int D_v,
+                                      int causal, int bottom_right, int window_left, int window_right,
+                                      int deterministic, int padded) {
+  if (basic_checks(B, H_q, H_kv, S_q, S_kv, D_qk, D_v) != SDPA_OK) return 0;
+  if (S_q == 0 || S_kv == 0) return 0;
+  const Shape sh{B, H_q, H_kv, S_q, S_kv, D_qk, D_v, causal, bottom_right, window_left, window_right,
+                 padded};
+  return carve(sh, choose_route(deterministic, D_qk), false, true).total;
 }
 
 size_t sdpa_bwd_nvfp4_qat_workspace_size(int B, int H_q, int H_kv, int S_q, int S_kv, int D_qk,
@@ -454,7 +465,7 @@ int run_chain(const void* q, const void* k, const void* v, const void* o, const 
   const bool ds_route = route != Route::kReduce;
   const Shape sh{B, H_q, H_kv, S_q, S_kv, D_qk, D_v, causal, bottom_right, window_left, window_right,
                  (seq_q_lens || seq_kv_lens) ? 1 : 0};
-  const Carve cv = carve(sh, route, qat);
+  const Carve cv = carve(sh, route, qat, mods.on != MOD_NONE);
   bool own_ws = false;
   if (workspace == nullptr) {
     if (cudaMallocAsync(&workspace, cv.total, stream) != cudaSuccess) return SDPA_ERR_CUDA;
@@ -519,6 +530,8 @@ int run_chain(const void* q, const void* k, const void* v, const void* o, const 
   // one set per query head) when a KV group spans several work units.
   p.dk_ws = p.n_part > 1 ? reinterpret_cast<__nv_bfloat16*>(ws + cv.dk_ws) : nullptr;
   p.dv_ws = p.n_part > 1 ? reinterpret_cast<__nv_bfloat16*>(ws + cv.dv_ws) : nullptr;
+  p.part_f32 = (mods.on != MOD_NONE && p.n_part > 1) ? 1 : 0;
+  p.sms = sms;
   p.status = status;
   p.mods = mods;
   {
@@ -565,10 +578,11 @@ int run_chain(const void* q, const void* k, const void* v, const void* o, const 
       !make_bhsd_map(&maps.k, kg, D_qk, S_kv, BHkv, BN, f16) ||
       !make_bhsd_map(&maps.v, vg, D_v, S_kv, BHkv, BN, f16) ||
       !make_bhsd_map(&maps.d_o, d_o, D_v, S_q, BHq, BQ, f16) ||
-      !make_bhsd_map(&maps.dk_out, p.dk_ws ? static_cast<void*>(p.dk_ws) : dk, D_qk, S_kv,
-                     p.dk_ws ? BHq : BHkv, BN, f16) ||
-      !make_bhsd_map(&maps.dv_out, p.dv_ws ? static_cast<void*>(p.dv_ws) : dv, D_v, S_kv,
-                     p.dv_ws ? BHq : BHkv, BN, f16)) {
+      // (fp32 partial sets are written without these maps)
+      !make_bhsd_map(&maps.dk_out, p.dk_ws && !p.part_f32 ? static_cast<void*>(p.dk_ws) : dk, D_qk, S_kv,
+                     p.dk_ws && !p.part_f32 ? BHq : BHkv, BN, f16) ||
+      !make_bhsd_map(&maps.dv_out, p.dv_ws && !p.part_f32 ? static_cast<void*>(p.dv_ws) : dv, D_v, S_kv,
+                     p.dv_ws && !p.part_f32 ? BHq : BHkv, BN, f16)) {
     if (dbias_tmp) cudaFreeAsync(dbias_tmp, stream);
     if (own_ws) cudaFreeAsync(workspace, stream);
     return SDPA_ERR_CUDA;

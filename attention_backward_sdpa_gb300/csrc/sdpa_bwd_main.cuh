@@ -918,6 +918,10 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) r[i] = 0u;
       }
+      if (MOD && p.part_f32) {  // a partial set of the group: fp32, straight from registers
+        store_partial_f32(p, slot ? p.dk_ws : p.dv_ws, out_head, k, slot ? p.Dqk : p.Dv, c32 * 32, r, mult);
+        continue;
+      }
       uint8_t* dst_row = stg + (c32 >> 1) * L::BLK_KV + row * 128;
 #pragma unroll
       for (int v8 = 0; v8 < 4; ++v8) {
@@ -932,7 +936,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
     }
     fence_proxy_async_smem();
     named_bar_sync(1 + slot, 128);
-    if (row == 0) {
+    if (row == 0 && !(MOD && p.part_f32)) {
       const long long head = out_head;
       const CUtensorMap* map = slot ? &maps.dk_out : &maps.dv_out;
       // Final dK/dV rows are not read again (partial sets are, by the group
@@ -965,10 +969,11 @@ template <bool BIAS, bool F16 = false, int MOD = MOD_NONE>
 static cudaError_t launch_main_variant(const MainMaps& maps, const ChainParams& p, cudaStream_t s) {
   const dim3 grid((unsigned)(p.n_kt * p.B * p.Hkv * p.n_part));
   const dim3 block(MAIN_THREADS);
-  // Launched while the preprocess drains, except with modified scores: there the early
-  // start made the chain slower (bwd_capped_gqa 524 us against 483, bwd_packed_docs 247
-  // against 215; without MOD the two are equal).
-  constexpr bool pdl = MOD == MOD_NONE;
+  // Launched while the preprocess drains; with modified scores only where the units fit the
+  // SMs at once. Over several waves the early start made their chain slower
+  // (bwd_capped_gqa 524 us against 483, bwd_packed_docs 247 against 215; without MOD the
+  // two are equal), in one it hides the launch (bwd_short 11.5 us against 15.6 in a graph).
+  const bool pdl = MOD == MOD_NONE || (int)grid.x <= p.sms;
   // D_qk = D_v up to 64 runs on the 64-column kernels, up to 128 on the 128-column
   // ones: TMA zero-fills the columns past D on loads and drops them on stores.
   if (p.Dqk <= 64)

@@ -599,6 +599,10 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) r[i] = 0u;
       }
+      if (MOD && p.part_f32) {  // a partial set of the group: fp32, straight from registers
+        store_partial_f32(p, slot ? p.dk_ws : p.dv_ws, bh, k, slot ? DQK : DV, half * D + c32 * 32, r, mult);
+        continue;
+      }
       uint8_t* dst_row = stg + (c32 >> 1) * L::BLK_KV + row * 128;
 #pragma unroll
       for (int v8 = 0; v8 < 4; ++v8) {
@@ -613,7 +617,7 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
     }
     fence_proxy_async_smem();
     named_bar_sync(1 + slot, 128);
-    if (row == 0) {
+    if (row == 0 && !(MOD && p.part_f32)) {
       const long long head = p.dk_ws ? (long long)bh : (long long)b * p.Hkv + hk;
       const CUtensorMap* map = slot ? &maps.dk_out : &maps.dv_out;
       for (int blk = 0; blk < D / 64; ++blk)

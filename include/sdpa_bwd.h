@@ -357,11 +357,22 @@ int sdpa_fwd_scored(int io_dtype, const void* q, const void* k, const void* v, v
                     float softcap, const float* alibi_slopes, const void* mask_plan, void* stream);
 
 /*
+ * Bytes of workspace sdpa_bwd_scored() needs: the regions of sdpa_bwd_workspace_size(),
+ * with the per-query-head dK/dV partials of the GQA reduction in fp32 (each dK and dV
+ * element is then rounded to the io type once). On the routes that store dS the band of
+ * tiles follows the call's causal and window arguments, not the mask plan: with a plan of
+ * causal documents, causal = 1 in the call too halves it.
+ */
+size_t sdpa_bwd_scored_workspace_size(int B, int H_q, int H_kv, int S_q, int S_kv, int D_qk, int D_v,
+                                      int causal, int bottom_right, int window_left, int window_right,
+                                      int deterministic, int padded);
+
+/*
  * SDPA backward with modified scores, with the O and LSE of sdpa_fwd_scored() for the
  * same arguments. Arguments of sdpa_bwd_typed() without a bias (sink and dsink
  * optional), then softcap, alibi_slopes and mask_plan as sdpa_fwd_scored(). The
- * slopes are constants: they have no gradient here. Workspace as
- * sdpa_bwd_workspace_size() for the same mask arguments. Served for every head-dim
+ * slopes are constants: they have no gradient here. Workspace:
+ * sdpa_bwd_scored_workspace_size() for the same mask arguments. Served for every head-dim
  * pair of sdpa_bwd(); a mask plan in deterministic mode only where dQ comes from
  * stored dS (D_qk 128, 192, 256), else SDPA_ERR_UNSUPPORTED.
  */

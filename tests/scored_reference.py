@@ -7,10 +7,10 @@ The bounds are elementwise and count roundings: u is half a step of the io type
 
   |O_gpu - O|   <= u (P|V| [P is rounded for the PV product] + |O| [O is rounded])
                    + 2 e (P|V|)           e: error of a score, in the numerator and the sum
-  |dV_gpu - dV| <= u (2 P^T|dO| [P rounded; per-head partials rounded under GQA] + |dV|) + e P^T|dO|
+  |dV_gpu - dV| <= u (P^T|dO| [P rounded] + |dV|) + e P^T|dO|
   |dS_gpu - dS| <= E = u |dS| [rounded for dQ, dK] + e |dS| + P (e_d + e_f |dP - delta|)
   |dQ_gpu - dQ| <= scale E |K| + u |dQ|
-  |dK_gpu - dK| <= scale (E^T |Q| + u |dS|^T |Q| [partials]) + u |dK|
+  |dK_gpu - dK| <= scale E^T |Q| + u |dK|
 
 e   = g (D + 16) max sum|q k| scale + g (|x| + |LSE|) + g |slope| distance (products and sums of D
       terms, the exponent's argument, the distance bias), g = 2^-23 (a unit of fp32: the tensor
@@ -144,7 +144,6 @@ class Case:
         dq, dk, dv, bq, bk, bv = z(self.q), z(self.k), z(self.v), z(self.q), z(self.k), z(self.v)
         sub = 2.0 ** -25 if self.io == torch.float16 else 0.0
         G = self.Hq // self.Hkv
-        part = 1.0 if G > 1 else 0.0
         for b in range(self.B):
             for h in range(self.Hq):
                 kh = h // G
@@ -160,11 +159,11 @@ class Case:
                 n = G23 * max(self.Sq, self.Skv)
                 pv = p.T @ do.abs()
                 dv[b, kh] += p.T @ do
-                bv[b, kh] += (self.u * (1 + part) * 1.01 + e + n) * pv + sub * (p > 0).double().T @ do.abs()
+                bv[b, kh] += (self.u * 1.01 + e + n) * pv + sub * (p > 0).double().T @ do.abs()
                 dq[b, h] = ds @ k * self.scale
                 bq[b, h] = self.scale * ((E + n * ds.abs()) @ k.abs()) + self.u * 1.01 * dq[b, h].abs() + 1e-30
                 dk[b, kh] += ds.T @ q * self.scale
-                bk[b, kh] += self.scale * ((E + (n + part * self.u) * ds.abs()).T @ q.abs())
+                bk[b, kh] += self.scale * ((E + n * ds.abs()).T @ q.abs())
         bk += self.u * 1.01 * dk.abs() + 1e-30
         bv += self.u * 1.01 * dv.abs() + 1e-30
         if sub:  # rounding into fp16's subnormal range

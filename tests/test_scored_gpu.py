@@ -166,9 +166,10 @@ def test_masked_scores_may_be_huge():
 
 
 def test_a_plan_that_masks_nothing():
-    """It gives the plain call's results: the backward bit for bit (the same operations in
-    the same order), the forward, whose two softmax halves split a row's keys by tiles
-    instead of within tiles, within the bounds that both keep to the exact result."""
+    """It gives the plain call's results: dQ bit for bit (the same operations in the same
+    order); O and LSE, whose exponents and sums are formed in another order, and dK and
+    dV, whose group sums are rounded once instead of once per head as well, within the
+    bounds that they keep to the exact result."""
     sdpa = _sdpa()
     c = Case(2, 4, 2, 200, 200, 128, 128, seed=9, causal=True)
     q, k, v, do = (t.cuda() for t in (c.q, c.k, c.v, c.do))
@@ -181,8 +182,10 @@ def test_a_plan_that_masks_nothing():
         assert_within("lse", lse, rl, bl)
     x = sdpa.sdpa_bwd(q, k, v, a[0], do, a[1], causal=True, deterministic=True)
     y = sdpa.sdpa_bwd(q, k, v, a[0], do, a[1], causal=True, deterministic=True, mask_plan=plan)
-    for s, t in zip(x, y):
-        assert torch.equal(s, t)
+    assert torch.equal(x[0], y[0])
+    ref, bounds = c.backward(a[0].cpu(), a[1].cpu())
+    for name, g, r, bound in zip(("dq", "dk", "dv"), y, ref, bounds):
+        assert_within(name, g, r, bound)
 
 
 @pytest.mark.parametrize("B,S", [(1, 1), (2, 63), (3, 1025), (2, 5000)])
