@@ -542,7 +542,7 @@ _Strides = ctypes.c_longlong * 12
 
 
 def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, k_out, stream):
-    lib = _lib or load()
+    lib = load()
     if q_out is None and isinstance(q, torch.Tensor):
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if k_out is None and isinstance(k, torch.Tensor):

@@ -79,7 +79,7 @@ class Case:
         self.softcap, self.rows, self.mask = softcap, rows, mask
         self.slopes = None if slopes is None else torch.tensor(slopes, dtype=torch.float32)
         self.lens_q, self.lens_kv = lens_q, lens_kv
-        self.scale = 1.0 / math.sqrt(Dqk)
+        self.scale = float(torch.tensor(1.0 / math.sqrt(Dqk), dtype=torch.float32))  # as the library holds it
         self.u = torch.finfo(io).eps / 2
 
     def _lens(self, b):
@@ -90,7 +90,7 @@ class Case:
         """(q, k, v, x with -inf where masked, dx/dy, error of a score)."""
         kh = h // (self.Hq // self.Hkv)
         q, k, v = self.q[b, h].double(), self.k[b, kh].double(), self.v[b, kh].double()
-        scale = float(torch.tensor(self.scale, dtype=torch.float32))
+        scale = self.scale
         y = q @ k.T * scale
         size = (q.abs() @ k.abs().T).max().item() * scale if self.Skv and self.Sq else 0.0
         f, x = torch.ones_like(y), y
