@@ -2,6 +2,7 @@
 // kernels and their host launcher.
 #pragma once
 
+#include <climits>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -148,46 +149,60 @@ __device__ inline void planned_query_tiles(const ScoreMods& m, int b, int kt, in
   qt_hi = min(qt_hi, s.y);
 }
 
-// Narrows the rows [lo, hi] that see key k by a mask plan whose rows are neighbours;
-// returns whether the plan's are not (then the tiles' row ranges decide).
-__device__ __forceinline__ bool key_rows(const ChainParams& p, int b, int k, long long& lo, long long& hi) {
-  if (p.mods.k_rows == nullptr) return false;
-  if (p.mods.k_exact[b] == 0) return true;
-  const int2 r = p.mods.k_rows[(long long)b * p.n_kt * BN + k];
-  lo = max(lo, (long long)r.x);
-  hi = min(hi, (long long)r.y);
-  return false;
+// A compute thread's key for a whole unit: the rows that see it, and the same over its
+// warp's keys, from which each tile's masks follow without loads or votes.
+struct ModKey {
+  int k, k_last;                       // the key, and the warp's last one
+  int lo, hi;                          // rows [lo, hi] see it (hi < lo: none; no upper bound: INT_MAX)
+  int lo_max, hi_min, lo_min, hi_max;  // over the warp: what all and what any of its keys see
+  bool row_ranges;                     // the plan's rows are not neighbours: each tile's own ranges decide
+};
+__device__ __forceinline__ ModKey mod_key(const ChainParams& p, int b, int k, int Lk, int diag) {
+  ModKey m;
+  m.k = k;
+  m.k_last = __reduce_max_sync(0xffffffffu, k);
+  long long lo = 0, hi = INT_MAX;
+  if (p.causal) lo = max(lo, (long long)k - diag - max(p.window_right, 0));
+  if (p.window_left >= 0) hi = min(hi, (long long)k - diag + p.window_left);
+  m.row_ranges = false;
+  if (p.mods.k_rows != nullptr) {
+    m.row_ranges = p.mods.k_exact[b] == 0;
+    if (!m.row_ranges) {
+      const int2 r = p.mods.k_rows[(long long)b * p.n_kt * BN + k];
+      lo = max(lo, (long long)r.x);
+      if (r.y < p.Sq - 1) hi = min(hi, (long long)r.y);
+    }
+  }
+  m.lo = (int)min(lo, (long long)INT_MAX);
+  m.hi = k < Lk ? (int)max(hi, -1ll) : -1;
+  m.lo_max = __reduce_max_sync(0xffffffffu, m.lo);
+  m.hi_min = __reduce_min_sync(0xffffffffu, m.hi);
+  m.lo_min = __reduce_min_sync(0xffffffffu, m.lo);
+  m.hi_max = __reduce_max_sync(0xffffffffu, m.hi);
+  return m;
 }
 
-// The replay state (score.cuh) of a thread that holds key k of the key tile at k0
-// against the 64-row query tile qt of batch row b, query head h. q_lo_vis and q_hi_vis
-// bound the rows that see the key (key_rows() included); `row_ranges`: the plan's rows
-// are not neighbours and each tile's own ranges decide.
-__device__ __forceinline__ ModTile mod_tile(const ChainParams& p, int b, int h, int qt, int k0, int k, int Lk, int diag,
-                                            bool edge, bool row_ranges, long long q_lo_vis, long long q_hi_vis) {
+// The replay state (score.cuh) of that thread against the 64-row query tile qt of batch
+// row b, with the head's slope.
+__device__ __forceinline__ ModTile mod_tile(const ChainParams& p, const ModKey& key, int b, int qt, int k0, int Lk,
+                                            int diag, float slope2) {
   ModTile m;
   const int q0 = qt * BQ;
-  m.cap_in = p.mods.cap_in;
-  m.cap_small = p.mods.cap_small;
-  const float c = p.mods.cap_in != 0.f ? p.mods.cap_log2 : p.scale_log2;
-  m.c2 = f2_pack(c, c);
-  m.slope2 = p.mods.slopes != nullptr ? p.mods.slopes[h] * 1.4426950408889634f : 0.f;
-  m.dist = (float)((long long)q0 + diag - k);
-  m.ahead = __all_sync(0xffffffffu, m.dist >= 0.f);
-  m.q_lo = (int)min(max(q_lo_vis - q0, 0ll), (long long)BQ);
-  m.q_hi = k < Lk ? (int)min(max(q_hi_vis - q0, -1ll), (long long)BQ) : -1;
-  m.k = k;
+  m.slope2 = slope2;
+  m.dist = (float)(q0 + diag - key.k);
+  m.ahead = slope2 == 0.f || q0 + diag >= key.k_last;
+  m.k = key.k;
+  m.q_lo = key.lo - q0;
+  m.q_hi = key.hi - q0;
   m.ranges = nullptr;
-  m.masked = edge;
-  if (row_ranges) {
+  if (key.row_ranges) {
     const int4 s = p.mods.q_sum[(long long)b * p.n_qt + qt];
-    if (s.z > k0 || s.w < min(k0 + BN, Lk)) {  // some row does not see the whole key tile
+    if (s.z > k0 || s.w < min(k0 + BN, Lk))  // some row does not see the whole key tile
       m.ranges = p.mods.ranges + ((long long)b * p.n_qt + qt) * BQ;
-      m.masked = true;
-    }
-  } else if (p.mods.k_rows != nullptr) {  // the bounds come from key_rows(): this warp's 32 keys
-    m.masked = __any_sync(0xffffffffu, m.q_lo > 0 || m.q_hi < BQ - 1);
   }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    m.full[h] = key.lo_max <= q0 + 32 * h && key.hi_min >= q0 + 32 * h + 31 && m.ranges == nullptr;
   return m;
 }
 

@@ -162,16 +162,25 @@ constexpr int SIDE = 8, FWD_SIDE = 16;
 // cap, P is then multiplied by t^2 - 1 instead of 1 - t^2, so dS comes out negated, and
 // the host hands these kernels -scale for dQ and dK.
 struct ModTile {
-  float cap_in, cap_small;
-  uint64_t c2;         // log2(e) times the cap, or times the scale: the exponent per tanh or per score
   float slope2;        // the head's slope * log2(e) (0 without slopes)
   float dist;          // q0 + diag - k: the distance of row i is |dist + i|
   int q_lo, q_hi;      // rows (relative to the tile) inside the causal / window / length / plan bounds
   int k;
   const int2* ranges;  // the tile's row ranges where those decide, or null
-  bool masked;         // the tile needs a mask (uniform across the warp)
+  bool full[2];        // by halves of 32 rows, uniform across the warp: all its keys see all the rows
   bool ahead;          // every row of the tile is at or past the warp's keys: no |.| needed
 };
+
+// The call's scaling: c2 = log2(e) times the cap, or times the scale, in pairs (the exponent
+// per tanh or per score), and the cap's other constants.
+struct ModCap {
+  uint64_t c2;
+  float cap_in, cap_small;
+};
+__device__ __forceinline__ ModCap mod_cap(const ScoreMods& m, float scale_log2) {
+  const float c = m.cap_in != 0.f ? m.cap_log2 : scale_log2;
+  return ModCap{f2_pack(c, c), m.cap_in, m.cap_small};
+}
 
 // Half H (rows 32 H .. 32 H + 31) of a tile's replay. r: S^T on entry. P gets the
 // masked probabilities (with a cap times t^2 - 1), which is all that the dS step reads; w
@@ -182,7 +191,8 @@ struct ModTile {
 // which the exponentials (a quarter of the FMA rate) run under the polynomials of the
 // neighbouring pairs; the general pass goes step by step.
 template <int MOD, bool F16, int H>
-__device__ __forceinline__ void mod_replay_half(const ModTile& m, const CapCoef& coef, const float* n_lse,
+__device__ __forceinline__ void mod_replay_half(const ModTile& m, const CapCoef& coef, const ModCap& cap,
+                                                const float* n_lse,
                                                 uint32_t (&r)[32], uint64_t (&P)[32], uint32_t (&w)[16]) {
   bool small = true;
   if constexpr (MOD == MOD_CAP) {
@@ -190,13 +200,13 @@ __device__ __forceinline__ void mod_replay_half(const ModTile& m, const CapCoef&
 #pragma unroll
     for (int i = 0; i < 32; i += 2)
       big[(i >> 1) & 3] = max3(big[(i >> 1) & 3], fabsf(__uint_as_float(r[i])), fabsf(__uint_as_float(r[i + 1])));
-    small = __all_sync(0xffffffffu, max3(big[0], big[1], fmaxf(big[2], big[3])) <= m.cap_small);
+    small = __all_sync(0xffffffffu, max3(big[0], big[1], fmaxf(big[2], big[3])) <= cap.cap_small);
   }
   const ulonglong2* l2 = reinterpret_cast<const ulonglong2*>(n_lse) + H * 8;  // two pairs a load
   const float bias = -m.slope2 * m.dist;  // -slope2 (dist + i): the i part is in the row statistics
   const uint64_t bias2 = f2_pack(bias, bias), minus_one = f2_pack(-1.f, -1.f);
   uint64_t* const Ph = P + H * 16;
-  if (small && !m.masked && m.ahead) {
+  if (small && m.full[H] && m.ahead) {
 #pragma unroll
     for (int blk = 0; blk < 16 / SIDE; ++blk) {
       uint64_t t[SIDE], x[SIDE];
@@ -210,8 +220,8 @@ __device__ __forceinline__ void mod_replay_half(const ModTile& m, const CapCoef&
 #pragma unroll
       for (int i = 0; i < SIDE; i += 2) {
         const ulonglong2 l = l2[(blk * SIDE + i) / 2];
-        x[i] = f2_fma(t[i], m.c2, f2_add(l.x, bias2));
-        x[i + 1] = f2_fma(t[i + 1], m.c2, f2_add(l.y, bias2));
+        x[i] = f2_fma(t[i], cap.c2, f2_add(l.x, bias2));
+        x[i + 1] = f2_fma(t[i + 1], cap.c2, f2_add(l.y, bias2));
       }
 #pragma unroll
       for (int i = 0; i < SIDE; ++i) {
@@ -242,7 +252,7 @@ __device__ __forceinline__ void mod_replay_half(const ModTile& m, const CapCoef&
 #pragma unroll
         for (int i = 0; i < SIDE; ++i) t[i] = f2_mul(t[i], x[i]);
       } else {
-        tanh2_any(t, m.cap_in);
+        tanh2_any(t, cap.cap_in);
       }
 #pragma unroll
       for (int i = 0; i < SIDE; ++i) f2_unpack(t[i], r[2 * (blk * SIDE + i)], r[2 * (blk * SIDE + i) + 1]);
@@ -251,8 +261,8 @@ __device__ __forceinline__ void mod_replay_half(const ModTile& m, const CapCoef&
 #pragma unroll
   for (int i4 = 0; i4 < 8; ++i4) {
     const ulonglong2 l = l2[i4];
-    Ph[2 * i4] = f2_fma(f2_pack(r[4 * i4], r[4 * i4 + 1]), m.c2, l.x);
-    Ph[2 * i4 + 1] = f2_fma(f2_pack(r[4 * i4 + 2], r[4 * i4 + 3]), m.c2, l.y);
+    Ph[2 * i4] = f2_fma(f2_pack(r[4 * i4], r[4 * i4 + 1]), cap.c2, l.x);
+    Ph[2 * i4 + 1] = f2_fma(f2_pack(r[4 * i4 + 2], r[4 * i4 + 3]), cap.c2, l.y);
   }
   if (m.slope2 != 0.f) {
     // -slope2 |dist + i| with the row statistics' -slope2 i taken back.
@@ -306,7 +316,7 @@ __device__ __forceinline__ uint4 mod_ds_chunk(const ModTile& m, const uint64_t (
     const uint64_t p = P[chunk * 4 + e];
     float s0, s1;
     f2_unpack(f2_mul(p, f2_add(f2_pack(r[i], r[i + 1]), d[e])), s0, s1);
-    if (m.masked) {  // a masked pair's dP may have overflowed: its dS is 0, not 0 * inf
+    if (!m.full[chunk >> 2]) {  // a masked pair's dP may have overflowed: its dS is 0, not 0 * inf
       float p0, p1;
       f2_unpack(p, p0, p1);
       s0 = p0 == 0.f ? 0.f : s0;

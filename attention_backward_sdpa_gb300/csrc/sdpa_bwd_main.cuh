@@ -692,10 +692,14 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
     const int k = k0 + row;            // this thread's key (S^T / dP^T lane)
     const bool row_dead = k >= Lk;
-    long long q_lo_vis = p.causal ? (long long)k - diag - Rp : -(1ll << 40);
-    long long q_hi_vis = has_window ? (long long)k - diag + p.window_left : (1ll << 40);
-    bool row_ranges = false;
-    if constexpr (MOD) row_ranges = key_rows(p, b, k, q_lo_vis, q_hi_vis);
+    const long long q_lo_vis = p.causal ? (long long)k - diag - Rp : -(1ll << 40);
+    const long long q_hi_vis = has_window ? (long long)k - diag + p.window_left : (1ll << 40);
+    ModKey mk;
+    ModCap cap;
+    if constexpr (MOD) {
+      mk = mod_key(p, b, k, Lk, diag);
+      cap = mod_cap(p.mods, p.scale_log2);
+    }
     const float scale_log2 = p.scale_log2;
     uint8_t* ds_row = sDS + slot * L::TILE_DS + row * 128;
     float P[MOD ? 1 : BQ];
@@ -721,17 +725,32 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
         for (int i = 0; i < BQ; ++i) bz[i] = 0.f;
     }
 
+    // MOD: head and query tile of the group's walk, counted along instead of divided out.
+    int mod_h = 0, mod_r = slot;
+    float slope2 = 0.f;
+    if constexpr (MOD) {
+      if (n > 0) {
+        while (mod_r >= n1) mod_r -= n1, ++mod_h;
+        if (p.mods.slopes != nullptr && mod_h < p.gsz) slope2 = p.mods.slopes[bh0 - b * p.Hq + mod_h] * LOG2E_F;
+      }
+    }
     for (int t = slot; t < n && ok; t += 2) {
       const int j = t >> 1, st = t % NSTAGE;
-      const int qt = qt_hi - (t % n1), q0 = qt * BQ;
+      const int qt = qt_hi - (MOD ? mod_r : t % n1), q0 = qt * BQ;
       const float* qs = sQS + st * QSTAT_FLOATS;
       const bool need_mask = (k0 + BN > Lk) ||
                              (p.causal && (long long)q0 < (long long)(k0 + BN - 1) - diag - Rp) ||
                              (has_window && (long long)(q0 + BQ - 1) > (long long)k0 - diag + p.window_left);
       const long long bias_off = BIAS ? bias_tile_off(t) : 0;
       ModTile mt;
-      if constexpr (MOD)
-        mt = mod_tile(p, b, bh0 + t / n1 - b * p.Hq, qt, k0, k, Lk, diag, need_mask, row_ranges, q_lo_vis, q_hi_vis);
+      if constexpr (MOD) {
+        mt = mod_tile(p, mk, b, qt, k0, Lk, diag, slope2);
+        mod_r += 2;
+        if (mod_r >= n1) {
+          while (mod_r >= n1) mod_r -= n1, ++mod_h;
+          if (p.mods.slopes != nullptr && mod_h < p.gsz) slope2 = p.mods.slopes[bh0 - b * p.Hq + mod_h] * LOG2E_F;
+        }
+      }
 
       // ---- softmax replay: P^T from S^T. The row statistics were written by
       // TMA, so this thread waits on the stage's transaction barrier itself.
@@ -746,10 +765,10 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
         tmem_ld32(t_lane + L::col_s(slot) + 32, rb);
         tmem_ld_wait(ra);
         tmem_ld_wait(rb);
-        mod_replay_half<MOD, F16, 0>(mt, coef, qs, ra, P2, w);
+        mod_replay_half<MOD, F16, 0>(mt, coef, cap, qs, ra, P2, w);
         __syncwarp();
         tmem_st16(t_lane + L::col_s(slot), w);
-        mod_replay_half<MOD, F16, 1>(mt, coef, qs, rb, P2, w);
+        mod_replay_half<MOD, F16, 1>(mt, coef, cap, qs, rb, P2, w);
         __syncwarp();
         tmem_st16(t_lane + L::col_s(slot) + 16, w);
       } else {

@@ -394,10 +394,16 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
     const int k = k0 + row;
     const bool row_dead = k >= Lk;
-    long long q_lo_vis = p.causal ? (long long)k - diag - Rp : -(1ll << 40);
-    long long q_hi_vis = has_window ? (long long)k - diag + p.window_left : (1ll << 40);
-    bool row_ranges = false;
-    if constexpr (MOD) row_ranges = key_rows(p, b, k, q_lo_vis, q_hi_vis);
+    const long long q_lo_vis = p.causal ? (long long)k - diag - Rp : -(1ll << 40);
+    const long long q_hi_vis = has_window ? (long long)k - diag + p.window_left : (1ll << 40);
+    ModKey mk;
+    ModCap cap;
+    float slope2 = 0.f;
+    if constexpr (MOD) {
+      mk = mod_key(p, b, k, Lk, diag);
+      cap = mod_cap(p.mods, p.scale_log2);
+      if (p.mods.slopes != nullptr) slope2 = p.mods.slopes[h] * 1.4426950408889634f;
+    }
     uint8_t* ds_row = sDS + slot * L::TILE_DS + row * 128;
     float P[MOD ? 1 : BQ];
     uint64_t P2[MOD ? BQ / 2 : 1];  // MOD: pairs of query rows
@@ -427,7 +433,7 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
                              (p.causal && (long long)q0 < (long long)(k0 + BN - 1) - diag - Rp) ||
                              (has_window && (long long)(q0 + BQ - 1) > (long long)k0 - diag + p.window_left);
       ModTile mt;
-      if constexpr (MOD) mt = mod_tile(p, b, h, qt, k0, k, Lk, diag, need_mask, row_ranges, q_lo_vis, q_hi_vis);
+      if constexpr (MOD) mt = mod_tile(p, mk, b, qt, k0, Lk, diag, slope2);
       if (!mbar_wait(&bars[BAR_QFULL + st], (t / NQ) & 1, abort_flag, WAIT_LIMIT_NS) ||
           !mbar_wait(&bars[BAR_SFULL + slot], j & 1, abort_flag, WAIT_LIMIT_NS)) { ok = false; break; }
       __syncwarp();
@@ -442,8 +448,8 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
         tc_fence_before();
         mbar_arrive(&bars[BAR_SREAD + slot]);  // the S^T columns may be overwritten
         if constexpr (MOD) {
-          mod_replay_half<MOD, F16, 0>(mt, coef, qs, ra, P2, pw[0]);
-          mod_replay_half<MOD, F16, 1>(mt, coef, qs, rb, P2, pw[1]);
+          mod_replay_half<MOD, F16, 0>(mt, coef, cap, qs, ra, P2, pw[0]);
+          mod_replay_half<MOD, F16, 1>(mt, coef, cap, qs, rb, P2, pw[1]);
         } else {
         const float4* lse4 = reinterpret_cast<const float4*>(qs);
 #pragma unroll
