@@ -191,18 +191,37 @@ __device__ __forceinline__ ModTile mod_tile(const ChainParams& p, const ModKey& 
   m.slope2 = slope2;
   m.dist = (float)(q0 + diag - key.k);
   m.ahead = slope2 == 0.f || q0 + diag >= key.k_last;
-  m.k = key.k;
-  m.q_lo = key.lo - q0;
-  m.q_hi = key.hi - q0;
-  m.ranges = nullptr;
+  const int2* ranges = nullptr;
   if (key.row_ranges) {
     const int4 s = p.mods.q_sum[(long long)b * p.n_qt + qt];
     if (s.z > k0 || s.w < min(k0 + BN, Lk))  // some row does not see the whole key tile
-      m.ranges = p.mods.ranges + ((long long)b * p.n_qt + qt) * BQ;
+      ranges = p.mods.ranges + ((long long)b * p.n_qt + qt) * BQ;
   }
+  m.full[0] = m.full[1] = key.lo_max <= q0 && key.hi_min >= q0 + BQ - 1 && ranges == nullptr;
+  m.see[0] = m.see[1] = 0xFFFFFFFFu;
+  if (m.full[0]) return m;
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    m.full[h] = key.lo_max <= q0 + 32 * h && key.hi_min >= q0 + 32 * h + 31 && m.ranges == nullptr;
+  for (int h = 0; h < 2; ++h) {
+    const int r0 = q0 + 32 * h, lo = key.lo - r0, hi = key.hi - r0;
+    m.full[h] = key.lo_max <= r0 && key.hi_min >= r0 + 31 && ranges == nullptr;
+    m.see[h] = lo <= 0 ? 0xFFFFFFFFu : lo >= 32 ? 0u : 0xFFFFFFFFu << lo;
+    if (hi < 31) m.see[h] &= hi < 0 ? 0u : (2u << hi) - 1u;
+  }
+  if (ranges != nullptr) {
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      const int4* rg = reinterpret_cast<const int4*>(ranges) + 16 * h;  // two rows, one address for the warp
+      uint32_t in = 0u;
+#pragma unroll 8
+      for (int i2 = 0; i2 < 16; ++i2) {
+        const int4 v = __ldg(rg + i2);
+        in |= (uint32_t)(key.k >= v.x && key.k < v.y) << (2 * i2);
+        in |= (uint32_t)(key.k >= v.z && key.k < v.w) << (2 * i2 + 1);
+      }
+      if (h == 0) m.see[0] &= in;
+      else m.see[1] &= in;
+    }
+  }
   return m;
 }
 

@@ -164,10 +164,8 @@ constexpr int SIDE = 8, FWD_SIDE = 16;
 struct ModTile {
   float slope2;        // the head's slope * log2(e) (0 without slopes)
   float dist;          // q0 + diag - k: the distance of row i is |dist + i|
-  int q_lo, q_hi;      // rows (relative to the tile) inside the causal / window / length / plan bounds
-  int k;
-  const int2* ranges;  // the tile's row ranges where those decide, or null
-  bool full[2];        // by halves of 32 rows, uniform across the warp: all its keys see all the rows
+  uint32_t see[2];     // by halves of 32 rows: bit i set when row i sees the key
+  bool full[2];        // uniform across the warp: all the half's rows see all its keys
   bool ahead;          // every row of the tile is at or past the warp's keys: no |.| needed
 };
 
@@ -276,55 +274,64 @@ __device__ __forceinline__ void mod_replay_half(const ModTile& m, const CapCoef&
       Ph[i2] = f2_pack(x0, x1);
     }
   }
-  const int4* rg = reinterpret_cast<const int4*>(m.ranges) + H * 16;
 #pragma unroll
   for (int i2 = 0; i2 < 16; ++i2) {
-    const int i = H * 32 + 2 * i2;
-    bool see0 = i >= m.q_lo && i <= m.q_hi, see1 = i + 1 >= m.q_lo && i + 1 <= m.q_hi;
-    if (m.ranges != nullptr) {  // two rows per 16-byte load, the same address for the whole warp
-      const int4 v = __ldg(rg + i2);
-      see0 = see0 && m.k >= v.x && m.k < v.y;
-      see1 = see1 && m.k >= v.z && m.k < v.w;
+    float x0, x1;
+    f2_unpack(Ph[i2], x0, x1);
+    Ph[i2] = f2_pack(ex2_approx(x0), ex2_approx(x1));
+  }
+  if (!m.full[H]) {
+    // (r as well with a cap: a masked score may be an overflow or NaN, and 0 times that is
+    // NaN, so its tanh is taken as 0.)
+#pragma unroll
+    for (int i2 = 0; i2 < 16; ++i2) {
+      const bool see0 = (m.see[H] >> (2 * i2)) & 1u, see1 = (m.see[H] >> (2 * i2 + 1)) & 1u;
+      float p0, p1;
+      f2_unpack(Ph[i2], p0, p1);
+      Ph[i2] = f2_pack(see0 ? p0 : 0.f, see1 ? p1 : 0.f);
+      if constexpr (MOD == MOD_CAP) {
+        r[2 * i2] = see0 ? r[2 * i2] : 0u;
+        r[2 * i2 + 1] = see1 ? r[2 * i2 + 1] : 0u;
+      }
     }
+  }
+#pragma unroll
+  for (int i2 = 0; i2 < 16; ++i2) {
     float p0, p1;
     f2_unpack(Ph[i2], p0, p1);
-    p0 = see0 ? ex2_approx(p0) : 0.f;
-    p1 = see1 ? ex2_approx(p1) : 0.f;
     w[i2] = pack_io2<F16>(p0, p1);
-    Ph[i2] = f2_pack(p0, p1);
     if constexpr (MOD == MOD_CAP) {
-      // (A masked score may be an overflow or NaN, and 0 times that is NaN: its tanh is
-      // taken as 0.)
-      const uint64_t t = f2_pack(see0 ? r[2 * i2] : 0u, see1 ? r[2 * i2 + 1] : 0u);
+      const uint64_t t = f2_pack(r[2 * i2], r[2 * i2 + 1]);
       Ph[i2] = f2_mul(Ph[i2], f2_fma(t, t, minus_one));
     }
   }
 }
 
-// dS of 8 query rows (chunk c of the tile) as io pairs: P (dP - delta); r holds dP^T of a
-// 32-row half, c its chunk there (0 .. 3).
-template <bool F16>
-__device__ __forceinline__ uint4 mod_ds_chunk(const ModTile& m, const uint64_t (&P)[32], const float* n_delta,
-                                              const uint32_t (&r)[32], int chunk) {
-  const ulonglong2* d2 = reinterpret_cast<const ulonglong2*>(n_delta) + chunk * 2;
-  const ulonglong2 da = d2[0], db = d2[1];
-  const uint64_t d[4] = {da.x, da.y, db.x, db.y};
-  uint32_t w[4];
+// dS of half H's 32 query rows as io pairs, P (dP - delta), into the thread's row of the dS^T
+// tile (16-byte pieces, XOR-swizzled by the row's `sw`); r holds the half's dP^T.
+// CUT: some pairs are masked; theirs is 0, not 0 times a dP that may have overflowed.
+template <bool F16, bool CUT, int H>
+__device__ __forceinline__ void mod_ds_half(const ModTile& m, const uint64_t (&P)[32], const float* n_delta,
+                                            const uint32_t (&r)[32], uint8_t* ds_row, int sw) {
+  const ulonglong2* d2 = reinterpret_cast<const ulonglong2*>(n_delta) + H * 8;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int i = (chunk & 3) * 8 + 2 * e;
-    const uint64_t p = P[chunk * 4 + e];
-    float s0, s1;
-    f2_unpack(f2_mul(p, f2_add(f2_pack(r[i], r[i + 1]), d[e])), s0, s1);
-    if (!m.full[chunk >> 2]) {  // a masked pair's dP may have overflowed: its dS is 0, not 0 * inf
-      float p0, p1;
-      f2_unpack(p, p0, p1);
-      s0 = p0 == 0.f ? 0.f : s0;
-      s1 = p1 == 0.f ? 0.f : s1;
+  for (int c = 0; c < 4; ++c) {
+    const ulonglong2 da = d2[2 * c], db = d2[2 * c + 1];
+    const uint64_t d[4] = {da.x, da.y, db.x, db.y};
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = c * 8 + 2 * e;
+      float s0, s1;
+      f2_unpack(f2_mul(P[H * 16 + c * 4 + e], f2_add(f2_pack(r[i], r[i + 1]), d[e])), s0, s1);
+      if constexpr (CUT) {
+        s0 = (m.see[H] >> i) & 1u ? s0 : 0.f;
+        s1 = (m.see[H] >> (i + 1)) & 1u ? s1 : 0.f;
+      }
+      w[e] = pack_io2<F16>(s0, s1);
     }
-    w[e] = pack_io2<F16>(s0, s1);
+    *reinterpret_cast<uint4*>(ds_row + (((H * 4 + c) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 }  // namespace sdpa

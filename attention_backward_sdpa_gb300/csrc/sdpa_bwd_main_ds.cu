@@ -515,12 +515,17 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
         tc_fence_before();
         mbar_arrive(&bars[BAR_DPREAD + slot]);  // the dP^T columns may be overwritten
         const float4* delta4 = reinterpret_cast<const float4*>(qs + BQ);
+        if constexpr (MOD) {
+          if (mt.full[0] && mt.full[1]) {
+            mod_ds_half<F16, false, 0>(mt, P2, qs + BQ, ra, ds_row, row & 7);
+            mod_ds_half<F16, false, 1>(mt, P2, qs + BQ, rb, ds_row, row & 7);
+          } else {
+            mod_ds_half<F16, true, 0>(mt, P2, qs + BQ, ra, ds_row, row & 7);
+            mod_ds_half<F16, true, 1>(mt, P2, qs + BQ, rb, ds_row, row & 7);
+          }
+        } else {
 #pragma unroll
         for (int chunk = 0; chunk < 8; ++chunk) {  // 8 queries = 16 bytes of dS^T per chunk
-          if constexpr (MOD) {
-            *reinterpret_cast<uint4*>(ds_row + ((chunk ^ (row & 7)) << 4)) =
-                mod_ds_chunk<F16>(mt, P2, qs + BQ, chunk < 4 ? ra : rb, chunk);
-          } else {
           const uint32_t* r = chunk < 4 ? ra : rb;
           const int i = (chunk & 3) * 8;
           const float4 d0 = delta4[chunk * 2], d1 = delta4[chunk * 2 + 1];
@@ -561,7 +566,7 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
               }
             }
           }
-          }
+        }
         }
       }
       fence_proxy_async_smem();
