@@ -180,64 +180,80 @@ __device__ __forceinline__ ModCap mod_cap(const ScoreMods& m, float scale_log2) 
   return ModCap{f2_pack(c, c), m.cap_in, m.cap_small};
 }
 
+// Whether a tile takes the straight pass below: no mask, no |.| and, with a cap, every
+// score within the polynomial (one vote over the 64 scores). `small`: the last alone.
+template <int MOD>
+__device__ __forceinline__ bool mod_replay_straight(const ModTile& m, const ModCap& cap, const uint32_t (&ra)[32],
+                                                    const uint32_t (&rb)[32], bool& small) {
+  small = true;
+  if constexpr (MOD == MOD_CAP) {
+    float big[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      big[(i >> 1) & 3] = max3(big[(i >> 1) & 3], fabsf(__uint_as_float(ra[i])), fabsf(__uint_as_float(ra[i + 1])));
+      big[4 + ((i >> 1) & 3)] =
+          max3(big[4 + ((i >> 1) & 3)], fabsf(__uint_as_float(rb[i])), fabsf(__uint_as_float(rb[i + 1])));
+    }
+    const float b0 = max3(big[0], big[1], big[2]), b1 = max3(big[3], big[4], big[5]);
+    small = __all_sync(0xffffffffu, max3(b0, b1, fmaxf(big[6], big[7])) <= cap.cap_small);
+  }
+  return small && m.full[0] && m.full[1] && m.ahead;
+}
+
 // Half H (rows 32 H .. 32 H + 31) of a tile's replay. r: S^T on entry. P gets the
 // masked probabilities (with a cap times t^2 - 1), which is all that the dS step reads; w
 // the probabilities themselves as io pairs for the dV product. (The two are formed
-// together so that no thread holds 64 derivatives.)
-//
-// A warp whose half needs no mask, no |.| and no quotient takes one straight pass, in
-// which the exponentials (a quarter of the FMA rate) run under the polynomials of the
-// neighbouring pairs; the general pass goes step by step.
+// together so that no thread holds 64 derivatives.) The straight pass, in which the
+// exponentials (a quarter of the FMA rate) run under the neighbouring pairs' polynomials:
 template <int MOD, bool F16, int H>
-__device__ __forceinline__ void mod_replay_half(const ModTile& m, const CapCoef& coef, const ModCap& cap,
-                                                const float* n_lse,
-                                                uint32_t (&r)[32], uint64_t (&P)[32], uint32_t (&w)[16]) {
-  bool small = true;
-  if constexpr (MOD == MOD_CAP) {
-    float big[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < 32; i += 2)
-      big[(i >> 1) & 3] = max3(big[(i >> 1) & 3], fabsf(__uint_as_float(r[i])), fabsf(__uint_as_float(r[i + 1])));
-    small = __all_sync(0xffffffffu, max3(big[0], big[1], fmaxf(big[2], big[3])) <= cap.cap_small);
-  }
+__device__ __forceinline__ void mod_replay_fast(const ModTile& m, const CapCoef& coef, const ModCap& cap,
+                                                const float* n_lse, const uint32_t (&r)[32], uint64_t (&P)[32],
+                                                uint32_t (&w)[16]) {
   const ulonglong2* l2 = reinterpret_cast<const ulonglong2*>(n_lse) + H * 8;  // two pairs a load
   const float bias = -m.slope2 * m.dist;  // -slope2 (dist + i): the i part is in the row statistics
   const uint64_t bias2 = f2_pack(bias, bias), minus_one = f2_pack(-1.f, -1.f);
   uint64_t* const Ph = P + H * 16;
-  if (small && m.full[H] && m.ahead) {
 #pragma unroll
-    for (int blk = 0; blk < 16 / SIDE; ++blk) {
-      uint64_t t[SIDE], x[SIDE];
+  for (int blk = 0; blk < 16 / SIDE; ++blk) {
+    uint64_t t[SIDE], x[SIDE];
 #pragma unroll
-      for (int i = 0; i < SIDE; ++i) t[i] = f2_pack(r[2 * (blk * SIDE + i)], r[2 * (blk * SIDE + i) + 1]);
-      if constexpr (MOD == MOD_CAP) {
-        tanh2_poly(t, coef, x);
+    for (int i = 0; i < SIDE; ++i) t[i] = f2_pack(r[2 * (blk * SIDE + i)], r[2 * (blk * SIDE + i) + 1]);
+    if constexpr (MOD == MOD_CAP) {
+      tanh2_poly(t, coef, x);
 #pragma unroll
-        for (int i = 0; i < SIDE; ++i) t[i] = f2_mul(t[i], x[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < SIDE; i += 2) {
-        const ulonglong2 l = l2[(blk * SIDE + i) / 2];
-        x[i] = f2_fma(t[i], cap.c2, f2_add(l.x, bias2));
-        x[i + 1] = f2_fma(t[i + 1], cap.c2, f2_add(l.y, bias2));
-      }
-#pragma unroll
-      for (int i = 0; i < SIDE; ++i) {
-        float x0, x1;
-        f2_unpack(x[i], x0, x1);
-        x[i] = f2_pack(ex2_approx(x0), ex2_approx(x1));
-        if constexpr (MOD == MOD_CAP) t[i] = f2_fma(t[i], t[i], minus_one);
-      }
-#pragma unroll
-      for (int i = 0; i < SIDE; ++i) {
-        float p0, p1;
-        f2_unpack(x[i], p0, p1);
-        w[blk * SIDE + i] = pack_io2<F16>(p0, p1);
-        Ph[blk * SIDE + i] = MOD == MOD_CAP ? f2_mul(x[i], t[i]) : x[i];
-      }
+      for (int i = 0; i < SIDE; ++i) t[i] = f2_mul(t[i], x[i]);
     }
-    return;
+#pragma unroll
+    for (int i = 0; i < SIDE; i += 2) {
+      const ulonglong2 l = l2[(blk * SIDE + i) / 2];
+      x[i] = f2_fma(t[i], cap.c2, f2_add(l.x, bias2));
+      x[i + 1] = f2_fma(t[i + 1], cap.c2, f2_add(l.y, bias2));
+    }
+#pragma unroll
+    for (int i = 0; i < SIDE; ++i) {
+      float x0, x1;
+      f2_unpack(x[i], x0, x1);
+      x[i] = f2_pack(ex2_approx(x0), ex2_approx(x1));
+      if constexpr (MOD == MOD_CAP) t[i] = f2_fma(t[i], t[i], minus_one);
+    }
+#pragma unroll
+    for (int i = 0; i < SIDE; ++i) {
+      float p0, p1;
+      f2_unpack(x[i], p0, p1);
+      w[blk * SIDE + i] = pack_io2<F16>(p0, p1);
+      Ph[blk * SIDE + i] = MOD == MOD_CAP ? f2_mul(x[i], t[i]) : x[i];
+    }
   }
+}
+
+// ... and the general one, step by step.
+template <int MOD, bool F16, int H>
+__device__ __forceinline__ void mod_replay_half(const ModTile& m, const CapCoef& coef, const ModCap& cap, bool small,
+                                                const float* n_lse, uint32_t (&r)[32], uint64_t (&P)[32],
+                                                uint32_t (&w)[16]) {
+  const ulonglong2* l2 = reinterpret_cast<const ulonglong2*>(n_lse) + H * 8;
+  const uint64_t minus_one = f2_pack(-1.f, -1.f);
+  uint64_t* const Ph = P + H * 16;
   if constexpr (MOD == MOD_CAP) {
     // r becomes the tanh.
 #pragma unroll

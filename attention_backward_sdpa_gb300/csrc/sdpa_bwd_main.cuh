@@ -765,11 +765,18 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
         tmem_ld32(t_lane + L::col_s(slot) + 32, rb);
         tmem_ld_wait(ra);
         tmem_ld_wait(rb);
-        mod_replay_half<MOD, F16, 0>(mt, coef, cap, qs, ra, P2, w);
-        __syncwarp();
-        tmem_st16(t_lane + L::col_s(slot), w);
-        mod_replay_half<MOD, F16, 1>(mt, coef, cap, qs, rb, P2, w);
-        __syncwarp();
+        bool small;
+        if (mod_replay_straight<MOD>(mt, cap, ra, rb, small)) {
+          mod_replay_fast<MOD, F16, 0>(mt, coef, cap, qs, ra, P2, w);
+          tmem_st16(t_lane + L::col_s(slot), w);
+          mod_replay_fast<MOD, F16, 1>(mt, coef, cap, qs, rb, P2, w);
+        } else {
+          mod_replay_half<MOD, F16, 0>(mt, coef, cap, small, qs, ra, P2, w);
+          __syncwarp();
+          tmem_st16(t_lane + L::col_s(slot), w);
+          mod_replay_half<MOD, F16, 1>(mt, coef, cap, small, qs, rb, P2, w);
+          __syncwarp();
+        }
         tmem_st16(t_lane + L::col_s(slot) + 16, w);
       } else {
       {

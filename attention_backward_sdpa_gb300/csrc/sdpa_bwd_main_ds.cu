@@ -448,8 +448,14 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
         tc_fence_before();
         mbar_arrive(&bars[BAR_SREAD + slot]);  // the S^T columns may be overwritten
         if constexpr (MOD) {
-          mod_replay_half<MOD, F16, 0>(mt, coef, cap, qs, ra, P2, pw[0]);
-          mod_replay_half<MOD, F16, 1>(mt, coef, cap, qs, rb, P2, pw[1]);
+          bool small;
+          if (mod_replay_straight<MOD>(mt, cap, ra, rb, small)) {
+            mod_replay_fast<MOD, F16, 0>(mt, coef, cap, qs, ra, P2, pw[0]);
+            mod_replay_fast<MOD, F16, 1>(mt, coef, cap, qs, rb, P2, pw[1]);
+          } else {
+            mod_replay_half<MOD, F16, 0>(mt, coef, cap, small, qs, ra, P2, pw[0]);
+            mod_replay_half<MOD, F16, 1>(mt, coef, cap, small, qs, rb, P2, pw[1]);
+          }
         } else {
         const float4* lse4 = reinterpret_cast<const float4*>(qs);
 #pragma unroll
