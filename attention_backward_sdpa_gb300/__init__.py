@@ -11,6 +11,7 @@ an sm_103 GPU, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from typing import Optional, Tuple
@@ -125,6 +126,11 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _addr(t: Optional[torch.Tensor]):
+    """The address as a plain integer (ctypes takes it for a pointer; no object is made)."""
+    return None if t is None else t.data_ptr()
+
+
 def _stream_handle(stream: Optional[torch.cuda.Stream]):
     if stream is not None:
         return stream.cuda_stream
@@ -157,6 +163,11 @@ def workspace_size(B, Hq, Hkv, Sq, Skv, Dqk, Dv, deterministic=False, *, causal=
     size = lib.sdpa_bwd_scored_workspace_size if scored else lib.sdpa_bwd_workspace_size
     return int(size(B, Hq, Hkv, Sq, Skv, Dqk, Dv, int(causal), int(bottom_right), int(window_left),
                     int(window_right), int(deterministic), int(padded)))
+
+
+@functools.lru_cache(maxsize=4096)
+def _scored_workspace(lib, *sizes) -> int:
+    return int(lib.sdpa_bwd_scored_workspace_size(*sizes))
 
 
 def _check_bf16(name, t, shape, dtype=torch.bfloat16):
@@ -262,6 +273,7 @@ def sdpa_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
     B, Hq, Sq, Dqk = q.shape
     Hkv, Skv = k.shape[1], k.shape[2]
     Dv = v.shape[3]
+    fresh = dq is None and dk is None and dv is None  # (outputs made here need no checks)
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
@@ -270,10 +282,13 @@ def sdpa_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
         dsink = _check_sink(sink, dsink, Hq)
     dev, q_shape, k_shape, o_shape = q.get_device(), (B, Hq, Sq, Dqk), (B, Hkv, Skv, Dqk), (B, Hq, Sq, Dv)
     if not (q.is_cuda and _is(q, io, dev, q_shape) and _is(k, io, dev, k_shape) and _is(v, io, dev, (B, Hkv, Skv, Dv))
-            and _is(o, io, dev, o_shape) and _is(do, io, dev, o_shape) and _is(dq, io, dev, q_shape)
-            and _is(dk, io, dev, k_shape) and _is(dv, io, dev, (B, Hkv, Skv, Dv))
-            and _optional(lse, torch.float32, dev, B * Hq * Sq) and _optional(seq_q_lens, torch.int32, dev, B)
-            and _optional(seq_kv_lens, torch.int32, dev, B) and workspace is None and sink is None and bias is None):
+            and _is(o, io, dev, o_shape) and _is(do, io, dev, o_shape)
+            and (fresh or _is(dq, io, dev, q_shape) and _is(dk, io, dev, k_shape)
+                 and _is(dv, io, dev, (B, Hkv, Skv, Dv)))
+            and lse is not None and _optional(lse, torch.float32, dev, B * Hq * Sq)
+            and (seq_q_lens is None or _optional(seq_q_lens, torch.int32, dev, B))
+            and (seq_kv_lens is None or _optional(seq_kv_lens, torch.int32, dev, B))
+            and workspace is None and sink is None and bias is None):
         _check_bf16("q", q, q_shape, io)
         _check_bf16("k", k, k_shape, io)
         _check_bf16("v", v, (B, Hkv, Skv, Dv), io)
@@ -291,17 +306,30 @@ def sdpa_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
     scored = _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias)
     _check_launch_device(q)
     sc = 0.0 if scale is None else float(scale)
+    if scored:
+        if workspace is None and stream is None:
+            # From torch's allocator, which keeps it for the next call. (The library's own
+            # comes from the stream-ordered pool, which returns its memory at every
+            # synchronization and maps it again at the next call: 2,018 us for the first
+            # call after one instead of 447 at B 1, Hq 32, S 4096, D 128, deterministic.)
+            # A call on a stream given to it leaves this to the library, whose allocation is
+            # ordered on that stream.
+            ws_bytes = _scored_workspace(lib, B, Hq, Hkv, Sq, Skv, Dqk, Dv, causal, bottom_right, window_left,
+                                         window_right, deterministic, seq_q_lens is not None or seq_kv_lens is not None)
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device) if ws_bytes else None
+        rc = lib.sdpa_bwd_scored(_IO_CODES[io], q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
+                                 lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Sq, Skv, Dqk,
+                                 Dv, sc, causal, bottom_right, window_left, window_right, deterministic,
+                                 _addr(seq_q_lens), _addr(seq_kv_lens), _addr(workspace), ws_bytes, _addr(sink),
+                                 None if sink is None else dsink.data_ptr(), softcap, _addr(alibi_slopes),
+                                 None if mask_plan is None else mask_plan.buffer.data_ptr(), _stream_handle(stream))
+        if rc != 0:
+            raise SdpaError(rc, "sdpa_bwd_scored")
+        return (dq, dk, dv) + ((dsink,) if sink is not None else ())
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do), _ptr(lse), _ptr(dq), _ptr(dk),
             _ptr(dv), B, Hq, Hkv, Sq, Skv, Dqk, Dv, sc, int(causal), int(bottom_right),
             int(window_left), int(window_right), int(deterministic), _ptr(seq_q_lens),
             _ptr(seq_kv_lens), _ptr(workspace), ws_bytes)
-    if scored:
-        rc = lib.sdpa_bwd_scored(_IO_CODES[io], *args, _ptr(sink), _ptr(dsink if sink is not None else None),
-                                 float(softcap), _ptr(alibi_slopes), _plan_ptr(mask_plan),
-                                 _stream_handle(stream))
-        if rc != 0:
-            raise SdpaError(rc, "sdpa_bwd_scored")
-        return (dq, dk, dv) + ((dsink,) if sink is not None else ())
     if io == torch.float16 or (bias is not None and bias_grad and dbias_dtype != torch.float32):
         # the general typed entry: fp16 io, or an io-type dBias (sink and bias optional)
         bias_dtype, bias_batch = 0, 0
@@ -380,10 +408,6 @@ class MaskPlan:
         return f"MaskPlan(B={self.B}, Sq={self.Sq}, Skv={self.Skv}, device={self.buffer.device})"
 
 
-def _plan_ptr(plan: Optional[MaskPlan]):
-    return None if plan is None else _ptr(plan.buffer)
-
-
 def _check_int32(name, t, shapes):
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous() \
             or tuple(t.shape) not in shapes:
@@ -445,8 +469,7 @@ def mask_plan(B: int, Sq: int, Skv: int, *, doc_ids: Optional[torch.Tensor] = No
 
 def _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias) -> bool:
     """Whether the call modifies its scores (and then that it may)."""
-    softcap = float(softcap)
-    if not (0.0 <= softcap < math.inf):
+    if not 0.0 <= softcap < math.inf:
         raise ValueError("softcap must be 0 (none) or a positive finite number")
     if softcap == 0.0 and alibi_slopes is None and mask_plan is None:
         return False
@@ -461,9 +484,10 @@ def _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias)
             raise TypeError("mask_plan must be a MaskPlan (made by mask_plan())")
         if (mask_plan.B, mask_plan.Sq, mask_plan.Skv) != (B, Sq, Skv):
             raise ValueError(f"mask_plan was made for {mask_plan!r}, not for B={B}, Sq={Sq}, Skv={Skv}")
-    for name, t in (("alibi_slopes", alibi_slopes), ("mask_plan", None if mask_plan is None else mask_plan.buffer)):
-        if t is not None and t.get_device() != q.get_device():
-            _check_same_device(q, **{name: t})
+    if alibi_slopes is not None and alibi_slopes.get_device() != q.get_device():
+        _check_same_device(q, alibi_slopes=alibi_slopes)
+    if mask_plan is not None and mask_plan.buffer.get_device() != q.get_device():
+        _check_same_device(q, mask_plan=mask_plan.buffer)
     return True
 
 
@@ -543,27 +567,34 @@ _Strides = ctypes.c_longlong * 12
 
 def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, k_out, stream):
     lib = load()
-    if q_out is None and isinstance(q, torch.Tensor):
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k_out is None and isinstance(k, torch.Tensor):
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
     try:
-        shape, sq, so = q.shape, q.stride(), q_out.stride()
+        shape, sq = q.shape, q.stride()
         B, Hq, S, D = shape
-        io, dev, Hkv, sk, sl = q.dtype, q.get_device(), 0, sq, so
-        good = q.is_cuda and io in _IO_CODES and q_out.dtype is io and q_out.get_device() == dev \
-            and q_out.shape == shape and sq[3] == 1 and so[3] == 1
-        if k is not None:
-            sk, sl, Hkv = k.stride(), k_out.stride(), k.shape[1]
-            good = good and k.dtype is io and k_out.dtype is io and k.get_device() == dev \
-                and k_out.get_device() == dev and k.shape == (B, Hkv, S, D) and k_out.shape == k.shape \
-                and sk[3] == 1 and sl[3] == 1
+        io, dev, Hkv = q.dtype, q.get_device(), 0
+        good = q.is_cuda and io in _IO_CODES and sq[3] == 1
+        # (Outputs made here need no checks.)
+        if q_out is None:
+            q_out, so = torch.empty(shape, dtype=io, device=q.device), (Hq * S * D, S * D, D)
+        else:
+            so = q_out.stride()
+            good = good and q_out.dtype is io and q_out.get_device() == dev and q_out.shape == shape and so[3] == 1
+        if k is None:
+            sk = sl = sq
+            good = good and k_out is None
+        else:
+            shape, sk = k.shape, k.stride()
+            Hkv = shape[1]
+            good = good and k.dtype is io and k.get_device() == dev and shape == (B, Hkv, S, D) and sk[3] == 1
+            if k_out is None:
+                k_out, sl = torch.empty(shape, dtype=io, device=q.device), (Hkv * S * D, S * D, D)
+            else:
+                sl = k_out.stride()
+                good = good and k_out.dtype is io and k_out.get_device() == dev and k_out.shape == shape and sl[3] == 1
         rot = 2 * inv_freq.shape[0]
-        good = good and _is(inv_freq, torch.float64, dev, (rot // 2,)) and 0 < rot <= D \
-            and (k_out is None or k is not None) \
+        good = good and 0 < rot <= D and _is(inv_freq, torch.float64, dev, (rot // 2,)) \
             and (positions is None or offset == 0 and (_is(positions, torch.int32, dev, (B, S))
                                                        or _is(positions, torch.int32, dev, (S,))))
-    except (AttributeError, IndexError, ValueError):  # not tensors, or of other dimensions
+    except (AttributeError, IndexError, TypeError, ValueError):  # not tensors, or of other dimensions
         good = False
     if not good:
         _check_rope_args(q, k, inv_freq, positions, offset, q_out, k_out)
@@ -574,9 +605,9 @@ def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, 
             sk, sl, Hkv = k.stride(), k_out.stride(), k.shape[1]
     _check_launch_device(q)
     if B > 0 and Hq > 0:
-        rc = lib.sdpa_rope(_IO_CODES[q.dtype], q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), B, Hq, Hkv, S, D,
+        rc = lib.sdpa_rope(_IO_CODES[q.dtype], q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out), B, Hq, Hkv, S, D,
                            _Strides(sq[0], sq[1], sq[2], so[0], so[1], so[2], sk[0], sk[1], sk[2], sl[0], sl[1], sl[2]),
-                           inv_freq.data_ptr(), rot, mult, _ptr(positions),
+                           inv_freq.data_ptr(), rot, mult, _addr(positions),
                            0 if positions is None else positions.dim() - 1, offset, interleaved, inverse,
                            _stream_handle(stream))
         if rc != 0:
@@ -634,14 +665,16 @@ def sdpa_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale: Option
     B, Hq, Sq, Dqk = q.shape
     Hkv, Skv = k.shape[1], k.shape[2]
     Dv = v.shape[3]
+    fresh = o is None and lse is None  # (outputs made here need no checks)
     o = torch.empty((B, Hq, Sq, Dv), dtype=io, device=q.device) if o is None else o
     lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device) if lse is None else lse
     dev = q.get_device()
     if not (q.is_cuda and _is(q, io, dev, (B, Hq, Sq, Dqk)) and _is(k, io, dev, (B, Hkv, Skv, Dqk))
-            and _is(v, io, dev, (B, Hkv, Skv, Dv)) and _is(o, io, dev, (B, Hq, Sq, Dv))
-            and _optional(lse, torch.float32, dev, B * Hq * Sq) and _optional(seq_q_lens, torch.int32, dev, B)
-            and _optional(seq_kv_lens, torch.int32, dev, B) and _optional(sink, torch.float32, dev, Hq)
-            and bias is None):
+            and _is(v, io, dev, (B, Hkv, Skv, Dv))
+            and (fresh or _is(o, io, dev, (B, Hq, Sq, Dv)) and _optional(lse, torch.float32, dev, B * Hq * Sq))
+            and (seq_q_lens is None or _optional(seq_q_lens, torch.int32, dev, B))
+            and (seq_kv_lens is None or _optional(seq_kv_lens, torch.int32, dev, B))
+            and (sink is None or _optional(sink, torch.float32, dev, Hq)) and bias is None):
         _check_bf16("q", q, (B, Hq, Sq, Dqk), io)
         _check_bf16("k", k, (B, Hkv, Skv, Dqk), io)
         _check_bf16("v", v, (B, Hkv, Skv, Dv), io)
@@ -656,15 +689,17 @@ def sdpa_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale: Option
     scored = _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias)
     _check_launch_device(q)
     sc = 0.0 if scale is None else float(scale)
-    args = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Sq, Skv, Dqk, Dv, sc,
-            int(causal), int(bottom_right), int(window_left), int(window_right),
-            _ptr(seq_q_lens), _ptr(seq_kv_lens), _ptr(sink))
     if scored:
-        rc = lib.sdpa_fwd_scored(_IO_CODES[io], *args, float(softcap), _ptr(alibi_slopes),
-                                 _plan_ptr(mask_plan), _stream_handle(stream))
+        rc = lib.sdpa_fwd_scored(_IO_CODES[io], q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                 B, Hq, Hkv, Sq, Skv, Dqk, Dv, sc, causal, bottom_right, window_left, window_right,
+                                 _addr(seq_q_lens), _addr(seq_kv_lens), _addr(sink), softcap, _addr(alibi_slopes),
+                                 None if mask_plan is None else mask_plan.buffer.data_ptr(), _stream_handle(stream))
         if rc != 0:
             raise SdpaError(rc, "sdpa_fwd_scored")
         return o, lse
+    args = (_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hkv, Sq, Skv, Dqk, Dv, sc,
+            int(causal), int(bottom_right), int(window_left), int(window_right),
+            _ptr(seq_q_lens), _ptr(seq_kv_lens), _ptr(sink))
     if io == torch.float16:
         bias_dtype = _check_bias(bias, B, Hq, Sq, Skv) if bias is not None else 0
         rc = lib.sdpa_fwd_typed(_IO_CODES[io], *args, _ptr(bias), bias_dtype,

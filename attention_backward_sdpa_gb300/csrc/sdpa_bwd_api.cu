@@ -383,6 +383,7 @@ int fill_mods(const ModArgs& ma, float scale, int B, int S_q, int S_kv, ScoreMod
     }
   }
   if (ma.plan) {
+    if (S_q == 0 || S_kv == 0) return SDPA_ERR_INVALID;  // there is no plan of no rows or no keys
     const MaskPlanLayout l = mask_plan_layout(B, ceil_div(S_q, BQ), ceil_div(S_kv, BN));
     const char* base = static_cast<const char*>(ma.plan);
     m.ranges = reinterpret_cast<const int2*>(base + l.ranges);
@@ -889,9 +890,10 @@ int sdpa_rope(int io_dtype, const void* q, const void* k, void* q_out, void* k_o
               int interleaved, int inverse, void* stream) {
   if (io_dtype != SDPA_DTYPE_BF16 && io_dtype != SDPA_DTYPE_F16) return SDPA_ERR_INVALID;
   if (B <= 0 || H_q <= 0 || H_kv < 0 || S < 0 || D <= 0 || !strides || !std::isfinite(mult)) return SDPA_ERR_INVALID;
-  if (!q || !q_out || !inv_freq || (H_kv > 0 && (!k || !k_out))) return SDPA_ERR_INVALID;
   if (rot_dim <= 0 || rot_dim % 2 != 0 || rot_dim > D) return SDPA_ERR_INVALID;
   if (rot_dim > 512) return SDPA_ERR_UNSUPPORTED;
+  if (S == 0) return SDPA_OK;  // no rows
+  if (!q || !q_out || !inv_freq || (H_kv > 0 && (!k || !k_out))) return SDPA_ERR_INVALID;
   if ((long long)B * S * (H_q + (long long)H_kv) >= 1ll << 31) return SDPA_ERR_INVALID;
   RopeArgs a{};
   const void* xs[2] = {q, k};
@@ -923,7 +925,6 @@ int sdpa_rope(int io_dtype, const void* q, const void* k, void* q_out, void* k_o
   }
   if (reinterpret_cast<uintptr_t>(inv_freq) % 8 != 0 || reinterpret_cast<uintptr_t>(positions) % 4 != 0)
     return SDPA_ERR_ALIGN;
-  if (S == 0) return SDPA_OK;
   if (!positions && (offset < 0 || (long long)offset + S > 1ll << 31)) return SDPA_ERR_INVALID;
   a.freq = inv_freq;
   a.positions = positions;

@@ -19,9 +19,10 @@
 // (token, pair) is shared by the heads a thread walks. So the bound is memory,
 // 4 bytes an element.
 //
-// Layout. A thread owns one token's 16 columns: eight pairs, two 16-byte loads and
-// two 16-byte stores per head, and keeps their sines and cosines in registers while
-// it walks HEADS heads, whose loads it issues together. Consecutive threads take
+// Layout. A thread owns one token's two pieces of 8 columns: eight pairs, two 16-byte loads
+// and two 16-byte stores per head, and keeps their sines and cosines in registers while
+// it walks its heads, whose loads it issues together. (Pieces of 4 or 2 columns where the
+// rotated width or the rows' alignment does not allow 8.) Consecutive threads take
 // consecutive column groups, then tokens. Tensors come with any strides of batch,
 // head and position (the projection's (B, S, H, D) as a transposed view, say), so
 // that no separate transposition is needed before or after.
@@ -81,18 +82,43 @@ __device__ __forceinline__ const RopeTensor& rope_head(const RopeParams& p, int 
   return p.t[second ? 1 : 0];
 }
 
-__device__ __forceinline__ uint32_t (&as_words(uint4& v))[4] { return reinterpret_cast<uint32_t(&)[4]>(v); }
+// A piece of VW columns (VW / 2 words), loaded and stored in one access.
+template <int VW>
+struct Piece {
+  uint32_t w[VW / 2];
+};
+template <int VW>
+__device__ __forceinline__ Piece<VW> ld_piece(const uint16_t* p) {
+  Piece<VW> v;
+  if constexpr (VW == 8) {
+    const uint4 x = *reinterpret_cast<const uint4*>(p);
+    v.w[0] = x.x, v.w[1] = x.y, v.w[2] = x.z, v.w[3] = x.w;
+  } else if constexpr (VW == 4) {
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    v.w[0] = x.x, v.w[1] = x.y;
+  } else {
+    v.w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+  return v;
+}
+template <int VW>
+__device__ __forceinline__ void st_piece(uint16_t* p, const Piece<VW>& v) {
+  if constexpr (VW == 8) *reinterpret_cast<uint4*>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+  else if constexpr (VW == 4) *reinterpret_cast<uint2*>(p) = make_uint2(v.w[0], v.w[1]);
+  else *reinterpret_cast<uint32_t*>(p) = v.w[0];
+}
 
-// 16-byte form: rot and D multiples of 16 (8 pairs a thread) for the rotated part,
-// pass-through columns in the same 16-column groups. A work item is (token, column
-// group); blockIdx.y selects a group of `heads` consecutive heads.
-template <bool F16, bool INTER, int UNROLL>
+// rot a multiple of 2 VW, D of VW, every row aligned to a piece. A work item is (token,
+// column group), a group being VW pairs, or two pass-through pieces (one, at an odd end);
+// blockIdx.y selects `heads` consecutive heads.
+template <bool F16, bool INTER, int VW>
 __global__ void __launch_bounds__(THREADS) rope_vec(const RopeParams p, int heads, long long n_items) {
+  constexpr int UNROLL = 4, NW = VW / 2;
   __shared__ uint64_t turns[256];  // rot <= 512
   const int half = p.rot / 2;
   for (int i = threadIdx.x; i < half; i += THREADS) turns[i] = turn_fraction(p.freq[i]);
   __syncthreads();
-  const int groups = p.D / 16, rot_groups = p.rot / 16;
+  const int groups = (p.D + 2 * VW - 1) / (2 * VW), rot_groups = p.rot / (2 * VW);
   const int H = p.t[0].H + p.t[1].H;
   const int h0 = blockIdx.y * heads, h1 = min(h0 + heads, H);
   for (long long it = (long long)blockIdx.x * THREADS + threadIdx.x; it < n_items;
@@ -100,31 +126,32 @@ __global__ void __launch_bounds__(THREADS) rope_vec(const RopeParams p, int head
     const int c = (int)(it % groups);
     const long long tok = it / groups;
     const int s = (int)(tok % p.S), b = (int)(tok / p.S);
-    // This thread's two 8-column pieces: the pairs' first and second halves, or
-    // two neighbouring pieces (interleaved, and past the rotated part).
+    // This thread's two pieces: the pairs' first and second halves, or two neighbouring
+    // pieces (interleaved, and past the rotated part).
     const bool rotated = c < rot_groups;
-    const int c0 = (rotated && !INTER) ? c * 8 : c * 16;
-    const int c1 = (rotated && !INTER) ? half + c * 8 : c * 16 + 8;
-    float sn[8], cs[8];
+    const int c0 = (rotated && !INTER) ? c * VW : c * 2 * VW;
+    const int c1 = (rotated && !INTER) ? half + c * VW : c * 2 * VW + VW;
+    const bool two = c1 < p.D;
+    float sn[VW], cs[VW];
     if (rotated) {
       const int pos = p.positions ? p.positions[b * p.pos_bstride + s] : p.offset + s;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        angle_sin_cos(turns[c * 8 + i], pos, sn[i], cs[i]);
+      for (int i = 0; i < VW; ++i) {
+        angle_sin_cos(turns[c * VW + i], pos, sn[i], cs[i]);
         sn[i] *= p.sign > 0 ? p.mult : -p.mult;
         cs[i] *= p.mult;
       }
     }
     for (int h = h0; h < h1; h += UNROLL) {
-      uint4 u[UNROLL], w[UNROLL];
+      Piece<VW> u[UNROLL], w[UNROLL];
 #pragma unroll
       for (int j = 0; j < UNROLL; ++j) {
         if (h + j >= h1) continue;
         int hh;
         const RopeTensor& t = rope_head(p, h + j, hh);
         const uint16_t* x = t.x + b * t.xs[0] + hh * t.xs[1] + s * t.xs[2];
-        u[j] = *reinterpret_cast<const uint4*>(x + c0);
-        w[j] = *reinterpret_cast<const uint4*>(x + c1);
+        u[j] = ld_piece<VW>(x + c0);
+        if (two) w[j] = ld_piece<VW>(x + c1);
       }
 #pragma unroll
       for (int j = 0; j < UNROLL; ++j) {
@@ -133,15 +160,15 @@ __global__ void __launch_bounds__(THREADS) rope_vec(const RopeParams p, int head
         const RopeTensor& t = rope_head(p, h + j, hh);
         uint16_t* y = t.y + b * t.ys[0] + hh * t.ys[1] + s * t.ys[2];
         if (rotated) {
-          uint32_t(&a)[4] = as_words(u[j]);
-          uint32_t(&z)[4] = as_words(w[j]);
+          uint32_t(&a)[NW] = u[j].w;
+          uint32_t(&z)[NW] = w[j].w;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < NW; ++i) {
             if (INTER) {  // a word is a pair
               const float a0 = io_lo<F16>(a[i]), b0 = io_hi<F16>(a[i]);
               const float a1 = io_lo<F16>(z[i]), b1 = io_hi<F16>(z[i]);
               a[i] = pack_io2<F16>(a0 * cs[i] - b0 * sn[i], b0 * cs[i] + a0 * sn[i]);
-              z[i] = pack_io2<F16>(a1 * cs[4 + i] - b1 * sn[4 + i], b1 * cs[4 + i] + a1 * sn[4 + i]);
+              z[i] = pack_io2<F16>(a1 * cs[NW + i] - b1 * sn[NW + i], b1 * cs[NW + i] + a1 * sn[NW + i]);
             } else {
               const float a0 = io_lo<F16>(a[i]), a1 = io_hi<F16>(a[i]);
               const float b0 = io_lo<F16>(z[i]), b1 = io_hi<F16>(z[i]);
@@ -151,14 +178,14 @@ __global__ void __launch_bounds__(THREADS) rope_vec(const RopeParams p, int head
             }
           }
         }
-        *reinterpret_cast<uint4*>(y + c0) = u[j];
-        *reinterpret_cast<uint4*>(y + c1) = w[j];
+        st_piece<VW>(y + c0, u[j]);
+        if (two) st_piece<VW>(y + c1, w[j]);
       }
     }
   }
 }
 
-// Any even rot, any D and any alignment: one pair (or two pass-through columns) a
+// Any even rot, odd D and odd alignments: one pair (or two pass-through columns) a
 // thread, element loads.
 template <bool F16>
 __global__ void __launch_bounds__(THREADS) rope_pairs(const RopeParams p, int interleaved, int heads,
@@ -204,16 +231,28 @@ __global__ void __launch_bounds__(THREADS) rope_pairs(const RopeParams p, int in
   }
 }
 
-// Whether every row of the tensor starts on a 16-byte boundary.
-bool rows_aligned16(const void* base, const long long (&st)[3]) {
-  return reinterpret_cast<uintptr_t>(base) % 16 == 0 && st[0] % 8 == 0 && st[1] % 8 == 0 && st[2] % 8 == 0;
+// The largest piece (8, 4 or 2 columns) that every row of the tensor is aligned to; 0: none.
+int piece_of(const void* base, const long long (&st)[3]) {
+  for (int vw = 8; vw >= 2; vw /= 2)
+    if (reinterpret_cast<uintptr_t>(base) % (2 * vw) == 0 && st[0] % vw == 0 && st[1] % vw == 0 && st[2] % vw == 0)
+      return vw;
+  return 0;
+}
+
+template <bool F16, bool INTER>
+void launch_vec(const RopeParams& p, int vw, int heads, long long items, dim3 grid, cudaStream_t s) {
+  if (vw == 8) rope_vec<F16, INTER, 8><<<grid, THREADS, 0, s>>>(p, heads, items);
+  else if (vw == 4) rope_vec<F16, INTER, 4><<<grid, THREADS, 0, s>>>(p, heads, items);
+  else rope_vec<F16, INTER, 2><<<grid, THREADS, 0, s>>>(p, heads, items);
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream, int num_sms) {
   RopeParams p{};
-  bool vec = a.D % 16 == 0 && a.rot % 16 == 0;
+  int vw = 8;  // columns of a piece: 8, 4 or 2; 0: pair by pair
+  while (vw > 1 && (a.rot % (2 * vw) != 0 || a.D % vw != 0)) vw /= 2;
+  if (vw == 1) vw = 0;
   for (int i = 0; i < 2; ++i) {
     RopeTensor& t = p.t[i];
     t.H = a.H[i];
@@ -224,7 +263,7 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream, int num_sms) {
       t.xs[j] = a.xs[3 * i + j];
       t.ys[j] = a.ys[3 * i + j];
     }
-    vec = vec && rows_aligned16(t.x, t.xs) && rows_aligned16(t.y, t.ys);
+    for (const int fit : {piece_of(t.x, t.xs), piece_of(t.y, t.ys)}) vw = fit < vw ? fit : vw;
   }
   p.freq = a.freq;
   p.positions = a.positions;
@@ -238,22 +277,22 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream, int num_sms) {
   p.mult = a.mult;
   const int H = a.H[0] + a.H[1];
   const long long tokens = (long long)a.B * a.S;
-  const long long items = tokens * (vec ? a.D / 16 : a.rot / 2 + (a.D - a.rot + 1) / 2);
+  const long long items = tokens * (vw ? (a.D + 2 * vw - 1) / (2 * vw) : a.rot / 2 + (a.D - a.rot + 1) / 2);
   const long long blocks = (items + THREADS - 1) / THREADS;
   // Heads a thread walks, sharing its sines and cosines: 8 (rope_batch 53.4 us, against
   // 58.1 with 4 and 80.4 with 2), but 2 where 8 leave SMs without a block, a short call's
   // time being that of one thread (16 tokens of 40 heads 3.3 us in a graph, against 5.0).
   const int heads = blocks * ceil_div(H, 8) < num_sms ? 2 : 8;
   const dim3 grid((unsigned)(blocks < num_sms * 64ll ? blocks : num_sms * 64ll), (unsigned)ceil_div(H, heads));
-  if (!vec) {
+  if (vw == 0) {
     if (a.f16) rope_pairs<true><<<grid, THREADS, 0, stream>>>(p, a.interleaved, heads, items);
     else rope_pairs<false><<<grid, THREADS, 0, stream>>>(p, a.interleaved, heads, items);
   } else if (a.f16) {
-    if (a.interleaved) rope_vec<true, true, 4><<<grid, THREADS, 0, stream>>>(p, heads, items);
-    else rope_vec<true, false, 4><<<grid, THREADS, 0, stream>>>(p, heads, items);
+    if (a.interleaved) launch_vec<true, true>(p, vw, heads, items, grid, stream);
+    else launch_vec<true, false>(p, vw, heads, items, grid, stream);
   } else {
-    if (a.interleaved) rope_vec<false, true, 4><<<grid, THREADS, 0, stream>>>(p, heads, items);
-    else rope_vec<false, false, 4><<<grid, THREADS, 0, stream>>>(p, heads, items);
+    if (a.interleaved) launch_vec<false, true>(p, vw, heads, items, grid, stream);
+    else launch_vec<false, false>(p, vw, heads, items, grid, stream);
   }
   return cudaGetLastError();
 }

@@ -394,9 +394,9 @@ int sdpa_bwd_scored(int io_dtype, const void* q, const void* k, const void* v, c
  * map, which takes the gradient of the outputs to the gradient of the inputs.
  * Scalings for long contexts are frequencies (and mult): the caller's inv_freq.
  *   q, k, q_out, k_out  device 16-bit tensors of H_q and H_kv heads, any strides of batch,
- *               head and position, columns contiguous; 2-byte aligned (16-byte loads are
- *               used when D and rot_dim are multiples of 16 and every row of every tensor
- *               is 16-byte aligned). H_kv = 0: q alone. An output may be its own input
+ *               head and position, columns contiguous; 2-byte aligned (16-byte accesses
+ *               where rot_dim is a multiple of 16, D of 8 and every row of every
+ *               tensor 16-byte aligned; else 8- or 4-byte ones, or single elements). H_kv = 0: q alone. An output may be its own input
  *               (same pointer and strides); any other overlap is undefined.
  *   strides     host array of 12: batch, head, position strides in elements of q, q_out, k,
  *               k_out in this order. Input strides must not be negative; output rows must
@@ -407,6 +407,7 @@ int sdpa_bwd_scored(int io_dtype, const void* q, const void* k, const void* v, c
  *   positions   device int32 (S,), or with positions_per_batch (B, S), of any sign; NULL:
  *               offset + s.
  *   offset      first position when positions is NULL (>= 0, offset + S <= 2^31).
+ * S = 0 returns SDPA_OK without work.
  * Angles are exact products of 64-bit fractions of a turn, at every position.
  * Returns SDPA_ERR_INVALID, SDPA_ERR_UNSUPPORTED (rot_dim above 512) or SDPA_ERR_ALIGN
  * before anything is enqueued on `stream`.

@@ -49,7 +49,8 @@ def _close(name, got, x, f, pos, mult, interleaved, inverse):
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("inverse", [False, True])
 @pytest.mark.parametrize("D,rot", [(128, 128), (128, 64), (64, 16), (80, 32), (80, 48), (256, 256), (72, 72), (64, 20),
-                                   (8, 2), (9, 4), (33, 32), (512, 512)])
+                                   (8, 2), (9, 4), (33, 32), (512, 512), (80, 20), (80, 40), (96, 24), (96, 48),
+                                   (88, 80), (10, 4)])
 def test_rotation(io, interleaved, inverse, D, rot):
     sdpa = _sdpa()
     B, Hq, Hkv, S = 2, 6, 3, 37
@@ -139,6 +140,32 @@ def test_strides_and_in_place(D, rot):
     _close("odd", sdpa.rope_fwd(odd, None, f)[0], odd, f, pos, 1.0, False, False)
     wide = torch.randn(B, 1, S, D, generator=g).bfloat16().cuda().expand(B, 3, S, D)
     _close("broadcast", sdpa.rope_fwd(wide, None, f)[0], wide, f, pos, 1.0, False, False)
+
+
+@pytest.mark.parametrize("shift", [1, 2, 4])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_rows_off_their_alignment(shift, interleaved):
+    """Rows that start 2, 4 or 8 bytes past a 16-byte boundary, in or out."""
+    sdpa = _sdpa()
+    B, H, S, D = 2, 3, 33, 64
+    g = torch.Generator().manual_seed(shift)
+    f = sdpa.rope_inv_freq(32)
+    pos = torch.arange(S).expand(B, S)
+    x = torch.randn(B, H, S, D + 8, generator=g).half().cuda()[..., shift:shift + D]
+    _close("in", sdpa.rope_fwd(x, None, f, interleaved=interleaved)[0], x, f, pos, 1.0, interleaved, False)
+    room = torch.full((B, H, S, D + 8), math.nan, dtype=torch.half, device="cuda")
+    y = room[..., shift:shift + D]
+    sdpa.rope_fwd(x.contiguous(), None, f, interleaved=interleaved, q_out=y)
+    _close("out", y, x, f, pos, 1.0, interleaved, False)
+    assert torch.isnan(room[..., :shift]).all() and torch.isnan(room[..., shift + D:]).all()
+
+
+def test_no_rows():
+    sdpa = _sdpa()
+    f = sdpa.rope_inv_freq(64)
+    q = torch.zeros(2, 4, 0, 64, dtype=torch.bfloat16, device="cuda")
+    yq, yk = sdpa.rope_fwd(q, q[:, :2], f)
+    assert yq.shape == q.shape and yk.shape == (2, 2, 0, 64)
 
 
 def test_gradient_is_the_transposed_map():

@@ -249,6 +249,27 @@ def test_plan_ranges(B, S, prefix):
     assert prefix == "row" or k_exact.all()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_sink_gradient(D):
+    """dsink = -sum exp(sink - LSE) delta over the live rows, within 2^-16 of the terms'
+    magnitudes: an fp32 dot of D terms (D 2^-24 <= 2^-16), an exponent of about 20 in
+    fp32 (20 2^-24 ln 2) and a sum of a few hundred terms."""
+    sdpa = _sdpa()
+    B, H, S = 2, 4, 130
+    c = Case(B, H, 2, S, S, D, D, seed=12, softcap=9.0, slopes=[0.1, 0.0, 1.0, 0.02], sink=True, causal=True,
+             lens_q=[130, 50], lens_kv=[130, 90])
+    q, k, v, do = (t.cuda() for t in (c.q, c.k, c.v, c.do))
+    kw = _kw(c, None)
+    o, lse = sdpa.sdpa_fwd(q, k, v, **kw)
+    dsink = sdpa.sdpa_bwd(q, k, v, o, do, lse, **kw)[3]
+    delta = (do.double() * o.double()).sum(-1).cpu()
+    term = torch.exp(c.sink.double()[None, :, None] - lse.double().cpu()) * delta
+    size = torch.exp(c.sink.double()[None, :, None] - lse.double().cpu()) * (do.double() * o.double()).abs().sum(-1).cpu()
+    for b in range(B):
+        term[b, :, c.lens_q[b]:] = size[b, :, c.lens_q[b]:] = 0.0
+    assert ((dsink.double().cpu() + term.sum((0, 2))).abs() <= 2.0 ** -16 * size.sum((0, 2))).all()
+
+
 def test_repeated_calls_are_bitwise_equal():
     sdpa = _sdpa()
     B, S = 2, 700

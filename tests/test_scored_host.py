@@ -57,6 +57,7 @@ def test_refusals_of_the_scored_calls(lib):
     assert _fwd(lib, q=None) == INVALID and _fwd(lib, q=P + 8) == ALIGN
     assert _fwd(lib, Hkv=3) == INVALID
     assert _fwd(lib, Dqk=72, Dv=64) == UNSUPPORTED and _fwd(lib, Dqk=160, Dv=160) == UNSUPPORTED
+    assert _fwd(lib, plan=P, Skv=0) == INVALID and _fwd(lib, plan=P, Sq=0) == INVALID
     assert _bwd(lib, dsink=P) == INVALID                          # dsink without a sink
     # The ordered relay does not take a plan; the stored-dS route (D 128 and above) does.
     assert _bwd(lib, plan=P, det=1, D=64) == UNSUPPORTED
@@ -115,6 +116,7 @@ def test_rope_refusals(lib):
     assert _rope(lib, D=1024, rot=514) == UNSUPPORTED
     assert _rope(lib, mult=NAN) == INVALID and _rope(lib, mult=INF) == INVALID
     assert _rope(lib, Hq=0) == INVALID and _rope(lib, S=-1) == INVALID and _rope(lib, B=0) == INVALID
+    assert _rope(lib, S=0) == OK
     assert _rope(lib, q=P + 1) == ALIGN and _rope(lib, freq=P + 4) == ALIGN and _rope(lib, pos=P + 2) == ALIGN
     assert _rope(lib, offset=-1) == INVALID and _rope(lib, offset=(1 << 31) - 7) == INVALID
     assert _rope(lib, B=1 << 14, S=1 << 14, Hq=8) == INVALID      # 2^31 rows or more
