@@ -79,7 +79,8 @@ struct Layout {
   static constexpr int TILE_K = BK * DQK * 2;
   static constexpr int TILE_V = BK * DV * 2;
   static constexpr int STAGE = TILE_K + TILE_V;
-  static constexpr int NS_FIT = (232448 - TILE_Q - NUM_BARS * 8 - 2 * 256 * 4 - 64 - (RING + 2) * MSG_INTS * 4) / STAGE;
+  static constexpr int NS_FIT = (232448 - TILE_Q - NUM_BARS * 8 - 2 * 256 * 4 - 64 -
+                                 (RING + 2) * (int)sizeof(FwdItemMsg)) / STAGE;
   static constexpr int NS = NS_FIT > 4 ? 4 : NS_FIT;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = TILE_Q;
@@ -88,7 +89,7 @@ struct Layout {
   static constexpr int OFF_MISC = OFF_XCH + 2 * 256 * 4;
   // More than half an SM's shared memory keeps one CTA per SM, so the 512
   // tensor-memory columns are never contended.
-  static constexpr int BYTES_RAW = OFF_MISC + 64 + (RING + 2) * MSG_INTS * 4;
+  static constexpr int BYTES_RAW = OFF_MISC + 64 + (RING + 2) * (int)sizeof(FwdItemMsg);
   static constexpr int BYTES = BYTES_RAW > 120 * 1024 ? BYTES_RAW : 120 * 1024;
   // Two O accumulators, one per half of the keys: O_h at COL_O + 128 h.
   static constexpr uint32_t COL_O = 128 * NSLOT;
@@ -136,8 +137,9 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
   volatile int* ring = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 16);  // [RING] items
   volatile int* sitem = ring + RING;  // [2] the softmax warpgroups' current item, by parity
   // MOD: the same two as messages with the items' bounds.
-  volatile int* ring_msg = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 64);
-  volatile int* smsg = ring_msg + RING * MSG_INTS;
+  FwdItemMsg* ring_msg = reinterpret_cast<FwdItemMsg*>(smem + L::OFF_MISC + 64);
+  FwdItemMsg* smsg = ring_msg + RING;
+  static_assert((L::OFF_MISC + 64) % 16 == 0, "messages are 16-byte words");
   const int n_items = p.n_qt * p.B * p.Hq;
   // Items a CTA walks at most: one without PERSIST, so that the compiler sees
   // a single pass and keeps no state across items.
@@ -159,16 +161,16 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
   };
 
   auto next_msg = [&](int e) -> FwdItemMsg {  // MOD
-    FwdItemMsg m{-1, 0, 0, 0, 0};
+    FwdItemMsg m{make_int4(-1, 0, 0, 0), make_int4(0, 0, 0, 0)};
     if (lane == 0) {
       const int r = e % RING;
       if (mbar_wait(&bars[BAR_RFULL + r], (e / RING) & 1, abort_flag, WAIT_LIMIT_NS)) {
-        m = get_msg(ring_msg + r * MSG_INTS);
+        m = get_msg(ring_msg + r);
         mbar_arrive(&bars[BAR_REMPTY + r]);
       }
     }
-    m.it = __shfl_sync(0xffffffffu, m.it, 0);
-    m.n = __shfl_sync(0xffffffffu, m.n, 0);  // (the issuers need no more; lane 0 has the rest)
+    m.id.x = __shfl_sync(0xffffffffu, m.id.x, 0);
+    m.bounds.y = __shfl_sync(0xffffffffu, m.bounds.y, 0);  // (the issuers need no more; lane 0 has the rest)
     return m;
   };
 
@@ -231,12 +233,12 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
             it = atomicAdd(&g_fwd_ticket[ticket_slot], 1);
             if (it >= n_items) it = -1;
             if constexpr (MOD) {
-              FwdItemMsg m{it, 0, 0, 0, 0};
+              FwdItemMsg m{make_int4(-1, 0, 0, 0), make_int4(0, 0, 0, 0)};
               if (it >= 0) {
                 w = fwd_item<MOD>(p, it);
-                m = FwdItemMsg{it, w.kt_lo, w.n, w.Lq, w.Lk};
+                m = FwdItemMsg{make_int4(it, w.qt, w.bh / p.Hq, w.h), make_int4(w.kt_lo, w.n, w.Lq, w.Lk)};
               }
-              put_msg(ring_msg + r * MSG_INTS, m);
+              put_msg(ring_msg + r, m);
             } else {
               ring[r] = it;
             }
@@ -279,8 +281,8 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         FwdItem w;
         if constexpr (MOD) {
           const FwdItemMsg m = next_msg(e);
-          if (m.it < 0) break;
-          w.n = m.n;
+          if (m.id.x < 0) break;
+          w.n = m.bounds.y;
         } else {
           const int it = next_item(e);
           if (it < 0) break;
@@ -377,11 +379,11 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
     ModRowLoads next_loads{};
     auto take_next = [&](int e) {
       if constexpr (MOD) {
-        const FwdItemMsg t = get_msg(smsg + (e & 1) * MSG_INTS);
-        next_it = t.it;
-        if (t.it < 0) return;
+        const FwdItemMsg t = get_msg(smsg + (e & 1));
+        next_it = t.id.x;
+        if (t.id.x < 0) return;
         next_w = fwd_item(p, t);
-        next_loads = mod_row_loads(p, next_w, next_w.q0 + row);
+        next_loads = mod_row_loads(p, next_w, t.id.z, next_w.q0 + row);
       }
     };
     for (int e = 0; e < E_MAX && ok; ++e) {
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         if (!have_next) {
           if (warp == 0) {
             const FwdItemMsg t = next_msg(e);
-            if (lane == 0) put_msg(smsg + (e & 1) * MSG_INTS, t);
+            if (lane == 0) put_msg(smsg + (e & 1), t);
           }
           named_bar_sync(3, 256);
           take_next(e);
@@ -609,7 +611,7 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         if (warp == 0) {
           if constexpr (MOD) {
             const FwdItemMsg t = next_msg(e + 1);
-            if (lane == 0) put_msg(smsg + ((e + 1) & 1) * MSG_INTS, t);
+            if (lane == 0) put_msg(smsg + ((e + 1) & 1), t);
           } else {
             const int t = next_item(e + 1);
             if (lane == 0) sitem[(e + 1) & 1] = t;
@@ -632,7 +634,7 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
       const float f0 = a0 * inv_l, f1 = a1 * inv_l;
       uint16_t* const orow_ptr = o_base + orow * p.Dv;
       const bool row_ok = q < p.Sq && in_bounds(p.status, orow_ptr, (size_t)p.Dv * 2, p.o, o_bytes);
-#pragma unroll 1
+#pragma unroll (MOD ? 2 : 1)
       for (int c32 = 0; c32 < DV / 64; ++c32) {
         const int cbase = half * (DV / 2) + c32 * 32;  // first O column of this chunk
         uint32_t o0[32], o1[32];

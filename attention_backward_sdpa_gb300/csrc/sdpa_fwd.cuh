@@ -407,35 +407,42 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int it) {
   return fwd_item<MOD>(p, it, fwd_item_loads<MOD>(p, it));
 }
 
-// An item as the producer publishes it under modified scores, with the bounds that it has
-// read already, so that no other role waits for memory to know its item.
+// An item as the producer publishes it under modified scores, decoded and with the bounds
+// that it has read, so that no other role divides indexes or waits for memory to know its
+// item: two 16-byte words.
 struct FwdItemMsg {
-  int it, kt_lo, n, Lq, Lk;
+  int4 id;      // item (-1: the end), query tile, batch row, head
+  int4 bounds;  // first key tile, number of them, L_q, L_k
 };
-constexpr int MSG_INTS = 5;
-__device__ __forceinline__ void put_msg(volatile int* at, const FwdItemMsg& m) {
-  at[0] = m.it;
-  at[1] = m.kt_lo;
-  at[2] = m.n;
-  at[3] = m.Lq;
-  at[4] = m.Lk;
+__device__ __forceinline__ int4 ld_shared_16b(const void* p) {
+  int4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(smem_u32(p)) : "memory");
+  return v;
 }
-__device__ __forceinline__ FwdItemMsg get_msg(const volatile int* at) {
-  return FwdItemMsg{at[0], at[1], at[2], at[3], at[4]};
+__device__ __forceinline__ void st_shared_16b(void* p, const int4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(smem_u32(p)), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void put_msg(FwdItemMsg* at, const FwdItemMsg& m) {
+  st_shared_16b(&at->id, m.id);
+  st_shared_16b(&at->bounds, m.bounds);
+}
+__device__ __forceinline__ FwdItemMsg get_msg(const FwdItemMsg* at) {
+  return FwdItemMsg{ld_shared_16b(&at->id), ld_shared_16b(&at->bounds)};
 }
 __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, const FwdItemMsg& m) {
   FwdItem w;
-  const int BH = p.B * p.Hq;
-  w.qt = p.n_qt - 1 - m.it / BH;
-  w.bh = m.it % BH;
-  w.h = w.bh % p.Hq;
-  w.kvh = w.bh / p.Hq * p.Hkv + w.h / p.G;
+  w.qt = m.id.y;
+  w.h = m.id.w;
+  w.bh = m.id.z * p.Hq + w.h;
+  w.kvh = 0;  // (the producer's alone)
   w.q0 = w.qt * fwd_shared::BM;
-  w.Lq = m.Lq;
-  w.Lk = m.Lk;
-  w.diag = p.bottom_right ? (long long)m.Lk - m.Lq : 0;
-  w.kt_lo = m.kt_lo;
-  w.n = m.n;
+  w.Lq = m.bounds.z;
+  w.Lk = m.bounds.w;
+  w.diag = p.bottom_right ? (long long)w.Lk - w.Lq : 0;
+  w.kt_lo = m.bounds.x;
+  w.n = m.bounds.y;
   return w;
 }
 
@@ -444,11 +451,11 @@ struct ModRowLoads {
   int2 range;
   float slope, sink;
 };
-__device__ __forceinline__ ModRowLoads mod_row_loads(const FwdParams& p, const FwdItem& w, int q) {
+__device__ __forceinline__ ModRowLoads mod_row_loads(const FwdParams& p, const FwdItem& w, int b, int q) {
   ModRowLoads l;
   l.range = make_int2(0, p.Skv);
   if (p.mods.ranges != nullptr && q < p.Sq)
-    l.range = p.mods.ranges[(long long)(w.bh / p.Hq) * ceil_div(p.Sq, BQ) * BQ + q];
+    l.range = p.mods.ranges[(long long)b * ceil_div(p.Sq, BQ) * BQ + q];
   l.slope = p.mods.slopes != nullptr ? p.mods.slopes[w.h] : 0.f;
   l.sink = p.sink != nullptr ? p.sink[w.h] : 0.f;
   return l;

@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(fwd_wide::THREADS, 1)
       const long long k_vis_hi = p.causal ? (long long)q + w.diag + Rp : (1ll << 40);
       const long long k_vis_lo = has_window ? (long long)q + w.diag - p.window_left : -(1ll << 40);
       ModRow mr;
-      if constexpr (MOD) mr = mod_row(p, w, q, live, mod_row_loads(p, w, q));
+      if constexpr (MOD) mr = mod_row(p, w, q, live, mod_row_loads(p, w, w.bh / p.Hq, q));
       const long long bias_row =
           BIAS ? (long long)(w.bh / p.Hq) * p.bias_bstride + ((long long)w.h * p.Sq + q) * p.Skv : 0;
       for (int j = 0; j < w.n; ++j, ++g) {
