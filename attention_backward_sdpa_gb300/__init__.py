@@ -228,6 +228,8 @@ def _check_launch_device(ref: torch.Tensor) -> None:
                          f"cuda:{torch.cuda.current_device()}: call under torch.cuda.device({ref.device})")
 
 
+_INT32 = 1 << 31  # (ctypes would take a larger int modulo 2^32)
+
 # io element types of the C ABI (sdpa_dtype) for the typed entry points.
 _IO_CODES = {torch.bfloat16: 0, torch.float16: 2}
 
@@ -303,7 +305,7 @@ def sdpa_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
                            seq_kv_lens=seq_kv_lens, dq=dq, dk=dk, dv=dv, workspace=workspace,
                            sink=sink, dsink=dsink if sink is not None else None, bias=bias,
                            dbias=dbias if bias is not None and bias_grad else None)
-    scored = _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias)
+    scored = _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias, window_left, window_right)
     _check_launch_device(q)
     sc = 0.0 if scale is None else float(scale)
     if scored:
@@ -433,6 +435,8 @@ def mask_plan(B: int, Sq: int, Skv: int, *, doc_ids: Optional[torch.Tensor] = No
     """
     lib = load()
     B, Sq, Skv = int(B), int(Sq), int(Skv)
+    if not all(0 < n < _INT32 for n in (B, Sq, Skv)):
+        raise ValueError("B, Sq and Skv must be positive 32-bit sizes")
     rows = row_lo is not None or row_hi is not None
     if rows and (row_lo is None or row_hi is None or doc_ids is not None or prefix_lens is not None or causal):
         raise ValueError("row_lo and row_hi come together, without doc_ids, prefix_lens or causal")
@@ -467,7 +471,7 @@ def mask_plan(B: int, Sq: int, Skv: int, *, doc_ids: Optional[torch.Tensor] = No
     return plan
 
 
-def _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias) -> bool:
+def _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias, window_left, window_right) -> bool:
     """Whether the call modifies its scores (and then that it may)."""
     if not 0.0 <= softcap < math.inf:
         raise ValueError("softcap must be 0 (none) or a positive finite number")
@@ -475,6 +479,8 @@ def _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias)
         return False
     if bias is not None:
         raise ValueError("softcap, alibi_slopes and mask_plan do not combine with bias")
+    if not (-_INT32 <= window_left < _INT32 and -_INT32 <= window_right < _INT32):
+        raise ValueError("window_left and window_right are 32-bit numbers of keys")
     if alibi_slopes is not None and (
             not isinstance(alibi_slopes, torch.Tensor) or alibi_slopes.dtype != torch.float32
             or not alibi_slopes.is_cuda or not alibi_slopes.is_contiguous() or tuple(alibi_slopes.shape) != (Hq,)):
@@ -604,6 +610,8 @@ def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, 
         if k is not None:
             sk, sl, Hkv = k.stride(), k_out.stride(), k.shape[1]
     _check_launch_device(q)
+    if not 0 <= offset <= _INT32 - S:
+        raise ValueError("offset must be at least 0, and offset + S at most 2^31")
     if B > 0 and Hq > 0:
         rc = lib.sdpa_rope(_IO_CODES[q.dtype], q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out), B, Hq, Hkv, S, D,
                            _Strides(sq[0], sq[1], sq[2], so[0], so[1], so[2], sk[0], sk[1], sk[2], sl[0], sl[1], sl[2]),
@@ -686,7 +694,7 @@ def sdpa_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale: Option
         _check_lse(lse, B, Hq, Sq)
         _check_same_device(q, k=k, v=v, o=o, lse=lse, seq_q_lens=seq_q_lens, seq_kv_lens=seq_kv_lens,
                            sink=sink, bias=bias)
-    scored = _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias)
+    scored = _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias, window_left, window_right)
     _check_launch_device(q)
     sc = 0.0 if scale is None else float(scale)
     if scored:

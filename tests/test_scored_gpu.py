@@ -331,3 +331,60 @@ def test_a_plan_may_be_written_again():
     assert again is plan and not torch.equal(before, plan.buffer)
     case = Case(1, 2, 2, S, S, 64, 64, seed=11, rows=doc_ranges(ids.tolist(), None, True, S))
     _check(case, plan)
+
+
+def test_a_long_row_of_documents():
+    """66,000 positions in one row: the documents' results are those of each document alone
+    (its own rows, keys and distances), within the bounds of the document alone."""
+    sdpa = _sdpa()
+    S, H, D = 66000, 2, 64
+    cuts = [0, 300, 40000, 65409, 65600, S]
+    ids = torch.zeros(1, S, dtype=torch.int32)
+    for c in cuts[1:-1]:
+        ids[0, c:] += 1
+    g = torch.Generator().manual_seed(31)
+    q, k, v, do = (torch.randn(1, H, S, D, generator=g).bfloat16() for _ in range(4))
+    slopes = [0.02, 0.3]
+    plan = sdpa.mask_plan(1, S, S, doc_ids=ids.cuda(), causal=True)
+    kw = dict(softcap=20.0, alibi_slopes=torch.tensor(slopes).cuda(), mask_plan=plan)
+    dev = [t.cuda() for t in (q, k, v, do)]
+    o, lse = sdpa.sdpa_fwd(*dev[:3], **kw)
+    got = sdpa.sdpa_bwd(*dev[:3], o, dev[3], lse, **kw)
+    sdpa.check_device_status()
+    for a, b in ((0, 300), (65409, 65600), (65600, S)):
+        one = Case(1, H, H, b - a, b - a, D, D, softcap=20.0, slopes=slopes, causal=True)
+        one.q, one.k, one.v, one.do = (t[:, :, a:b] for t in (q, k, v, do))
+        ro, rl, bo, bl = one.forward()
+        assert_within("o", o[:, :, a:b], ro, bo)
+        assert_within("lse", lse[:, :, a:b], rl, bl)
+        ref, bounds = one.backward(o[:, :, a:b].cpu(), lse[:, :, a:b].cpu())
+        for name, t, r, bound in zip(("dq", "dk", "dv"), got, ref, bounds):
+            assert_within(f"{name} of [{a}, {b})", t[:, :, a:b], r, bound)
+
+
+@pytest.mark.parametrize("det", [False, True])
+def test_a_workspace_of_the_exact_size_and_a_given_stream(det):
+    sdpa = _sdpa()
+    B, Hq, Hkv, S, D = 2, 6, 2, 200, 128
+    c = Case(B, Hq, Hkv, S, S, D, D, seed=13, softcap=7.0, causal=True)
+    q, k, v, do = (t.cuda() for t in (c.q, c.k, c.v, c.do))
+    o, lse = sdpa.sdpa_fwd(q, k, v, softcap=7.0, causal=True)
+    want = sdpa.sdpa_bwd(q, k, v, o, do, lse, softcap=7.0, causal=True, deterministic=True)
+    n = sdpa.workspace_size(B, Hq, Hkv, S, S, D, D, det, causal=True, scored=True)
+    room = torch.full((n + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+    got = sdpa.sdpa_bwd(q, k, v, o, do, lse, softcap=7.0, causal=True, deterministic=det, workspace=room[:n])
+    assert (room[n:] == 0x5A).all()
+    ref, bounds = c.backward(o.cpu(), lse.cpu())
+    for g, w, r, b in zip(got, want, ref, bounds):
+        assert_within("workspace", g, r, b)
+        assert not det or torch.equal(g, w)
+    with pytest.raises(sdpa.SdpaError):
+        sdpa.sdpa_bwd(q, k, v, o, do, lse, softcap=7.0, causal=True, deterministic=det, workspace=room[:n - 256])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o2, lse2 = sdpa.sdpa_fwd(q, k, v, softcap=7.0, causal=True, stream=side)
+    other = sdpa.sdpa_bwd(q, k, v, o2, do, lse2, softcap=7.0, causal=True, deterministic=True, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    for a, b in zip(other, want):
+        assert torch.equal(a, b)

@@ -163,7 +163,8 @@ def test_scored_argument_checks(fake):  # noqa: F811
                     (dict(alibi_slopes=torch.zeros(4, dtype=torch.float64)), ValueError),
                     (dict(alibi_slopes=torch.zeros(8)[::2]), ValueError), (dict(alibi_slopes=[1.0] * 4), ValueError),
                     (dict(mask_plan=plan), ValueError), (dict(mask_plan=torch.zeros(8)), TypeError),
-                    (dict(softcap=2.0, bias=bias), ValueError)):
+                    (dict(softcap=2.0, bias=bias), ValueError), (dict(softcap=2.0, window_left=1 << 32), ValueError),
+                    (dict(softcap=2.0, causal=True, window_right=1 << 31), ValueError)):
         with pytest.raises(err):
             pkg.sdpa_fwd(q, k, v, **kw)
         with pytest.raises(err):
@@ -180,6 +181,9 @@ def test_mask_plan_argument_checks(fake):  # noqa: F811
                dict(row_lo=ids.t().contiguous().t(), row_hi=ids)):
         with pytest.raises(ValueError):
             pkg.mask_plan(2, 96, kw.pop("Skv", 96), **kw)
+    for sizes in ((0, 96, 96), (2, -1, -1), ((1 << 32) + 1, 96, 96), (1, 1 << 31, 1 << 31)):
+        with pytest.raises(ValueError):
+            pkg.mask_plan(*sizes, causal=True)
     assert not [c for c in fake.calls if c[0] != "sdpa_mask_plan_size"]
 
 
@@ -200,6 +204,7 @@ def test_rope_argument_checks(fake):  # noqa: F811
                   ((q, k[:1], f), {}), ((q, k[:, :, :15], f), {}), ((q[0], k, f), {}), ((q, k[0], f), {}),
                   ((q.transpose(2, 3), None, f[:8]), {}), ((q, k, f), dict(positions=pos.long())),
                   ((q, k, f), dict(positions=pos[:, :15])), ((q, k, f), dict(positions=pos, offset=3)),
+                  ((q, k, f), dict(offset=-1)), ((q, k, f), dict(offset=(1 << 31) - 15)), ((q, k, f), dict(offset=1 << 32)),
                   ((q, None, f), dict(k_out=k)), ((q, k, f), dict(q_out=k)), ((q, k, f), dict(q_out=q.half()))):
         with pytest.raises((ValueError, TypeError)):
             pkg.rope_fwd(*a, **kw)
