@@ -134,6 +134,9 @@ class Case:
                 bo[b, h] = self.u * 1.01 * (a + o[b, h].abs()) + 2 * e * a + 1e-30
                 # an fp16 weight relative to the running reference (at most 2^8 above it)
                 bo[b, h] += sub * 256 * v.abs().sum(0)
+                # O itself below 2^-14 is rounded to multiples of 2^-24: half a step is 2^-25, for
+                # O = 8.0993e-9 (0.136 steps) rounded to 0 more than the relative terms above allow
+                bo[b, h] += sub
                 fin = torch.nan_to_num(lse[b, h], neginf=0.0).abs()
                 bl[b, h] = e + 4 * G23 * (1 + fin)
         return o, lse, bo, bl

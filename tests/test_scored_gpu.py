@@ -388,3 +388,9 @@ def test_a_workspace_of_the_exact_size_and_a_given_stream(det):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
     for a, b in zip(other, want):
         assert torch.equal(a, b)
+
+
+def test_outputs_below_fp16_normals():
+    """A sink that takes nearly all of the weight: outputs down to 1e-9, fp16 subnormals and zeros."""
+    _check(Case(2, 3, 3, 1, 1, 80, 80, io=torch.float16, seed=2587, gain=15.0, sink=True, causal=True,
+                bottom_right=True, window_left=0, slopes=[0.5, 0.0, 2.0]), deterministic=(False, True))
