@@ -190,7 +190,8 @@ __device__ __forceinline__ ModTile mod_tile(const ChainParams& p, const ModKey& 
   const int q0 = qt * BQ;
   m.slope2 = slope2;
   m.dist = (float)(q0 + diag - key.k);
-  m.ahead = slope2 == 0.f || q0 + diag >= key.k_last;
+  m.ahead[0] = slope2 == 0.f || q0 + diag >= key.k_last;
+  m.ahead[1] = slope2 == 0.f || q0 + 32 + diag >= key.k_last;
   const int2* ranges = nullptr;
   if (key.row_ranges) {
     const int4 s = p.mods.q_sum[(long long)b * p.n_qt + qt];

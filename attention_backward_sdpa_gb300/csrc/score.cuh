@@ -166,7 +166,7 @@ struct ModTile {
   float dist;          // q0 + diag - k: the distance of row i is |dist + i|
   uint32_t see[2];     // by halves of 32 rows: bit i set when row i sees the key
   bool full[2];        // uniform across the warp: all the half's rows see all its keys
-  bool ahead;          // every row of the tile is at or past the warp's keys: no |.| needed
+  bool ahead[2];       // all the half's rows are at or past the warp's keys: no |.| needed
 };
 
 // The call's scaling: c2 = log2(e) times the cap, or times the scale, in pairs (the exponent
@@ -180,39 +180,43 @@ __device__ __forceinline__ ModCap mod_cap(const ScoreMods& m, float scale_log2) 
   return ModCap{f2_pack(c, c), m.cap_in, m.cap_small};
 }
 
-// Whether a tile takes the straight pass below: no mask, no |.| and, with a cap, every
-// score within the polynomial (one vote over the 64 scores). `small`: the last alone.
-template <int MOD>
-__device__ __forceinline__ bool mod_replay_straight(const ModTile& m, const ModCap& cap, const uint32_t (&ra)[32],
-                                                    const uint32_t (&rb)[32], bool& small) {
-  small = true;
-  if constexpr (MOD == MOD_CAP) {
-    float big[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      big[(i >> 1) & 3] = max3(big[(i >> 1) & 3], fabsf(__uint_as_float(ra[i])), fabsf(__uint_as_float(ra[i + 1])));
-      big[4 + ((i >> 1) & 3)] =
-          max3(big[4 + ((i >> 1) & 3)], fabsf(__uint_as_float(rb[i])), fabsf(__uint_as_float(rb[i + 1])));
-    }
-    const float b0 = max3(big[0], big[1], big[2]), b1 = max3(big[3], big[4], big[5]);
-    small = __all_sync(0xffffffffu, max3(b0, b1, fmaxf(big[6], big[7])) <= cap.cap_small);
-  }
-  return small && m.full[0] && m.full[1] && m.ahead;
+// What half h (0, 1) of a tile looks like.
+struct ModHalf {
+  uint32_t see;
+  bool full, ahead;
+};
+__device__ __forceinline__ ModHalf mod_half(const ModTile& m, int h) {
+  return h ? ModHalf{m.see[1], m.full[1], m.ahead[1]} : ModHalf{m.see[0], m.full[0], m.ahead[0]};
 }
 
-// Half H (rows 32 H .. 32 H + 31) of a tile's replay. r: S^T on entry. P gets the
-// masked probabilities (with a cap times t^2 - 1), which is all that the dS step reads; w
-// the probabilities themselves as io pairs for the dV product. (The two are formed
-// together so that no thread holds 64 derivatives.) The straight pass, in which the
-// exponentials (a quarter of the FMA rate) run under the neighbouring pairs' polynomials:
-template <int MOD, bool F16, int H>
-__device__ __forceinline__ void mod_replay_fast(const ModTile& m, const CapCoef& coef, const ModCap& cap,
-                                                const float* n_lse, const uint32_t (&r)[32], uint64_t (&P)[32],
-                                                uint32_t (&w)[16]) {
-  const ulonglong2* l2 = reinterpret_cast<const ulonglong2*>(n_lse) + H * 8;  // two pairs a load
-  const float bias = -m.slope2 * m.dist;  // -slope2 (dist + i): the i part is in the row statistics
-  const uint64_t bias2 = f2_pack(bias, bias), minus_one = f2_pack(-1.f, -1.f);
-  uint64_t* const Ph = P + H * 16;
+// With a cap: whether all of the warp's scores r (32 rows of its keys) are within the polynomial.
+template <int N>
+__device__ __forceinline__ float mod_largest(const uint32_t (&r)[N]) {
+  float big[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < N; i += 2)
+    big[(i >> 1) & 3] = max3(big[(i >> 1) & 3], fabsf(__uint_as_float(r[i])), fabsf(__uint_as_float(r[i + 1])));
+  return fmaxf(max3(big[0], big[1], big[2]), big[3]);
+}
+__device__ __forceinline__ bool mod_small(const ModCap& cap, float largest) {
+  return __all_sync(0xffffffffu, largest <= cap.cap_small);
+}
+
+// Half h (rows 32 h .. 32 h + 31) of a tile's replay. r: S^T on entry. P gets the masked
+// probabilities (with a cap times t^2 - 1), which is all that the dS step reads; w the
+// probabilities themselves as io pairs for the dV product. (The two are formed together so
+// that no thread holds the derivatives too.)
+//
+// The straight pass, for a half without a mask or |.| and with mod_small(), in which the
+// exponentials (a quarter of the FMA rate) run under the neighbouring pairs' polynomials.
+template <int MOD, bool F16>
+__device__ __forceinline__ void mod_replay_straight(const ModTile& tile, int h, const CapCoef& coef, const ModCap& cap,
+                                                    const float* n_lse, const uint32_t (&r)[32], uint64_t (&P)[16],
+                                                    uint32_t (&w)[16]) {
+  const ulonglong2* l2 = reinterpret_cast<const ulonglong2*>(n_lse) + h * 8;  // two pairs a load
+  const uint64_t minus_one = f2_pack(-1.f, -1.f);
+  const float bias = -tile.slope2 * tile.dist;  // -slope2 (dist + i): the i part is in the row statistics
+  const uint64_t bias2 = f2_pack(bias, bias);
 #pragma unroll
   for (int blk = 0; blk < 16 / SIDE; ++blk) {
     uint64_t t[SIDE], x[SIDE];
@@ -241,19 +245,19 @@ __device__ __forceinline__ void mod_replay_fast(const ModTile& m, const CapCoef&
       float p0, p1;
       f2_unpack(x[i], p0, p1);
       w[blk * SIDE + i] = pack_io2<F16>(p0, p1);
-      Ph[blk * SIDE + i] = MOD == MOD_CAP ? f2_mul(x[i], t[i]) : x[i];
+      P[blk * SIDE + i] = MOD == MOD_CAP ? f2_mul(x[i], t[i]) : x[i];
     }
   }
 }
 
-// ... and the general one, step by step.
-template <int MOD, bool F16, int H>
-__device__ __forceinline__ void mod_replay_half(const ModTile& m, const CapCoef& coef, const ModCap& cap, bool small,
-                                                const float* n_lse, uint32_t (&r)[32], uint64_t (&P)[32],
-                                                uint32_t (&w)[16]) {
-  const ulonglong2* l2 = reinterpret_cast<const ulonglong2*>(n_lse) + H * 8;
+// ... and any other half, step by step.
+template <int MOD, bool F16>
+__device__ __forceinline__ void mod_replay_steps(const ModTile& tile, int h, bool small, const CapCoef& coef,
+                                                 const ModCap& cap, const float* n_lse, uint32_t (&r)[32],
+                                                 uint64_t (&P)[16], uint32_t (&w)[16]) {
+  const ModHalf m = mod_half(tile, h);
+  const ulonglong2* l2 = reinterpret_cast<const ulonglong2*>(n_lse) + h * 8;
   const uint64_t minus_one = f2_pack(-1.f, -1.f);
-  uint64_t* const Ph = P + H * 16;
   if constexpr (MOD == MOD_CAP) {
     // r becomes the tanh.
 #pragma unroll
@@ -275,36 +279,37 @@ __device__ __forceinline__ void mod_replay_half(const ModTile& m, const CapCoef&
 #pragma unroll
   for (int i4 = 0; i4 < 8; ++i4) {
     const ulonglong2 l = l2[i4];
-    Ph[2 * i4] = f2_fma(f2_pack(r[4 * i4], r[4 * i4 + 1]), cap.c2, l.x);
-    Ph[2 * i4 + 1] = f2_fma(f2_pack(r[4 * i4 + 2], r[4 * i4 + 3]), cap.c2, l.y);
+    P[2 * i4] = f2_fma(f2_pack(r[4 * i4], r[4 * i4 + 1]), cap.c2, l.x);
+    P[2 * i4 + 1] = f2_fma(f2_pack(r[4 * i4 + 2], r[4 * i4 + 3]), cap.c2, l.y);
   }
-  if (m.slope2 != 0.f) {
+  if (tile.slope2 != 0.f) {
     // -slope2 |dist + i| with the row statistics' -slope2 i taken back.
+    const float i0 = h ? 32.f : 0.f;
 #pragma unroll
     for (int i2 = 0; i2 < 16; ++i2) {
-      const float i = (float)(H * 32 + 2 * i2);
+      const float i = i0 + (float)(2 * i2);
       float x0, x1;
-      f2_unpack(Ph[i2], x0, x1);
-      x0 = fmaf(m.slope2, i - fabsf(m.dist + i), x0);
-      x1 = fmaf(m.slope2, (i + 1.f) - fabsf(m.dist + (i + 1.f)), x1);
-      Ph[i2] = f2_pack(x0, x1);
+      f2_unpack(P[i2], x0, x1);
+      x0 = fmaf(tile.slope2, i - fabsf(tile.dist + i), x0);
+      x1 = fmaf(tile.slope2, (i + 1.f) - fabsf(tile.dist + (i + 1.f)), x1);
+      P[i2] = f2_pack(x0, x1);
     }
   }
 #pragma unroll
   for (int i2 = 0; i2 < 16; ++i2) {
     float x0, x1;
-    f2_unpack(Ph[i2], x0, x1);
-    Ph[i2] = f2_pack(ex2_approx(x0), ex2_approx(x1));
+    f2_unpack(P[i2], x0, x1);
+    P[i2] = f2_pack(ex2_approx(x0), ex2_approx(x1));
   }
-  if (!m.full[H]) {
+  if (!m.full) {
     // (r as well with a cap: a masked score may be an overflow or NaN, and 0 times that is
     // NaN, so its tanh is taken as 0.)
 #pragma unroll
     for (int i2 = 0; i2 < 16; ++i2) {
-      const bool see0 = (m.see[H] >> (2 * i2)) & 1u, see1 = (m.see[H] >> (2 * i2 + 1)) & 1u;
+      const bool see0 = (m.see >> (2 * i2)) & 1u, see1 = (m.see >> (2 * i2 + 1)) & 1u;
       float p0, p1;
-      f2_unpack(Ph[i2], p0, p1);
-      Ph[i2] = f2_pack(see0 ? p0 : 0.f, see1 ? p1 : 0.f);
+      f2_unpack(P[i2], p0, p1);
+      P[i2] = f2_pack(see0 ? p0 : 0.f, see1 ? p1 : 0.f);
       if constexpr (MOD == MOD_CAP) {
         r[2 * i2] = see0 ? r[2 * i2] : 0u;
         r[2 * i2 + 1] = see1 ? r[2 * i2 + 1] : 0u;
@@ -314,22 +319,23 @@ __device__ __forceinline__ void mod_replay_half(const ModTile& m, const CapCoef&
 #pragma unroll
   for (int i2 = 0; i2 < 16; ++i2) {
     float p0, p1;
-    f2_unpack(Ph[i2], p0, p1);
+    f2_unpack(P[i2], p0, p1);
     w[i2] = pack_io2<F16>(p0, p1);
     if constexpr (MOD == MOD_CAP) {
       const uint64_t t = f2_pack(r[2 * i2], r[2 * i2 + 1]);
-      Ph[i2] = f2_mul(Ph[i2], f2_fma(t, t, minus_one));
+      P[i2] = f2_mul(P[i2], f2_fma(t, t, minus_one));
     }
   }
 }
 
-// dS of half H's 32 query rows as io pairs, P (dP - delta), into the thread's row of the dS^T
+// dS of half h's 32 query rows as io pairs, P (dP - delta), into the thread's row of the dS^T
 // tile (16-byte pieces, XOR-swizzled by the row's `sw`); r holds the half's dP^T.
-// CUT: some pairs are masked; theirs is 0, not 0 times a dP that may have overflowed.
-template <bool F16, bool CUT, int H>
-__device__ __forceinline__ void mod_ds_half(const ModTile& m, const uint64_t (&P)[32], const float* n_delta,
-                                            const uint32_t (&r)[32], uint8_t* ds_row, int sw) {
-  const ulonglong2* d2 = reinterpret_cast<const ulonglong2*>(n_delta) + H * 8;
+// CUT: some pairs are masked (not in `see`); theirs is 0, not 0 times a dP that may have
+// overflowed.
+template <bool F16, bool CUT>
+__device__ __forceinline__ void mod_ds_pieces(uint32_t see, int h, const uint64_t (&P)[16], const float* n_delta,
+                                              const uint32_t (&r)[32], uint8_t* ds_row, int sw) {
+  const ulonglong2* d2 = reinterpret_cast<const ulonglong2*>(n_delta) + h * 8;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const ulonglong2 da = d2[2 * c], db = d2[2 * c + 1];
@@ -339,14 +345,14 @@ __device__ __forceinline__ void mod_ds_half(const ModTile& m, const uint64_t (&P
     for (int e = 0; e < 4; ++e) {
       const int i = c * 8 + 2 * e;
       float s0, s1;
-      f2_unpack(f2_mul(P[H * 16 + c * 4 + e], f2_add(f2_pack(r[i], r[i + 1]), d[e])), s0, s1);
+      f2_unpack(f2_mul(P[c * 4 + e], f2_add(f2_pack(r[i], r[i + 1]), d[e])), s0, s1);
       if constexpr (CUT) {
-        s0 = (m.see[H] >> i) & 1u ? s0 : 0.f;
-        s1 = (m.see[H] >> (i + 1)) & 1u ? s1 : 0.f;
+        s0 = (see >> i) & 1u ? s0 : 0.f;
+        s1 = (see >> (i + 1)) & 1u ? s1 : 0.f;
       }
       w[e] = pack_io2<F16>(s0, s1);
     }
-    *reinterpret_cast<uint4*>(ds_row + (((H * 4 + c) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(ds_row + (((h * 4 + c) ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 

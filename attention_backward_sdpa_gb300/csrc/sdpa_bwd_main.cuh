@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
         __syncwarp();
         tc_fence_after();
         if (elect_one()) {
-#pragma unroll
+#pragma unroll (DS_OUT ? BQ / 16 : 1)
           for (int k = 0; k < BQ / 16; ++k)
             mma_ts(tmem + L::COL_DV, tmem + L::col_s(su) + 8 * k, sdesc_at(T_MN, aDO + k * 2048), ID_G3,
                    (u > 0 || k > 0));
@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
           tc_fence_after();
           if (elect_one()) {
             // G1: S^T[key, q] = sum_d K[key, d] Q[q, d]   (both K-major)
-#pragma unroll
+#pragma unroll (MOD && !DS_OUT ? 1 : D / 16)  // (rolled: see MOD_LOOP)
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t kk = (k >> 2) * L::BLK_KV + (k & 3) * 32;
               const uint32_t kq = (k >> 2) * L::BLK_Q + (k & 3) * 32;
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
           tc_fence_after();
           if (elect_one()) {
             // G2: dP^T[key, q] = sum_d V[key, d] dO[q, d]
-#pragma unroll
+#pragma unroll (MOD && !DS_OUT ? 1 : D / 16)
             for (int k = 0; k < D / 16; ++k) {
               const uint32_t kk = (k >> 2) * L::BLK_KV + (k & 3) * 32;
               const uint32_t kq = (k >> 2) * L::BLK_Q + (k & 3) * 32;
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
           tc_fence_after();
           if (elect_one()) {
             // G4: dK[key, d] += sum_q dS^T[key, q] Q[q, d]   (dS^T K-major, Q MN-major)
-#pragma unroll
+#pragma unroll (MOD && !DS_OUT ? 1 : BQ / 16)
             for (int k = 0; k < BQ / 16; ++k)
               mma_ss(tmem + L::COL_DK, sdesc_at(T_KMAJ, aDS + k * 32), sdesc_at(T_MN_Q, aQ + k * 2048),
                      ID_G34, (u > 0 || k > 0));
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
             if (u + NSTAGE < n) mma_commit(&bars[BAR_QEMPTY + stu]);
             if (!DS_OUT) {
               // G5: dQ^T[d, q] = sum_key K[key, d] dS^T[key, q]   (both MN-major)
-#pragma unroll
+#pragma unroll (MOD && !DS_OUT ? 1 : BN / 16)
               for (int k = 0; k < BN / 16; ++k)
                 mma_ss(tmem + L::col_dp(su), sdesc_at(T_MN_KV, aK + k * 2048),
                        sdesc_at(T_MN_KV, aDS + k * 2048), ID_G5, k > 0);
@@ -703,7 +703,20 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
     const float scale_log2 = p.scale_log2;
     uint8_t* ds_row = sDS + slot * L::TILE_DS + row * 128;
     float P[MOD ? 1 : BQ];
-    uint64_t P2[MOD ? BQ / 2 : 1];  // MOD: pairs of query rows
+    // MOD: pairs of query rows, of the tile's two halves.
+    //
+    // These kernels' pace is partly their instruction fetch: the compute warps' two phases,
+    // each straight-line code for 64 rows, the MMA issuers and the dQ warps run through more
+    // code than the caches feed (ncu, dQ-reduction route with a cap: 3.95 warps waiting for
+    // instructions per issue, 1.12 on the dS route). So the passes that a mask or large
+    // scores take go over the halves in a loop that is not unrolled (one half's registers
+    // move over at its second turn), the reduction route's MMAs are issued in rolled loops,
+    // and with a cap on that route (MOD_LOOP) the straight pass and the dS step loop too.
+    // Main kernel, B 1, Hq 32, Hkv 8, S 4096, causal: with a cap 430 -> 362 us (D 64 389 ->
+    // 323), 2 x 16 heads in 9 documents 149 -> 142. MOD_LOOP without a cap costs (308 ->
+    // 325), as does rolling on the dS route (276 -> 304), whose code is shorter.
+    constexpr bool MOD_LOOP = MOD == MOD_CAP && !DS_OUT;
+    uint64_t Pa[MOD ? BQ / 4 : 1], Pb[MOD ? BQ / 4 : 1] = {};
     CapCoef coef;
     if constexpr (MOD == MOD_CAP) coef = cap_coef(p.mods.cap_c, 1.f);
     bool ok = true;
@@ -760,24 +773,42 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
       tc_fence_after();
       if constexpr (MOD) {
         // Modified scores: P^T formed, masked and written out half by half.
-        uint32_t ra[32], rb[32], w[16];
-        tmem_ld32(t_lane + L::col_s(slot), ra);
-        tmem_ld32(t_lane + L::col_s(slot) + 32, rb);
-        tmem_ld_wait(ra);
-        tmem_ld_wait(rb);
-        bool small;
-        if (mod_replay_straight<MOD>(mt, cap, ra, rb, small)) {
-          mod_replay_fast<MOD, F16, 0>(mt, coef, cap, qs, ra, P2, w);
-          tmem_st16(t_lane + L::col_s(slot), w);
-          mod_replay_fast<MOD, F16, 1>(mt, coef, cap, qs, rb, P2, w);
-        } else {
-          mod_replay_half<MOD, F16, 0>(mt, coef, cap, small, qs, ra, P2, w);
-          __syncwarp();
-          tmem_st16(t_lane + L::col_s(slot), w);
-          mod_replay_half<MOD, F16, 1>(mt, coef, cap, small, qs, rb, P2, w);
-          __syncwarp();
+        bool straight = false;
+        if constexpr (!MOD_LOOP) {
+          uint32_t ra[32], rb[32], w[16];
+          tmem_ld32(t_lane + L::col_s(slot), ra);
+          tmem_ld32(t_lane + L::col_s(slot) + 32, rb);
+          tmem_ld_wait(ra);
+          tmem_ld_wait(rb);
+          // One choice for the tile (a choice per half: main kernel of bwd_capped_gqa 324 us
+          // against 282).
+          straight = mt.full[0] && mt.full[1] && mt.ahead[0] &&
+                     (MOD != MOD_CAP || mod_small(cap, fmaxf(mod_largest(ra), mod_largest(rb))));
+          if (straight) {
+            mod_replay_straight<MOD, F16>(mt, 0, coef, cap, qs, ra, Pa, w);
+            tmem_st16(t_lane + L::col_s(slot), w);
+            mod_replay_straight<MOD, F16>(mt, 1, coef, cap, qs, rb, Pb, w);
+            tmem_st16(t_lane + L::col_s(slot) + 16, w);
+          }
         }
-        tmem_st16(t_lane + L::col_s(slot) + 16, w);
+        if (!straight) {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[32], w[16];
+            tmem_ld32(t_lane + L::col_s(slot) + 32 * h, r);
+            tmem_ld_wait(r);
+            if (h) {
+#pragma unroll
+              for (int i = 0; i < BQ / 4; ++i) Pa[i] = Pb[i];
+            }
+            const bool small = MOD != MOD_CAP || mod_small(cap, mod_largest(r));
+            const ModHalf m = mod_half(mt, h);
+            if (MOD_LOOP && small && m.full && m.ahead) mod_replay_straight<MOD, F16>(mt, h, coef, cap, qs, r, Pb, w);
+            else mod_replay_steps<MOD, F16>(mt, h, small, coef, cap, qs, r, Pb, w);
+            __syncwarp();
+            tmem_st16(t_lane + L::col_s(slot) + 16 * h, w);
+          }
+        }
       } else {
       {
         uint32_t ra[32], rb[32];
@@ -842,7 +873,36 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
           !mbar_wait(&bars[BAR_DSCOPIED + slot], (j - 1) & 1, abort_flag, WAIT_LIMIT_NS)) { ok = false; break; }
       __syncwarp();
       tc_fence_after();
-      {
+      if constexpr (MOD) {
+        if (!MOD_LOOP && mt.full[0] && mt.full[1]) {
+          uint32_t ra[32], rb[32];
+          tmem_ld32(t_lane + L::col_dp(slot), ra);
+          tmem_ld32(t_lane + L::col_dp(slot) + 32, rb);
+          tmem_ld_wait(ra);
+          tmem_ld_wait(rb);
+          tc_fence_before();
+          mbar_arrive(&bars[BAR_DPREAD + slot]);  // the dP^T columns may be overwritten
+          mod_ds_pieces<F16, false>(0u, 0, Pa, qs + BQ, ra, ds_row, row & 7);
+          mod_ds_pieces<F16, false>(0u, 1, Pb, qs + BQ, rb, ds_row, row & 7);
+        } else {
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
+            tmem_ld32(t_lane + L::col_dp(slot) + 32 * h, r);
+            tmem_ld_wait(r);
+            if (h) {
+              tc_fence_before();
+              mbar_arrive(&bars[BAR_DPREAD + slot]);
+#pragma unroll
+              for (int i = 0; i < BQ / 4; ++i) Pa[i] = Pb[i];
+            }
+            const ModHalf m = mod_half(mt, h);
+            if (MOD_LOOP && m.full) mod_ds_pieces<F16, false>(0u, h, Pa, qs + BQ, r, ds_row, row & 7);
+            else mod_ds_pieces<F16, true>(m.see, h, Pa, qs + BQ, r, ds_row, row & 7);
+            __syncwarp();
+          }
+        }
+      } else {
         uint32_t ra[32], rb[32];
         tmem_ld32(t_lane + L::col_dp(slot), ra);
         tmem_ld32(t_lane + L::col_dp(slot) + 32, rb);
@@ -851,15 +911,6 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
         tc_fence_before();
         mbar_arrive(&bars[BAR_DPREAD + slot]);  // the dP^T columns may be overwritten
         const float4* delta4 = reinterpret_cast<const float4*>(qs + BQ);
-        if constexpr (MOD) {
-          if (mt.full[0] && mt.full[1]) {
-            mod_ds_half<F16, false, 0>(mt, P2, qs + BQ, ra, ds_row, row & 7);
-            mod_ds_half<F16, false, 1>(mt, P2, qs + BQ, rb, ds_row, row & 7);
-          } else {
-            mod_ds_half<F16, true, 0>(mt, P2, qs + BQ, ra, ds_row, row & 7);
-            mod_ds_half<F16, true, 1>(mt, P2, qs + BQ, rb, ds_row, row & 7);
-          }
-        } else {
 #pragma unroll
         for (int chunk = 0; chunk < 8; ++chunk) {  // 8 queries = 16 bytes of dS^T per chunk
           const uint32_t* r = chunk < 4 ? ra : rb;
@@ -903,7 +954,6 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
               }
             }
           }
-        }
         }
       }
       fence_proxy_async_smem();

@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
     }
     uint8_t* ds_row = sDS + slot * L::TILE_DS + row * 128;
     float P[MOD ? 1 : BQ];
-    uint64_t P2[MOD ? BQ / 2 : 1];  // MOD: pairs of query rows
+    uint64_t Pa[MOD ? BQ / 4 : 1], Pb[MOD ? BQ / 4 : 1];  // MOD: pairs of query rows, of the tile's halves
     CapCoef coef;
     if constexpr (MOD == MOD_CAP) coef = cap_coef(p.mods.cap_c, 1.f);
     bool ok = true;
@@ -448,13 +448,13 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
         tc_fence_before();
         mbar_arrive(&bars[BAR_SREAD + slot]);  // the S^T columns may be overwritten
         if constexpr (MOD) {
-          bool small;
-          if (mod_replay_straight<MOD>(mt, cap, ra, rb, small)) {
-            mod_replay_fast<MOD, F16, 0>(mt, coef, cap, qs, ra, P2, pw[0]);
-            mod_replay_fast<MOD, F16, 1>(mt, coef, cap, qs, rb, P2, pw[1]);
+          const bool small = MOD != MOD_CAP || mod_small(cap, fmaxf(mod_largest(ra), mod_largest(rb)));
+          if (small && mt.full[0] && mt.full[1] && mt.ahead[0]) {
+            mod_replay_straight<MOD, F16>(mt, 0, coef, cap, qs, ra, Pa, pw[0]);
+            mod_replay_straight<MOD, F16>(mt, 1, coef, cap, qs, rb, Pb, pw[1]);
           } else {
-            mod_replay_half<MOD, F16, 0>(mt, coef, cap, small, qs, ra, P2, pw[0]);
-            mod_replay_half<MOD, F16, 1>(mt, coef, cap, small, qs, rb, P2, pw[1]);
+            mod_replay_steps<MOD, F16>(mt, 0, small, coef, cap, qs, ra, Pa, pw[0]);
+            mod_replay_steps<MOD, F16>(mt, 1, small, coef, cap, qs, rb, Pb, pw[1]);
           }
         } else {
         const float4* lse4 = reinterpret_cast<const float4*>(qs);
@@ -523,11 +523,11 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
         const float4* delta4 = reinterpret_cast<const float4*>(qs + BQ);
         if constexpr (MOD) {
           if (mt.full[0] && mt.full[1]) {
-            mod_ds_half<F16, false, 0>(mt, P2, qs + BQ, ra, ds_row, row & 7);
-            mod_ds_half<F16, false, 1>(mt, P2, qs + BQ, rb, ds_row, row & 7);
+            mod_ds_pieces<F16, false>(0u, 0, Pa, qs + BQ, ra, ds_row, row & 7);
+            mod_ds_pieces<F16, false>(0u, 1, Pb, qs + BQ, rb, ds_row, row & 7);
           } else {
-            mod_ds_half<F16, true, 0>(mt, P2, qs + BQ, ra, ds_row, row & 7);
-            mod_ds_half<F16, true, 1>(mt, P2, qs + BQ, rb, ds_row, row & 7);
+            mod_ds_pieces<F16, true>(mt.see[0], 0, Pa, qs + BQ, ra, ds_row, row & 7);
+            mod_ds_pieces<F16, true>(mt.see[1], 1, Pb, qs + BQ, rb, ds_row, row & 7);
           }
         } else {
 #pragma unroll
