@@ -14,6 +14,7 @@ import ctypes
 import functools
 import math
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -88,7 +89,7 @@ def load(build_if_missing: bool = False):
     lib.sdpa_mask_plan_rows.restype = i
     lib.sdpa_mask_plan_docs.argtypes = [vp, vp, i, i, i, i, vp, sz, vp]
     lib.sdpa_mask_plan_docs.restype = i
-    lib.sdpa_rope.argtypes = [i, vp, vp, vp, vp, i, i, i, i, i, ctypes.POINTER(ctypes.c_longlong), vp, i,
+    lib.sdpa_rope.argtypes = [i, vp, vp, vp, vp, i, i, i, i, i, vp, vp, i,
                               ctypes.c_float, vp, i, i, i, i, vp]
     lib.sdpa_rope.restype = i
     lib.sdpa_nvfp4_fake_quant.argtypes = [vp, vp, ctypes.c_longlong, vp]
@@ -136,7 +137,7 @@ def _stream_handle(stream: Optional[torch.cuda.Stream]):
         return stream.cuda_stream
     # (torch.cuda.current_stream() builds a Stream object: 2.9 us a call on the Arm
     # host against 0.1 us for the handle itself)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _is(t, dtype, dev: int, shape) -> bool:
@@ -223,7 +224,7 @@ def _check_same_device(ref: torch.Tensor, _ref: str = "q", **tensors) -> None:
 
 def _check_launch_device(ref: torch.Tensor) -> None:
     """The library launches on the current CUDA device: it must be the tensors' one."""
-    if ref.device.index != torch.cuda.current_device():
+    if ref.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"the tensors are on {ref.device} but the current device is "
                          f"cuda:{torch.cuda.current_device()}: call under torch.cuda.device({ref.device})")
 
@@ -568,7 +569,7 @@ def _check_rope_args(q, k, inv_freq, positions, offset, q_out, k_out):
     _check_same_device(q, k=k, inv_freq=inv_freq, positions=positions, q_out=q_out, k_out=k_out)
 
 
-_Strides = ctypes.c_longlong * 12
+_strides = struct.Struct("12q").pack  # (0.1 us on the Arm host, against 1.1 for a ctypes array)
 
 
 def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, k_out, stream):
@@ -614,7 +615,7 @@ def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, 
         raise ValueError("offset must be at least 0, and offset + S at most 2^31")
     if B > 0 and Hq > 0:
         rc = lib.sdpa_rope(_IO_CODES[q.dtype], q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out), B, Hq, Hkv, S, D,
-                           _Strides(sq[0], sq[1], sq[2], so[0], so[1], so[2], sk[0], sk[1], sk[2], sl[0], sl[1], sl[2]),
+                           _strides(sq[0], sq[1], sq[2], so[0], so[1], so[2], sk[0], sk[1], sk[2], sl[0], sl[1], sl[2]),
                            inv_freq.data_ptr(), rot, mult, _addr(positions),
                            0 if positions is None else positions.dim() - 1, offset, interleaved, inverse,
                            _stream_handle(stream))

@@ -4,6 +4,7 @@ routes, and pins of the 64-bit reference that the GPU tests use: float64 autogra
 central differences."""
 import ctypes
 import math
+import struct
 
 import pytest
 import torch
@@ -191,11 +192,13 @@ def test_rope_argument_checks(fake):  # noqa: F811
     q, k = torch.zeros(2, 4, 16, 64, dtype=torch.bfloat16), torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16)
     f = pkg.rope_inv_freq(64, device="cpu")
     pkg.rope_fwd(q, k, f)
-    assert _last(fake, "sdpa_rope")[0] == 0 and list(_last(fake, "sdpa_rope")[10]) == [4096, 1024, 64] * 2 + [2048, 1024, 64] * 2
+    assert _last(fake, "sdpa_rope")[0] == 0
+    assert list(struct.unpack("12q", _last(fake, "sdpa_rope")[10])) == [4096, 1024, 64] * 2 + [2048, 1024, 64] * 2
     pkg.rope_bwd(q.transpose(1, 2).contiguous().transpose(1, 2), None, f[:8].contiguous(), interleaved=True,
                  positions=torch.zeros(16, dtype=torch.int32))
     args = _last(fake, "sdpa_rope")
-    assert list(args[10]) == [4096, 64, 256, 4096, 1024, 64] + list(args[10])[6:] and args[7] == 0 and args[12] == 16
+    st = list(struct.unpack("12q", args[10]))
+    assert st[:6] == [4096, 64, 256, 4096, 1024, 64] and args[7] == 0 and args[12] == 16
     assert args[15] == 0 and args[-3:-1] == (True, True)
     n = len(fake.calls)
     pos = torch.zeros(2, 16, dtype=torch.int32)
