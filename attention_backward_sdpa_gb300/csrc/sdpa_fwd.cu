@@ -116,8 +116,8 @@ __device__ int g_fwd_done[FWD_SLOTS];
 // CTA per SM takes items from the launch's ticket, and the K/V ring, the S/P
 // slots and their barrier phases run on from one item to the next; otherwise
 // one item per CTA (blockIdx.x).
-// MOD (MOD_ROWS, MOD_CAP): modified scores (score.cuh).
-template <int DQK, int DV, bool BIAS, bool F16 = false, bool PERSIST = false, int MOD = MOD_NONE>
+// MOD (MOD_ROWS, MOD_CAP): modified scores (score.cuh), SLOPES: with distance slopes.
+template <int DQK, int DV, bool BIAS, bool F16 = false, bool PERSIST = false, int MOD = MOD_NONE, bool SLOPES = false>
 __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
     sdpa_fwd_kernel(const __grid_constant__ FwdMaps maps, const FwdParams p, const int ticket_slot) {
   using namespace fwd_kernel;
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
           const int st = g % NS;
           if (g >= NS && !mbar_wait(&bars[BAR_KVEMPTY + st], ((g / NS) - 1) & 1, abort_flag, WAIT_LIMIT_NS))
             return false;
-          const int k0 = (w.kt_lo + j) * BK;
+          const int k0 = key_tile<SLOPES>(w, j) * BK;
           uint8_t* sK = sKV + st * L::STAGE;
           uint8_t* sV = sK + L::TILE_K;
           uint64_t* full = &bars[BAR_KVFULL + st];
@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
     // With a bias the scores are rewritten in place as x = s * c + bias * log2e,
     // and everything below reads them with the factor cs = 1 instead of c.
     // (The same for capped or distance-biased scores.)
-    const bool modified = MOD == MOD_CAP || (MOD && p.mods.slopes != nullptr);
+    const bool modified = MOD == MOD_CAP || SLOPES;
     const float cs = (BIAS || modified) ? 1.f : c;
     CapCoef coef;
     if constexpr (MOD == MOD_CAP) coef = cap_coef(p.mods.cap_c, p.mods.cap_log2);
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
           BIAS ? (long long)(w.bh / p.Hq) * p.bias_bstride + ((long long)w.h * p.Sq + q) * p.Skv : 0;
       for (int j = 0; j < w.n; ++j, ++g) {
         const int s = g % NSLOT;
-        const int k0 = (w.kt_lo + j) * BK;
+        const int k0 = key_tile<SLOPES>(w, j) * BK;
         uint32_t braw[BIAS ? 64 : 1];
         bool bpacked = false;
         if constexpr (BIAS) {
@@ -493,8 +493,8 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         for (int a = 0; a < 8; ++a) mp[a] = -INFINITY;
         if constexpr (MOD) {
           mod_chunks(mr, k0 + i0, ch);
-          as_before = MOD == MOD_CAP && mod_tile_as_before(p.mods, mr, sr, ch);
-          if (!as_before) mp[0] = mod_scores<MOD>(p.mods, coef, c, cs, modified, mr, k0 + i0, sr, ch);
+          as_before = mod_tile_as_before<MOD, SLOPES>(p.mods, mr, coef, c, k0 + i0, m, RESCALE_THRESHOLD, sr, ch);
+          if (!as_before) mp[0] = mod_scores<MOD, SLOPES>(p.mods, coef, c, cs, modified, mr, k0 + i0, sr, ch);
         } else if (full) {
 #pragma unroll
           for (int i = 0; i < 64; ++i) mp[i & 7] = fmaxf(mp[i & 7], __uint_as_float(sr[i >> 5][i & 31]));
@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         }
         l *= alpha;
         m = m_new;
-        if constexpr (MOD == MOD_CAP) {
+        if constexpr (MOD == MOD_CAP && !SLOPES) {
           if (!as_before && ch.deferred[0] && ch.deferred[1])
             mr.raw_ok = raise ? ch.big + RESCALE_THRESHOLD / c : fmaxf(mr.raw_ok, ch.big);
         }
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         for (int c16 = 0; c16 < 2; ++c16) {
           uint32_t wv[16];
           if constexpr (MOD) {
-            mod_exp_chunk<F16, MOD>(sr[c16], ch, c16, coef, cs, neg_m, rs, wv);
+            mod_exp_chunk<F16, MOD, SLOPES>(sr[c16], ch, c16, mr, k0 + i0 + 32 * c16, coef, c, cs, neg_m, rs, wv);
           } else if (full) {
 #pragma unroll
             for (int i2 = 0; i2 < 16; ++i2) {
@@ -699,16 +699,16 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
   }
 }
 
-template <int DQK, int DV, bool BIAS, bool F16, int MOD>
+template <int DQK, int DV, bool BIAS, bool F16, int MOD, bool SLOPES>
 static cudaError_t set_fwd_smem() {
-  return cudaFuncSetAttribute(sdpa_fwd_kernel<DQK, DV, BIAS, F16, true, MOD>,
+  return cudaFuncSetAttribute(sdpa_fwd_kernel<DQK, DV, BIAS, F16, true, MOD, SLOPES>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, fwd_kernel::Layout<DQK, DV>::BYTES);
 }
 
-template <bool BIAS, bool F16, int MOD = MOD_NONE>
+template <bool BIAS, bool F16, int MOD = MOD_NONE, bool SLOPES = false>
 static cudaError_t fwd_setup_variant() {
-  cudaError_t e = set_fwd_smem<64, 64, BIAS, F16, MOD>();
-  if (e == cudaSuccess) e = set_fwd_smem<128, 128, BIAS, F16, MOD>();
+  cudaError_t e = set_fwd_smem<64, 64, BIAS, F16, MOD, SLOPES>();
+  if (e == cudaSuccess) e = set_fwd_smem<128, 128, BIAS, F16, MOD, SLOPES>();
   return e;
 }
 
@@ -721,12 +721,16 @@ cudaError_t fwd_kernel_setup() {
   if (e == cudaSuccess) e = fwd_setup_variant<false, true, MOD_ROWS>();
   if (e == cudaSuccess) e = fwd_setup_variant<false, false, MOD_CAP>();
   if (e == cudaSuccess) e = fwd_setup_variant<false, true, MOD_CAP>();
+  if (e == cudaSuccess) e = fwd_setup_variant<false, false, MOD_ROWS, true>();
+  if (e == cudaSuccess) e = fwd_setup_variant<false, true, MOD_ROWS, true>();
+  if (e == cudaSuccess) e = fwd_setup_variant<false, false, MOD_CAP, true>();
+  if (e == cudaSuccess) e = fwd_setup_variant<false, true, MOD_CAP, true>();
   if (e == cudaSuccess) e = fwd_shared_setup();
   if (e == cudaSuccess) e = fwd_wide_setup();
   return e;
 }
 
-template <bool BIAS, bool F16, int MOD = MOD_NONE>
+template <bool BIAS, bool F16, int MOD = MOD_NONE, bool SLOPES = false>
 static cudaError_t launch_fwd_variant(const FwdMaps& maps, const FwdParams& p, cudaStream_t s, int sms,
                                       int slot) {
   // Persistent: one CTA per SM (more than half its shared memory each) taking
@@ -738,10 +742,10 @@ static cudaError_t launch_fwd_variant(const FwdMaps& maps, const FwdParams& p, c
   // D_qk = D_v up to 64 runs on the 64-column kernel, up to 128 on the 128-column
   // one: TMA zero-fills the columns past D on loads and drops them on stores.
   if (p.Dqk <= 64 && p.Dv == p.Dqk)
-    return launch_kernel(sdpa_fwd_kernel<64, 64, BIAS, F16, PERSIST, MOD>, grid, block,
+    return launch_kernel(sdpa_fwd_kernel<64, 64, BIAS, F16, PERSIST, MOD, SLOPES>, grid, block,
                          fwd_kernel::Layout<64, 64>::BYTES, s, false, maps, p, slot);
   if (p.Dqk <= 128 && p.Dv == p.Dqk)
-    return launch_kernel(sdpa_fwd_kernel<128, 128, BIAS, F16, PERSIST, MOD>, grid, block,
+    return launch_kernel(sdpa_fwd_kernel<128, 128, BIAS, F16, PERSIST, MOD, SLOPES>, grid, block,
                          fwd_kernel::Layout<128, 128>::BYTES, s, false, maps, p, slot);
   return cudaErrorInvalidValue;
 }
@@ -758,6 +762,15 @@ cudaError_t launch_fwd(const FwdMaps& maps, const FwdParams& p, cudaStream_t s) 
   // (sdpa_fwd_wide.cu).
   if (p.Dqk == 192 && p.Dv == 128) return launch_fwd_shared(maps, p, s, sms, slot);
   if (p.Dqk == 256 && p.Dv == 256) return launch_fwd_wide(maps, p, s, sms, slot);
+  // Slopes have kernels of their own: their code in the others cost those (a cap alone 160.7
+  // -> 176 us at B 1, Hq 32, Hkv 8, S 4096, D 128).
+  if (p.mods.on && p.mods.slopes) {
+    if (p.mods.on == MOD_CAP)
+      return p.f16 ? launch_fwd_variant<false, true, MOD_CAP, true>(maps, p, s, sms, slot)
+                   : launch_fwd_variant<false, false, MOD_CAP, true>(maps, p, s, sms, slot);
+    return p.f16 ? launch_fwd_variant<false, true, MOD_ROWS, true>(maps, p, s, sms, slot)
+                 : launch_fwd_variant<false, false, MOD_ROWS, true>(maps, p, s, sms, slot);
+  }
   if (p.mods.on == MOD_CAP)
     return p.f16 ? launch_fwd_variant<false, true, MOD_CAP>(maps, p, s, sms, slot)
                  : launch_fwd_variant<false, false, MOD_CAP>(maps, p, s, sms, slot);

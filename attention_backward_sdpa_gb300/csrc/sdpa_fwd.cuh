@@ -126,6 +126,8 @@ struct ModChunks {
   bool full[2];     // every row of the warp sees the whole chunk
   bool any[2];      // some row may see a key of it
   bool deferred[2]; // the scores are left to be capped with the exponentials
+  bool biased;      // all of them are left to be modified there, the distance bias included:
+  float side;       // key i's is -side * (dist - i), side = +-slope2
   float big;        // the largest score of the deferred chunks as it is
 };
 
@@ -142,12 +144,12 @@ struct ModRow {
 };
 
 // The chunk's scores as modified scores times log2(e): keys from kb, `dist` = q + diag - kb.
-template <int MOD>
+template <int MOD, bool SLOPES>
 __device__ __forceinline__ void modify_chunk(const ScoreMods& m, const CapCoef& coef, float c, float slope2, float dist,
                                              bool small, uint32_t (&s)[32]) {
   // Every key at or before its row: the bias is -slope2 (dist - i), one multiply-add a
   // score without |.|.
-  const bool biased = m.slopes != nullptr, ahead = __all_sync(0xffffffffu, dist >= 31.f);
+  const bool biased = SLOPES && m.slopes != nullptr, ahead = biased && __all_sync(0xffffffffu, dist >= 31.f);
   const float base = -slope2 * dist;
   const uint64_t c2 = f2_pack(c, c), log2_cap = f2_pack(m.cap_log2, m.cap_log2);
 #pragma unroll
@@ -156,12 +158,17 @@ __device__ __forceinline__ void modify_chunk(const ScoreMods& m, const CapCoef& 
     uint32_t* const sb = s + blk * FWD_SIDE * 2;
 #pragma unroll
     for (int i = 0; i < FWD_SIDE; ++i) x[i] = f2_pack(sb[2 * i], sb[2 * i + 1]);
-    if (biased) {
+    if (biased && ahead) {
 #pragma unroll
       for (int i = 0; i < FWD_SIDE; ++i) {
         const float i0 = (float)(2 * (blk * FWD_SIDE + i)), i1 = i0 + 1.f;
-        b[i] = ahead ? f2_pack(fmaf(slope2, i0, base), fmaf(slope2, i1, base))
-                     : f2_pack(-slope2 * fabsf(dist - i0), -slope2 * fabsf(dist - i1));
+        b[i] = f2_pack(fmaf(slope2, i0, base), fmaf(slope2, i1, base));
+      }
+    } else if (biased) {
+#pragma unroll
+      for (int i = 0; i < FWD_SIDE; ++i) {
+        const float i0 = (float)(2 * (blk * FWD_SIDE + i)), i1 = i0 + 1.f;
+        b[i] = f2_pack(-slope2 * fabsf(dist - i0), -slope2 * fabsf(dist - i1));
       }
     } else {
 #pragma unroll
@@ -206,6 +213,7 @@ __device__ __forceinline__ void mod_chunks(const ModRow& r, int kb, ModChunks& c
     ch.any[k] = c0 + 31 >= r.lo_min && c0 <= r.hi_max;
     ch.deferred[k] = false;
   }
+  ch.biased = false;
   ch.big = -INFINITY;
 }
 
@@ -222,18 +230,45 @@ __device__ __forceinline__ float chunk_extremes(const uint32_t (&s)[32], float& 
   return max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
 }
 
-// The common tile under a cap alone: both chunks visible to the whole warp, every score
-// within the polynomial and none that would raise its row's reference. One pass and one
-// vote; the scores stay as they are for exp_chunk<CAPPED>.
-__device__ __forceinline__ bool mod_tile_as_before(const ScoreMods& m, const ModRow& r, const uint32_t (&sr)[2][32],
+// The common tile: both chunks visible to the whole warp, with slopes all keys on one side of
+// their rows, with a cap every score within the polynomial, and no score that would raise its
+// row's reference m by more than `slack`. One pass and one vote; the scores stay as they are
+// for exp_chunk. kb: the thread's first key; c: scale * log2(e).
+template <int MOD, bool SLOPES>
+__device__ __forceinline__ bool mod_tile_as_before(const ScoreMods& mods, const ModRow& r, const CapCoef& coef, float c,
+                                                   int kb, float m, float slack, const uint32_t (&sr)[2][32],
                                                    ModChunks& ch) {
-  if (!ch.full[0] || !ch.full[1] || m.slopes != nullptr) return false;
-  float least = 0.f;
-  const float b0 = chunk_extremes(sr[0], least);
-  const float b1 = chunk_extremes(sr[1], least);
-  const float big = fmaxf(b0, b1);
-  if (!__all_sync(0xffffffffu, fmaxf(big, -least) <= m.cap_small && big <= r.raw_ok)) return false;
+  if ((MOD != MOD_CAP && !SLOPES) || !ch.full[0] || !ch.full[1]) return false;
+  if constexpr (SLOPES) {
+    const int first = r.place - (int)(threadIdx.x & 31u);  // the warp's first row's place
+    if (first >= kb + 63) ch.side = r.slope2;
+    else if (first + 31 <= kb) ch.side = -r.slope2;
+    else return false;
+  }
+  const float d0 = (float)(r.place - kb);
+  const float bias = SLOPES ? -fminf(ch.side * d0, ch.side * (d0 - 63.f)) : 0.f;  // the largest of the 64
+  bool fine;
+  if constexpr (MOD == MOD_CAP) {
+    float least = 0.f;
+    const float b0 = chunk_extremes(sr[0], least);
+    const float b1 = chunk_extremes(sr[1], least);
+    const float big = fmaxf(b0, b1);
+    fine = fmaxf(big, -least) <= mods.cap_small;
+    if constexpr (SLOPES) fine = fine && cap_score(big, coef) + bias <= m + slack;
+    else fine = fine && big <= r.raw_ok;
+  } else {
+    float mx[8];
+#pragma unroll
+    for (int a = 0; a < 8; ++a) mx[a] = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 64; i += 2)
+      mx[(i >> 1) & 7] = max3(mx[(i >> 1) & 7], __uint_as_float(sr[i >> 5][i & 31]), __uint_as_float(sr[i >> 5][(i & 31) + 1]));
+    const float big = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+    fine = fmaf(big, c, bias) <= m + slack;
+  }
+  if (!__all_sync(0xffffffffu, fine)) return false;
   ch.deferred[0] = ch.deferred[1] = true;
+  ch.biased = SLOPES;
   return true;
 }
 
@@ -241,7 +276,7 @@ __device__ __forceinline__ bool mod_tile_as_before(const ScoreMods& m, const Mod
 // biased; else they stay, and the exponent takes them times cs), -inf where masked. The
 // thread's 64 keys start at kb. Returns the row's maximum in log2 units (-inf when it
 // sees none).
-template <int MOD>
+template <int MOD, bool SLOPES = true>
 __device__ __forceinline__ float mod_scores(const ScoreMods& m, const CapCoef& coef, float c, float cs, bool modified,
                                             const ModRow& r, int kb, uint32_t (&sr)[2][32], ModChunks& ch) {
   float big[2] = {-INFINITY, -INFINITY};  // the chunks' largest scores as they are
@@ -257,13 +292,13 @@ __device__ __forceinline__ float mod_scores(const ScoreMods& m, const CapCoef& c
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (!ch.any[k]) continue;
-    if (MOD == MOD_CAP && small && ch.full[k] && m.slopes == nullptr) {
+    if (MOD == MOD_CAP && small && ch.full[k] && (!SLOPES || m.slopes == nullptr)) {
       ch.deferred[k] = true;
       ch.big = fmaxf(ch.big, big[k]);
       continue;
     }
     const int c0 = kb + 32 * k;
-    if (modified) modify_chunk<MOD>(m, coef, c, r.slope2, (float)(r.place - c0), small, sr[k]);
+    if (modified) modify_chunk<MOD, SLOPES>(m, coef, c, r.slope2, (float)(r.place - c0), small, sr[k]);
     if (!ch.full[k]) {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
@@ -279,11 +314,16 @@ __device__ __forceinline__ float mod_scores(const ScoreMods& m, const CapCoef& c
   return mt;
 }
 
-// The chunk's P = ex2(x * cs + neg_m) as io pairs, added to the row sum's partials.
-template <bool F16, bool CAPPED>
+// The chunk's P = ex2(x * cs + neg_m) as io pairs, added to the row sum's partials. CAPPED:
+// x * cs is the capped score instead; BIASED: key i adds slope2 * i (its bias, less what
+// neg_m holds of it).
+template <bool F16, bool CAPPED, bool BIASED>
 __device__ __forceinline__ void exp_chunk(const uint32_t (&s)[32], const CapCoef& coef, float cs, float neg_m,
-                                          float (&rs)[8], uint32_t (&w)[16]) {
+                                          float slope2, float (&rs)[8], uint32_t (&w)[16]) {
   const uint64_t c2 = f2_pack(cs, cs), m2 = f2_pack(neg_m, neg_m);
+  auto add = [&](int i) -> uint64_t {
+    return BIASED ? f2_pack(fmaf(slope2, (float)(2 * i), neg_m), fmaf(slope2, (float)(2 * i + 1), neg_m)) : m2;
+  };
   uint64_t sum[4];
 #pragma unroll
   for (int a = 0; a < 4; ++a) sum[a] = f2_pack(rs[2 * a], rs[2 * a + 1]);
@@ -296,10 +336,10 @@ __device__ __forceinline__ void exp_chunk(const uint32_t (&s)[32], const CapCoef
       uint64_t r[FWD_SIDE];
       tanh2_poly(x, coef, r);
 #pragma unroll
-      for (int i = 0; i < FWD_SIDE; ++i) x[i] = f2_fma(x[i], r[i], m2);
+      for (int i = 0; i < FWD_SIDE; ++i) x[i] = f2_fma(x[i], r[i], add(blk * FWD_SIDE + i));
     } else {
 #pragma unroll
-      for (int i = 0; i < FWD_SIDE; ++i) x[i] = f2_fma(x[i], c2, m2);
+      for (int i = 0; i < FWD_SIDE; ++i) x[i] = f2_fma(x[i], c2, add(blk * FWD_SIDE + i));
     }
 #pragma unroll
     for (int i = 0; i < FWD_SIDE; ++i) {
@@ -318,16 +358,20 @@ __device__ __forceinline__ void exp_chunk(const uint32_t (&s)[32], const CapCoef
 #pragma unroll
   for (int a = 0; a < 4; ++a) f2_unpack(sum[a], rs[2 * a], rs[2 * a + 1]);
 }
-template <bool F16, int MOD>
-__device__ __forceinline__ void mod_exp_chunk(const uint32_t (&s)[32], const ModChunks& ch, int k, const CapCoef& coef,
-                                              float cs, float neg_m, float (&rs)[8], uint32_t (&w)[16]) {
+// Chunk k (keys from kb) of the row; c: scale * log2(e).
+template <bool F16, int MOD, bool SLOPES = true>
+__device__ __forceinline__ void mod_exp_chunk(const uint32_t (&s)[32], const ModChunks& ch, int k, const ModRow& r,
+                                              int kb, const CapCoef& coef, float c, float cs, float neg_m,
+                                              float (&rs)[8], uint32_t (&w)[16]) {
   if (!ch.any[k]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = 0u;
+  } else if (SLOPES && ch.biased) {
+    exp_chunk<F16, MOD == MOD_CAP, true>(s, coef, c, fmaf(-ch.side, (float)(r.place - kb), neg_m), ch.side, rs, w);
   } else if (MOD == MOD_CAP && ch.deferred[k]) {
-    exp_chunk<F16, true>(s, coef, cs, neg_m, rs, w);
+    exp_chunk<F16, true, false>(s, coef, cs, neg_m, 0.f, rs, w);
   } else {
-    exp_chunk<F16, false>(s, coef, cs, neg_m, rs, w);
+    exp_chunk<F16, false, false>(s, coef, cs, neg_m, 0.f, rs, w);
   }
 }
 
@@ -405,6 +449,14 @@ __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int it, const Fw
 template <int MOD = MOD_NONE>
 __device__ __forceinline__ FwdItem fwd_item(const FwdParams& p, int it) {
   return fwd_item<MOD>(p, it, fwd_item_loads<MOD>(p, it));
+}
+
+// The item's j-th key tile. Under distance slopes from the last to the first: the bias grows
+// towards the row's own place, so in ascending order nearly every tile would raise the
+// softmax reference and rescale O.
+template <bool SLOPES>
+__device__ __forceinline__ int key_tile(const FwdItem& w, int j) {
+  return SLOPES ? w.kt_lo + w.n - 1 - j : w.kt_lo + j;
 }
 
 // An item as the producer publishes it under modified scores, decoded and with the bounds

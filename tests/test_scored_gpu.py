@@ -394,3 +394,13 @@ def test_outputs_below_fp16_normals():
     """A sink that takes nearly all of the weight: outputs down to 1e-9, fp16 subnormals and zeros."""
     _check(Case(2, 3, 3, 1, 1, 80, 80, io=torch.float16, seed=2587, gain=15.0, sink=True, causal=True,
                 bottom_right=True, window_left=0, slopes=[0.5, 0.0, 2.0]), deterministic=(False, True))
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("softcap", [0.0, 30.0, 2.0])
+@pytest.mark.parametrize("mask", [dict(), dict(bottom_right=True), dict(causal=True), dict(window_left=200)])
+def test_slopes_on_both_sides_of_the_rows(mask, softcap, io):
+    """Several key tiles before and behind every row; slopes of both signs, none, steep ones."""
+    case = Case(1, 6, 2, 520, 700, 64, 64, io=io, seed=37, softcap=softcap,
+                slopes=[0.002, 0.06, -0.003, 0.0, 1.5, 0.25], **mask)
+    _check(case, deterministic=(False, True))
