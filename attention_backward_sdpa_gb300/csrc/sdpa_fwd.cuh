@@ -233,7 +233,9 @@ __device__ __forceinline__ float chunk_extremes(const uint32_t (&s)[32], float& 
 // The common tile: both chunks visible to the whole warp, with slopes all keys on one side of
 // their rows, with a cap every score within the polynomial, and no score that would raise its
 // row's reference m by more than `slack`. One pass and one vote; the scores stay as they are
-// for exp_chunk. kb: the thread's first key; c: scale * log2(e).
+// for exp_chunk. (With a cap one maximum, of the sizes, serves both tests: a negative score
+// that fails the second only costs the other path.) kb: the thread's first key; c: scale *
+// log2(e).
 template <int MOD, bool SLOPES>
 __device__ __forceinline__ bool mod_tile_as_before(const ScoreMods& mods, const ModRow& r, const CapCoef& coef, float c,
                                                    int kb, float m, float slack, const uint32_t (&sr)[2][32],
@@ -247,25 +249,20 @@ __device__ __forceinline__ bool mod_tile_as_before(const ScoreMods& mods, const 
   }
   const float d0 = (float)(r.place - kb);
   const float bias = SLOPES ? -fminf(ch.side * d0, ch.side * (d0 - 63.f)) : 0.f;  // the largest of the 64
-  bool fine;
-  if constexpr (MOD == MOD_CAP) {
-    float least = 0.f;
-    const float b0 = chunk_extremes(sr[0], least);
-    const float b1 = chunk_extremes(sr[1], least);
-    const float big = fmaxf(b0, b1);
-    fine = fmaxf(big, -least) <= mods.cap_small;
-    if constexpr (SLOPES) fine = fine && cap_score(big, coef) + bias <= m + slack;
-    else fine = fine && big <= r.raw_ok;
-  } else {
-    float mx[8];
+  float mx[8];
 #pragma unroll
-    for (int a = 0; a < 8; ++a) mx[a] = -INFINITY;
+  for (int a = 0; a < 8; ++a) mx[a] = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 64; i += 2)
-      mx[(i >> 1) & 7] = max3(mx[(i >> 1) & 7], __uint_as_float(sr[i >> 5][i & 31]), __uint_as_float(sr[i >> 5][(i & 31) + 1]));
-    const float big = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-    fine = fmaf(big, c, bias) <= m + slack;
+  for (int i = 0; i < 64; i += 2) {
+    float s0 = __uint_as_float(sr[i >> 5][i & 31]), s1 = __uint_as_float(sr[i >> 5][(i & 31) + 1]);
+    if constexpr (MOD == MOD_CAP) s0 = fabsf(s0), s1 = fabsf(s1);
+    mx[(i >> 1) & 7] = max3(mx[(i >> 1) & 7], s0, s1);
   }
+  const float big = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+  bool fine;
+  if constexpr (MOD != MOD_CAP) fine = fmaf(big, c, bias) <= m + slack;
+  else if constexpr (SLOPES) fine = big <= mods.cap_small && cap_score(big, coef) + bias <= m + slack;
+  else fine = big <= fminf(mods.cap_small, r.raw_ok);
   if (!__all_sync(0xffffffffu, fine)) return false;
   ch.deferred[0] = ch.deferred[1] = true;
   ch.biased = SLOPES;
