@@ -115,14 +115,18 @@ __device__ __forceinline__ float clamp_nan(float x, float lim) {
   asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}" : "=f"(r) : "f"(x), "f"(-lim), "f"(lim));
   return r;
 }
-// N pairs of any scores, in place: tanh(s * cap_in).
-template <int N>
+// N pairs of any scores, in place: tanh(s * cap_in). CLAMP: |s * cap_in| may pass TANH_CLAMP.
+template <int N, bool CLAMP = true>
 __device__ __forceinline__ void tanh2_any(uint64_t (&s)[N], float cap_in) {
   constexpr float NU[5] = {9.999999936e-01f, 1.344449871e-01f, 3.571599056e-03f, 2.189467996e-05f, 1.523044372e-08f};
   constexpr float DE[5] = {1.0f, 4.677782538e-01f, 2.616444638e-02f, 3.411293732e-04f, 8.522456963e-07f};
   uint64_t u[N], n[N], d[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
+    if constexpr (!CLAMP) {
+      s[i] = f2_mul(s[i], f2_pack(cap_in, cap_in));
+      continue;
+    }
     float y0, y1;
     f2_unpack(s[i], y0, y1);
     s[i] = f2_pack(clamp_nan(y0 * cap_in, TANH_CLAMP), clamp_nan(y1 * cap_in, TANH_CLAMP));

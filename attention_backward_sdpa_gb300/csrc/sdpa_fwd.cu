@@ -48,6 +48,7 @@ constexpr int THREADS = 384;
 using fwd_shared::BM;
 using fwd_shared::BK;
 using fwd_shared::WAIT_LIMIT_NS;
+using fwd_shared::MOD_THRESHOLD;
 using fwd_shared::RESCALE_THRESHOLD;
 constexpr int NSLOT = 2;  // S/P slots in tensor memory
 
@@ -361,6 +362,7 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
     // and everything below reads them with the factor cs = 1 instead of c.
     // (The same for capped or distance-biased scores.)
     const bool modified = MOD == MOD_CAP || SLOPES;
+    constexpr float RAISE = MOD ? MOD_THRESHOLD : RESCALE_THRESHOLD;
     const float cs = (BIAS || modified) ? 1.f : c;
     CapCoef coef;
     if constexpr (MOD == MOD_CAP) coef = cap_coef(p.mods.cap_c, p.mods.cap_log2);
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         for (int a = 0; a < 8; ++a) mp[a] = -INFINITY;
         if constexpr (MOD) {
           mod_chunks(mr, k0 + i0, ch);
-          as_before = mod_tile_as_before<MOD, SLOPES>(p.mods, mr, coef, c, k0 + i0, m, RESCALE_THRESHOLD, sr, ch);
+          as_before = mod_tile_as_before<MOD, SLOPES>(p.mods, mr, c, k0 + i0, m, RAISE, sr, ch);
           if (!as_before) mp[0] = mod_scores<MOD, SLOPES>(p.mods, coef, c, cs, modified, mr, k0 + i0, sr, ch);
         } else if (full) {
 #pragma unroll
@@ -508,7 +510,7 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
                          (MOD ? 1.f : cs);  // cs > 0 (mod_scores has multiplied)
         // Raise the reference when the tile's maximum exceeds it by more than the
         // threshold (or when it is the row's first visible key).
-        const bool raise = !as_before && (mt > m + RESCALE_THRESHOLD || (m == -INFINITY && mt > -INFINITY));
+        const bool raise = !as_before && (mt > m + RAISE || (m == -INFINITY && mt > -INFINITY));
         const float m_new = raise ? mt : m;
         const float alpha = raise ? ex2_approx(m - m_new) : 1.f;  // 0 when m was -inf
         // O_half holds contributions of this item's earlier tiles once m is
@@ -543,8 +545,8 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         l *= alpha;
         m = m_new;
         if constexpr (MOD == MOD_CAP && !SLOPES) {
-          if (!as_before && ch.deferred[0] && ch.deferred[1])
-            mr.raw_ok = raise ? ch.big + RESCALE_THRESHOLD / c : fmaxf(mr.raw_ok, ch.big);
+          if (!as_before && ch.full[0] && ch.full[1])
+            mr.raw_ok = raise ? ch.big + RAISE / c : fmaxf(mr.raw_ok, ch.big);
         }
         // P = exp2(x - m) on visible keys, as bf16 pairs into the slot's columns
         // [64 half, 64 half + 32): inside this half's own S columns, which this
@@ -560,7 +562,7 @@ __global__ void __launch_bounds__(fwd_kernel::THREADS, 1)
         for (int c16 = 0; c16 < 2; ++c16) {
           uint32_t wv[16];
           if constexpr (MOD) {
-            mod_exp_chunk<F16, MOD, SLOPES>(sr[c16], ch, c16, mr, k0 + i0 + 32 * c16, coef, c, cs, neg_m, rs, wv);
+            mod_exp_chunk<F16, MOD, SLOPES>(p.mods, sr[c16], ch, c16, mr, k0 + i0 + 32 * c16, coef, c, cs, neg_m, rs, wv);
           } else if (full) {
 #pragma unroll
             for (int i2 = 0; i2 < 16; ++i2) {

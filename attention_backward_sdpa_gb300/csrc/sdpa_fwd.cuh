@@ -18,6 +18,10 @@ constexpr int BM = 128;  // query rows per item
 constexpr int BK = 128;  // keys per tile
 constexpr uint64_t WAIT_LIMIT_NS = 4000000000ull;
 constexpr float RESCALE_THRESHOLD = 8.f;  // log2 units: P stays below 2^8 until a raise
+// The same under modified scores: P below 2^15, within fp16 (at 8, one row in a warp of 32
+// with a late maximum more often takes the tile off the common path: fwd_capped_gqa 170 us
+// against 153).
+constexpr float MOD_THRESHOLD = 15.f;
 constexpr int FWD_SLOTS = 64;             // launch slots of the persistent tickets
 }  // namespace fwd_shared
 
@@ -126,9 +130,10 @@ struct ModChunks {
   bool full[2];     // every row of the warp sees the whole chunk
   bool any[2];      // some row may see a key of it
   bool deferred[2]; // the scores are left to be capped with the exponentials
+  bool large;       // ... with some past the polynomial (all within TANH_CLAMP caps)
   bool biased;      // all of them are left to be modified there, the distance bias included:
   float side;       // key i's is -side * (dist - i), side = +-slope2
-  float big;        // the largest score of the deferred chunks as it is
+  float big;        // the largest score of the chunks seen in full, as it is (a cap alone)
 };
 
 // A row's state under modified scores, for one item.
@@ -213,7 +218,7 @@ __device__ __forceinline__ void mod_chunks(const ModRow& r, int kb, ModChunks& c
     ch.any[k] = c0 + 31 >= r.lo_min && c0 <= r.hi_max;
     ch.deferred[k] = false;
   }
-  ch.biased = false;
+  ch.large = ch.biased = false;
   ch.big = -INFINITY;
 }
 
@@ -231,14 +236,13 @@ __device__ __forceinline__ float chunk_extremes(const uint32_t (&s)[32], float& 
 }
 
 // The common tile: both chunks visible to the whole warp, with slopes all keys on one side of
-// their rows, with a cap every score within the polynomial, and no score that would raise its
-// row's reference m by more than `slack`. One pass and one vote; the scores stay as they are
-// for exp_chunk. (With a cap one maximum, of the sizes, serves both tests: a negative score
-// that fails the second only costs the other path.) kb: the thread's first key; c: scale *
-// log2(e).
+// their rows, and no score that would raise its row's reference m by more than `slack`. The
+// scores stay as they are for exp_chunk. (With a cap the maximum is of the sizes, which also
+// tells whether the polynomial serves; a negative score that fails the test for a raise only
+// costs the other path. The cap never raises a positive score, so that bounds it.) kb: the
+// thread's first key; c: scale * log2(e).
 template <int MOD, bool SLOPES>
-__device__ __forceinline__ bool mod_tile_as_before(const ScoreMods& mods, const ModRow& r, const CapCoef& coef, float c,
-                                                   int kb, float m, float slack, const uint32_t (&sr)[2][32],
+__device__ __forceinline__ bool mod_tile_as_before(const ScoreMods& mods, const ModRow& r, float c, int kb, float m, float slack, const uint32_t (&sr)[2][32],
                                                    ModChunks& ch) {
   if ((MOD != MOD_CAP && !SLOPES) || !ch.full[0] || !ch.full[1]) return false;
   if constexpr (SLOPES) {
@@ -259,11 +263,14 @@ __device__ __forceinline__ bool mod_tile_as_before(const ScoreMods& mods, const 
     mx[(i >> 1) & 7] = max3(mx[(i >> 1) & 7], s0, s1);
   }
   const float big = max3(max3(mx[0], mx[1], mx[2]), max3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-  bool fine;
-  if constexpr (MOD != MOD_CAP) fine = fmaf(big, c, bias) <= m + slack;
-  else if constexpr (SLOPES) fine = big <= mods.cap_small && cap_score(big, coef) + bias <= m + slack;
-  else fine = big <= fminf(mods.cap_small, r.raw_ok);
-  if (!__all_sync(0xffffffffu, fine)) return false;
+  bool fine = MOD == MOD_CAP && !SLOPES ? big <= r.raw_ok : fmaf(big, c, bias) <= m + slack;
+  if (MOD != MOD_CAP) {
+    if (!__all_sync(0xffffffffu, fine)) return false;
+  } else if (!__all_sync(0xffffffffu, fine && big <= mods.cap_small)) {
+    fine = fine && big * mods.cap_in <= TANH_CLAMP;
+    if (!__all_sync(0xffffffffu, fine)) return false;
+    ch.large = true;
+  }
   ch.deferred[0] = ch.deferred[1] = true;
   ch.biased = SLOPES;
   return true;
@@ -289,10 +296,12 @@ __device__ __forceinline__ float mod_scores(const ScoreMods& m, const CapCoef& c
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (!ch.any[k]) continue;
-    if (MOD == MOD_CAP && small && ch.full[k] && (!SLOPES || m.slopes == nullptr)) {
-      ch.deferred[k] = true;
+    if (MOD == MOD_CAP && ch.full[k] && (!SLOPES || m.slopes == nullptr)) {
       ch.big = fmaxf(ch.big, big[k]);
-      continue;
+      if (small) {
+        ch.deferred[k] = true;
+        continue;
+      }
     }
     const int c0 = kb + 32 * k;
     if (modified) modify_chunk<MOD, SLOPES>(m, coef, c, r.slope2, (float)(r.place - c0), small, sr[k]);
@@ -311,12 +320,12 @@ __device__ __forceinline__ float mod_scores(const ScoreMods& m, const CapCoef& c
   return mt;
 }
 
-// The chunk's P = ex2(x * cs + neg_m) as io pairs, added to the row sum's partials. CAPPED:
-// x * cs is the capped score instead; BIASED: key i adds slope2 * i (its bias, less what
-// neg_m holds of it).
-template <bool F16, bool CAPPED, bool BIASED>
-__device__ __forceinline__ void exp_chunk(const uint32_t (&s)[32], const CapCoef& coef, float cs, float neg_m,
-                                          float slope2, float (&rs)[8], uint32_t (&w)[16]) {
+// The chunk's P = ex2(x * cs + neg_m) as io pairs, added to the row sum's partials. CAPPED 1:
+// the polynomial's capped score instead of x * cs, 2: that of x up to TANH_CLAMP caps (cs = cap * log2(e));
+// BIASED: key i adds slope2 * i (its bias, less what neg_m holds of it).
+template <bool F16, int CAPPED, bool BIASED>
+__device__ __forceinline__ void exp_chunk(const uint32_t (&s)[32], const CapCoef& coef, float cap_in, float cs,
+                                          float neg_m, float slope2, float (&rs)[8], uint32_t (&w)[16]) {
   const uint64_t c2 = f2_pack(cs, cs), m2 = f2_pack(neg_m, neg_m);
   auto add = [&](int i) -> uint64_t {
     return BIASED ? f2_pack(fmaf(slope2, (float)(2 * i), neg_m), fmaf(slope2, (float)(2 * i + 1), neg_m)) : m2;
@@ -329,7 +338,8 @@ __device__ __forceinline__ void exp_chunk(const uint32_t (&s)[32], const CapCoef
     uint64_t x[FWD_SIDE];
 #pragma unroll
     for (int i = 0; i < FWD_SIDE; ++i) x[i] = f2_pack(s[2 * (blk * FWD_SIDE + i)], s[2 * (blk * FWD_SIDE + i) + 1]);
-    if constexpr (CAPPED) {
+    if constexpr (CAPPED == 2) tanh2_any<FWD_SIDE, false>(x, cap_in);
+    if constexpr (CAPPED == 1) {
       uint64_t r[FWD_SIDE];
       tanh2_poly(x, coef, r);
 #pragma unroll
@@ -357,18 +367,21 @@ __device__ __forceinline__ void exp_chunk(const uint32_t (&s)[32], const CapCoef
 }
 // Chunk k (keys from kb) of the row; c: scale * log2(e).
 template <bool F16, int MOD, bool SLOPES = true>
-__device__ __forceinline__ void mod_exp_chunk(const uint32_t (&s)[32], const ModChunks& ch, int k, const ModRow& r,
-                                              int kb, const CapCoef& coef, float c, float cs, float neg_m,
-                                              float (&rs)[8], uint32_t (&w)[16]) {
+__device__ __forceinline__ void mod_exp_chunk(const ScoreMods& mods, const uint32_t (&s)[32], const ModChunks& ch,
+                                              int k, const ModRow& r, int kb, const CapCoef& coef, float c, float cs,
+                                              float neg_m, float (&rs)[8], uint32_t (&w)[16]) {
   if (!ch.any[k]) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = 0u;
   } else if (SLOPES && ch.biased) {
-    exp_chunk<F16, MOD == MOD_CAP, true>(s, coef, c, fmaf(-ch.side, (float)(r.place - kb), neg_m), ch.side, rs, w);
+    const float add = fmaf(-ch.side, (float)(r.place - kb), neg_m);
+    if (MOD == MOD_CAP && ch.large) exp_chunk<F16, 2, true>(s, coef, mods.cap_in, mods.cap_log2, add, ch.side, rs, w);
+    else exp_chunk<F16, MOD == MOD_CAP, true>(s, coef, 0.f, c, add, ch.side, rs, w);
   } else if (MOD == MOD_CAP && ch.deferred[k]) {
-    exp_chunk<F16, true, false>(s, coef, cs, neg_m, 0.f, rs, w);
+    if (ch.large) exp_chunk<F16, 2, false>(s, coef, mods.cap_in, mods.cap_log2, neg_m, 0.f, rs, w);
+    else exp_chunk<F16, 1, false>(s, coef, 0.f, cs, neg_m, 0.f, rs, w);
   } else {
-    exp_chunk<F16, false, false>(s, coef, cs, neg_m, 0.f, rs, w);
+    exp_chunk<F16, 0, false>(s, coef, 0.f, cs, neg_m, 0.f, rs, w);
   }
 }
 

@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(fwd_sh::THREADS, 1)
         for (int c16 = 0; c16 < 2; ++c16) {
           uint32_t wv[16];
           if constexpr (MOD) {
-            mod_exp_chunk<F16, MOD>(sr[c16], ch, c16, mr, k0 + i0 + 32 * c16, coef, c, cs, neg_m, rs, wv);
+            mod_exp_chunk<F16, MOD>(p.mods, sr[c16], ch, c16, mr, k0 + i0 + 32 * c16, coef, c, cs, neg_m, rs, wv);
           } else if (full) {
 #pragma unroll
             for (int i2 = 0; i2 < 16; ++i2) {

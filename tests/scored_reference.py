@@ -132,7 +132,8 @@ class Case:
                 a = p @ v.abs()
                 e = e + G23 * self.Skv
                 bo[b, h] = self.u * 1.01 * (a + o[b, h].abs()) + 2 * e * a + 1e-30
-                # an fp16 weight relative to the running reference (at most 2^8 above it)
+                # an fp16 weight below 2^-14 relative to the running reference, which is at most
+                # the row's maximum, so the sum that divides it is at least 1 (256: to spare)
                 bo[b, h] += sub * 256 * v.abs().sum(0)
                 # O itself below 2^-14 is rounded to multiples of 2^-24: half a step is 2^-25, for
                 # O = 8.0993e-9 (0.136 steps) rounded to 0 more than the relative terms above allow
