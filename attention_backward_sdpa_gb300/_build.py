@@ -26,7 +26,7 @@ BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libsdpa_bwd_debug.so")
 DEBUG_FLAGS = ["-DSDPA_DEBUG_BOUNDS"]
 SOURCES = ["sdpa_bwd_api.cu", "sdpa_bwd_main.cu", "sdpa_bwd_main_bias.cu", "sdpa_bwd_main_qat.cu",
-           "sdpa_bwd_main_f16.cu", "sdpa_bwd_main_mod.cu", "sdpa_bwd_main_cap.cu",
+           "sdpa_bwd_main_f16.cu", "sdpa_bwd_main_mod.cu", "sdpa_bwd_main_cap.cu", "sdpa_bwd_main_slopes.cu",
            "sdpa_bwd_main_ds.cu",
            "sdpa_bwd_aux.cu",
            "sdpa_bwd_dq.cu", "sdpa_bwd_noalloc.cu", "sdpa_fwd.cu", "sdpa_fwd_shared.cu", "sdpa_fwd_wide.cu",

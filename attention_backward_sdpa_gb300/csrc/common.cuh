@@ -357,6 +357,8 @@ cudaError_t launch_main_mod(const MainMaps& maps, const ChainParams& p, cudaStre
 cudaError_t main_mod_kernel_setup();
 cudaError_t launch_main_cap(const MainMaps& maps, const ChainParams& p, cudaStream_t s);
 cudaError_t main_cap_kernel_setup();
+cudaError_t launch_main_slopes(const MainMaps& maps, const ChainParams& p, cudaStream_t s);
+cudaError_t main_slopes_kernel_setup();
 // A mask plan (score.cuh) from row ranges (row_lo, row_hi) or from documents.
 struct MaskPlanArgs {
   int B, Sq, Skv;

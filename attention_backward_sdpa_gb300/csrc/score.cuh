@@ -213,7 +213,7 @@ __device__ __forceinline__ bool mod_small(const ModCap& cap, float largest) {
 //
 // The straight pass, for a half without a mask or |.| and with mod_small(), in which the
 // exponentials (a quarter of the FMA rate) run under the neighbouring pairs' polynomials.
-template <int MOD, bool F16>
+template <int MOD, bool F16, bool SLOPES>
 __device__ __forceinline__ void mod_replay_straight(const ModTile& tile, int h, const CapCoef& coef, const ModCap& cap,
                                                     const float* n_lse, const uint32_t (&r)[32], uint64_t (&P)[16],
                                                     uint32_t (&w)[16]) {
@@ -234,8 +234,8 @@ __device__ __forceinline__ void mod_replay_straight(const ModTile& tile, int h, 
 #pragma unroll
     for (int i = 0; i < SIDE; i += 2) {
       const ulonglong2 l = l2[(blk * SIDE + i) / 2];
-      x[i] = f2_fma(t[i], cap.c2, f2_add(l.x, bias2));
-      x[i + 1] = f2_fma(t[i + 1], cap.c2, f2_add(l.y, bias2));
+      x[i] = f2_fma(t[i], cap.c2, SLOPES ? f2_add(l.x, bias2) : l.x);
+      x[i + 1] = f2_fma(t[i + 1], cap.c2, SLOPES ? f2_add(l.y, bias2) : l.y);
     }
 #pragma unroll
     for (int i = 0; i < SIDE; ++i) {
@@ -255,7 +255,7 @@ __device__ __forceinline__ void mod_replay_straight(const ModTile& tile, int h, 
 }
 
 // ... and any other half, step by step.
-template <int MOD, bool F16>
+template <int MOD, bool F16, bool SLOPES>
 __device__ __forceinline__ void mod_replay_steps(const ModTile& tile, int h, bool small, const CapCoef& coef,
                                                  const ModCap& cap, const float* n_lse, uint32_t (&r)[32],
                                                  uint64_t (&P)[16], uint32_t (&w)[16]) {
@@ -286,7 +286,7 @@ __device__ __forceinline__ void mod_replay_steps(const ModTile& tile, int h, boo
     P[2 * i4] = f2_fma(f2_pack(r[4 * i4], r[4 * i4 + 1]), cap.c2, l.x);
     P[2 * i4 + 1] = f2_fma(f2_pack(r[4 * i4 + 2], r[4 * i4 + 3]), cap.c2, l.y);
   }
-  if (tile.slope2 != 0.f) {
+  if (SLOPES && tile.slope2 != 0.f) {
     // -slope2 |dist + i| with the row statistics' -slope2 i taken back.
     const float i0 = h ? 32.f : 0.f;
 #pragma unroll

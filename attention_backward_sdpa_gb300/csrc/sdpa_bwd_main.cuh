@@ -199,8 +199,8 @@ __device__ __forceinline__ uint32_t fake_nvfp4_p_pair(float p0, float p1, float 
 // BIAS adds the additive bias to the replay and writes dBias (when p.dbias).
 // QAT writes G3's P^T fake-quantized to NVFP4. F16: fp16 io tensors (and
 // fp16 P^T / dS^T MMA operands) instead of bf16. MOD (MOD_ROWS,
-// MOD_CAP): modified scores (score.cuh).
-template <int D, bool DS_OUT, bool BIAS, bool QAT = false, bool F16 = false, int MOD = MOD_NONE>
+// MOD_CAP): modified scores (score.cuh), SLOPES: with distance slopes.
+template <int D, bool DS_OUT, bool BIAS, bool QAT = false, bool F16 = false, int MOD = MOD_NONE, bool SLOPES = false>
 __global__ void __launch_bounds__(MAIN_THREADS, 1)
     sdpa_bwd_main(const __grid_constant__ MainMaps maps, const ChainParams p) {
   using L = MainLayout<D, DS_OUT>;
@@ -714,7 +714,8 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
     // and with a cap on that route (MOD_LOOP) the straight pass and the dS step loop too.
     // Main kernel, B 1, Hq 32, Hkv 8, S 4096, causal: with a cap 430 -> 362 us (D 64 389 ->
     // 323), 2 x 16 heads in 9 documents 149 -> 142. MOD_LOOP without a cap costs (308 ->
-    // 325), as does rolling on the dS route (276 -> 304), whose code is shorter.
+    // 325), as does rolling on the dS route (276 -> 304), whose code is shorter. (Without the
+    // slopes' code, which has kernels of its own, 359 us, and 377 without MOD_LOOP.)
     constexpr bool MOD_LOOP = MOD == MOD_CAP && !DS_OUT;
     uint64_t Pa[MOD ? BQ / 4 : 1], Pb[MOD ? BQ / 4 : 1] = {};
     CapCoef coef;
@@ -744,7 +745,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
     if constexpr (MOD) {
       if (n > 0) {
         while (mod_r >= n1) mod_r -= n1, ++mod_h;
-        if (p.mods.slopes != nullptr && mod_h < p.gsz) slope2 = p.mods.slopes[bh0 - b * p.Hq + mod_h] * LOG2E_F;
+        if (SLOPES && mod_h < p.gsz) slope2 = p.mods.slopes[bh0 - b * p.Hq + mod_h] * LOG2E_F;
       }
     }
     for (int t = slot; t < n && ok; t += 2) {
@@ -761,7 +762,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
         mod_r += 2;
         if (mod_r >= n1) {
           while (mod_r >= n1) mod_r -= n1, ++mod_h;
-          if (p.mods.slopes != nullptr && mod_h < p.gsz) slope2 = p.mods.slopes[bh0 - b * p.Hq + mod_h] * LOG2E_F;
+          if (SLOPES && mod_h < p.gsz) slope2 = p.mods.slopes[bh0 - b * p.Hq + mod_h] * LOG2E_F;
         }
       }
 
@@ -782,12 +783,12 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
           tmem_ld_wait(rb);
           // One choice for the tile (a choice per half: main kernel of bwd_capped_gqa 324 us
           // against 282).
-          straight = mt.full[0] && mt.full[1] && mt.ahead[0] &&
+          straight = mt.full[0] && mt.full[1] && (!SLOPES || mt.ahead[0]) &&
                      (MOD != MOD_CAP || mod_small(cap, fmaxf(mod_largest(ra), mod_largest(rb))));
           if (straight) {
-            mod_replay_straight<MOD, F16>(mt, 0, coef, cap, qs, ra, Pa, w);
+            mod_replay_straight<MOD, F16, SLOPES>(mt, 0, coef, cap, qs, ra, Pa, w);
             tmem_st16(t_lane + L::col_s(slot), w);
-            mod_replay_straight<MOD, F16>(mt, 1, coef, cap, qs, rb, Pb, w);
+            mod_replay_straight<MOD, F16, SLOPES>(mt, 1, coef, cap, qs, rb, Pb, w);
             tmem_st16(t_lane + L::col_s(slot) + 16, w);
           }
         }
@@ -803,8 +804,8 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
             }
             const bool small = MOD != MOD_CAP || mod_small(cap, mod_largest(r));
             const ModHalf m = mod_half(mt, h);
-            if (MOD_LOOP && small && m.full && m.ahead) mod_replay_straight<MOD, F16>(mt, h, coef, cap, qs, r, Pb, w);
-            else mod_replay_steps<MOD, F16>(mt, h, small, coef, cap, qs, r, Pb, w);
+            if (MOD_LOOP && small && m.full && (!SLOPES || m.ahead)) mod_replay_straight<MOD, F16, SLOPES>(mt, h, coef, cap, qs, r, Pb, w);
+            else mod_replay_steps<MOD, F16, SLOPES>(mt, h, small, coef, cap, qs, r, Pb, w);
             __syncwarp();
             tmem_st16(t_lane + L::col_s(slot) + 16 * h, w);
           }
@@ -1039,14 +1040,14 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
   }
 }
 
-template <int D, bool DS_OUT, bool BIAS, bool QAT = false, bool F16 = false, int MOD = MOD_NONE>
+template <int D, bool DS_OUT, bool BIAS, bool QAT = false, bool F16 = false, int MOD = MOD_NONE, bool SLOPES = false>
 static cudaError_t set_main_smem() {
-  return cudaFuncSetAttribute(sdpa_bwd_main<D, DS_OUT, BIAS, QAT, F16, MOD>,
+  return cudaFuncSetAttribute(sdpa_bwd_main<D, DS_OUT, BIAS, QAT, F16, MOD, SLOPES>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize, MainLayout<D, DS_OUT>::BYTES);
 }
 
 // One CTA per (key tile, head group) work unit.
-template <bool BIAS, bool F16 = false, int MOD = MOD_NONE>
+template <bool BIAS, bool F16 = false, int MOD = MOD_NONE, bool SLOPES = false>
 static cudaError_t launch_main_variant(const MainMaps& maps, const ChainParams& p, cudaStream_t s) {
   const dim3 grid((unsigned)(p.n_kt * p.B * p.Hkv * p.n_part));
   const dim3 block(MAIN_THREADS);
@@ -1058,20 +1059,20 @@ static cudaError_t launch_main_variant(const MainMaps& maps, const ChainParams& 
   // D_qk = D_v up to 64 runs on the 64-column kernels, up to 128 on the 128-column
   // ones: TMA zero-fills the columns past D on loads and drops them on stores.
   if (p.Dqk <= 64)
-    return launch_kernel(sdpa_bwd_main<64, false, BIAS, false, F16, MOD>, grid, block,
+    return launch_kernel(sdpa_bwd_main<64, false, BIAS, false, F16, MOD, SLOPES>, grid, block,
                          MainLayout<64, false>::BYTES, s, pdl, maps, p);
   if (p.ds_route)
-    return launch_kernel(sdpa_bwd_main<128, true, BIAS, false, F16, MOD>, grid, block,
+    return launch_kernel(sdpa_bwd_main<128, true, BIAS, false, F16, MOD, SLOPES>, grid, block,
                          MainLayout<128, true>::BYTES, s, pdl, maps, p);
-  return launch_kernel(sdpa_bwd_main<128, false, BIAS, false, F16, MOD>, grid, block,
+  return launch_kernel(sdpa_bwd_main<128, false, BIAS, false, F16, MOD, SLOPES>, grid, block,
                        MainLayout<128, false>::BYTES, s, pdl, maps, p);
 }
 
-template <bool BIAS, bool F16 = false, int MOD = MOD_NONE>
+template <bool BIAS, bool F16 = false, int MOD = MOD_NONE, bool SLOPES = false>
 static cudaError_t main_variant_setup() {
-  cudaError_t e = set_main_smem<64, false, BIAS, false, F16, MOD>();
-  if (e == cudaSuccess) e = set_main_smem<128, false, BIAS, false, F16, MOD>();
-  if (e == cudaSuccess) e = set_main_smem<128, true, BIAS, false, F16, MOD>();
+  cudaError_t e = set_main_smem<64, false, BIAS, false, F16, MOD, SLOPES>();
+  if (e == cudaSuccess) e = set_main_smem<128, false, BIAS, false, F16, MOD, SLOPES>();
+  if (e == cudaSuccess) e = set_main_smem<128, true, BIAS, false, F16, MOD, SLOPES>();
   return e;
 }
 

@@ -1,5 +1,5 @@
 // sdpa_bwd_main_cap.cu -- the main kernels (sdpa_bwd_main.cuh) with capped scores
-// (score.cuh), for both io types, in their own translation unit so that they compile
+// (score.cuh) and no slopes, for both io types, in their own translation unit so that they compile
 // in parallel with the others.
 #include "sdpa_bwd_main.cuh"
 

@@ -450,11 +450,11 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
         if constexpr (MOD) {
           const bool small = MOD != MOD_CAP || mod_small(cap, fmaxf(mod_largest(ra), mod_largest(rb)));
           if (small && mt.full[0] && mt.full[1] && mt.ahead[0]) {
-            mod_replay_straight<MOD, F16>(mt, 0, coef, cap, qs, ra, Pa, pw[0]);
-            mod_replay_straight<MOD, F16>(mt, 1, coef, cap, qs, rb, Pb, pw[1]);
+            mod_replay_straight<MOD, F16, true>(mt, 0, coef, cap, qs, ra, Pa, pw[0]);
+            mod_replay_straight<MOD, F16, true>(mt, 1, coef, cap, qs, rb, Pb, pw[1]);
           } else {
-            mod_replay_steps<MOD, F16>(mt, 0, small, coef, cap, qs, ra, Pa, pw[0]);
-            mod_replay_steps<MOD, F16>(mt, 1, small, coef, cap, qs, rb, Pb, pw[1]);
+            mod_replay_steps<MOD, F16, true>(mt, 0, small, coef, cap, qs, ra, Pa, pw[0]);
+            mod_replay_steps<MOD, F16, true>(mt, 1, small, coef, cap, qs, rb, Pb, pw[1]);
           }
         } else {
         const float4* lse4 = reinterpret_cast<const float4*>(qs);
