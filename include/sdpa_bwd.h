@@ -302,8 +302,10 @@ int sdpa_fwd_typed(int io_dtype, const void* q, const void* k, const void* v, vo
  * with O, LSE and the gradients of sdpa_fwd() / sdpa_bwd() on the scores x:
  *     P = exp(x - LSE),  dS = P * (dP - delta) * (1 - tanh(y / softcap)^2).
  * Every row may lose all its keys (O = 0, LSE = -inf or the sink, zero
- * gradients). Values of masked keys must still be finite: a masked weight is an
- * exact 0, and 0 times an infinity or NaN of V, K or dO is NaN.
+ * gradients). A masked pair's score and its dP may overflow or be NaN: its weight and its dS
+ * are an exact 0. But the elements of Q, K, V and dO must be finite also where they are
+ * masked, as in every call of this library: they meet other rows in the products, and 0 times
+ * an infinity or NaN is NaN.
  * tanh is exact to a few fp32 roundings for every score and cap. A distance
  * bias is one fp32 product and sum: |slope * distance| * 2^-24 is lost.
  */
