@@ -512,6 +512,8 @@ def rope_inv_freq(rot_dim: int, base: float = 10000.0, *, scaling: str = "none",
                 r <= low, a linear mix between (the ramp of the YaRN paper, Peng et al.
                 2023; its factor on the scores is rope_fwd's mult =
                 0.1 ln(factor) + 1 on both queries and keys).
+
+    Made on the host and copied to ``device``: once, outside of a graph's capture.
     """
     if rot_dim <= 0 or rot_dim % 2:
         raise ValueError("rot_dim must be even and positive")
