@@ -711,12 +711,14 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
     // instructions per issue, 1.12 on the dS route). So the passes that a mask or large
     // scores take go over the halves in a loop that is not unrolled (one half's registers
     // move over at its second turn), the reduction route's MMAs are issued in rolled loops,
-    // and with a cap on that route (MOD_LOOP) the straight pass and the dS step loop too.
-    // Main kernel, B 1, Hq 32, Hkv 8, S 4096, causal: with a cap 430 -> 362 us (D 64 389 ->
-    // 323), 2 x 16 heads in 9 documents 149 -> 142. MOD_LOOP without a cap costs (308 ->
-    // 325), as does rolling on the dS route (276 -> 304), whose code is shorter. (Without the
-    // slopes' code, which has kernels of its own, 359 us, and 377 without MOD_LOOP.)
-    constexpr bool MOD_LOOP = MOD == MOD_CAP && !DS_OUT;
+    // and on that route, with a cap or without slopes, so does the straight pass of the
+    // replay (MOD_LOOP).
+    // Main kernel, B 1, Hq 32, Hkv 8, S 4096, D 128, causal: with a cap 430 -> 338 us (377
+    // without MOD_LOOP; 359 with the dS step in the loop too), with a prefix plan 307 -> 301;
+    // 2 x 16 heads in 9 documents 149 -> 135. MOD_LOOP costs with slopes alone (304 -> 314)
+    // and on the dS route (cap 271 -> 280, prefix 231 -> 235; documents gain, 77 -> 75.5), as
+    // does rolling the MMAs there (276 -> 304).
+    constexpr bool MOD_LOOP = !DS_OUT && (MOD == MOD_CAP || (MOD == MOD_ROWS && !SLOPES));
     uint64_t Pa[MOD ? BQ / 4 : 1], Pb[MOD ? BQ / 4 : 1] = {};
     CapCoef coef;
     if constexpr (MOD == MOD_CAP) coef = cap_coef(p.mods.cap_c, 1.f);
@@ -875,7 +877,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
       __syncwarp();
       tc_fence_after();
       if constexpr (MOD) {
-        if (!MOD_LOOP && mt.full[0] && mt.full[1]) {
+        if (mt.full[0] && mt.full[1]) {
           uint32_t ra[32], rb[32];
           tmem_ld32(t_lane + L::col_dp(slot), ra);
           tmem_ld32(t_lane + L::col_dp(slot) + 32, rb);
@@ -898,8 +900,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
               for (int i = 0; i < BQ / 4; ++i) Pa[i] = Pb[i];
             }
             const ModHalf m = mod_half(mt, h);
-            if (MOD_LOOP && m.full) mod_ds_pieces<F16, false>(0u, h, Pa, qs + BQ, r, ds_row, row & 7);
-            else mod_ds_pieces<F16, true>(m.see, h, Pa, qs + BQ, r, ds_row, row & 7);
+            mod_ds_pieces<F16, true>(m.see, h, Pa, qs + BQ, r, ds_row, row & 7);
             __syncwarp();
           }
         }
