@@ -388,6 +388,11 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s, int num_sms);
 cudaError_t launch_nvfp4_fake_quant(const void* x, void* y, long long n_blocks, int num_sms,
                                     cudaStream_t s);
 
+// `pdl`: the launch may start while the stream's previous kernel drains. A kernel launched so
+// waits for the previous grid (pdl_wait_prior_grid) in every CTA, also in one that has nothing
+// to do: the next kernel of the chain waits for this grid only and counts on all before it.
+// A call in which no row sees a key has no other CTAs, and without their wait the dQ
+// kernels would start before the preprocess has cleared their accumulator and ticket.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                                  cudaStream_t stream, bool pdl, Args&&... args) {

@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
         zero_unvisited_dbias_blocks(p, b0, b0 * p.Hq + hk0 * p.G + (gi0 % p.n_part) * p.gsz, p.gsz, kt0,
                                     lo0, hi0, threadIdx.x, blockDim.x);
       }
+      pdl_wait_prior_grid();  // (common.cuh, launch_kernel: no CTA leaves without it)
       return;
     }
   }

@@ -149,15 +149,17 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
                         hi0);
     if constexpr (MOD) planned_query_tiles(p.mods, b0, kt0, p.n_kt, lo0, hi0);
     if (hi0 < lo0) {
-      if (blockIdx.x % SPLIT != 0) return;  // the first half-unit writes the zeros
-      // gsz = 1: the partial set of a query head is its bh index.
-      // (Under row ranges each empty tile writes its own zeros: they can leave
-      // every key tile of a row empty.)
-      if (MOD || !row_has_visible_pair(Lq0, Lk0))
-        zero_key_tile_rows(p, p.dk_ws ? (long long)bh0 : (long long)b0 * p.Hkv + (bh0 % p.Hq) / p.G,
-                                    kt0 * BN);
-      if (BIAS && p.dbias != nullptr && !p.dbias_red)
-        zero_unvisited_dbias_blocks(p, b0, bh0, 1, kt0, lo0, hi0, threadIdx.x, blockDim.x);
+      if (blockIdx.x % SPLIT == 0) {  // the first half-unit writes the zeros
+        // gsz = 1: the partial set of a query head is its bh index.
+        // (Under row ranges each empty tile writes its own zeros: they can leave
+        // every key tile of a row empty.)
+        if (MOD || !row_has_visible_pair(Lq0, Lk0))
+          zero_key_tile_rows(p, p.dk_ws ? (long long)bh0 : (long long)b0 * p.Hkv + (bh0 % p.Hq) / p.G,
+                                      kt0 * BN);
+        if (BIAS && p.dbias != nullptr && !p.dbias_red)
+          zero_unvisited_dbias_blocks(p, b0, bh0, 1, kt0, lo0, hi0, threadIdx.x, blockDim.x);
+      }
+      pdl_wait_prior_grid();  // (common.cuh, launch_kernel: no CTA leaves without it)
       return;
     }
   }
