@@ -31,8 +31,9 @@ struct ScoreMods {
   int on;              // MOD_NONE, MOD_ROWS or MOD_CAP: which instantiation runs
   float cap_in;        // scale / cap: tanh argument per unit of q . k (0: no cap)
   float cap_log2;      // cap * log2(e)
-  float cap_small;     // |q . k| up to which the polynomial below serves (may be 0)
-  float cap_c[5];      // its coefficients in powers of q . k: TANH_C[i] * cap_in^(2 i + 1)
+  float cap_small;     // |q . k| up to which the polynomial below serves (-1: it never does)
+  float cap_c[5];      // its coefficients in powers of q . k: TANH_C[i] * cap_in^(2 i + 1), or 0 where that
+                       // is no normal fp32 number (cap_small is then lower)
   const float* slopes; // (Hq,) distance slopes, or null
   // Mask plan regions, or null. lo/hi are keys, clamped to [0, S_kv].
   const int2* ranges;  // [B][n_qt * 64] {lo, hi}; rows past S_q hold {0, 0}
@@ -70,7 +71,8 @@ __host__ __device__ inline MaskPlanLayout mask_plan_layout(int B, int n_qt, int 
 // multiplies whatever absolute error small values have):
 //   |y| <= 0.65  an odd polynomial of degree 9 (least-maximum fit of tanh(y) / y in
 //                y^2, 1.5e-7 before its roundings), with the powers of cap_in taken
-//                into its coefficients: 6 multiply-adds, no division;
+//                into its coefficients: 6 multiply-adds, no division (a lower bound for caps whose
+//                powers leave fp32's range);
 //   any y        y N(y^2) / D(y^2), N and D of degree 4, fitted on [0, 8] (6.4e-9,
 //                3.1e-7 with the fp32 roundings), y clamped to [-8, 8] (1 - tanh(8) =
 //                2.3e-7): 12 multiply-adds and a reciprocal.

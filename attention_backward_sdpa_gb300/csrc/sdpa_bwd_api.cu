@@ -373,14 +373,26 @@ int fill_mods(const ModArgs& ma, float scale, int B, int S_q, int S_kv, ScoreMod
     // A cap so far from the scale that their ratio leaves the normal fp32 range
     // would turn the capped scores into zeros or NaN.
     if (!std::isnormal(m.cap_in) || !std::isfinite(m.cap_log2)) return SDPA_ERR_INVALID;
-    // The polynomial with the powers of cap_in in its coefficients, where those (and
-    // the squared scores up to its bound) stay finite.
-    double power = m.cap_in;
-    m.cap_small = (float)std::fmin(TANH_SMALL / (double)m.cap_in, 1e18);
+    // The polynomial with the powers of cap_in in its coefficients, also times cap * log2(e) as
+    // the forward takes them. It serves the scores up to `bound` caps:
+    //   - a small cap's powers may overflow: then the quotient serves every score;
+    //   - a large cap's may leave fp32's normal range (degree 9 from scale / cap = 1e-4 on, past a
+    //     cap of 900 at D 128). Such a term is left out, and the bound lowered to where it is
+    //     below 2^-25 of the value: 0.19 caps without degree 9, 0.09 without 7, 0.02
+    //     without 5, 3e-4 without 3.
+    double power = m.cap_in, bound = TANH_SMALL;
     for (int i = 0; i < 5; ++i, power *= (double)m.cap_in * m.cap_in) {
       m.cap_c[i] = (float)(TANH_C[i] * power);
-      if (!std::isfinite(m.cap_c[i] * m.cap_log2)) m.cap_small = -1.f;  // the quotient serves every score
+      const float in_log2 = m.cap_c[i] * m.cap_log2;
+      if (!std::isfinite(in_log2) || (i == 0 && !std::isnormal(in_log2))) {
+        bound = -1.0;
+      } else if (!std::isnormal(m.cap_c[i]) || !std::isnormal(in_log2)) {
+        m.cap_c[i] = 0.f;
+        bound = std::fmin(bound, std::pow(std::exp2(-25.0) / std::fabs(TANH_C[i]), 1.0 / (2 * i)));
+      }
     }
+    // (1e18: a score's square stays finite.)
+    m.cap_small = bound > 0.0 ? (float)std::fmin(bound / (double)m.cap_in, 1e18) : -1.f;
   }
   if (ma.plan) {
     if (S_q == 0 || S_kv == 0) return SDPA_ERR_INVALID;  // there is no plan of no rows or no keys

@@ -308,6 +308,9 @@ int sdpa_fwd_typed(int io_dtype, const void* q, const void* k, const void* v, vo
  * an infinity or NaN is NaN.
  * tanh is exact to a few fp32 roundings for every score and cap. A distance
  * bias is one fp32 product and sum: |slope * distance| * 2^-24 is lost.
+ * What a score loses to fp32, a few times |x| * 2^-24, its weight exp(x - LSE) takes as a
+ * factor, as in every call of this library: past |x| of 2^23 or so weights say
+ * nothing any more, and they may overflow.
  */
 
 /* Bytes of a mask plan for B batch rows of S_q queries over S_kv keys (0 for sizes that

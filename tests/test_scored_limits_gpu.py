@@ -1,10 +1,12 @@
 """Attention with modified scores at the ends of its ranges, on the GPU against the
-64-bit reference: calls in which no row sees a key."""
+64-bit reference: calls in which no row sees a key, caps far above the usual scores.
+Bounds: scored_reference."""
 import math
 
 import pytest
 import torch
 
+from scored_reference import G23, Case, assert_within
 from test_scored_gpu import _sdpa
 
 pytestmark = pytest.mark.gpu
@@ -41,3 +43,47 @@ def test_a_call_in_which_no_row_sees_a_key(deterministic, how, dims):
         for name, t in zip(("dq", "dk", "dv"), got):
             assert (t == 0).all(), name
     sdpa.check_device_status()
+
+
+class OneColumn(Case):
+    """Queries and keys with one column that is not 0, keys of ones: a score is one exact
+    product, so that scores of any size keep a small bound. What is left of a score's error
+    is relative: scale / cap, the cap in log2 units and their products round to fp32 (5 roundings),
+    the tanh is off by 3.1e-7 with its own roundings (5 more), and the exponent's argument rounds once: 11
+    half units of fp32 of the largest capped score, taken as 6 units."""
+
+    def __init__(self, *a, share, **kw):
+        super().__init__(*a, **kw)
+        y = share * self.softcap / self.scale  # q . k: scale * q . k is `share` caps
+        self.q = torch.zeros_like(self.q)
+        self.q[..., 0] = (y * torch.linspace(-1.0, 1.0, self.Sq)).to(self.io)
+        self.k = torch.zeros_like(self.k)
+        self.k[..., 0] = 1.0
+
+    def head(self, b, h):
+        q, k, v, x, f, _ = super().head(b, h)
+        return q, k, v, x, f, 6 * G23 * x[torch.isfinite(x)].abs().max().item()
+
+
+@pytest.mark.parametrize("dims", [(64, 64), (80, 80), (128, 128), (192, 128), (256, 256)])
+@pytest.mark.parametrize("share", [0.2, 0.64, 2.5])
+@pytest.mark.parametrize("softcap,io", [(50.0, torch.bfloat16), (900.0, torch.float16), (2e3, torch.float16), (5e3, torch.bfloat16),
+                                        (1e4, torch.bfloat16), (1e6, torch.bfloat16)])
+def test_scores_near_a_large_cap(softcap, io, share, dims):
+    """Scores up to 0.2, 0.64 (under the polynomial's bound) and 2.5 caps: LSE holds the capped score
+    itself, and the backward gets the exact one."""
+    if io == torch.float16 and share * softcap * 16 > 6e4:
+        pytest.skip("no such fp16 score")
+    case = OneColumn(1, 2, 1, 150, 391, *dims, io=io, seed=40, softcap=softcap, share=share)
+    sdpa = _sdpa()
+    q, k, v, do = (t.cuda() for t in (case.q, case.k, case.v, case.do))
+    o, lse = sdpa.sdpa_fwd(q, k, v, softcap=softcap)
+    ro, rl, bo, bl = case.forward()
+    assert_within("o", o, ro, bo)
+    assert_within("lse", lse, rl, bl)
+    o, lse = ro.to(io), rl.float()
+    ref, bounds = case.backward(o, lse)
+    for det in (False, True):
+        got = sdpa.sdpa_bwd(q, k, v, o.cuda(), do, lse.cuda(), softcap=softcap, deterministic=det)
+        for name, g, r, b in zip(("dq", "dk", "dv"), got, ref, bounds):
+            assert_within(f"{name} (deterministic={det})", g, r, b)
