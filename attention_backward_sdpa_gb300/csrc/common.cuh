@@ -157,13 +157,16 @@ struct ModKey {
   int lo_max, hi_min, lo_min, hi_max;  // over the warp: what all and what any of its keys see
   bool row_ranges;                     // the plan's rows are not neighbours: each tile's own ranges decide
 };
-__device__ __forceinline__ ModKey mod_key(const ChainParams& p, int b, int k, int Lk, int diag) {
+__device__ __forceinline__ ModKey mod_key(const ChainParams& p, int b, int k, int Lq, int Lk, int diag) {
   ModKey m;
   m.k = k;
   m.k_last = __reduce_max_sync(0xffffffffu, k);
   long long lo = 0, hi = INT_MAX;
   if (p.causal) lo = max(lo, (long long)k - diag - max(p.window_right, 0));
   if (p.window_left >= 0) hi = min(hi, (long long)k - diag + p.window_left);
+  // Rows past the length: their statistics alone (LSE as +inf, delta 0) leave NaN of a score or
+  // dP that overflows.
+  if (Lq < p.Sq) hi = min(hi, (long long)Lq - 1);
   m.row_ranges = false;
   if (p.mods.k_rows != nullptr) {
     m.row_ranges = p.mods.k_exact[b] == 0;

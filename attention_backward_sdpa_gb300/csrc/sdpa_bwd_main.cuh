@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(MAIN_THREADS, 1)
     ModKey mk;
     ModCap cap;
     if constexpr (MOD) {
-      mk = mod_key(p, b, k, Lk, diag);
+      mk = mod_key(p, b, k, Lq, Lk, diag);
       cap = mod_cap(p.mods, p.scale_log2);
     }
     const float scale_log2 = p.scale_log2;

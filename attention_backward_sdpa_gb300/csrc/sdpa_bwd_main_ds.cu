@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(ds_kernel::THREADS, 1)
     ModCap cap;
     float slope2 = 0.f;
     if constexpr (MOD) {
-      mk = mod_key(p, b, k, Lk, diag);
+      mk = mod_key(p, b, k, Lq, Lk, diag);
       cap = mod_cap(p.mods, p.scale_log2);
       if (p.mods.slopes != nullptr) slope2 = p.mods.slopes[h] * 1.4426950408889634f;
     }

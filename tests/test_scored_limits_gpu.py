@@ -1,13 +1,13 @@
 """Attention with modified scores at the ends of its ranges, on the GPU against the
-64-bit reference: calls in which no row sees a key, caps far above the usual scores.
-Bounds: scored_reference."""
+64-bit reference: calls in which no row sees a key, caps far above the usual scores, padded
+rows of any finite values. Bounds: scored_reference."""
 import math
 
 import pytest
 import torch
 
 from scored_reference import G23, Case, assert_within
-from test_scored_gpu import _sdpa
+from test_scored_gpu import _kw, _plan, _sdpa
 
 pytestmark = pytest.mark.gpu
 
@@ -86,4 +86,37 @@ def test_scores_near_a_large_cap(softcap, io, share, dims):
     for det in (False, True):
         got = sdpa.sdpa_bwd(q, k, v, o.cuda(), do, lse.cuda(), softcap=softcap, deterministic=det)
         for name, g, r, b in zip(("dq", "dk", "dv"), got, ref, bounds):
+            assert_within(f"{name} (deterministic={det})", g, r, b)
+
+
+@pytest.mark.parametrize("mods", ["cap", "slopes", "both", "rows"])
+@pytest.mark.parametrize("dims", [(64, 64), (128, 128), (192, 128), (256, 256)])
+@pytest.mark.parametrize("L", [1, 100, 128])
+def test_padded_query_rows_may_be_huge(L, dims, mods):
+    """Query rows past the length carry the io type's largest values in Q and dO: their
+    scores and dP overflow to infinities and NaN, and must not reach any gradient."""
+    S, Skv = 200, 140
+    case = Case(1, 4, 2, S, Skv, *dims, seed=41, softcap=8.0 if mods in ("cap", "both") else 0.0,
+                slopes=[0.1, 1.0, 0.0, 0.02] if mods in ("slopes", "both") else None,
+                rows=[[(0, Skv)] * S] if mods == "rows" else None)
+    most = torch.finfo(case.io).max
+    sign = torch.where(torch.rand(S - L, 1, generator=torch.Generator().manual_seed(2)) < 0.5, -most, most)
+    case.q[:, :, L:], case.do[:, :, L:] = sign.to(case.io), sign.flip(0).to(case.io)
+    case.lens_q = [L]
+    sdpa = _sdpa()
+    q, k, v, do = (t.cuda() for t in (case.q, case.k, case.v, case.do))
+    kw = _kw(case, _plan(case))
+    o, lse = sdpa.sdpa_fwd(q, k, v, **kw)
+    assert (o[:, :, L:] == 0).all() and (lse[:, :, L:] == -math.inf).all()
+    got = {det: sdpa.sdpa_bwd(q, k, v, o, do, lse, deterministic=det, **kw)
+           for det in ((False, True) if mods != "rows" or dims[0] >= 128 else (False,))}
+    case.q, case.do, case.Sq, case.lens_q = case.q[:, :, :L], case.do[:, :, :L], L, None
+    case.rows = None
+    ro, rl, bo, bl = case.forward()
+    assert_within("o", o[:, :, :L], ro, bo)
+    assert_within("lse", lse[:, :, :L], rl, bl)
+    ref, bounds = case.backward(o[:, :, :L].cpu(), lse[:, :, :L].cpu())
+    for det, (dq, dk, dv) in got.items():
+        assert (dq[:, :, L:] == 0).all()
+        for name, g, r, b in zip(("dq", "dk", "dv"), (dq[:, :, :L], dk, dv), ref, bounds):
             assert_within(f"{name} (deterministic={det})", g, r, b)
