@@ -615,8 +615,11 @@ def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, 
     _check_launch_device(q)
     if not 0 <= offset <= _INT32 - S:
         raise ValueError("offset must be at least 0, and offset + S at most 2^31")
-    if B > 0 and Hq > 0:
-        rc = lib.sdpa_rope(_IO_CODES[q.dtype], q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out), B, Hq, Hkv, S, D,
+    if B > 0 and Hq + Hkv > 0:
+        x, z, x_out, z_out = q, k, q_out, k_out
+        if Hq == 0:  # the keys alone, as the C call's first tensor
+            x, z, x_out, z_out, sq, so, Hq, Hkv = k, None, k_out, None, sk, sl, Hkv, 0
+        rc = lib.sdpa_rope(_IO_CODES[x.dtype], x.data_ptr(), _addr(z), x_out.data_ptr(), _addr(z_out), B, Hq, Hkv, S, D,
                            _strides(sq[0], sq[1], sq[2], so[0], so[1], so[2], sk[0], sk[1], sk[2], sl[0], sl[1], sl[2]),
                            inv_freq.data_ptr(), rot, mult, _addr(positions),
                            0 if positions is None else positions.dim() - 1, offset, interleaved, inverse,

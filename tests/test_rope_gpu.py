@@ -201,3 +201,19 @@ def test_captured_and_on_another_stream():
         want = sdpa.rope_fwd(q, k, f, offset=start, stream=side)
         torch.cuda.synchronize()
         assert torch.equal(yq, want[0]) and torch.equal(yk, want[1])
+
+
+def test_keys_alone():
+    """No query heads: the keys are rotated all the same."""
+    sdpa = _sdpa()
+    g = torch.Generator().manual_seed(6)
+    k = torch.randn(2, 3, 50, 64, generator=g).bfloat16().cuda()
+    f = sdpa.rope_inv_freq(64)
+    for fn, inverse in ((sdpa.rope_fwd, False), (sdpa.rope_bwd, True)):
+        out = torch.full_like(k, math.nan)
+        yq, yk = fn(k[:, :0], k, f, k_out=out, offset=9)
+        assert yq.shape == (2, 0, 50, 64) and yk is out
+        _close("k", yk, k, f, (torch.arange(50) + 9).expand(2, 50), 1.0, False, inverse)
+    for q, k in ((k[:, :0], k[:, :0]), (k[:, :0], None), (k[:0], k[:0])):  # nothing to rotate
+        yq, yk = sdpa.rope_fwd(q, k, f)
+        assert yq.shape == q.shape and (yk is None if k is None else yk.shape == k.shape)

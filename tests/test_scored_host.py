@@ -214,6 +214,20 @@ def test_rope_argument_checks(fake):  # noqa: F811
     assert len(fake.calls) == n
 
 
+def test_rope_of_keys_alone(fake):  # noqa: F811
+    """Without query heads the keys are the call's first tensor; without any head there is no call."""
+    q, k = torch.zeros(2, 0, 16, 64, dtype=torch.bfloat16), torch.zeros(2, 3, 16, 64, dtype=torch.bfloat16)
+    f = pkg.rope_inv_freq(64, device="cpu")
+    yq, yk = pkg.rope_fwd(q, k.transpose(1, 2).contiguous().transpose(1, 2), f)
+    args = _last(fake, "sdpa_rope")
+    assert args[2] is None and args[3] == yk.data_ptr() and args[4] is None and args[5:10] == (2, 3, 0, 16, 64)
+    assert list(struct.unpack("12q", args[10]))[:6] == [3072, 64, 192, 3072, 1024, 64]
+    assert yq.shape == q.shape and yk.shape == k.shape
+    n = len(fake.calls)
+    pkg.rope_fwd(q, q, f), pkg.rope_fwd(q, None, f), pkg.rope_fwd(k[:0], k[:0], f)
+    assert len(fake.calls) == n
+
+
 def test_inverse_frequencies():
     f = pkg.rope_inv_freq(8, 100.0, device="cpu")
     assert f.dtype == torch.float64
