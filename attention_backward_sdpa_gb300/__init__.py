@@ -140,6 +140,19 @@ def _stream_handle(stream: Optional[torch.cuda.Stream]):
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
+def _empty(shape, dtype: torch.dtype, device: torch.device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A tensor that a call makes. For a call on a stream given to it the memory is that
+    stream's, so that its work comes after whatever held the block before, and the current
+    stream, where the caller has the tensor in hand, is recorded as a user of it: dropped
+    on either side, the block serves nothing else before both have passed that point."""
+    if stream is None or device.type != "cuda":  # (the checks refuse the latter)
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _is(t, dtype, dev: int, shape) -> bool:
     """Whether t is a contiguous tensor of this type, device index and shape: the checks
     of a call in one test. A call whose tensors fail it goes through the checks
@@ -201,12 +214,12 @@ def _check_workspace(workspace) -> int:
     return workspace.numel() * workspace.element_size()
 
 
-def _check_sink(sink, dsink, Hq):
+def _check_sink(sink, dsink, Hq, stream=None):
     """Validates the fp32 (Hq,) sink logits; returns dsink (allocated when None)."""
     if sink.dtype != torch.float32 or not sink.is_cuda or not sink.is_contiguous() \
             or sink.numel() != Hq:
         raise ValueError("sink must be a contiguous fp32 CUDA tensor of Hq elements")
-    dsink = torch.empty_like(sink) if dsink is None else dsink
+    dsink = _empty(sink.shape, sink.dtype, sink.device, stream) if dsink is None else dsink
     if dsink.dtype != torch.float32 or not dsink.is_cuda or not dsink.is_contiguous() \
             or dsink.numel() != Hq:
         raise ValueError("dsink must be a contiguous fp32 CUDA tensor of Hq elements")
@@ -277,12 +290,12 @@ def sdpa_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
     Hkv, Skv = k.shape[1], k.shape[2]
     Dv = v.shape[3]
     fresh = dq is None and dk is None and dv is None  # (outputs made here need no checks)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _empty(k.shape, k.dtype, k.device, stream) if dk is None else dk
+    dv = _empty(v.shape, v.dtype, v.device, stream) if dv is None else dv
     ws_bytes = _check_workspace(workspace)
     if sink is not None:
-        dsink = _check_sink(sink, dsink, Hq)
+        dsink = _check_sink(sink, dsink, Hq, stream)
     dev, q_shape, k_shape, o_shape = q.get_device(), (B, Hq, Sq, Dqk), (B, Hkv, Skv, Dqk), (B, Hq, Sq, Dv)
     if not (q.is_cuda and _is(q, io, dev, q_shape) and _is(k, io, dev, k_shape) and _is(v, io, dev, (B, Hkv, Skv, Dv))
             and _is(o, io, dev, o_shape) and _is(do, io, dev, o_shape)
@@ -325,7 +338,7 @@ def sdpa_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
                                  Dv, sc, causal, bottom_right, window_left, window_right, deterministic,
                                  _addr(seq_q_lens), _addr(seq_kv_lens), _addr(workspace), ws_bytes, _addr(sink),
                                  None if sink is None else dsink.data_ptr(), softcap, _addr(alibi_slopes),
-                                 None if mask_plan is None else mask_plan.buffer.data_ptr(), _stream_handle(stream))
+                                 None if mask_plan is None else mask_plan._on(stream), _stream_handle(stream))
         if rc != 0:
             raise SdpaError(rc, "sdpa_bwd_scored")
         return (dq, dk, dv) + ((dsink,) if sink is not None else ())
@@ -342,8 +355,7 @@ def sdpa_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
             if bias_grad:
                 if dbias_dtype not in (torch.float32, torch.bfloat16, torch.float16):
                     raise ValueError("dbias_dtype must be float32, bfloat16 or float16")
-                dbias = torch.empty(bias.shape, dtype=dbias_dtype, device=bias.device) \
-                    if dbias is None else dbias
+                dbias = _empty(bias.shape, dbias_dtype, bias.device, stream) if dbias is None else dbias
                 if dbias.dtype != dbias_dtype or not dbias.is_cuda or not dbias.is_contiguous() \
                         or tuple(dbias.shape) != tuple(bias.shape):
                     raise ValueError("dbias must be a contiguous CUDA tensor shaped like bias, of dbias_dtype")
@@ -372,7 +384,7 @@ def sdpa_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
         return dq, dk, dv, dsink
     bias_dtype = _check_bias(bias, B, Hq, Sq, Skv)
     if bias_grad:
-        dbias = torch.empty(bias.shape, dtype=torch.float32, device=bias.device) if dbias is None else dbias
+        dbias = _empty(bias.shape, torch.float32, bias.device, stream) if dbias is None else dbias
         if dbias.dtype != torch.float32 or not dbias.is_cuda or not dbias.is_contiguous() \
                 or tuple(dbias.shape) != tuple(bias.shape):
             raise ValueError("dbias must be a contiguous fp32 CUDA tensor shaped like bias")
@@ -404,8 +416,16 @@ class MaskPlan:
     """The key range of every query row of a batch, with the tile summaries that the
     kernels take their loop bounds from; made by mask_plan()."""
 
-    def __init__(self, B: int, Sq: int, Skv: int, buffer: torch.Tensor):
+    def __init__(self, B: int, Sq: int, Skv: int, buffer: torch.Tensor, home: Optional[int] = None):
         self.B, self.Sq, self.Skv, self.buffer = B, Sq, Skv, buffer
+        self._home = home  # the stream whose memory the buffer is, as a handle
+
+    def _on(self, stream: Optional[torch.cuda.Stream]) -> int:
+        """The buffer's address, for work on ``stream`` (None: the current one): recorded as a
+        user of the buffer, so that a plan may be dropped while work that reads it is queued."""
+        if _stream_handle(stream) != self._home:
+            self.buffer.record_stream(torch.cuda.current_stream(self.buffer.device) if stream is None else stream)
+        return self.buffer.data_ptr()
 
     def __repr__(self) -> str:
         return f"MaskPlan(B={self.B}, Sq={self.Sq}, Skv={self.Skv}, device={self.buffer.device})"
@@ -455,18 +475,18 @@ def mask_plan(B: int, Sq: int, Skv: int, *, doc_ids: Optional[torch.Tensor] = No
     if plan is None:
         given = next((t for t in tensors.values() if t is not None), None)
         dev = given.device if given is not None else torch.device("cuda" if device is None else device)
-        plan = MaskPlan(B, Sq, Skv, torch.empty(size, dtype=torch.uint8, device=dev))
+        plan = MaskPlan(B, Sq, Skv, _empty(size, torch.uint8, dev, stream), _stream_handle(stream))
     elif (plan.B, plan.Sq, plan.Skv) != (B, Sq, Skv):
         raise ValueError(f"plan was made for {plan!r}, not for B={B}, Sq={Sq}, Skv={Skv}")
     _check_same_device(plan.buffer, _ref="the plan", **tensors)
     _check_launch_device(plan.buffer)
     if rows:
-        rc = lib.sdpa_mask_plan_rows(_ptr(row_lo), _ptr(row_hi), B, Sq, Skv, _ptr(plan.buffer), size,
+        rc = lib.sdpa_mask_plan_rows(_ptr(row_lo), _ptr(row_hi), B, Sq, Skv, plan._on(stream), size,
                                      _stream_handle(stream))
     else:
         rc = lib.sdpa_mask_plan_docs(_ptr(doc_ids), _ptr(prefix_lens),
                                      int(prefix_lens is not None and prefix_lens.dim() == 2), int(causal), B, Sq,
-                                     _ptr(plan.buffer), size, _stream_handle(stream))
+                                     plan._on(stream), size, _stream_handle(stream))
     if rc != 0:
         raise SdpaError(rc, "sdpa_mask_plan_rows" if rows else "sdpa_mask_plan_docs")
     return plan
@@ -583,7 +603,7 @@ def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, 
         good = q.is_cuda and io in _IO_CODES and sq[3] == 1
         # (Outputs made here need no checks.)
         if q_out is None:
-            q_out, so = torch.empty(shape, dtype=io, device=q.device), (Hq * S * D, S * D, D)
+            q_out, so = _empty(shape, io, q.device, stream), (Hq * S * D, S * D, D)
         else:
             so = q_out.stride()
             good = good and q_out.dtype is io and q_out.get_device() == dev and q_out.shape == shape and so[3] == 1
@@ -595,7 +615,7 @@ def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, 
             Hkv = shape[1]
             good = good and k.dtype is io and k.get_device() == dev and shape == (B, Hkv, S, D) and sk[3] == 1
             if k_out is None:
-                k_out, sl = torch.empty(shape, dtype=io, device=q.device), (Hkv * S * D, S * D, D)
+                k_out, sl = _empty(shape, io, q.device, stream), (Hkv * S * D, S * D, D)
             else:
                 sl = k_out.stride()
                 good = good and k_out.dtype is io and k_out.get_device() == dev and k_out.shape == shape and sl[3] == 1
@@ -680,8 +700,8 @@ def sdpa_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale: Option
     Hkv, Skv = k.shape[1], k.shape[2]
     Dv = v.shape[3]
     fresh = o is None and lse is None  # (outputs made here need no checks)
-    o = torch.empty((B, Hq, Sq, Dv), dtype=io, device=q.device) if o is None else o
-    lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device) if lse is None else lse
+    o = _empty((B, Hq, Sq, Dv), io, q.device, stream) if o is None else o
+    lse = _empty((B, Hq, Sq), torch.float32, q.device, stream) if lse is None else lse
     dev = q.get_device()
     if not (q.is_cuda and _is(q, io, dev, (B, Hq, Sq, Dqk)) and _is(k, io, dev, (B, Hkv, Skv, Dqk))
             and _is(v, io, dev, (B, Hkv, Skv, Dv))
@@ -707,7 +727,7 @@ def sdpa_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale: Option
         rc = lib.sdpa_fwd_scored(_IO_CODES[io], q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
                                  B, Hq, Hkv, Sq, Skv, Dqk, Dv, sc, causal, bottom_right, window_left, window_right,
                                  _addr(seq_q_lens), _addr(seq_kv_lens), _addr(sink), softcap, _addr(alibi_slopes),
-                                 None if mask_plan is None else mask_plan.buffer.data_ptr(), _stream_handle(stream))
+                                 None if mask_plan is None else mask_plan._on(stream), _stream_handle(stream))
         if rc != 0:
             raise SdpaError(rc, "sdpa_fwd_scored")
         return o, lse
@@ -736,7 +756,7 @@ def nvfp4_fake_quant(x: torch.Tensor, out: Optional[torch.Tensor] = None,
     if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or not x.is_cuda \
             or not x.is_contiguous():
         raise ValueError("x must be a contiguous bf16 CUDA tensor")
-    out = torch.empty_like(x) if out is None else out
+    out = _empty(x.shape, x.dtype, x.device, stream) if out is None else out
     _check_bf16("out", out, x.shape)
     _check_same_device(x, out=out)
     _check_launch_device(x)
@@ -775,9 +795,9 @@ def sdpa_bwd_nvfp4_qat(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o_hp: 
         _check_bf16(name, t, shape)
     _check_lse(lse, B, Hq, Sq)
     _check_lens(B, seq_q_lens, seq_kv_lens)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _empty(k.shape, k.dtype, k.device, stream) if dk is None else dk
+    dv = _empty(v.shape, v.dtype, v.device, stream) if dv is None else dv
     _check_bf16("dq", dq, q.shape)
     _check_bf16("dk", dk, k.shape)
     _check_bf16("dv", dv, v.shape)
