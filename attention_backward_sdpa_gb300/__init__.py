@@ -661,8 +661,8 @@ def rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: torch.Tensor,
     projection's (B,S,H,D) output goes in as a transposed view and comes out contiguous
     (B,H,S,D) for sdpa_fwd. ``inv_freq``: fp64 CUDA vector (rope_inv_freq).
     ``positions``: int32 (S,) or (B,S), else offset .. offset + S - 1. Pairs are columns
-    (i, i + rot/2), or (2i, 2i+1) when ``interleaved``. Returns (q_out, k_out); the
-    outputs may be the inputs (in place).
+    (i, i + rot/2), or (2i, 2i+1) when ``interleaved``. Returns (q_out, k_out). An
+    output may be its own input (the same tensor: in place) and overlaps nothing else.
     """
     return _rope(q, k, inv_freq, mult, positions, offset, interleaved, False, q_out, k_out, stream)
 

@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -655,6 +656,57 @@ int sdpa_bwd(const void* q, const void* k, const void* v, const void* o, const v
 
 namespace {
 
+// The rows of a rotary call's tensor: places in elements, dimensions batch, head, position.
+struct RopeRows {
+  long long base, end;  // first element, and one past the last
+  long long st[3];
+  int ext[3], D;
+};
+RopeRows rope_rows(const void* ptr, const long long* st, int B, int H, int S, int D) {
+  RopeRows r{(long long)(reinterpret_cast<uintptr_t>(ptr) / 2), 0, {st[0], st[1], st[2]}, {B, H, S}, D};
+  r.end = r.base + D;
+  for (int j = 0; j < 3; ++j)
+    if (r.ext[j] > 1) r.end += st[j] * (r.ext[j] - 1);
+  return r;
+}
+bool same_rows(const RopeRows& a, const RopeRows& b) {
+  bool same = a.base == b.base;
+  for (int j = 0; j < 3; ++j) same = same && a.ext[j] == b.ext[j] && (a.ext[j] == 1 || a.st[j] == b.st[j]);
+  return same;
+}
+// Whether rows `delta` apart come within D of one another by up to `back[j]` steps back and
+// `on[j]` steps on of the strides st, descending: of each only those few are tried that the smaller
+// ones can make up for.
+bool steps_meet(const long long* st, const int* back, const int* on, int n, long long D, long long delta) {
+  if (n == 0) return delta < D && -delta < D;
+  long long reach = D;
+  for (int j = 1; j < n; ++j) reach += st[j] * std::max(back[j], on[j]);
+  const long long lo = std::max(floor_div(-delta - reach, st[0]), -(long long)back[0]);
+  const long long hi = std::min(floor_div(reach - delta, st[0]) + 1, (long long)on[0]);
+  for (long long k = lo; k <= hi; ++k)
+    if (steps_meet(st + 1, back + 1, on + 1, n - 1, D, delta + k * st[0])) return true;
+  return false;
+}
+// Whether an output y shares an element with x: exact for tensors that step alike (slices of
+// one projection), and taken to be so for others whose places interleave.
+bool rows_meet(const RopeRows& x, const RopeRows& y) {
+  if (x.end <= y.base || y.end <= x.base) return false;
+  long long st[3];
+  int back[3], on[3], n = 0;
+  for (int j = 0; j < 3; ++j) {
+    if (x.ext[j] == 1 && y.ext[j] == 1) continue;
+    if (x.ext[j] > 1 && y.ext[j] > 1 && x.st[j] != y.st[j]) return true;
+    const long long s = y.ext[j] > 1 ? y.st[j] : x.st[j];
+    if (s <= 0) return true;
+    int at = n++;
+    for (; at > 0 && st[at - 1] < s; --at) st[at] = st[at - 1], back[at] = back[at - 1], on[at] = on[at - 1];
+    st[at] = s;
+    back[at] = x.ext[j] - 1;
+    on[at] = y.ext[j] - 1;
+  }
+  return steps_meet(st, back, on, n, x.D, y.base - x.base);
+}
+
 int plan_checks(int B, int S_q, int S_kv) {
   if (B <= 0 || S_q <= 0 || S_kv <= 0) return SDPA_ERR_INVALID;
   const long long limit = 1ll << 30;  // rows, tiles and (position + prefix) stay 32-bit
@@ -938,6 +990,17 @@ int sdpa_rope(int io_dtype, const void* q, const void* k, void* q_out, void* k_o
   if (reinterpret_cast<uintptr_t>(inv_freq) % 8 != 0 || reinterpret_cast<uintptr_t>(positions) % 4 != 0)
     return SDPA_ERR_ALIGN;
   if (!positions && (offset < 0 || (long long)offset + S > 1ll << 31)) return SDPA_ERR_INVALID;
+  // An output is its own input, element by element, or shares no element with any tensor.
+  for (int i = 0; i < 2; ++i) {
+    if (Hs[i] == 0) continue;
+    const RopeRows y = rope_rows(ys[i], a.ys + 3 * i, B, Hs[i], S, D);
+    for (int j = 0; j < 2; ++j) {
+      if (Hs[j] == 0) continue;
+      const RopeRows x = rope_rows(xs[j], a.xs + 3 * j, B, Hs[j], S, D);
+      if (!(i == j && same_rows(x, y)) && rows_meet(x, y)) return SDPA_ERR_INVALID;
+      if (i < j && rows_meet(y, rope_rows(ys[j], a.ys + 3 * j, B, Hs[j], S, D))) return SDPA_ERR_INVALID;
+    }
+  }
   a.freq = inv_freq;
   a.positions = positions;
   a.pos_bstride = positions_per_batch ? S : 0;

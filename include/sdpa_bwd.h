@@ -401,8 +401,10 @@ int sdpa_bwd_scored(int io_dtype, const void* q, const void* k, const void* v, c
  *   q, k, q_out, k_out  device 16-bit tensors of H_q and H_kv heads, any strides of batch,
  *               head and position, columns contiguous; 2-byte aligned (16-byte accesses
  *               where rot_dim is a multiple of 16, D of 8 and every row of every
- *               tensor 16-byte aligned; else 8- or 4-byte ones, or single elements). H_kv = 0: q alone. An output may be its own input
- *               (same pointer and strides); any other overlap is undefined.
+ *               tensor 16-byte aligned; else 8- or 4-byte ones, or single elements).
+ *               H_kv = 0: q alone. An output may be its own input (same pointer and strides);
+ *               any other element that it shares with an input or output is refused
+ *               (SDPA_ERR_INVALID), and so are places that interleave at different strides.
  *   strides     host array of 12: batch, head, position strides in elements of q, q_out, k,
  *               k_out in this order. Input strides must not be negative; output rows must
  *               not overlap (SDPA_ERR_INVALID).

@@ -217,3 +217,29 @@ def test_keys_alone():
     for q, k in ((k[:, :0], k[:, :0]), (k[:, :0], None), (k[:0], k[:0])):  # nothing to rotate
         yq, yk = sdpa.rope_fwd(q, k, f)
         assert yq.shape == q.shape and (yk is None if k is None else yk.shape == k.shape)
+
+
+@pytest.mark.parametrize("layout", ["(B, S, H, D)", "(B, H, S, D)"])
+@pytest.mark.parametrize("Hkv", [1, 3])
+def test_neighbouring_slices_of_one_buffer(layout, Hkv):
+    """Outputs beside their inputs in one buffer: every slice is written alone, in place or not."""
+    sdpa = _sdpa()
+    B, S, Hq, D = 2, 29, 4, 64
+    g = torch.Generator().manual_seed(7)
+    room = torch.randn(B, S, 2 * (Hq + Hkv), D, generator=g).bfloat16().cuda()
+    if layout == "(B, H, S, D)":
+        room = room.transpose(1, 2).contiguous().transpose(1, 2)
+    f = sdpa.rope_inv_freq(D)
+    cut = (0, Hq, Hq + Hkv, 2 * Hq + Hkv, 2 * (Hq + Hkv))
+    q, k, yq, yk = (room[:, :, a:b].transpose(1, 2) for a, b in zip(cut, cut[1:]))
+    want = sdpa.rope_fwd(q, k, f)
+    x = room.clone()
+    sdpa.rope_fwd(q, k, f, q_out=yq, k_out=yk)
+    assert torch.equal(yq, want[0]) and torch.equal(yk, want[1]) and torch.equal(room[:, :, :Hq + Hkv], x[:, :, :Hq + Hkv])
+    sdpa.rope_fwd(q, k, f, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])
+    before = room.clone()
+    for bad in (dict(q_out=yq, k_out=yq[:, :Hkv]), dict(q_out=q, k_out=q[:, :Hkv]), dict(q_out=yq, k_out=q[:, 1:1 + Hkv])):
+        with pytest.raises(sdpa.SdpaError):
+            sdpa.rope_fwd(q, k, f, **bad)
+        assert torch.equal(room, before)

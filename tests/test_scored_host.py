@@ -129,6 +129,35 @@ def test_rope_refusals(lib):
     assert _rope(lib, strides=[4 * 8 * 64, -8 * 64, 64] + plain + kv) == INVALID  # a negative input stride
 
 
+def test_rope_outputs_that_overlap(lib):
+    """An output shares elements with its own input alone, one for one (all refused: nothing runs)."""
+    B, Hq, Hkv, S, D = 2, 4, 2, 8, 64
+    far = [P + (i << 20) for i in range(4)]  # q, k, q_out, k_out apart from each other
+
+    def call(strides=None, **at):
+        ptr = dict(zip(("q", "k", "qo", "ko"), far))
+        ptr.update(at)
+        return _rope(lib, strides=strides, **ptr)
+
+    row = 2 * D
+    assert call(qo=far[0] + row) == INVALID and call(qo=far[0] + 16) == INVALID     # q, a row or less further on
+    assert call(qo=far[0] + (B * Hq * S - 1) * row) == INVALID                      # its last row
+    assert call(qo=far[1]) == INVALID and call(ko=far[0]) == INVALID                # the other input
+    assert call(ko=far[2]) == INVALID and call(ko=far[2] + 5 * row) == INVALID      # the other output
+    plain, turned = [Hq * S * D, S * D, D], [S * Hq * D, D, Hq * D]                 # (B, H, S, D) and (B, S, H, D)
+    kv = [Hkv * S * D, S * D, D] * 2
+    assert call(strides=plain + turned + kv, qo=far[0]) == INVALID                  # in place, but rows change places
+    assert call(strides=turned + plain + kv, qo=far[0]) == INVALID
+    # A projection's row of Hq + Hkv + Hkv heads: each tensor a slice; the keys one head too low meet the queries.
+    width = (Hq + 2 * Hkv) * D
+    fused = [S * width, D, width]
+    assert call(strides=fused * 4, q=far[0], qo=far[0], k=far[0] + Hq * row, ko=far[0] + (Hq - 1) * row) == INVALID
+    assert call(strides=fused * 4, q=far[0], qo=far[0] + Hkv * row, k=far[1], ko=far[3]) == INVALID
+    # The same places with other strides: not followed row by row.
+    assert call(strides=fused * 2 + fused + [S * width, D, 2 * width], q=far[0], qo=far[0], k=far[0] + Hq * row,
+                ko=far[0] + (Hq + Hkv) * row) == INVALID
+
+
 # ------------------------------------------------------------------ the binding
 def _cpu(B=2, Hq=4, Hkv=2, S=96, D=64, io=torch.bfloat16):
     q, k = torch.zeros(B, Hq, S, D, dtype=io), torch.zeros(B, Hkv, S, D, dtype=io)
