@@ -494,8 +494,8 @@ def mask_plan(B: int, Sq: int, Skv: int, *, doc_ids: Optional[torch.Tensor] = No
 
 def _check_score_mods(q, B, Hq, Sq, Skv, softcap, alibi_slopes, mask_plan, bias, window_left, window_right) -> bool:
     """Whether the call modifies its scores (and then that it may)."""
-    if not 0.0 <= softcap < math.inf:
-        raise ValueError("softcap must be 0 (none) or a positive finite number")
+    if not (softcap == 0.0 or 2.0 ** -126 <= softcap < math.inf):  # (a smaller one may be 0 in fp32: no cap)
+        raise ValueError("softcap must be 0 (none) or a positive finite number, normal in fp32")
     if softcap == 0.0 and alibi_slopes is None and mask_plan is None:
         return False
     if bias is not None:

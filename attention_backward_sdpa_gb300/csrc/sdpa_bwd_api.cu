@@ -363,7 +363,7 @@ struct ModArgs {
 int fill_mods(const ModArgs& ma, float scale, int B, int S_q, int S_kv, ScoreMods& m) {
   m = ScoreMods{};
   if (!ma.on()) return SDPA_OK;
-  if (!(ma.softcap >= 0.f) || !std::isfinite(ma.softcap)) return SDPA_ERR_INVALID;
+  if (ma.softcap != 0.f && !(ma.softcap > 0.f && std::isnormal(ma.softcap))) return SDPA_ERR_INVALID;
   if (reinterpret_cast<uintptr_t>(ma.slopes) % 4 != 0) return SDPA_ERR_ALIGN;
   if (reinterpret_cast<uintptr_t>(ma.plan) % 256 != 0) return SDPA_ERR_ALIGN;
   m.on = ma.softcap > 0.f ? MOD_CAP : MOD_ROWS;

@@ -347,8 +347,8 @@ int sdpa_mask_plan_docs(const int32_t* doc_ids, const int32_t* prefix_lens, int 
 
 /*
  * SDPA forward with modified scores. Arguments of sdpa_fwd_typed() without a bias, then
- *   softcap       cap of the scores, 0 for none. Negative, infinite or NaN caps, and
- *                 caps whose ratio to the scale leaves the normal fp32 range, return
+ *   softcap       cap of the scores, 0 for none. Negative, infinite, NaN or subnormal caps,
+ *                 and caps whose ratio to the scale leaves the normal fp32 range, return
  *                 SDPA_ERR_INVALID.
  *   alibi_slopes  device fp32 (H_q,) finite slopes of any sign, or NULL.
  *   mask_plan     a plan for (B, S_q, S_kv), 256-byte aligned, or NULL.

@@ -42,6 +42,18 @@ def test_caps_that_are_refused(lib, softcap):
     assert _bwd(lib, softcap=softcap) == INVALID
 
 
+def test_caps_below_fp32s_normal_numbers(lib, fake):  # noqa: F811
+    """A cap that rounds to 0 in fp32 would be no cap at all."""
+    assert _fwd(lib, softcap=1e-39, scale=1e-30) == INVALID and _bwd(lib, softcap=1e-39) == INVALID
+    q, k, v, o, do, lse = _cpu()
+    for softcap in (5e-324, 1e-60, 2.0 ** -127):
+        with pytest.raises(ValueError):
+            pkg.sdpa_fwd(q, k, v, softcap=softcap)
+        with pytest.raises(ValueError):
+            pkg.sdpa_bwd(q, k, v, o, do, lse, softcap=softcap)
+    assert not fake.calls
+
+
 def test_cap_far_from_the_scale(lib):
     """scale / cap or cap * log2(e) outside fp32's normal range."""
     assert _fwd(lib, softcap=1e-38, scale=100.0) == INVALID       # the ratio overflows
