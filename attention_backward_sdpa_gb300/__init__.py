@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import operator
 import os
 import struct
 from typing import Optional, Tuple
@@ -330,14 +331,16 @@ def sdpa_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
             # call after one instead of 447 at B 1, Hq 32, S 4096, D 128, deterministic.)
             # A call on a stream given to it leaves this to the library, whose allocation is
             # ordered on that stream.
-            ws_bytes = _scored_workspace(lib, B, Hq, Hkv, Sq, Skv, Dqk, Dv, causal, bottom_right, window_left,
-                                         window_right, deterministic, seq_q_lens is not None or seq_kv_lens is not None)
+            ws_bytes = _scored_workspace(lib, B, Hq, Hkv, Sq, Skv, Dqk, Dv, int(causal), int(bottom_right),
+                                         int(window_left), int(window_right), int(deterministic),
+                                         int(seq_q_lens is not None or seq_kv_lens is not None))
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device) if ws_bytes else None
         rc = lib.sdpa_bwd_scored(_IO_CODES[io], q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(),
                                  lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Sq, Skv, Dqk,
-                                 Dv, sc, causal, bottom_right, window_left, window_right, deterministic,
-                                 _addr(seq_q_lens), _addr(seq_kv_lens), _addr(workspace), ws_bytes, _addr(sink),
-                                 None if sink is None else dsink.data_ptr(), softcap, _addr(alibi_slopes),
+                                 Dv, sc, int(causal), int(bottom_right), int(window_left), int(window_right),
+                                 int(deterministic), _addr(seq_q_lens), _addr(seq_kv_lens), _addr(workspace), ws_bytes,
+                                 _addr(sink), None if sink is None else dsink.data_ptr(), float(softcap),
+                                 _addr(alibi_slopes),
                                  None if mask_plan is None else mask_plan._on(stream), _stream_handle(stream))
         if rc != 0:
             raise SdpaError(rc, "sdpa_bwd_scored")
@@ -641,9 +644,9 @@ def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, 
             x, z, x_out, z_out, sq, so, Hq, Hkv = k, None, k_out, None, sk, sl, Hkv, 0
         rc = lib.sdpa_rope(_IO_CODES[x.dtype], x.data_ptr(), _addr(z), x_out.data_ptr(), _addr(z_out), B, Hq, Hkv, S, D,
                            _strides(sq[0], sq[1], sq[2], so[0], so[1], so[2], sk[0], sk[1], sk[2], sl[0], sl[1], sl[2]),
-                           inv_freq.data_ptr(), rot, mult, _addr(positions),
-                           0 if positions is None else positions.dim() - 1, offset, interleaved, inverse,
-                           _stream_handle(stream))
+                           inv_freq.data_ptr(), rot, float(mult), _addr(positions),
+                           0 if positions is None else positions.dim() - 1, operator.index(offset), bool(interleaved),
+                           inverse, _stream_handle(stream))
         if rc != 0:
             raise SdpaError(rc, "sdpa_rope")
     return q_out, k_out
@@ -725,8 +728,9 @@ def sdpa_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale: Option
     sc = 0.0 if scale is None else float(scale)
     if scored:
         rc = lib.sdpa_fwd_scored(_IO_CODES[io], q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
-                                 B, Hq, Hkv, Sq, Skv, Dqk, Dv, sc, causal, bottom_right, window_left, window_right,
-                                 _addr(seq_q_lens), _addr(seq_kv_lens), _addr(sink), softcap, _addr(alibi_slopes),
+                                 B, Hq, Hkv, Sq, Skv, Dqk, Dv, sc, int(causal), int(bottom_right), int(window_left),
+                                 int(window_right), _addr(seq_q_lens), _addr(seq_kv_lens), _addr(sink),
+                                 float(softcap), _addr(alibi_slopes),
                                  None if mask_plan is None else mask_plan._on(stream), _stream_handle(stream))
         if rc != 0:
             raise SdpaError(rc, "sdpa_fwd_scored")

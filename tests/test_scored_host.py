@@ -6,6 +6,7 @@ import ctypes
 import math
 import struct
 
+import numpy as np
 import pytest
 import torch
 
@@ -194,6 +195,32 @@ def test_scored_routes(fake):  # noqa: F811
     assert _last(fake, "sdpa_fwd_scored")[0] == 2
     pkg.sdpa_fwd(q, k, v, softcap=0.0)
     _last(fake, "sdpa_fwd")
+
+
+def test_numpy_scalars(fake):  # noqa: F811
+    """The scored and rotary calls take the numbers that the plain calls take."""
+    q, k, v, o, do, lse = _cpu()
+    kw = dict(scale=np.float32(0.125), causal=np.bool_(True), bottom_right=np.bool_(False), window_left=np.int64(40),
+              window_right=np.int32(3), softcap=np.float32(30.0))
+    pkg.sdpa_fwd(q, k, v, **kw)
+    args = _last(fake, "sdpa_fwd_scored")
+    assert _taken(fake, "sdpa_fwd_scored", args)
+    pkg.sdpa_bwd(q, k, v, o, do, lse, deterministic=np.bool_(True), **kw)
+    assert _taken(fake, "sdpa_bwd_scored", _last(fake, "sdpa_bwd_scored"))
+    size = [a for n, a in fake.calls if n == "sdpa_bwd_scored_workspace_size"]
+    assert len(size) == 1 and _taken(fake, "sdpa_bwd_scored_workspace_size", size[0])
+    f = pkg.rope_inv_freq(64, device="cpu")
+    pkg.rope_fwd(q, k, f, mult=np.float32(1.5), offset=np.int64(7), interleaved=np.bool_(True))
+    assert _taken(fake, "sdpa_rope", _last(fake, "sdpa_rope"))
+    with pytest.raises(TypeError):
+        pkg.rope_fwd(q, k, f, offset=1.5)
+
+
+def _taken(fake, name, args):  # noqa: F811
+    """Whether ctypes takes the arguments as declared (nothing is called)."""
+    for kind, a in zip(getattr(fake.real, name).argtypes, args):
+        kind.from_param(a)
+    return True
 
 
 def test_scored_argument_checks(fake):  # noqa: F811
