@@ -13,6 +13,7 @@ import torch
 import attention_backward_sdpa_gb300 as pkg
 from scored_reference import Case, doc_ranges, visible
 from test_binding_host import _last, fake  # noqa: F401  (the recording library)
+from test_scored_limits_gpu import fp16_bound
 
 OK, INVALID, UNSUPPORTED, ALIGN, WORKSPACE = range(5)
 P = 1 << 20  # a stand-in pointer, 256-byte aligned; never read (every call is refused)
@@ -381,3 +382,16 @@ def test_reference_against_autograd_and_differences(i):
             # central differences: h^2 times the third derivative (a few units here) and
             # the loss's rounding (1e-14) over h
             assert abs((up - down) / (2 * h) - (a * d).sum()) <= 1e-7 * (1 + (a * d).abs().sum())
+
+
+@pytest.mark.parametrize("S,gain", [(77, 1.0), (333, 3.0), (700, 1.0)])
+def test_the_fp16_bound_sees_one_rounding(S, gain):
+    """Weights rounded once to fp16 are within it; weights rounded to bf16, or a unit off, are not."""
+    case = Case(1, 1, 1, S, S, 64, 64, io=torch.float16, seed=43, gain=gain, softcap=20.0, causal=True)
+    ro, _, bo, _ = case.forward()
+    bound = fp16_bound(case, bo)[0, 0]
+    q, k, v, x, f, e = case.head(0, 0)
+    p = torch.exp(x - x.amax(1, keepdim=True))
+    for weight, fits in ((p.half().double(), True), (p.bfloat16().double(), False), (p.half().double() * (1 + 2.0 ** -9), False)):
+        o = (weight @ v / p.sum(1, keepdim=True)).half().double()
+        assert bool(((o - ro[0, 0]).abs() <= bound).all()) == fits

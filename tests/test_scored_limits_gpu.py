@@ -1,6 +1,6 @@
 """Attention with modified scores at the ends of its ranges, on the GPU against the
 64-bit reference: calls in which no row sees a key, caps far above the usual scores, padded
-rows of any finite values. Bounds: scored_reference."""
+rows of any finite values, fp16 weights. Bounds: scored_reference."""
 import math
 
 import pytest
@@ -120,3 +120,29 @@ def test_padded_query_rows_may_be_huge(L, dims, mods):
         assert (dq[:, :, L:] == 0).all()
         for name, g, r, b in zip(("dq", "dk", "dv"), (dq[:, :, :L], dk, dv), ref, bounds):
             assert_within(f"{name} (deterministic={det})", g, r, b)
+
+
+def fp16_bound(case, bo):
+    """Case.forward's bound of O with one rounding of each fp16 weight: an absolute part of 2^-25
+    for a weight below 2^-14 of the row's reference. The reference is a score of the row (or its
+    sink), whose weight is 1 in the sum that divides O, so the part reaches O times 1 at most.
+    (Case.forward allows 256 times that part, several times everything else at a few hundred keys.)"""
+    size = case.v.double().abs().sum(2).repeat_interleave(case.Hq // case.Hkv, 1)
+    return bo - 255 * 2.0 ** -25 * size[:, :, None]
+
+
+@pytest.mark.parametrize("dims", [(64, 64), (80, 80), (128, 128), (192, 128), (256, 256)])
+@pytest.mark.parametrize("mods", [dict(softcap=20.0), dict(slopes=[0.5, 0.02, 0.0]), dict(softcap=6.0, slopes=[0.5, 0.02, 0.0]),
+                                  dict(rows=True), dict(rows=True, softcap=30.0, sink=True)])
+@pytest.mark.parametrize("S,gain", [(77, 1.0), (333, 3.0), (700, 1.0)])
+def test_fp16_outputs_by_their_own_roundings(S, gain, mods, dims):
+    mods = dict(mods)
+    if mods.pop("rows", False):
+        mods["rows"] = [[(max(0, i // 90 * 90 - 7), min(S, i + 40)) for i in range(S)]] * 2
+    else:
+        mods["causal"] = True
+    case = Case(2, 3, 1, S, S, *dims, io=torch.float16, seed=43, gain=gain, **mods)
+    o, lse = _sdpa().sdpa_fwd(case.q.cuda(), case.k.cuda(), case.v.cuda(), **_kw(case, _plan(case)))
+    ro, rl, bo, bl = case.forward()
+    assert_within("o", o, ro, fp16_bound(case, bo))
+    assert_within("lse", lse, rl, bl)
