@@ -142,16 +142,21 @@ def _stream_handle(stream: Optional[torch.cuda.Stream]):
 
 
 def _empty(shape, dtype: torch.dtype, device: torch.device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
-    """A tensor that a call makes. For a call on a stream given to it the memory is that
-    stream's, so that its work comes after whatever held the block before, and the current
-    stream, where the caller has the tensor in hand, is recorded as a user of it: dropped
-    on either side, the block serves nothing else before both have passed that point."""
+    """A tensor that a call on a stream given to it makes (a call without one takes torch.empty
+    itself, which is 0.6 us less). The memory is that stream's, so that its work comes after
+    whatever held the block before, and the current stream, where the caller has the tensor
+    in hand, is recorded as a user of it: dropped on either side, the block serves nothing
+    else before both have passed that point."""
     if stream is None or device.type != "cuda":  # (the checks refuse the latter)
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(torch.cuda.current_stream(t.device))
     return t
+
+
+def _empty_like(t: torch.Tensor, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    return torch.empty_like(t) if stream is None else _empty(t.shape, t.dtype, t.device, stream)
 
 
 def _is(t, dtype, dev: int, shape) -> bool:
@@ -220,7 +225,7 @@ def _check_sink(sink, dsink, Hq, stream=None):
     if sink.dtype != torch.float32 or not sink.is_cuda or not sink.is_contiguous() \
             or sink.numel() != Hq:
         raise ValueError("sink must be a contiguous fp32 CUDA tensor of Hq elements")
-    dsink = _empty(sink.shape, sink.dtype, sink.device, stream) if dsink is None else dsink
+    dsink = _empty_like(sink, stream) if dsink is None else dsink
     if dsink.dtype != torch.float32 or not dsink.is_cuda or not dsink.is_contiguous() \
             or dsink.numel() != Hq:
         raise ValueError("dsink must be a contiguous fp32 CUDA tensor of Hq elements")
@@ -291,9 +296,9 @@ def sdpa_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
     Hkv, Skv = k.shape[1], k.shape[2]
     Dv = v.shape[3]
     fresh = dq is None and dk is None and dv is None  # (outputs made here need no checks)
-    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
-    dk = _empty(k.shape, k.dtype, k.device, stream) if dk is None else dk
-    dv = _empty(v.shape, v.dtype, v.device, stream) if dv is None else dv
+    dq = _empty_like(q, stream) if dq is None else dq
+    dk = _empty_like(k, stream) if dk is None else dk
+    dv = _empty_like(v, stream) if dv is None else dv
     ws_bytes = _check_workspace(workspace)
     if sink is not None:
         dsink = _check_sink(sink, dsink, Hq, stream)
@@ -599,6 +604,7 @@ _strides = struct.Struct("12q").pack  # (0.1 us on the Arm host, against 1.1 for
 
 def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, k_out, stream):
     lib = load()
+    new = torch.empty if stream is None else functools.partial(_empty, stream=stream)
     try:
         shape, sq = q.shape, q.stride()
         B, Hq, S, D = shape
@@ -606,7 +612,7 @@ def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, 
         good = q.is_cuda and io in _IO_CODES and sq[3] == 1
         # (Outputs made here need no checks.)
         if q_out is None:
-            q_out, so = _empty(shape, io, q.device, stream), (Hq * S * D, S * D, D)
+            q_out, so = new(shape, dtype=io, device=q.device), (Hq * S * D, S * D, D)
         else:
             so = q_out.stride()
             good = good and q_out.dtype is io and q_out.get_device() == dev and q_out.shape == shape and so[3] == 1
@@ -618,7 +624,7 @@ def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, 
             Hkv = shape[1]
             good = good and k.dtype is io and k.get_device() == dev and shape == (B, Hkv, S, D) and sk[3] == 1
             if k_out is None:
-                k_out, sl = _empty(shape, io, q.device, stream), (Hkv * S * D, S * D, D)
+                k_out, sl = new(shape, dtype=io, device=q.device), (Hkv * S * D, S * D, D)
             else:
                 sl = k_out.stride()
                 good = good and k_out.dtype is io and k_out.get_device() == dev and k_out.shape == shape and sl[3] == 1
@@ -703,8 +709,9 @@ def sdpa_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale: Option
     Hkv, Skv = k.shape[1], k.shape[2]
     Dv = v.shape[3]
     fresh = o is None and lse is None  # (outputs made here need no checks)
-    o = _empty((B, Hq, Sq, Dv), io, q.device, stream) if o is None else o
-    lse = _empty((B, Hq, Sq), torch.float32, q.device, stream) if lse is None else lse
+    new = torch.empty if stream is None else functools.partial(_empty, stream=stream)
+    o = new((B, Hq, Sq, Dv), dtype=io, device=q.device) if o is None else o
+    lse = new((B, Hq, Sq), dtype=torch.float32, device=q.device) if lse is None else lse
     dev = q.get_device()
     if not (q.is_cuda and _is(q, io, dev, (B, Hq, Sq, Dqk)) and _is(k, io, dev, (B, Hkv, Skv, Dqk))
             and _is(v, io, dev, (B, Hkv, Skv, Dv))
@@ -760,7 +767,7 @@ def nvfp4_fake_quant(x: torch.Tensor, out: Optional[torch.Tensor] = None,
     if not isinstance(x, torch.Tensor) or x.dtype != torch.bfloat16 or not x.is_cuda \
             or not x.is_contiguous():
         raise ValueError("x must be a contiguous bf16 CUDA tensor")
-    out = _empty(x.shape, x.dtype, x.device, stream) if out is None else out
+    out = _empty_like(x, stream) if out is None else out
     _check_bf16("out", out, x.shape)
     _check_same_device(x, out=out)
     _check_launch_device(x)
@@ -799,9 +806,9 @@ def sdpa_bwd_nvfp4_qat(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o_hp: 
         _check_bf16(name, t, shape)
     _check_lse(lse, B, Hq, Sq)
     _check_lens(B, seq_q_lens, seq_kv_lens)
-    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
-    dk = _empty(k.shape, k.dtype, k.device, stream) if dk is None else dk
-    dv = _empty(v.shape, v.dtype, v.device, stream) if dv is None else dv
+    dq = _empty_like(q, stream) if dq is None else dq
+    dk = _empty_like(k, stream) if dk is None else dk
+    dv = _empty_like(v, stream) if dv is None else dv
     _check_bf16("dq", dq, q.shape)
     _check_bf16("dk", dk, k.shape)
     _check_bf16("dv", dv, v.shape)
