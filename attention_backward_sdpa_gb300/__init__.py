@@ -276,7 +276,8 @@ def sdpa_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
 
     q (B,Hq,Sq,Dqk), k (B,Hkv,Skv,Dqk), v (B,Hkv,Skv,Dv), o/do (B,Hq,Sq,Dv): bf16 or fp16
     (one type for all) CUDA tensors on the current device, contiguous. lse (B,Hq,Sq) fp32 natural-log forward statistic. Lengths: int32 (B,) CUDA.
-    Outputs are allocated when not given. Runs on ``stream`` (default: current stream).
+    Outputs are allocated when not given. Runs on ``stream`` (default: current stream; the
+    caller orders the inputs before it and the outputs' uses after it).
     With ``sink`` (fp32 (Hq,) CUDA sink logits, already folded into ``lse`` by the
     forward) the call goes through sdpa_bwd_sink and returns (dq, dk, dv, dsink).
     With ``bias`` ((1|B, Hq, Sq, Skv) bf16, fp16 or fp32 CUDA, contiguous: the additive
@@ -286,7 +287,7 @@ def sdpa_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
     io-type dBias of the general entry point).
     With ``softcap`` (> 0), ``alibi_slopes`` (fp32 (Hq,) CUDA) or ``mask_plan`` the call
     goes through sdpa_bwd_scored: the gradient of sdpa_fwd with the same three (not
-    together with ``bias``).
+    together with ``bias``; a plan with ``deterministic`` only at D_qk 128, 192 and 256).
     """
     lib = load()
     if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:

@@ -73,8 +73,8 @@ __host__ __device__ inline MaskPlanLayout mask_plan_layout(int B, int n_qt, int 
 //                y^2, 1.5e-7 before its roundings), with the powers of cap_in taken
 //                into its coefficients: 6 multiply-adds, no division (a lower bound for caps whose
 //                powers leave fp32's range);
-//   any y        y N(y^2) / D(y^2), N and D of degree 4, fitted on [0, 8] (6.4e-9,
-//                3.1e-7 with the fp32 roundings), y clamped to [-8, 8] (1 - tanh(8) =
+//   any y        y N(y^2) / D(y^2), N and D of degree 4, fitted on [0, 8] (1.6e-8 with the
+//                constants below, 3.1e-7 with the fp32 roundings), y clamped to [-8, 8] (1 - tanh(8) =
 //                2.3e-7): 12 multiply-adds and a reciprocal.
 // A warp takes the first when all its scores of a tile allow it, which they do unless
 // scores come near the cap. (The quotient 1 - 2 / (1 + e^2y) would take two
