@@ -16,13 +16,14 @@ import math
 import operator
 import os
 import struct
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
 from . import _build
 
-__all__ = ["sdpa_bwd", "sdpa_fwd", "mask_plan", "MaskPlan", "rope_fwd", "rope_bwd", "rope_inv_freq",
+__all__ = ["sdpa_bwd", "sdpa_fwd", "mask_plan", "MaskPlan", "rope_fwd", "rope_bwd", "rope_inv_freq", "rope_axes",
+           "KVCache", "kv_cache", "kv_append", "kv_gather", "sdpa_fwd_cached", "cached_workspace_size",
            "workspace_size", "nvfp4_fake_quant", "sdpa_fwd_nvfp4_qat",
            "sdpa_bwd_nvfp4_qat", "nvfp4_qat_workspace_size", "check_device_status", "debug_relay",
            "profile_enable", "profile_read", "library_path", "load", "SdpaError", "KERNEL_NAMES"]
@@ -30,7 +31,8 @@ __all__ = ["sdpa_bwd", "sdpa_fwd", "mask_plan", "MaskPlan", "rope_fwd", "rope_bw
 KERNEL_NAMES = ("preprocess", "main", "dq")
 
 _STATUS = {0: "SDPA_OK", 1: "SDPA_ERR_INVALID", 2: "SDPA_ERR_UNSUPPORTED", 3: "SDPA_ERR_ALIGN",
-           4: "SDPA_ERR_WORKSPACE", 5: "SDPA_ERR_CUDA", 6: "SDPA_ERR_TIMEOUT", 7: "SDPA_ERR_BOUNDS"}
+           4: "SDPA_ERR_WORKSPACE", 5: "SDPA_ERR_CUDA", 6: "SDPA_ERR_TIMEOUT", 7: "SDPA_ERR_BOUNDS",
+           8: "SDPA_ERR_PAGE"}
 
 
 class SdpaError(RuntimeError):
@@ -93,6 +95,18 @@ def load(build_if_missing: bool = False):
     lib.sdpa_rope.argtypes = [i, vp, vp, vp, vp, i, i, i, i, i, vp, vp, i,
                               ctypes.c_float, vp, i, i, i, i, vp]
     lib.sdpa_rope.restype = i
+    lib.sdpa_rope_axes.argtypes = [i, vp, vp, vp, vp, i, i, i, i, i, vp, vp, i,
+                                   ctypes.c_float, vp, i, i, vp, i, i, vp]
+    lib.sdpa_rope_axes.restype = i
+    lib.sdpa_kv_append.argtypes = [i, i] + [vp] * 11 + [i] * 8 + [vp, vp, i, ctypes.c_float, vp, i, i, vp, i, vp]
+    lib.sdpa_kv_append.restype = i
+    lib.sdpa_kv_gather.argtypes = [i, i] + [vp] * 8 + [i] * 7 + [vp]
+    lib.sdpa_kv_gather.restype = i
+    lib.sdpa_fwd_cached_workspace_size.argtypes = [i] * 8
+    lib.sdpa_fwd_cached_workspace_size.restype = sz
+    lib.sdpa_fwd_cached.argtypes = [i, i] + [vp] * 10 + [i] * 8 + [ctypes.c_float, i, i, i, vp, ctypes.c_float, vp, vp,
+                                                                  sz, vp]
+    lib.sdpa_fwd_cached.restype = i
     lib.sdpa_nvfp4_fake_quant.argtypes = [vp, vp, ctypes.c_longlong, vp]
     lib.sdpa_nvfp4_fake_quant.restype = i
     lib.sdpa_bwd_nvfp4_qat_workspace_size.argtypes = [i, i, i, i, i, i, i]
@@ -252,6 +266,8 @@ _INT32 = 1 << 31  # (ctypes would take a larger int modulo 2^32)
 
 # io element types of the C ABI (sdpa_dtype) for the typed entry points.
 _IO_CODES = {torch.bfloat16: 0, torch.float16: 2}
+
+_MAX_AXES = 16  # axes of rotary positions
 
 
 def _io_dtype(q):
@@ -565,7 +581,32 @@ def rope_inv_freq(rot_dim: int, base: float = 10000.0, *, scaling: str = "none",
     return f.to(torch.device("cuda") if device is None else device)
 
 
-def _check_rope_args(q, k, inv_freq, positions, offset, q_out, k_out):
+def rope_axes(sections: Sequence[int], *, mixed: bool = False, device=None) -> torch.Tensor:
+    """The int32 (sum(sections),) ``axes`` that rope_fwd takes: axis a turns sections[a] pairs,
+    one section after another, or with ``mixed`` the axes in turn from pair to pair, each while
+    it has pairs left. Copied to ``device``: once, outside of a graph's capture."""
+    sizes = [operator.index(n) for n in sections]
+    if not sizes or len(sizes) > _MAX_AXES or min(sizes) < 0 or sum(sizes) == 0:
+        raise ValueError(f"sections are 1 to {_MAX_AXES} numbers of pairs, not all 0")
+    if mixed:
+        order = [a for turn in range(max(sizes)) for a, n in enumerate(sizes) if turn < n]
+    else:
+        order = [a for a, n in enumerate(sizes) for _ in range(n)]
+    return torch.tensor(order, dtype=torch.int32).to(torch.device("cuda") if device is None else device)
+
+
+def _check_axes(axes, positions, pairs, B, S):
+    """Names what is wrong with a call's axes and their positions."""
+    if positions is None:
+        raise ValueError("axes need positions, (n_axes, S) or (n_axes, B, S)")
+    _check_int32("axes", axes, ((pairs,),))
+    if not isinstance(positions, torch.Tensor) or positions.dim() not in (2, 3) or not 1 <= positions.shape[0] <= _MAX_AXES:
+        raise ValueError(f"positions must be (n_axes, S) or (n_axes, B, S) with axes, n_axes from 1 to {_MAX_AXES}")
+    n = positions.shape[0]
+    _check_int32("positions", positions, ((n, S), (n, B, S)))
+
+
+def _check_rope_args(q, k, inv_freq, positions, offset, q_out, k_out, axes=None):
     """Names what is wrong with a rope call's arguments."""
     io = _io_dtype(q)
     if q.dim() != 4:
@@ -593,17 +634,20 @@ def _check_rope_args(q, k, inv_freq, positions, offset, q_out, k_out):
     rot = 2 * inv_freq.numel()
     if rot == 0 or rot > D:
         raise ValueError(f"inv_freq rotates {rot} columns of {D}")
+    if axes is not None:
+        _check_axes(axes, positions, rot // 2, B, S)
     if positions is not None:
-        _check_int32("positions", positions, ((S,), (B, S)))
+        if axes is None:
+            _check_int32("positions", positions, ((S,), (B, S)))
         if offset != 0:
             raise ValueError("offset counts from position 0 where no positions are given")
-    _check_same_device(q, k=k, inv_freq=inv_freq, positions=positions, q_out=q_out, k_out=k_out)
+    _check_same_device(q, k=k, inv_freq=inv_freq, positions=positions, q_out=q_out, k_out=k_out, axes=axes)
 
 
 _strides = struct.Struct("12q").pack  # (0.1 us on the Arm host, against 1.1 for a ctypes array)
 
 
-def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, k_out, stream):
+def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, k_out, stream, axes=None):
     lib = load()
     new = torch.empty if stream is None else functools.partial(_empty, stream=stream)
     try:
@@ -632,11 +676,15 @@ def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, 
         rot = 2 * inv_freq.shape[0]
         good = good and 0 < rot <= D and _is(inv_freq, torch.float64, dev, (rot // 2,)) \
             and (positions is None or offset == 0 and (_is(positions, torch.int32, dev, (B, S))
-                                                       or _is(positions, torch.int32, dev, (S,))))
+                                                       or _is(positions, torch.int32, dev, (S,)))
+                 if axes is None else
+                 offset == 0 and _is(axes, torch.int32, dev, (rot // 2,)) and 1 <= positions.shape[0] <= _MAX_AXES
+                 and (_is(positions, torch.int32, dev, (positions.shape[0], B, S))
+                      or _is(positions, torch.int32, dev, (positions.shape[0], S))))
     except (AttributeError, IndexError, TypeError, ValueError):  # not tensors, or of other dimensions
         good = False
     if not good:
-        _check_rope_args(q, k, inv_freq, positions, offset, q_out, k_out)
+        _check_rope_args(q, k, inv_freq, positions, offset, q_out, k_out, axes)
         B, Hq, S, D = q.shape
         sq, so, Hkv, rot = q.stride(), q_out.stride(), 0, 2 * inv_freq.numel()
         sk, sl = sq, so
@@ -649,9 +697,17 @@ def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, 
         x, z, x_out, z_out = q, k, q_out, k_out
         if Hq == 0:  # the keys alone, as the C call's first tensor
             x, z, x_out, z_out, sq, so, Hq, Hkv = k, None, k_out, None, sk, sl, Hkv, 0
+        at = _strides(sq[0], sq[1], sq[2], so[0], so[1], so[2], sk[0], sk[1], sk[2], sl[0], sl[1], sl[2])
+        if axes is not None:
+            rc = lib.sdpa_rope_axes(_IO_CODES[x.dtype], x.data_ptr(), _addr(z), x_out.data_ptr(), _addr(z_out), B, Hq,
+                                    Hkv, S, D, at, inv_freq.data_ptr(), rot, float(mult), positions.data_ptr(),
+                                    positions.dim() - 2, positions.shape[0], axes.data_ptr(), bool(interleaved), inverse,
+                                    _stream_handle(stream))
+            if rc != 0:
+                raise SdpaError(rc, "sdpa_rope_axes")
+            return q_out, k_out
         rc = lib.sdpa_rope(_IO_CODES[x.dtype], x.data_ptr(), _addr(z), x_out.data_ptr(), _addr(z_out), B, Hq, Hkv, S, D,
-                           _strides(sq[0], sq[1], sq[2], so[0], so[1], so[2], sk[0], sk[1], sk[2], sl[0], sl[1], sl[2]),
-                           inv_freq.data_ptr(), rot, float(mult), _addr(positions),
+                           at, inv_freq.data_ptr(), rot, float(mult), _addr(positions),
                            0 if positions is None else positions.dim() - 1, operator.index(offset), bool(interleaved),
                            inverse, _stream_handle(stream))
         if rc != 0:
@@ -662,7 +718,7 @@ def _rope(q, k, inv_freq, mult, positions, offset, interleaved, inverse, q_out, 
 def rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: torch.Tensor, *, mult: float = 1.0,
              positions: Optional[torch.Tensor] = None, offset: int = 0, interleaved: bool = False,
              q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
-             stream: Optional[torch.cuda.Stream] = None):
+             axes: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
     """Rotary embedding of q (B,Hq,S,D) and k (B,Hkv,S,D) (or of q alone, k None): the
     first 2 * inv_freq.numel() columns turn pair by pair by position * inv_freq and are
     multiplied by ``mult``, the others are copied (sdpa_rope in include/sdpa_bwd.h).
@@ -671,19 +727,209 @@ def rope_fwd(q: torch.Tensor, k: Optional[torch.Tensor], inv_freq: torch.Tensor,
     projection's (B,S,H,D) output goes in as a transposed view and comes out contiguous
     (B,H,S,D) for sdpa_fwd. ``inv_freq``: fp64 CUDA vector (rope_inv_freq).
     ``positions``: int32 (S,) or (B,S), else offset .. offset + S - 1. Pairs are columns
-    (i, i + rot/2), or (2i, 2i+1) when ``interleaved``. Returns (q_out, k_out). An
+    (i, i + rot/2), or (2i, 2i+1) when ``interleaved``. With ``axes`` (int32 (rot/2,), the axis of
+    each pair: rope_axes) positions are (n_axes,S) or (n_axes,B,S), and pair i turns by that of
+    its axis (tokens of images and videos; sdpa_rope_axes). Returns (q_out, k_out). An
     output may be its own input (the same tensor: in place) and overlaps nothing else.
     """
-    return _rope(q, k, inv_freq, mult, positions, offset, interleaved, False, q_out, k_out, stream)
+    return _rope(q, k, inv_freq, mult, positions, offset, interleaved, False, q_out, k_out, stream, axes)
 
 
 def rope_bwd(dq: torch.Tensor, dk: Optional[torch.Tensor], inv_freq: torch.Tensor, *, mult: float = 1.0,
              positions: Optional[torch.Tensor] = None, offset: int = 0, interleaved: bool = False,
              q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
-             stream: Optional[torch.cuda.Stream] = None):
+             axes: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None):
     """The gradients of rope_fwd's inputs from those of its outputs (dq, dk of sdpa_bwd):
     the transposed rotation, with rope_fwd's other arguments."""
-    return _rope(dq, dk, inv_freq, mult, positions, offset, interleaved, True, q_out, k_out, stream)
+    return _rope(dq, dk, inv_freq, mult, positions, offset, interleaved, True, q_out, k_out, stream, axes)
+
+
+class KVCache(NamedTuple):
+    """A paged cache: keys and values (n_pages, Hkv, page_size, D), bf16, fp16 or float8_e4m3fn, and in 8
+    bits the scale of every page and head, fp32 (n_pages, Hkv): a code stands for code * scale.
+    Position j of a sequence is slot j % page_size of the page that its page table names at
+    j // page_size. page_size is 16, 32, 64, 128 or 256; D a multiple of 16 up to 128."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: Optional[torch.Tensor] = None
+    v_scale: Optional[torch.Tensor] = None
+
+
+def kv_cache(n_pages: int, Hkv: int, page_size: int, D: int, dtype: torch.dtype = torch.bfloat16,
+             device=None) -> KVCache:
+    """An empty cache of that many pages."""
+    if dtype not in _CACHE_CODES:
+        raise ValueError("a cache is bfloat16, float16 or float8_e4m3fn")
+    if page_size not in (16, 32, 64, 128, 256) or D <= 0 or D % 16 or D > 128 or n_pages <= 0 or Hkv <= 0:
+        raise ValueError("page_size must be 16, 32, 64, 128 or 256, D a multiple of 16 up to 128, n_pages and Hkv positive")
+    dev = torch.device("cuda") if device is None else device
+    k, v = (torch.zeros(n_pages, Hkv, page_size, D, dtype=torch.uint8 if dtype == torch.float8_e4m3fn else dtype, device=dev)
+            for _ in range(2))
+    if dtype != torch.float8_e4m3fn:
+        return KVCache(k, v)
+    scales = [torch.ones(n_pages, Hkv, dtype=torch.float32, device=dev) for _ in range(2)]
+    return KVCache(k.view(dtype), v.view(dtype), *scales)
+
+
+# Element types of a cache (sdpa_dtype).
+_CACHE_CODES = {torch.bfloat16: 0, torch.float16: 2, torch.float8_e4m3fn: 3}
+
+
+def _check_cache(cache, page_table, seq_kv_lens, B, io, ref):
+    """Names what is wrong with a cache call's cache, table and lengths."""
+    if not isinstance(cache, tuple) or len(cache) != 4:
+        raise TypeError("cache must be a KVCache")
+    k, v, ks, vs = cache
+    for name, t in (("cache.k", k), ("cache.v", v)):
+        if not isinstance(t, torch.Tensor) or t.dim() != 4 or not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous (n_pages, Hkv, page_size, D) CUDA tensor")
+        if t.dtype not in (io, torch.float8_e4m3fn) or t.dtype != k.dtype:
+            raise ValueError(f"the cache must be {io} or float8_e4m3fn, keys and values alike")
+    if k.shape != v.shape:
+        raise ValueError("cache.k and cache.v must have one shape")
+    for name, t in (("cache.k_scale", ks), ("cache.v_scale", vs)):
+        if (t is not None) != (k.dtype == torch.float8_e4m3fn):
+            raise ValueError(f"{name} goes with a float8_e4m3fn cache, and only with one")
+        if t is not None and (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda
+                              or not t.is_contiguous() or t.shape != k.shape[:2]):
+            raise ValueError(f"{name} must be a contiguous fp32 CUDA tensor of shape (n_pages, Hkv)")
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be an int32 (B, max_pages) CUDA tensor")
+    _check_int32("page_table", page_table, ((B, page_table.shape[1]),))
+    _check_int32("seq_kv_lens", seq_kv_lens, ((B,),))
+    _check_same_device(ref, k_cache=k, v_cache=v, k_scale=ks, v_scale=vs, page_table=page_table, seq_kv_lens=seq_kv_lens)
+
+
+def _cache_fits(cache, page_table, seq_kv_lens, B, io, dev) -> bool:
+    """The same in one test: whether all is as it has to be."""
+    try:
+        k, v, ks, vs = cache
+        shape, t = k.shape, k.dtype
+        f8 = t is torch.float8_e4m3fn
+        return (len(shape) == 4 and (f8 or t is io) and _is(k, t, dev, shape) and _is(v, t, dev, shape)
+                and (_is(ks, torch.float32, dev, shape[:2]) and _is(vs, torch.float32, dev, shape[:2]) if f8
+                     else ks is None and vs is None)
+                and _is(page_table, torch.int32, dev, (B, page_table.shape[1])) and _is(seq_kv_lens, torch.int32, dev, (B,)))
+    except (AttributeError, IndexError, TypeError, ValueError):
+        return False
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_kv_lens: torch.Tensor, *,
+              seq_q_lens: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+              inv_freq: Optional[torch.Tensor] = None, mult: float = 1.0, positions: Optional[torch.Tensor] = None,
+              axes: Optional[torch.Tensor] = None, interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+              stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """Appends the rows of k and v (B,Hkv,S,D) to the cache, in place, and rotates keys and queries
+    on the way (sdpa_kv_append in include/sdpa_bwd.h).
+
+    ``page_table`` int32 (B,max_pages), ``seq_kv_lens`` int32 (B,): the lengths with the new rows,
+    which sdpa_fwd_cached then takes as they are. Row t of the first n = ``seq_q_lens``[b] rows (default: all S)
+    goes to position seq_kv_lens[b] - n + t. With ``inv_freq`` (rope_inv_freq) keys and queries turn as in rope_fwd, by
+    the positions in the cache or by ``positions`` ((S,), (B,S), or with ``axes`` (n_axes,S), (n_axes,B,S)).
+    bf16 or fp16, any strides of batch, head and position with contiguous columns. Returns the rotated
+    ``q`` (B,Hq,S,D), contiguous unless ``q_out`` is given (it may be q itself); None without q.
+    """
+    lib = load()
+    io = _io_dtype(k)
+    if k.dim() != 4:
+        raise ValueError("k must be (B, H, S, D)")
+    B, Hkv, S, D = k.shape
+    dev, Hq = k.get_device(), 0
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+            raise ValueError("q must be a (B, H, S, D) tensor")
+        Hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((B, Hq, S, D), dtype=io, device=k.device) if stream is None \
+                else _empty((B, Hq, S, D), io, k.device, stream)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    for name, t, H in (("k", k, Hkv), ("v", v, Hkv), ("q", q, Hq), ("q_out", q_out, Hq)):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype is not io or not t.is_cuda:
+            raise ValueError(f"{name} must be a {io} CUDA tensor")
+        if t.shape != (B, H, S, D):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, H, S, D)}")
+        if t.stride(3) != 1 and D > 1:
+            raise ValueError(f"{name} must have contiguous columns (stride 1 in its last dimension)")
+        if t.get_device() != dev:
+            _check_same_device(k, _ref="k", **{name: t})
+    if not _cache_fits(cache, page_table, seq_kv_lens, B, io, dev):
+        _check_cache(cache, page_table, seq_kv_lens, B, io, k)
+    kc, vc, ks, vs = cache
+    if kc.shape[1] != Hkv or kc.shape[3] != D:
+        raise ValueError(f"the cache holds {kc.shape[1]} heads of {kc.shape[3]} columns, k has {Hkv} of {D}")
+    if seq_q_lens is not None and not _is(seq_q_lens, torch.int32, dev, (B,)):
+        _check_int32("seq_q_lens", seq_q_lens, ((B,),))
+        _check_same_device(k, _ref="k", seq_q_lens=seq_q_lens)
+    rot = 0
+    if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1 or not _is(inv_freq, torch.float64, dev, inv_freq.shape):
+            raise ValueError("inv_freq must be a contiguous fp64 CUDA vector (rope_inv_freq) on k's device")
+        rot = 2 * inv_freq.shape[0]
+        if rot == 0 or rot > D:
+            raise ValueError(f"inv_freq rotates {rot} columns of {D}")
+    elif positions is not None or axes is not None:
+        raise ValueError("positions and axes go with inv_freq")
+    if axes is not None:
+        _check_axes(axes, positions, rot // 2, B, S)
+    elif positions is not None:
+        _check_int32("positions", positions, ((S,), (B, S)))
+    if positions is not None:
+        _check_same_device(k, _ref="k", positions=positions, axes=axes)
+    _check_launch_device(k)
+    st, sv = k.stride(), v.stride()
+    sq, so = (st, st) if q is None else (q.stride(), q_out.stride())
+    rc = lib.sdpa_kv_append(
+        _IO_CODES[io], _CACHE_CODES[kc.dtype], _addr(q), _addr(q_out), k.data_ptr(), v.data_ptr(), kc.data_ptr(),
+        vc.data_ptr(), _addr(ks), _addr(vs), page_table.data_ptr(), seq_kv_lens.data_ptr(), _addr(seq_q_lens), B, Hq,
+        Hkv, S, D, kc.shape[0], kc.shape[2], page_table.shape[1],
+        _strides(sq[0], sq[1], sq[2], so[0], so[1], so[2], st[0], st[1], st[2], sv[0], sv[1], sv[2]),
+        _addr(inv_freq), rot, float(mult), _addr(positions),
+        0 if positions is None else positions.dim() - (1 if axes is None else 2),
+        1 if axes is None else positions.shape[0], _addr(axes), bool(interleaved), _stream_handle(stream))
+    if rc != 0:
+        raise SdpaError(rc, "sdpa_kv_append")
+    return q_out
+
+
+def kv_gather(cache: KVCache, page_table: torch.Tensor, seq_kv_lens: torch.Tensor, S: Optional[int] = None, *,
+              dtype: Optional[torch.dtype] = None, k_out: Optional[torch.Tensor] = None,
+              v_out: Optional[torch.Tensor] = None,
+              stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The cached keys and values of the first ``S`` positions (default: all that the page table has) of
+    every sequence as contiguous (B,Hkv,S,D) tensors, zeros past the lengths (sdpa_kv_gather), for
+    sdpa_fwd, say. ``dtype`` is bf16 or fp16; a 16-bit cache has its own (the default), an 8-bit one bf16."""
+    lib = load()
+    kc = cache[0] if isinstance(cache, tuple) and len(cache) == 4 else None
+    if not isinstance(kc, torch.Tensor) or kc.dim() != 4 or not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("cache must be a KVCache and page_table an int32 (B, max_pages) CUDA tensor")
+    io = dtype if dtype is not None else torch.bfloat16 if kc.dtype == torch.float8_e4m3fn else kc.dtype
+    if io not in _IO_CODES:
+        raise ValueError("dtype must be bfloat16 or float16")
+    B, dev = page_table.shape[0], kc.get_device()
+    if not _cache_fits(cache, page_table, seq_kv_lens, B, io, dev):
+        _check_cache(cache, page_table, seq_kv_lens, B, io, kc)
+    n_pages, Hkv, P, D = kc.shape
+    most = page_table.shape[1] * P
+    S = most if S is None else operator.index(S)
+    if not 0 <= S <= most:
+        raise ValueError(f"S must be from 0 to {most}, what the page table has")
+    new = torch.empty if stream is None else functools.partial(_empty, stream=stream)
+    k_out = new((B, Hkv, S, D), dtype=io, device=kc.device) if k_out is None else k_out
+    v_out = new((B, Hkv, S, D), dtype=io, device=kc.device) if v_out is None else v_out
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if not _is(t, io, dev, (B, Hkv, S, D)):
+            _check_bf16(name, t, (B, Hkv, S, D), io)
+            _check_same_device(kc, _ref="the cache", **{name: t})
+    _check_launch_device(kc)
+    rc = lib.sdpa_kv_gather(_IO_CODES[io], _CACHE_CODES[kc.dtype], kc.data_ptr(), cache[1].data_ptr(), _addr(cache[2]),
+                            _addr(cache[3]), page_table.data_ptr(), seq_kv_lens.data_ptr(), k_out.data_ptr(),
+                            v_out.data_ptr(), B, Hkv, S, D, n_pages, P, page_table.shape[1], _stream_handle(stream))
+    if rc != 0:
+        raise SdpaError(rc, "sdpa_kv_gather")
+    return k_out, v_out
 
 
 def sdpa_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale: Optional[float] = None,
@@ -757,6 +1003,81 @@ def sdpa_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, scale: Option
         rc = lib.sdpa_fwd_bias(*args, _ptr(bias), dt, int(bias.shape[0]), _stream_handle(stream))
     if rc != 0:
         raise SdpaError(rc, "sdpa_fwd_bias" if bias is not None else "sdpa_fwd")
+    return o, lse
+
+
+def cached_workspace_size(B, Hq, Hkv, Sq, D, cache_dtype, page_size, max_pages) -> int:
+    """Workspace bytes of sdpa_fwd_cached for these sizes (cache_dtype: the cache's torch dtype)."""
+    return int(load().sdpa_fwd_cached_workspace_size(B, Hq, Hkv, Sq, D, _CACHE_CODES[cache_dtype], page_size, max_pages))
+
+
+@functools.lru_cache(maxsize=4096)
+def _cached_workspace(lib, *sizes) -> int:
+    return int(lib.sdpa_fwd_cached_workspace_size(*sizes))
+
+
+def sdpa_fwd_cached(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_kv_lens: torch.Tensor, *,
+                    scale: Optional[float] = None, causal: bool = True, window_left: int = -1, first_keys: int = 0,
+                    seq_q_lens: Optional[torch.Tensor] = None, sink: Optional[torch.Tensor] = None,
+                    softcap: float = 0.0, alibi_slopes: Optional[torch.Tensor] = None,
+                    o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None,
+                    stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """O (as q) and natural-log LSE (fp32 (B,Hq,Sq)) of queries q (B,Hq,Sq,D) over a paged cache (sdpa_fwd_cached in
+    include/sdpa_bwd.h): one token, a few, or a chunk of a prompt.
+
+    ``page_table`` int32 (B,max_pages), ``seq_kv_lens`` int32 (B,): what kv_append took, so the queries are the last
+    positions: query i of the first n = ``seq_q_lens``[b] (default Sq) stands at seq_kv_lens[b] - n + i. It sees the
+    keys up to its own (``causal``), from ``window_left`` before it on, and under a window the ``first_keys`` first
+    ones too. ``sink``, ``softcap`` and ``alibi_slopes`` as in sdpa_fwd.
+    """
+    lib = load()
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be (B, H, S, D)")
+    io = _io_dtype(q)
+    B, Hq, Sq, D = q.shape
+    dev, fresh = q.get_device(), o is None and lse is None  # (outputs made here need no checks)
+    new = torch.empty if stream is None else functools.partial(_empty, stream=stream)
+    o = new((B, Hq, Sq, D), dtype=io, device=q.device) if o is None else o
+    lse = new((B, Hq, Sq), dtype=torch.float32, device=q.device) if lse is None else lse
+    if not _cache_fits(cache, page_table, seq_kv_lens, B, io, dev):
+        _check_cache(cache, page_table, seq_kv_lens, B, io, q)
+    kc, vc, ks, vs = cache
+    n_pages, Hkv, P, Dc = kc.shape
+    if Dc != D:
+        raise ValueError(f"the cache holds {Dc} columns, q has {D}")
+    if not (q.is_cuda and _is(q, io, dev, (B, Hq, Sq, D))
+            and (fresh or _is(o, io, dev, (B, Hq, Sq, D)) and _optional(lse, torch.float32, dev, B * Hq * Sq))
+            and (seq_q_lens is None or _optional(seq_q_lens, torch.int32, dev, B))
+            and (sink is None or _optional(sink, torch.float32, dev, Hq)) and workspace is None):
+        _check_bf16("q", q, (B, Hq, Sq, D), io)
+        _check_lens(B, seq_q_lens, None)
+        if sink is not None and (sink.dtype != torch.float32 or not sink.is_cuda
+                                 or not sink.is_contiguous() or sink.numel() != Hq):
+            raise ValueError("sink must be a contiguous fp32 CUDA tensor of Hq elements")
+        _check_bf16("o", o, (B, Hq, Sq, D), io)
+        _check_lse(lse, B, Hq, Sq)
+        _check_workspace(workspace)
+        _check_same_device(q, o=o, lse=lse, seq_q_lens=seq_q_lens, sink=sink, workspace=workspace)
+    if softcap != 0.0 or alibi_slopes is not None:
+        _check_score_mods(q, B, Hq, Sq, 0, softcap, alibi_slopes, None, None, -1, -1)
+    window_left, first_keys = operator.index(window_left), operator.index(first_keys)
+    if not (-_INT32 <= window_left < _INT32 and 0 <= first_keys < _INT32):
+        raise ValueError("window_left and first_keys are 32-bit numbers of keys, first_keys not negative")
+    _check_launch_device(q)
+    if workspace is not None:
+        ws_bytes = _check_workspace(workspace)
+    else:
+        ws_bytes = _cached_workspace(lib, B, Hq, Hkv, Sq, D, _CACHE_CODES[kc.dtype], P, page_table.shape[1])
+        if ws_bytes and stream is None:  # (a call on a stream given to it leaves this to the library, as sdpa_bwd)
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    rc = lib.sdpa_fwd_cached(
+        _IO_CODES[io], _CACHE_CODES[kc.dtype], q.data_ptr(), kc.data_ptr(), vc.data_ptr(), _addr(ks), _addr(vs),
+        page_table.data_ptr(), seq_kv_lens.data_ptr(), _addr(seq_q_lens), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Sq, D,
+        n_pages, P, page_table.shape[1], 0.0 if scale is None else float(scale), int(causal), window_left, first_keys,
+        _addr(sink), float(softcap), _addr(alibi_slopes), _addr(workspace), ws_bytes, _stream_handle(stream))
+    if rc != 0:
+        raise SdpaError(rc, "sdpa_fwd_cached")
     return o, lse
 
 

@@ -1,0 +1,203 @@
+// cached.cuh -- attention over a paged cache: what its two kernels (sdpa_cached_rows.cuh for few
+// rows, sdpa_cached_tiles.cu for many) and the merge of their parts share.
+//
+//   y = scale * (q . k),  x = cap tanh(y / cap) - slope |place - j|,  place = L - Lq + i,
+//   row i sees key j < L when j <= place (causal) and (j >= place - W or j < F),
+//   O = sum_j softmax(x [, sink])_j v_j,  LSE = log(sum_j exp(x_j) [+ exp(sink)]).
+//
+// Rows. The G query heads of a key/value head read the same keys, and the (B, Hq, Sq, D)
+// queries of such a group are G * Sq consecutive rows: row r is query r % Sq of head r / Sq. A kernel takes
+// them in tiles of `tile_rows`, whatever head and query they are.
+//
+// Schedule. A segment is one (batch row, row tile, key/value head); it visits n units of
+// `tk` keys: those that some of its rows sees, the tiles of the first F keys and then those of the
+// window, so nothing between them is read. All segments' units in a row are cut into equal shares,
+// one a CTA: lengths as uneven as they come leave no SM idle, and one long sequence is shared by
+// all. A segment inside one share is written at once; of one that is cut every share leaves
+// a part (O / l in fp32, and log2 of its sum) in the workspace, two at most: of the segment that
+// it begins in the middle of (slot 0), and of the one that it does not finish (slot 1). The merge
+// kernel weighs the parts in their order, so results do not depend on timing.
+#pragma once
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace sdpa {
+
+struct CachedParams {
+  KvCacheRef c;
+  int B, Hq, G, Sq, R, D;  // R = G * Sq rows of a key/value head
+  const void* q;           // (B, Hq, Sq, D)
+  void* o;
+  float* lse;              // (B, Hq, Sq)
+  int f16;
+  float scale_log2;        // scale * log2(e)
+  int causal, window_left, first_keys;
+  const int32_t* seq_q_lens;  // or null
+  const float* sink;          // or null
+  ScoreMods mods;             // cap and slopes
+  int tile_rows, n_rt, tk;    // rows of a tile, tiles of a key/value head, keys of a unit
+  int n_ctas;
+  float* part_o;              // [n_ctas][2][tile_rows][D]
+  float* part_lse;            // [n_ctas][2][tile_rows], log2 units
+  int* status;
+};
+
+struct CachedBounds {
+  int L, Lq;
+  int k_lo, k_hi;  // keys that some row's window sees: [k_lo, k_hi)
+  int n, nf, kt;   // units: nf tiles from 0, then n - nf from tile kt
+};
+
+__device__ __forceinline__ CachedBounds cached_bounds(const CachedParams& p, int b, int rt) {
+  CachedBounds s;
+  s.L = cached_len(p.c, b);
+  s.Lq = p.seq_q_lens ? min(max(p.seq_q_lens[b], 0), p.Sq) : p.Sq;
+  const int r0 = rt * p.tile_rows, r1 = min(r0 + p.tile_rows, p.R) - 1;
+  int i0 = 0, i1 = p.Sq - 1;
+  if (p.Sq > 1 && r0 / p.Sq == r1 / p.Sq) i0 = r0 % p.Sq, i1 = r1 % p.Sq;
+  i1 = min(i1, s.Lq - 1);
+  const int place = s.L - s.Lq;  // of query 0
+  s.k_hi = p.causal ? min(s.L, place + i1 + 1) : s.L;
+  s.k_lo = p.window_left >= 0 ? (int)max(0ll, (long long)place + i0 - p.window_left) : 0;
+  s.n = s.nf = s.kt = 0;
+  if (i0 > i1 || s.k_hi <= 0) return s;
+  s.kt = s.k_lo / p.tk;
+  s.nf = min(ceil_div(min(p.first_keys, s.k_hi), p.tk), s.kt);
+  s.n = s.nf + ceil_div(s.k_hi, p.tk) - s.kt;
+  return s;
+}
+__device__ __forceinline__ int cached_tile(const CachedBounds& s, int j) { return j < s.nf ? j : s.kt + (j - s.nf); }
+
+// First unit of CTA i's share of T units, and the CTA that has unit t.
+__device__ __forceinline__ long long share_begin(long long T, int n, int i) { return T * i / n; }
+__device__ __forceinline__ int share_of(long long T, int n, long long t) { return (int)(((t + 1) * n + T - 1) / T) - 1; }
+
+// Where unit `at(T)` of all T lies: entry e (b * n_rt + rt) and its first unit. One call by
+// every thread of the block; `sh` is shared memory.
+struct CachedStart {
+  long long T, at, te;
+  int e;
+};
+template <int THREADS, typename At>
+__device__ __forceinline__ CachedStart cached_start(const CachedParams& p, CachedStart* sh, long long* warp_sum,
+                                                    bool report, At at) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int E = p.B * p.n_rt, per = ceil_div(E, THREADS), e0 = min(tid * per, E), e1 = min(e0 + per, E);
+  long long sum = 0;
+  for (int e = e0; e < e1; ++e) {
+    sum += (long long)cached_bounds(p, e / p.n_rt, e % p.n_rt).n * p.c.Hkv;
+    if (report) {
+      const int len = p.c.lens[e / p.n_rt];
+      if (len < 0 || len > (long long)p.c.max_pages * p.c.page) atomicOr(p.status, STATUS_PAGE);
+    }
+  }
+  long long incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  if (tid == 0) sh->e = -1;
+  __syncthreads();
+  long long T = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w == warp) incl += T;
+    T += warp_sum[w];
+  }
+  const long long want = at(T);
+  long long te = incl - sum;
+  if (want >= te && want < incl) {
+    for (int e = e0; e < e1; ++e) {
+      const long long n = (long long)cached_bounds(p, e / p.n_rt, e % p.n_rt).n * p.c.Hkv;
+      if (want < te + n) {
+        sh->e = e;
+        sh->te = te;
+        break;
+      }
+      te += n;
+    }
+  }
+  __syncthreads();
+  return CachedStart{T, want, sh->te, sh->e};
+}
+
+// A share's walk over its portions of segments, the same for every thread that makes it.
+struct CachedPortion {
+  int b, rt, kvh, j0, j1;  // units [j0, j1) of the segment
+  CachedBounds s;
+  int slot;                // part slot, or -1: the whole segment
+};
+struct CachedWalk {
+  long long u, end, te;
+  int e;
+  __device__ __forceinline__ bool next(const CachedParams& p, CachedPortion& w) {
+    if (u >= end) return false;
+    for (;;) {
+      w.b = e / p.n_rt;
+      w.rt = e % p.n_rt;
+      w.s = cached_bounds(p, w.b, w.rt);
+      const long long n = (long long)w.s.n * p.c.Hkv;
+      if (u < te + n) break;
+      te += n;
+      ++e;
+    }
+    const long long off = u - te;
+    w.kvh = (int)(off / w.s.n);
+    w.j0 = (int)(off % w.s.n);
+    w.j1 = (int)min((long long)w.s.n, w.j0 + (end - u));
+    w.slot = w.j0 > 0 ? 0 : w.j1 < w.s.n ? 1 : -1;
+    u += w.j1 - w.j0;
+    return true;
+  }
+};
+
+// The keys that row r sees: [lo, hi], and below F those up to hi.
+struct CachedRow {
+  int lo, hi, place;
+};
+__device__ __forceinline__ CachedRow cached_row(const CachedParams& p, const CachedBounds& s, int r) {
+  const int i = r % p.Sq;
+  CachedRow w;
+  w.place = s.L - s.Lq + i;
+  w.hi = p.causal ? min(w.place, s.L - 1) : s.L - 1;
+  if (i >= s.Lq) w.hi = -1;
+  w.lo = p.window_left >= 0 ? (int)max(0ll, (long long)w.place - p.window_left) : 0;
+  return w;
+}
+
+// The page of keys [k, k + 16) of batch row b, or -1 (reported).
+__device__ __forceinline__ int cached_page(const CachedParams& p, int b, int k) {
+  const int page = p.c.table[(long long)b * p.c.max_pages + (k >> p.c.page_shift)];
+  if ((unsigned)page < (unsigned)p.c.n_pages) return page;
+  atomicOr(p.status, STATUS_PAGE);
+  return -1;
+}
+
+// A sink joins the sum 2^lse2: returns log2 of the whole and the factor on O.
+__device__ __forceinline__ float cached_with_sink(const CachedParams& p, int head, float lse2, float& factor) {
+  factor = 1.f;
+  if (p.sink == nullptr) return lse2;
+  const float s2 = p.sink[head] * 1.4426950408889634f;
+  if (s2 == -INFINITY) return lse2;
+  if (lse2 == -INFINITY) {
+    factor = 0.f;
+    return s2;
+  }
+  const float m = fmaxf(lse2, s2), all = m + __log2f(ex2_approx(lse2 - m) + ex2_approx(s2 - m));
+  factor = ex2_approx(lse2 - all);
+  return all;
+}
+
+cudaError_t launch_cached_rows_16(const CachedParams& p, int mt, cudaStream_t s);
+cudaError_t launch_cached_rows_8(const CachedParams& p, int mt, cudaStream_t s);
+cudaError_t cached_rows_16_setup();
+cudaError_t cached_rows_8_setup();
+cudaError_t launch_cached_merge(const CachedParams& p, cudaStream_t s);
+
+// Keys of a unit of the few-rows kernel: four warps of 16 keys, or of 32 in 8 bits.
+constexpr int CACHED_ROWS_TK_16 = 64, CACHED_ROWS_TK_8 = 128;
+
+}  // namespace sdpa

@@ -27,6 +27,7 @@ constexpr int QSTAT_FLOATS = 2 * BQ;
 // Device status bits (OR-ed into the per-device status word).
 constexpr int STATUS_TIMEOUT = 1;
 constexpr int STATUS_SMEM_ALIGN = 2;
+constexpr int STATUS_PAGE = 8;    // a cache call met a page id or a length outside the cache
 constexpr int STATUS_BOUNDS = 4;  // debug-bounds build: an access outside its region was skipped
 
 struct ChainParams {
@@ -382,11 +383,68 @@ struct RopeArgs {
   const double* freq;
   const int32_t* positions;  // or null: offset + s
   long long pos_bstride;
+  const int32_t* pair_axis;  // (rot / 2,) axis of each pair, or null: one axis
+  int n_axes;
+  long long axis_stride;     // between the axes' positions
   int offset, B, S, D, rot;
   int f16, interleaved, inverse;
   float mult;
 };
+constexpr int ROPE_MAX_AXES = 16;
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s, int num_sms);
+// A paged cache of keys and values (sdpa_kv_cache.cu, sdpa_cached*.cu). Position j of batch
+// row b is slot j % page of page table[b * max_pages + j / page]; a page holds `page` (16,
+// 32, ... 256) rows of D columns for each of Hkv heads. F8: e4m3 codes, with a scale a page
+// and head (a code stands for code * scale); else 16-bit values.
+struct KvCacheRef {
+  void* k;
+  void* v;            // [n_pages][Hkv][page][D]
+  float* ks;
+  float* vs;          // [n_pages][Hkv], or null
+  const int32_t* table;  // (B, max_pages)
+  const int32_t* lens;   // (B,): cached positions, those of the call included
+  int n_pages, page, page_shift, max_pages, Hkv, D;
+  int f8;
+};
+__device__ __forceinline__ int cached_len(const KvCacheRef& c, int b) {
+  const long long cap = (long long)c.max_pages << c.page_shift;
+  return (int)min((long long)max(c.lens[b], 0), cap);
+}
+// Appends T rows a batch row (the first new_lens[b] of them, or all) at positions lens[b] -
+// new_lens[b] .. lens[b] - 1, rotating keys and, where given, queries (H[0] heads, 0: none).
+struct KvAppendArgs {
+  KvCacheRef c;
+  const void* q;
+  void* q_out;
+  const void* k;
+  const void* v;
+  int Hq, B, T;
+  long long qs[3], qos[3], kst[3], vst[3];  // batch, head, position strides in elements
+  const int32_t* new_lens;                  // or null: T
+  const double* freq;                       // or null: no rotation
+  int rot;
+  float mult;
+  const int32_t* positions;                 // or null: the cache's positions
+  long long pos_bstride, axis_stride;
+  const int32_t* pair_axis;                 // or null
+  int n_axes;
+  int f16, interleaved;
+  int* status;
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t s, int num_sms);
+// The first S positions of every batch row as (B, Hkv, S, D) 16-bit rows, zeros past the lengths.
+struct KvGatherArgs {
+  KvCacheRef c;
+  void* k_out;
+  void* v_out;
+  int B, S, f16;
+  int* status;
+};
+cudaError_t launch_kv_gather(const KvGatherArgs& a, cudaStream_t s, int num_sms);
+cudaError_t kv_cache_setup();
+// Host: the current device's status word and SM count (an sdpa_status), and a cap's constants.
+int current_device_state(int** status, int* sms);
+int fill_cap(float softcap, float scale, ScoreMods& m);
 // NVFP4 fake quantization of n_blocks blocks of 16 consecutive bf16 values.
 cudaError_t launch_nvfp4_fake_quant(const void* x, void* y, long long n_blocks, int num_sms,
                                     cudaStream_t s);

@@ -20,7 +20,9 @@
 #include <mutex>
 
 #include "sdpa_bwd.h"
+#include "cached.cuh"
 #include "common.cuh"
+#include "rows.h"
 #include "tmap.h"
 
 namespace sdpa {
@@ -179,7 +181,9 @@ int device_state(int dev, int** status_out, int* sms_out) {
       g_status_ptr[dev] = static_cast<int*>(p);
       if (main_kernel_setup() != cudaSuccess || main_ds_kernel_setup() != cudaSuccess ||
           preprocess_kernel_setup() != cudaSuccess ||
-          dq_kernel_setup() != cudaSuccess || fwd_kernel_setup() != cudaSuccess)
+          dq_kernel_setup() != cudaSuccess || fwd_kernel_setup() != cudaSuccess ||
+          kv_cache_setup() != cudaSuccess || cached_rows_16_setup() != cudaSuccess ||
+          cached_rows_8_setup() != cudaSuccess)
         return SDPA_ERR_CUDA;
     }
     g_device_checked[dev] = true;
@@ -189,6 +193,16 @@ int device_state(int dev, int** status_out, int* sms_out) {
   *sms_out = g_num_sms[dev];
   return SDPA_OK;
 }
+
+}  // namespace
+
+int current_device_state(int** status, int* sms) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SDPA_ERR_CUDA;
+  return device_state(dev, status, sms);
+}
+
+namespace {
 
 // 3-D map {D, S, B*H} of a contiguous (B, H, S, D) bf16 tensor; boxes of 64
 // columns (128 bytes, the swizzle span) by `rows` sequence positions.
@@ -260,6 +274,7 @@ const char* sdpa_status_string(int status) {
     case SDPA_ERR_WORKSPACE: return "workspace too small";
     case SDPA_ERR_CUDA: return "CUDA runtime error";
     case SDPA_ERR_TIMEOUT: return "device-side wait timed out";
+    case SDPA_ERR_PAGE: return "a page id or length outside the cache was skipped";
     case SDPA_ERR_BOUNDS: return "debug-bounds build: an out-of-range access was skipped";
     default: return "unknown status";
   }
@@ -332,12 +347,42 @@ int sdpa_bwd_check_device_status(void* stream) {
   if (v != 0) {
     const int zero = 0;
     cudaMemcpy(status, &zero, sizeof(int), cudaMemcpyHostToDevice);
-    return (v & STATUS_BOUNDS) ? SDPA_ERR_BOUNDS : SDPA_ERR_TIMEOUT;
+    return (v & STATUS_BOUNDS) ? SDPA_ERR_BOUNDS : v == STATUS_PAGE ? SDPA_ERR_PAGE : SDPA_ERR_TIMEOUT;
   }
   return SDPA_OK;
 }
 
 }  // extern "C"
+
+// The constants of a tanh cap (> 0) for the kernels.
+int sdpa::fill_cap(float softcap, float scale, ScoreMods& m) {
+  m.cap_in = scale / softcap;
+  m.cap_log2 = softcap * 1.4426950408889634f;
+  // A cap so far from the scale that their ratio leaves the normal fp32 range
+  // would turn the capped scores into zeros or NaN.
+  if (!std::isnormal(m.cap_in) || !std::isfinite(m.cap_log2)) return SDPA_ERR_INVALID;
+  // The polynomial with the powers of cap_in in its coefficients, also times cap * log2(e) as
+  // the forward takes them. It serves the scores up to `bound` caps:
+  //   - a small cap's powers may overflow: then the quotient serves every score;
+  //   - a large cap's may leave fp32's normal range (degree 9 from scale / cap = 1e-4 on, past a
+  //     cap of 900 at D 128). Such a term is left out, and the bound lowered to where it is
+  //     below 2^-25 of the value: 0.19 caps without degree 9, 0.09 without 7, 0.02
+  //     without 5, 3e-4 without 3.
+  double power = m.cap_in, bound = TANH_SMALL;
+  for (int i = 0; i < 5; ++i, power *= (double)m.cap_in * m.cap_in) {
+    m.cap_c[i] = (float)(TANH_C[i] * power);
+    const float in_log2 = m.cap_c[i] * m.cap_log2;
+    if (!std::isfinite(in_log2) || (i == 0 && !std::isnormal(in_log2))) {
+      bound = -1.0;
+    } else if (!std::isnormal(m.cap_c[i]) || !std::isnormal(in_log2)) {
+      m.cap_c[i] = 0.f;
+      bound = std::fmin(bound, std::pow(std::exp2(-25.0) / std::fabs(TANH_C[i]), 1.0 / (2 * i)));
+    }
+  }
+  // (1e18: a score's square stays finite.)
+  m.cap_small = bound > 0.0 ? (float)std::fmin(bound / (double)m.cap_in, 1e18) : -1.f;
+  return SDPA_OK;
+}
 
 namespace {
 
@@ -369,31 +414,8 @@ int fill_mods(const ModArgs& ma, float scale, int B, int S_q, int S_kv, ScoreMod
   m.on = ma.softcap > 0.f ? MOD_CAP : MOD_ROWS;
   m.slopes = ma.slopes;
   if (ma.softcap > 0.f) {
-    m.cap_in = scale / ma.softcap;
-    m.cap_log2 = ma.softcap * 1.4426950408889634f;
-    // A cap so far from the scale that their ratio leaves the normal fp32 range
-    // would turn the capped scores into zeros or NaN.
-    if (!std::isnormal(m.cap_in) || !std::isfinite(m.cap_log2)) return SDPA_ERR_INVALID;
-    // The polynomial with the powers of cap_in in its coefficients, also times cap * log2(e) as
-    // the forward takes them. It serves the scores up to `bound` caps:
-    //   - a small cap's powers may overflow: then the quotient serves every score;
-    //   - a large cap's may leave fp32's normal range (degree 9 from scale / cap = 1e-4 on, past a
-    //     cap of 900 at D 128). Such a term is left out, and the bound lowered to where it is
-    //     below 2^-25 of the value: 0.19 caps without degree 9, 0.09 without 7, 0.02
-    //     without 5, 3e-4 without 3.
-    double power = m.cap_in, bound = TANH_SMALL;
-    for (int i = 0; i < 5; ++i, power *= (double)m.cap_in * m.cap_in) {
-      m.cap_c[i] = (float)(TANH_C[i] * power);
-      const float in_log2 = m.cap_c[i] * m.cap_log2;
-      if (!std::isfinite(in_log2) || (i == 0 && !std::isnormal(in_log2))) {
-        bound = -1.0;
-      } else if (!std::isnormal(m.cap_c[i]) || !std::isnormal(in_log2)) {
-        m.cap_c[i] = 0.f;
-        bound = std::fmin(bound, std::pow(std::exp2(-25.0) / std::fabs(TANH_C[i]), 1.0 / (2 * i)));
-      }
-    }
-    // (1e18: a score's square stays finite.)
-    m.cap_small = bound > 0.0 ? (float)std::fmin(bound / (double)m.cap_in, 1e18) : -1.f;
+    const int rc = fill_cap(ma.softcap, scale, m);
+    if (rc != SDPA_OK) return rc;
   }
   if (ma.plan) {
     if (S_q == 0 || S_kv == 0) return SDPA_ERR_INVALID;  // there is no plan of no rows or no keys
@@ -656,57 +678,6 @@ int sdpa_bwd(const void* q, const void* k, const void* v, const void* o, const v
 
 namespace {
 
-// The rows of a rotary call's tensor: places in elements, dimensions batch, head, position.
-struct RopeRows {
-  long long base, end;  // first element, and one past the last
-  long long st[3];
-  int ext[3], D;
-};
-RopeRows rope_rows(const void* ptr, const long long* st, int B, int H, int S, int D) {
-  RopeRows r{(long long)(reinterpret_cast<uintptr_t>(ptr) / 2), 0, {st[0], st[1], st[2]}, {B, H, S}, D};
-  r.end = r.base + D;
-  for (int j = 0; j < 3; ++j)
-    if (r.ext[j] > 1) r.end += st[j] * (r.ext[j] - 1);
-  return r;
-}
-bool same_rows(const RopeRows& a, const RopeRows& b) {
-  bool same = a.base == b.base;
-  for (int j = 0; j < 3; ++j) same = same && a.ext[j] == b.ext[j] && (a.ext[j] == 1 || a.st[j] == b.st[j]);
-  return same;
-}
-// Whether rows `delta` apart come within D of one another by up to `back[j]` steps back and
-// `on[j]` steps on of the strides st, descending: of each only those few are tried that the smaller
-// ones can make up for.
-bool steps_meet(const long long* st, const int* back, const int* on, int n, long long D, long long delta) {
-  if (n == 0) return delta < D && -delta < D;
-  long long reach = D;
-  for (int j = 1; j < n; ++j) reach += st[j] * std::max(back[j], on[j]);
-  const long long lo = std::max(floor_div(-delta - reach, st[0]), -(long long)back[0]);
-  const long long hi = std::min(floor_div(reach - delta, st[0]) + 1, (long long)on[0]);
-  for (long long k = lo; k <= hi; ++k)
-    if (steps_meet(st + 1, back + 1, on + 1, n - 1, D, delta + k * st[0])) return true;
-  return false;
-}
-// Whether an output y shares an element with x: exact for tensors that step alike (slices of
-// one projection), and taken to be so for others whose places interleave.
-bool rows_meet(const RopeRows& x, const RopeRows& y) {
-  if (x.end <= y.base || y.end <= x.base) return false;
-  long long st[3];
-  int back[3], on[3], n = 0;
-  for (int j = 0; j < 3; ++j) {
-    if (x.ext[j] == 1 && y.ext[j] == 1) continue;
-    if (x.ext[j] > 1 && y.ext[j] > 1 && x.st[j] != y.st[j]) return true;
-    const long long s = y.ext[j] > 1 ? y.st[j] : x.st[j];
-    if (s <= 0) return true;
-    int at = n++;
-    for (; at > 0 && st[at - 1] < s; --at) st[at] = st[at - 1], back[at] = back[at - 1], on[at] = on[at - 1];
-    st[at] = s;
-    back[at] = x.ext[j] - 1;
-    on[at] = y.ext[j] - 1;
-  }
-  return steps_meet(st, back, on, n, x.D, y.base - x.base);
-}
-
 int plan_checks(int B, int S_q, int S_kv) {
   if (B <= 0 || S_q <= 0 || S_kv <= 0) return SDPA_ERR_INVALID;
   const long long limit = 1ll << 30;  // rows, tiles and (position + prefix) stay 32-bit
@@ -948,10 +919,14 @@ int sdpa_mask_plan_docs(const int32_t* doc_ids, const int32_t* prefix_lens, int 
                        plan, plan_bytes, stream);
 }
 
-int sdpa_rope(int io_dtype, const void* q, const void* k, void* q_out, void* k_out, int B, int H_q,
-              int H_kv, int S, int D, const long long* strides, const double* inv_freq, int rot_dim,
-              float mult, const int32_t* positions, int positions_per_batch, int offset,
-              int interleaved, int inverse, void* stream) {
+}  // extern "C"
+
+namespace {
+
+int run_rope(int io_dtype, const void* q, const void* k, void* q_out, void* k_out, int B, int H_q, int H_kv, int S,
+             int D, const long long* strides, const double* inv_freq, int rot_dim, float mult,
+             const int32_t* positions, int positions_per_batch, int offset, const int32_t* pair_axis, int n_axes,
+             int interleaved, int inverse, void* stream) {
   if (io_dtype != SDPA_DTYPE_BF16 && io_dtype != SDPA_DTYPE_F16) return SDPA_ERR_INVALID;
   if (B <= 0 || H_q <= 0 || H_kv < 0 || S < 0 || D <= 0 || !strides || !std::isfinite(mult)) return SDPA_ERR_INVALID;
   if (rot_dim <= 0 || rot_dim % 2 != 0 || rot_dim > D) return SDPA_ERR_INVALID;
@@ -974,18 +949,9 @@ int sdpa_rope(int io_dtype, const void* q, const void* k, void* q_out, void* k_o
       a.ys[3 * i + j] = strides[6 * i + 3 + j];
       if ((j == 1 ? Hs[i] : dims[j]) > 1 && a.xs[3 * i + j] < 0) return SDPA_ERR_INVALID;
     }
-    // Two output rows that share a place would race: taken by ascending stride,
-    // each dimension has to step over everything that the smaller ones span.
-    long long span = D, ext[3] = {B, Hs[i], S}, st[3] = {a.ys[3 * i], a.ys[3 * i + 1], a.ys[3 * i + 2]};
-    for (int pass = 0; pass < 3; ++pass) {
-      int low = -1;
-      for (int j = 0; j < 3; ++j)
-        if (ext[j] > 1 && (low < 0 || st[j] < st[low])) low = j;
-      if (low < 0) break;
-      if (st[low] < span || st[low] > (1ll << 40)) return SDPA_ERR_INVALID;
-      span += st[low] * (ext[low] - 1);
-      ext[low] = 1;
-    }
+    // Two output rows that share a place would race.
+    const long long st[3] = {a.ys[3 * i], a.ys[3 * i + 1], a.ys[3 * i + 2]};
+    if (!rows_apart(st, B, Hs[i], S, D)) return SDPA_ERR_INVALID;
   }
   if (reinterpret_cast<uintptr_t>(inv_freq) % 8 != 0 || reinterpret_cast<uintptr_t>(positions) % 4 != 0)
     return SDPA_ERR_ALIGN;
@@ -1004,6 +970,9 @@ int sdpa_rope(int io_dtype, const void* q, const void* k, void* q_out, void* k_o
   a.freq = inv_freq;
   a.positions = positions;
   a.pos_bstride = positions_per_batch ? S : 0;
+  a.pair_axis = pair_axis;
+  a.n_axes = n_axes;
+  a.axis_stride = positions_per_batch ? (long long)B * S : S;
   a.offset = offset;
   a.B = B;
   a.S = S;
@@ -1023,6 +992,29 @@ int sdpa_rope(int io_dtype, const void* q, const void* k, void* q_out, void* k_o
   const cudaError_t e = launch_rope(a, static_cast<cudaStream_t>(stream), sms);
   nvtxRangePop();
   return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sdpa_rope(int io_dtype, const void* q, const void* k, void* q_out, void* k_out, int B, int H_q,
+              int H_kv, int S, int D, const long long* strides, const double* inv_freq, int rot_dim,
+              float mult, const int32_t* positions, int positions_per_batch, int offset,
+              int interleaved, int inverse, void* stream) {
+  return run_rope(io_dtype, q, k, q_out, k_out, B, H_q, H_kv, S, D, strides, inv_freq, rot_dim, mult, positions,
+                  positions_per_batch, offset, nullptr, 1, interleaved, inverse, stream);
+}
+
+int sdpa_rope_axes(int io_dtype, const void* q, const void* k, void* q_out, void* k_out, int B, int H_q,
+                   int H_kv, int S, int D, const long long* strides, const double* inv_freq, int rot_dim,
+                   float mult, const int32_t* positions, int positions_per_batch, int n_axes,
+                   const int32_t* pair_axis, int interleaved, int inverse, void* stream) {
+  if (n_axes <= 0 || n_axes > ROPE_MAX_AXES) return SDPA_ERR_INVALID;
+  if (S > 0 && (!positions || !pair_axis)) return SDPA_ERR_INVALID;
+  if (reinterpret_cast<uintptr_t>(pair_axis) % 4 != 0) return SDPA_ERR_ALIGN;
+  return run_rope(io_dtype, q, k, q_out, k_out, B, H_q, H_kv, S, D, strides, inv_freq, rot_dim, mult, positions,
+                  positions_per_batch, 0, pair_axis, n_axes, interleaved, inverse, stream);
 }
 
 int sdpa_nvfp4_fake_quant(const void* x, void* y, long long n, void* stream) {

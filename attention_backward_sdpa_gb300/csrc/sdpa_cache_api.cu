@@ -1,0 +1,287 @@
+// sdpa_cache_api.cu -- host side of the cache entry points of include/sdpa_bwd.h: arguments
+// checked, then one launch (or two: the attention and the merge of its parts).
+#include <cuda_runtime.h>
+#include <nvtx3/nvToolsExt.h>
+
+#include <cmath>
+#include <cstdint>
+#include <initializer_list>
+
+#include "sdpa_bwd.h"
+#include "cached.cuh"
+#include "common.cuh"
+#include "rows.h"
+
+using namespace sdpa;
+
+namespace {
+
+struct CacheArgs {
+  int dtype;
+  const void *k, *v, *k_scale, *v_scale;
+  const int32_t *table, *lens;
+  int n_pages, page, max_pages, H_kv, D;
+};
+
+bool misaligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
+
+int fill_cache(const CacheArgs& a, int io_dtype, int B, KvCacheRef& c) {
+  if (io_dtype != SDPA_DTYPE_BF16 && io_dtype != SDPA_DTYPE_F16) return SDPA_ERR_INVALID;
+  if (a.dtype != SDPA_DTYPE_E4M3 && a.dtype != io_dtype) return SDPA_ERR_INVALID;
+  if (B <= 0 || a.H_kv <= 0 || a.D <= 0 || a.n_pages <= 0 || a.max_pages <= 0) return SDPA_ERR_INVALID;
+  if (a.D % 16 != 0 || a.D > 128) return SDPA_ERR_UNSUPPORTED;
+  if (a.page < 16 || a.page > 256 || (a.page & (a.page - 1)) != 0) return SDPA_ERR_UNSUPPORTED;
+  // Positions, page rows and table entries are 32-bit; element offsets 64-bit.
+  if ((long long)a.max_pages * a.page >= 1ll << 31 || (long long)a.n_pages * a.H_kv >= 1ll << 31 ||
+      (long long)B * a.max_pages >= 1ll << 31)
+    return SDPA_ERR_INVALID;
+  if (!a.k || !a.v || !a.table || !a.lens) return SDPA_ERR_INVALID;
+  const bool f8 = a.dtype == SDPA_DTYPE_E4M3;
+  if (f8 != (a.k_scale != nullptr) || f8 != (a.v_scale != nullptr)) return SDPA_ERR_INVALID;
+  if (misaligned(a.k, 16) || misaligned(a.v, 16)) return SDPA_ERR_ALIGN;
+  for (const void* p : {a.k_scale, a.v_scale, (const void*)a.table, (const void*)a.lens})
+    if (misaligned(p, 4)) return SDPA_ERR_ALIGN;
+  c.k = const_cast<void*>(a.k);
+  c.v = const_cast<void*>(a.v);
+  c.ks = static_cast<float*>(const_cast<void*>(a.k_scale));
+  c.vs = static_cast<float*>(const_cast<void*>(a.v_scale));
+  c.table = a.table;
+  c.lens = a.lens;
+  c.n_pages = a.n_pages;
+  c.page = a.page;
+  c.page_shift = 0;
+  while ((1 << c.page_shift) < a.page) ++c.page_shift;
+  c.max_pages = a.max_pages;
+  c.Hkv = a.H_kv;
+  c.D = a.D;
+  c.f8 = f8 ? 1 : 0;
+  return SDPA_OK;
+}
+
+struct Span {
+  uintptr_t lo, hi;  // bytes [lo, hi)
+};
+bool meet(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+Span span_of(const void* p, size_t bytes) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return {lo, lo + bytes};
+}
+Span span_of(const RopeRows& r) { return {(uintptr_t)(r.base * 2), (uintptr_t)(r.end * 2)}; }
+size_t cache_bytes(const KvCacheRef& c) { return (size_t)c.n_pages * c.Hkv * c.page * c.D * (c.f8 ? 1 : 2); }
+
+// How a call over the cache is cut, from its sizes alone (not from the device it runs on, so that
+// neither the workspace nor any result depends on that).
+struct CachedPlan {
+  int tile_rows, n_rt, tk, n_ctas, mt;
+  size_t o_bytes, bytes;
+};
+constexpr int SHARE_SMS = 152;  // SMs of a GB300
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+CachedPlan cached_plan(long long B, int H_q, int H_kv, int S_q, int D, bool f8, long long max_keys) {
+  CachedPlan c{};
+  const long long R = (long long)(H_q / H_kv) * S_q;
+  c.mt = R <= 16 ? 1 : 2;
+  c.tile_rows = 16 * c.mt;
+  c.tk = f8 ? CACHED_ROWS_TK_8 : CACHED_ROWS_TK_16;
+  c.n_rt = (int)((R + c.tile_rows - 1) / c.tile_rows);
+  // Two CTAs an SM (their shared memory), fewer where there are not that many units.
+  const long long units = B * c.n_rt * H_kv * ((max_keys + c.tk - 1) / c.tk);
+  c.n_ctas = (int)(units < 2 * SHARE_SMS ? units : 2 * SHARE_SMS);
+  c.o_bytes = align256((size_t)c.n_ctas * 2 * c.tile_rows * D * sizeof(float));
+  c.bytes = c.o_bytes + align256((size_t)c.n_ctas * 2 * c.tile_rows * sizeof(float));
+  return c;
+}
+
+int cached_sizes(int B, int H_q, int H_kv, int S_q, int D) {
+  if (B <= 0 || H_q <= 0 || H_kv <= 0 || S_q < 0 || D <= 0 || H_q % H_kv != 0) return SDPA_ERR_INVALID;
+  if (D % 16 != 0 || D > 128) return SDPA_ERR_UNSUPPORTED;
+  if ((long long)B * H_q * S_q * D >= 1ll << 31) return SDPA_ERR_INVALID;
+  return SDPA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sdpa_fwd_cached_workspace_size(int B, int H_q, int H_kv, int S_q, int D, int cache_dtype, int page_size,
+                                      int max_pages) {
+  if (cached_sizes(B, H_q, H_kv, S_q, D) != SDPA_OK || S_q == 0 || page_size <= 0 || max_pages <= 0) return 0;
+  if ((long long)max_pages * page_size >= 1ll << 31) return 0;
+  return cached_plan(B, H_q, H_kv, S_q, D, cache_dtype == SDPA_DTYPE_E4M3, (long long)max_pages * page_size).bytes;
+}
+
+int sdpa_fwd_cached(int io_dtype, int cache_dtype, const void* q, const void* k_cache, const void* v_cache,
+                    const float* k_scale, const float* v_scale, const int32_t* page_table, const int32_t* seq_kv_lens,
+                    const int32_t* seq_q_lens, void* o, float* lse, int B, int H_q, int H_kv, int S_q, int D,
+                    int n_pages, int page_size, int max_pages, float scale, int causal, int window_left,
+                    int first_keys, const float* sink, float softcap, const float* alibi_slopes, void* workspace,
+                    size_t workspace_bytes, void* stream_) {
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  CachedParams p{};
+  const CacheArgs ca{cache_dtype, k_cache, v_cache, k_scale, v_scale, page_table, seq_kv_lens,
+                     n_pages, page_size, max_pages, H_kv, D};
+  int rc = fill_cache(ca, io_dtype, B, p.c);
+  if (rc == SDPA_OK) rc = cached_sizes(B, H_q, H_kv, S_q, D);
+  if (rc != SDPA_OK) return rc;
+  if (first_keys < 0) return SDPA_ERR_INVALID;
+  if (!(scale > 0.f) || !std::isfinite(scale)) scale = 1.0f / std::sqrt((float)D);
+  if (softcap != 0.f) {
+    if (!(softcap > 0.f && std::isnormal(softcap))) return SDPA_ERR_INVALID;
+    rc = fill_cap(softcap, scale, p.mods);
+    if (rc != SDPA_OK) return rc;
+  }
+  if (S_q == 0) return SDPA_OK;  // no rows
+  if (!q || !o || !lse) return SDPA_ERR_INVALID;
+  if (misaligned(q, 16) || misaligned(o, 16)) return SDPA_ERR_ALIGN;
+  for (const void* x : {(const void*)lse, (const void*)sink, (const void*)alibi_slopes, (const void*)seq_q_lens})
+    if (misaligned(x, 4)) return SDPA_ERR_ALIGN;
+  const CachedPlan plan = cached_plan(B, H_q, H_kv, S_q, D, p.c.f8 != 0, (long long)max_pages * page_size);
+  if ((long long)B * plan.n_rt >= 1ll << 24) return SDPA_ERR_INVALID;
+  if (workspace) {
+    if (workspace_bytes < plan.bytes) return SDPA_ERR_WORKSPACE;
+    if (misaligned(workspace, 256)) return SDPA_ERR_ALIGN;
+  }
+  int sms = 0;
+  rc = current_device_state(&p.status, &sms);
+  if (rc != SDPA_OK) return rc;
+  const bool own = workspace == nullptr;
+  if (own && cudaMallocAsync(&workspace, plan.bytes, stream) != cudaSuccess) return SDPA_ERR_CUDA;
+  p.B = B;
+  p.Hq = H_q;
+  p.G = H_q / H_kv;
+  p.Sq = S_q;
+  p.R = p.G * S_q;
+  p.D = D;
+  p.q = q;
+  p.o = o;
+  p.lse = lse;
+  p.f16 = io_dtype == SDPA_DTYPE_F16 ? 1 : 0;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.causal = causal ? 1 : 0;
+  p.window_left = window_left < 0 ? -1 : window_left;
+  p.first_keys = window_left < 0 ? 0 : first_keys;
+  p.seq_q_lens = seq_q_lens;
+  p.sink = sink;
+  p.mods.slopes = alibi_slopes;
+  p.tile_rows = plan.tile_rows;
+  p.n_rt = plan.n_rt;
+  p.tk = plan.tk;
+  p.n_ctas = plan.n_ctas;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.o_bytes);
+  nvtxRangePushA("sdpa_fwd_cached");
+  cudaError_t e = p.c.f8 ? launch_cached_rows_8(p, plan.mt, stream) : launch_cached_rows_16(p, plan.mt, stream);
+  if (e == cudaSuccess) e = launch_cached_merge(p, stream);
+  nvtxRangePop();
+  if (own) cudaFreeAsync(workspace, stream);
+  return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
+int sdpa_kv_append(int io_dtype, int cache_dtype, const void* q, void* q_out, const void* k, const void* v,
+                   void* k_cache, void* v_cache, float* k_scale, float* v_scale, const int32_t* page_table,
+                   const int32_t* seq_kv_lens, const int32_t* seq_q_lens, int B, int H_q, int H_kv, int S, int D,
+                   int n_pages, int page_size, int max_pages, const long long* strides, const double* inv_freq,
+                   int rot_dim, float mult, const int32_t* positions, int positions_per_batch, int n_axes,
+                   const int32_t* pair_axis, int interleaved, void* stream) {
+  KvAppendArgs a{};
+  const CacheArgs ca{cache_dtype, k_cache, v_cache, k_scale, v_scale, page_table, seq_kv_lens,
+                     n_pages, page_size, max_pages, H_kv, D};
+  int rc = fill_cache(ca, io_dtype, B, a.c);
+  if (rc != SDPA_OK) return rc;
+  if (H_q < 0 || S < 0 || !strides || !std::isfinite(mult)) return SDPA_ERR_INVALID;
+  if (rot_dim < 0 || rot_dim % 2 != 0 || rot_dim > D) return SDPA_ERR_INVALID;
+  if (rot_dim > 0 && !inv_freq) return SDPA_ERR_INVALID;
+  if (pair_axis && (!positions || n_axes <= 0 || n_axes > ROPE_MAX_AXES)) return SDPA_ERR_INVALID;
+  if (S == 0) return SDPA_OK;  // no rows
+  if (!k || !v || (H_q > 0 && (!q || !q_out))) return SDPA_ERR_INVALID;
+  if ((long long)B * S * (H_q + 2ll * H_kv) >= 1ll << 31 ||
+      (long long)B * (S / page_size + 2) * H_kv * 2 >= 1ll << 30)
+    return SDPA_ERR_INVALID;
+  for (const void* p : {q, (const void*)q_out, k, v})
+    if (misaligned(p, 2)) return SDPA_ERR_ALIGN;
+  if (misaligned(inv_freq, 8)) return SDPA_ERR_ALIGN;
+  for (const void* p : {(const void*)positions, (const void*)pair_axis, (const void*)seq_q_lens})
+    if (misaligned(p, 4)) return SDPA_ERR_ALIGN;
+  long long(*const st[4])[3] = {&a.qs, &a.qos, &a.kst, &a.vst};
+  const int heads[4] = {H_q, H_q, H_kv, H_kv};
+  const int ext0 = B, ext2 = S;
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 3; ++j) {
+      (*st[i])[j] = strides[3 * i + j];
+      if ((j == 0 ? ext0 : j == 1 ? heads[i] : ext2) > 1 && (*st[i])[j] < 0) return SDPA_ERR_INVALID;
+    }
+  // The rotated queries are the queries themselves, element by element, or share no element
+  // with any tensor of the call; the cache shares none with any other.
+  const Span pages[2] = {span_of(k_cache, cache_bytes(a.c)), span_of(v_cache, cache_bytes(a.c))};
+  if (meet(pages[0], pages[1])) return SDPA_ERR_INVALID;
+  const RopeRows kr = rope_rows(k, a.kst, B, H_kv, S, D), vr = rope_rows(v, a.vst, B, H_kv, S, D);
+  for (const Span& p : pages)
+    if (meet(p, span_of(kr)) || meet(p, span_of(vr))) return SDPA_ERR_INVALID;
+  if (H_q > 0) {
+    if (!rows_apart(a.qos, B, H_q, S, D)) return SDPA_ERR_INVALID;
+    const RopeRows qr = rope_rows(q, a.qs, B, H_q, S, D), qo = rope_rows(q_out, a.qos, B, H_q, S, D);
+    if ((!same_rows(qr, qo) && rows_meet(qr, qo)) || rows_meet(kr, qo) || rows_meet(vr, qo)) return SDPA_ERR_INVALID;
+    for (const Span& p : pages)
+      if (meet(p, span_of(qr)) || meet(p, span_of(qo))) return SDPA_ERR_INVALID;
+  }
+  a.q = q;
+  a.q_out = q_out;
+  a.k = k;
+  a.v = v;
+  a.Hq = H_q;
+  a.B = B;
+  a.T = S;
+  a.new_lens = seq_q_lens;
+  a.freq = inv_freq;
+  a.rot = rot_dim;
+  a.mult = mult;
+  a.positions = positions;
+  a.pos_bstride = positions_per_batch ? S : 0;
+  a.axis_stride = positions_per_batch ? (long long)B * S : S;
+  a.pair_axis = pair_axis;
+  a.n_axes = pair_axis ? n_axes : 1;
+  a.f16 = io_dtype == SDPA_DTYPE_F16 ? 1 : 0;
+  a.interleaved = interleaved ? 1 : 0;
+  int sms = 0;
+  rc = current_device_state(&a.status, &sms);
+  if (rc != SDPA_OK) return rc;
+  nvtxRangePushA("sdpa_kv_append");
+  const cudaError_t e = launch_kv_append(a, static_cast<cudaStream_t>(stream), sms);
+  nvtxRangePop();
+  return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
+int sdpa_kv_gather(int out_dtype, int cache_dtype, const void* k_cache, const void* v_cache, const float* k_scale,
+                   const float* v_scale, const int32_t* page_table, const int32_t* seq_kv_lens, void* k_out,
+                   void* v_out, int B, int H_kv, int S, int D, int n_pages, int page_size, int max_pages,
+                   void* stream) {
+  KvGatherArgs a{};
+  const CacheArgs ca{cache_dtype, k_cache, v_cache, k_scale, v_scale, page_table, seq_kv_lens,
+                     n_pages, page_size, max_pages, H_kv, D};
+  int rc = fill_cache(ca, out_dtype, B, a.c);
+  if (rc != SDPA_OK) return rc;
+  if (S < 0 || S > (long long)max_pages * page_size) return SDPA_ERR_INVALID;
+  if (S == 0) return SDPA_OK;  // no rows
+  if (!k_out || !v_out) return SDPA_ERR_INVALID;
+  if (misaligned(k_out, 16) || misaligned(v_out, 16)) return SDPA_ERR_ALIGN;
+  const size_t bytes = (size_t)B * H_kv * S * D * 2;
+  const Span out[2] = {span_of(k_out, bytes), span_of(v_out, bytes)};
+  if (meet(out[0], out[1])) return SDPA_ERR_INVALID;
+  for (const Span& p : {span_of(k_cache, cache_bytes(a.c)), span_of(v_cache, cache_bytes(a.c))})
+    if (meet(p, out[0]) || meet(p, out[1])) return SDPA_ERR_INVALID;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.B = B;
+  a.S = S;
+  a.f16 = out_dtype == SDPA_DTYPE_F16 ? 1 : 0;
+  int sms = 0;
+  rc = current_device_state(&a.status, &sms);
+  if (rc != SDPA_OK) return rc;
+  nvtxRangePushA("sdpa_kv_gather");
+  const cudaError_t e = launch_kv_gather(a, static_cast<cudaStream_t>(stream), sms);
+  nvtxRangePop();
+  return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,557 @@
+// sdpa_cached_rows.cuh -- attention over a paged cache for few rows a key/value head: generated tokens.
+//
+// Bound by memory: each key and value is read once for all query heads of its group, 2 D sizes
+// of bytes for 4 D flops a row. So the work is to keep enough reads in flight and everything
+// else out of their way.
+//
+//   - Warps share nothing while they run. A unit's keys are four pieces of 16 (or, in 8 bits, 32), one a warp, and
+//     each warp has a ring of stages of its own that it fills by 16-byte asynchronous copies and waits for
+//     by itself: no barrier of the CTA in the loop. Pieces that no row sees are neither read nor
+//     computed; rows of a piece that none sees are filled with zeros, so that what a recycled page
+//     holds never meets a product.
+//   - Both products on m16n8k16 with the softmax in registers: 16 rows are the most that such a call
+//     has as a rule (G heads, one token), and 16 rows of P against 16 keys of V take 2 clocks where the
+//     keys' bytes take 180; a 128-row tcgen05 tile would stand empty to seven eighths.
+//   - The maximum is a lazy reference: it is raised, and O rescaled, only when some score exceeds
+//     it by 2^8; one vote a piece asks for that.
+//   - 8 bits: codes become fp16 in registers (exact), the queries are fp16 times a power of two a row (exact
+//     down to 2^-29 of the row's largest), and P is fp16. A page's key scale joins the
+//     score's factor. Its value scale joins the weight's exponent, y = x + log2(vs), and O has a reference of
+//     its own for y: the largest weighted value is held to full precision however the scales differ.
+//     The contraction index is free to be permuted, so a thread's 16-byte piece of a key serves four steps,
+//     and byte pairs of V go through the 16-bit transposing load as they are.
+//   - P is fp16 or bf16 (the cache's type; rounded once, off by 2^-12 or 2^-9 of a weight); P in fp16 is
+//     taken times 2^6, so that what falls below its smallest step is below 2^-30 of the row's largest.
+#pragma once
+
+#include "cached.cuh"
+
+namespace sdpa {
+
+namespace cached_rows {
+
+constexpr int WARPS = 4, THREADS = 128;
+constexpr float RAISE = 8.f;
+
+enum : int { BF16 = 0, F16 = 1, E4M3 = 2 };
+
+template <int CT, int DP, int MT>
+struct Layout {
+  static constexpr int GROUPS = CT == E4M3 ? 2 : 1;  // of 16 keys
+  static constexpr int KS = 16 * GROUPS;             // keys of a warp's piece
+  static constexpr int TK = KS * WARPS;
+  static constexpr int RB = DP * (CT == E4M3 ? 1 : 2);  // bytes of a row
+  static constexpr int CH = RB / 16;
+  static constexpr int SIDE = KS * RB;                  // keys or values of a piece
+  static constexpr int STAGE = 2 * SIDE;
+  static constexpr int NST = 3 * 8192 / STAGE;
+  static constexpr int META = 32;                       // {ks, ks, vs, vs, page bits}
+  static constexpr int RING = NST * (STAGE + META);
+  static constexpr int TR = 16 * MT;
+  static constexpr int OROW = DP + 4;                   // floats of an O row in the exchange
+  static constexpr int XCH = WARPS * TR * (OROW + 3) * 4;
+  static constexpr int BYTES = WARPS * RING > XCH ? WARPS * RING : XCH;
+  static_assert(NST >= 2 && (CT != E4M3 || TK == CACHED_ROWS_TK_8) && (CT == E4M3 || TK == CACHED_ROWS_TK_16), "");
+};
+
+// 16-byte piece c of row r: rows of a piece lie on different banks for the eight rows of a
+// matrix load, and neighbouring rows in different halves for 16-byte loads.
+template <int CH>
+__device__ __forceinline__ int phys(int r, int c) {
+  if constexpr (CH == 4) return c ^ ((r >> 1) & 3);
+  else return c ^ (((r & 1) << 2) | ((r >> 1) & 3));
+}
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+// c += a (16 x 16, rows) * b (16 x 8, columns).
+template <bool F>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Four codes as two fp16 pairs, exact.
+__device__ __forceinline__ void codes_f16(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(four));
+}
+
+// CT: type of the cache; IOF: the queries and O are fp16 (a 16-bit cache has their type). MOD: capped or
+// distance-biased scores.
+template <int CT, bool IOF, int DP, int MT, bool MOD>
+__global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams p) {
+  using L = Layout<CT, DP, MT>;
+  constexpr bool PF = CT != BF16;  // the products are fp16
+  constexpr float BIAS = PF ? 6.f : 0.f;
+  constexpr int KD = DP / 16, NT = DP / 8, ESZ = CT == E4M3 ? 1 : 2;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ CachedStart sh_start;
+  __shared__ long long sh_sum[WARPS];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  const CachedStart st = cached_start<THREADS>(p, &sh_start, sh_sum, blockIdx.x == 0, [&](long long T) {
+    return share_begin(T, p.n_ctas, blockIdx.x);
+  });
+  pdl_launch_dependents();  // (the merge waits for this grid before it reads the parts)
+  CachedWalk walk{st.at, share_begin(st.T, p.n_ctas, blockIdx.x + 1), st.te, st.e};
+  if (walk.u >= walk.end) return;
+  const uint32_t ring = smem_u32(smem) + warp * L::RING;
+  // Columns past D are never copied: zeros, once (and again after the exchange has used the place).
+  auto clear = [&] {
+    if (p.D == DP) return;
+    for (int i = tid; i < WARPS * L::RING / 16; i += THREADS) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+  };
+  clear();
+  const int copy_row = lane / L::CH, copy_c = lane % L::CH;
+  const bool copy_in = copy_c * 16 < p.D * ESZ;
+  CachedPortion w;
+  while (walk.next(p, w)) {
+    const CachedBounds& s = w.s;
+    const int r0 = w.rt * L::TR;
+    // Piece of unit j: its first key, and which of its groups of 16 keys some row sees.
+    auto piece = [&](int j, int& k0) -> uint32_t {
+      k0 = cached_tile(s, j) * L::TK + warp * L::KS;
+      uint32_t seen = 0;
+#pragma unroll
+      for (int u = 0; u < L::GROUPS; ++u) {
+        const int a = k0 + 16 * u;
+        if (a < s.k_hi && (a + 15 >= s.k_lo || a < p.first_keys)) seen |= 1u << u;
+      }
+      return seen;
+    };
+    int next_page[L::GROUPS];
+    auto find_pages = [&](int j) {
+      int k0;
+      const uint32_t seen = j < w.j1 ? piece(j, k0) : 0u;
+#pragma unroll
+      for (int u = 0; u < L::GROUPS; ++u) next_page[u] = (seen >> u) & 1u ? cached_page(p, w.b, k0 + 16 * u) : -1;
+    };
+    auto issue = [&](int j) {
+      const int stage = j % L::NST;
+      const uint32_t to = ring + stage * (L::STAGE + L::META), meta = to + L::STAGE;
+      int k0;
+      if (j < w.j1 && piece(j, k0) != 0u) {
+        uint32_t ok = 0;
+#pragma unroll
+        for (int u = 0; u < L::GROUPS; ++u) {
+          const int page = next_page[u];
+          if (page < 0) continue;
+          ok |= 1u << u;
+          const int slot = (k0 + 16 * u) & (p.c.page - 1);
+          const long long head = (long long)page * p.c.Hkv + w.kvh, row = (head << p.c.page_shift) + slot;
+          const char* const kb = static_cast<const char*>(p.c.k) + row * p.D * ESZ + copy_c * 16;
+          const char* const vb = static_cast<const char*>(p.c.v) + row * p.D * ESZ + copy_c * 16;
+          if (copy_in) {
+#pragma unroll
+            for (int i = 0; i < 16 * L::CH / 32; ++i) {
+              const int r = copy_row + i * (32 / L::CH), key = k0 + 16 * u + r;
+              const bool take = key < s.k_hi && (key >= s.k_lo || key < p.first_keys);
+              const uint32_t at = to + (16 * u + r) * L::RB + phys<L::CH>(16 * u + r, copy_c) * 16;
+              const int off = r * p.D * ESZ;
+              copy16(at, kb + off, take);
+              copy16(at + L::SIDE, vb + off, take);
+            }
+          }
+          if constexpr (CT == E4M3) {
+            if (lane < 2) copy4(meta + (2 * lane + u) * 4, (lane ? p.c.vs : p.c.ks) + head);
+          }
+        }
+        if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(meta + 16), "r"(ok) : "memory");
+      }
+      copies_commit();
+      find_pages(j + 1);
+    };
+    find_pages(w.j0);
+#pragma unroll
+    for (int i = 0; i < L::NST - 1; ++i) issue(w.j0 + i);
+
+    // Queries as A fragments, and the rows' state. Thread rows: 16 m + g and 16 m + g + 8.
+    uint32_t qf[MT][KD][4];
+    float xmul[2 * MT], m[2 * MT], mv[CT == E4M3 ? 2 * MT : 1], l[2 * MT], slope2[MOD ? 2 * MT : 1];
+    CachedRow rows[2 * MT];
+    int lo_max = 0, hi_min = INT_MAX;
+#pragma unroll
+    for (int ri = 0; ri < 2 * MT; ++ri) {
+      const int mt = ri >> 1, half = ri & 1, r = r0 + 16 * mt + g + 8 * half;
+      const bool in = r < p.R;
+      const uint16_t* const q = static_cast<const uint16_t*>(p.q) + (((long long)w.b * p.c.Hkv + w.kvh) * p.R + r) * p.D;
+      float amax = 0.f;
+#pragma unroll
+      for (int kd = 0; kd < KD; ++kd) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int d = CT == E4M3 ? 64 * (kd >> 2) + 16 * t + 4 * (kd & 3) + 2 * x : 16 * kd + 2 * t + 8 * x;
+          uint32_t v = 0u;
+          if (in && d < p.D) v = *reinterpret_cast<const uint32_t*>(q + d);
+          qf[mt][kd][half + 2 * x] = v;
+          if constexpr (CT == E4M3 && !IOF) amax = fmaxf(amax, fmaxf(fabsf(io_lo<false>(v)), fabsf(io_hi<false>(v))));
+        }
+      }
+      xmul[ri] = 1.f;
+      if constexpr (CT == E4M3 && !IOF) {
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // 2^e brings the row's largest into [2^14, 2^15).
+        const int e = amax > 0.f ? min(max(14 - ((int)(__float_as_uint(amax) >> 23) - 127), -113), 126) : 0;
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        xmul[ri] = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int kd = 0; kd < KD; ++kd)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t& v = qf[mt][kd][half + 2 * x];
+            v = pack_f16x2(io_lo<false>(v) * up, io_hi<false>(v) * up);
+          }
+      }
+      if constexpr (!MOD) xmul[ri] *= p.scale_log2;
+      rows[ri] = cached_row(p, s, r);
+      if (!in) rows[ri].lo = 0, rows[ri].hi = s.L - 1;  // (not written; never the reason for a mask)
+      lo_max = max(lo_max, rows[ri].lo);
+      hi_min = min(hi_min, rows[ri].hi);
+      if constexpr (MOD)
+        slope2[ri] = p.mods.slopes && in ? p.mods.slopes[w.kvh * p.G + r / p.Sq] * 1.4426950408889634f : 0.f;
+      m[ri] = -INFINITY;
+      l[ri] = 0.f;
+      if constexpr (CT == E4M3) mv[ri] = -INFINITY;
+    }
+    lo_max = __reduce_max_sync(0xffffffffu, lo_max);
+    hi_min = __reduce_min_sync(0xffffffffu, hi_min);
+    float o[MT][NT][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+
+#pragma unroll 1
+    for (int j = w.j0; j < w.j1; ++j) {
+      copies_wait<L::NST - 2>();
+      __syncwarp();  // every lane's copies of this stage have landed, and all are done with the one before
+      issue(j + L::NST - 1);
+      int k0;
+      const uint32_t seen = piece(j, k0);
+      if (seen == 0u) continue;
+      const uint32_t at = ring + (j % L::NST) * (L::STAGE + L::META), meta = at + L::STAGE;
+      uint32_t ok;
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(ok) : "r"(meta + 16) : "memory");
+#pragma unroll
+      for (int u = 0; u < L::GROUPS; ++u) {
+        if (!((ok >> u) & 1u)) continue;
+        const uint32_t sk = at + 16 * u * L::RB, sv = sk + L::SIDE;
+        // ---- S = Q K^T: element [mt][n][e]: row g + 8 (e >> 1), key 8 n + 2 t + (e & 1)
+        float sc[MT][2][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[mt][n][e] = 0.f;
+        if constexpr (CT == E4M3) {
+#pragma unroll
+          for (int h = 0; h < DP / 64; ++h)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              const uint4 v = lds16(sk + (8 * n + g) * L::RB + phys<L::CH>(8 * n + g, 4 * h + t) * 16);
+              const uint32_t four[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int jj = 0; jj < 4; ++jj) {
+                uint32_t b0, b1;
+                codes_f16(four[jj], b0, b1);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) mma<true>(sc[mt][n], qf[mt][4 * h + jj], b0, b1);
+              }
+            }
+        } else {
+          const int r = (lane & 7) + ((lane >> 4) << 3), c = (lane >> 3) & 1;
+#pragma unroll
+          for (int kd = 0; kd < KD; ++kd) {
+            uint32_t b[4];
+            ldm4(b, sk + r * L::RB + phys<L::CH>(r, 2 * kd + c) * 16);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma<PF>(sc[mt][0], qf[mt][kd], b[0], b[1]);
+              mma<PF>(sc[mt][1], qf[mt][kd], b[2], b[3]);
+            }
+          }
+        }
+        // ---- scores in log2 units, masked
+        float lvs = 0.f, ks = 1.f;
+        if constexpr (CT == E4M3) {
+          float vs;
+          asm volatile("ld.shared.b32 %0, [%1];" : "=f"(ks) : "r"(meta + u * 4) : "memory");
+          asm volatile("ld.shared.b32 %0, [%1];" : "=f"(vs) : "r"(meta + 8 + u * 4) : "memory");
+          lvs = __log2f(vs);
+        }
+        const int ka = k0 + 16 * u;
+#pragma unroll
+        for (int ri = 0; ri < 2 * MT; ++ri) {
+          const float f = xmul[ri] * ks;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) sc[ri >> 1][n][2 * (ri & 1) + e] *= f;
+        }
+        if constexpr (MOD) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            uint64_t x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = f2_pack(sc[mt][i >> 1][2 * (i & 1)], sc[mt][i >> 1][2 * (i & 1) + 1]);
+            const bool cap = p.mods.cap_in != 0.f;
+            if (cap) tanh2_any(x, p.mods.cap_in);
+            const float c = cap ? p.mods.cap_log2 : p.scale_log2;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float x0, x1;
+              f2_unpack(x[i], x0, x1);
+              const int ri = 2 * mt + (i & 1), key = ka + 8 * (i >> 1) + 2 * t;
+              sc[mt][i >> 1][2 * (i & 1)] = fmaf(-slope2[ri], fabsf((float)(rows[ri].place - key)), x0 * c);
+              sc[mt][i >> 1][2 * (i & 1) + 1] = fmaf(-slope2[ri], fabsf((float)(rows[ri].place - key - 1)), x1 * c);
+            }
+          }
+        }
+        if (!(ka + 15 <= hi_min && (ka >= lo_max || ka + 15 < p.first_keys))) {
+#pragma unroll
+          for (int ri = 0; ri < 2 * MT; ++ri)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int key = ka + 8 * n + 2 * t + e;
+                if (key > rows[ri].hi || (key < rows[ri].lo && key >= p.first_keys)) sc[ri >> 1][n][2 * (ri & 1) + e] = -INFINITY;
+              }
+        }
+        // ---- the reference
+        bool raise = false;
+        float mx[2 * MT];
+#pragma unroll
+        for (int ri = 0; ri < 2 * MT; ++ri) {
+          const float(&a)[2][4] = sc[ri >> 1];
+          const int e = 2 * (ri & 1);
+          mx[ri] = fmaxf(fmaxf(a[0][e], a[0][e + 1]), fmaxf(a[1][e], a[1][e + 1]));
+          raise |= mx[ri] > m[ri] + RAISE;
+          if constexpr (CT == E4M3) raise |= mx[ri] + lvs > mv[ri] + RAISE;
+        }
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int ri = 0; ri < 2 * MT; ++ri) {
+            float x = fmaxf(mx[ri], __shfl_xor_sync(0xffffffffu, mx[ri], 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            float fo = 1.f;
+            if (x > m[ri] + RAISE) {
+              const float a = ex2_approx(m[ri] - x);  // 0 for the first key
+              l[ri] *= a;
+              m[ri] = x;
+              if constexpr (CT != E4M3) fo = a;
+            }
+            if constexpr (CT == E4M3) {
+              if (x + lvs > mv[ri] + RAISE) {
+                fo = ex2_approx(mv[ri] - (x + lvs));
+                mv[ri] = x + lvs;
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              o[ri >> 1][n][2 * (ri & 1)] *= fo;
+              o[ri >> 1][n][2 * (ri & 1) + 1] *= fo;
+            }
+          }
+        }
+        // ---- P, as A fragments
+        uint32_t pf[MT][4];
+#pragma unroll
+        for (int ri = 0; ri < 2 * MT; ++ri) {
+          const float neg = m[ri] == -INFINITY ? 0.f : (CT == E4M3 ? 0.f : BIAS) - m[ri];
+          const float neg_v = CT == E4M3 ? (mv[ri] == -INFINITY ? 0.f : BIAS + lvs - mv[ri]) : 0.f;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const float x0 = sc[ri >> 1][n][2 * (ri & 1)], x1 = sc[ri >> 1][n][2 * (ri & 1) + 1];
+            const float p0 = ex2_approx(x0 + neg), p1 = ex2_approx(x1 + neg);
+            l[ri] += p0 + p1;
+            if constexpr (CT == E4M3) pf[ri >> 1][(ri & 1) + 2 * n] = pack_f16x2(ex2_approx(x0 + neg_v), ex2_approx(x1 + neg_v));
+            else pf[ri >> 1][(ri & 1) + 2 * n] = pack_io2<PF>(p0, p1);
+          }
+        }
+        // ---- O += P V
+        if constexpr (CT == E4M3) {
+          const int r = (lane & 7) + (((lane >> 3) & 1) << 3), c = lane >> 4;
+#pragma unroll
+          for (int cp = 0; cp < DP / 32; ++cp) {
+            uint32_t b[4], ev[4], od[4];
+            ldm4t(b, sv + r * L::RB + phys<L::CH>(r, 2 * cp + c) * 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) codes_f16(__byte_perm(b[i], 0u, 0x3120), ev[i], od[i]);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma<true>(o[mt][4 * cp], pf[mt], ev[0], ev[1]);
+              mma<true>(o[mt][4 * cp + 1], pf[mt], od[0], od[1]);
+              mma<true>(o[mt][4 * cp + 2], pf[mt], ev[2], ev[3]);
+              mma<true>(o[mt][4 * cp + 3], pf[mt], od[2], od[3]);
+            }
+          }
+        } else {
+          const int r = (lane & 7) + (((lane >> 3) & 1) << 3), c = lane >> 4;
+#pragma unroll
+          for (int dn = 0; dn < KD; ++dn) {
+            uint32_t b[4];
+            ldm4t(b, sv + r * L::RB + phys<L::CH>(r, 2 * dn + c) * 16);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma<PF>(o[mt][2 * dn], pf[mt], b[0], b[1]);
+              mma<PF>(o[mt][2 * dn + 1], pf[mt], b[2], b[3]);
+            }
+          }
+        }
+      }
+    }
+
+    // ---- the four warps' states together, through the ring's place
+    copies_wait<0>();
+    __syncthreads();
+    float* const xo = reinterpret_cast<float*>(smem);  // [WARPS][TR][OROW]
+    float* const xm = xo + WARPS * L::TR * L::OROW;    // [WARPS][TR] m, then l, then mv
+    float* const xl = xm + WARPS * L::TR;
+    float* const xv = xl + WARPS * L::TR;
+#pragma unroll
+    for (int ri = 0; ri < 2 * MT; ++ri) {
+      float x = l[ri] + __shfl_xor_sync(0xffffffffu, l[ri], 1);
+      x += __shfl_xor_sync(0xffffffffu, x, 2);
+      if (t == 0) {
+        const int at = warp * L::TR + 16 * (ri >> 1) + g + 8 * (ri & 1);
+        xm[at] = m[ri];
+        xl[at] = x;
+        if constexpr (CT == E4M3) xv[at] = mv[ri];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int ri = 0; ri < 2 * MT; ++ri) {
+      const int row = 16 * (ri >> 1) + g + 8 * (ri & 1);
+      const float* const ref = CT == E4M3 ? xv : xm;
+      const float mine = ref[warp * L::TR + row];
+      const float M = fmaxf(fmaxf(ref[row], ref[L::TR + row]), fmaxf(ref[2 * L::TR + row], ref[3 * L::TR + row]));
+      const float f = mine == -INFINITY ? 0.f : ex2_approx(mine - M);
+      float* const to = xo + (warp * L::TR + row) * L::OROW;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float v0 = o[ri >> 1][n][2 * (ri & 1)] * f, v1 = o[ri >> 1][n][2 * (ri & 1) + 1] * f;
+        if constexpr (CT == E4M3) {  // tile n holds the even or odd columns of 16-column piece n / 2
+          to[16 * (n >> 1) + 4 * t + (n & 1)] = v0;
+          to[16 * (n >> 1) + 4 * t + 2 + (n & 1)] = v1;
+        } else {
+          to[8 * n + 2 * t] = v0;
+          to[8 * n + 2 * t + 1] = v1;
+        }
+      }
+    }
+    __syncthreads();
+    const int live_rows = min(L::TR, p.R - r0), pieces = p.D / 8;
+    for (int i = tid; i < live_rows * pieces; i += THREADS) {
+      const int row = i / pieces, c = i % pieces;
+      float M = -INFINITY, Mv = -INFINITY, lt = 0.f;
+#pragma unroll
+      for (int k = 0; k < WARPS; ++k) {
+        M = fmaxf(M, xm[k * L::TR + row]);
+        if constexpr (CT == E4M3) Mv = fmaxf(Mv, xv[k * L::TR + row]);
+      }
+#pragma unroll
+      for (int k = 0; k < WARPS; ++k) {
+        const float mk = xm[k * L::TR + row];
+        if (mk != -INFINITY) lt += xl[k * L::TR + row] * ex2_approx(mk - M);
+      }
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = 0.f;
+#pragma unroll
+      for (int k = 0; k < WARPS; ++k) {
+        const float4* from = reinterpret_cast<const float4*>(xo + (k * L::TR + row) * L::OROW + c * 8);
+        const float4 a = from[0], b = from[1];
+        y[0] += a.x, y[1] += a.y, y[2] += a.z, y[3] += a.w, y[4] += b.x, y[5] += b.y, y[6] += b.z, y[7] += b.w;
+      }
+      const bool none = M == -INFINITY;
+      float f = none ? 0.f : 1.f / lt;
+      if constexpr (CT == E4M3) f = none ? 0.f : f * exp2f(Mv - M - BIAS);
+      const float lse2 = none ? -INFINITY : M - (CT == E4M3 ? 0.f : BIAS) + __log2f(lt);
+      const int r = r0 + row;
+      if (w.slot >= 0) {
+        const long long at = ((long long)blockIdx.x * 2 + w.slot) * L::TR + row;
+        float4* to = reinterpret_cast<float4*>(p.part_o + at * p.D + c * 8);
+        to[0] = make_float4(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
+        to[1] = make_float4(y[4] * f, y[5] * f, y[6] * f, y[7] * f);
+        if (c == 0) p.part_lse[at] = lse2;
+      } else {
+        float fs;
+        const float all = cached_with_sink(p, w.kvh * p.G + r / p.Sq, lse2, fs);
+        f *= fs;
+        const long long orow = ((long long)w.b * p.c.Hkv + w.kvh) * p.R + r;
+        uint4 v;
+        v.x = pack_io2<IOF>(y[0] * f, y[1] * f), v.y = pack_io2<IOF>(y[2] * f, y[3] * f);
+        v.z = pack_io2<IOF>(y[4] * f, y[5] * f), v.w = pack_io2<IOF>(y[6] * f, y[7] * f);
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + orow * p.D + c * 8) = v;
+        if (c == 0) p.lse[orow] = all * 0.6931471805599453f;
+      }
+    }
+    __syncthreads();
+    clear();
+  }
+}
+
+template <int CT, bool IOF, int DP, int MT, bool MOD>
+cudaError_t setup_one() {
+  return cudaFuncSetAttribute(cached_rows_kernel<CT, IOF, DP, MT, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Layout<CT, DP, MT>::BYTES);
+}
+template <int CT, bool IOF>
+cudaError_t setup_type() {
+  cudaError_t e = cudaSuccess;
+  for (auto* f : {setup_one<CT, IOF, 64, 1, false>, setup_one<CT, IOF, 64, 1, true>, setup_one<CT, IOF, 64, 2, false>,
+                  setup_one<CT, IOF, 64, 2, true>, setup_one<CT, IOF, 128, 1, false>, setup_one<CT, IOF, 128, 1, true>,
+                  setup_one<CT, IOF, 128, 2, false>, setup_one<CT, IOF, 128, 2, true>})
+    if (e == cudaSuccess) e = f();
+  return e;
+}
+template <int CT, bool IOF, int DP, int MT, bool MOD>
+cudaError_t launch_one(const CachedParams& p, cudaStream_t s) {
+  return launch_kernel(cached_rows_kernel<CT, IOF, DP, MT, MOD>, dim3((unsigned)p.n_ctas), dim3(THREADS),
+                       Layout<CT, DP, MT>::BYTES, s, false, p);
+}
+template <int CT, bool IOF, int DP>
+cudaError_t launch_width(const CachedParams& p, int mt, cudaStream_t s) {
+  const bool mod = p.mods.cap_in != 0.f || p.mods.slopes != nullptr;
+  if (mt == 1) return mod ? launch_one<CT, IOF, DP, 1, true>(p, s) : launch_one<CT, IOF, DP, 1, false>(p, s);
+  return mod ? launch_one<CT, IOF, DP, 2, true>(p, s) : launch_one<CT, IOF, DP, 2, false>(p, s);
+}
+template <int CT, bool IOF>
+cudaError_t launch_type(const CachedParams& p, int mt, cudaStream_t s) {
+  return p.D <= 64 ? launch_width<CT, IOF, 64>(p, mt, s) : launch_width<CT, IOF, 128>(p, mt, s);
+}
+
+}  // namespace cached_rows
+
+}  // namespace sdpa

@@ -15,6 +15,9 @@
 // t * 2^-54 turns of f's own rounding and 2^-33 of the cut. They convert to fp32 in
 // [-1/2, 1/2) turns (rounded once, 2^-25 relative) and go through sincospif.
 //
+// Several axes. Tokens of images and videos have a position on each of a few axes (time,
+// height, width); each pair then turns by the position on its own axis, pair_axis[i].
+//
 // Cost. Every element is read once and written once; the angle work of a
 // (token, pair) is shared by the heads a thread walks. So the bound is memory,
 // 4 bytes an element.
@@ -30,6 +33,7 @@
 
 #include "common.cuh"
 #include "ptx.cuh"
+#include "rope.cuh"
 
 namespace sdpa {
 
@@ -49,31 +53,16 @@ struct RopeParams {
   const double* freq;      // (rot / 2,) radians per position
   const int32_t* positions;  // or null: offset + s
   long long pos_bstride;   // 0: one row of positions for every batch row
+  // Several axes: pair i takes its position from row pair_axis[i] (clamped to the n_axes
+  // there are) of positions (n_axes, S) or (n_axes, B, S), axis_stride apart. Else null.
+  const int32_t* pair_axis;
+  int n_axes;
+  long long axis_stride;
   int offset;
   int B, S, D, rot;
   int sign;                // +1, or -1 for the gradient
   float mult;
 };
-
-// 2^64 * f / (2 pi) modulo 2^64, for any finite f.
-__device__ __forceinline__ uint64_t turn_fraction(double f) {
-  double t = f * 0.15915494309189533577;
-  t -= floor(t);
-  // [0, 1] in two 32-bit pieces (a product by 2^64 may round to 2^64).
-  const double hi = floor(t * 4294967296.0);
-  const double lo = (t * 4294967296.0 - hi) * 4294967296.0;
-  return ((uint64_t)hi << 32) + (uint64_t)lo;
-}
-
-__device__ __forceinline__ void angle_sin_cos(uint64_t turn, int pos, float& sn, float& cs) {
-  const uint64_t a = turn * (uint64_t)(int64_t)pos;
-  sincospif((float)(int32_t)(a >> 32) * 4.6566128730773926e-10f, &sn, &cs);  // 2^-31: half turns
-}
-
-template <bool F16>
-__device__ __forceinline__ float io_f32(uint16_t v) {
-  return F16 ? __half2float(__ushort_as_half(v)) : __uint_as_float((uint32_t)v << 16);
-}
 
 // Head h of the call's H0 + H1 heads: its tensor and the head's index there.
 __device__ __forceinline__ const RopeTensor& rope_head(const RopeParams& p, int h, int& hh) {
@@ -111,12 +100,16 @@ __device__ __forceinline__ void st_piece(uint16_t* p, const Piece<VW>& v) {
 // rot a multiple of 2 VW, D of VW, every row aligned to a piece. A work item is (token,
 // column group), a group being VW pairs, or two pass-through pieces (one, at an odd end);
 // blockIdx.y selects `heads` consecutive heads.
-template <bool F16, bool INTER, int VW>
+template <bool F16, bool INTER, int VW, bool AXES>
 __global__ void __launch_bounds__(THREADS) rope_vec(const RopeParams p, int heads, long long n_items) {
   constexpr int UNROLL = 4, NW = VW / 2;
-  __shared__ uint64_t turns[256];  // rot <= 512
+  __shared__ uint64_t turns[ROPE_MAX_PAIRS];
+  __shared__ uint8_t axis_of[AXES ? ROPE_MAX_PAIRS : 1];
   const int half = p.rot / 2;
-  for (int i = threadIdx.x; i < half; i += THREADS) turns[i] = turn_fraction(p.freq[i]);
+  for (int i = threadIdx.x; i < half; i += THREADS) {
+    turns[i] = turn_fraction(p.freq[i]);
+    if constexpr (AXES) axis_of[i] = (uint8_t)min(max(p.pair_axis[i], 0), p.n_axes - 1);
+  }
   __syncthreads();
   const int groups = (p.D + 2 * VW - 1) / (2 * VW), rot_groups = p.rot / (2 * VW);
   const int H = p.t[0].H + p.t[1].H;
@@ -134,9 +127,16 @@ __global__ void __launch_bounds__(THREADS) rope_vec(const RopeParams p, int head
     const bool two = c1 < p.D;
     float sn[VW], cs[VW];
     if (rotated) {
-      const int pos = p.positions ? p.positions[b * p.pos_bstride + s] : p.offset + s;
+      int pos = 0, axis = -1;
+      if constexpr (!AXES) pos = p.positions ? p.positions[b * p.pos_bstride + s] : p.offset + s;
 #pragma unroll
       for (int i = 0; i < VW; ++i) {
+        if constexpr (AXES) {  // (neighbouring pairs mostly turn by the same axis)
+          if (axis_of[c * VW + i] != axis) {
+            axis = axis_of[c * VW + i];
+            pos = p.positions[axis * p.axis_stride + b * p.pos_bstride + s];
+          }
+        }
         angle_sin_cos(turns[c * VW + i], pos, sn[i], cs[i]);
         sn[i] *= p.sign > 0 ? p.mult : -p.mult;
         cs[i] *= p.mult;
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(THREADS) rope_vec(const RopeParams p, int head
 template <bool F16>
 __global__ void __launch_bounds__(THREADS) rope_pairs(const RopeParams p, int interleaved, int heads,
                                                       long long n_items) {
-  __shared__ uint64_t turns[256];
+  __shared__ uint64_t turns[ROPE_MAX_PAIRS];
   const int half = p.rot / 2;
   for (int i = threadIdx.x; i < half; i += THREADS) turns[i] = turn_fraction(p.freq[i]);
   __syncthreads();
@@ -207,7 +207,8 @@ __global__ void __launch_bounds__(THREADS) rope_pairs(const RopeParams p, int in
     const int c1 = rotated ? (interleaved ? 2 * c + 1 : c + half) : c0 + 1;
     float sn = 0.f, cs = 0.f;
     if (rotated) {
-      const int pos = p.positions ? p.positions[b * p.pos_bstride + s] : p.offset + s;
+      const int axis = p.pair_axis ? min(max(p.pair_axis[c], 0), p.n_axes - 1) : 0;
+      const int pos = p.positions ? p.positions[axis * p.axis_stride + b * p.pos_bstride + s] : p.offset + s;
       angle_sin_cos(turns[c], pos, sn, cs);
       sn *= p.sign > 0 ? p.mult : -p.mult;
       cs *= p.mult;
@@ -239,11 +240,16 @@ int piece_of(const void* base, const long long (&st)[3]) {
   return 0;
 }
 
+template <bool F16, bool INTER, bool AXES>
+void launch_vec_axes(const RopeParams& p, int vw, int heads, long long items, dim3 grid, cudaStream_t s) {
+  if (vw == 8) rope_vec<F16, INTER, 8, AXES><<<grid, THREADS, 0, s>>>(p, heads, items);
+  else if (vw == 4) rope_vec<F16, INTER, 4, AXES><<<grid, THREADS, 0, s>>>(p, heads, items);
+  else rope_vec<F16, INTER, 2, AXES><<<grid, THREADS, 0, s>>>(p, heads, items);
+}
 template <bool F16, bool INTER>
 void launch_vec(const RopeParams& p, int vw, int heads, long long items, dim3 grid, cudaStream_t s) {
-  if (vw == 8) rope_vec<F16, INTER, 8><<<grid, THREADS, 0, s>>>(p, heads, items);
-  else if (vw == 4) rope_vec<F16, INTER, 4><<<grid, THREADS, 0, s>>>(p, heads, items);
-  else rope_vec<F16, INTER, 2><<<grid, THREADS, 0, s>>>(p, heads, items);
+  if (p.pair_axis) launch_vec_axes<F16, INTER, true>(p, vw, heads, items, grid, s);
+  else launch_vec_axes<F16, INTER, false>(p, vw, heads, items, grid, s);
 }
 
 }  // namespace
@@ -268,6 +274,9 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream, int num_sms) {
   p.freq = a.freq;
   p.positions = a.positions;
   p.pos_bstride = a.pos_bstride;
+  p.pair_axis = a.pair_axis;
+  p.n_axes = a.n_axes;
+  p.axis_stride = a.axis_stride;
   p.offset = a.offset;
   p.B = a.B;
   p.S = a.S;

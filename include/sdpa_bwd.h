@@ -53,10 +53,12 @@ typedef enum {
   SDPA_ERR_WORKSPACE = 4,   /* workspace smaller than sdpa_bwd_workspace_size()     */
   SDPA_ERR_CUDA = 5,        /* a CUDA runtime call failed                           */
   SDPA_ERR_TIMEOUT = 6,     /* a device-side bounded wait ran out (reported later)  */
-  SDPA_ERR_BOUNDS = 7       /* debug-bounds build only (libsdpa_bwd_debug.so, built
+  SDPA_ERR_BOUNDS = 7,      /* debug-bounds build only (libsdpa_bwd_debug.so, built
                                with SDPA_DEBUG_BOUNDS): a kernel found a global
                                access outside its region and skipped it (reported
                                later, results invalid)                               */
+  SDPA_ERR_PAGE = 8         /* a cache call met a page id outside the cache, or a length past
+                               its page table, and skipped it (reported later)       */
 } sdpa_status;
 
 /* Element types: of an optional additive bias (BF16, F16 or F32) and of the
@@ -64,7 +66,8 @@ typedef enum {
 typedef enum {
   SDPA_DTYPE_BF16 = 0,
   SDPA_DTYPE_F32 = 1,
-  SDPA_DTYPE_F16 = 2
+  SDPA_DTYPE_F16 = 2,
+  SDPA_DTYPE_E4M3 = 3  /* 8-bit floating point of a cache: 4 exponent and 3 fraction bits, up to 448 */
 } sdpa_dtype;
 
 /*
@@ -423,6 +426,105 @@ int sdpa_rope(int io_dtype, const void* q, const void* k, void* q_out, void* k_o
               int H_kv, int S, int D, const long long* strides, const double* inv_freq, int rot_dim,
               float mult, const int32_t* positions, int positions_per_batch, int offset,
               int interleaved, int inverse, void* stream);
+
+/*
+ * sdpa_rope() for tokens with a position on each of several axes (time, height and width
+ * of a video, say): pair i turns by the position on its axis,
+ *     positions[pair_axis[i]][(b,) s] * inv_freq[i].
+ * Arguments as sdpa_rope() without the offset, with
+ *   positions   device int32 (n_axes, S), or with positions_per_batch (n_axes, B, S).
+ *   n_axes      1 to 16.
+ *   pair_axis   device int32 (rot_dim / 2,): the axis of each pair, in any order; values outside
+ *               [0, n_axes) count as the nearest one.
+ * Returns as sdpa_rope().
+ */
+int sdpa_rope_axes(int io_dtype, const void* q, const void* k, void* q_out, void* k_out, int B, int H_q,
+                   int H_kv, int S, int D, const long long* strides, const double* inv_freq, int rot_dim,
+                   float mult, const int32_t* positions, int positions_per_batch, int n_axes,
+                   const int32_t* pair_axis, int interleaved, int inverse, void* stream);
+
+/*
+ * A paged cache of keys and values, for generating token by token. Position j of batch row b
+ * is slot j % page_size of page page_table[b, j / page_size] (int32 (B, max_pages)). Two buffers,
+ * keys and values, of shape (n_pages, H_kv, page_size, D), 16-byte aligned; page_size 16, 32, 64, 128 or 256;
+ * D a multiple of 16 up to 128. cache_dtype is the io type, or SDPA_DTYPE_E4M3 with scales
+ * k_scale, v_scale, fp32 (n_pages, H_kv): a code of a page and head stands for code * scale. (In 16
+ * bits both are NULL.) A zeroed buffer, its scales any positive numbers, is an empty cache.
+ * seq_kv_lens, int32 (B,), are the positions in use, those that the call itself appends
+ * included. A page may serve several batch rows (a shared prefix) as long as no call appends to it.
+ * The cache calls read page ids and lengths on the device: a page id outside [0, n_pages) within a
+ * length, and a length outside [0, max_pages * page_size], are reported by
+ * sdpa_bwd_check_device_status() (SDPA_ERR_PAGE). Nothing outside the buffers is touched: such
+ * rows are not appended, read back as zeros, and invisible to the attention, which takes
+ * a length past the table as the table's.
+ */
+
+/*
+ * Appends keys and values, and rotates them and the queries on the way. Row t of batch row b's
+ * first n = seq_q_lens[b] rows (seq_q_lens NULL: all S) goes to position seq_kv_lens[b] - n + t.
+ * Keys and queries are rotated as by sdpa_rope() at their positions, or at those given;
+ * values are copied. Each cached element is rounded once, from fp32.
+ * In 8 bits each page and head that gets rows has its scale set to the smallest power of two,
+ * at least 2^-64, that brings the largest new magnitude within 448, or keeps a larger one that
+ * its older slots have; where it grows they are multiplied anew, exactly but for
+ * values below 2^-6 of the new scale, which are rounded to its steps. A page whose first slot is
+ * written starts anew. Infinities saturate, NaN stay, and neither counts for the scale. What
+ * lies behind a sequence's last position has no meaning.
+ *   q, q_out    device 16-bit (B, H_q, S, D) by strides, every row rotated; H_q = 0: none.
+ *   k, v        device 16-bit (B, H_kv, S, D) by strides.
+ *   strides     host array of 12: batch, head, position strides in elements of q, q_out, k, v.
+ *   inv_freq, rot_dim, mult, interleaved  as sdpa_rope(); rot_dim 0: nothing is rotated.
+ *   positions   device int32 (S,), or with positions_per_batch (B, S); with pair_axis (n_axes
+ *               and pair_axis as sdpa_rope_axes()) an (n_axes, ...) of these. NULL: the
+ *               positions in the cache.
+ * q_out may be q itself (same pointer and strides) and otherwise shares no element with any
+ * tensor; the buffers share none with the others (SDPA_ERR_INVALID). No two rows of a call may have
+ * the same page to write. S = 0 returns SDPA_OK without work. Returns SDPA_ERR_INVALID,
+ * SDPA_ERR_UNSUPPORTED (page_size, D) or SDPA_ERR_ALIGN before anything is enqueued on `stream`.
+ */
+int sdpa_kv_append(int io_dtype, int cache_dtype, const void* q, void* q_out, const void* k, const void* v,
+                   void* k_cache, void* v_cache, float* k_scale, float* v_scale, const int32_t* page_table,
+                   const int32_t* seq_kv_lens, const int32_t* seq_q_lens, int B, int H_q, int H_kv, int S, int D,
+                   int n_pages, int page_size, int max_pages, const long long* strides, const double* inv_freq,
+                   int rot_dim, float mult, const int32_t* positions, int positions_per_batch, int n_axes,
+                   const int32_t* pair_axis, int interleaved, void* stream);
+
+/*
+ * Reads the first S (at most max_pages * page_size) positions of every batch row back as k_out, v_out:
+ * contiguous (B, H_kv, S, D) of out_dtype (SDPA_DTYPE_BF16 or F16; that of a 16-bit cache), 16-byte
+ * aligned, zeros at and past seq_kv_lens[b]. Codes times a power of two are exact in bf16.
+ */
+int sdpa_kv_gather(int out_dtype, int cache_dtype, const void* k_cache, const void* v_cache, const float* k_scale,
+                   const float* v_scale, const int32_t* page_table, const int32_t* seq_kv_lens, void* k_out,
+                   void* v_out, int B, int H_kv, int S, int D, int n_pages, int page_size, int max_pages,
+                   void* stream);
+
+/*
+ * Attention of queries to the keys and values of a cache: O and LSE as sdpa_fwd(), for one new
+ * token, a few, or a chunk of a prompt. Query i of batch row b, of its n = seq_q_lens[b] (NULL: S_q),
+ * stands at position seq_kv_lens[b] - n + i, its place, and sees key j < seq_kv_lens[b] when
+ *     j <= place (causal), and j >= place - window_left (window_left >= 0) or j < first_keys:
+ * under a window the first few keys may stay visible from everywhere. Rows past n, and
+ * rows that see no key, get O = 0 and LSE = -inf, or the sink's logit.
+ *   q, o       device 16-bit (B, H_q, S_q, D) contiguous, 16-byte aligned; lse fp32 (B, H_q, S_q).
+ *   scale, sink, softcap, alibi_slopes  as sdpa_fwd_scored(); the distance is |place - j|.
+ *   first_keys >= 0; without a window (window_left < 0) it changes nothing.
+ *   workspace  device buffer of >= sdpa_fwd_cached_workspace_size() bytes, 256-byte aligned, used only for
+ *              the duration of the call on `stream`; NULL: from the stream-ordered allocator.
+ * Elements of q and of visible keys and values must be finite, as in every call of this library;
+ * what lies in the cache elsewhere has no effect. In 8 bits scales must be positive. Scores and sums are fp32; weights meet 16-bit values as
+ * bf16 or fp16 (the cache's type), and codes as fp16 (sums over rows are taken before that rounding).
+ * Over an 8-bit cache the result is that of the values that the codes stand for, with no further
+ * rounding of them where scales are powers of two. Results do not depend on timing. Returns as sdpa_fwd_scored(), SDPA_ERR_UNSUPPORTED for page_size and D, and SDPA_ERR_WORKSPACE.
+ */
+size_t sdpa_fwd_cached_workspace_size(int B, int H_q, int H_kv, int S_q, int D, int cache_dtype, int page_size,
+                                      int max_pages);
+int sdpa_fwd_cached(int io_dtype, int cache_dtype, const void* q, const void* k_cache, const void* v_cache,
+                    const float* k_scale, const float* v_scale, const int32_t* page_table, const int32_t* seq_kv_lens,
+                    const int32_t* seq_q_lens, void* o, float* lse, int B, int H_q, int H_kv, int S_q, int D,
+                    int n_pages, int page_size, int max_pages, float scale, int causal, int window_left,
+                    int first_keys, const float* sink, float softcap, const float* alibi_slopes, void* workspace,
+                    size_t workspace_bytes, void* stream);
 
 /*
  * NVFP4 fake quantization ("NVFP4 Attention QAT Backward" page, Overview):
