@@ -31,9 +31,9 @@ SOURCES = ["sdpa_bwd_api.cu", "sdpa_bwd_main.cu", "sdpa_bwd_main_bias.cu", "sdpa
            "sdpa_bwd_aux.cu",
            "sdpa_bwd_dq.cu", "sdpa_bwd_noalloc.cu", "sdpa_fwd.cu", "sdpa_fwd_shared.cu", "sdpa_fwd_wide.cu",
            "sdpa_mask_plan.cu", "sdpa_rope.cu", "sdpa_kv_cache.cu", "sdpa_cache_api.cu",
-           "sdpa_cached_rows_16.cu", "sdpa_cached_rows_8.cu"]
+           "sdpa_cached_rows_16.cu", "sdpa_cached_rows_8.cu", "sdpa_cached_tiles_16.cu", "sdpa_cached_tiles_8.cu"]
 HEADERS = ["common.cuh", "gqa.cuh", "ptx.cuh", "tmap.h", "sdpa_bwd_main.cuh", "nvfp4.cuh", "bias.cuh", "sdpa_fwd.cuh", "score.cuh",
-           "rope.cuh", "rows.h", "cached.cuh", "sdpa_cached_rows.cuh"]
+           "rope.cuh", "rows.h", "cached.cuh", "sdpa_cached_rows.cuh", "sdpa_cached_tiles.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",

@@ -176,6 +176,18 @@ __device__ __forceinline__ int cached_page(const CachedParams& p, int b, int k) 
   return -1;
 }
 
+// Named barrier over nthreads threads that tells all of them whether `pred` holds for any.
+__device__ __forceinline__ bool named_bar_any(uint32_t id, uint32_t nthreads, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred pi, po;\n\tsetp.ne.u32 pi, %1, 0;\n\tbar.red.or.pred po, %2, %3, pi;\n\t"
+      "selp.u32 %0, 1, 0, po;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)pred), "r"(id), "r"(nthreads)
+      : "memory");
+  return r != 0;
+}
+
 // A sink joins the sum 2^lse2: returns log2 of the whole and the factor on O.
 __device__ __forceinline__ float cached_with_sink(const CachedParams& p, int head, float lse2, float& factor) {
   factor = 1.f;
@@ -195,6 +207,10 @@ cudaError_t launch_cached_rows_16(const CachedParams& p, int mt, cudaStream_t s)
 cudaError_t launch_cached_rows_8(const CachedParams& p, int mt, cudaStream_t s);
 cudaError_t cached_rows_16_setup();
 cudaError_t cached_rows_8_setup();
+cudaError_t launch_cached_tiles_16(const CachedParams& p, cudaStream_t s);
+cudaError_t launch_cached_tiles_8(const CachedParams& p, cudaStream_t s);
+cudaError_t cached_tiles_16_setup();
+cudaError_t cached_tiles_8_setup();
 cudaError_t launch_cached_merge(const CachedParams& p, cudaStream_t s);
 
 // Keys of a unit of the few-rows kernel: four warps of 16 keys, or of 32 in 8 bits.

@@ -183,7 +183,8 @@ int device_state(int dev, int** status_out, int* sms_out) {
           preprocess_kernel_setup() != cudaSuccess ||
           dq_kernel_setup() != cudaSuccess || fwd_kernel_setup() != cudaSuccess ||
           kv_cache_setup() != cudaSuccess || cached_rows_16_setup() != cudaSuccess ||
-          cached_rows_8_setup() != cudaSuccess)
+          cached_rows_8_setup() != cudaSuccess || cached_tiles_16_setup() != cudaSuccess ||
+          cached_tiles_8_setup() != cudaSuccess)
         return SDPA_ERR_CUDA;
     }
     g_device_checked[dev] = true;

@@ -81,13 +81,15 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 CachedPlan cached_plan(long long B, int H_q, int H_kv, int S_q, int D, bool f8, long long max_keys) {
   CachedPlan c{};
   const long long R = (long long)(H_q / H_kv) * S_q;
-  c.mt = R <= 16 ? 1 : 2;
-  c.tile_rows = 16 * c.mt;
-  c.tk = f8 ? CACHED_ROWS_TK_8 : CACHED_ROWS_TK_16;
+  c.mt = R <= 16 ? 1 : R <= 32 ? 2 : 0;  // 0: the many-rows kernel
+  c.tile_rows = c.mt ? 16 * c.mt : 128;
+  c.tk = c.mt == 0 || f8 ? 128 : 64;
+  static_assert(CACHED_ROWS_TK_16 == 64 && CACHED_ROWS_TK_8 == 128, "units");
   c.n_rt = (int)((R + c.tile_rows - 1) / c.tile_rows);
-  // Two CTAs an SM (their shared memory), fewer where there are not that many units.
-  const long long units = B * c.n_rt * H_kv * ((max_keys + c.tk - 1) / c.tk);
-  c.n_ctas = (int)(units < 2 * SHARE_SMS ? units : 2 * SHARE_SMS);
+  // As many CTAs as the device holds at once (by their shared memory), fewer where there are
+  // not that many units.
+  const long long units = B * c.n_rt * H_kv * ((max_keys + c.tk - 1) / c.tk), most = c.mt ? 2 * SHARE_SMS : SHARE_SMS;
+  c.n_ctas = (int)(units < most ? units : most);
   c.o_bytes = align256((size_t)c.n_ctas * 2 * c.tile_rows * D * sizeof(float));
   c.bytes = c.o_bytes + align256((size_t)c.n_ctas * 2 * c.tile_rows * sizeof(float));
   return c;
@@ -171,7 +173,8 @@ int sdpa_fwd_cached(int io_dtype, int cache_dtype, const void* q, const void* k_
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.o_bytes);
   nvtxRangePushA("sdpa_fwd_cached");
-  cudaError_t e = p.c.f8 ? launch_cached_rows_8(p, plan.mt, stream) : launch_cached_rows_16(p, plan.mt, stream);
+  cudaError_t e = plan.mt ? (p.c.f8 ? launch_cached_rows_8(p, plan.mt, stream) : launch_cached_rows_16(p, plan.mt, stream))
+                          : (p.c.f8 ? launch_cached_tiles_8(p, stream) : launch_cached_tiles_16(p, stream));
   if (e == cudaSuccess) e = launch_cached_merge(p, stream);
   nvtxRangePop();
   if (own) cudaFreeAsync(workspace, stream);
