@@ -16,8 +16,8 @@
 //     it by 2^8; one vote a piece asks for that.
 //   - 8 bits: codes become fp16 in registers (exact), the queries are fp16 times a power of two a row (exact
 //     down to 2^-29 of the row's largest), and P is fp16. A page's key scale joins the
-//     score's factor. Its value scale joins the weight's exponent, y = x + log2(vs), and O has a reference of
-//     its own for y: the largest weighted value is held to full precision however the scales differ.
+//     score's factor. Its value scale joins the weight's exponent, w = 2^(x + log2(vs) - reference), so that
+//     O = sum w * code / sum w / vs: the reference is the largest weighted value's, whatever the scales are.
 //     The contraction index is free to be permuted, so a thread's 16-byte piece of a key serves four steps,
 //     and byte pairs of V go through the 16-bit transposing load as they are.
 //   - P is fp16 or bf16 (the cache's type; rounded once, off by 2^-12 or 2^-9 of a weight); P in fp16 is
@@ -49,7 +49,7 @@ struct Layout {
   static constexpr int RING = NST * (STAGE + META);
   static constexpr int TR = 16 * MT;
   static constexpr int OROW = DP + 4;                   // floats of an O row in the exchange
-  static constexpr int XCH = WARPS * TR * (OROW + 3) * 4;
+  static constexpr int XCH = WARPS * TR * (OROW + 2) * 4;
   static constexpr int BYTES = WARPS * RING > XCH ? WARPS * RING : XCH;
   static_assert(NST >= 2 && (CT != E4M3 || TK == CACHED_ROWS_TK_8) && (CT == E4M3 || TK == CACHED_ROWS_TK_16), "");
 };
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams
 
     // Queries as A fragments, and the rows' state. Thread rows: 16 m + g and 16 m + g + 8.
     uint32_t qf[MT][KD][4];
-    float xmul[2 * MT], m[2 * MT], mv[CT == E4M3 ? 2 * MT : 1], l[2 * MT], slope2[MOD ? 2 * MT : 1];
+    float xmul[2 * MT], m[2 * MT], l[2 * MT], slope2[MOD ? 2 * MT : 1];
     CachedRow rows[2 * MT];
     int lo_max = 0, hi_min = INT_MAX;
 #pragma unroll
@@ -237,7 +237,6 @@ __global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams
         slope2[ri] = p.mods.slopes && in ? p.mods.slopes[w.kvh * p.G + r / p.Sq] * 1.4426950408889634f : 0.f;
       m[ri] = -INFINITY;
       l[ri] = 0.f;
-      if constexpr (CT == E4M3) mv[ri] = -INFINITY;
     }
     lo_max = __reduce_max_sync(0xffffffffu, lo_max);
     hi_min = __reduce_min_sync(0xffffffffu, hi_min);
@@ -301,12 +300,13 @@ __global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams
           }
         }
         // ---- scores in log2 units, masked
-        float lvs = 0.f, ks = 1.f;
+        float lvs = 0.f, ks = 1.f, inv_vs = 1.f;
         if constexpr (CT == E4M3) {
           float vs;
           asm volatile("ld.shared.b32 %0, [%1];" : "=f"(ks) : "r"(meta + u * 4) : "memory");
           asm volatile("ld.shared.b32 %0, [%1];" : "=f"(vs) : "r"(meta + 8 + u * 4) : "memory");
           lvs = __log2f(vs);
+          inv_vs = __fdividef(1.f, vs);
         }
         const int ka = k0 + 16 * u;
 #pragma unroll
@@ -355,8 +355,8 @@ __global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams
           const float(&a)[2][4] = sc[ri >> 1];
           const int e = 2 * (ri & 1);
           mx[ri] = fmaxf(fmaxf(a[0][e], a[0][e + 1]), fmaxf(a[1][e], a[1][e + 1]));
+          mx[ri] += lvs;
           raise |= mx[ri] > m[ri] + RAISE;
-          if constexpr (CT == E4M3) raise |= mx[ri] + lvs > mv[ri] + RAISE;
         }
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -365,16 +365,9 @@ __global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
             float fo = 1.f;
             if (x > m[ri] + RAISE) {
-              const float a = ex2_approx(m[ri] - x);  // 0 for the first key
-              l[ri] *= a;
+              fo = ex2_approx(m[ri] - x);  // 0 for the first key
+              l[ri] *= fo;
               m[ri] = x;
-              if constexpr (CT != E4M3) fo = a;
-            }
-            if constexpr (CT == E4M3) {
-              if (x + lvs > mv[ri] + RAISE) {
-                fo = ex2_approx(mv[ri] - (x + lvs));
-                mv[ri] = x + lvs;
-              }
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -387,16 +380,16 @@ __global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams
         uint32_t pf[MT][4];
 #pragma unroll
         for (int ri = 0; ri < 2 * MT; ++ri) {
-          const float neg = m[ri] == -INFINITY ? 0.f : (CT == E4M3 ? 0.f : BIAS) - m[ri];
-          const float neg_v = CT == E4M3 ? (mv[ri] == -INFINITY ? 0.f : BIAS + lvs - mv[ri]) : 0.f;
+          const float neg = m[ri] == -INFINITY ? 0.f : BIAS + lvs - m[ri];
+          float sum = 0.f;
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             const float x0 = sc[ri >> 1][n][2 * (ri & 1)], x1 = sc[ri >> 1][n][2 * (ri & 1) + 1];
             const float p0 = ex2_approx(x0 + neg), p1 = ex2_approx(x1 + neg);
-            l[ri] += p0 + p1;
-            if constexpr (CT == E4M3) pf[ri >> 1][(ri & 1) + 2 * n] = pack_f16x2(ex2_approx(x0 + neg_v), ex2_approx(x1 + neg_v));
-            else pf[ri >> 1][(ri & 1) + 2 * n] = pack_io2<PF>(p0, p1);
+            sum += p0 + p1;
+            pf[ri >> 1][(ri & 1) + 2 * n] = pack_io2<PF>(p0, p1);
           }
+          l[ri] = CT == E4M3 ? fmaf(sum, inv_vs, l[ri]) : l[ri] + sum;
         }
         // ---- O += P V
         if constexpr (CT == E4M3) {
@@ -435,9 +428,8 @@ __global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams
     copies_wait<0>();
     __syncthreads();
     float* const xo = reinterpret_cast<float*>(smem);  // [WARPS][TR][OROW]
-    float* const xm = xo + WARPS * L::TR * L::OROW;    // [WARPS][TR] m, then l, then mv
+    float* const xm = xo + WARPS * L::TR * L::OROW;    // [WARPS][TR] m, then l
     float* const xl = xm + WARPS * L::TR;
-    float* const xv = xl + WARPS * L::TR;
 #pragma unroll
     for (int ri = 0; ri < 2 * MT; ++ri) {
       float x = l[ri] + __shfl_xor_sync(0xffffffffu, l[ri], 1);
@@ -446,16 +438,14 @@ __global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams
         const int at = warp * L::TR + 16 * (ri >> 1) + g + 8 * (ri & 1);
         xm[at] = m[ri];
         xl[at] = x;
-        if constexpr (CT == E4M3) xv[at] = mv[ri];
       }
     }
     __syncthreads();
 #pragma unroll
     for (int ri = 0; ri < 2 * MT; ++ri) {
       const int row = 16 * (ri >> 1) + g + 8 * (ri & 1);
-      const float* const ref = CT == E4M3 ? xv : xm;
-      const float mine = ref[warp * L::TR + row];
-      const float M = fmaxf(fmaxf(ref[row], ref[L::TR + row]), fmaxf(ref[2 * L::TR + row], ref[3 * L::TR + row]));
+      const float mine = xm[warp * L::TR + row];
+      const float M = fmaxf(fmaxf(xm[row], xm[L::TR + row]), fmaxf(xm[2 * L::TR + row], xm[3 * L::TR + row]));
       const float f = mine == -INFINITY ? 0.f : ex2_approx(mine - M);
       float* const to = xo + (warp * L::TR + row) * L::OROW;
 #pragma unroll
@@ -474,12 +464,9 @@ __global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams
     const int live_rows = min(L::TR, p.R - r0), pieces = p.D / 8;
     for (int i = tid; i < live_rows * pieces; i += THREADS) {
       const int row = i / pieces, c = i % pieces;
-      float M = -INFINITY, Mv = -INFINITY, lt = 0.f;
+      float M = -INFINITY, lt = 0.f;
 #pragma unroll
-      for (int k = 0; k < WARPS; ++k) {
-        M = fmaxf(M, xm[k * L::TR + row]);
-        if constexpr (CT == E4M3) Mv = fmaxf(Mv, xv[k * L::TR + row]);
-      }
+      for (int k = 0; k < WARPS; ++k) M = fmaxf(M, xm[k * L::TR + row]);
 #pragma unroll
       for (int k = 0; k < WARPS; ++k) {
         const float mk = xm[k * L::TR + row];
@@ -496,8 +483,7 @@ __global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams
       }
       const bool none = M == -INFINITY;
       float f = none ? 0.f : 1.f / lt;
-      if constexpr (CT == E4M3) f = none ? 0.f : f * exp2f(Mv - M - BIAS);
-      const float lse2 = none ? -INFINITY : M - (CT == E4M3 ? 0.f : BIAS) + __log2f(lt);
+      const float lse2 = none ? -INFINITY : M - BIAS + __log2f(lt);
       const int r = r0 + row;
       if (w.slot >= 0) {
         const long long at = ((long long)blockIdx.x * 2 + w.slot) * L::TR + row;

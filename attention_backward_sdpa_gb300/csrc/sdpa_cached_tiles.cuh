@@ -7,11 +7,17 @@
 // sum and an O of their own (raised lazily, joined at the end).
 //
 // What differs is where the tiles come from. Four loader warps fill the stages: 16-byte asynchronous
-// copies (16-bit caches), or loads that become io values on the way (8 bits: codes are widened
-// and multiplied by their page's scale, exactly where that is a power of two). A thread keeps the next
-// tile's codes in registers while it widens this one's. They write the 128-byte swizzle that the
+// copies (16-bit caches), or loads whose codes become fp16 on the way (8 bits, exact; a thread keeps the next
+// tile's codes in registers while it widens this one's). They write the 128-byte swizzle that the
 // tensor core reads, take any page size, and fill rows that no query sees with zeros. (A bulk tensor
 // copy could bring 16-bit pages, but not widen codes, and a page of 16 rows is a copy of 2 KB.)
+//
+// 8 bits. All products are fp16. bf16 queries become fp16 times a power of two a row (exact down to 2^-29 of
+// the row's largest). Scales stay out of the tiles: a page's key scale is in its scores' factor, and its
+// value scale in the weight's exponent, w = 2^(x + log2(vs) - reference), so that
+//   O = sum w * code / sum w / vs:
+// the reference is the largest weighted value's, whatever the scales are. (bf16 tiles with the scales multiplied
+// in took five instructions a pair of codes where fp16 takes one.)
 //
 // Warps: 0-7 softmax, 8-11 loaders, 12 issues S = Q K^T and owns the tensor memory, 13 issues
 // O += P V. Registers (launched with 128 a thread): 184 for softmax, 104 loaders, 40 issuers:
@@ -46,15 +52,16 @@ struct Layout {
   static constexpr int BLK = 128 * 128;  // 64 columns of 128 rows
   static constexpr int TILE = BM * DP * 2;
   static constexpr int STAGE = 2 * TILE;
-  static constexpr int REST = NUM_BARS * 8 + 2 * 256 * 4 + 512 + 64;
+  static constexpr int REST = NUM_BARS * 8 + 2 * 256 * 4 + 544 + 3 * 128 + 16;
   static constexpr int NS_FIT = (232448 - TILE - REST) / STAGE;
   static constexpr int NS = NS_FIT > 4 ? 4 : NS_FIT;
   static constexpr int OFF_KV = TILE;
   static constexpr int OFF_BAR = OFF_KV + NS * STAGE;
   static constexpr int OFF_XCH = OFF_BAR + NUM_BARS * 8;
-  static constexpr int OFF_META = OFF_XCH + 2 * 256 * 4;  // page[2][8], scales[2][16], bad[4]
-  static constexpr int OFF_MISC = OFF_META + 512;
-  static constexpr int BYTES_RAW = OFF_MISC + 64;
+  static constexpr int OFF_META = OFF_XCH + 2 * 256 * 4;  // TileMeta
+  static constexpr int OFF_QEXP = OFF_META + 544;         // [3][128] exponents of the rows' factors, by portion
+  static constexpr int OFF_MISC = OFF_QEXP + 3 * 128;
+  static constexpr int BYTES_RAW = OFF_MISC + 16;
   static constexpr int BYTES = BYTES_RAW > 120 * 1024 ? BYTES_RAW : 120 * 1024;  // one CTA an SM
   static constexpr uint32_t COL_O = 128 * NSLOT;
   static_assert(NS >= 2 && BYTES <= 232448, "shared memory budget");
@@ -71,69 +78,26 @@ template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 __device__ __forceinline__ void codes_f16(uint32_t four, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
       "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(four));
 }
 
-// How a page's codes become io values: `fast`, one multiplication by `c` (a pair) after the bits
-// of a code have been put where an io value has them; else through fp32.
-struct Widen {
-  bool fast;
-  uint32_t c;
-  float scale;
+// What the loaders tell of a tile, by groups of 16 keys.
+struct TileMeta {
+  long long off[2][8];              // by parity of the tile: byte offset of the group's first row, -1: none is read
+  int full[2];                      // every row of the tile is
+  int bad[4];                       // by stage: groups without a page
+  float ks[4][8], lvs[4][8], inv[4][8];  // by stage, 8 bits: key scale, log2 and inverse of the value scale
 };
-template <bool F16>
-__device__ __forceinline__ Widen widen_by(float scale) {
-  Widen w;
-  const uint32_t u = __float_as_uint(scale), e = u >> 23;
-  const bool two = (u & 0x7FFFFFu) == 0;
-  w.scale = scale;
-  if constexpr (F16) {  // e4m3 -> fp16 is exact; the scale as an fp16 number
-    w.fast = two && e >= 127 - 14 && e <= 127 + 15;
-    w.c = ((e - 127 + 15) << 10) * 0x10001u;
-  } else {
-    // A code's exponent and fraction bits as those of a bf16 number stand for 2^-120 of its
-    // value (bias 127 against 7), the smallest ones included.
-    w.fast = two && e >= 27 && e <= 127 + 7;
-    w.c = ((e + 120) << 7) * 0x10001u;
-  }
-  return w;
-}
-// Four codes as two io pairs.
-template <bool F16>
-__device__ __forceinline__ void widen4(uint32_t four, const Widen& w, uint32_t& lo, uint32_t& hi) {
-  if (w.fast) {
-    if constexpr (F16) {
-      codes_f16(four, lo, hi);
-      lo = mul_f16x2(lo, w.c);
-      hi = mul_f16x2(hi, w.c);
-    } else {
-      const uint32_t a = __byte_perm(four, 0u, 0x1404), b = __byte_perm(four, 0u, 0x3424);  // codes in the upper bytes
-      lo = mul_bf16x2((a & 0x80008000u) | ((a >> 4) & 0x07F007F0u), w.c);
-      hi = mul_bf16x2((b & 0x80008000u) | ((b >> 4) & 0x07F007F0u), w.c);
-    }
-  } else {
-    codes_f16(four, lo, hi);
-    lo = pack_io2<F16>(io_lo<true>(lo) * w.scale, io_hi<true>(lo) * w.scale);
-    hi = pack_io2<F16>(io_lo<true>(hi) * w.scale, io_hi<true>(hi) * w.scale);
-  }
-}
+static_assert(sizeof(TileMeta) <= 544, "");
 
 template <int DP, bool F8, bool F16, bool MOD>
 __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedParams p) {
   using L = Layout<DP>;
   constexpr int NS = L::NS;
+  constexpr bool PF = F8 || F16;          // the products are fp16
+  constexpr float BIAS = F8 ? 6.f : 0.f;  // weights times 2^6: what fp16's smallest step loses is below 2^-30 of the largest
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if ((smem_u32(smem) & 1023u) != 0) {
@@ -141,9 +105,8 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
     return;
   }
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-  int* meta_page = reinterpret_cast<int*>(smem + L::OFF_META);        // [2][8]
-  float* meta_scale = reinterpret_cast<float*>(smem + L::OFF_META + 64);  // [2][16]
-  int* meta_bad = reinterpret_cast<int*>(smem + L::OFF_META + 192);   // [4] by stage: groups of 16 keys without a page
+  TileMeta& meta = *reinterpret_cast<TileMeta*>(smem + L::OFF_META);
+  int8_t* const q_exp = reinterpret_cast<int8_t*>(smem + L::OFF_QEXP);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   // (its shared memory: the place that the halves exchange their sums in later)
@@ -179,8 +142,8 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
     regs_decrease<REGS_CTRL>();
     if (warp < 14) {
       // ------------------------------------------------------------ MMA issuers
-      constexpr uint32_t ID_S = idesc_io(BM, BK, false, false, F16);
-      constexpr uint32_t ID_O = idesc_io(BM, DP, false, true, F16);
+      constexpr uint32_t ID_S = idesc_io(BM, BK, false, false, PF);
+      constexpr uint32_t ID_O = idesc_io(BM, DP, false, true, PF);
       constexpr uint64_t T_KMAJ = sdesc_sw128_template(16, 1024);
       constexpr uint64_t T_MN_V = sdesc_sw128_template(L::BLK, 1024);
       int g = 0, np = 0;
@@ -245,96 +208,133 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
     CachedPortion w;
     while (ok && walk.next(p, w)) {
       const CachedBounds& s = w.s;
-      // Q, in a copy group of its own.
       // (A wait that gives up leaves the portion going, so that all loaders meet at their barriers; they
       // end together after it.)
       if (np > 0) ok = mbar_wait(&bars[BAR_QEMPTY], (np - 1) & 1, abort_flag, WAIT_LIMIT_NS);
       {
-        constexpr int CQ = DP / 8, SQ = 128 / CQ;
+        constexpr int CQ = DP / 8, SQ = 128 / CQ;  // a row's pieces on CQ neighbouring lanes
         const int cq = lid % CQ;
         const uint16_t* const q = static_cast<const uint16_t*>(p.q) + ((long long)w.b * p.c.Hkv + w.kvh) * p.R * p.D + cq * 8;
-        if (cq * 8 < p.D) {
 #pragma unroll 4
-          for (int i = 0; i < CQ; ++i) {
-            const int row = lid / CQ + i * SQ, r = w.rt * BM + row;
-            copy16(smem_u32(smem) + tile_at(row, cq), q + (long long)min(r, p.R - 1) * p.D, r < p.R);
+        for (int i = 0; i < CQ; ++i) {
+          const int row = lid / CQ + i * SQ, r = w.rt * BM + row;
+          if constexpr (!F8 || F16) {  // in a copy group of its own
+            if (cq * 8 < p.D) copy16(smem_u32(smem) + tile_at(row, cq), q + (long long)min(r, p.R - 1) * p.D, r < p.R);
+          } else {
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (cq * 8 < p.D && r < p.R) v = __ldg(reinterpret_cast<const uint4*>(q + (long long)r * p.D));
+            uint32_t x[4] = {v.x, v.y, v.z, v.w};
+            float amax = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) amax = fmaxf(amax, fmaxf(fabsf(io_lo<false>(x[k])), fabsf(io_hi<false>(x[k]))));
+#pragma unroll
+            for (int k = 1; k < CQ; k <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, k));
+            // 2^e brings the row's largest into [2^14, 2^15).
+            const int e = amax > 0.f ? min(max(14 - ((int)(__float_as_uint(amax) >> 23) - 127), -113), 126) : 0;
+            const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = pack_f16x2(io_lo<false>(x[k]) * up, io_hi<false>(x[k]) * up);
+            *reinterpret_cast<uint4*>(smem + tile_at(row, cq)) = make_uint4(x[0], x[1], x[2], x[3]);
+            if (cq == 0) q_exp[(np % 3) * 128 + row] = (int8_t)-e;
           }
         }
         copies_commit();
       }
-      // Threads 0-7 look up the pages of a tile's eight groups of 16 keys two tiles ahead, and their
-      // scales one tile ahead.
+      // Threads 0-7 look up the pages of a tile's eight groups of 16 keys two tiles ahead, and in 8 bits
+      // their scales one tile ahead. Pages: -1 there is none, -2 no row sees the group.
       auto page_for = [&](int j) -> int {
-        if (lid >= 8 || j >= w.j1) return -1;
+        if (lid >= 8 || j >= w.j1) return -2;
         const int a = cached_tile(s, j) * BK + 16 * lid;
         return a < s.k_hi && (a + 15 >= s.k_lo || a < p.first_keys) ? cached_page(p, w.b, a) : -2;
       };
-      auto scale_for = [&](int page, const float* scales) -> float {
-        return F8 && lid < 8 && page >= 0 ? scales[(long long)page * p.c.Hkv + w.kvh] : 1.f;
+      float ks = 1.f, vs = 1.f;
+      auto scales_for = [&](int page) {
+        ks = vs = 1.f;
+        if (F8 && lid < 8 && page >= 0) {
+          ks = p.c.ks[(long long)page * p.c.Hkv + w.kvh];
+          vs = p.c.vs[(long long)page * p.c.Hkv + w.kvh];
+        }
+      };
+      // Where tile j's groups are, for its loads (parity x): warp 8.
+      auto tell_places = [&](int x, int j, int page) {
+        if (warp != 8) return;
+        const int k0 = cached_tile(s, j) * BK, a = k0 + 16 * (lid & 7);
+        if (lid < 8)
+          meta.off[x][lid] = page < 0 ? -1 : ((((long long)page * p.c.Hkv + w.kvh) << p.c.page_shift) + (a & (p.c.page - 1))) * p.D * ESZ;
+        const bool all = __all_sync(0xffu | 0xffffff00u, lid >= 8 || page >= 0);
+        if (lid == 0) meta.full[x] = all && k0 + BK <= s.k_hi && (k0 >= s.k_lo || k0 + BK <= p.first_keys);
+      };
+      // What the others need of the tile in stage st.
+      auto tell_stage = [&](int st, int page) {
+        if (warp != 8) return;
+        const uint32_t bad = __ballot_sync(0xffffffffu, page == -1);
+        if (lid == 0) meta.bad[st] = (int)bad;
+        if (F8 && lid < 8) {
+          meta.ks[st][lid] = ks;
+          meta.lvs[st][lid] = __log2f(vs);
+          meta.inv[st][lid] = 1.f / vs;
+        }
       };
       int page0 = page_for(w.j0), page1 = page_for(w.j0 + 1);
-      float ks = scale_for(page0, p.c.ks), vs = scale_for(page0, p.c.vs);
-      auto row_from = [&](const int* pages, int j, int i, long long& off) -> bool {
-        // row rl + STEP i of tile j: element offset of its piece, and whether some query sees it
-        const int row = rl + STEP * i, key = cached_tile(s, j) * BK + row, page = pages[row >> 4];
-        const bool take = in && page >= 0 && key < s.k_hi && (key >= s.k_lo || key < p.first_keys);
-        off = take ? ((((long long)page * p.c.Hkv + w.kvh) << p.c.page_shift) + (key & (p.c.page - 1))) * p.D * ESZ + c * 16 : 0;
-        return take;
-      };
-      const char* const kc = static_cast<const char*>(p.c.k);
-      const char* const vc = static_cast<const char*>(p.c.v);
-      auto bad_groups = [&](int page) -> uint32_t {  // (lanes 0-7 of warp 8)
-        return __ballot_sync(0xffffffffu, lid < 8 && page == -1);
+      const char* const kc = static_cast<const char*>(p.c.k) + (long long)(rl & 15) * p.D * ESZ + c * 16;
+      const char* const vc = static_cast<const char*>(p.c.v) + (long long)(rl & 15) * p.D * ESZ + c * 16;
+      // Row rl + STEP i of a tile: its group, and its byte offset past the group's row rl & 15.
+      auto group_of = [&](int i) { return (rl + STEP * i) >> 4; };
+      const int step_bytes = STEP < 16 ? STEP * p.D * ESZ : 0;
+      auto extra = [&](int i) { return STEP < 16 ? (i & (16 / (STEP < 16 ? STEP : 16) - 1)) * step_bytes : 0; };
+      auto seen = [&](int k0, int i) {
+        const int key = k0 + rl + STEP * i;
+        return key < s.k_hi && (key >= s.k_lo || key < p.first_keys);
       };
       if constexpr (F8) {
+        static_assert(STEP >= 16, "a pass's rows lie in the same place of their groups");
         uint4 kr[N], vr[N];
-        // Pages of the first tile, then its codes.
-        if (lid < 8) meta_page[lid] = page0;
-        uint32_t bad = warp == 8 ? bad_groups(page0) : 0u;
+        auto load = [&](int x, int k0, int i, bool full, uint4& kv, const char* base) {
+          const long long off = meta.off[x][group_of(i)];
+          kv = make_uint4(0u, 0u, 0u, 0u);
+          if (in && (full || (off >= 0 && seen(k0, i)))) kv = __ldg(reinterpret_cast<const uint4*>(base + off));
+        };
+        scales_for(page0);
+        tell_places(0, w.j0, page0);
         named_bar_sync(2, 128);
+        {
+          const int k0 = cached_tile(s, w.j0) * BK;
+          const bool full = meta.full[0] != 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          long long off;
-          const bool take = row_from(meta_page, w.j0, i, off);
-          kr[i] = take ? __ldg(reinterpret_cast<const uint4*>(kc + off)) : make_uint4(0u, 0u, 0u, 0u);
-          vr[i] = take ? __ldg(reinterpret_cast<const uint4*>(vc + off)) : make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < N; ++i) {
+            load(0, k0, i, full, kr[i], kc);
+            load(0, k0, i, full, vr[i], vc);
+          }
         }
         for (int j = w.j0; j < w.j1; ++j, ++g) {
-          const int x = (j - w.j0) & 1, st = g % NS;
-          // The scales of this tile, and the pages of the next one.
-          if (lid < 8) {
-            meta_scale[16 * x + lid] = ks;
-            meta_scale[16 * x + 8 + lid] = vs;
-            meta_page[8 * (x ^ 1) + lid] = page1;
-          }
-          const uint32_t bad_next = warp == 8 ? bad_groups(page1) : 0u;
-          named_bar_sync(2, 128);
-          ks = scale_for(page1, p.c.ks);
-          vs = scale_for(page1, p.c.vs);
-          page1 = page_for(j + 2);
+          const int x1 = (j - w.j0 + 1) & 1, st = g % NS;
+          const bool more = j + 1 < w.j1;
+          if (more) tell_places(x1, j + 1, page1);
           if (g >= NS && ok) ok = mbar_wait(&bars[BAR_KVEMPTY + st], ((g / NS) - 1) & 1, abort_flag, WAIT_LIMIT_NS);
+          __syncwarp();
+          tell_stage(st, page0);
+          named_bar_sync(2, 128);
+          scales_for(page1);
+          page0 = page1;
+          page1 = page_for(j + 2);
+          const int k1 = more ? cached_tile(s, j + 1) * BK : 0;
+          const bool full = more && meta.full[x1] != 0;
           uint8_t* const tile = smem + L::OFF_KV + st * L::STAGE;
-          if (lid == 0) meta_bad[st] = (int)bad;
-          bad = bad_next;
 #pragma unroll
           for (int side = 0; side < 2; ++side) {
             uint8_t* const to = tile + side * L::TILE;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
               const int row = rl + STEP * i;
-              const uint4 v = side ? vr[i] : kr[i];
-              long long off;
-              const bool take = j + 1 < w.j1 && row_from(meta_page + 8 * (x ^ 1), j + 1, i, off);
-              uint4& next = side ? vr[i] : kr[i];
-              next = make_uint4(0u, 0u, 0u, 0u);
-              if (take) next = __ldg(reinterpret_cast<const uint4*>((side ? vc : kc) + off));
+              uint4& reg = side ? vr[i] : kr[i];
+              const uint4 v = reg;
+              if (more) load(x1, k1, i, full, reg, side ? vc : kc);
               if (in) {
-                const Widen wd = widen_by<F16>(meta_scale[16 * x + 8 * side + (row >> 4)]);
                 uint4 a, b;
-                widen4<F16>(v.x, wd, a.x, a.y);
-                widen4<F16>(v.y, wd, a.z, a.w);
-                widen4<F16>(v.z, wd, b.x, b.y);
-                widen4<F16>(v.w, wd, b.z, b.w);
+                codes_f16(v.x, a.x, a.y);
+                codes_f16(v.y, a.z, a.w);
+                codes_f16(v.z, b.x, b.y);
+                codes_f16(v.w, b.z, b.w);
                 // (Threads of the second block store their pieces in the other order: no bank twice.)
                 const bool swap = c >= 4;
                 *reinterpret_cast<uint4*>(to + tile_at(row, 2 * c + (swap ? 1 : 0))) = swap ? b : a;
@@ -349,18 +349,15 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
         }
       } else {
         int signalled = 0;  // tiles of this portion (and Q, before the first) that the others know of
+        const int g0 = g;
         auto signal = [&](int upto) {
           fence_proxy_async_smem();
           if (signalled == 0 && upto > 0) mbar_arrive(&bars[BAR_QFULL]);
-          for (; signalled < upto; ++signalled) mbar_arrive(&bars[BAR_KVFULL + (g - (upto - signalled)) % NS]);
+          for (; signalled < upto; ++signalled) mbar_arrive(&bars[BAR_KVFULL + (g0 + signalled) % NS]);
         };
-        for (int j = w.j0; j < w.j1; ++j) {
-          const int x = (j - w.j0) & 1, st = g % NS;
-          if (lid < 8) meta_page[8 * x + lid] = page0;
-          const uint32_t bad = warp == 8 ? bad_groups(page0) : 0u;
-          page0 = page1;
-          page1 = page_for(j + 2);
-          named_bar_sync(2, 128);
+        for (int j = w.j0; j < w.j1; ++j, ++g) {
+          const int x = (j - w.j0) & 1, st = g % NS, k0 = cached_tile(s, j) * BK;
+          tell_places(x, j, page0);
           if (g >= NS && ok) {
             if (!mbar_try_wait(&bars[BAR_KVEMPTY + st], ((g / NS) - 1) & 1)) {
               copies_wait<0>();  // nothing to fill yet: what has been filled is handed over
@@ -368,27 +365,27 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
               ok = mbar_wait(&bars[BAR_KVEMPTY + st], ((g / NS) - 1) & 1, abort_flag, WAIT_LIMIT_NS);
             }
           }
+          __syncwarp();
+          tell_stage(st, page0);
+          named_bar_sync(2, 128);
+          page0 = page1;
+          page1 = page_for(j + 2);
           const uint32_t tile = smem_u32(smem + L::OFF_KV + st * L::STAGE);
-          if (lid == 0) meta_bad[st] = (int)bad;
+          const bool full = meta.full[x] != 0;
           if (in) {
-#pragma unroll 4
+#pragma unroll
             for (int i = 0; i < N; ++i) {
-              long long off;
-              const bool take = row_from(meta_page + 8 * x, j, i, off);
+              const long long off = meta.off[x][group_of(i)];
+              const bool take = full || (off >= 0 && seen(k0, i));
+              const long long from = take ? off + extra(i) : 0;
               const int at = tile_at(rl + STEP * i, c);
-              copy16(tile + at, kc + off, take);
-              copy16(tile + L::TILE + at, vc + off, take);
+              copy16(tile + at, kc + from, take);
+              copy16(tile + L::TILE + at, vc + from, take);
             }
           }
           copies_commit();
-          ++g;
           copies_wait<1>();
-          if (j > w.j0) {
-            // (tile j - 1 and Q have landed; g counts tile j too)
-            --g;
-            signal(j - w.j0);
-            ++g;
-          }
+          if (j > w.j0) signal(j - w.j0);  // the tile before, and Q
         }
         copies_wait<0>();
         signal(w.j1 - w.j0);
@@ -404,8 +401,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
     float* const xch = reinterpret_cast<float*>(smem + L::OFF_XCH);
     const uint32_t col_o = L::COL_O + 128u * half;
-    const float cs = MOD ? 1.f : p.scale_log2;  // log2 units of a score as it is below
-    int g = 0;
+    int g = 0, np = 0;
     bool ok = true;
     CachedPortion w;
     while (ok && walk.next(p, w)) {
@@ -414,7 +410,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
       if (r >= p.R) rw.lo = 0, rw.hi = w.s.L - 1;  // (not written; never the reason for a mask)
       const int head = w.kvh * p.G + min(r, p.R - 1) / p.Sq;
       const float slope2 = MOD && p.mods.slopes ? p.mods.slopes[head] * 1.4426950408889634f : 0.f;
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f, unit = 1.f;  // unit: 8 bits, q . k of a product as it is
       for (int j = 0; j < n; ++j, ++g) {
         const int s = g % NSLOT, st = g % NS;
         const int kb = cached_tile(w.s, w.j0 + j) * BK + i0;
@@ -422,7 +418,22 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
         ok = __all_sync(0xffffffffu, mbar_wait(&bars[BAR_KVFULL + st], (g / NS) & 1, abort_flag, WAIT_LIMIT_NS) &&
                                          mbar_wait(&bars[BAR_SFULL + s], (g / NSLOT) & 1, abort_flag, WAIT_LIMIT_NS));
         if (!ok) break;
-        const uint32_t bad = ((uint32_t)meta_bad[st] >> (4 * half)) & 15u;
+        const uint32_t bad = ((uint32_t)meta.bad[st] >> (4 * half)) & 15u;
+        // Factors of the four groups' scores (log2 units of a score as it is below), and what their weights'
+        // exponents get and their sums are multiplied by.
+        float cg[4], add[4], inv[4];
+        if constexpr (F8) {
+          if (!F16 && j == 0) unit = __uint_as_float((uint32_t)(127 + q_exp[(np % 3) * 128 + row]) << 23);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            cg[k] = meta.ks[st][4 * half + k] * unit * (MOD ? 1.f : p.scale_log2);
+            add[k] = meta.lvs[st][4 * half + k];
+            inv[k] = meta.inv[st][4 * half + k];
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) cg[k] = MOD ? 1.f : p.scale_log2, add[k] = 0.f, inv[k] = 1.f;
+        }
         tc_fence_after();
         uint32_t sr[2][32];
         tmem_ld32(t_lane + 128u * s + i0, sr[0]);
@@ -436,7 +447,10 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
           for (int b8 = 0; b8 < 8; ++b8) {
             uint64_t x[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = f2_pack(sr[b8 >> 2][(b8 & 3) * 8 + 2 * i], sr[b8 >> 2][(b8 & 3) * 8 + 2 * i + 1]);
+            for (int i = 0; i < 4; ++i) {
+              x[i] = f2_pack(sr[b8 >> 2][(b8 & 3) * 8 + 2 * i], sr[b8 >> 2][(b8 & 3) * 8 + 2 * i + 1]);
+              if constexpr (F8) x[i] = f2_mul(x[i], f2_pack(cg[b8 >> 1], cg[b8 >> 1]));
+            }
             if (cap) tanh2_any(x, p.mods.cap_in);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -447,6 +461,10 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
               sr[b8 >> 2][(b8 & 3) * 8 + 2 * i + 1] = __float_as_uint(fmaf(-slope2, fabsf((float)(rw.place - key - 1)), x1 * c));
             }
           }
+        }
+        if constexpr (MOD) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) cg[k] = 1.f;
         }
         const bool mine = kb + 63 <= rw.hi && (kb >= rw.lo || kb + 63 < p.first_keys);
         if (!__all_sync(0xffffffffu, mine) || bad != 0u) {
@@ -461,9 +479,17 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
 #pragma unroll
         for (int a = 0; a < 8; ++a) mp[a] = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 64; i += 2)
-          mp[(i >> 1) & 7] = max3(mp[(i >> 1) & 7], __uint_as_float(sr[i >> 5][i & 31]), __uint_as_float(sr[i >> 5][(i & 31) + 1]));
-        const float mt = max3(max3(mp[0], mp[1], mp[2]), max3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7])) * cs;
+        for (int i = 0; i < 64; i += 2)  // two partial maxima a group
+          mp[2 * (i >> 4) + ((i >> 1) & 1)] = max3(mp[2 * (i >> 4) + ((i >> 1) & 1)], __uint_as_float(sr[i >> 5][i & 31]),
+                                                   __uint_as_float(sr[i >> 5][(i & 31) + 1]));
+        float mt;
+        if constexpr (F8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mp[k] = fmaf(fmaxf(mp[2 * k], mp[2 * k + 1]), cg[k], add[k]);
+          mt = fmaxf(max3(mp[0], mp[1], mp[2]), mp[3]);
+        } else {
+          mt = max3(max3(mp[0], mp[1], mp[2]), max3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7])) * cg[0];
+        }
         const bool raise = mt > m + RAISE || (m == -INFINITY && mt > -INFINITY);
         const float m_new = raise ? mt : m, alpha = raise ? ex2_approx(m - m_new) : 1.f;
         const bool rescale = raise && j > 0 && m > -INFINITY;
@@ -494,22 +520,29 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
         float rs[8];
 #pragma unroll
         for (int a = 0; a < 8; ++a) rs[a] = 0.f;
-        const float neg_m = m == -INFINITY ? 0.f : -m;
+        const float neg_m = m == -INFINITY ? 0.f : BIAS - m;
 #pragma unroll
         for (int c16 = 0; c16 < 2; ++c16) {
           uint32_t wv[16];
 #pragma unroll
           for (int i2 = 0; i2 < 16; ++i2) {
-            const float p0 = ex2_approx(fmaf(__uint_as_float(sr[c16][2 * i2]), cs, neg_m));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(sr[c16][2 * i2 + 1]), cs, neg_m));
-            rs[(2 * i2) & 7] += p0;
-            rs[(2 * i2 + 1) & 7] += p1;
-            wv[i2] = pack_io2<F16>(p0, p1);
+            const int k = 2 * c16 + (i2 >> 3);
+            const float f = F8 ? cg[k] : cg[0], a = F8 ? add[k] + neg_m : neg_m;
+            const float p0 = ex2_approx(fmaf(__uint_as_float(sr[c16][2 * i2]), f, a));
+            const float p1 = ex2_approx(fmaf(__uint_as_float(sr[c16][2 * i2 + 1]), f, a));
+            rs[2 * k] += p0;
+            rs[2 * k + 1] += p1;
+            wv[i2] = pack_io2<PF>(p0, p1);
           }
           __syncwarp();
           tmem_st16(t_lane + 128u * s + half * 64 + c16 * 16, wv);
         }
-        l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+        if constexpr (F8) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) l = fmaf(rs[2 * k] + rs[2 * k + 1], inv[k], l);
+        } else {
+          l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+        }
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&bars[BAR_PREADY + s]);
@@ -528,7 +561,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
       const float a0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - M), a1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - M);
       const float lt = l0 * a0 + l1 * a1;
       const float inv = M == -INFINITY ? 0.f : 1.f / lt;
-      const float lse2 = M == -INFINITY ? -INFINITY : M + __log2f(lt);
+      const float lse2 = M == -INFINITY ? -INFINITY : M - BIAS + __log2f(lt);
       float f0 = a0 * inv, f1 = a1 * inv, all = lse2;
       const long long at = ((long long)blockIdx.x * 2 + max(w.slot, 0)) * BM + row;
       if (w.slot < 0) {
@@ -577,6 +610,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
         if (w.slot >= 0) p.part_lse[at] = lse2;
         else p.lse[orow] = all * 0.6931471805599453f;
       }
+      ++np;
     }
   }
 
