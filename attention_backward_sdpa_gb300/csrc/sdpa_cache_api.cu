@@ -31,8 +31,8 @@ int fill_cache(const CacheArgs& a, int io_dtype, int B, KvCacheRef& c) {
   if (B <= 0 || a.H_kv <= 0 || a.D <= 0 || a.n_pages <= 0 || a.max_pages <= 0) return SDPA_ERR_INVALID;
   if (a.D % 16 != 0 || a.D > 128) return SDPA_ERR_UNSUPPORTED;
   if (a.page < 16 || a.page > 256 || (a.page & (a.page - 1)) != 0) return SDPA_ERR_UNSUPPORTED;
-  // Positions, page rows and table entries are 32-bit; element offsets 64-bit.
-  if ((long long)a.max_pages * a.page >= 1ll << 31 || (long long)a.n_pages * a.H_kv >= 1ll << 31 ||
+  // Positions, table entries and groups of 16 rows are 32-bit; element offsets 64-bit.
+  if ((long long)a.max_pages * a.page >= 1ll << 31 || (long long)a.n_pages * a.H_kv * (a.page / 16) >= 1ll << 31 ||
       (long long)B * a.max_pages >= 1ll << 31)
     return SDPA_ERR_INVALID;
   if (!a.k || !a.v || !a.table || !a.lens) return SDPA_ERR_INVALID;

@@ -20,9 +20,11 @@
 // in took five instructions a pair of codes where fp16 takes one.)
 //
 // Warps: 0-7 softmax, 8-11 loaders, 12 issues S = Q K^T and owns the tensor memory, 13 issues
-// O += P V. Registers (launched with 128 a thread): 184 for softmax, 104 loaders, 40 issuers:
-// 256 x 184 + 128 x 104 + 128 x 40 = 512 x 128.
+// O += P V. Registers (launched with 128 a thread): 168 for softmax, 120 loaders, 56 issuers:
+// 256 x 168 + 128 x 120 + 128 x 56 = 512 x 128.
 #pragma once
+
+#include <type_traits>
 
 #include "cached.cuh"
 
@@ -31,7 +33,7 @@ namespace sdpa {
 namespace cached_tiles {
 
 constexpr int THREADS = 512, BM = 128, BK = 128, NSLOT = 2;
-constexpr uint32_t REGS_SOFTMAX = 184, REGS_LOAD = 104, REGS_CTRL = 40;
+constexpr uint32_t REGS_SOFTMAX = 168, REGS_LOAD = 120, REGS_CTRL = 56;
 static_assert(256 * REGS_SOFTMAX + 128 * REGS_LOAD + 128 * REGS_CTRL <= THREADS * 128, "register split");
 constexpr uint64_t WAIT_LIMIT_NS = 4000000000ull;
 constexpr float RAISE = 8.f;  // P stays below 2^8 until its reference is raised
@@ -52,19 +54,18 @@ struct Layout {
   static constexpr int BLK = 128 * 128;  // 64 columns of 128 rows
   static constexpr int TILE = BM * DP * 2;
   static constexpr int STAGE = 2 * TILE;
-  static constexpr int REST = NUM_BARS * 8 + 2 * 256 * 4 + 544 + 3 * 128 + 16;
-  static constexpr int NS_FIT = (232448 - TILE - REST) / STAGE;
-  static constexpr int NS = NS_FIT > 4 ? 4 : NS_FIT;
+  static constexpr int NS = DP == 128 ? 3 : 4;
+  static constexpr int META = 112 + NS * 96;  // TileMeta
   static constexpr int OFF_KV = TILE;
   static constexpr int OFF_BAR = OFF_KV + NS * STAGE;
   static constexpr int OFF_XCH = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_META = OFF_XCH + 2 * 256 * 4;  // TileMeta
-  static constexpr int OFF_QEXP = OFF_META + 544;         // [3][128] exponents of the rows' factors, by portion
+  static constexpr int OFF_QEXP = OFF_META + META;        // [3][128] exponents of the rows' factors, by portion
   static constexpr int OFF_MISC = OFF_QEXP + 3 * 128;
   static constexpr int BYTES_RAW = OFF_MISC + 16;
   static constexpr int BYTES = BYTES_RAW > 120 * 1024 ? BYTES_RAW : 120 * 1024;  // one CTA an SM
   static constexpr uint32_t COL_O = 128 * NSLOT;
-  static_assert(NS >= 2 && BYTES <= 232448, "shared memory budget");
+  static_assert(BYTES <= 232448 && OFF_META % 16 == 0, "shared memory budget");
 };
 
 // Byte of 16-byte piece c (8 columns) of row r in a tile: blocks of 64 columns, 128-byte swizzle.
@@ -84,13 +85,15 @@ __device__ __forceinline__ void codes_f16(uint32_t four, uint32_t& lo, uint32_t&
 }
 
 // What the loaders tell of a tile, by groups of 16 keys.
+template <int NS>
 struct TileMeta {
-  long long off[2][8];              // by parity of the tile: byte offset of the group's first row, -1: none is read
-  int full[2];                      // every row of the tile is
-  int bad[4];                       // by stage: groups without a page
-  float ks[4][8], lvs[4][8], inv[4][8];  // by stage, 8 bits: key scale, log2 and inverse of the value scale
+  int at[2][8];   // by parity of the tile: the group's rows are 16 at of the cache, -1: none is read
+  int full[2];    // every row of the tile is read
+  int bad[4];     // by stage: groups without a page
+  int unused[6];
+  float ks[NS][8], lvs[NS][8], inv[NS][8];  // by stage, 8 bits: key scale, log2 and inverse of the value scale
 };
-static_assert(sizeof(TileMeta) <= 544, "");
+static_assert(sizeof(TileMeta<3>) == Layout<128>::META && sizeof(TileMeta<4>) == Layout<64>::META, "");
 
 template <int DP, bool F8, bool F16, bool MOD>
 __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedParams p) {
@@ -105,7 +108,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
     return;
   }
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
-  TileMeta& meta = *reinterpret_cast<TileMeta*>(smem + L::OFF_META);
+  TileMeta<NS>& meta = *reinterpret_cast<TileMeta<NS>*>(smem + L::OFF_META);
   int8_t* const q_exp = reinterpret_cast<int8_t*>(smem + L::OFF_QEXP);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
         if (warp != 8) return;
         const int k0 = cached_tile(s, j) * BK, a = k0 + 16 * (lid & 7);
         if (lid < 8)
-          meta.off[x][lid] = page < 0 ? -1 : ((((long long)page * p.c.Hkv + w.kvh) << p.c.page_shift) + (a & (p.c.page - 1))) * p.D * ESZ;
+          meta.at[x][lid] = page < 0 ? -1 : ((page * p.c.Hkv + w.kvh) << (p.c.page_shift - 4)) + ((a & (p.c.page - 1)) >> 4);
         const bool all = __all_sync(0xffu | 0xffffff00u, lid >= 8 || page >= 0);
         if (lid == 0) meta.full[x] = all && k0 + BK <= s.k_hi && (k0 >= s.k_lo || k0 + BK <= p.first_keys);
       };
@@ -278,32 +281,45 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
       int page0 = page_for(w.j0), page1 = page_for(w.j0 + 1);
       const char* const kc = static_cast<const char*>(p.c.k) + (long long)(rl & 15) * p.D * ESZ + c * 16;
       const char* const vc = static_cast<const char*>(p.c.v) + (long long)(rl & 15) * p.D * ESZ + c * 16;
-      // Row rl + STEP i of a tile: its group, and its byte offset past the group's row rl & 15.
-      auto group_of = [&](int i) { return (rl + STEP * i) >> 4; };
-      const int step_bytes = STEP < 16 ? STEP * p.D * ESZ : 0;
-      auto extra = [&](int i) { return STEP < 16 ? (i & (16 / (STEP < 16 ? STEP : 16) - 1)) * step_bytes : 0; };
+      // Row rl + STEP i of a tile lies in group (rl + STEP i) / 16, the first one of pass 0 in the
+      // place of the group that kc and vc point to.
+      const long long group_bytes = 16ll * p.D * ESZ;
       auto seen = [&](int k0, int i) {
         const int key = k0 + rl + STEP * i;
         return key < s.k_hi && (key >= s.k_lo || key < p.first_keys);
       };
+      auto groups_of = [&](int x, int (&at)[8]) {
+        const int4 u = *reinterpret_cast<const int4*>(meta.at[x]), v = *reinterpret_cast<const int4*>(meta.at[x] + 4);
+        at[0] = u.x, at[1] = u.y, at[2] = u.z, at[3] = u.w, at[4] = v.x, at[5] = v.y, at[6] = v.z, at[7] = v.w;
+      };
       if constexpr (F8) {
         static_assert(STEP >= 16, "a pass's rows lie in the same place of their groups");
         uint4 kr[N], vr[N];
-        auto load = [&](int x, int k0, int i, bool full, uint4& kv, const char* base) {
-          const long long off = meta.off[x][group_of(i)];
-          kv = make_uint4(0u, 0u, 0u, 0u);
-          if (in && (full || (off >= 0 && seen(k0, i)))) kv = __ldg(reinterpret_cast<const uint4*>(base + off));
+        const bool upper = DP == 64 && rl >= 16;  // (at 64 columns a pass is two groups)
+        auto group_at = [&](const int (&at)[8], int i) {
+          if constexpr (DP == 64) return upper ? at[2 * i + 1] : at[2 * i];
+          else return at[i];
+        };
+        auto load = [&](uint4& reg, const char* base, const int (&at)[8], int k0, int i, bool full) {
+          const int from = group_at(at, i);
+          if (full) {
+            reg = __ldg(reinterpret_cast<const uint4*>(base + from * group_bytes));
+          } else {
+            reg = make_uint4(0u, 0u, 0u, 0u);
+            if (from >= 0 && seen(k0, i)) reg = __ldg(reinterpret_cast<const uint4*>(base + from * group_bytes));
+          }
         };
         scales_for(page0);
         tell_places(0, w.j0, page0);
         named_bar_sync(2, 128);
-        {
+        if (in) {
           const int k0 = cached_tile(s, w.j0) * BK;
-          const bool full = meta.full[0] != 0;
+          int at[8];
+          groups_of(0, at);
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            load(0, k0, i, full, kr[i], kc);
-            load(0, k0, i, full, vr[i], vc);
+            load(kr[i], kc, at, k0, i, false);
+            load(vr[i], vc, at, k0, i, false);
           }
         }
         for (int j = w.j0; j < w.j1; ++j, ++g) {
@@ -318,29 +334,36 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
           page0 = page1;
           page1 = page_for(j + 2);
           const int k1 = more ? cached_tile(s, j + 1) * BK : 0;
-          const bool full = more && meta.full[x1] != 0;
           uint8_t* const tile = smem + L::OFF_KV + st * L::STAGE;
+          // Each piece is widened and stored, and its registers take the next tile's.
+          auto fill = [&](auto how) {  // 0: no next tile, 1: all of it is read, 2: what some row sees
+            constexpr int HOW = decltype(how)::value;
+            int at[8];
+            if constexpr (HOW != 0) groups_of(x1, at);
 #pragma unroll
-          for (int side = 0; side < 2; ++side) {
-            uint8_t* const to = tile + side * L::TILE;
+            for (int side = 0; side < 2; ++side) {
+              uint8_t* const to = tile + side * L::TILE;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const int row = rl + STEP * i;
-              uint4& reg = side ? vr[i] : kr[i];
-              const uint4 v = reg;
-              if (more) load(x1, k1, i, full, reg, side ? vc : kc);
-              if (in) {
+              for (int i = 0; i < N; ++i) {
+                const int row = rl + STEP * i;
+                uint4& reg = side ? vr[i] : kr[i];
                 uint4 a, b;
-                codes_f16(v.x, a.x, a.y);
-                codes_f16(v.y, a.z, a.w);
-                codes_f16(v.z, b.x, b.y);
-                codes_f16(v.w, b.z, b.w);
+                codes_f16(reg.x, a.x, a.y);
+                codes_f16(reg.y, a.z, a.w);
+                codes_f16(reg.z, b.x, b.y);
+                codes_f16(reg.w, b.z, b.w);
+                if constexpr (HOW != 0) load(reg, side ? vc : kc, at, k1, i, HOW == 1);
                 // (Threads of the second block store their pieces in the other order: no bank twice.)
                 const bool swap = c >= 4;
                 *reinterpret_cast<uint4*>(to + tile_at(row, 2 * c + (swap ? 1 : 0))) = swap ? b : a;
                 *reinterpret_cast<uint4*>(to + tile_at(row, 2 * c + (swap ? 0 : 1))) = swap ? a : b;
               }
             }
+          };
+          if (in) {
+            if (!more) fill(std::integral_constant<int, 0>());
+            else if (meta.full[x1]) fill(std::integral_constant<int, 1>());
+            else fill(std::integral_constant<int, 2>());
           }
           if (j == w.j0) copies_wait<0>();  // Q
           fence_proxy_async_smem();
@@ -371,16 +394,26 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
           page0 = page1;
           page1 = page_for(j + 2);
           const uint32_t tile = smem_u32(smem + L::OFF_KV + st * L::STAGE);
-          const bool full = meta.full[x] != 0;
           if (in) {
+            int at[8];
+            groups_of(x, at);
+            if (meta.full[x]) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const long long off = meta.off[x][group_of(i)];
-              const bool take = full || (off >= 0 && seen(k0, i));
-              const long long from = take ? off + extra(i) : 0;
-              const int at = tile_at(rl + STEP * i, c);
-              copy16(tile + at, kc + from, take);
-              copy16(tile + L::TILE + at, vc + from, take);
+              for (int i = 0; i < N; ++i) {
+                const long long from = at[i * STEP / 16] * group_bytes + (i * STEP % 16) * p.D * ESZ;
+                const int to = tile_at(rl + STEP * i, c);
+                copy16(tile + to, kc + from, true);
+                copy16(tile + L::TILE + to, vc + from, true);
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < N; ++i) {
+                const bool take = at[i * STEP / 16] >= 0 && seen(k0, i);
+                const long long from = take ? at[i * STEP / 16] * group_bytes + (i * STEP % 16) * p.D * ESZ : 0;
+                const int to = tile_at(rl + STEP * i, c);
+                copy16(tile + to, kc + from, take);
+                copy16(tile + L::TILE + to, vc + from, take);
+              }
             }
           }
           copies_commit();
