@@ -168,10 +168,13 @@ __device__ __forceinline__ CachedRow cached_row(const CachedParams& p, const Cac
   return w;
 }
 
-// The page of keys [k, k + 16) of batch row b, or -1 (reported).
-__device__ __forceinline__ int cached_page(const CachedParams& p, int b, int k) {
-  const int page = p.c.table[(long long)b * p.c.max_pages + (k >> p.c.page_shift)];
-  if ((unsigned)page < (unsigned)p.c.n_pages) return page;
+// The page of keys [k, k + 16) of batch row b as the table has it, and the page or -1 (reported) if
+// that is none: apart, so that a lookup made ahead is not waited for before its use.
+__device__ __forceinline__ int cached_lookup(const CachedParams& p, int b, int k) {
+  return __ldg(p.c.table + (long long)b * p.c.max_pages + (k >> p.c.page_shift));
+}
+__device__ __forceinline__ int cached_page(const CachedParams& p, int entry) {
+  if ((unsigned)entry < (unsigned)p.c.n_pages) return entry;
   atomicOr(p.status, STATUS_PAGE);
   return -1;
 }

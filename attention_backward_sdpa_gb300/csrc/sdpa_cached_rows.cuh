@@ -144,22 +144,25 @@ __global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams
       }
       return seen;
     };
-    int next_page[L::GROUPS];
+    int next_entry[L::GROUPS];
     auto find_pages = [&](int j) {
       int k0;
       const uint32_t seen = j < w.j1 ? piece(j, k0) : 0u;
 #pragma unroll
-      for (int u = 0; u < L::GROUPS; ++u) next_page[u] = (seen >> u) & 1u ? cached_page(p, w.b, k0 + 16 * u) : -1;
+      for (int u = 0; u < L::GROUPS; ++u)
+        if ((seen >> u) & 1u) next_entry[u] = cached_lookup(p, w.b, k0 + 16 * u);
     };
     auto issue = [&](int j) {
       const int stage = j % L::NST;
       const uint32_t to = ring + stage * (L::STAGE + L::META), meta = to + L::STAGE;
       int k0;
-      if (j < w.j1 && piece(j, k0) != 0u) {
+      const uint32_t seen = j < w.j1 ? piece(j, k0) : 0u;
+      if (seen != 0u) {
         uint32_t ok = 0;
 #pragma unroll
         for (int u = 0; u < L::GROUPS; ++u) {
-          const int page = next_page[u];
+          if (!((seen >> u) & 1u)) continue;
+          const int page = cached_page(p, next_entry[u]);
           if (page < 0) continue;
           ok |= 1u << u;
           const int slot = (k0 + 16 * u) & (p.c.page - 1);

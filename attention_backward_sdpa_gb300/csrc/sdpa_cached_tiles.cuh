@@ -6,11 +6,12 @@
 // and O in tensor memory, two softmax warpgroups that take half of a tile's keys each with a reference, a
 // sum and an O of their own (raised lazily, joined at the end).
 //
-// What differs is where the tiles come from. Four loader warps fill the stages: 16-byte asynchronous
-// copies (16-bit caches), or loads whose codes become fp16 on the way (8 bits, exact; a thread keeps the next
-// tile's codes in registers while it widens this one's). They write the 128-byte swizzle that the
-// tensor core reads, take any page size, and fill rows that no query sees with zeros. (A bulk tensor
-// copy could bring 16-bit pages, but not widen codes, and a page of 16 rows is a copy of 2 KB.)
+// What differs is where the tiles come from. Four loader warps fill the key tiles and four the
+// value tiles, each side with a ring of its own (a key tile is free again as soon as its scores are there):
+// 16-byte asynchronous copies (16-bit caches), or loads whose codes become fp16 on the way (8 bits, exact; a
+// thread keeps the next tile's codes in registers while it widens this one's). They write the 128-byte
+// swizzle that the tensor core reads, take any page size, and fill rows that no query sees with zeros. (A bulk
+// tensor copy could bring 16-bit pages, but not widen codes, and a page of 16 rows is a copy of 2 KB.)
 //
 // 8 bits. All products are fp16. bf16 queries become fp16 times a power of two a row (exact down to 2^-29 of
 // the row's largest). Scales stay out of the tiles: a page's key scale is in its scores' factor, and its
@@ -19,9 +20,9 @@
 // the reference is the largest weighted value's, whatever the scales are. (bf16 tiles with the scales multiplied
 // in took five instructions a pair of codes where fp16 takes one.)
 //
-// Warps: 0-7 softmax, 8-11 loaders, 12 issues S = Q K^T and owns the tensor memory, 13 issues
-// O += P V. Registers (launched with 128 a thread): 168 for softmax, 120 loaders, 56 issuers:
-// 256 x 168 + 128 x 120 + 128 x 56 = 512 x 128.
+// Warps: 0-7 softmax, 8-11 key loaders (and queries), 12-15 value loaders, 16 issues S = Q K^T and owns the
+// tensor memory, 17 issues O += P V. Registers (launched with 96 a thread): 144 for softmax, 80 loaders, 32
+// issuers: 256 x 144 + 256 x 80 + 128 x 32 = 640 x 96.
 #pragma once
 
 #include <type_traits>
@@ -32,32 +33,30 @@ namespace sdpa {
 
 namespace cached_tiles {
 
-constexpr int THREADS = 512, BM = 128, BK = 128, NSLOT = 2;
-constexpr uint32_t REGS_SOFTMAX = 168, REGS_LOAD = 120, REGS_CTRL = 56;
-static_assert(256 * REGS_SOFTMAX + 128 * REGS_LOAD + 128 * REGS_CTRL <= THREADS * 128, "register split");
+constexpr int THREADS = 640, BM = 128, BK = 128, NSLOT = 2;
+constexpr uint32_t REGS_SOFTMAX = 144, REGS_LOAD = 80, REGS_CTRL = 32;
+static_assert(256 * REGS_SOFTMAX + 256 * REGS_LOAD + 128 * REGS_CTRL <= THREADS * 96, "register split");
 constexpr uint64_t WAIT_LIMIT_NS = 4000000000ull;
 constexpr float RAISE = 8.f;  // P stays below 2^8 until its reference is raised
 
 enum : int {
   BAR_QFULL = 0,                   // 128 arrivals: the portion's Q tile is there
   BAR_QEMPTY = 1,                  // its last S product is done
-  BAR_KVFULL = 2,                  // + stage (up to 4), 128 arrivals
-  BAR_KVEMPTY = 6,                 // + stage: the tile's PV product is done
-  BAR_SFULL = 10,                  // + slot
+  BAR_SFULL = 2,                   // + slot
   BAR_PREADY = BAR_SFULL + NSLOT,  // + slot, 256 arrivals
   BAR_PVDONE = BAR_PREADY + NSLOT, // + slot
-  NUM_BARS = BAR_PVDONE + NSLOT
+  BAR_RING = BAR_PVDONE + NSLOT    // keys: full (128 arrivals) + stage, empty (their S product is done) + stage; then values
 };
 
 template <int DP>
 struct Layout {
   static constexpr int BLK = 128 * 128;  // 64 columns of 128 rows
   static constexpr int TILE = BM * DP * 2;
-  static constexpr int STAGE = 2 * TILE;
   static constexpr int NS = DP == 128 ? 3 : 4;
-  static constexpr int META = 112 + NS * 96;  // TileMeta
+  static constexpr int NUM_BARS = BAR_RING + 4 * NS;
+  static constexpr int META = 160 + NS * 96;  // TileMeta
   static constexpr int OFF_KV = TILE;
-  static constexpr int OFF_BAR = OFF_KV + NS * STAGE;
+  static constexpr int OFF_BAR = OFF_KV + 2 * NS * TILE;  // key stages, then value stages
   static constexpr int OFF_XCH = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_META = OFF_XCH + 2 * 256 * 4;  // TileMeta
   static constexpr int OFF_QEXP = OFF_META + META;        // [3][128] exponents of the rows' factors, by portion
@@ -87,11 +86,10 @@ __device__ __forceinline__ void codes_f16(uint32_t four, uint32_t& lo, uint32_t&
 // What the loaders tell of a tile, by groups of 16 keys.
 template <int NS>
 struct TileMeta {
-  int at[2][8];   // by parity of the tile: the group's rows are 16 at of the cache, -1: none is read
-  int full[2];    // every row of the tile is read
-  int bad[4];     // by stage: groups without a page
-  int unused[6];
-  float ks[NS][8], lvs[NS][8], inv[NS][8];  // by stage, 8 bits: key scale, log2 and inverse of the value scale
+  int at[2][2][8];  // by side, by parity of the tile: the group's rows are 16 at of the cache, -1: none is read
+  int full[2][2];   // every row of the tile is read
+  int bad[4];       // by value stage: groups without a page
+  float ks[NS][8], lvs[NS][8], inv[NS][8];  // by value stage, 8 bits: key scale, log2 and inverse of the value scale
 };
 static_assert(sizeof(TileMeta<3>) == Layout<128>::META && sizeof(TileMeta<4>) == Layout<64>::META, "");
 
@@ -121,16 +119,17 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
   if (walk.u >= walk.end) return;
   if (tid == 0) {
     *abort_flag = 0;
-    for (int i = 0; i < NUM_BARS; ++i)
-      mbar_init(&bars[i], i == BAR_QFULL || (i >= BAR_KVFULL && i < BAR_KVFULL + 4) ? 128
-                          : i >= BAR_PREADY && i < BAR_PREADY + NSLOT ? 256 : 1);
+    for (int i = 0; i < L::NUM_BARS; ++i) {
+      const bool full = i == BAR_QFULL || (i >= BAR_RING && (i - BAR_RING) % (2 * NS) < NS);
+      mbar_init(&bars[i], full ? 128 : i >= BAR_PREADY && i < BAR_PREADY + NSLOT ? 256 : 1);
+    }
     fence_mbar_init();
   }
   if (p.D < DP) {  // columns past D are never written
     for (int i = tid; i < L::OFF_BAR / 16; i += THREADS) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
   }
-  if (warp == 12) {
+  if (warp == 16) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
@@ -141,9 +140,10 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
 
   // Every role makes the same walk and counts the tiles that it has passed (g) and the portions
   // (np), whose phases the stages, the S/P slots and the Q buffer go by.
-  if (warp >= 12) {
+  constexpr int K_FULL = BAR_RING, K_EMPTY = K_FULL + NS, V_FULL = K_EMPTY + NS, V_EMPTY = V_FULL + NS;
+  if (warp >= 16) {
     regs_decrease<REGS_CTRL>();
-    if (warp < 14) {
+    if (warp < 18) {
       // ------------------------------------------------------------ MMA issuers
       constexpr uint32_t ID_S = idesc_io(BM, BK, false, false, PF);
       constexpr uint32_t ID_O = idesc_io(BM, DP, false, true, PF);
@@ -154,24 +154,25 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
       CachedPortion w;
       while (ok && walk.next(p, w)) {
         const int n = w.j1 - w.j0;
-        if (warp == 12) {
+        if (warp == 16) {
           ok = mbar_wait(&bars[BAR_QFULL], np & 1, abort_flag, WAIT_LIMIT_NS);
           for (int j = 0; j < n && ok; ++j, ++g) {
             const int st = g % NS, s = g % NSLOT;
-            ok = mbar_wait(&bars[BAR_KVFULL + st], (g / NS) & 1, abort_flag, WAIT_LIMIT_NS);
+            ok = mbar_wait(&bars[K_FULL + st], (g / NS) & 1, abort_flag, WAIT_LIMIT_NS);
             if (ok && g >= NSLOT)
               ok = mbar_wait(&bars[BAR_PVDONE + s], ((g - NSLOT) / NSLOT) & 1, abort_flag, WAIT_LIMIT_NS);
             if (!ok) break;
             __syncwarp();
             tc_fence_after();
             if (elect_one()) {
-              const uint32_t aQ = smem_u32(smem), aK = smem_u32(smem + L::OFF_KV + st * L::STAGE);
+              const uint32_t aQ = smem_u32(smem), aK = smem_u32(smem + L::OFF_KV + st * L::TILE);
 #pragma unroll
               for (int k = 0; k < DP / 16; ++k) {
                 const uint32_t ko = (k >> 2) * L::BLK + (k & 3) * 32;
                 mma_ss(tmem + 128u * s, sdesc_at(T_KMAJ, aQ + ko), sdesc_at(T_KMAJ, aK + ko), ID_S, k > 0);
               }
               mma_commit(&bars[BAR_SFULL + s]);
+              mma_commit(&bars[K_EMPTY + st]);
               if (j == n - 1) mma_commit(&bars[BAR_QEMPTY]);
             }
             __syncwarp();
@@ -180,18 +181,18 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
           for (int u = 0; u < n && ok; ++u, ++g) {
             const int su = g % NSLOT, stu = g % NS;
             ok = mbar_wait(&bars[BAR_PREADY + su], (g / NSLOT) & 1, abort_flag, WAIT_LIMIT_NS) &&
-                 mbar_wait(&bars[BAR_KVFULL + stu], (g / NS) & 1, abort_flag, WAIT_LIMIT_NS);
+                 mbar_wait(&bars[V_FULL + stu], (g / NS) & 1, abort_flag, WAIT_LIMIT_NS);
             if (!ok) break;
             __syncwarp();
             tc_fence_after();
             if (elect_one()) {
-              const uint32_t aV = smem_u32(smem + L::OFF_KV + stu * L::STAGE + L::TILE);
+              const uint32_t aV = smem_u32(smem + L::OFF_KV + (NS + stu) * L::TILE);
 #pragma unroll
               for (int k = 0; k < BK / 16; ++k)
                 mma_ts(tmem + L::COL_O + 128u * (k >> 2), tmem + 128u * su + 64u * (k >> 2) + 8 * (k & 3),
                        sdesc_at(T_MN_V, aV + k * 2048), ID_O, (u > 0 || (k & 3) > 0));
               mma_commit(&bars[BAR_PVDONE + su]);
-              mma_commit(&bars[BAR_KVEMPTY + stu]);
+              mma_commit(&bars[V_EMPTY + stu]);
             }
             __syncwarp();
           }
@@ -202,9 +203,17 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
   } else if (warp >= 8) {
     regs_decrease<REGS_LOAD>();
     // ------------------------------------------------------------ loaders
-    const int lid = tid - 256;
+    const int side = warp >= 12, lid = tid & 127;  // 0: keys, 1: values
+    const int first_warp = 8 + 4 * side, bar_id = 2 + side;
+    uint64_t* const full_bar = bars + (side ? V_FULL : K_FULL);
+    uint64_t* const empty_bar = bars + (side ? V_EMPTY : K_EMPTY);
+    uint8_t* const ring = smem + L::OFF_KV + side * NS * L::TILE;
     constexpr int ESZ = F8 ? 1 : 2, CHR = DP * ESZ / 16, STEP = 128 / CHR, N = CHR;  // pieces of a row, rows a pass, passes
-    const int c = lid % CHR, rl = lid / CHR;
+    // Thread to piece c of row rl of a pass. 8 bits: a piece becomes two neighbouring ones of the tile, so eight
+    // lanes that store together take four pieces of an even and an odd row, whose swizzles keep them on
+    // different banks.
+    const int c = !F8 ? lid % CHR : CHR == 8 ? (lid & 3) | ((lid >> 1) & 4) : lid & 3;
+    const int rl = !F8 ? lid / CHR : CHR == 8 ? ((lid >> 2) & 1) | ((lid >> 3) & ~1) : lid >> 2;
     const bool in = c * 16 < p.D * ESZ;
     int g = 0, np = 0;
     bool ok = true;
@@ -213,8 +222,9 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
       const CachedBounds& s = w.s;
       // (A wait that gives up leaves the portion going, so that all loaders meet at their barriers; they
       // end together after it.)
-      if (np > 0) ok = mbar_wait(&bars[BAR_QEMPTY], (np - 1) & 1, abort_flag, WAIT_LIMIT_NS);
-      {
+      if (side == 0 && np > 0) ok = mbar_wait(&bars[BAR_QEMPTY], (np - 1) & 1, abort_flag, WAIT_LIMIT_NS);
+      if (side == 0) {
+        __syncwarp();
         constexpr int CQ = DP / 8, SQ = 128 / CQ;  // a row's pieces on CQ neighbouring lanes
         const int cq = lid % CQ;
         const uint16_t* const q = static_cast<const uint16_t*>(p.q) + ((long long)w.b * p.c.Hkv + w.kvh) * p.R * p.D + cq * 8;
@@ -244,32 +254,35 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
         copies_commit();
       }
       // Threads 0-7 look up the pages of a tile's eight groups of 16 keys two tiles ahead, and in 8 bits
-      // their scales one tile ahead. Pages: -1 there is none, -2 no row sees the group.
-      auto page_for = [&](int j) -> int {
-        if (lid >= 8 || j >= w.j1) return -2;
+      // their scales one tile ahead.
+      auto wanted = [&](int j) {  // whether some row sees group lid of tile j
         const int a = cached_tile(s, j) * BK + 16 * lid;
-        return a < s.k_hi && (a + 15 >= s.k_lo || a < p.first_keys) ? cached_page(p, w.b, a) : -2;
+        return lid < 8 && j < w.j1 && a < s.k_hi && (a + 15 >= s.k_lo || a < p.first_keys);
       };
+      auto entry_for = [&](int j) { return wanted(j) ? cached_lookup(p, w.b, cached_tile(s, j) * BK + 16 * lid) : 0; };
+      // Pages: -1 there is none, -2 no row sees the group.
+      auto page_for = [&](int j, int entry) { return wanted(j) ? cached_page(p, entry) : -2; };
       float ks = 1.f, vs = 1.f;
       auto scales_for = [&](int page) {
         ks = vs = 1.f;
-        if (F8 && lid < 8 && page >= 0) {
+        if (F8 && side == 1 && lid < 8 && page >= 0) {
           ks = p.c.ks[(long long)page * p.c.Hkv + w.kvh];
           vs = p.c.vs[(long long)page * p.c.Hkv + w.kvh];
         }
       };
-      // Where tile j's groups are, for its loads (parity x): warp 8.
+      // Where tile j's groups are, for its loads (parity x): the side's first warp.
       auto tell_places = [&](int x, int j, int page) {
-        if (warp != 8) return;
+        if (warp != first_warp) return;
         const int k0 = cached_tile(s, j) * BK, a = k0 + 16 * (lid & 7);
         if (lid < 8)
-          meta.at[x][lid] = page < 0 ? -1 : ((page * p.c.Hkv + w.kvh) << (p.c.page_shift - 4)) + ((a & (p.c.page - 1)) >> 4);
-        const bool all = __all_sync(0xffu | 0xffffff00u, lid >= 8 || page >= 0);
-        if (lid == 0) meta.full[x] = all && k0 + BK <= s.k_hi && (k0 >= s.k_lo || k0 + BK <= p.first_keys);
+          meta.at[side][x][lid] = page < 0 ? -1 : ((page * p.c.Hkv + w.kvh) << (p.c.page_shift - 4)) + ((a & (p.c.page - 1)) >> 4);
+        const bool all = __all_sync(0xffffffffu, lid >= 8 || page >= 0);
+        if (lid == 0) meta.full[side][x] = all && k0 + BK <= s.k_hi && (k0 >= s.k_lo || k0 + BK <= p.first_keys);
       };
-      // What the others need of the tile in stage st.
+      // What the softmax needs of the tile in stage st (from the values' side: its stage is kept until
+      // the softmax is done with the tile).
       auto tell_stage = [&](int st, int page) {
-        if (warp != 8) return;
+        if (warp != 12) return;
         const uint32_t bad = __ballot_sync(0xffffffffu, page == -1);
         if (lid == 0) meta.bad[st] = (int)bad;
         if (F8 && lid < 8) {
@@ -278,141 +291,120 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
           meta.inv[st][lid] = 1.f / vs;
         }
       };
-      int page0 = page_for(w.j0), page1 = page_for(w.j0 + 1);
-      const char* const kc = static_cast<const char*>(p.c.k) + (long long)(rl & 15) * p.D * ESZ + c * 16;
-      const char* const vc = static_cast<const char*>(p.c.v) + (long long)(rl & 15) * p.D * ESZ + c * 16;
-      // Row rl + STEP i of a tile lies in group (rl + STEP i) / 16, the first one of pass 0 in the
-      // place of the group that kc and vc point to.
+      int page = page_for(w.j0, entry_for(w.j0)), entry = entry_for(w.j0 + 1);  // of this tile, of the next one
+      const char* const rows = static_cast<const char*>(side ? p.c.v : p.c.k) + (long long)(rl & 15) * p.D * ESZ + c * 16;
+      // Row rl + STEP i of a tile lies in group (rl + STEP i) / 16, the first
+      // one of pass 0 in the place of the group that `rows` points to.
       const long long group_bytes = 16ll * p.D * ESZ;
       auto seen = [&](int k0, int i) {
         const int key = k0 + rl + STEP * i;
         return key < s.k_hi && (key >= s.k_lo || key < p.first_keys);
       };
       auto groups_of = [&](int x, int (&at)[8]) {
-        const int4 u = *reinterpret_cast<const int4*>(meta.at[x]), v = *reinterpret_cast<const int4*>(meta.at[x] + 4);
+        const int4 u = *reinterpret_cast<const int4*>(meta.at[side][x]), v = *reinterpret_cast<const int4*>(meta.at[side][x] + 4);
         at[0] = u.x, at[1] = u.y, at[2] = u.z, at[3] = u.w, at[4] = v.x, at[5] = v.y, at[6] = v.z, at[7] = v.w;
       };
       if constexpr (F8) {
         static_assert(STEP >= 16, "a pass's rows lie in the same place of their groups");
-        uint4 kr[N], vr[N];
+        uint4 reg[N];
         const bool upper = DP == 64 && rl >= 16;  // (at 64 columns a pass is two groups)
-        auto group_at = [&](const int (&at)[8], int i) {
-          if constexpr (DP == 64) return upper ? at[2 * i + 1] : at[2 * i];
-          else return at[i];
-        };
-        auto load = [&](uint4& reg, const char* base, const int (&at)[8], int k0, int i, bool full) {
-          const int from = group_at(at, i);
+        auto load = [&](uint4& v, const int (&at)[8], int k0, int i, bool full) {
+          const int from = DP == 64 ? (upper ? at[(2 * i + 1) & 7] : at[(2 * i) & 7]) : at[i];
           if (full) {
-            reg = __ldg(reinterpret_cast<const uint4*>(base + from * group_bytes));
+            v = __ldg(reinterpret_cast<const uint4*>(rows + from * group_bytes));
           } else {
-            reg = make_uint4(0u, 0u, 0u, 0u);
-            if (from >= 0 && seen(k0, i)) reg = __ldg(reinterpret_cast<const uint4*>(base + from * group_bytes));
+            v = make_uint4(0u, 0u, 0u, 0u);
+            if (from >= 0 && seen(k0, i)) v = __ldg(reinterpret_cast<const uint4*>(rows + from * group_bytes));
           }
         };
-        scales_for(page0);
-        tell_places(0, w.j0, page0);
-        named_bar_sync(2, 128);
+        scales_for(page);
+        tell_places(0, w.j0, page);
+        named_bar_sync(bar_id, 128);
         if (in) {
           const int k0 = cached_tile(s, w.j0) * BK;
           int at[8];
           groups_of(0, at);
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            load(kr[i], kc, at, k0, i, false);
-            load(vr[i], vc, at, k0, i, false);
-          }
+          for (int i = 0; i < N; ++i) load(reg[i], at, k0, i, false);
         }
         for (int j = w.j0; j < w.j1; ++j, ++g) {
           const int x1 = (j - w.j0 + 1) & 1, st = g % NS;
           const bool more = j + 1 < w.j1;
+          const int page1 = page_for(j + 1, entry);
+          entry = entry_for(j + 2);
           if (more) tell_places(x1, j + 1, page1);
-          if (g >= NS && ok) ok = mbar_wait(&bars[BAR_KVEMPTY + st], ((g / NS) - 1) & 1, abort_flag, WAIT_LIMIT_NS);
+          if (g >= NS && ok) ok = mbar_wait(&empty_bar[st], ((g / NS) - 1) & 1, abort_flag, WAIT_LIMIT_NS);
           __syncwarp();
-          tell_stage(st, page0);
-          named_bar_sync(2, 128);
+          tell_stage(st, page);
+          named_bar_sync(bar_id, 128);
           scales_for(page1);
-          page0 = page1;
-          page1 = page_for(j + 2);
+          page = page1;
           const int k1 = more ? cached_tile(s, j + 1) * BK : 0;
-          uint8_t* const tile = smem + L::OFF_KV + st * L::STAGE;
+          uint8_t* const to = ring + st * L::TILE;
           // Each piece is widened and stored, and its registers take the next tile's.
           auto fill = [&](auto how) {  // 0: no next tile, 1: all of it is read, 2: what some row sees
             constexpr int HOW = decltype(how)::value;
             int at[8];
             if constexpr (HOW != 0) groups_of(x1, at);
 #pragma unroll
-            for (int side = 0; side < 2; ++side) {
-              uint8_t* const to = tile + side * L::TILE;
-#pragma unroll
-              for (int i = 0; i < N; ++i) {
-                const int row = rl + STEP * i;
-                uint4& reg = side ? vr[i] : kr[i];
-                uint4 a, b;
-                codes_f16(reg.x, a.x, a.y);
-                codes_f16(reg.y, a.z, a.w);
-                codes_f16(reg.z, b.x, b.y);
-                codes_f16(reg.w, b.z, b.w);
-                if constexpr (HOW != 0) load(reg, side ? vc : kc, at, k1, i, HOW == 1);
-                // (Threads of the second block store their pieces in the other order: no bank twice.)
-                const bool swap = c >= 4;
-                *reinterpret_cast<uint4*>(to + tile_at(row, 2 * c + (swap ? 1 : 0))) = swap ? b : a;
-                *reinterpret_cast<uint4*>(to + tile_at(row, 2 * c + (swap ? 0 : 1))) = swap ? a : b;
-              }
+            for (int i = 0; i < N; ++i) {
+              const int row = rl + STEP * i;
+              uint4 a, b;
+              codes_f16(reg[i].x, a.x, a.y);
+              codes_f16(reg[i].y, a.z, a.w);
+              codes_f16(reg[i].z, b.x, b.y);
+              codes_f16(reg[i].w, b.z, b.w);
+              if constexpr (HOW != 0) load(reg[i], at, k1, i, HOW == 1);
+              *reinterpret_cast<uint4*>(to + tile_at(row, 2 * c)) = a;
+              *reinterpret_cast<uint4*>(to + tile_at(row, 2 * c + 1)) = b;
             }
           };
           if (in) {
             if (!more) fill(std::integral_constant<int, 0>());
-            else if (meta.full[x1]) fill(std::integral_constant<int, 1>());
+            else if (meta.full[side][x1]) fill(std::integral_constant<int, 1>());
             else fill(std::integral_constant<int, 2>());
           }
           if (j == w.j0) copies_wait<0>();  // Q
           fence_proxy_async_smem();
-          if (j == w.j0) mbar_arrive(&bars[BAR_QFULL]);
-          mbar_arrive(&bars[BAR_KVFULL + st]);
+          if (side == 0 && j == w.j0) mbar_arrive(&bars[BAR_QFULL]);
+          mbar_arrive(&full_bar[st]);
         }
       } else {
         int signalled = 0;  // tiles of this portion (and Q, before the first) that the others know of
         const int g0 = g;
         auto signal = [&](int upto) {
           fence_proxy_async_smem();
-          if (signalled == 0 && upto > 0) mbar_arrive(&bars[BAR_QFULL]);
-          for (; signalled < upto; ++signalled) mbar_arrive(&bars[BAR_KVFULL + (g0 + signalled) % NS]);
+          if (side == 0 && signalled == 0 && upto > 0) mbar_arrive(&bars[BAR_QFULL]);
+          for (; signalled < upto; ++signalled) mbar_arrive(&full_bar[(g0 + signalled) % NS]);
         };
         for (int j = w.j0; j < w.j1; ++j, ++g) {
           const int x = (j - w.j0) & 1, st = g % NS, k0 = cached_tile(s, j) * BK;
-          tell_places(x, j, page0);
+          if (j > w.j0) page = page_for(j, entry), entry = entry_for(j + 1);
+          tell_places(x, j, page);
           if (g >= NS && ok) {
-            if (!mbar_try_wait(&bars[BAR_KVEMPTY + st], ((g / NS) - 1) & 1)) {
+            if (!mbar_try_wait(&empty_bar[st], ((g / NS) - 1) & 1)) {
               copies_wait<0>();  // nothing to fill yet: what has been filled is handed over
               signal(j - w.j0);
-              ok = mbar_wait(&bars[BAR_KVEMPTY + st], ((g / NS) - 1) & 1, abort_flag, WAIT_LIMIT_NS);
+              ok = mbar_wait(&empty_bar[st], ((g / NS) - 1) & 1, abort_flag, WAIT_LIMIT_NS);
             }
           }
           __syncwarp();
-          tell_stage(st, page0);
-          named_bar_sync(2, 128);
-          page0 = page1;
-          page1 = page_for(j + 2);
-          const uint32_t tile = smem_u32(smem + L::OFF_KV + st * L::STAGE);
+          tell_stage(st, page);
+          named_bar_sync(bar_id, 128);
+          const uint32_t tile = smem_u32(ring + st * L::TILE);
           if (in) {
             int at[8];
             groups_of(x, at);
-            if (meta.full[x]) {
+            if (meta.full[side][x]) {
 #pragma unroll
-              for (int i = 0; i < N; ++i) {
-                const long long from = at[i * STEP / 16] * group_bytes + (i * STEP % 16) * p.D * ESZ;
-                const int to = tile_at(rl + STEP * i, c);
-                copy16(tile + to, kc + from, true);
-                copy16(tile + L::TILE + to, vc + from, true);
-              }
+              for (int i = 0; i < N; ++i)
+                copy16(tile + tile_at(rl + STEP * i, c), rows + at[i * STEP / 16] * group_bytes + (i * STEP % 16) * p.D * ESZ, true);
             } else {
 #pragma unroll
               for (int i = 0; i < N; ++i) {
                 const bool take = at[i * STEP / 16] >= 0 && seen(k0, i);
-                const long long from = take ? at[i * STEP / 16] * group_bytes + (i * STEP % 16) * p.D * ESZ : 0;
-                const int to = tile_at(rl + STEP * i, c);
-                copy16(tile + to, kc + from, take);
-                copy16(tile + L::TILE + to, vc + from, take);
+                copy16(tile + tile_at(rl + STEP * i, c),
+                       rows + (take ? at[i * STEP / 16] * group_bytes + (i * STEP % 16) * p.D * ESZ : 0), take);
               }
             }
           }
@@ -424,7 +416,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
         signal(w.j1 - w.j0);
       }
       ++np;
-      ok = !named_bar_any(2, 128, !ok);  // (and the next portion's pages may replace these)
+      ok = !named_bar_any(bar_id, 128, !ok);  // (and the next portion's pages may replace these)
     }
     copies_wait<0>();
   } else {
@@ -447,8 +439,8 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
       for (int j = 0; j < n; ++j, ++g) {
         const int s = g % NSLOT, st = g % NS;
         const int kb = cached_tile(w.s, w.j0 + j) * BK + i0;
-        // (the stage's barrier too: what the loaders wrote beside the tile)
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars[BAR_KVFULL + st], (g / NS) & 1, abort_flag, WAIT_LIMIT_NS) &&
+        // (the value stage's barrier too: what the loaders wrote beside the tile)
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars[V_FULL + st], (g / NS) & 1, abort_flag, WAIT_LIMIT_NS) &&
                                          mbar_wait(&bars[BAR_SFULL + s], (g / NSLOT) & 1, abort_flag, WAIT_LIMIT_NS));
         if (!ok) break;
         const uint32_t bad = ((uint32_t)meta.bad[st] >> (4 * half)) & 15u;
@@ -650,7 +642,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
   tc_fence_before();
   __syncthreads();
   if (*abort_flag && tid == 0) atomicOr(p.status, STATUS_TIMEOUT);
-  if (warp == 12) {
+  if (warp == 16) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
