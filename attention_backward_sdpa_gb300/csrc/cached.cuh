@@ -15,8 +15,10 @@
 // one a CTA: lengths as uneven as they come leave no SM idle, and one long sequence is shared by
 // all. A segment inside one share is written at once; of one that is cut every share leaves
 // a part (O / l in fp32, and log2 of its sum) in the workspace, two at most: of the segment that
-// it begins in the middle of (slot 0), and of the one that it does not finish (slot 1). The merge
-// kernel weighs the parts in their order, so results do not depend on timing.
+// it begins in the middle of (slot 0), and of the one that it does not finish (slot 1). The first share to
+// begin in the middle of a segment also notes which shares have parts of it; the merge kernel, a
+// block a share, weighs them in their order, so that results do not depend on timing. (A merge that found the
+// cut segments by the schedule again took 10 to 28 us, most of it in scans and 64-bit divisions.)
 #pragma once
 
 #include "common.cuh"
@@ -40,6 +42,7 @@ struct CachedParams {
   int n_ctas;
   float* part_o;              // [n_ctas][2][tile_rows][D]
   float* part_lse;            // [n_ctas][2][tile_rows], log2 units
+  int4* cuts;                 // [n_ctas] {segment (entry * Hkv + head), first share, last share, 0} or {-1, ..}
   int* status;
 };
 
@@ -69,19 +72,20 @@ __device__ __forceinline__ CachedBounds cached_bounds(const CachedParams& p, int
 }
 __device__ __forceinline__ int cached_tile(const CachedBounds& s, int j) { return j < s.nf ? j : s.kt + (j - s.nf); }
 
-// First unit of CTA i's share of T units, and the CTA that has unit t.
+// Shares of T units, each of one unit at least; first unit of share i of n, and the share that has unit t.
+__device__ __forceinline__ int shares_of(const CachedParams& p, long long T) { return (int)min((long long)p.n_ctas, T); }
 __device__ __forceinline__ long long share_begin(long long T, int n, int i) { return T * i / n; }
 __device__ __forceinline__ int share_of(long long T, int n, long long t) { return (int)(((t + 1) * n + T - 1) / T) - 1; }
 
-// Where unit `at(T)` of all T lies: entry e (b * n_rt + rt) and its first unit. One call by
-// every thread of the block; `sh` is shared memory.
+// Where this CTA's share begins: its first unit and the one past its last, its entry e (b * n_rt + rt),
+// and that entry's first unit. One call by every thread of the block; `sh` and `warp_sum` are shared memory.
 struct CachedStart {
-  long long T, at, te;
+  long long begin, end, te;
   int e;
 };
-template <int THREADS, typename At>
-__device__ __forceinline__ CachedStart cached_start(const CachedParams& p, CachedStart* sh, long long* warp_sum,
-                                                    bool report, At at) {
+template <int THREADS>
+__device__ __forceinline__ CachedStart cached_start(const CachedParams& p, CachedStart* sh, long long* warp_sum) {
+  const bool report = blockIdx.x == 0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = p.B * p.n_rt, per = ceil_div(E, THREADS), e0 = min(tid * per, E), e1 = min(e0 + per, E);
   long long sum = 0;
@@ -107,21 +111,46 @@ __device__ __forceinline__ CachedStart cached_start(const CachedParams& p, Cache
     if (w == warp) incl += T;
     T += warp_sum[w];
   }
-  const long long want = at(T);
+  const int n = shares_of(p, T), i = blockIdx.x;
+  const long long begin = i < n ? share_begin(T, n, i) : T, end = i < n ? share_begin(T, n, i + 1) : T;
   long long te = incl - sum;
-  if (want >= te && want < incl) {
+  if (begin >= te && begin < incl) {
     for (int e = e0; e < e1; ++e) {
-      const long long n = (long long)cached_bounds(p, e / p.n_rt, e % p.n_rt).n * p.c.Hkv;
-      if (want < te + n) {
+      const long long k = (long long)cached_bounds(p, e / p.n_rt, e % p.n_rt).n * p.c.Hkv;
+      if (begin < te + k) {
         sh->e = e;
         sh->te = te;
+        // A segment that the share begins in the middle of, and the share before does not.
+        const int m = (int)(k / p.c.Hkv), h = (int)((begin - te) / m);
+        const long long first = te + (long long)h * m;
+        int4 cut = make_int4(-1, 0, 0, 0);
+        if (begin > first && share_begin(T, n, i - 1) <= first)
+          cut = make_int4(e * p.c.Hkv + h, i - 1, share_of(T, n, first + m - 1), 0);
+        p.cuts[i] = cut;
         break;
       }
-      te += n;
+      te += k;
     }
   }
+  if (begin >= T && tid == 0) p.cuts[i] = make_int4(-1, 0, 0, 0);
   __syncthreads();
-  return CachedStart{T, want, sh->te, sh->e};
+  return CachedStart{begin, end, sh->te, sh->e};
+}
+
+// Rows that see no key: entries that visit no unit, each written by one of the CTAs.
+template <int THREADS>
+__device__ __forceinline__ void cached_empty_rows(const CachedParams& p) {
+  for (int e = blockIdx.x; e < p.B * p.n_rt; e += gridDim.x) {
+    const int b = e / p.n_rt, rt = e % p.n_rt;
+    if (cached_bounds(p, b, rt).n > 0) continue;
+    const int r0 = rt * p.tile_rows, rows = min(p.tile_rows, p.R - r0), pieces = p.D / 8;
+    for (int i = threadIdx.x; i < p.c.Hkv * rows * pieces; i += THREADS) {
+      const int c = i % pieces, r = r0 + i / pieces % rows, h = i / pieces / rows;
+      const long long orow = ((long long)b * p.c.Hkv + h) * p.R + r;
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + orow * p.D + c * 8) = make_uint4(0u, 0u, 0u, 0u);
+      if (c == 0) p.lse[orow] = p.sink ? p.sink[h * p.G + r / p.Sq] : -INFINITY;
+    }
+  }
 }
 
 // A share's walk over its portions of segments, the same for every thread that makes it.
@@ -216,7 +245,10 @@ cudaError_t cached_tiles_16_setup();
 cudaError_t cached_tiles_8_setup();
 cudaError_t launch_cached_merge(const CachedParams& p, cudaStream_t s);
 
-// Keys of a unit of the few-rows kernel: four warps of 16 keys, or of 32 in 8 bits.
-constexpr int CACHED_ROWS_TK_16 = 64, CACHED_ROWS_TK_8 = 128;
+// Keys of a unit of the few-rows kernel with 16 mt rows: four warps of 16 keys, or of 32 in 8 bits
+// where the registers allow it.
+__host__ __device__ constexpr int cached_rows_tk(bool f8, int mt) { return f8 && mt == 1 ? 128 : 64; }
+// CTAs of it that an SM holds.
+__host__ __device__ constexpr int cached_rows_ctas(int mt) { return mt == 1 ? 3 : 2; }
 
 }  // namespace sdpa

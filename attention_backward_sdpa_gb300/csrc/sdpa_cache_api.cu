@@ -73,7 +73,7 @@ size_t cache_bytes(const KvCacheRef& c) { return (size_t)c.n_pages * c.Hkv * c.p
 // neither the workspace nor any result depends on that).
 struct CachedPlan {
   int tile_rows, n_rt, tk, n_ctas, mt;
-  size_t o_bytes, bytes;
+  size_t o_bytes, lse_bytes, bytes;
 };
 constexpr int SHARE_SMS = 152;  // SMs of a GB300
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -83,15 +83,15 @@ CachedPlan cached_plan(long long B, int H_q, int H_kv, int S_q, int D, bool f8, 
   const long long R = (long long)(H_q / H_kv) * S_q;
   c.mt = R <= 16 ? 1 : R <= 32 ? 2 : 0;  // 0: the many-rows kernel
   c.tile_rows = c.mt ? 16 * c.mt : 128;
-  c.tk = c.mt == 0 || f8 ? 128 : 64;
-  static_assert(CACHED_ROWS_TK_16 == 64 && CACHED_ROWS_TK_8 == 128, "units");
+  c.tk = c.mt ? cached_rows_tk(f8, c.mt) : 128;
   c.n_rt = (int)((R + c.tile_rows - 1) / c.tile_rows);
   // As many CTAs as the device holds at once (by their shared memory), fewer where there are
   // not that many units.
-  const long long units = B * c.n_rt * H_kv * ((max_keys + c.tk - 1) / c.tk), most = c.mt ? 2 * SHARE_SMS : SHARE_SMS;
+  const long long units = B * c.n_rt * H_kv * ((max_keys + c.tk - 1) / c.tk), most = c.mt ? cached_rows_ctas(c.mt) * SHARE_SMS : SHARE_SMS;
   c.n_ctas = (int)(units < most ? units : most);
   c.o_bytes = align256((size_t)c.n_ctas * 2 * c.tile_rows * D * sizeof(float));
-  c.bytes = c.o_bytes + align256((size_t)c.n_ctas * 2 * c.tile_rows * sizeof(float));
+  c.lse_bytes = align256((size_t)c.n_ctas * 2 * c.tile_rows * sizeof(float));
+  c.bytes = c.o_bytes + c.lse_bytes + align256((size_t)c.n_ctas * sizeof(int4));
   return c;
 }
 
@@ -139,7 +139,7 @@ int sdpa_fwd_cached(int io_dtype, int cache_dtype, const void* q, const void* k_
   for (const void* x : {(const void*)lse, (const void*)sink, (const void*)alibi_slopes, (const void*)seq_q_lens})
     if (misaligned(x, 4)) return SDPA_ERR_ALIGN;
   const CachedPlan plan = cached_plan(B, H_q, H_kv, S_q, D, p.c.f8 != 0, (long long)max_pages * page_size);
-  if ((long long)B * plan.n_rt >= 1ll << 24) return SDPA_ERR_INVALID;
+  if ((long long)B * plan.n_rt >= 1ll << 24 || (long long)B * plan.n_rt * H_kv >= 1ll << 31) return SDPA_ERR_INVALID;
   if (workspace) {
     if (workspace_bytes < plan.bytes) return SDPA_ERR_WORKSPACE;
     if (misaligned(workspace, 256)) return SDPA_ERR_ALIGN;
@@ -172,6 +172,7 @@ int sdpa_fwd_cached(int io_dtype, int cache_dtype, const void* q, const void* k_
   p.n_ctas = plan.n_ctas;
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.o_bytes);
+  p.cuts = reinterpret_cast<int4*>(static_cast<char*>(workspace) + plan.o_bytes + plan.lse_bytes);
   nvtxRangePushA("sdpa_fwd_cached");
   cudaError_t e = plan.mt ? (p.c.f8 ? launch_cached_rows_8(p, plan.mt, stream) : launch_cached_rows_16(p, plan.mt, stream))
                           : (p.c.f8 ? launch_cached_tiles_8(p, stream) : launch_cached_tiles_16(p, stream));

@@ -4,7 +4,7 @@
 // of bytes for 4 D flops a row. So the work is to keep enough reads in flight and everything
 // else out of their way.
 //
-//   - Warps share nothing while they run. A unit's keys are four pieces of 16 (or, in 8 bits, 32), one a warp, and
+//   - Warps share nothing while they run. A unit's keys are four pieces of 16 (or, in 8 bits with 16 rows, 32), one a warp, and
 //     each warp has a ring of stages of its own that it fills by 16-byte asynchronous copies and waits for
 //     by itself: no barrier of the CTA in the loop. Pieces that no row sees are neither read nor
 //     computed; rows of a piece that none sees are filled with zeros, so that what a recycled page
@@ -37,21 +37,23 @@ enum : int { BF16 = 0, F16 = 1, E4M3 = 2 };
 
 template <int CT, int DP, int MT>
 struct Layout {
-  static constexpr int GROUPS = CT == E4M3 ? 2 : 1;  // of 16 keys
+  static constexpr int GROUPS = CT == E4M3 && MT == 1 ? 2 : 1;  // of 16 keys
   static constexpr int KS = 16 * GROUPS;             // keys of a warp's piece
   static constexpr int TK = KS * WARPS;
   static constexpr int RB = DP * (CT == E4M3 ? 1 : 2);  // bytes of a row
   static constexpr int CH = RB / 16;
   static constexpr int SIDE = KS * RB;                  // keys or values of a piece
   static constexpr int STAGE = 2 * SIDE;
-  static constexpr int NST = 3 * 8192 / STAGE;
+  // Three CTAs an SM with 16 rows, two with 32, by their registers; what shared memory that leaves is stages.
+  static constexpr int CTAS = cached_rows_ctas(MT);
+  static constexpr int NST = (CTAS == 3 ? 2 : 3) * 8192 / STAGE;
   static constexpr int META = 32;                       // {ks, ks, vs, vs, page bits}
   static constexpr int RING = NST * (STAGE + META);
   static constexpr int TR = 16 * MT;
   static constexpr int OROW = DP + 4;                   // floats of an O row in the exchange
   static constexpr int XCH = WARPS * TR * (OROW + 2) * 4;
   static constexpr int BYTES = WARPS * RING > XCH ? WARPS * RING : XCH;
-  static_assert(NST >= 2 && (CT != E4M3 || TK == CACHED_ROWS_TK_8) && (CT == E4M3 || TK == CACHED_ROWS_TK_16), "");
+  static_assert(NST >= 2 && TK == cached_rows_tk(CT == E4M3, MT), "");
 };
 
 // 16-byte piece c of row r: rows of a piece lie on different banks for the eight rows of a
@@ -104,7 +106,7 @@ __device__ __forceinline__ void codes_f16(uint32_t four, uint32_t& lo, uint32_t&
 // CT: type of the cache; IOF: the queries and O are fp16 (a 16-bit cache has their type). MOD: capped or
 // distance-biased scores.
 template <int CT, bool IOF, int DP, int MT, bool MOD>
-__global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams p) {
+__global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows_kernel(const CachedParams p) {
   using L = Layout<CT, DP, MT>;
   constexpr bool PF = CT != BF16;  // the products are fp16
   constexpr float BIAS = PF ? 6.f : 0.f;
@@ -113,11 +115,10 @@ __global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams
   __shared__ CachedStart sh_start;
   __shared__ long long sh_sum[WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const CachedStart st = cached_start<THREADS>(p, &sh_start, sh_sum, blockIdx.x == 0, [&](long long T) {
-    return share_begin(T, p.n_ctas, blockIdx.x);
-  });
+  const CachedStart st = cached_start<THREADS>(p, &sh_start, sh_sum);
   pdl_launch_dependents();  // (the merge waits for this grid before it reads the parts)
-  CachedWalk walk{st.at, share_begin(st.T, p.n_ctas, blockIdx.x + 1), st.te, st.e};
+  cached_empty_rows<THREADS>(p);
+  CachedWalk walk{st.begin, st.end, st.te, st.e};
   if (walk.u >= walk.end) return;
   const uint32_t ring = smem_u32(smem) + warp * L::RING;
   // Columns past D are never copied: zeros, once (and again after the exchange has used the place).
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams
   clear();
   const int copy_row = lane / L::CH, copy_c = lane % L::CH;
   const bool copy_in = copy_c * 16 < p.D * ESZ;
+  const int row_bytes = p.D * ESZ, pass_bytes = (32 / L::CH) * row_bytes;
   CachedPortion w;
   while (walk.next(p, w)) {
     const CachedBounds& s = w.s;
@@ -161,27 +163,42 @@ __global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams
         uint32_t ok = 0;
 #pragma unroll
         for (int u = 0; u < L::GROUPS; ++u) {
-          if (!((seen >> u) & 1u)) continue;
-          const int page = cached_page(p, next_entry[u]);
-          if (page < 0) continue;
-          ok |= 1u << u;
-          const int slot = (k0 + 16 * u) & (p.c.page - 1);
-          const long long head = (long long)page * p.c.Hkv + w.kvh, row = (head << p.c.page_shift) + slot;
-          const char* const kb = static_cast<const char*>(p.c.k) + row * p.D * ESZ + copy_c * 16;
-          const char* const vb = static_cast<const char*>(p.c.v) + row * p.D * ESZ + copy_c * 16;
+          const int a = k0 + 16 * u, page = (seen >> u) & 1u ? cached_page(p, next_entry[u]) : -1;
+          if (page >= 0) ok |= 1u << u;
+          const bool all = page >= 0 && a + 16 <= s.k_hi && (a >= s.k_lo || a + 16 <= p.first_keys);
+          const long long head = (long long)max(page, 0) * p.c.Hkv + w.kvh;
+          const long long at = ((head << p.c.page_shift) + (a & (p.c.page - 1)) + copy_row) * row_bytes + copy_c * 16;
+          const char* kb = static_cast<const char*>(p.c.k) + at;
+          const char* vb = static_cast<const char*>(p.c.v) + at;
           if (copy_in) {
+            if (all) {
 #pragma unroll
-            for (int i = 0; i < 16 * L::CH / 32; ++i) {
-              const int r = copy_row + i * (32 / L::CH), key = k0 + 16 * u + r;
-              const bool take = key < s.k_hi && (key >= s.k_lo || key < p.first_keys);
-              const uint32_t at = to + (16 * u + r) * L::RB + phys<L::CH>(16 * u + r, copy_c) * 16;
-              const int off = r * p.D * ESZ;
-              copy16(at, kb + off, take);
-              copy16(at + L::SIDE, vb + off, take);
+              for (int i = 0; i < 16 * L::CH / 32; ++i) {
+                const int r = 16 * u + copy_row + i * (32 / L::CH);
+                const uint32_t dst = to + r * L::RB + phys<L::CH>(r, copy_c) * 16;
+                copy16(dst, kb, true);
+                copy16(dst + L::SIDE, vb, true);
+                kb += pass_bytes;
+                vb += pass_bytes;
+              }
+            } else {  // rows that no query sees: zeros
+#pragma unroll 1
+              for (int i = 0; i < 16 * L::CH / 32; ++i) {
+                const int r = 16 * u + copy_row + i * (32 / L::CH), key = k0 + r;
+                const bool take = page >= 0 && key < s.k_hi && (key >= s.k_lo || key < p.first_keys);
+                const uint32_t dst = to + r * L::RB + phys<L::CH>(r, copy_c) * 16;
+                copy16(dst, take ? kb : static_cast<const char*>(p.c.k), take);
+                copy16(dst + L::SIDE, take ? vb : static_cast<const char*>(p.c.v), take);
+                kb += pass_bytes;
+                vb += pass_bytes;
+              }
             }
           }
           if constexpr (CT == E4M3) {
-            if (lane < 2) copy4(meta + (2 * lane + u) * 4, (lane ? p.c.vs : p.c.ks) + head);
+            if (lane < 2) {
+              if (page >= 0) copy4(meta + (2 * lane + u) * 4, (lane ? p.c.vs : p.c.ks) + head);
+              else asm volatile("st.shared.f32 [%0], %1;" ::"r"(meta + (2 * lane + u) * 4), "f"(1.f) : "memory");
+            }
           }
         }
         if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(meta + 16), "r"(ok) : "memory");
@@ -262,70 +279,77 @@ __global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams
       const uint32_t at = ring + (j % L::NST) * (L::STAGE + L::META), meta = at + L::STAGE;
       uint32_t ok;
       asm volatile("ld.shared.b32 %0, [%1];" : "=r"(ok) : "r"(meta + 16) : "memory");
+      constexpr int KT = 2 * L::GROUPS;  // tiles of 8 keys
+      const uint32_t sk = at, sv = at + L::SIDE;
+      // ---- S = Q K^T: element [mt][n][e]: row g + 8 (e >> 1), key 8 n + 2 t + (e & 1)
+      float sc[MT][KT][4];
 #pragma unroll
-      for (int u = 0; u < L::GROUPS; ++u) {
-        if (!((ok >> u) & 1u)) continue;
-        const uint32_t sk = at + 16 * u * L::RB, sv = sk + L::SIDE;
-        // ---- S = Q K^T: element [mt][n][e]: row g + 8 (e >> 1), key 8 n + 2 t + (e & 1)
-        float sc[MT][2][4];
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int n = 0; n < KT; ++n)
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int e = 0; e < 4; ++e) sc[mt][n][e] = 0.f;
+      if constexpr (CT == E4M3) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[mt][n][e] = 0.f;
-        if constexpr (CT == E4M3) {
+        for (int h = 0; h < DP / 64; ++h) {
+          uint4 v[KT];
 #pragma unroll
-          for (int h = 0; h < DP / 64; ++h)
+          for (int n = 0; n < KT; ++n) v[n] = lds16(sk + (8 * n + g) * L::RB + phys<L::CH>(8 * n + g, 4 * h + t) * 16);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const uint4 v = lds16(sk + (8 * n + g) * L::RB + phys<L::CH>(8 * n + g, 4 * h + t) * 16);
-              const uint32_t four[4] = {v.x, v.y, v.z, v.w};
+          for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
-              for (int jj = 0; jj < 4; ++jj) {
-                uint32_t b0, b1;
-                codes_f16(four[jj], b0, b1);
+            for (int n = 0; n < KT; ++n) {
+              uint32_t b0, b1;
+              codes_f16(jj == 0 ? v[n].x : jj == 1 ? v[n].y : jj == 2 ? v[n].z : v[n].w, b0, b1);
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) mma<true>(sc[mt][n], qf[mt][4 * h + jj], b0, b1);
-              }
+              for (int mt = 0; mt < MT; ++mt) mma<true>(sc[mt][n], qf[mt][4 * h + jj], b0, b1);
             }
-        } else {
-          const int r = (lane & 7) + ((lane >> 4) << 3), c = (lane >> 3) & 1;
+        }
+      } else {
+        const int r = (lane & 7) + ((lane >> 4) << 3), c = (lane >> 3) & 1;
 #pragma unroll
-          for (int kd = 0; kd < KD; ++kd) {
-            uint32_t b[4];
-            ldm4(b, sk + r * L::RB + phys<L::CH>(r, 2 * kd + c) * 16);
+        for (int kd = 0; kd < KD; ++kd) {
+          uint32_t b[4];
+          ldm4(b, sk + r * L::RB + phys<L::CH>(r, 2 * kd + c) * 16);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma<PF>(sc[mt][0], qf[mt][kd], b[0], b[1]);
-              mma<PF>(sc[mt][1], qf[mt][kd], b[2], b[3]);
-            }
+          for (int mt = 0; mt < MT; ++mt) {
+            mma<PF>(sc[mt][0], qf[mt][kd], b[0], b[1]);
+            mma<PF>(sc[mt][1], qf[mt][kd], b[2], b[3]);
           }
         }
-        // ---- scores in log2 units, masked
-        float lvs = 0.f, ks = 1.f, inv_vs = 1.f;
+      }
+      // ---- scores in log2 units, masked
+      float lvs[L::GROUPS], inv_vs[L::GROUPS];
+#pragma unroll
+      for (int u = 0; u < L::GROUPS; ++u) {
+        lvs[u] = 0.f;
+        inv_vs[u] = 1.f;
+        float ks = 1.f;
         if constexpr (CT == E4M3) {
           float vs;
           asm volatile("ld.shared.b32 %0, [%1];" : "=f"(ks) : "r"(meta + u * 4) : "memory");
           asm volatile("ld.shared.b32 %0, [%1];" : "=f"(vs) : "r"(meta + 8 + u * 4) : "memory");
-          lvs = __log2f(vs);
-          inv_vs = __fdividef(1.f, vs);
+          lvs[u] = __log2f(vs);
+          inv_vs[u] = __fdividef(1.f, vs);
         }
-        const int ka = k0 + 16 * u;
 #pragma unroll
         for (int ri = 0; ri < 2 * MT; ++ri) {
           const float f = xmul[ri] * ks;
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 2 * u; n < 2 * u + 2; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) sc[ri >> 1][n][2 * (ri & 1) + e] *= f;
         }
-        if constexpr (MOD) {
+      }
+      if constexpr (MOD) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int u = 0; u < L::GROUPS; ++u) {
             uint64_t x[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = f2_pack(sc[mt][i >> 1][2 * (i & 1)], sc[mt][i >> 1][2 * (i & 1) + 1]);
+            for (int i = 0; i < 4; ++i)
+              x[i] = f2_pack(sc[mt][2 * u + (i >> 1)][2 * (i & 1)], sc[mt][2 * u + (i >> 1)][2 * (i & 1) + 1]);
             const bool cap = p.mods.cap_in != 0.f;
             if (cap) tanh2_any(x, p.mods.cap_in);
             const float c = cap ? p.mods.cap_log2 : p.scale_log2;
@@ -333,94 +357,104 @@ __global__ void __launch_bounds__(THREADS) cached_rows_kernel(const CachedParams
             for (int i = 0; i < 4; ++i) {
               float x0, x1;
               f2_unpack(x[i], x0, x1);
-              const int ri = 2 * mt + (i & 1), key = ka + 8 * (i >> 1) + 2 * t;
-              sc[mt][i >> 1][2 * (i & 1)] = fmaf(-slope2[ri], fabsf((float)(rows[ri].place - key)), x0 * c);
-              sc[mt][i >> 1][2 * (i & 1) + 1] = fmaf(-slope2[ri], fabsf((float)(rows[ri].place - key - 1)), x1 * c);
+              const int ri = 2 * mt + (i & 1), n = 2 * u + (i >> 1), key = k0 + 8 * n + 2 * t;
+              sc[mt][n][2 * (i & 1)] = fmaf(-slope2[ri], fabsf((float)(rows[ri].place - key)), x0 * c);
+              sc[mt][n][2 * (i & 1) + 1] = fmaf(-slope2[ri], fabsf((float)(rows[ri].place - key - 1)), x1 * c);
             }
           }
+      }
+      constexpr uint32_t ALL = (1u << L::GROUPS) - 1u;
+      if (!(ok == ALL && k0 + L::KS - 1 <= hi_min && (k0 >= lo_max || k0 + L::KS <= p.first_keys))) {
+#pragma unroll
+        for (int ri = 0; ri < 2 * MT; ++ri)
+#pragma unroll
+          for (int n = 0; n < KT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int key = k0 + 8 * n + 2 * t + e;
+              if (key > rows[ri].hi || (key < rows[ri].lo && key >= p.first_keys) || !((ok >> (n >> 1)) & 1u))
+                sc[ri >> 1][n][2 * (ri & 1) + e] = -INFINITY;
+            }
+      }
+      // ---- the reference
+      bool raise = false;
+      float mx[2 * MT];
+#pragma unroll
+      for (int ri = 0; ri < 2 * MT; ++ri) {
+        const int e = 2 * (ri & 1);
+        mx[ri] = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < L::GROUPS; ++u) {
+          const float(&a)[KT][4] = sc[ri >> 1];
+          mx[ri] = fmaxf(mx[ri], fmaxf(fmaxf(a[2 * u][e], a[2 * u][e + 1]), fmaxf(a[2 * u + 1][e], a[2 * u + 1][e + 1])) + lvs[u]);
         }
-        if (!(ka + 15 <= hi_min && (ka >= lo_max || ka + 15 < p.first_keys))) {
-#pragma unroll
-          for (int ri = 0; ri < 2 * MT; ++ri)
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int key = ka + 8 * n + 2 * t + e;
-                if (key > rows[ri].hi || (key < rows[ri].lo && key >= p.first_keys)) sc[ri >> 1][n][2 * (ri & 1) + e] = -INFINITY;
-              }
-        }
-        // ---- the reference
-        bool raise = false;
-        float mx[2 * MT];
+        raise |= mx[ri] > m[ri] + RAISE;
+      }
+      if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int ri = 0; ri < 2 * MT; ++ri) {
-          const float(&a)[2][4] = sc[ri >> 1];
-          const int e = 2 * (ri & 1);
-          mx[ri] = fmaxf(fmaxf(a[0][e], a[0][e + 1]), fmaxf(a[1][e], a[1][e + 1]));
-          mx[ri] += lvs;
-          raise |= mx[ri] > m[ri] + RAISE;
-        }
-        if (__any_sync(0xffffffffu, raise)) {
+          float x = fmaxf(mx[ri], __shfl_xor_sync(0xffffffffu, mx[ri], 1));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          float fo = 1.f;
+          if (x > m[ri] + RAISE) {
+            fo = ex2_approx(m[ri] - x);  // 0 for the first key
+            l[ri] *= fo;
+            m[ri] = x;
+          }
 #pragma unroll
-          for (int ri = 0; ri < 2 * MT; ++ri) {
-            float x = fmaxf(mx[ri], __shfl_xor_sync(0xffffffffu, mx[ri], 1));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-            float fo = 1.f;
-            if (x > m[ri] + RAISE) {
-              fo = ex2_approx(m[ri] - x);  // 0 for the first key
-              l[ri] *= fo;
-              m[ri] = x;
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              o[ri >> 1][n][2 * (ri & 1)] *= fo;
-              o[ri >> 1][n][2 * (ri & 1) + 1] *= fo;
-            }
+          for (int n = 0; n < NT; ++n) {
+            o[ri >> 1][n][2 * (ri & 1)] *= fo;
+            o[ri >> 1][n][2 * (ri & 1) + 1] *= fo;
           }
         }
-        // ---- P, as A fragments
-        uint32_t pf[MT][4];
+      }
+      // ---- P, as A fragments
+      uint32_t pf[MT][L::GROUPS][4];
 #pragma unroll
-        for (int ri = 0; ri < 2 * MT; ++ri) {
-          const float neg = m[ri] == -INFINITY ? 0.f : BIAS + lvs - m[ri];
+      for (int ri = 0; ri < 2 * MT; ++ri) {
+        const float neg = m[ri] == -INFINITY ? 0.f : BIAS - m[ri];
+#pragma unroll
+        for (int u = 0; u < L::GROUPS; ++u) {
           float sum = 0.f;
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
-            const float x0 = sc[ri >> 1][n][2 * (ri & 1)], x1 = sc[ri >> 1][n][2 * (ri & 1) + 1];
-            const float p0 = ex2_approx(x0 + neg), p1 = ex2_approx(x1 + neg);
+            const float x0 = sc[ri >> 1][2 * u + n][2 * (ri & 1)], x1 = sc[ri >> 1][2 * u + n][2 * (ri & 1) + 1];
+            const float p0 = ex2_approx(x0 + (neg + lvs[u])), p1 = ex2_approx(x1 + (neg + lvs[u]));
             sum += p0 + p1;
-            pf[ri >> 1][(ri & 1) + 2 * n] = pack_io2<PF>(p0, p1);
+            pf[ri >> 1][u][(ri & 1) + 2 * n] = pack_io2<PF>(p0, p1);
           }
-          l[ri] = CT == E4M3 ? fmaf(sum, inv_vs, l[ri]) : l[ri] + sum;
+          l[ri] = CT == E4M3 ? fmaf(sum, inv_vs[u], l[ri]) : l[ri] + sum;
         }
-        // ---- O += P V
+      }
+      // ---- O += P V
+      {
+        const int r = (lane & 7) + (((lane >> 3) & 1) << 3), c = lane >> 4;
         if constexpr (CT == E4M3) {
-          const int r = (lane & 7) + (((lane >> 3) & 1) << 3), c = lane >> 4;
 #pragma unroll
-          for (int cp = 0; cp < DP / 32; ++cp) {
-            uint32_t b[4], ev[4], od[4];
-            ldm4t(b, sv + r * L::RB + phys<L::CH>(r, 2 * cp + c) * 16);
+          for (int cp = 0; cp < DP / 32; ++cp)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) codes_f16(__byte_perm(b[i], 0u, 0x3120), ev[i], od[i]);
+            for (int u = 0; u < L::GROUPS; ++u) {
+              uint32_t b[4], ev[4], od[4];
+              ldm4t(b, sv + (16 * u + r) * L::RB + phys<L::CH>(16 * u + r, 2 * cp + c) * 16);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              mma<true>(o[mt][4 * cp], pf[mt], ev[0], ev[1]);
-              mma<true>(o[mt][4 * cp + 1], pf[mt], od[0], od[1]);
-              mma<true>(o[mt][4 * cp + 2], pf[mt], ev[2], ev[3]);
-              mma<true>(o[mt][4 * cp + 3], pf[mt], od[2], od[3]);
+              for (int i = 0; i < 4; ++i) codes_f16(__byte_perm(b[i], 0u, 0x3120), ev[i], od[i]);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                mma<true>(o[mt][4 * cp], pf[mt][u], ev[0], ev[1]);
+                mma<true>(o[mt][4 * cp + 1], pf[mt][u], od[0], od[1]);
+                mma<true>(o[mt][4 * cp + 2], pf[mt][u], ev[2], ev[3]);
+                mma<true>(o[mt][4 * cp + 3], pf[mt][u], od[2], od[3]);
+              }
             }
-          }
         } else {
-          const int r = (lane & 7) + (((lane >> 3) & 1) << 3), c = lane >> 4;
 #pragma unroll
           for (int dn = 0; dn < KD; ++dn) {
             uint32_t b[4];
             ldm4t(b, sv + r * L::RB + phys<L::CH>(r, 2 * dn + c) * 16);
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-              mma<PF>(o[mt][2 * dn], pf[mt], b[0], b[1]);
-              mma<PF>(o[mt][2 * dn + 1], pf[mt], b[2], b[3]);
+              mma<PF>(o[mt][2 * dn], pf[mt][0], b[0], b[1]);
+              mma<PF>(o[mt][2 * dn + 1], pf[mt][0], b[2], b[3]);
             }
           }
         }

@@ -6,79 +6,76 @@ namespace sdpa {
 
 namespace {
 
-// Block (x, y): rows 4 y .. 4 y + 3 of a tile, one a warp. x < n_ctas - 1: the segment that share
-// x + 1 begins in the middle of, if it is the first to do so; its parts weighed by their sums,
-// in the shares' order. Past that, entry x - (n_ctas - 1): the rows of one that visits no unit.
-template <bool IOF>
+// Block (x, y): of the segment that share x + 1 begins in the middle of, if it is the first to do so (the
+// share notes it), the parts weighed by their sums in the shares' order. WIDE: row y, the parts dealt out to
+// the block's four warps (few rows, which may be cut into very many parts); else rows 4 y .. 4 y + 3, one a
+// warp (many rows, in a few parts).
+template <bool IOF, bool WIDE>
 __global__ void __launch_bounds__(128) cached_merge_kernel(const CachedParams p) {
-  __shared__ CachedStart sh_start;
-  __shared__ long long sh_sum[4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y * 4 + warp;
-  uint16_t* const out = static_cast<uint16_t*>(p.o);
-  if ((int)blockIdx.x >= p.n_ctas - 1) {
-    pdl_wait_prior_grid();
-    const int e = blockIdx.x - (p.n_ctas - 1), b = e / p.n_rt, r = (e % p.n_rt) * p.tile_rows + row;
-    if (r >= p.R || cached_bounds(p, b, e % p.n_rt).n > 0) return;
-    for (int h = 0; h < p.c.Hkv; ++h) {
-      const long long orow = ((long long)b * p.c.Hkv + h) * p.R + r;
-      if (lane * 4 < p.D) *reinterpret_cast<uint2*>(out + orow * p.D + lane * 4) = make_uint2(0u, 0u);
-      if (lane == 0) p.lse[orow] = p.sink ? p.sink[h * p.G + r / p.Sq] : -INFINITY;
-    }
-    return;
-  }
-  const int cta = blockIdx.x + 1;
-  const CachedStart st = cached_start<128>(p, &sh_start, sh_sum, false,
-                                           [&](long long T) { return share_begin(T, p.n_ctas, cta); });
+  __shared__ float4 sh_y[WIDE ? 4 : 1][32];
+  __shared__ float sh_m[4], sh_l[4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = WIDE ? blockIdx.y : blockIdx.y * 4 + warp;
   pdl_wait_prior_grid();
-  if (st.e < 0) return;  // nothing from here on
-  const int b = st.e / p.n_rt, rt = st.e % p.n_rt;
-  const int n = cached_bounds(p, b, rt).n;
-  const int kvh = (int)((st.at - st.te) / n);
-  const long long begin = st.te + (long long)kvh * n;
-  if (st.at == begin || share_begin(st.T, p.n_ctas, cta - 1) > begin) return;  // not cut here, or cut before
-  const int r = rt * p.tile_rows + row;
+  const int4 cut = p.cuts[blockIdx.x + 1];
+  if (cut.x < 0) return;
+  const int e = cut.x / p.c.Hkv, kvh = cut.x % p.c.Hkv, b = e / p.n_rt, r = (e % p.n_rt) * p.tile_rows + row;
   if (r >= p.R) return;
-  // The segment's shares: cta - 1 (or, where that one is empty, the one that has its first unit) .. last.
-  const int first = share_of(st.T, p.n_ctas, begin), last = share_of(st.T, p.n_ctas, begin + n - 1);
+  const int n = cut.z - cut.y + 1, step = WIDE ? 4 : 1, c = lane * 4;
   auto part = [&](int i) {  // the first share left its part in slot 1: it does not finish the segment
-    return ((long long)i * 2 + (i == first ? 1 : 0)) * p.tile_rows + row;
+    return ((long long)(cut.y + i) * 2 + (i == 0 ? 1 : 0)) * p.tile_rows + row;
   };
-  // (shares between first and last that hold no unit: none, as T >= n_ctas wherever a segment is cut twice or more,
-  // and a share without units lies before a unit's begin)
-  float M = -INFINITY;
-  for (int i = first + lane; i <= last; i += 32)
-    if (share_begin(st.T, p.n_ctas, i) < share_begin(st.T, p.n_ctas, i + 1)) M = fmaxf(M, p.part_lse[part(i)]);
+  float m = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int i0 = WIDE ? warp : 0; i0 < n; i0 += 8 * step) {
+    float lse[8];
+    float4 v[8];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float sum = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-  const int c = lane * 4;
-  if (M != -INFINITY) {
-    for (int i0 = first; i0 <= last; i0 += 32) {
-      const int mine = i0 + lane;
-      float wgt = 0.f;
-      if (mine <= last && share_begin(st.T, p.n_ctas, mine) < share_begin(st.T, p.n_ctas, mine + 1))
-        wgt = ex2_approx(p.part_lse[part(mine)] - M);
-      sum += wgt;
-      const int here = min(32, last - i0 + 1);
-#pragma unroll 4
-      for (int k = 0; k < here; ++k) {
-        const float f = __shfl_sync(0xffffffffu, wgt, k);
-        if (c < p.D && f != 0.f) {
-          const float4 v = *reinterpret_cast<const float4*>(p.part_o + part(i0 + k) * p.D + c);
-          y[0] = fmaf(f, v.x, y[0]), y[1] = fmaf(f, v.y, y[1]), y[2] = fmaf(f, v.z, y[2]), y[3] = fmaf(f, v.w, y[3]);
-        }
+    for (int k = 0; k < 8; ++k) {  // eight parts' loads at once
+      const int i = i0 + k * step;
+      lse[k] = -INFINITY;
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        lse[k] = p.part_lse[part(i)];
+        if (c < p.D) v[k] = *reinterpret_cast<const float4*>(p.part_o + part(i) * p.D + c);
       }
     }
+    float mx = m;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    for (int k = 0; k < 8; ++k) mx = fmaxf(mx, lse[k]);
+    if (mx == -INFINITY) continue;
+    const float a = ex2_approx(m - mx);
+    l *= a;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) y[q] *= a;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float f = ex2_approx(lse[k] - mx);
+      l += f;
+      y[0] = fmaf(f, v[k].x, y[0]), y[1] = fmaf(f, v[k].y, y[1]), y[2] = fmaf(f, v[k].z, y[2]), y[3] = fmaf(f, v[k].w, y[3]);
+    }
+    m = mx;
+  }
+  if constexpr (WIDE) {
+    sh_y[warp][lane] = make_float4(y[0], y[1], y[2], y[3]);
+    if (lane == 0) sh_m[warp] = m, sh_l[warp] = l;
+    __syncthreads();
+    if (warp != 0) return;
+    m = fmaxf(fmaxf(sh_m[0], sh_m[1]), fmaxf(sh_m[2], sh_m[3]));
+    l = y[0] = y[1] = y[2] = y[3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = sh_m[k] == -INFINITY ? 0.f : ex2_approx(sh_m[k] - m);
+      const float4 v = sh_y[k][lane];
+      l = fmaf(f, sh_l[k], l);
+      y[0] = fmaf(f, v.x, y[0]), y[1] = fmaf(f, v.y, y[1]), y[2] = fmaf(f, v.z, y[2]), y[3] = fmaf(f, v.w, y[3]);
+    }
   }
   float fs;
-  const float lse2 = M == -INFINITY ? -INFINITY : M + __log2f(sum);
+  const float lse2 = m == -INFINITY ? -INFINITY : m + __log2f(l);
   const float all = cached_with_sink(p, kvh * p.G + r / p.Sq, lse2, fs);
-  const float f = M == -INFINITY ? 0.f : fs / sum;
+  const float f = m == -INFINITY ? 0.f : fs / l;
   const long long orow = ((long long)b * p.c.Hkv + kvh) * p.R + r;
   if (c < p.D)
-    *reinterpret_cast<uint2*>(out + orow * p.D + c) =
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + orow * p.D + c) =
         make_uint2(pack_io2<IOF>(y[0] * f, y[1] * f), pack_io2<IOF>(y[2] * f, y[3] * f));
   if (lane == 0) p.lse[orow] = all * 0.6931471805599453f;
 }
@@ -96,9 +93,13 @@ cudaError_t cached_rows_16_setup() {
 }
 
 cudaError_t launch_cached_merge(const CachedParams& p, cudaStream_t s) {
-  const dim3 grid((unsigned)(p.n_ctas - 1 + p.B * p.n_rt), (unsigned)ceil_div(p.R < p.tile_rows ? p.R : p.tile_rows, 4));
-  return p.f16 ? launch_kernel(cached_merge_kernel<true>, grid, dim3(128), 0, s, true, p)
-               : launch_kernel(cached_merge_kernel<false>, grid, dim3(128), 0, s, true, p);
+  if (p.n_ctas < 2) return cudaSuccess;  // one share: nothing is cut
+  const int rows = p.R < p.tile_rows ? p.R : p.tile_rows;
+  const bool wide = p.tile_rows <= 32;
+  const dim3 grid((unsigned)(p.n_ctas - 1), (unsigned)(wide ? rows : ceil_div(rows, 4)));
+  auto* kernel = p.f16 ? (wide ? cached_merge_kernel<true, true> : cached_merge_kernel<true, false>)
+                       : (wide ? cached_merge_kernel<false, true> : cached_merge_kernel<false, false>);
+  return launch_kernel(kernel, grid, dim3(128), 0, s, true, p);
 }
 
 }  // namespace sdpa

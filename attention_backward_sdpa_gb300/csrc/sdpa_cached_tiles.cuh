@@ -111,11 +111,11 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   // (its shared memory: the place that the halves exchange their sums in later)
-  const CachedStart st0 = cached_start<THREADS>(
-      p, reinterpret_cast<CachedStart*>(smem + L::OFF_XCH), reinterpret_cast<long long*>(smem + L::OFF_XCH + 64),
-      blockIdx.x == 0, [&](long long T) { return share_begin(T, p.n_ctas, blockIdx.x); });
+  const CachedStart st0 = cached_start<THREADS>(p, reinterpret_cast<CachedStart*>(smem + L::OFF_XCH),
+                                                reinterpret_cast<long long*>(smem + L::OFF_XCH + 64));
   pdl_launch_dependents();  // (the merge waits for this grid before it reads the parts)
-  CachedWalk walk{st0.at, share_begin(st0.T, p.n_ctas, blockIdx.x + 1), st0.te, st0.e};
+  cached_empty_rows<THREADS>(p);
+  CachedWalk walk{st0.begin, st0.end, st0.te, st0.e};
   if (walk.u >= walk.end) return;
   if (tid == 0) {
     *abort_flag = 0;

@@ -222,6 +222,7 @@ __device__ __forceinline__ uint4 codes16(const float (&x)[16], float up, float s
 template <bool F16>
 __device__ __forceinline__ void append_page(const KvAppendArgs& a, const AppendPlan& pl, int block, float* sx) {
   __shared__ float warp_max[THREADS / 32];
+  __shared__ uint64_t turns[64];  // D <= 128
   const KvCacheRef& c = a.c;
   const int tid = threadIdx.x, D = c.D;
   const int side = block & 1;
@@ -248,6 +249,7 @@ __device__ __forceinline__ void append_page(const KvAppendArgs& a, const AppendP
   float amax = 0.f;
   const bool turned = !side && a.rot > 0;
   const int rot = turned ? a.rot : 0;
+  if (tid < rot / 2) turns[tid] = turn_fraction(a.freq[tid]);
   for (int i = tid; i < n * pieces; i += THREADS) {
     const int r = i / pieces, p = i % pieces;
     float f[8];
@@ -265,7 +267,7 @@ __device__ __forceinline__ void append_page(const KvAppendArgs& a, const AppendP
     for (int i = tid; i < n * half; i += THREADS) {
       const int r = i / half, pair = i % half;
       float sn, cs;
-      angle_sin_cos_near(turn_fraction(a.freq[pair]), row_position(a, b, t0 + r, start, axis_of(a, pair)), sn, cs);
+      angle_sin_cos_near(turns[pair], row_position(a, b, t0 + r, start, axis_of(a, pair)), sn, cs);
       sn *= a.mult;
       cs *= a.mult;
       float* p0 = sx + r * D + (a.interleaved ? 2 * pair : pair);
