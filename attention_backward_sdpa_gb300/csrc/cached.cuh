@@ -11,14 +11,14 @@
 //
 // Schedule. A segment is one (batch row, row tile, key/value head); it visits n units of
 // `tk` keys: those that some of its rows sees, the tiles of the first F keys and then those of the
-// window, so nothing between them is read. All segments' units in a row are cut into equal shares,
-// one a CTA: lengths as uneven as they come leave no SM idle, and one long sequence is shared by
-// all. A segment inside one share is written at once; of one that is cut every share leaves
+// window, so nothing between them is read. All segments' units in a row are cut into equal shares, one
+// a CTA (many rows) or one a warp (few rows): lengths as uneven as they come leave no SM idle, and one long
+// sequence is shared by all. A segment inside one share is written at once; of one that is cut every share leaves
 // a part (O / l in fp32, and log2 of its sum) in the workspace, two at most: of the segment that
-// it begins in the middle of (slot 0), and of the one that it does not finish (slot 1). The first share to
-// begin in the middle of a segment also notes which shares have parts of it; the merge kernel, a
-// block a share, weighs them in their order, so that results do not depend on timing. (A merge that found the
-// cut segments by the schedule again took 10 to 28 us, most of it in scans and 64-bit divisions.)
+// it begins in the middle of (slot 0), and of the one that it does not finish (slot 1). A note says which
+// shares have parts of a segment, and the merge kernel weighs them in their order, so that results do not
+// depend on timing. (A merge that found the cut segments by the schedule again took 10 to 28 us, most of
+// it in scans and 64-bit divisions.)
 #pragma once
 
 #include "common.cuh"
@@ -39,10 +39,12 @@ struct CachedParams {
   const float* sink;          // or null
   ScoreMods mods;             // cap and slopes
   int tile_rows, n_rt, tk;    // rows of a tile, tiles of a key/value head, keys of a unit
-  int n_ctas;
-  float* part_o;              // [n_ctas][2][tile_rows][D]
-  float* part_lse;            // [n_ctas][2][tile_rows], log2 units
-  int4* cuts;                 // [n_ctas] {segment (entry * Hkv + head), first share, last share, 0} or {-1, ..}
+  int n_ctas, n_shares, share_units;  // shares at most, and the fewest units of one past 512 of them
+  int part_rows;              // rows of a part: those of a tile, or R
+  float* part_o;              // [n_shares][2][part_rows][D]
+  float* part_lse;            // [n_shares][2][part_rows], log2 units
+  int4* cuts;                 // {segment (entry * Hkv + head), first share, last share, 0} or {-1, ..}: many rows,
+                              // by the first share to begin in the middle of it; few rows, by segment
   int* status;
 };
 
@@ -73,17 +75,21 @@ __device__ __forceinline__ CachedBounds cached_bounds(const CachedParams& p, int
 __device__ __forceinline__ int cached_tile(const CachedBounds& s, int j) { return j < s.nf ? j : s.kt + (j - s.nf); }
 
 // Shares of T units, each of one unit at least; first unit of share i of n, and the share that has unit t.
-__device__ __forceinline__ int shares_of(const CachedParams& p, long long T) { return (int)min((long long)p.n_ctas, T); }
+__device__ __forceinline__ int shares_of(const CachedParams& p, long long T) {
+  return (int)min((long long)p.n_shares, max(T / p.share_units, min(T, 512ll)));
+}
 __device__ __forceinline__ long long share_begin(long long T, int n, int i) { return T * i / n; }
 __device__ __forceinline__ int share_of(long long T, int n, long long t) { return (int)(((t + 1) * n + T - 1) / T) - 1; }
 
-// Where this CTA's share begins: its first unit and the one past its last, its entry e (b * n_rt + rt),
-// and that entry's first unit. One call by every thread of the block; `sh` and `warp_sum` are shared memory.
+// Where a share begins: its first unit and the one past its last, its entry e (b * n_rt + rt),
+// and that entry's first unit. One call by every thread of the block; sh[W] and `warp_sum` are shared memory.
+// W 1: the CTA is a share (and notes the segment that it cuts); else each of its W warps is one.
 struct CachedStart {
   long long begin, end, te;
-  int e;
+  int e, n;  // n: shares
+  long long T;
 };
-template <int THREADS>
+template <int THREADS, int W>
 __device__ __forceinline__ CachedStart cached_start(const CachedParams& p, CachedStart* sh, long long* warp_sum) {
   const bool report = blockIdx.x == 0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -103,7 +109,7 @@ __device__ __forceinline__ CachedStart cached_start(const CachedParams& p, Cache
     if (lane >= o) incl += u;
   }
   if (lane == 31) warp_sum[warp] = incl;
-  if (tid == 0) sh->e = -1;
+  if (tid < W) sh[tid].e = -1;
   __syncthreads();
   long long T = 0;
 #pragma unroll
@@ -111,38 +117,48 @@ __device__ __forceinline__ CachedStart cached_start(const CachedParams& p, Cache
     if (w == warp) incl += T;
     T += warp_sum[w];
   }
-  const int n = shares_of(p, T), i = blockIdx.x;
-  const long long begin = i < n ? share_begin(T, n, i) : T, end = i < n ? share_begin(T, n, i + 1) : T;
-  long long te = incl - sum;
-  if (begin >= te && begin < incl) {
-    for (int e = e0; e < e1; ++e) {
-      const long long k = (long long)cached_bounds(p, e / p.n_rt, e % p.n_rt).n * p.c.Hkv;
-      if (begin < te + k) {
-        sh->e = e;
-        sh->te = te;
-        // A segment that the share begins in the middle of, and the share before does not.
-        const int m = (int)(k / p.c.Hkv), h = (int)((begin - te) / m);
-        const long long first = te + (long long)h * m;
-        int4 cut = make_int4(-1, 0, 0, 0);
-        if (begin > first && share_begin(T, n, i - 1) <= first)
-          cut = make_int4(e * p.c.Hkv + h, i - 1, share_of(T, n, first + m - 1), 0);
-        p.cuts[i] = cut;
-        break;
+  const int n = shares_of(p, T);
+  const long long te0 = incl - sum;
+#pragma unroll 1
+  for (int w = 0; w < W; ++w) {
+    const int i = blockIdx.x * W + w;
+    const long long begin = i < n ? share_begin(T, n, i) : T;
+    if (begin >= te0 && begin < incl) {
+      long long te = te0;
+      for (int e = e0; e < e1; ++e) {
+        const long long k = (long long)cached_bounds(p, e / p.n_rt, e % p.n_rt).n * p.c.Hkv;
+        if (begin < te + k) {
+          sh[w].e = e;
+          sh[w].te = te;
+          if constexpr (W == 1) {
+            // A segment that the share begins in the middle of, and the share before does not.
+            const int m = (int)(k / p.c.Hkv), h = (int)((begin - te) / m);
+            const long long first = te + (long long)h * m;
+            int4 cut = make_int4(-1, 0, 0, 0);
+            if (begin > first && share_begin(T, n, i - 1) <= first)
+              cut = make_int4(e * p.c.Hkv + h, i - 1, share_of(T, n, first + m - 1), 0);
+            p.cuts[i] = cut;
+          }
+          break;
+        }
+        te += k;
       }
-      te += k;
     }
+    if (W == 1 && begin >= T && tid == 0) p.cuts[i] = make_int4(-1, 0, 0, 0);
   }
-  if (begin >= T && tid == 0) p.cuts[i] = make_int4(-1, 0, 0, 0);
   __syncthreads();
-  return CachedStart{begin, end, sh->te, sh->e};
+  const int w = W == 1 ? 0 : warp, i = blockIdx.x * W + w;
+  return CachedStart{i < n ? share_begin(T, n, i) : T, i < n ? share_begin(T, n, i + 1) : T, sh[w].te, sh[w].e, n, T};
 }
 
 // Rows that see no key: entries that visit no unit, each written by one of the CTAs.
-template <int THREADS>
+template <int THREADS, bool NOTE>
 __device__ __forceinline__ void cached_empty_rows(const CachedParams& p) {
   for (int e = blockIdx.x; e < p.B * p.n_rt; e += gridDim.x) {
     const int b = e / p.n_rt, rt = e % p.n_rt;
     if (cached_bounds(p, b, rt).n > 0) continue;
+    if constexpr (NOTE)
+      for (int h = threadIdx.x; h < p.c.Hkv; h += THREADS) p.cuts[e * p.c.Hkv + h] = make_int4(-1, 0, 0, 0);
     const int r0 = rt * p.tile_rows, rows = min(p.tile_rows, p.R - r0), pieces = p.D / 8;
     for (int i = threadIdx.x; i < p.c.Hkv * rows * pieces; i += THREADS) {
       const int c = i % pieces, r = r0 + i / pieces % rows, h = i / pieces / rows;
@@ -245,9 +261,8 @@ cudaError_t cached_tiles_16_setup();
 cudaError_t cached_tiles_8_setup();
 cudaError_t launch_cached_merge(const CachedParams& p, cudaStream_t s);
 
-// Keys of a unit of the few-rows kernel with 16 mt rows: four warps of 16 keys, or of 32 in 8 bits
-// where the registers allow it.
-__host__ __device__ constexpr int cached_rows_tk(bool f8, int mt) { return f8 && mt == 1 ? 128 : 64; }
+// Keys of a unit of the few-rows kernel with 16 mt rows, a warp's piece.
+__host__ __device__ constexpr int cached_rows_tk(bool f8, int mt) { return f8 && mt == 1 ? 32 : 16; }
 // CTAs of it that an SM holds.
 __host__ __device__ constexpr int cached_rows_ctas(int mt) { return mt == 1 ? 3 : 2; }
 

@@ -72,7 +72,7 @@ size_t cache_bytes(const KvCacheRef& c) { return (size_t)c.n_pages * c.Hkv * c.p
 // How a call over the cache is cut, from its sizes alone (not from the device it runs on, so that
 // neither the workspace nor any result depends on that).
 struct CachedPlan {
-  int tile_rows, n_rt, tk, n_ctas, mt;
+  int tile_rows, n_rt, tk, n_ctas, n_shares, part_rows, mt;
   size_t o_bytes, lse_bytes, bytes;
 };
 constexpr int SHARE_SMS = 152;  // SMs of a GB300
@@ -86,12 +86,17 @@ CachedPlan cached_plan(long long B, int H_q, int H_kv, int S_q, int D, bool f8, 
   c.tk = c.mt ? cached_rows_tk(f8, c.mt) : 128;
   c.n_rt = (int)((R + c.tile_rows - 1) / c.tile_rows);
   // As many CTAs as the device holds at once (by their shared memory), fewer where there are
-  // not that many units.
-  const long long units = B * c.n_rt * H_kv * ((max_keys + c.tk - 1) / c.tk), most = c.mt ? cached_rows_ctas(c.mt) * SHARE_SMS : SHARE_SMS;
-  c.n_ctas = (int)(units < most ? units : most);
-  c.o_bytes = align256((size_t)c.n_ctas * 2 * c.tile_rows * D * sizeof(float));
-  c.lse_bytes = align256((size_t)c.n_ctas * 2 * c.tile_rows * sizeof(float));
-  c.bytes = c.o_bytes + c.lse_bytes + align256((size_t)c.n_ctas * sizeof(int4));
+  // not that many units. A share is a CTA, or one of four warps of it.
+  const long long units = B * c.n_rt * H_kv * ((max_keys + c.tk - 1) / c.tk), warps = c.mt ? 4 : 1;
+  const long long ctas = (units + warps - 1) / warps, most = c.mt ? cached_rows_ctas(c.mt) * SHARE_SMS : SHARE_SMS;
+  c.n_ctas = (int)(ctas < most ? ctas : most);
+  c.n_shares = (int)(c.n_ctas * warps);
+  c.part_rows = R < c.tile_rows ? (int)R : c.tile_rows;
+  const size_t parts = (size_t)c.n_shares * 2 * c.part_rows;
+  const size_t notes = c.mt ? (size_t)(B * c.n_rt * H_kv) : (size_t)c.n_shares;
+  c.o_bytes = align256(parts * D * sizeof(float));
+  c.lse_bytes = align256(parts * sizeof(float));
+  c.bytes = c.o_bytes + c.lse_bytes + align256(notes * sizeof(int4));
   return c;
 }
 
@@ -170,6 +175,9 @@ int sdpa_fwd_cached(int io_dtype, int cache_dtype, const void* q, const void* k_
   p.n_rt = plan.n_rt;
   p.tk = plan.tk;
   p.n_ctas = plan.n_ctas;
+  p.n_shares = plan.n_shares;
+  p.share_units = plan.mt ? 8 : 1;
+  p.part_rows = plan.part_rows;
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.o_bytes);
   p.cuts = reinterpret_cast<int4*>(static_cast<char*>(workspace) + plan.o_bytes + plan.lse_bytes);

@@ -4,10 +4,10 @@
 // of bytes for 4 D flops a row. So the work is to keep enough reads in flight and everything
 // else out of their way.
 //
-//   - Warps share nothing while they run. A unit's keys are four pieces of 16 (or, in 8 bits with 16 rows, 32), one a warp, and
-//     each warp has a ring of stages of its own that it fills by 16-byte asynchronous copies and waits for
-//     by itself: no barrier of the CTA in the loop. Pieces that no row sees are neither read nor
-//     computed; rows of a piece that none sees are filled with zeros, so that what a recycled page
+//   - A warp is a share of its own and has nothing to do with the others: it walks its share's units, pieces of 16
+//     keys (in 8 bits with 16 rows, 32), through a ring of stages that it fills by 16-byte asynchronous
+//     copies and waits for by itself.
+//     Rows of a piece that no query sees are filled with zeros, so that what a recycled page
 //     holds never meets a product.
 //   - Both products on m16n8k16 with the softmax in registers: 16 rows are the most that such a call
 //     has as a rule (G heads, one token), and 16 rows of P against 16 keys of V take 2 clocks where the
@@ -38,22 +38,19 @@ enum : int { BF16 = 0, F16 = 1, E4M3 = 2 };
 template <int CT, int DP, int MT>
 struct Layout {
   static constexpr int GROUPS = CT == E4M3 && MT == 1 ? 2 : 1;  // of 16 keys
-  static constexpr int KS = 16 * GROUPS;             // keys of a warp's piece
-  static constexpr int TK = KS * WARPS;
+  static constexpr int KS = 16 * GROUPS;                // keys of a piece
   static constexpr int RB = DP * (CT == E4M3 ? 1 : 2);  // bytes of a row
   static constexpr int CH = RB / 16;
   static constexpr int SIDE = KS * RB;                  // keys or values of a piece
   static constexpr int STAGE = 2 * SIDE;
   // Three CTAs an SM with 16 rows, two with 32, by their registers; what shared memory that leaves is stages.
   static constexpr int CTAS = cached_rows_ctas(MT);
-  static constexpr int NST = (CTAS == 3 ? 2 : 3) * 8192 / STAGE;
+  static constexpr int NST_FIT = (CTAS == 3 ? 2 : 3) * 8192 / STAGE, NST = NST_FIT < 6 ? NST_FIT : 6;
   static constexpr int META = 32;                       // {ks, ks, vs, vs, page bits}
-  static constexpr int RING = NST * (STAGE + META);
   static constexpr int TR = 16 * MT;
-  static constexpr int OROW = DP + 4;                   // floats of an O row in the exchange
-  static constexpr int XCH = WARPS * TR * (OROW + 2) * 4;
-  static constexpr int BYTES = WARPS * RING > XCH ? WARPS * RING : XCH;
-  static_assert(NST >= 2 && TK == cached_rows_tk(CT == E4M3, MT), "");
+  static constexpr int RING = NST * (STAGE + META);     // of a warp
+  static constexpr int BYTES = WARPS * RING;
+  static_assert(NST >= 2 && KS == cached_rows_tk(CT == E4M3, MT), "");
 };
 
 // 16-byte piece c of row r: rows of a piece lie on different banks for the eight rows of a
@@ -112,58 +109,49 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
   constexpr float BIAS = PF ? 6.f : 0.f;
   constexpr int KD = DP / 16, NT = DP / 8, ESZ = CT == E4M3 ? 1 : 2;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ CachedStart sh_start;
+  __shared__ CachedStart sh_start[WARPS];
   __shared__ long long sh_sum[WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const CachedStart st = cached_start<THREADS>(p, &sh_start, sh_sum);
+  if (p.D < DP)  // columns past D are never copied
+    for (int i = tid; i < L::BYTES / 16; i += THREADS) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+  const CachedStart st = cached_start<THREADS, WARPS>(p, sh_start, sh_sum);
   pdl_launch_dependents();  // (the merge waits for this grid before it reads the parts)
-  cached_empty_rows<THREADS>(p);
-  CachedWalk walk{st.begin, st.end, st.te, st.e};
-  if (walk.u >= walk.end) return;
+  cached_empty_rows<THREADS, true>(p);
+  if (st.begin >= st.end) return;
+  const int share = blockIdx.x * WARPS + warp;
   const uint32_t ring = smem_u32(smem) + warp * L::RING;
-  // Columns past D are never copied: zeros, once (and again after the exchange has used the place).
-  auto clear = [&] {
-    if (p.D == DP) return;
-    for (int i = tid; i < WARPS * L::RING / 16; i += THREADS) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-  };
-  clear();
   const int copy_row = lane / L::CH, copy_c = lane % L::CH;
   const bool copy_in = copy_c * 16 < p.D * ESZ;
   const int row_bytes = p.D * ESZ, pass_bytes = (32 / L::CH) * row_bytes;
+
+  CachedWalk walk{st.begin, st.end, st.te, st.e};
   CachedPortion w;
   while (walk.next(p, w)) {
     const CachedBounds& s = w.s;
     const int r0 = w.rt * L::TR;
-    // Piece of unit j: its first key, and which of its groups of 16 keys some row sees.
-    auto piece = [&](int j, int& k0) -> uint32_t {
-      k0 = cached_tile(s, j) * L::TK + warp * L::KS;
-      uint32_t seen = 0;
-#pragma unroll
-      for (int u = 0; u < L::GROUPS; ++u) {
-        const int a = k0 + 16 * u;
-        if (a < s.k_hi && (a + 15 >= s.k_lo || a < p.first_keys)) seen |= 1u << u;
-      }
-      return seen;
-    };
+    if (w.j0 == 0 && lane == 0) {  // the segment's first share
+      int4 cut = make_int4(-1, 0, 0, 0);
+      const int seg = (w.b * p.n_rt + w.rt) * p.c.Hkv + w.kvh;
+      if (w.slot >= 0) cut = make_int4(seg, share, share_of(st.T, st.n, walk.u - w.j1 + s.n - 1), 0);
+      p.cuts[seg] = cut;
+    }
+    auto group_seen = [&](int a) { return a < s.k_hi && (a + 15 >= s.k_lo || a < p.first_keys); };
     int next_entry[L::GROUPS];
     auto find_pages = [&](int j) {
-      int k0;
-      const uint32_t seen = j < w.j1 ? piece(j, k0) : 0u;
+      if (j >= w.j1) return;
+      const int k0 = cached_tile(s, j) * L::KS;
 #pragma unroll
       for (int u = 0; u < L::GROUPS; ++u)
-        if ((seen >> u) & 1u) next_entry[u] = cached_lookup(p, w.b, k0 + 16 * u);
+        if (group_seen(k0 + 16 * u)) next_entry[u] = cached_lookup(p, w.b, k0 + 16 * u);
     };
-    auto issue = [&](int j) {
-      const int stage = j % L::NST;
-      const uint32_t to = ring + stage * (L::STAGE + L::META), meta = to + L::STAGE;
-      int k0;
-      const uint32_t seen = j < w.j1 ? piece(j, k0) : 0u;
-      if (seen != 0u) {
+    auto issue = [&](int j, int stage) {
+      if (j < w.j1) {
+        const uint32_t to = ring + stage * (L::STAGE + L::META), meta = to + L::STAGE;
+        const int k0 = cached_tile(s, j) * L::KS;
         uint32_t ok = 0;
 #pragma unroll
         for (int u = 0; u < L::GROUPS; ++u) {
-          const int a = k0 + 16 * u, page = (seen >> u) & 1u ? cached_page(p, next_entry[u]) : -1;
+          const int a = k0 + 16 * u, page = group_seen(a) ? cached_page(p, next_entry[u]) : -1;
           if (page >= 0) ok |= 1u << u;
           const bool all = page >= 0 && a + 16 <= s.k_hi && (a >= s.k_lo || a + 16 <= p.first_keys);
           const long long head = (long long)max(page, 0) * p.c.Hkv + w.kvh;
@@ -207,8 +195,8 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
       find_pages(j + 1);
     };
     find_pages(w.j0);
-#pragma unroll
-    for (int i = 0; i < L::NST - 1; ++i) issue(w.j0 + i);
+#pragma unroll 1
+    for (int i = 0; i < L::NST - 1; ++i) issue(w.j0 + i, i);
 
     // Queries as A fragments, and the rows' state. Thread rows: 16 m + g and 16 m + g + 8.
     uint32_t qf[MT][KD][4];
@@ -268,17 +256,18 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
 
+    int stage = 0;
 #pragma unroll 1
     for (int j = w.j0; j < w.j1; ++j) {
       copies_wait<L::NST - 2>();
       __syncwarp();  // every lane's copies of this stage have landed, and all are done with the one before
-      issue(j + L::NST - 1);
-      int k0;
-      const uint32_t seen = piece(j, k0);
-      if (seen == 0u) continue;
-      const uint32_t at = ring + (j % L::NST) * (L::STAGE + L::META), meta = at + L::STAGE;
+      issue(j + L::NST - 1, stage == 0 ? L::NST - 1 : stage - 1);
+      const uint32_t at = ring + stage * (L::STAGE + L::META), meta = at + L::STAGE;
+      if (++stage == L::NST) stage = 0;
+      const int k0 = cached_tile(s, j) * L::KS;
       uint32_t ok;
       asm volatile("ld.shared.b32 %0, [%1];" : "=r"(ok) : "r"(meta + 16) : "memory");
+      if (ok == 0u) continue;
       constexpr int KT = 2 * L::GROUPS;  // tiles of 8 keys
       const uint32_t sk = at, sv = at + L::SIDE;
       // ---- S = Q K^T: element [mt][n][e]: row g + 8 (e >> 1), key 8 n + 2 t + (e & 1)
@@ -461,87 +450,51 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
       }
     }
 
-    // ---- the four warps' states together, through the ring's place
+    // ---- the portion's rows as results, or as a part
     copies_wait<0>();
-    __syncthreads();
-    float* const xo = reinterpret_cast<float*>(smem);  // [WARPS][TR][OROW]
-    float* const xm = xo + WARPS * L::TR * L::OROW;    // [WARPS][TR] m, then l
-    float* const xl = xm + WARPS * L::TR;
+    __syncwarp();  // (and the ring is free for the next portion)
+    const int b = w.b, kvh = w.kvh, slot = w.slot;
 #pragma unroll
     for (int ri = 0; ri < 2 * MT; ++ri) {
-      float x = l[ri] + __shfl_xor_sync(0xffffffffu, l[ri], 1);
-      x += __shfl_xor_sync(0xffffffffu, x, 2);
-      if (t == 0) {
-        const int at = warp * L::TR + 16 * (ri >> 1) + g + 8 * (ri & 1);
-        xm[at] = m[ri];
-        xl[at] = x;
+      float lt = l[ri] + __shfl_xor_sync(0xffffffffu, l[ri], 1);
+      lt += __shfl_xor_sync(0xffffffffu, lt, 2);
+      const int row = 16 * (ri >> 1) + g + 8 * (ri & 1), r = r0 + row;
+      if (r >= p.R) continue;
+      const bool none = m[ri] == -INFINITY;
+      float f = none ? 0.f : 1.f / lt;
+      const float lse2 = none ? -INFINITY : m[ri] - BIAS + __log2f(lt);
+      const long long part = ((long long)share * 2 + slot) * p.part_rows + row;
+      const long long orow = ((long long)b * p.c.Hkv + kvh) * p.R + r;
+      if (slot >= 0) {
+        if (t == 0) p.part_lse[part] = lse2;
+      } else {
+        float fs;
+        const float all = cached_with_sink(p, kvh * p.G + r / p.Sq, lse2, fs);
+        f *= fs;
+        if (t == 0) p.lse[orow] = all * 0.6931471805599453f;
       }
-    }
-    __syncthreads();
+      const int e = 2 * (ri & 1);
+      if constexpr (CT == E4M3) {  // tiles 2 n, 2 n + 1 hold the even and odd columns of 16-column piece n
 #pragma unroll
-    for (int ri = 0; ri < 2 * MT; ++ri) {
-      const int row = 16 * (ri >> 1) + g + 8 * (ri & 1);
-      const float mine = xm[warp * L::TR + row];
-      const float M = fmaxf(fmaxf(xm[row], xm[L::TR + row]), fmaxf(xm[2 * L::TR + row], xm[3 * L::TR + row]));
-      const float f = mine == -INFINITY ? 0.f : ex2_approx(mine - M);
-      float* const to = xo + (warp * L::TR + row) * L::OROW;
+        for (int n = 0; n < DP / 16; ++n) {
+          if (16 * n >= p.D) continue;
+          const float(&ev)[4] = o[ri >> 1][2 * n], (&od)[4] = o[ri >> 1][2 * n + 1];
+          const float y0 = ev[e] * f, y1 = od[e] * f, y2 = ev[e + 1] * f, y3 = od[e + 1] * f;
+          const int d = 16 * n + 4 * t;
+          if (slot >= 0) *reinterpret_cast<float4*>(p.part_o + part * p.D + d) = make_float4(y0, y1, y2, y3);
+          else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + orow * p.D + d) = make_uint2(pack_io2<IOF>(y0, y1), pack_io2<IOF>(y2, y3));
+        }
+      } else {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float v0 = o[ri >> 1][n][2 * (ri & 1)] * f, v1 = o[ri >> 1][n][2 * (ri & 1) + 1] * f;
-        if constexpr (CT == E4M3) {  // tile n holds the even or odd columns of 16-column piece n / 2
-          to[16 * (n >> 1) + 4 * t + (n & 1)] = v0;
-          to[16 * (n >> 1) + 4 * t + 2 + (n & 1)] = v1;
-        } else {
-          to[8 * n + 2 * t] = v0;
-          to[8 * n + 2 * t + 1] = v1;
+        for (int n = 0; n < NT; ++n) {
+          if (8 * n >= p.D) continue;
+          const float y0 = o[ri >> 1][n][e] * f, y1 = o[ri >> 1][n][e + 1] * f;
+          const int d = 8 * n + 2 * t;
+          if (slot >= 0) *reinterpret_cast<float2*>(p.part_o + part * p.D + d) = make_float2(y0, y1);
+          else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + orow * p.D + d) = pack_io2<IOF>(y0, y1);
         }
       }
     }
-    __syncthreads();
-    const int live_rows = min(L::TR, p.R - r0), pieces = p.D / 8;
-    for (int i = tid; i < live_rows * pieces; i += THREADS) {
-      const int row = i / pieces, c = i % pieces;
-      float M = -INFINITY, lt = 0.f;
-#pragma unroll
-      for (int k = 0; k < WARPS; ++k) M = fmaxf(M, xm[k * L::TR + row]);
-#pragma unroll
-      for (int k = 0; k < WARPS; ++k) {
-        const float mk = xm[k * L::TR + row];
-        if (mk != -INFINITY) lt += xl[k * L::TR + row] * ex2_approx(mk - M);
-      }
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = 0.f;
-#pragma unroll
-      for (int k = 0; k < WARPS; ++k) {
-        const float4* from = reinterpret_cast<const float4*>(xo + (k * L::TR + row) * L::OROW + c * 8);
-        const float4 a = from[0], b = from[1];
-        y[0] += a.x, y[1] += a.y, y[2] += a.z, y[3] += a.w, y[4] += b.x, y[5] += b.y, y[6] += b.z, y[7] += b.w;
-      }
-      const bool none = M == -INFINITY;
-      float f = none ? 0.f : 1.f / lt;
-      const float lse2 = none ? -INFINITY : M - BIAS + __log2f(lt);
-      const int r = r0 + row;
-      if (w.slot >= 0) {
-        const long long at = ((long long)blockIdx.x * 2 + w.slot) * L::TR + row;
-        float4* to = reinterpret_cast<float4*>(p.part_o + at * p.D + c * 8);
-        to[0] = make_float4(y[0] * f, y[1] * f, y[2] * f, y[3] * f);
-        to[1] = make_float4(y[4] * f, y[5] * f, y[6] * f, y[7] * f);
-        if (c == 0) p.part_lse[at] = lse2;
-      } else {
-        float fs;
-        const float all = cached_with_sink(p, w.kvh * p.G + r / p.Sq, lse2, fs);
-        f *= fs;
-        const long long orow = ((long long)w.b * p.c.Hkv + w.kvh) * p.R + r;
-        uint4 v;
-        v.x = pack_io2<IOF>(y[0] * f, y[1] * f), v.y = pack_io2<IOF>(y[2] * f, y[3] * f);
-        v.z = pack_io2<IOF>(y[4] * f, y[5] * f), v.w = pack_io2<IOF>(y[6] * f, y[7] * f);
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + orow * p.D + c * 8) = v;
-        if (c == 0) p.lse[orow] = all * 0.6931471805599453f;
-      }
-    }
-    __syncthreads();
-    clear();
   }
 }
 

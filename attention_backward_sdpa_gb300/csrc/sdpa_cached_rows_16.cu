@@ -6,23 +6,24 @@ namespace sdpa {
 
 namespace {
 
-// Block (x, y): of the segment that share x + 1 begins in the middle of, if it is the first to do so (the
-// share notes it), the parts weighed by their sums in the shares' order. WIDE: row y, the parts dealt out to
-// the block's four warps (few rows, which may be cut into very many parts); else rows 4 y .. 4 y + 3, one a
-// warp (many rows, in a few parts).
-template <bool IOF, bool WIDE>
-__global__ void __launch_bounds__(128) cached_merge_kernel(const CachedParams p) {
-  __shared__ float4 sh_y[WIDE ? 4 : 1][32];
-  __shared__ float sh_m[4], sh_l[4];
+// The parts of a cut segment weighed by their sums, in the shares' order. WARPS > 1 (few rows, which may be
+// cut into very many parts): block (segment, row), the parts dealt out to its warps. WARPS 1 (many rows, in a few
+// parts): block (x, y) has rows 4 y .. 4 y + 3, one a warp, of the segment that share x + 1 is the first to
+// begin in the middle of.
+template <bool IOF, int WARPS>
+__global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) cached_merge_kernel(const CachedParams p) {
+  constexpr bool WIDE = WARPS > 1;
+  __shared__ float4 sh_y[WARPS][32];
+  __shared__ float sh_m[WARPS], sh_l[WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = WIDE ? blockIdx.y : blockIdx.y * 4 + warp;
   pdl_wait_prior_grid();
-  const int4 cut = p.cuts[blockIdx.x + 1];
+  const int4 cut = p.cuts[WIDE ? blockIdx.x : blockIdx.x + 1];
   if (cut.x < 0) return;
   const int e = cut.x / p.c.Hkv, kvh = cut.x % p.c.Hkv, b = e / p.n_rt, r = (e % p.n_rt) * p.tile_rows + row;
   if (r >= p.R) return;
-  const int n = cut.z - cut.y + 1, step = WIDE ? 4 : 1, c = lane * 4;
+  const int n = cut.z - cut.y + 1, step = WARPS, c = lane * 4;
   auto part = [&](int i) {  // the first share left its part in slot 1: it does not finish the segment
-    return ((long long)(cut.y + i) * 2 + (i == 0 ? 1 : 0)) * p.tile_rows + row;
+    return ((long long)(cut.y + i) * 2 + (i == 0 ? 1 : 0)) * p.part_rows + row;
   };
   float m = -INFINITY, l = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
   for (int i0 = WIDE ? warp : 0; i0 < n; i0 += 8 * step) {
@@ -59,10 +60,12 @@ __global__ void __launch_bounds__(128) cached_merge_kernel(const CachedParams p)
     if (lane == 0) sh_m[warp] = m, sh_l[warp] = l;
     __syncthreads();
     if (warp != 0) return;
-    m = fmaxf(fmaxf(sh_m[0], sh_m[1]), fmaxf(sh_m[2], sh_m[3]));
+    m = sh_m[0];
+#pragma unroll
+    for (int k = 1; k < WARPS; ++k) m = fmaxf(m, sh_m[k]);
     l = y[0] = y[1] = y[2] = y[3] = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < WARPS; ++k) {
       const float f = sh_m[k] == -INFINITY ? 0.f : ex2_approx(sh_m[k] - m);
       const float4 v = sh_y[k][lane];
       l = fmaf(f, sh_l[k], l);
@@ -93,13 +96,17 @@ cudaError_t cached_rows_16_setup() {
 }
 
 cudaError_t launch_cached_merge(const CachedParams& p, cudaStream_t s) {
-  if (p.n_ctas < 2) return cudaSuccess;  // one share: nothing is cut
+  if (p.n_shares < 2) return cudaSuccess;  // one share: nothing is cut
   const int rows = p.R < p.tile_rows ? p.R : p.tile_rows;
-  const bool wide = p.tile_rows <= 32;
-  const dim3 grid((unsigned)(p.n_ctas - 1), (unsigned)(wide ? rows : ceil_div(rows, 4)));
-  auto* kernel = p.f16 ? (wide ? cached_merge_kernel<true, true> : cached_merge_kernel<true, false>)
-                       : (wide ? cached_merge_kernel<false, true> : cached_merge_kernel<false, false>);
-  return launch_kernel(kernel, grid, dim3(128), 0, s, true, p);
+  if (p.tile_rows > 32) {
+    const dim3 grid((unsigned)(p.n_shares - 1), (unsigned)ceil_div(rows, 4));
+    return launch_kernel(p.f16 ? cached_merge_kernel<true, 1> : cached_merge_kernel<false, 1>, grid, dim3(128), 0, s, true, p);
+  }
+  // Sixteen warps a row where there are few rows to merge: their parts are many then.
+  const dim3 grid((unsigned)(p.B * p.n_rt * p.c.Hkv), (unsigned)rows);
+  if ((long long)grid.x * rows <= 2 * 152)
+    return launch_kernel(p.f16 ? cached_merge_kernel<true, 16> : cached_merge_kernel<false, 16>, grid, dim3(512), 0, s, true, p);
+  return launch_kernel(p.f16 ? cached_merge_kernel<true, 4> : cached_merge_kernel<false, 4>, grid, dim3(128), 0, s, true, p);
 }
 
 }  // namespace sdpa

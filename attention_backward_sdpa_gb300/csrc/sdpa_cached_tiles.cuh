@@ -111,10 +111,10 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   // (its shared memory: the place that the halves exchange their sums in later)
-  const CachedStart st0 = cached_start<THREADS>(p, reinterpret_cast<CachedStart*>(smem + L::OFF_XCH),
+  const CachedStart st0 = cached_start<THREADS, 1>(p, reinterpret_cast<CachedStart*>(smem + L::OFF_XCH),
                                                 reinterpret_cast<long long*>(smem + L::OFF_XCH + 64));
   pdl_launch_dependents();  // (the merge waits for this grid before it reads the parts)
-  cached_empty_rows<THREADS>(p);
+  cached_empty_rows<THREADS, false>(p);
   CachedWalk walk{st0.begin, st0.end, st0.te, st0.e};
   if (walk.u >= walk.end) return;
   if (tid == 0) {
@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
       const float inv = M == -INFINITY ? 0.f : 1.f / lt;
       const float lse2 = M == -INFINITY ? -INFINITY : M - BIAS + __log2f(lt);
       float f0 = a0 * inv, f1 = a1 * inv, all = lse2;
-      const long long at = ((long long)blockIdx.x * 2 + max(w.slot, 0)) * BM + row;
+      const long long at = ((long long)blockIdx.x * 2 + max(w.slot, 0)) * p.part_rows + row;
       if (w.slot < 0) {
         float fs;
         all = cached_with_sink(p, head, lse2, fs);
