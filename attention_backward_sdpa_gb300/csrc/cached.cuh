@@ -74,69 +74,71 @@ __device__ __forceinline__ CachedBounds cached_bounds(const CachedParams& p, int
 }
 __device__ __forceinline__ int cached_tile(const CachedBounds& s, int j) { return j < s.nf ? j : s.kt + (j - s.nf); }
 
-// Shares of T units, each of one unit at least; first unit of share i of n, and the share that has unit t.
-__device__ __forceinline__ int shares_of(const CachedParams& p, long long T) {
-  return (int)min((long long)p.n_shares, max(T / p.share_units, min(T, 512ll)));
-}
-__device__ __forceinline__ long long share_begin(long long T, int n, int i) { return T * i / n; }
-__device__ __forceinline__ int share_of(long long T, int n, long long t) { return (int)(((t + 1) * n + T - 1) / T) - 1; }
+// T units (below 2^31) in n shares of q units, the first r of them one more.
+struct CachedShares {
+  int n, q, r;
+  __device__ __forceinline__ CachedShares(const CachedParams& p, int T) {
+    n = max(1, min(p.n_shares, max(T / p.share_units, min(T, 512))));
+    q = T / n;
+    r = T - q * n;
+  }
+  __device__ __forceinline__ int begin(int i) const { return i * q + min(i, r); }
+  __device__ __forceinline__ int of(int t) const {  // the share that has unit t < T
+    const int big = r * (q + 1);
+    return t < big ? t / (q + 1) : r + (t - big) / q;
+  }
+};
 
 // Where a share begins: its first unit and the one past its last, its entry e (b * n_rt + rt),
 // and that entry's first unit. One call by every thread of the block; sh[W] and `warp_sum` are shared memory.
 // W 1: the CTA is a share (and notes the segment that it cuts); else each of its W warps is one.
 struct CachedStart {
-  long long begin, end, te;
-  int e, n;  // n: shares
-  long long T;
+  int begin, end, te, e;
 };
 template <int THREADS, int W>
-__device__ __forceinline__ CachedStart cached_start(const CachedParams& p, CachedStart* sh, long long* warp_sum) {
+__device__ __forceinline__ CachedStart cached_start(const CachedParams& p, CachedStart* sh, int* warp_sum, int& total) {
   const bool report = blockIdx.x == 0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int E = p.B * p.n_rt, per = ceil_div(E, THREADS), e0 = min(tid * per, E), e1 = min(e0 + per, E);
-  long long sum = 0;
+  int sum = 0;
   for (int e = e0; e < e1; ++e) {
-    sum += (long long)cached_bounds(p, e / p.n_rt, e % p.n_rt).n * p.c.Hkv;
+    sum += cached_bounds(p, e / p.n_rt, e % p.n_rt).n * p.c.Hkv;
     if (report) {
       const int len = p.c.lens[e / p.n_rt];
       if (len < 0 || len > (long long)p.c.max_pages * p.c.page) atomicOr(p.status, STATUS_PAGE);
     }
   }
-  long long incl = sum;
+  int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, incl, o);
+    const int u = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += u;
   }
   if (lane == 31) warp_sum[warp] = incl;
-  if (tid < W) sh[tid].e = -1;
   __syncthreads();
-  long long T = 0;
+  int T = 0;
 #pragma unroll
   for (int w = 0; w < THREADS / 32; ++w) {
     if (w == warp) incl += T;
     T += warp_sum[w];
   }
-  const int n = shares_of(p, T);
-  const long long te0 = incl - sum;
+  total = T;
+  const CachedShares shares(p, T);
+  const int te0 = incl - sum;
 #pragma unroll 1
   for (int w = 0; w < W; ++w) {
-    const int i = blockIdx.x * W + w;
-    const long long begin = i < n ? share_begin(T, n, i) : T;
+    const int i = blockIdx.x * W + w, begin = i < shares.n ? shares.begin(i) : T;
     if (begin >= te0 && begin < incl) {
-      long long te = te0;
+      int te = te0;
       for (int e = e0; e < e1; ++e) {
-        const long long k = (long long)cached_bounds(p, e / p.n_rt, e % p.n_rt).n * p.c.Hkv;
+        const int k = cached_bounds(p, e / p.n_rt, e % p.n_rt).n * p.c.Hkv;
         if (begin < te + k) {
-          sh[w].e = e;
-          sh[w].te = te;
+          sh[w] = CachedStart{begin, shares.begin(i + 1), te, e};
           if constexpr (W == 1) {
             // A segment that the share begins in the middle of, and the share before does not.
-            const int m = (int)(k / p.c.Hkv), h = (int)((begin - te) / m);
-            const long long first = te + (long long)h * m;
+            const int m = k / p.c.Hkv, h = (begin - te) / m, first = te + h * m;
             int4 cut = make_int4(-1, 0, 0, 0);
-            if (begin > first && share_begin(T, n, i - 1) <= first)
-              cut = make_int4(e * p.c.Hkv + h, i - 1, share_of(T, n, first + m - 1), 0);
+            if (begin > first && shares.begin(i - 1) <= first) cut = make_int4(e * p.c.Hkv + h, i - 1, shares.of(first + m - 1), 0);
             p.cuts[i] = cut;
           }
           break;
@@ -144,11 +146,13 @@ __device__ __forceinline__ CachedStart cached_start(const CachedParams& p, Cache
         te += k;
       }
     }
-    if (W == 1 && begin >= T && tid == 0) p.cuts[i] = make_int4(-1, 0, 0, 0);
+    if (begin >= T && tid == 0) {
+      sh[w] = CachedStart{T, T, T, -1};
+      if (W == 1) p.cuts[i] = make_int4(-1, 0, 0, 0);
+    }
   }
   __syncthreads();
-  const int w = W == 1 ? 0 : warp, i = blockIdx.x * W + w;
-  return CachedStart{i < n ? share_begin(T, n, i) : T, i < n ? share_begin(T, n, i + 1) : T, sh[w].te, sh[w].e, n, T};
+  return sh[W == 1 ? 0 : warp];
 }
 
 // Rows that see no key: entries that visit no unit, each written by one of the CTAs.
@@ -176,23 +180,22 @@ struct CachedPortion {
   int slot;                // part slot, or -1: the whole segment
 };
 struct CachedWalk {
-  long long u, end, te;
-  int e;
+  int u, end, te, e;
   __device__ __forceinline__ bool next(const CachedParams& p, CachedPortion& w) {
     if (u >= end) return false;
     for (;;) {
       w.b = e / p.n_rt;
       w.rt = e % p.n_rt;
       w.s = cached_bounds(p, w.b, w.rt);
-      const long long n = (long long)w.s.n * p.c.Hkv;
+      const int n = w.s.n * p.c.Hkv;
       if (u < te + n) break;
       te += n;
       ++e;
     }
-    const long long off = u - te;
-    w.kvh = (int)(off / w.s.n);
-    w.j0 = (int)(off % w.s.n);
-    w.j1 = (int)min((long long)w.s.n, w.j0 + (end - u));
+    const int off = u - te;
+    w.kvh = off / w.s.n;
+    w.j0 = off - w.kvh * w.s.n;
+    w.j1 = min(w.s.n, w.j0 + (end - u));
     w.slot = w.j0 > 0 ? 0 : w.j1 < w.s.n ? 1 : -1;
     u += w.j1 - w.j0;
     return true;

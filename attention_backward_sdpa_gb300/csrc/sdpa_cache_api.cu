@@ -144,7 +144,9 @@ int sdpa_fwd_cached(int io_dtype, int cache_dtype, const void* q, const void* k_
   for (const void* x : {(const void*)lse, (const void*)sink, (const void*)alibi_slopes, (const void*)seq_q_lens})
     if (misaligned(x, 4)) return SDPA_ERR_ALIGN;
   const CachedPlan plan = cached_plan(B, H_q, H_kv, S_q, D, p.c.f8 != 0, (long long)max_pages * page_size);
-  if ((long long)B * plan.n_rt >= 1ll << 24 || (long long)B * plan.n_rt * H_kv >= 1ll << 31) return SDPA_ERR_INVALID;
+  // Units of the schedule are 32-bit.
+  if ((double)B * plan.n_rt * H_kv * (((long long)max_pages * page_size + plan.tk - 1) / plan.tk) >= 2147483648.0)
+    return SDPA_ERR_INVALID;
   if (workspace) {
     if (workspace_bytes < plan.bytes) return SDPA_ERR_WORKSPACE;
     if (misaligned(workspace, 256)) return SDPA_ERR_ALIGN;

@@ -110,11 +110,12 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
   constexpr int KD = DP / 16, NT = DP / 8, ESZ = CT == E4M3 ? 1 : 2;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ CachedStart sh_start[WARPS];
-  __shared__ long long sh_sum[WARPS];
+  __shared__ int sh_sum[WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   if (p.D < DP)  // columns past D are never copied
     for (int i = tid; i < L::BYTES / 16; i += THREADS) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
-  const CachedStart st = cached_start<THREADS, WARPS>(p, sh_start, sh_sum);
+  int total;
+  const CachedStart st = cached_start<THREADS, WARPS>(p, sh_start, sh_sum, total);
   pdl_launch_dependents();  // (the merge waits for this grid before it reads the parts)
   cached_empty_rows<THREADS, true>(p);
   if (st.begin >= st.end) return;
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
     if (w.j0 == 0 && lane == 0) {  // the segment's first share
       int4 cut = make_int4(-1, 0, 0, 0);
       const int seg = (w.b * p.n_rt + w.rt) * p.c.Hkv + w.kvh;
-      if (w.slot >= 0) cut = make_int4(seg, share, share_of(st.T, st.n, walk.u - w.j1 + s.n - 1), 0);
+      if (w.slot >= 0) cut = make_int4(seg, share, CachedShares(p, total).of(walk.u - w.j1 + s.n - 1), 0);
       p.cuts[seg] = cut;
     }
     auto group_seen = [&](int a) { return a < s.k_hi && (a + 15 >= s.k_lo || a < p.first_keys); };

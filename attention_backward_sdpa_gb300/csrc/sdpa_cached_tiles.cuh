@@ -25,8 +25,6 @@
 // issuers: 256 x 144 + 256 x 80 + 128 x 32 = 640 x 96.
 #pragma once
 
-#include <type_traits>
-
 #include "cached.cuh"
 
 namespace sdpa {
@@ -83,6 +81,13 @@ __device__ __forceinline__ void codes_f16(uint32_t four, uint32_t& lo, uint32_t&
       "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(four));
 }
 
+// Sixteen bytes, or zeros: one predicated load, so that no path of the program has to wait for another's.
+__device__ __forceinline__ void load_if(uint4& v, const void* from, uint32_t take) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+      "mov.b32 %3, 0;\n\t@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(from), "r"(take));
+}
 // What the loaders tell of a tile, by groups of 16 keys.
 template <int NS>
 struct TileMeta {
@@ -111,8 +116,9 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::OFF_MISC + 4);
   // (its shared memory: the place that the halves exchange their sums in later)
+  int total;
   const CachedStart st0 = cached_start<THREADS, 1>(p, reinterpret_cast<CachedStart*>(smem + L::OFF_XCH),
-                                                reinterpret_cast<long long*>(smem + L::OFF_XCH + 64));
+                                                   reinterpret_cast<int*>(smem + L::OFF_XCH + 64), total);
   pdl_launch_dependents();  // (the merge waits for this grid before it reads the parts)
   cached_empty_rows<THREADS, false>(p);
   CachedWalk walk{st0.begin, st0.end, st0.te, st0.e};
@@ -146,7 +152,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
     if (warp < 18) {
       // ------------------------------------------------------------ MMA issuers
       constexpr uint32_t ID_S = idesc_io(BM, BK, false, false, PF);
-      constexpr uint32_t ID_O = idesc_io(BM, DP, false, true, PF);
+      const uint32_t ID_O = idesc_io(BM, p.D, false, true, PF);  // (D is a multiple of 16)
       constexpr uint64_t T_KMAJ = sdesc_sw128_template(16, 1024);
       constexpr uint64_t T_MN_V = sdesc_sw128_template(L::BLK, 1024);
       int g = 0, np = 0;
@@ -168,6 +174,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
               const uint32_t aQ = smem_u32(smem), aK = smem_u32(smem + L::OFF_KV + st * L::TILE);
 #pragma unroll
               for (int k = 0; k < DP / 16; ++k) {
+                if (16 * k >= p.D) break;
                 const uint32_t ko = (k >> 2) * L::BLK + (k & 3) * 32;
                 mma_ss(tmem + 128u * s, sdesc_at(T_KMAJ, aQ + ko), sdesc_at(T_KMAJ, aK + ko), ID_S, k > 0);
               }
@@ -308,24 +315,31 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
         static_assert(STEP >= 16, "a pass's rows lie in the same place of their groups");
         uint4 reg[N];
         const bool upper = DP == 64 && rl >= 16;  // (at 64 columns a pass is two groups)
-        auto load = [&](uint4& v, const int (&at)[8], int k0, int i, bool full) {
-          const int from = DP == 64 ? (upper ? at[(2 * i + 1) & 7] : at[(2 * i) & 7]) : at[i];
-          if (full) {
-            v = __ldg(reinterpret_cast<const uint4*>(rows + from * group_bytes));
-          } else {
-            v = make_uint4(0u, 0u, 0u, 0u);
-            if (from >= 0 && seen(k0, i)) v = __ldg(reinterpret_cast<const uint4*>(rows + from * group_bytes));
+        // The passes whose pieces of the tile at k0 this thread reads, as bits.
+        auto takes = [&](const int (&at)[8], int k0, bool full) -> uint32_t {
+          if (!in) return 0u;
+          if (full) return 0xFFu;
+          uint32_t bits = 0;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int from = DP == 64 ? (upper ? at[(2 * i + 1) & 7] : at[(2 * i) & 7]) : at[i];
+            if (from >= 0 && seen(k0, i)) bits |= 1u << i;
           }
+          return bits;
+        };
+        auto load = [&](uint4& v, const int (&at)[8], int i, uint32_t bits) {
+          const int from = DP == 64 ? (upper ? at[(2 * i + 1) & 7] : at[(2 * i) & 7]) : at[i];
+          load_if(v, rows + from * group_bytes, bits & (1u << i));
         };
         scales_for(page);
         tell_places(0, w.j0, page);
         named_bar_sync(bar_id, 128);
-        if (in) {
-          const int k0 = cached_tile(s, w.j0) * BK;
+        {
           int at[8];
           groups_of(0, at);
+          const uint32_t bits = takes(at, cached_tile(s, w.j0) * BK, false);
 #pragma unroll
-          for (int i = 0; i < N; ++i) load(reg[i], at, k0, i, false);
+          for (int i = 0; i < N; ++i) load(reg[i], at, i, bits);
         }
         for (int j = w.j0; j < w.j1; ++j, ++g) {
           const int x1 = (j - w.j0 + 1) & 1, st = g % NS;
@@ -339,30 +353,23 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
           named_bar_sync(bar_id, 128);
           scales_for(page1);
           page = page1;
-          const int k1 = more ? cached_tile(s, j + 1) * BK : 0;
           uint8_t* const to = ring + st * L::TILE;
-          // Each piece is widened and stored, and its registers take the next tile's.
-          auto fill = [&](auto how) {  // 0: no next tile, 1: all of it is read, 2: what some row sees
-            constexpr int HOW = decltype(how)::value;
-            int at[8];
-            if constexpr (HOW != 0) groups_of(x1, at);
+          int at[8];
+          groups_of(x1, at);
+          const uint32_t bits = more ? takes(at, cached_tile(s, j + 1) * BK, meta.full[side][x1] != 0) : 0u;
+          // Each piece is widened and stored, and its registers take the next tile's. (Pieces past D
+          // are zeros and stay so.)
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const int row = rl + STEP * i;
-              uint4 a, b;
-              codes_f16(reg[i].x, a.x, a.y);
-              codes_f16(reg[i].y, a.z, a.w);
-              codes_f16(reg[i].z, b.x, b.y);
-              codes_f16(reg[i].w, b.z, b.w);
-              if constexpr (HOW != 0) load(reg[i], at, k1, i, HOW == 1);
-              *reinterpret_cast<uint4*>(to + tile_at(row, 2 * c)) = a;
-              *reinterpret_cast<uint4*>(to + tile_at(row, 2 * c + 1)) = b;
-            }
-          };
-          if (in) {
-            if (!more) fill(std::integral_constant<int, 0>());
-            else if (meta.full[side][x1]) fill(std::integral_constant<int, 1>());
-            else fill(std::integral_constant<int, 2>());
+          for (int i = 0; i < N; ++i) {
+            const int row = rl + STEP * i;
+            uint4 a, b;
+            codes_f16(reg[i].x, a.x, a.y);
+            codes_f16(reg[i].y, a.z, a.w);
+            codes_f16(reg[i].z, b.x, b.y);
+            codes_f16(reg[i].w, b.z, b.w);
+            load(reg[i], at, i, bits);
+            *reinterpret_cast<uint4*>(to + tile_at(row, 2 * c)) = a;
+            *reinterpret_cast<uint4*>(to + tile_at(row, 2 * c + 1)) = b;
           }
           if (j == w.j0) copies_wait<0>();  // Q
           fence_proxy_async_smem();
@@ -491,13 +498,25 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
 #pragma unroll
           for (int k = 0; k < 4; ++k) cg[k] = 1.f;
         }
-        const bool mine = kb + 63 <= rw.hi && (kb >= rw.lo || kb + 63 < p.first_keys);
-        if (!__all_sync(0xffffffffu, mine) || bad != 0u) {
+        // Masks, by halves of 32 keys and by what the warp's rows need: the last key, then the first
+        // ones, then pages that there are not.
+        const int hi = rw.hi - kb, lo = rw.lo - kb, first = p.first_keys - kb;
 #pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            const int key = kb + i;
-            if (key > rw.hi || (key < rw.lo && key >= p.first_keys) || ((bad >> (i >> 4)) & 1u))
-              sr[i >> 5][i & 31] = 0xFF800000u;  // -inf
+        for (int h = 0; h < 2; ++h) {
+          if (!__all_sync(0xffffffffu, hi >= 32 * h + 31)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * h + i > hi) sr[h][i] = 0xFF800000u;  // -inf
+          }
+          if (!__all_sync(0xffffffffu, lo <= 32 * h || first > 32 * h + 31)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * h + i < lo && 32 * h + i >= first) sr[h][i] = 0xFF800000u;
+          }
+          if ((bad >> (2 * h)) & 3u) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if ((bad >> (2 * h + (i >> 4))) & 1u) sr[h][i] = 0xFF800000u;
           }
         }
         float mp[8];
@@ -542,31 +561,43 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
         }
         l *= alpha;
         m = m_new;
-        float rs[8];
-#pragma unroll
-        for (int a = 0; a < 8; ++a) rs[a] = 0.f;
+        uint64_t rs[4];  // sums of the groups, in pairs
         const float neg_m = m == -INFINITY ? 0.f : BIAS - m;
 #pragma unroll
         for (int c16 = 0; c16 < 2; ++c16) {
           uint32_t wv[16];
 #pragma unroll
-          for (int i2 = 0; i2 < 16; ++i2) {
-            const int k = 2 * c16 + (i2 >> 3);
+          for (int k2 = 0; k2 < 2; ++k2) {
+            const int k = 2 * c16 + k2;
             const float f = F8 ? cg[k] : cg[0], a = F8 ? add[k] + neg_m : neg_m;
-            const float p0 = ex2_approx(fmaf(__uint_as_float(sr[c16][2 * i2]), f, a));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(sr[c16][2 * i2 + 1]), f, a));
-            rs[2 * k] += p0;
-            rs[2 * k + 1] += p1;
-            wv[i2] = pack_io2<PF>(p0, p1);
+            const uint64_t f2 = f2_pack(f, f), a2 = f2_pack(a, a);
+            uint64_t x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = f2_fma(f2_pack(sr[c16][16 * k2 + 2 * i], sr[c16][16 * k2 + 2 * i + 1]), f2, a2);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float x0, x1;
+              f2_unpack(x[i], x0, x1);
+              const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+              x[i] = f2_pack(p0, p1);
+              wv[8 * k2 + i] = pack_io2<PF>(p0, p1);
+            }
+            rs[k] = f2_add(f2_add(f2_add(x[0], x[1]), f2_add(x[2], x[3])), f2_add(f2_add(x[4], x[5]), f2_add(x[6], x[7])));
           }
           __syncwarp();
           tmem_st16(t_lane + 128u * s + half * 64 + c16 * 16, wv);
         }
         if constexpr (F8) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) l = fmaf(rs[2 * k] + rs[2 * k + 1], inv[k], l);
+          for (int k = 0; k < 4; ++k) {
+            float s0, s1;
+            f2_unpack(rs[k], s0, s1);
+            l = fmaf(s0 + s1, inv[k], l);
+          }
         } else {
-          l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
+          float s0, s1;
+          f2_unpack(f2_add(f2_add(rs[0], rs[1]), f2_add(rs[2], rs[3])), s0, s1);
+          l += s0 + s1;
         }
         tmem_st_wait();
         tc_fence_before();
@@ -617,10 +648,10 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               y[e] = __uint_as_float(o0[v8 * 8 + e]) * f0 + __uint_as_float(o1[v8 * 8 + e]) * f1;
-            if (w.slot >= 0) {
-              float4* to = reinterpret_cast<float4*>(p.part_o + at * p.D + cbase + v8 * 8);
-              to[0] = make_float4(y[0], y[1], y[2], y[3]);
-              to[1] = make_float4(y[4], y[5], y[6], y[7]);
+            if (w.slot >= 0) {  // (rows of a part are whole 32-byte sectors)
+              float* const to = p.part_o + at * p.D + cbase + v8 * 8;
+              asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "f"(y[0]), "f"(y[1]), "f"(y[2]),
+                           "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]) : "memory");
             } else {
               *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + orow * p.D + cbase + v8 * 8) =
                   make_uint4(pack_io2<F16>(y[0], y[1]), pack_io2<F16>(y[2], y[3]), pack_io2<F16>(y[4], y[5]),
