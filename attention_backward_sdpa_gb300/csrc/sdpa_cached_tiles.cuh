@@ -7,11 +7,13 @@
 // sum and an O of their own (raised lazily, joined at the end).
 //
 // What differs is where the tiles come from. Four loader warps fill the key tiles and four the
-// value tiles, each side with a ring of its own (a key tile is free again as soon as its scores are there):
-// 16-byte asynchronous copies (16-bit caches), or loads whose codes become fp16 on the way (8 bits, exact; a
-// thread keeps the next tile's codes in registers while it widens this one's). They write the 128-byte
-// swizzle that the tensor core reads, take any page size, and fill rows that no query sees with zeros. (A bulk
-// tensor copy could bring 16-bit pages, but not widen codes, and a page of 16 rows is a copy of 2 KB.)
+// value tiles, each side with a ring of its own (a key tile is free again as soon as its scores are there).
+// 16-bit caches: by 16-byte asynchronous copies. 8 bits: bulk copies of the pages' rows, 16 at a time, land in two
+// staging tiles a side, and the warps widen the codes to fp16 (exact) on their way into the ring. (Codes through
+// registers by plain loads waited for the small L1 that the rings leave: 445 us for 2,048 rows of 32 heads
+// over 10,240 keys, 413 with rings of two stages.) Both write the 128-byte swizzle that the tensor core reads, take
+// any page size, and put zeros where no query sees a row. (A tensor-map copy could bring 16-bit pages, but
+// a page of 16 rows is a copy of 2 KB, and what a recycled page holds would have to be cleared.)
 //
 // 8 bits. All products are fp16. bf16 queries become fp16 times a power of two a row (exact down to 2^-29 of
 // the row's largest). Scales stay out of the tiles: a page's key scale is in its scores' factor, and its
@@ -46,15 +48,17 @@ enum : int {
   BAR_RING = BAR_PVDONE + NSLOT    // keys: full (128 arrivals) + stage, empty (their S product is done) + stage; then values
 };
 
-template <int DP>
+template <int DP, bool F8>
 struct Layout {
   static constexpr int BLK = 128 * 128;  // 64 columns of 128 rows
   static constexpr int TILE = BM * DP * 2;
-  static constexpr int NS = DP == 128 ? 3 : 4;
-  static constexpr int NUM_BARS = BAR_RING + 4 * NS;
+  static constexpr int NS = DP == 64 ? 4 : F8 ? 2 : 3;
+  static constexpr int STAGING = F8 ? 128 * DP : 0;   // codes of a tile; two a side
+  static constexpr int NUM_BARS = BAR_RING + 4 * NS + (F8 ? 4 : 0);
   static constexpr int META = 160 + NS * 96;  // TileMeta
   static constexpr int OFF_KV = TILE;
-  static constexpr int OFF_BAR = OFF_KV + 2 * NS * TILE;  // key stages, then value stages
+  static constexpr int OFF_STAGING = OFF_KV + 2 * NS * TILE;  // key stages, then value stages
+  static constexpr int OFF_BAR = OFF_STAGING + 4 * STAGING;
   static constexpr int OFF_XCH = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_META = OFF_XCH + 2 * 256 * 4;  // TileMeta
   static constexpr int OFF_QEXP = OFF_META + META;        // [3][128] exponents of the rows' factors, by portion
@@ -81,26 +85,19 @@ __device__ __forceinline__ void codes_f16(uint32_t four, uint32_t& lo, uint32_t&
       "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(lo), "=r"(hi) : "r"(four));
 }
 
-// Sixteen bytes, or zeros: one predicated load, so that no path of the program has to wait for another's.
-__device__ __forceinline__ void load_if(uint4& v, const void* from, uint32_t take) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
-      "mov.b32 %3, 0;\n\t@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(from), "r"(take));
-}
 // What the loaders tell of a tile, by groups of 16 keys.
 template <int NS>
 struct TileMeta {
   int at[2][2][8];  // by side, by parity of the tile: the group's rows are 16 at of the cache, -1: none is read
-  int full[2][2];   // every row of the tile is read
+  int full[2][2];   // every row of the tile is read (16 bits)
   int bad[4];       // by value stage: groups without a page
   float ks[NS][8], lvs[NS][8], inv[NS][8];  // by value stage, 8 bits: key scale, log2 and inverse of the value scale
 };
-static_assert(sizeof(TileMeta<3>) == Layout<128>::META && sizeof(TileMeta<4>) == Layout<64>::META, "");
+static_assert(sizeof(TileMeta<3>) == Layout<128, false>::META && sizeof(TileMeta<4>) == Layout<64, true>::META, "");
 
 template <int DP, bool F8, bool F16, bool MOD>
 __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedParams p) {
-  using L = Layout<DP>;
+  using L = Layout<DP, F8>;
   constexpr int NS = L::NS;
   constexpr bool PF = F8 || F16;          // the products are fp16
   constexpr float BIAS = F8 ? 6.f : 0.f;  // weights times 2^6: what fp16's smallest step loses is below 2^-30 of the largest
@@ -126,7 +123,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
   if (tid == 0) {
     *abort_flag = 0;
     for (int i = 0; i < L::NUM_BARS; ++i) {
-      const bool full = i == BAR_QFULL || (i >= BAR_RING && (i - BAR_RING) % (2 * NS) < NS);
+      const bool full = i == BAR_QFULL || (i >= BAR_RING && i < BAR_RING + 4 * NS && (i - BAR_RING) % (2 * NS) < NS);
       mbar_init(&bars[i], full ? 128 : i >= BAR_PREADY && i < BAR_PREADY + NSLOT ? 256 : 1);
     }
     fence_mbar_init();
@@ -146,7 +143,8 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
 
   // Every role makes the same walk and counts the tiles that it has passed (g) and the portions
   // (np), whose phases the stages, the S/P slots and the Q buffer go by.
-  constexpr int K_FULL = BAR_RING, K_EMPTY = K_FULL + NS, V_FULL = K_EMPTY + NS, V_EMPTY = V_FULL + NS;
+  constexpr int K_FULL = BAR_RING, K_EMPTY = K_FULL + NS, V_FULL = K_EMPTY + NS, V_EMPTY = V_FULL + NS,
+                STAGED = V_EMPTY + NS;  // 8 bits: + 2 side + parity, the staging tile's codes have landed
   if (warp >= 16) {
     regs_decrease<REGS_CTRL>();
     if (warp < 18) {
@@ -216,14 +214,16 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
     uint64_t* const empty_bar = bars + (side ? V_EMPTY : K_EMPTY);
     uint8_t* const ring = smem + L::OFF_KV + side * NS * L::TILE;
     constexpr int ESZ = F8 ? 1 : 2, CHR = DP * ESZ / 16, STEP = 128 / CHR, N = CHR;  // pieces of a row, rows a pass, passes
-    // Thread to piece c of row rl of a pass. 8 bits: a piece becomes two neighbouring ones of the tile, so eight
-    // lanes that store together take four pieces of an even and an odd row, whose swizzles keep them on
-    // different banks.
-    const int c = !F8 ? lid % CHR : CHR == 8 ? (lid & 3) | ((lid >> 1) & 4) : lid & 3;
+    // Thread to piece c of row rl of a pass. 8 bits: a piece becomes two neighbouring ones of the tile; eight
+    // lanes together take four pieces of an even row and the other four of the next one (or two whole rows
+    // of 64), which lie on different banks both where they come from and, by the rows' swizzles, where they go.
+    const int c = !F8 ? lid % CHR : CHR == 8 ? (lid & 3) | ((((lid >> 2) ^ (lid >> 3)) & 1) << 2) : lid & 3;
     const int rl = !F8 ? lid / CHR : CHR == 8 ? ((lid >> 2) & 1) | ((lid >> 3) & ~1) : lid >> 2;
     const bool in = c * 16 < p.D * ESZ;
-    int g = 0, np = 0;
+    int g = 0, np = 0, staged = 0;  // staged: 8 bits, staging tiles taken
     bool ok = true;
+    bool lost = false;
+    volatile int never = 0;
     CachedPortion w;
     while (ok && walk.next(p, w)) {
       const CachedBounds& s = w.s;
@@ -312,70 +312,77 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
         at[0] = u.x, at[1] = u.y, at[2] = u.z, at[3] = u.w, at[4] = v.x, at[5] = v.y, at[6] = v.z, at[7] = v.w;
       };
       if constexpr (F8) {
-        static_assert(STEP >= 16, "a pass's rows lie in the same place of their groups");
-        uint4 reg[N];
-        const bool upper = DP == 64 && rl >= 16;  // (at 64 columns a pass is two groups)
-        // The passes whose pieces of the tile at k0 this thread reads, as bits.
-        auto takes = [&](const int (&at)[8], int k0, bool full) -> uint32_t {
-          if (!in) return 0u;
-          if (full) return 0xFFu;
-          uint32_t bits = 0;
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int from = DP == 64 ? (upper ? at[(2 * i + 1) & 7] : at[(2 * i) & 7]) : at[i];
-            if (from >= 0 && seen(k0, i)) bits |= 1u << i;
+        uint8_t* const staging = smem + L::OFF_STAGING + side * 2 * L::STAGING;
+        uint64_t* const staged_bar = bars + STAGED + 2 * side;
+        // The side's first warp has tile j's codes on their way into the staging tile of its parity: eight
+        // lanes a group each.
+        auto stage = [&](int j, int pg) {
+          if (warp != first_warp || j >= w.j1) return;
+          const int x = (staged + j - w.j0) & 1, bytes = 16 * p.D;
+          const uint32_t there = __ballot_sync(0xffffffffu, pg >= 0);
+          if (lid == 0) {
+            meta.full[side][x] = (int)there;  // (here: groups that have been read)
+            if (there) mbar_arrive_expect_tx(&staged_bar[x], __popc(there) * bytes);
+            else mbar_arrive(&staged_bar[x]);
           }
-          return bits;
+          __syncwarp();
+          if (pg >= 0) {
+            const int a = cached_tile(s, j) * BK + 16 * lid;
+            const long long row = (((long long)pg * p.c.Hkv + w.kvh) << p.c.page_shift) + (a & (p.c.page - 1));
+            bulk_load(staging + x * L::STAGING + lid * bytes, static_cast<const char*>(side ? p.c.v : p.c.k) + row * p.D, bytes, &staged_bar[x]);
+          }
         };
-        auto load = [&](uint4& v, const int (&at)[8], int i, uint32_t bits) {
-          const int from = DP == 64 ? (upper ? at[(2 * i + 1) & 7] : at[(2 * i) & 7]) : at[i];
-          load_if(v, rows + from * group_bytes, bits & (1u << i));
-        };
+        int page1 = page_for(w.j0 + 1, entry);
+        entry = entry_for(w.j0 + 2);
+        stage(w.j0, page);
+        stage(w.j0 + 1, page1);
         scales_for(page);
-        tell_places(0, w.j0, page);
-        named_bar_sync(bar_id, 128);
-        {
-          int at[8];
-          groups_of(0, at);
-          const uint32_t bits = takes(at, cached_tile(s, w.j0) * BK, false);
-#pragma unroll
-          for (int i = 0; i < N; ++i) load(reg[i], at, i, bits);
-        }
         for (int j = w.j0; j < w.j1; ++j, ++g) {
-          const int x1 = (j - w.j0 + 1) & 1, st = g % NS;
-          const bool more = j + 1 < w.j1;
-          const int page1 = page_for(j + 1, entry);
-          entry = entry_for(j + 2);
-          if (more) tell_places(x1, j + 1, page1);
+          const int st = g % NS, t = staged + j - w.j0, x = t & 1, k0 = cached_tile(s, j) * BK;
+          // (Waited for also by loaders that have given up: no copy is in flight when they leave.)
+          if (!lost && !mbar_wait(&staged_bar[x], (t >> 1) & 1, &never, WAIT_LIMIT_NS)) {
+            lost = true;
+            ok = false;
+            *abort_flag = 1;
+          }
           if (g >= NS && ok) ok = mbar_wait(&empty_bar[st], ((g / NS) - 1) & 1, abort_flag, WAIT_LIMIT_NS);
           __syncwarp();
           tell_stage(st, page);
-          named_bar_sync(bar_id, 128);
           scales_for(page1);
-          page = page1;
+          const uint32_t there = (uint32_t)meta.full[side][x];
+          const bool full = there == 0xFFu && k0 + BK <= s.k_hi && (k0 >= s.k_lo || k0 + BK <= p.first_keys);
+          const uint8_t* const from = staging + x * L::STAGING + rl * p.D + c * 16;
           uint8_t* const to = ring + st * L::TILE;
-          int at[8];
-          groups_of(x1, at);
-          const uint32_t bits = more ? takes(at, cached_tile(s, j + 1) * BK, meta.full[side][x1] != 0) : 0u;
-          // Each piece is widened and stored, and its registers take the next tile's. (Pieces past D
-          // are zeros and stay so.)
+          if (in) {
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int row = rl + STEP * i;
-            uint4 a, b;
-            codes_f16(reg[i].x, a.x, a.y);
-            codes_f16(reg[i].y, a.z, a.w);
-            codes_f16(reg[i].z, b.x, b.y);
-            codes_f16(reg[i].w, b.z, b.w);
-            load(reg[i], at, i, bits);
-            *reinterpret_cast<uint4*>(to + tile_at(row, 2 * c)) = a;
-            *reinterpret_cast<uint4*>(to + tile_at(row, 2 * c + 1)) = b;
+            for (int i = 0; i < N; ++i) {
+              const int row = rl + STEP * i;
+              uint4 v = *reinterpret_cast<const uint4*>(from + STEP * i * p.D);
+              if (!full && !(((there >> (row >> 4)) & 1u) && seen(k0, i))) v = make_uint4(0u, 0u, 0u, 0u);
+              uint4 a, b;
+              codes_f16(v.x, a.x, a.y);
+              codes_f16(v.y, a.z, a.w);
+              codes_f16(v.z, b.x, b.y);
+              codes_f16(v.w, b.z, b.w);
+              *reinterpret_cast<uint4*>(to + tile_at(row, 2 * c)) = a;
+              *reinterpret_cast<uint4*>(to + tile_at(row, 2 * c + 1)) = b;
+            }
           }
-          if (j == w.j0) copies_wait<0>();  // Q
           fence_proxy_async_smem();
-          if (side == 0 && j == w.j0) mbar_arrive(&bars[BAR_QFULL]);
+          if (side == 0 && j == w.j0) {
+            copies_wait<0>();  // Q
+            fence_proxy_async_smem();
+            mbar_arrive(&bars[BAR_QFULL]);
+          }
           mbar_arrive(&full_bar[st]);
+          named_bar_sync(bar_id, 128);  // every warp has read the staging tile: it takes the tile after next
+          const int page2 = page_for(j + 2, entry);
+          entry = entry_for(j + 3);
+          stage(j + 2, page2);
+          page = page1;
+          page1 = page2;
         }
+        staged += w.j1 - w.j0;
       } else {
         int signalled = 0;  // tiles of this portion (and Q, before the first) that the others know of
         const int g0 = g;
@@ -681,7 +688,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
 
 template <int DP, bool F8, bool F16, bool MOD>
 cudaError_t setup_one() {
-  return cudaFuncSetAttribute(cached_tiles_kernel<DP, F8, F16, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP>::BYTES);
+  return cudaFuncSetAttribute(cached_tiles_kernel<DP, F8, F16, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP, F8>::BYTES);
 }
 template <bool F8, bool F16>
 cudaError_t setup_type() {
@@ -694,7 +701,7 @@ template <int DP, bool F8, bool F16>
 cudaError_t launch_width(const CachedParams& p, cudaStream_t s) {
   const bool mod = p.mods.cap_in != 0.f || p.mods.slopes != nullptr;
   return launch_kernel(mod ? cached_tiles_kernel<DP, F8, F16, true> : cached_tiles_kernel<DP, F8, F16, false>,
-                       dim3((unsigned)p.n_ctas), dim3(THREADS), Layout<DP>::BYTES, s, false, p);
+                       dim3((unsigned)p.n_ctas), dim3(THREADS), Layout<DP, F8>::BYTES, s, false, p);
 }
 template <bool F8>
 cudaError_t launch_type(const CachedParams& p, cudaStream_t s) {
