@@ -8,8 +8,8 @@
 //
 // What differs is where the tiles come from. Four loader warps fill the key tiles and four the
 // value tiles, each side with a ring of its own (a key tile is free again as soon as its scores are there).
-// 16-bit caches: by 16-byte asynchronous copies. 8 bits: bulk copies of the pages' rows, 16 at a time, land in two
-// staging tiles a side, and the warps widen the codes to fp16 (exact) on their way into the ring. (Codes through
+// 16-bit caches: by 16-byte asynchronous copies. 8 bits: a warp a side has bulk copies of the pages' rows, 16 at a
+// time, land in two staging tiles, and the loaders widen the codes to fp16 (exact) on their way into the ring. (Codes through
 // registers by plain loads waited for the small L1 that the rings leave: 445 us for 2,048 rows of 32 heads
 // over 10,240 keys, 413 with rings of two stages.) Both write the 128-byte swizzle that the tensor core reads, take
 // any page size, and put zeros where no query sees a row. (A tensor-map copy could bring 16-bit pages, but
@@ -23,8 +23,8 @@
 // in took five instructions a pair of codes where fp16 takes one.)
 //
 // Warps: 0-7 softmax, 8-11 key loaders (and queries), 12-15 value loaders, 16 issues S = Q K^T and owns the
-// tensor memory, 17 issues O += P V. Registers (launched with 96 a thread): 144 for softmax, 80 loaders, 32
-// issuers: 256 x 144 + 256 x 80 + 128 x 32 = 640 x 96.
+// tensor memory, 17 issues O += P V, 18 and 19 have codes staged. Registers (launched with 96 a thread): 152 for
+// softmax, 64 loaders, 48 the others: 256 x 152 + 256 x 64 + 128 x 48 = 640 x 96.
 #pragma once
 
 #include "cached.cuh"
@@ -34,7 +34,7 @@ namespace sdpa {
 namespace cached_tiles {
 
 constexpr int THREADS = 640, BM = 128, BK = 128, NSLOT = 2;
-constexpr uint32_t REGS_SOFTMAX = 144, REGS_LOAD = 80, REGS_CTRL = 32;
+constexpr uint32_t REGS_SOFTMAX = 152, REGS_LOAD = 64, REGS_CTRL = 48;
 static_assert(256 * REGS_SOFTMAX + 256 * REGS_LOAD + 128 * REGS_CTRL <= THREADS * 96, "register split");
 constexpr uint64_t WAIT_LIMIT_NS = 4000000000ull;
 constexpr float RAISE = 8.f;  // P stays below 2^8 until its reference is raised
@@ -54,7 +54,7 @@ struct Layout {
   static constexpr int TILE = BM * DP * 2;
   static constexpr int NS = DP == 64 ? 4 : F8 ? 2 : 3;
   static constexpr int STAGING = F8 ? 128 * DP : 0;   // codes of a tile; two a side
-  static constexpr int NUM_BARS = BAR_RING + 4 * NS + (F8 ? 4 : 0);
+  static constexpr int NUM_BARS = BAR_RING + 4 * NS + (F8 ? 8 : 0);
   static constexpr int META = 160 + NS * 96;  // TileMeta
   static constexpr int OFF_KV = TILE;
   static constexpr int OFF_STAGING = OFF_KV + 2 * NS * TILE;  // key stages, then value stages
@@ -88,8 +88,11 @@ __device__ __forceinline__ void codes_f16(uint32_t four, uint32_t& lo, uint32_t&
 // What the loaders tell of a tile, by groups of 16 keys.
 template <int NS>
 struct TileMeta {
-  int at[2][2][8];  // by side, by parity of the tile: the group's rows are 16 at of the cache, -1: none is read
-  int full[2][2];   // every row of the tile is read (16 bits)
+  // By side, by parity of the tile. 16 bits: the group's rows are 16 at of the cache, -1: none is read; every row of
+  // the tile is. 8 bits: the staged groups' key scales and (in the second) value scales; the groups that are there,
+  // and from bit 8 those without a page.
+  int at[2][2][8];
+  int full[2][2];
   int bad[4];       // by value stage: groups without a page
   float ks[NS][8], lvs[NS][8], inv[NS][8];  // by value stage, 8 bits: key scale, log2 and inverse of the value scale
 };
@@ -124,7 +127,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
     *abort_flag = 0;
     for (int i = 0; i < L::NUM_BARS; ++i) {
       const bool full = i == BAR_QFULL || (i >= BAR_RING && i < BAR_RING + 4 * NS && (i - BAR_RING) % (2 * NS) < NS);
-      mbar_init(&bars[i], full ? 128 : i >= BAR_PREADY && i < BAR_PREADY + NSLOT ? 256 : 1);
+      mbar_init(&bars[i], full ? 128 : i >= BAR_PREADY && i < BAR_PREADY + NSLOT ? 256 : i >= BAR_RING + 4 * NS + 4 ? 4 : 1);
     }
     fence_mbar_init();
   }
@@ -144,7 +147,8 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
   // Every role makes the same walk and counts the tiles that it has passed (g) and the portions
   // (np), whose phases the stages, the S/P slots and the Q buffer go by.
   constexpr int K_FULL = BAR_RING, K_EMPTY = K_FULL + NS, V_FULL = K_EMPTY + NS, V_EMPTY = V_FULL + NS,
-                STAGED = V_EMPTY + NS;  // 8 bits: + 2 side + parity, the staging tile's codes have landed
+                STAGED = V_EMPTY + NS,   // 8 bits: + 2 side + parity, the staging tile's codes have landed
+                STAGE_FREE = STAGED + 4; // and (an arrival a loader warp) have been read
   if (warp >= 16) {
     regs_decrease<REGS_CTRL>();
     if (warp < 18) {
@@ -204,6 +208,63 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
         }
         ++np;
       }
+    } else if constexpr (F8) {
+      // ------------------------------------------------------------ staging of codes
+      const int side = warp - 18, group = lane & 7, bytes = 16 * p.D;
+      const char* const codes = static_cast<const char*>(side ? p.c.v : p.c.k);
+      uint8_t* const staging = smem + L::OFF_STAGING + side * 2 * L::STAGING + group * bytes;
+      int t = 0;  // staging tiles taken
+      bool ok = true;
+      CachedPortion w;
+      while (ok && walk.next(p, w)) {
+        // Lanes 0-7 look up the pages of a tile's eight groups of 16 keys two tiles ahead, and the value side
+        // their scales one tile ahead. Pages: -1 there is none, -2 no row sees the group.
+        auto wanted = [&](int j) {
+          const int a = cached_tile(w.s, j) * BK + 16 * group;
+          return lane < 8 && j < w.j1 && a < w.s.k_hi && (a + 15 >= w.s.k_lo || a < p.first_keys);
+        };
+        auto entry_for = [&](int j) { return wanted(j) ? cached_lookup(p, w.b, cached_tile(w.s, j) * BK + 16 * group) : 0; };
+        auto page_for = [&](int j, int entry) { return wanted(j) ? cached_page(p, entry) : -2; };
+        float ks = 1.f, vs = 1.f;
+        auto scales_for = [&](int page) {
+          ks = vs = 1.f;
+          if (side == 1 && page >= 0) {
+            ks = p.c.ks[(long long)page * p.c.Hkv + w.kvh];
+            vs = p.c.vs[(long long)page * p.c.Hkv + w.kvh];
+          }
+        };
+        int page = page_for(w.j0, entry_for(w.j0)), entry = entry_for(w.j0 + 1);
+        scales_for(page);
+        for (int j = w.j0; j < w.j1 && ok; ++j, ++t) {
+          const int x = t & 1;
+          uint64_t* const full = &bars[STAGED + 2 * side + x];
+          if (t >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&bars[STAGE_FREE + 2 * side + x], ((t >> 1) - 1) & 1, abort_flag, WAIT_LIMIT_NS));
+          if (!ok) break;
+          const uint32_t there = __ballot_sync(0xffffffffu, page >= 0), bad = __ballot_sync(0xffffffffu, page == -1);
+          if (side == 1 && lane < 8) {
+            meta.at[0][x][lane] = __float_as_int(ks);
+            meta.at[1][x][lane] = __float_as_int(vs);
+          }
+          if (lane == 0) meta.full[side][x] = (int)(there | (bad << 8));
+          __syncwarp();
+          if (lane == 0) {
+            if (there) mbar_arrive_expect_tx(full, __popc(there) * bytes);
+            else mbar_arrive(full);
+          }
+          __syncwarp();
+          if (page >= 0) {
+            const int a = cached_tile(w.s, j) * BK + 16 * group;
+            const long long row = (((long long)page * p.c.Hkv + w.kvh) << p.c.page_shift) + (a & (p.c.page - 1));
+            bulk_load(staging + x * L::STAGING, codes + row * p.D, bytes, full);
+          }
+          page = page_for(j + 1, entry);
+          entry = entry_for(j + 2);
+          scales_for(page);
+        }
+      }
+      // No copy is in flight when the CTA ends, also where it has given up.
+      volatile int never = 0;
+      for (int k = max(t - 2, 0); k < t; ++k) mbar_wait(&bars[STAGED + 2 * side + (k & 1)], (k >> 1) & 1, &never, WAIT_LIMIT_NS);
     }
   } else if (warp >= 8) {
     regs_decrease<REGS_LOAD>();
@@ -220,10 +281,8 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
     const int c = !F8 ? lid % CHR : CHR == 8 ? (lid & 3) | ((((lid >> 2) ^ (lid >> 3)) & 1) << 2) : lid & 3;
     const int rl = !F8 ? lid / CHR : CHR == 8 ? ((lid >> 2) & 1) | ((lid >> 3) & ~1) : lid >> 2;
     const bool in = c * 16 < p.D * ESZ;
-    int g = 0, np = 0, staged = 0;  // staged: 8 bits, staging tiles taken
+    int g = 0, np = 0;
     bool ok = true;
-    bool lost = false;
-    volatile int never = 0;
     CachedPortion w;
     while (ok && walk.next(p, w)) {
       const CachedBounds& s = w.s;
@@ -260,45 +319,11 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
         }
         copies_commit();
       }
-      // Threads 0-7 look up the pages of a tile's eight groups of 16 keys two tiles ahead, and in 8 bits
-      // their scales one tile ahead.
-      auto wanted = [&](int j) {  // whether some row sees group lid of tile j
-        const int a = cached_tile(s, j) * BK + 16 * lid;
-        return lid < 8 && j < w.j1 && a < s.k_hi && (a + 15 >= s.k_lo || a < p.first_keys);
+      // What the softmax needs of the tile in stage st, told by the values' side: its stage is kept until the
+      // softmax is done with the tile.
+      auto tell_bad = [&](int st, uint32_t bad) {
+        if (warp == 12 && lid == 0) meta.bad[st] = (int)bad;
       };
-      auto entry_for = [&](int j) { return wanted(j) ? cached_lookup(p, w.b, cached_tile(s, j) * BK + 16 * lid) : 0; };
-      // Pages: -1 there is none, -2 no row sees the group.
-      auto page_for = [&](int j, int entry) { return wanted(j) ? cached_page(p, entry) : -2; };
-      float ks = 1.f, vs = 1.f;
-      auto scales_for = [&](int page) {
-        ks = vs = 1.f;
-        if (F8 && side == 1 && lid < 8 && page >= 0) {
-          ks = p.c.ks[(long long)page * p.c.Hkv + w.kvh];
-          vs = p.c.vs[(long long)page * p.c.Hkv + w.kvh];
-        }
-      };
-      // Where tile j's groups are, for its loads (parity x): the side's first warp.
-      auto tell_places = [&](int x, int j, int page) {
-        if (warp != first_warp) return;
-        const int k0 = cached_tile(s, j) * BK, a = k0 + 16 * (lid & 7);
-        if (lid < 8)
-          meta.at[side][x][lid] = page < 0 ? -1 : ((page * p.c.Hkv + w.kvh) << (p.c.page_shift - 4)) + ((a & (p.c.page - 1)) >> 4);
-        const bool all = __all_sync(0xffffffffu, lid >= 8 || page >= 0);
-        if (lid == 0) meta.full[side][x] = all && k0 + BK <= s.k_hi && (k0 >= s.k_lo || k0 + BK <= p.first_keys);
-      };
-      // What the softmax needs of the tile in stage st (from the values' side: its stage is kept until
-      // the softmax is done with the tile).
-      auto tell_stage = [&](int st, int page) {
-        if (warp != 12) return;
-        const uint32_t bad = __ballot_sync(0xffffffffu, page == -1);
-        if (lid == 0) meta.bad[st] = (int)bad;
-        if (F8 && lid < 8) {
-          meta.ks[st][lid] = ks;
-          meta.lvs[st][lid] = __log2f(vs);
-          meta.inv[st][lid] = 1.f / vs;
-        }
-      };
-      int page = page_for(w.j0, entry_for(w.j0)), entry = entry_for(w.j0 + 1);  // of this tile, of the next one
       const char* const rows = static_cast<const char*>(side ? p.c.v : p.c.k) + (long long)(rl & 15) * p.D * ESZ + c * 16;
       // Row rl + STEP i of a tile lies in group (rl + STEP i) / 16, the first
       // one of pass 0 in the place of the group that `rows` points to.
@@ -312,44 +337,19 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
         at[0] = u.x, at[1] = u.y, at[2] = u.z, at[3] = u.w, at[4] = v.x, at[5] = v.y, at[6] = v.z, at[7] = v.w;
       };
       if constexpr (F8) {
-        uint8_t* const staging = smem + L::OFF_STAGING + side * 2 * L::STAGING;
-        uint64_t* const staged_bar = bars + STAGED + 2 * side;
-        // The side's first warp has tile j's codes on their way into the staging tile of its parity: eight
-        // lanes a group each.
-        auto stage = [&](int j, int pg) {
-          if (warp != first_warp || j >= w.j1) return;
-          const int x = (staged + j - w.j0) & 1, bytes = 16 * p.D;
-          const uint32_t there = __ballot_sync(0xffffffffu, pg >= 0);
-          if (lid == 0) {
-            meta.full[side][x] = (int)there;  // (here: groups that have been read)
-            if (there) mbar_arrive_expect_tx(&staged_bar[x], __popc(there) * bytes);
-            else mbar_arrive(&staged_bar[x]);
-          }
-          __syncwarp();
-          if (pg >= 0) {
-            const int a = cached_tile(s, j) * BK + 16 * lid;
-            const long long row = (((long long)pg * p.c.Hkv + w.kvh) << p.c.page_shift) + (a & (p.c.page - 1));
-            bulk_load(staging + x * L::STAGING + lid * bytes, static_cast<const char*>(side ? p.c.v : p.c.k) + row * p.D, bytes, &staged_bar[x]);
-          }
-        };
-        int page1 = page_for(w.j0 + 1, entry);
-        entry = entry_for(w.j0 + 2);
-        stage(w.j0, page);
-        stage(w.j0 + 1, page1);
-        scales_for(page);
-        for (int j = w.j0; j < w.j1; ++j, ++g) {
-          const int st = g % NS, t = staged + j - w.j0, x = t & 1, k0 = cached_tile(s, j) * BK;
-          // (Waited for also by loaders that have given up: no copy is in flight when they leave.)
-          if (!lost && !mbar_wait(&staged_bar[x], (t >> 1) & 1, &never, WAIT_LIMIT_NS)) {
-            lost = true;
-            ok = false;
-            *abort_flag = 1;
-          }
+        const uint8_t* const staging = smem + L::OFF_STAGING + side * 2 * L::STAGING;
+        for (int j = w.j0; j < w.j1; ++j, ++g) {  // (g counts the staging tiles too)
+          const int st = g % NS, x = g & 1, k0 = cached_tile(s, j) * BK;
+          if (ok) ok = mbar_wait(&bars[STAGED + 2 * side + x], (g >> 1) & 1, abort_flag, WAIT_LIMIT_NS);
           if (g >= NS && ok) ok = mbar_wait(&empty_bar[st], ((g / NS) - 1) & 1, abort_flag, WAIT_LIMIT_NS);
-          __syncwarp();
-          tell_stage(st, page);
-          scales_for(page1);
-          const uint32_t there = (uint32_t)meta.full[side][x];
+          const uint32_t about = (uint32_t)meta.full[side][x], there = about & 0xFFu;
+          tell_bad(st, about >> 8);
+          if (warp == 12 && lid < 8) {
+            const float vs = __int_as_float(meta.at[1][x][lid]);
+            meta.ks[st][lid] = __int_as_float(meta.at[0][x][lid]);
+            meta.lvs[st][lid] = __log2f(vs);
+            meta.inv[st][lid] = __fdividef(1.f, vs);
+          }
           const bool full = there == 0xFFu && k0 + BK <= s.k_hi && (k0 >= s.k_lo || k0 + BK <= p.first_keys);
           const uint8_t* const from = staging + x * L::STAGING + rl * p.D + c * 16;
           uint8_t* const to = ring + st * L::TILE;
@@ -375,15 +375,28 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
             mbar_arrive(&bars[BAR_QFULL]);
           }
           mbar_arrive(&full_bar[st]);
-          named_bar_sync(bar_id, 128);  // every warp has read the staging tile: it takes the tile after next
-          const int page2 = page_for(j + 2, entry);
-          entry = entry_for(j + 3);
-          stage(j + 2, page2);
-          page = page1;
-          page1 = page2;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[STAGE_FREE + 2 * side + x]);
         }
-        staged += w.j1 - w.j0;
       } else {
+        // Threads 0-7 look up the pages of a tile's eight groups of 16 keys one tile ahead. Pages: -1 there is none, -2 no
+        // row sees the group.
+        auto wanted = [&](int j) {
+          const int a = cached_tile(s, j) * BK + 16 * lid;
+          return lid < 8 && j < w.j1 && a < s.k_hi && (a + 15 >= s.k_lo || a < p.first_keys);
+        };
+        auto entry_for = [&](int j) { return wanted(j) ? cached_lookup(p, w.b, cached_tile(s, j) * BK + 16 * lid) : 0; };
+        auto page_for = [&](int j, int entry) { return wanted(j) ? cached_page(p, entry) : -2; };
+        // Where tile j's groups are, for its loads (parity x): the side's first warp.
+        auto tell_places = [&](int x, int j, int page) {
+          if (warp != first_warp) return;
+          const int k0 = cached_tile(s, j) * BK, a = k0 + 16 * (lid & 7);
+          if (lid < 8)
+            meta.at[side][x][lid] = page < 0 ? -1 : ((page * p.c.Hkv + w.kvh) << (p.c.page_shift - 4)) + ((a & (p.c.page - 1)) >> 4);
+          const bool all = __all_sync(0xffffffffu, lid >= 8 || page >= 0);
+          if (lid == 0) meta.full[side][x] = all && k0 + BK <= s.k_hi && (k0 >= s.k_lo || k0 + BK <= p.first_keys);
+        };
+        int page = page_for(w.j0, entry_for(w.j0)), entry = entry_for(w.j0 + 1);
         int signalled = 0;  // tiles of this portion (and Q, before the first) that the others know of
         const int g0 = g;
         auto signal = [&](int upto) {
@@ -403,7 +416,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
             }
           }
           __syncwarp();
-          tell_stage(st, page);
+          if (warp == first_warp) tell_bad(st, __ballot_sync(0xffffffffu, page == -1));
           named_bar_sync(bar_id, 128);
           const uint32_t tile = smem_u32(ring + st * L::TILE);
           if (in) {
