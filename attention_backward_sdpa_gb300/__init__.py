@@ -804,14 +804,59 @@ def _cache_fits(cache, page_table, seq_kv_lens, B, io, dev) -> bool:
     """The same in one test: whether all is as it has to be."""
     try:
         k, v, ks, vs = cache
-        shape, t = k.shape, k.dtype
-        f8 = t is torch.float8_e4m3fn
-        return (len(shape) == 4 and (f8 or t is io) and _is(k, t, dev, shape) and _is(v, t, dev, shape)
-                and (_is(ks, torch.float32, dev, shape[:2]) and _is(vs, torch.float32, dev, shape[:2]) if f8
-                     else ks is None and vs is None)
-                and _is(page_table, torch.int32, dev, (B, page_table.shape[1])) and _is(seq_kv_lens, torch.int32, dev, (B,)))
+        shape, t, table = k.shape, k.dtype, page_table.shape
+        good = (k.get_device() == dev == v.get_device() == page_table.get_device() == seq_kv_lens.get_device()
+                and len(shape) == 4 and v.shape == shape and v.dtype is t and k.is_contiguous() and v.is_contiguous()
+                and len(table) == 2 and table[0] == B and page_table.dtype is torch.int32 is seq_kv_lens.dtype
+                and page_table.is_contiguous() and seq_kv_lens.shape == (B,) and seq_kv_lens.is_contiguous())
+        if t is torch.float8_e4m3fn:
+            return good and _is(ks, torch.float32, dev, shape[:2]) and _is(vs, torch.float32, dev, shape[:2])
+        return good and t is io and ks is None and vs is None
     except (AttributeError, IndexError, TypeError, ValueError):
         return False
+
+
+def _check_append_args(k, v, cache, seq_q_lens, q, inv_freq, positions, axes, q_out):
+    """Names what is wrong with an append's arguments other than its cache, table and lengths."""
+    io = _io_dtype(k)
+    if k.dim() != 4:
+        raise ValueError("k must be (B, H, S, D)")
+    B, Hkv, S, D = k.shape
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    if q is not None and (not isinstance(q, torch.Tensor) or q.dim() != 4):
+        raise ValueError("q must be a (B, H, S, D) tensor")
+    for name, t, H in (("k", k, Hkv), ("v", v, Hkv), ("q", q, 0 if q is None else q.shape[1]),
+                       ("q_out", q_out, 0 if q is None else q.shape[1])):
+        if t is None and name in ("q", "q_out"):
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype != io or not t.is_cuda:
+            raise ValueError(f"{name} must be a {io} CUDA tensor")
+        if tuple(t.shape) != (B, H, S, D):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, H, S, D)}")
+        if t.stride(3) != 1 and D > 1:
+            raise ValueError(f"{name} must have contiguous columns (stride 1 in its last dimension)")
+    if cache[0].shape[1] != Hkv or cache[0].shape[3] != D:
+        raise ValueError(f"the cache holds {cache[0].shape[1]} heads of {cache[0].shape[3]} columns, k has {Hkv} of {D}")
+    if seq_q_lens is not None:
+        _check_int32("seq_q_lens", seq_q_lens, ((B,),))
+    if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dtype != torch.float64 or not inv_freq.is_cuda \
+                or not inv_freq.is_contiguous() or inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be a contiguous fp64 CUDA vector (rope_inv_freq)")
+        rot = 2 * inv_freq.numel()
+        if rot == 0 or rot > D:
+            raise ValueError(f"inv_freq rotates {rot} columns of {D}")
+        if axes is not None:
+            _check_axes(axes, positions, rot // 2, B, S)
+        elif positions is not None:
+            _check_int32("positions", positions, ((S,), (B, S)))
+    elif positions is not None or axes is not None:
+        raise ValueError("positions and axes go with inv_freq")
+    _check_same_device(k, _ref="k", v=v, q=q, q_out=q_out, seq_q_lens=seq_q_lens, inv_freq=inv_freq, positions=positions,
+                       axes=axes, k_cache=cache[0])
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, page_table: torch.Tensor, seq_kv_lens: torch.Tensor, *,
@@ -830,61 +875,52 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, page_table: torc
     ``q`` (B,Hq,S,D), contiguous unless ``q_out`` is given (it may be q itself); None without q.
     """
     lib = load()
+    new = torch.empty if stream is None else functools.partial(_empty, stream=stream)
     io = _io_dtype(k)
-    if k.dim() != 4:
-        raise ValueError("k must be (B, H, S, D)")
-    B, Hkv, S, D = k.shape
-    dev, Hq = k.get_device(), 0
-    if q is not None:
-        if not isinstance(q, torch.Tensor) or q.dim() != 4:
-            raise ValueError("q must be a (B, H, S, D) tensor")
-        Hq = q.shape[1]
-        if q_out is None:
-            q_out = torch.empty((B, Hq, S, D), dtype=io, device=k.device) if stream is None \
-                else _empty((B, Hq, S, D), io, k.device, stream)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    for name, t, H in (("k", k, Hkv), ("v", v, Hkv), ("q", q, Hq), ("q_out", q_out, Hq)):
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or t.dtype is not io or not t.is_cuda:
-            raise ValueError(f"{name} must be a {io} CUDA tensor")
-        if t.shape != (B, H, S, D):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, H, S, D)}")
-        if t.stride(3) != 1 and D > 1:
-            raise ValueError(f"{name} must have contiguous columns (stride 1 in its last dimension)")
-        if t.get_device() != dev:
-            _check_same_device(k, _ref="k", **{name: t})
-    if not _cache_fits(cache, page_table, seq_kv_lens, B, io, dev):
-        _check_cache(cache, page_table, seq_kv_lens, B, io, k)
+    rot = good = Hq = 0
+    try:
+        B, Hkv, S, D = shape = k.shape
+        dev, st, sv = k.get_device(), k.stride(), v.stride()
+        sq = so = st
+        good = (k.is_cuda and v.dtype is io and v.get_device() == dev and v.shape == shape and st[3] == 1 == sv[3]
+                and (seq_q_lens is None or _is(seq_q_lens, torch.int32, dev, (B,))))
+        if q is None:
+            good = good and q_out is None
+        else:
+            Hq, sq = q.shape[1], q.stride()
+            good = good and q.dtype is io and q.get_device() == dev and q.shape == (B, Hq, S, D) and sq[3] == 1
+            if q_out is None:
+                q_out, so = new((B, Hq, S, D), dtype=io, device=k.device), (Hq * S * D, S * D, D)
+            else:
+                so = q_out.stride()
+                good = good and q_out.dtype is io and q_out.get_device() == dev and q_out.shape == q.shape and so[3] == 1
+        if inv_freq is not None:
+            rot = 2 * inv_freq.shape[0]
+            good = good and 0 < rot <= D and _is(inv_freq, torch.float64, dev, (rot // 2,))
+        if positions is not None or axes is not None:
+            good = good and rot > 0
+            if axes is None:
+                good = good and (_is(positions, torch.int32, dev, (B, S)) or _is(positions, torch.int32, dev, (S,)))
+            else:
+                n = positions.shape[0]
+                good = good and 1 <= n <= _MAX_AXES and _is(axes, torch.int32, dev, (rot // 2,)) \
+                    and (_is(positions, torch.int32, dev, (n, B, S)) or _is(positions, torch.int32, dev, (n, S)))
+    except (AttributeError, IndexError, TypeError, ValueError):  # not tensors, or of other dimensions
+        good = False
+    if not good or not _cache_fits(cache, page_table, seq_kv_lens, B, io, dev):
+        if k.dim() != 4:
+            raise ValueError("k must be (B, H, S, D)")
+        _check_cache(cache, page_table, seq_kv_lens, k.shape[0], io, k)
+        _check_append_args(k, v, cache, seq_q_lens, q, inv_freq, positions, axes, q_out)
     kc, vc, ks, vs = cache
-    if kc.shape[1] != Hkv or kc.shape[3] != D:
-        raise ValueError(f"the cache holds {kc.shape[1]} heads of {kc.shape[3]} columns, k has {Hkv} of {D}")
-    if seq_q_lens is not None and not _is(seq_q_lens, torch.int32, dev, (B,)):
-        _check_int32("seq_q_lens", seq_q_lens, ((B,),))
-        _check_same_device(k, _ref="k", seq_q_lens=seq_q_lens)
-    rot = 0
-    if inv_freq is not None:
-        if not isinstance(inv_freq, torch.Tensor) or inv_freq.dim() != 1 or not _is(inv_freq, torch.float64, dev, inv_freq.shape):
-            raise ValueError("inv_freq must be a contiguous fp64 CUDA vector (rope_inv_freq) on k's device")
-        rot = 2 * inv_freq.shape[0]
-        if rot == 0 or rot > D:
-            raise ValueError(f"inv_freq rotates {rot} columns of {D}")
-    elif positions is not None or axes is not None:
-        raise ValueError("positions and axes go with inv_freq")
-    if axes is not None:
-        _check_axes(axes, positions, rot // 2, B, S)
-    elif positions is not None:
-        _check_int32("positions", positions, ((S,), (B, S)))
-    if positions is not None:
-        _check_same_device(k, _ref="k", positions=positions, axes=axes)
+    n_pages, heads, P, columns = kc.shape
+    if heads != Hkv or columns != D:
+        raise ValueError(f"the cache holds {heads} heads of {columns} columns, k has {Hkv} of {D}")
     _check_launch_device(k)
-    st, sv = k.stride(), v.stride()
-    sq, so = (st, st) if q is None else (q.stride(), q_out.stride())
     rc = lib.sdpa_kv_append(
         _IO_CODES[io], _CACHE_CODES[kc.dtype], _addr(q), _addr(q_out), k.data_ptr(), v.data_ptr(), kc.data_ptr(),
         vc.data_ptr(), _addr(ks), _addr(vs), page_table.data_ptr(), seq_kv_lens.data_ptr(), _addr(seq_q_lens), B, Hq,
-        Hkv, S, D, kc.shape[0], kc.shape[2], page_table.shape[1],
+        Hkv, S, D, n_pages, P, page_table.shape[1],
         _strides(sq[0], sq[1], sq[2], so[0], so[1], so[2], st[0], st[1], st[2], sv[0], sv[1], sv[2]),
         _addr(inv_freq), rot, float(mult), _addr(positions),
         0 if positions is None else positions.dim() - (1 if axes is None else 2),
@@ -917,12 +953,13 @@ def kv_gather(cache: KVCache, page_table: torch.Tensor, seq_kv_lens: torch.Tenso
     if not 0 <= S <= most:
         raise ValueError(f"S must be from 0 to {most}, what the page table has")
     new = torch.empty if stream is None else functools.partial(_empty, stream=stream)
-    k_out = new((B, Hkv, S, D), dtype=io, device=kc.device) if k_out is None else k_out
-    v_out = new((B, Hkv, S, D), dtype=io, device=kc.device) if v_out is None else v_out
+    shape, device = (B, Hkv, S, D), kc.device
     for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if not _is(t, io, dev, (B, Hkv, S, D)):
-            _check_bf16(name, t, (B, Hkv, S, D), io)
+        if t is not None and not _is(t, io, dev, shape):
+            _check_bf16(name, t, shape, io)
             _check_same_device(kc, _ref="the cache", **{name: t})
+    k_out = new(shape, dtype=io, device=device) if k_out is None else k_out
+    v_out = new(shape, dtype=io, device=device) if v_out is None else v_out
     _check_launch_device(kc)
     rc = lib.sdpa_kv_gather(_IO_CODES[io], _CACHE_CODES[kc.dtype], kc.data_ptr(), cache[1].data_ptr(), _addr(cache[2]),
                             _addr(cache[3]), page_table.data_ptr(), seq_kv_lens.data_ptr(), k_out.data_ptr(),
@@ -1035,46 +1072,49 @@ def sdpa_fwd_cached(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, s
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be (B, H, S, D)")
     io = _io_dtype(q)
-    B, Hq, Sq, D = q.shape
+    B, Hq, Sq, D = shape = q.shape
     dev, fresh = q.get_device(), o is None and lse is None  # (outputs made here need no checks)
-    new = torch.empty if stream is None else functools.partial(_empty, stream=stream)
-    o = new((B, Hq, Sq, D), dtype=io, device=q.device) if o is None else o
-    lse = new((B, Hq, Sq), dtype=torch.float32, device=q.device) if lse is None else lse
-    if not _cache_fits(cache, page_table, seq_kv_lens, B, io, dev):
-        _check_cache(cache, page_table, seq_kv_lens, B, io, q)
-    kc, vc, ks, vs = cache
-    n_pages, Hkv, P, Dc = kc.shape
-    if Dc != D:
-        raise ValueError(f"the cache holds {Dc} columns, q has {D}")
-    if not (q.is_cuda and _is(q, io, dev, (B, Hq, Sq, D))
-            and (fresh or _is(o, io, dev, (B, Hq, Sq, D)) and _optional(lse, torch.float32, dev, B * Hq * Sq))
+    if not (q.is_cuda and q.is_contiguous() and _cache_fits(cache, page_table, seq_kv_lens, B, io, dev)
+            and (fresh or _is(o, io, dev, shape) and _optional(lse, torch.float32, dev, B * Hq * Sq))
             and (seq_q_lens is None or _optional(seq_q_lens, torch.int32, dev, B))
             and (sink is None or _optional(sink, torch.float32, dev, Hq)) and workspace is None):
-        _check_bf16("q", q, (B, Hq, Sq, D), io)
+        _check_cache(cache, page_table, seq_kv_lens, B, io, q)
+        _check_bf16("q", q, shape, io)
         _check_lens(B, seq_q_lens, None)
         if sink is not None and (sink.dtype != torch.float32 or not sink.is_cuda
                                  or not sink.is_contiguous() or sink.numel() != Hq):
             raise ValueError("sink must be a contiguous fp32 CUDA tensor of Hq elements")
-        _check_bf16("o", o, (B, Hq, Sq, D), io)
-        _check_lse(lse, B, Hq, Sq)
+        if o is not None:
+            _check_bf16("o", o, shape, io)
+        if lse is not None:
+            _check_lse(lse, B, Hq, Sq)
         _check_workspace(workspace)
         _check_same_device(q, o=o, lse=lse, seq_q_lens=seq_q_lens, sink=sink, workspace=workspace)
+    kc, vc, ks, vs = cache
+    n_pages, Hkv, P, columns = kc.shape
+    max_pages, cache_code = page_table.shape[1], _CACHE_CODES[kc.dtype]
+    if columns != D:
+        raise ValueError(f"the cache holds {columns} columns, q has {D}")
     if softcap != 0.0 or alibi_slopes is not None:
         _check_score_mods(q, B, Hq, Sq, 0, softcap, alibi_slopes, None, None, -1, -1)
     window_left, first_keys = operator.index(window_left), operator.index(first_keys)
     if not (-_INT32 <= window_left < _INT32 and 0 <= first_keys < _INT32):
         raise ValueError("window_left and first_keys are 32-bit numbers of keys, first_keys not negative")
     _check_launch_device(q)
+    o = _empty_like(q, stream) if o is None else o
+    if lse is None:
+        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device) if stream is None \
+            else _empty((B, Hq, Sq), torch.float32, q.device, stream)
     if workspace is not None:
         ws_bytes = _check_workspace(workspace)
     else:
-        ws_bytes = _cached_workspace(lib, B, Hq, Hkv, Sq, D, _CACHE_CODES[kc.dtype], P, page_table.shape[1])
+        ws_bytes = _cached_workspace(lib, B, Hq, Hkv, Sq, D, cache_code, P, max_pages)
         if ws_bytes and stream is None:  # (a call on a stream given to it leaves this to the library, as sdpa_bwd)
             workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
     rc = lib.sdpa_fwd_cached(
-        _IO_CODES[io], _CACHE_CODES[kc.dtype], q.data_ptr(), kc.data_ptr(), vc.data_ptr(), _addr(ks), _addr(vs),
+        _IO_CODES[io], cache_code, q.data_ptr(), kc.data_ptr(), vc.data_ptr(), _addr(ks), _addr(vs),
         page_table.data_ptr(), seq_kv_lens.data_ptr(), _addr(seq_q_lens), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Sq, D,
-        n_pages, P, page_table.shape[1], 0.0 if scale is None else float(scale), int(causal), window_left, first_keys,
+        n_pages, P, max_pages, 0.0 if scale is None else float(scale), int(causal), window_left, first_keys,
         _addr(sink), float(softcap), _addr(alibi_slopes), _addr(workspace), ws_bytes, _stream_handle(stream))
     if rc != 0:
         raise SdpaError(rc, "sdpa_fwd_cached")

@@ -28,6 +28,7 @@
 #pragma once
 
 #include "cached.cuh"
+#include "sdpa_fwd.cuh"
 
 namespace sdpa {
 
@@ -98,7 +99,8 @@ struct TileMeta {
 };
 static_assert(sizeof(TileMeta<3>) == Layout<128, false>::META && sizeof(TileMeta<4>) == Layout<64, true>::META, "");
 
-template <int DP, bool F8, bool F16, bool MOD>
+// MOD (score.cuh): MOD_NONE, MOD_ROWS (distance slopes) or MOD_CAP (a cap, and slopes where given).
+template <int DP, bool F8, bool F16, int MOD>
 __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedParams p) {
   using L = Layout<DP, F8>;
   constexpr int NS = L::NS;
@@ -453,6 +455,8 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
     const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
     float* const xch = reinterpret_cast<float*>(smem + L::OFF_XCH);
     const uint32_t col_o = L::COL_O + 128u * half;
+    CapCoef coef;
+    if constexpr (MOD == MOD_CAP) coef = cap_coef(p.mods.cap_c, p.mods.cap_log2);
     int g = 0, np = 0;
     bool ok = true;
     CachedPortion w;
@@ -461,7 +465,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
       CachedRow rw = cached_row(p, w.s, r);
       if (r >= p.R) rw.lo = 0, rw.hi = w.s.L - 1;  // (not written; never the reason for a mask)
       const int head = w.kvh * p.G + min(r, p.R - 1) / p.Sq;
-      const float slope2 = MOD && p.mods.slopes ? p.mods.slopes[head] * 1.4426950408889634f : 0.f;
+      const float slope2 = MOD != MOD_NONE && p.mods.slopes ? p.mods.slopes[head] * 1.4426950408889634f : 0.f;
       float m = -INFINITY, l = 0.f, unit = 1.f;  // unit: 8 bits, q . k of a product as it is
       for (int j = 0; j < n; ++j, ++g) {
         const int s = g % NSLOT, st = g % NS;
@@ -478,13 +482,13 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
           if (!F16 && j == 0) unit = __uint_as_float((uint32_t)(127 + q_exp[(np % 3) * 128 + row]) << 23);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            cg[k] = meta.ks[st][4 * half + k] * unit * (MOD ? 1.f : p.scale_log2);
+            cg[k] = meta.ks[st][4 * half + k] * unit * (MOD != MOD_NONE ? 1.f : p.scale_log2);
             add[k] = meta.lvs[st][4 * half + k];
             inv[k] = meta.inv[st][4 * half + k];
           }
         } else {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) cg[k] = MOD ? 1.f : p.scale_log2, add[k] = 0.f, inv[k] = 1.f;
+          for (int k = 0; k < 4; ++k) cg[k] = MOD != MOD_NONE ? 1.f : p.scale_log2, add[k] = 0.f, inv[k] = 1.f;
         }
         tc_fence_after();
         uint32_t sr[2][32];
@@ -492,29 +496,26 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
         tmem_ld32(t_lane + 128u * s + i0 + 32, sr[1]);
         tmem_ld_wait(sr[0]);
         tmem_ld_wait(sr[1]);
-        if constexpr (MOD) {
-          const bool cap = p.mods.cap_in != 0.f;
-          const float c = cap ? p.mods.cap_log2 : p.scale_log2;
+        if constexpr (MOD != MOD_NONE) {
+          if constexpr (F8) {
 #pragma unroll
-          for (int b8 = 0; b8 < 8; ++b8) {
-            uint64_t x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x[i] = f2_pack(sr[b8 >> 2][(b8 & 3) * 8 + 2 * i], sr[b8 >> 2][(b8 & 3) * 8 + 2 * i + 1]);
-              if constexpr (F8) x[i] = f2_mul(x[i], f2_pack(cg[b8 >> 1], cg[b8 >> 1]));
-            }
-            if (cap) tanh2_any(x, p.mods.cap_in);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float x0, x1;
-              f2_unpack(x[i], x0, x1);
-              const int key = kb + b8 * 8 + 2 * i;
-              sr[b8 >> 2][(b8 & 3) * 8 + 2 * i] = __float_as_uint(fmaf(-slope2, fabsf((float)(rw.place - key)), x0 * c));
-              sr[b8 >> 2][(b8 & 3) * 8 + 2 * i + 1] = __float_as_uint(fmaf(-slope2, fabsf((float)(rw.place - key - 1)), x1 * c));
+            for (int i = 0; i < 64; i += 2) {
+              uint32_t& s0 = sr[i >> 5][i & 31];
+              uint32_t& s1 = sr[i >> 5][(i & 31) + 1];
+              f2_unpack(f2_mul(f2_pack(s0, s1), f2_pack(cg[i >> 4], cg[i >> 4])), s0, s1);
             }
           }
-        }
-        if constexpr (MOD) {
+          bool small = false;
+          if constexpr (MOD == MOD_CAP) {
+            float big = 0.f;
+#pragma unroll
+            for (int i = 0; i < 64; i += 2)
+              big = max3(big, fabsf(__uint_as_float(sr[i >> 5][i & 31])), fabsf(__uint_as_float(sr[i >> 5][(i & 31) + 1])));
+            small = __all_sync(0xffffffffu, big <= p.mods.cap_small);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            modify_chunk<MOD, true>(p.mods, coef, p.scale_log2, slope2, (float)(rw.place - kb - 32 * h), small, sr[h]);
 #pragma unroll
           for (int k = 0; k < 4; ++k) cg[k] = 1.f;
         }
@@ -699,22 +700,23 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
   }
 }
 
-template <int DP, bool F8, bool F16, bool MOD>
-cudaError_t setup_one() {
-  return cudaFuncSetAttribute(cached_tiles_kernel<DP, F8, F16, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP, F8>::BYTES);
+template <int DP, bool F8, bool F16>
+cudaError_t setup_width() {
+  cudaError_t e = cudaSuccess;
+  for (auto* k : {cached_tiles_kernel<DP, F8, F16, MOD_NONE>, cached_tiles_kernel<DP, F8, F16, MOD_ROWS>, cached_tiles_kernel<DP, F8, F16, MOD_CAP>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<DP, F8>::BYTES);
+  return e;
 }
 template <bool F8, bool F16>
 cudaError_t setup_type() {
-  cudaError_t e = cudaSuccess;
-  for (auto* f : {setup_one<64, F8, F16, false>, setup_one<64, F8, F16, true>, setup_one<128, F8, F16, false>, setup_one<128, F8, F16, true>})
-    if (e == cudaSuccess) e = f();
-  return e;
+  const cudaError_t e = setup_width<64, F8, F16>();
+  return e != cudaSuccess ? e : setup_width<128, F8, F16>();
 }
 template <int DP, bool F8, bool F16>
 cudaError_t launch_width(const CachedParams& p, cudaStream_t s) {
-  const bool mod = p.mods.cap_in != 0.f || p.mods.slopes != nullptr;
-  return launch_kernel(mod ? cached_tiles_kernel<DP, F8, F16, true> : cached_tiles_kernel<DP, F8, F16, false>,
-                       dim3((unsigned)p.n_ctas), dim3(THREADS), Layout<DP, F8>::BYTES, s, false, p);
+  auto* kernel = p.mods.cap_in != 0.f ? cached_tiles_kernel<DP, F8, F16, MOD_CAP>
+                 : p.mods.slopes      ? cached_tiles_kernel<DP, F8, F16, MOD_ROWS> : cached_tiles_kernel<DP, F8, F16, MOD_NONE>;
+  return launch_kernel(kernel, dim3((unsigned)p.n_ctas), dim3(THREADS), Layout<DP, F8>::BYTES, s, false, p);
 }
 template <bool F8>
 cudaError_t launch_type(const CachedParams& p, cudaStream_t s) {
