@@ -101,8 +101,8 @@ __device__ __forceinline__ void codes_f16(uint32_t four, uint32_t& lo, uint32_t&
 }
 
 // CT: type of the cache; IOF: the queries and O are fp16 (a 16-bit cache has their type). MOD: capped or
-// distance-biased scores.
-template <int CT, bool IOF, int DP, int MT, bool MOD>
+// distance-biased scores. FULL: D is DP, so that rows and copies lie at fixed distances.
+template <int CT, bool IOF, int DP, int MT, bool MOD, bool FULL>
 __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows_kernel(const CachedParams p) {
   using L = Layout<CT, DP, MT>;
   constexpr bool PF = CT != BF16;  // the products are fp16
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
   __shared__ CachedStart sh_start[WARPS];
   __shared__ int sh_sum[WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  if (p.D < DP)  // columns past D are never copied
+  if (!FULL && p.D < DP)  // columns past D are never copied
     for (int i = tid; i < L::BYTES / 16; i += THREADS) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
   int total;
   const CachedStart st = cached_start<THREADS, WARPS>(p, sh_start, sh_sum, total);
@@ -122,9 +122,22 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
   const int share = blockIdx.x * WARPS + warp;
   const uint32_t ring = smem_u32(smem) + warp * L::RING;
   const int copy_row = lane / L::CH, copy_c = lane % L::CH;
-  const bool copy_in = copy_c * 16 < p.D * ESZ;
-  const int row_bytes = p.D * ESZ, pass_bytes = (32 / L::CH) * row_bytes;
+  const int D = FULL ? DP : p.D;
+  const bool copy_in = FULL || copy_c * 16 < D * ESZ;
+  const int row_bytes = D * ESZ;
+  // A lane's place in rows copy_row + i * PASS of a group: the swizzle alternates from pass to pass at most.
+  constexpr int PASS = 32 / L::CH;
+  const uint32_t place[2] = {(uint32_t)(copy_row * L::RB + phys<L::CH>(copy_row, copy_c) * 16),
+                             (uint32_t)(copy_row * L::RB + phys<L::CH>(copy_row + PASS, copy_c) * 16)};
 
+  auto place_of = [&](int i) -> uint32_t {
+    // (16 rows of CH pieces: PASS 2, 4 or 8; the swizzle repeats after 8 rows, and with CH 4 after 8 as well)
+    const int x = (i * PASS) & 7;
+    if (x == 0) return place[0] + i * PASS * L::RB;
+    if (PASS == 4) return place[1] + i * PASS * L::RB;
+    const int r = copy_row + i * PASS;
+    return r * L::RB + phys<L::CH>(r, copy_c) * 16;
+  };
   CachedWalk walk{st.begin, st.end, st.te, st.e};
   CachedPortion w;
   while (walk.next(p, w)) {
@@ -160,26 +173,21 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
           const char* kb = static_cast<const char*>(p.c.k) + at;
           const char* vb = static_cast<const char*>(p.c.v) + at;
           if (copy_in) {
+            const uint32_t dst = to + 16 * u * L::RB;
             if (all) {
 #pragma unroll
-              for (int i = 0; i < 16 * L::CH / 32; ++i) {
-                const int r = 16 * u + copy_row + i * (32 / L::CH);
-                const uint32_t dst = to + r * L::RB + phys<L::CH>(r, copy_c) * 16;
-                copy16(dst, kb, true);
-                copy16(dst + L::SIDE, vb, true);
-                kb += pass_bytes;
-                vb += pass_bytes;
+              for (int i = 0; i < 16 / PASS; ++i) {
+                copy16(dst + place_of(i), kb + i * PASS * row_bytes, true);
+                copy16(dst + L::SIDE + place_of(i), vb + i * PASS * row_bytes, true);
               }
             } else {  // rows that no query sees: zeros
 #pragma unroll 1
-              for (int i = 0; i < 16 * L::CH / 32; ++i) {
-                const int r = 16 * u + copy_row + i * (32 / L::CH), key = k0 + r;
+              for (int i = 0; i < 16 / PASS; ++i) {
+                const int r = copy_row + i * PASS, key = a + r;
                 const bool take = page >= 0 && key < s.k_hi && (key >= s.k_lo || key < p.first_keys);
-                const uint32_t dst = to + r * L::RB + phys<L::CH>(r, copy_c) * 16;
-                copy16(dst, take ? kb : static_cast<const char*>(p.c.k), take);
-                copy16(dst + L::SIDE, take ? vb : static_cast<const char*>(p.c.v), take);
-                kb += pass_bytes;
-                vb += pass_bytes;
+                const uint32_t at = dst + r * L::RB + phys<L::CH>(r, copy_c) * 16;
+                copy16(at, take ? kb + i * PASS * row_bytes : static_cast<const char*>(p.c.k), take);
+                copy16(at + L::SIDE, take ? vb + i * PASS * row_bytes : static_cast<const char*>(p.c.v), take);
               }
             }
           }
@@ -208,7 +216,7 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
     for (int ri = 0; ri < 2 * MT; ++ri) {
       const int mt = ri >> 1, half = ri & 1, r = r0 + 16 * mt + g + 8 * half;
       const bool in = r < p.R;
-      const uint16_t* const q = static_cast<const uint16_t*>(p.q) + (((long long)w.b * p.c.Hkv + w.kvh) * p.R + r) * p.D;
+      const uint16_t* const q = static_cast<const uint16_t*>(p.q) + (((long long)w.b * p.c.Hkv + w.kvh) * p.R + r) * D;
       float amax = 0.f;
 #pragma unroll
       for (int kd = 0; kd < KD; ++kd) {
@@ -216,7 +224,7 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
         for (int x = 0; x < 2; ++x) {
           const int d = CT == E4M3 ? 64 * (kd >> 2) + 16 * t + 4 * (kd & 3) + 2 * x : 16 * kd + 2 * t + 8 * x;
           uint32_t v = 0u;
-          if (in && d < p.D) v = *reinterpret_cast<const uint32_t*>(q + d);
+          if (in && d < D) v = *reinterpret_cast<const uint32_t*>(q + d);
           qf[mt][kd][half + 2 * x] = v;
           if constexpr (CT == E4M3 && !IOF) amax = fmaxf(amax, fmaxf(fabsf(io_lo<false>(v)), fabsf(io_hi<false>(v))));
         }
@@ -309,7 +317,8 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
         }
       }
       // ---- scores in log2 units, masked
-      float lvs[L::GROUPS], inv_vs[L::GROUPS];
+      // (unmodified ones stay as they are: their factor fx is part of the exponent)
+      float lvs[L::GROUPS], inv_vs[L::GROUPS], fx[2 * MT][L::GROUPS];
 #pragma unroll
       for (int u = 0; u < L::GROUPS; ++u) {
         lvs[u] = 0.f;
@@ -324,11 +333,14 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
         }
 #pragma unroll
         for (int ri = 0; ri < 2 * MT; ++ri) {
-          const float f = xmul[ri] * ks;
+          fx[ri][u] = fmaxf(xmul[ri] * ks, 1e-38f);  // (positive: a masked score stays -inf)
+          if constexpr (MOD) {
 #pragma unroll
-          for (int n = 2 * u; n < 2 * u + 2; ++n)
+            for (int n = 2 * u; n < 2 * u + 2; ++n)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) sc[ri >> 1][n][2 * (ri & 1) + e] *= f;
+              for (int e = 0; e < 2; ++e) sc[ri >> 1][n][2 * (ri & 1) + e] *= fx[ri][u];
+            fx[ri][u] = 1.f;
+          }
         }
       }
       if constexpr (MOD) {
@@ -376,7 +388,7 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
 #pragma unroll
         for (int u = 0; u < L::GROUPS; ++u) {
           const float(&a)[KT][4] = sc[ri >> 1];
-          mx[ri] = fmaxf(mx[ri], fmaxf(fmaxf(a[2 * u][e], a[2 * u][e + 1]), fmaxf(a[2 * u + 1][e], a[2 * u + 1][e + 1])) + lvs[u]);
+          mx[ri] = fmaxf(mx[ri], fmaf(fmaxf(fmaxf(a[2 * u][e], a[2 * u][e + 1]), fmaxf(a[2 * u + 1][e], a[2 * u + 1][e + 1])), fx[ri][u], lvs[u]));
         }
         raise |= mx[ri] > m[ri] + RAISE;
       }
@@ -409,7 +421,7 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
             const float x0 = sc[ri >> 1][2 * u + n][2 * (ri & 1)], x1 = sc[ri >> 1][2 * u + n][2 * (ri & 1) + 1];
-            const float p0 = ex2_approx(x0 + (neg + lvs[u])), p1 = ex2_approx(x1 + (neg + lvs[u]));
+            const float p0 = ex2_approx(fmaf(x0, fx[ri][u], neg + lvs[u])), p1 = ex2_approx(fmaf(x1, fx[ri][u], neg + lvs[u]));
             sum += p0 + p1;
             pf[ri >> 1][u][(ri & 1) + 2 * n] = pack_io2<PF>(p0, p1);
           }
@@ -478,51 +490,51 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
       if constexpr (CT == E4M3) {  // tiles 2 n, 2 n + 1 hold the even and odd columns of 16-column piece n
 #pragma unroll
         for (int n = 0; n < DP / 16; ++n) {
-          if (16 * n >= p.D) continue;
+          if (16 * n >= D) continue;
           const float(&ev)[4] = o[ri >> 1][2 * n], (&od)[4] = o[ri >> 1][2 * n + 1];
           const float y0 = ev[e] * f, y1 = od[e] * f, y2 = ev[e + 1] * f, y3 = od[e + 1] * f;
           const int d = 16 * n + 4 * t;
-          if (slot >= 0) *reinterpret_cast<float4*>(p.part_o + part * p.D + d) = make_float4(y0, y1, y2, y3);
-          else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + orow * p.D + d) = make_uint2(pack_io2<IOF>(y0, y1), pack_io2<IOF>(y2, y3));
+          if (slot >= 0) *reinterpret_cast<float4*>(p.part_o + part * D + d) = make_float4(y0, y1, y2, y3);
+          else *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + orow * D + d) = make_uint2(pack_io2<IOF>(y0, y1), pack_io2<IOF>(y2, y3));
         }
       } else {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          if (8 * n >= p.D) continue;
+          if (8 * n >= D) continue;
           const float y0 = o[ri >> 1][n][e] * f, y1 = o[ri >> 1][n][e + 1] * f;
           const int d = 8 * n + 2 * t;
-          if (slot >= 0) *reinterpret_cast<float2*>(p.part_o + part * p.D + d) = make_float2(y0, y1);
-          else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + orow * p.D + d) = pack_io2<IOF>(y0, y1);
+          if (slot >= 0) *reinterpret_cast<float2*>(p.part_o + part * D + d) = make_float2(y0, y1);
+          else *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + orow * D + d) = pack_io2<IOF>(y0, y1);
         }
       }
     }
   }
 }
 
-template <int CT, bool IOF, int DP, int MT, bool MOD>
+template <int CT, bool IOF, int DP, int MT>
 cudaError_t setup_one() {
-  return cudaFuncSetAttribute(cached_rows_kernel<CT, IOF, DP, MT, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Layout<CT, DP, MT>::BYTES);
+  cudaError_t e = cudaSuccess;
+  for (auto* k : {cached_rows_kernel<CT, IOF, DP, MT, false, true>, cached_rows_kernel<CT, IOF, DP, MT, false, false>,
+                  cached_rows_kernel<CT, IOF, DP, MT, true, false>})
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<CT, DP, MT>::BYTES);
+  return e;
 }
 template <int CT, bool IOF>
 cudaError_t setup_type() {
   cudaError_t e = cudaSuccess;
-  for (auto* f : {setup_one<CT, IOF, 64, 1, false>, setup_one<CT, IOF, 64, 1, true>, setup_one<CT, IOF, 64, 2, false>,
-                  setup_one<CT, IOF, 64, 2, true>, setup_one<CT, IOF, 128, 1, false>, setup_one<CT, IOF, 128, 1, true>,
-                  setup_one<CT, IOF, 128, 2, false>, setup_one<CT, IOF, 128, 2, true>})
+  for (auto* f : {setup_one<CT, IOF, 64, 1>, setup_one<CT, IOF, 64, 2>, setup_one<CT, IOF, 128, 1>, setup_one<CT, IOF, 128, 2>})
     if (e == cudaSuccess) e = f();
   return e;
 }
-template <int CT, bool IOF, int DP, int MT, bool MOD>
+template <int CT, bool IOF, int DP, int MT>
 cudaError_t launch_one(const CachedParams& p, cudaStream_t s) {
-  return launch_kernel(cached_rows_kernel<CT, IOF, DP, MT, MOD>, dim3((unsigned)p.n_ctas), dim3(THREADS),
-                       Layout<CT, DP, MT>::BYTES, s, false, p);
+  auto* kernel = p.mods.cap_in != 0.f || p.mods.slopes != nullptr ? cached_rows_kernel<CT, IOF, DP, MT, true, false>
+                 : p.D == DP ? cached_rows_kernel<CT, IOF, DP, MT, false, true> : cached_rows_kernel<CT, IOF, DP, MT, false, false>;
+  return launch_kernel(kernel, dim3((unsigned)p.n_ctas), dim3(THREADS), Layout<CT, DP, MT>::BYTES, s, false, p);
 }
 template <int CT, bool IOF, int DP>
 cudaError_t launch_width(const CachedParams& p, int mt, cudaStream_t s) {
-  const bool mod = p.mods.cap_in != 0.f || p.mods.slopes != nullptr;
-  if (mt == 1) return mod ? launch_one<CT, IOF, DP, 1, true>(p, s) : launch_one<CT, IOF, DP, 1, false>(p, s);
-  return mod ? launch_one<CT, IOF, DP, 2, true>(p, s) : launch_one<CT, IOF, DP, 2, false>(p, s);
+  return mt == 1 ? launch_one<CT, IOF, DP, 1>(p, s) : launch_one<CT, IOF, DP, 2>(p, s);
 }
 template <int CT, bool IOF>
 cudaError_t launch_type(const CachedParams& p, int mt, cudaStream_t s) {

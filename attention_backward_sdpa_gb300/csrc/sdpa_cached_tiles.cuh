@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
           if (!F16 && j == 0) unit = __uint_as_float((uint32_t)(127 + q_exp[(np % 3) * 128 + row]) << 23);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            cg[k] = meta.ks[st][4 * half + k] * unit * (MOD != MOD_NONE ? 1.f : p.scale_log2);
+            cg[k] = fmaxf(meta.ks[st][4 * half + k] * unit * (MOD != MOD_NONE ? 1.f : p.scale_log2), 1e-38f);  // (positive: a masked score stays -inf)
             add[k] = meta.lvs[st][4 * half + k];
             inv[k] = meta.inv[st][4 * half + k];
           }
