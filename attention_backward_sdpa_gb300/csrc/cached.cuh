@@ -10,7 +10,7 @@
 // them in tiles of `tile_rows`, whatever head and query they are.
 //
 // Schedule. A segment is one (batch row, row tile, key/value head); it visits n units of
-// `tk` keys: those that some of its rows sees, the tiles of the first F keys and then those of the
+// keys: those that some of its rows sees, the tiles of the first F keys and then those of the
 // window, so nothing between them is read. All segments' units in a row are cut into equal shares, one
 // a CTA (many rows) or one a warp (few rows): lengths as uneven as they come leave no SM idle, and one long
 // sequence is shared by all. A segment inside one share is written at once; of one that is cut every share leaves
@@ -38,7 +38,7 @@ struct CachedParams {
   const int32_t* seq_q_lens;  // or null
   const float* sink;          // or null
   ScoreMods mods;             // cap and slopes
-  int tile_rows, n_rt, tk;    // rows of a tile, tiles of a key/value head, keys of a unit
+  int tile_rows, n_rt, tk_shift;  // rows of a tile, tiles of a key/value head, log2 of a unit's keys
   int n_ctas, n_shares, share_units;  // shares at most, and the fewest units of one past 512 of them
   int part_rows;              // rows of a part: those of a tile, or R
   float* part_o;              // [n_shares][2][part_rows][D]
@@ -67,9 +67,10 @@ __device__ __forceinline__ CachedBounds cached_bounds(const CachedParams& p, int
   s.k_lo = p.window_left >= 0 ? (int)max(0ll, (long long)place + i0 - p.window_left) : 0;
   s.n = s.nf = s.kt = 0;
   if (i0 > i1 || s.k_hi <= 0) return s;
-  s.kt = s.k_lo / p.tk;
-  s.nf = min(ceil_div(min(p.first_keys, s.k_hi), p.tk), s.kt);
-  s.n = s.nf + ceil_div(s.k_hi, p.tk) - s.kt;
+  const int up = (1 << p.tk_shift) - 1;
+  s.kt = s.k_lo >> p.tk_shift;
+  s.nf = min((min(p.first_keys, s.k_hi) + up) >> p.tk_shift, s.kt);
+  s.n = s.nf + ((s.k_hi + up) >> p.tk_shift) - s.kt;
   return s;
 }
 __device__ __forceinline__ int cached_tile(const CachedBounds& s, int j) { return j < s.nf ? j : s.kt + (j - s.nf); }
@@ -99,12 +100,14 @@ template <int THREADS, int W>
 __device__ __forceinline__ CachedStart cached_start(const CachedParams& p, CachedStart* sh, int* warp_sum, int& total) {
   const bool report = blockIdx.x == 0;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // (entry e: batch row e / n_rt; few rows have one row tile)
+  auto batch = [&](int e) { return W > 1 ? e : e / p.n_rt; };
   const int E = p.B * p.n_rt, per = ceil_div(E, THREADS), e0 = min(tid * per, E), e1 = min(e0 + per, E);
   int sum = 0;
   for (int e = e0; e < e1; ++e) {
-    sum += cached_bounds(p, e / p.n_rt, e % p.n_rt).n * p.c.Hkv;
+    sum += cached_bounds(p, batch(e), e - batch(e) * p.n_rt).n * p.c.Hkv;
     if (report) {
-      const int len = p.c.lens[e / p.n_rt];
+      const int len = p.c.lens[batch(e)];
       if (len < 0 || len > (long long)p.c.max_pages * p.c.page) atomicOr(p.status, STATUS_PAGE);
     }
   }
@@ -125,13 +128,14 @@ __device__ __forceinline__ CachedStart cached_start(const CachedParams& p, Cache
   total = T;
   const CachedShares shares(p, T);
   const int te0 = incl - sum;
+  const bool one = per == 1;  // the thread's sum is its entry's
 #pragma unroll 1
   for (int w = 0; w < W; ++w) {
     const int i = blockIdx.x * W + w, begin = i < shares.n ? shares.begin(i) : T;
     if (begin >= te0 && begin < incl) {
       int te = te0;
       for (int e = e0; e < e1; ++e) {
-        const int k = cached_bounds(p, e / p.n_rt, e % p.n_rt).n * p.c.Hkv;
+        const int k = one ? sum : cached_bounds(p, batch(e), e - batch(e) * p.n_rt).n * p.c.Hkv;
         if (begin < te + k) {
           sh[w] = CachedStart{begin, shares.begin(i + 1), te, e};
           if constexpr (W == 1) {
@@ -179,13 +183,14 @@ struct CachedPortion {
   CachedBounds s;
   int slot;                // part slot, or -1: the whole segment
 };
+template <bool ONE_TILE>
 struct CachedWalk {
   int u, end, te, e;
   __device__ __forceinline__ bool next(const CachedParams& p, CachedPortion& w) {
     if (u >= end) return false;
     for (;;) {
-      w.b = e / p.n_rt;
-      w.rt = e % p.n_rt;
+      w.b = ONE_TILE ? e : e / p.n_rt;
+      w.rt = ONE_TILE ? 0 : e - w.b * p.n_rt;
       w.s = cached_bounds(p, w.b, w.rt);
       const int n = w.s.n * p.c.Hkv;
       if (u < te + n) break;

@@ -175,7 +175,7 @@ int sdpa_fwd_cached(int io_dtype, int cache_dtype, const void* q, const void* k_
   p.mods.slopes = alibi_slopes;
   p.tile_rows = plan.tile_rows;
   p.n_rt = plan.n_rt;
-  p.tk = plan.tk;
+  while ((1 << p.tk_shift) < plan.tk) ++p.tk_shift;
   p.n_ctas = plan.n_ctas;
   p.n_shares = plan.n_shares;
   p.share_units = plan.mt ? 8 : 1;

@@ -116,7 +116,6 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
     for (int i = tid; i < L::BYTES / 16; i += THREADS) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
   int total;
   const CachedStart st = cached_start<THREADS, WARPS>(p, sh_start, sh_sum, total);
-  pdl_launch_dependents();  // (the merge waits for this grid before it reads the parts)
   cached_empty_rows<THREADS, true>(p);
   if (st.begin >= st.end) return;
   const int share = blockIdx.x * WARPS + warp;
@@ -138,7 +137,7 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, MT>::CTAS) cached_rows
     const int r = copy_row + i * PASS;
     return r * L::RB + phys<L::CH>(r, copy_c) * 16;
   };
-  CachedWalk walk{st.begin, st.end, st.te, st.e};
+  CachedWalk<true> walk{st.begin, st.end, st.te, st.e};
   CachedPortion w;
   while (walk.next(p, w)) {
     const CachedBounds& s = w.s;

@@ -16,7 +16,6 @@ __global__ void __launch_bounds__(WARPS == 1 ? 128 : 32 * WARPS) cached_merge_ke
   __shared__ float4 sh_y[WARPS][32];
   __shared__ float sh_m[WARPS], sh_l[WARPS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = WIDE ? blockIdx.y : blockIdx.y * 4 + warp;
-  pdl_wait_prior_grid();
   const int4 cut = p.cuts[WIDE ? blockIdx.x : blockIdx.x + 1];
   if (cut.x < 0) return;
   const int e = cut.x / p.c.Hkv, kvh = cut.x % p.c.Hkv, b = e / p.n_rt, r = (e % p.n_rt) * p.tile_rows + row;
@@ -100,13 +99,13 @@ cudaError_t launch_cached_merge(const CachedParams& p, cudaStream_t s) {
   const int rows = p.R < p.tile_rows ? p.R : p.tile_rows;
   if (p.tile_rows > 32) {
     const dim3 grid((unsigned)(p.n_shares - 1), (unsigned)ceil_div(rows, 4));
-    return launch_kernel(p.f16 ? cached_merge_kernel<true, 1> : cached_merge_kernel<false, 1>, grid, dim3(128), 0, s, true, p);
+    return launch_kernel(p.f16 ? cached_merge_kernel<true, 1> : cached_merge_kernel<false, 1>, grid, dim3(128), 0, s, false, p);
   }
   // Sixteen warps a row where there are few rows to merge: their parts are many then.
   const dim3 grid((unsigned)(p.B * p.n_rt * p.c.Hkv), (unsigned)rows);
   if ((long long)grid.x * rows <= 2 * 152)
-    return launch_kernel(p.f16 ? cached_merge_kernel<true, 16> : cached_merge_kernel<false, 16>, grid, dim3(512), 0, s, true, p);
-  return launch_kernel(p.f16 ? cached_merge_kernel<true, 4> : cached_merge_kernel<false, 4>, grid, dim3(128), 0, s, true, p);
+    return launch_kernel(p.f16 ? cached_merge_kernel<true, 16> : cached_merge_kernel<false, 16>, grid, dim3(512), 0, s, false, p);
+  return launch_kernel(p.f16 ? cached_merge_kernel<true, 4> : cached_merge_kernel<false, 4>, grid, dim3(128), 0, s, false, p);
 }
 
 }  // namespace sdpa

@@ -121,9 +121,8 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
   int total;
   const CachedStart st0 = cached_start<THREADS, 1>(p, reinterpret_cast<CachedStart*>(smem + L::OFF_XCH),
                                                    reinterpret_cast<int*>(smem + L::OFF_XCH + 64), total);
-  pdl_launch_dependents();  // (the merge waits for this grid before it reads the parts)
   cached_empty_rows<THREADS, false>(p);
-  CachedWalk walk{st0.begin, st0.end, st0.te, st0.e};
+  CachedWalk<false> walk{st0.begin, st0.end, st0.te, st0.e};
   if (walk.u >= walk.end) return;
   if (tid == 0) {
     *abort_flag = 0;
