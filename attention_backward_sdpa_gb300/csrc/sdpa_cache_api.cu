@@ -81,7 +81,11 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 CachedPlan cached_plan(long long B, int H_q, int H_kv, int S_q, int D, bool f8, long long max_keys) {
   CachedPlan c{};
   const long long R = (long long)(H_q / H_kv) * S_q;
-  c.mt = R <= 16 ? 1 : R <= 32 ? 2 : 0;  // 0: the many-rows kernel
+  // 16-row tiles of the few-rows kernel; 0: the many-rows kernel. For 17 to 32 rows of more than 64 columns that one
+  // is the faster, though its tiles are of 128: 214 us against 252 for 32 rows a head, 64 sequences of up to
+  // 8,192 keys (8 bits: 234, 246), 13.4 against 16.1 over 2,000 keys of one. Of 64 columns it is not where keys are
+  // many: 69 against 59 us over 131,072 keys, 136 against 131 for the batch (12.2 against 13.3 over 2,000).
+  c.mt = R <= 16 ? 1 : R <= 32 && D <= 64 ? 2 : 0;
   c.tile_rows = c.mt ? 16 * c.mt : 128;
   c.tk = c.mt ? cached_rows_tk(f8, c.mt) : 128;
   c.n_rt = (int)((R + c.tile_rows - 1) / c.tile_rows);

@@ -521,7 +521,7 @@ cudaError_t setup_one() {
 template <int CT, bool IOF>
 cudaError_t setup_type() {
   cudaError_t e = cudaSuccess;
-  for (auto* f : {setup_one<CT, IOF, 64, 1>, setup_one<CT, IOF, 64, 2>, setup_one<CT, IOF, 128, 1>, setup_one<CT, IOF, 128, 2>})
+  for (auto* f : {setup_one<CT, IOF, 64, 1>, setup_one<CT, IOF, 64, 2>, setup_one<CT, IOF, 128, 1>})
     if (e == cudaSuccess) e = f();
   return e;
 }
@@ -531,13 +531,10 @@ cudaError_t launch_one(const CachedParams& p, cudaStream_t s) {
                  : p.D == DP ? cached_rows_kernel<CT, IOF, DP, MT, false, true> : cached_rows_kernel<CT, IOF, DP, MT, false, false>;
   return launch_kernel(kernel, dim3((unsigned)p.n_ctas), dim3(THREADS), Layout<CT, DP, MT>::BYTES, s, false, p);
 }
-template <int CT, bool IOF, int DP>
-cudaError_t launch_width(const CachedParams& p, int mt, cudaStream_t s) {
-  return mt == 1 ? launch_one<CT, IOF, DP, 1>(p, s) : launch_one<CT, IOF, DP, 2>(p, s);
-}
 template <int CT, bool IOF>
 cudaError_t launch_type(const CachedParams& p, int mt, cudaStream_t s) {
-  return p.D <= 64 ? launch_width<CT, IOF, 64>(p, mt, s) : launch_width<CT, IOF, 128>(p, mt, s);
+  if (p.D > 64) return launch_one<CT, IOF, 128, 1>(p, s);
+  return mt == 1 ? launch_one<CT, IOF, 64, 1>(p, s) : launch_one<CT, IOF, 64, 2>(p, s);
 }
 
 }  // namespace cached_rows

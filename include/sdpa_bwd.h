@@ -513,8 +513,8 @@ int sdpa_kv_gather(int out_dtype, int cache_dtype, const void* k_cache, const vo
  *              the duration of the call on `stream`; NULL: from the stream-ordered allocator.
  * Elements of q and of visible keys and values must be finite, as in every call of this library;
  * what lies in the cache elsewhere has no effect. In 8 bits scales must be positive. Scores and sums
- * are fp32; a weight is rounded once to the type that it meets values in: the io type, or over an
- * 8-bit cache fp16 where a key/value head has at most 32 rows (H_q / H_kv * S_q).
+ * are fp32; a weight is rounded once to the type that it meets values in: the io type, or fp16 over
+ * an 8-bit cache.
  * Over an 8-bit cache the result is that of the values that the codes stand for, with no further
  * rounding of them where scales are powers of two (and, for fp16, the values fp16 numbers). Results do
  * not depend on timing. Returns as sdpa_fwd_scored(), SDPA_ERR_UNSUPPORTED for page_size and D, and

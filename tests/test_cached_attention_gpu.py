@@ -2,9 +2,8 @@
 cache holds.
 
 Bounds, elementwise; P the exact weights, u half a step of the io type, A = P |V|:
-  |O_gpu - O| <= u |O| [rounded once] + u_P A [weights rounded to the type that they meet values in: the io
-                 type, bf16 2^-8 or fp16 2^-11; over codes fp16 up to 32 rows a key/value head, where codes are
-                 widened to fp16, and the io type, to which they are widened, with more]
+  |O_gpu - O| <= u |O| [rounded once] + u_P A [weights rounded to the type that they meet values in: the cache's,
+                 bf16 2^-8 or fp16 2^-11; over codes fp16, to which these are widened]
                  + 2 e A [scores, in the numerator and the sum] + w 2^-31 sum |V| [weights below fp16's
                  smallest step: taken times 2^6 of a reference at most the row's largest, half a step 2^-25]
                  (fp16 results below 2^-14: 2^-25 more)
@@ -38,8 +37,7 @@ def reference(q, cache, table, lens, new, *, causal=True, window=-1, first=0, si
     rep, dev = Hq // Hkv, "cuda"
     scale = 1.0 / math.sqrt(D) if scale is None else scale
     io = q.dtype
-    few = rep * Sq <= 32
-    u, u_p = torch.finfo(io).eps / 2, 2.0 ** -11 if io == torch.float16 or (ks is not None and few) else 2.0 ** -8
+    u, u_p = torch.finfo(io).eps / 2, 2.0 ** -11 if io == torch.float16 or ks is not None else 2.0 ** -8
     o = torch.zeros(B, Hq, Sq, D, dtype=torch.float64, device=dev)
     lse = torch.full((B, Hq, Sq), -math.inf, dtype=torch.float64, device=dev)
     bo, bl = torch.full_like(o, 2.0 ** -149), torch.full_like(lse, 2.0 ** -19)
