@@ -106,53 +106,73 @@ __global__ void __launch_bounds__(THREADS) rope_vec(const RopeParams p, int head
   __shared__ uint64_t turns[ROPE_MAX_PAIRS];
   __shared__ uint8_t axis_of[AXES ? ROPE_MAX_PAIRS : 1];
   const int half = p.rot / 2;
+  const int groups = (p.D + 2 * VW - 1) / (2 * VW), rot_groups = p.rot / (2 * VW);
+  const int H = p.t[0].H + p.t[1].H;
+  const int h0 = blockIdx.y * heads, h1 = min(h0 + heads, H);
+  const long long step = (long long)gridDim.x * THREADS;
+  long long it = (long long)blockIdx.x * THREADS + threadIdx.x;
+  int c = 0, s = 0, b = 0, c0 = 0, c1 = 0;
+  bool rotated = false, two = false;
+  // With axes the token's positions on the first four, read with the first loads (further ones pair by pair:
+  // all so 21.3 us, 19.5 with these, for rope_axes_grad). The one position without is read when it is needed: ahead of
+  // the loads it costs them (60 us for rope_batch, 52.6).
+  constexpr int NEAR = AXES ? 4 : 1;
+  int places[NEAR] = {};
+  // Item `it`: this thread's two pieces are the pairs' first and second halves, or two neighbouring
+  // pieces (interleaved, and past the rotated part).
+  auto item = [&]() {
+    c = (int)(it % groups);
+    const long long tok = it / groups;
+    s = (int)(tok % p.S), b = (int)(tok / p.S);
+    rotated = c < rot_groups;
+    c0 = (rotated && !INTER) ? c * VW : c * 2 * VW;
+    c1 = (rotated && !INTER) ? half + c * VW : c * 2 * VW + VW;
+    two = c1 < p.D;
+#pragma unroll
+    for (int j = 0; j < NEAR; ++j)
+      if (AXES && j < p.n_axes) places[j] = p.positions[j * p.axis_stride + b * p.pos_bstride + s];
+  };
+  Piece<VW> u[UNROLL], w[UNROLL];
+  auto load = [&](int h) {
+#pragma unroll
+    for (int j = 0; j < UNROLL; ++j) {
+      if (h + j >= h1) continue;
+      int hh;
+      const RopeTensor& t = rope_head(p, h + j, hh);
+      const uint16_t* x = t.x + b * t.xs[0] + hh * t.xs[1] + s * t.xs[2];
+      u[j] = ld_piece<VW>(x + c0);
+      if (two) w[j] = ld_piece<VW>(x + c1);
+    }
+  };
+  if (it < n_items) {  // (the first loads are on their way while the angles are made)
+    item();
+    load(h0);
+  }
   for (int i = threadIdx.x; i < half; i += THREADS) {
     turns[i] = turn_fraction(p.freq[i]);
     if constexpr (AXES) axis_of[i] = (uint8_t)min(max(p.pair_axis[i], 0), p.n_axes - 1);
   }
   __syncthreads();
-  const int groups = (p.D + 2 * VW - 1) / (2 * VW), rot_groups = p.rot / (2 * VW);
-  const int H = p.t[0].H + p.t[1].H;
-  const int h0 = blockIdx.y * heads, h1 = min(h0 + heads, H);
-  for (long long it = (long long)blockIdx.x * THREADS + threadIdx.x; it < n_items;
-       it += (long long)gridDim.x * THREADS) {
-    const int c = (int)(it % groups);
-    const long long tok = it / groups;
-    const int s = (int)(tok % p.S), b = (int)(tok / p.S);
-    // This thread's two pieces: the pairs' first and second halves, or two neighbouring
-    // pieces (interleaved, and past the rotated part).
-    const bool rotated = c < rot_groups;
-    const int c0 = (rotated && !INTER) ? c * VW : c * 2 * VW;
-    const int c1 = (rotated && !INTER) ? half + c * VW : c * 2 * VW + VW;
-    const bool two = c1 < p.D;
+  while (it < n_items) {
     float sn[VW], cs[VW];
     if (rotated) {
-      int pos = 0, axis = -1;
-      if constexpr (!AXES) pos = p.positions ? p.positions[b * p.pos_bstride + s] : p.offset + s;
+      int one = 0;
+      if constexpr (!AXES) one = p.positions ? p.positions[b * p.pos_bstride + s] : p.offset + s;
 #pragma unroll
       for (int i = 0; i < VW; ++i) {
-        if constexpr (AXES) {  // (neighbouring pairs mostly turn by the same axis)
-          if (axis_of[c * VW + i] != axis) {
-            axis = axis_of[c * VW + i];
-            pos = p.positions[axis * p.axis_stride + b * p.pos_bstride + s];
-          }
+        int pos = AXES ? places[0] : one;
+        if constexpr (AXES) {
+          const int axis = axis_of[c * VW + i];
+          if (axis >= NEAR) pos = p.positions[axis * p.axis_stride + b * p.pos_bstride + s];
+#pragma unroll
+          for (int j = 1; j < NEAR; ++j) pos = axis == j ? places[j] : pos;
         }
         angle_sin_cos(turns[c * VW + i], pos, sn[i], cs[i]);
         sn[i] *= p.sign > 0 ? p.mult : -p.mult;
         cs[i] *= p.mult;
       }
     }
-    for (int h = h0; h < h1; h += UNROLL) {
-      Piece<VW> u[UNROLL], w[UNROLL];
-#pragma unroll
-      for (int j = 0; j < UNROLL; ++j) {
-        if (h + j >= h1) continue;
-        int hh;
-        const RopeTensor& t = rope_head(p, h + j, hh);
-        const uint16_t* x = t.x + b * t.xs[0] + hh * t.xs[1] + s * t.xs[2];
-        u[j] = ld_piece<VW>(x + c0);
-        if (two) w[j] = ld_piece<VW>(x + c1);
-      }
+    for (int h = h0; h < h1;) {
 #pragma unroll
       for (int j = 0; j < UNROLL; ++j) {
         if (h + j >= h1) continue;
@@ -181,6 +201,13 @@ __global__ void __launch_bounds__(THREADS) rope_vec(const RopeParams p, int head
         st_piece<VW>(y + c0, u[j]);
         if (two) st_piece<VW>(y + c1, w[j]);
       }
+      h += UNROLL;
+      if (h < h1) load(h);
+    }
+    it += step;
+    if (it < n_items) {
+      item();
+      load(h0);
     }
   }
 }
