@@ -64,9 +64,19 @@ struct Span {
 bool meet(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
 Span span_of(const void* p, size_t bytes) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return {lo, lo + bytes};
+  return p ? Span{lo, lo + bytes} : Span{1, 0};  // (NULL meets nothing)
 }
 Span span_of(const RopeRows& r) { return {(uintptr_t)(r.base * 2), (uintptr_t)(r.end * 2)}; }
+// Whether something written shares a byte with anything else that is written, or read (NULL: nothing).
+bool writes_meet(std::initializer_list<Span> writes, std::initializer_list<Span> reads) {
+  for (const Span& w : writes) {
+    for (const Span& r : reads)
+      if (meet(w, r)) return true;
+    for (const Span& o : writes)
+      if (&o < &w && meet(w, o)) return true;
+  }
+  return false;
+}
 size_t cache_bytes(const KvCacheRef& c) { return (size_t)c.n_pages * c.Hkv * c.page * c.D * (c.f8 ? 1 : 2); }
 
 // How a call over the cache is cut, from its sizes alone (not from the device it runs on, so that
@@ -155,6 +165,13 @@ int sdpa_fwd_cached(int io_dtype, int cache_dtype, const void* q, const void* k_
     if (workspace_bytes < plan.bytes) return SDPA_ERR_WORKSPACE;
     if (misaligned(workspace, 256)) return SDPA_ERR_ALIGN;
   }
+  const size_t rows = (size_t)B * H_q * S_q, scales = (size_t)n_pages * H_kv * 4;
+  if (writes_meet({span_of(o, rows * D * 2), span_of(lse, rows * 4), span_of(workspace, plan.bytes)},
+                  {span_of(q, rows * D * 2), span_of(k_cache, cache_bytes(p.c)), span_of(v_cache, cache_bytes(p.c)),
+                   span_of(k_scale, scales), span_of(v_scale, scales), span_of(page_table, (size_t)B * max_pages * 4),
+                   span_of(seq_kv_lens, (size_t)B * 4), span_of(seq_q_lens, (size_t)B * 4), span_of(sink, (size_t)H_q * 4),
+                   span_of(alibi_slopes, (size_t)H_q * 4)}))
+    return SDPA_ERR_INVALID;
   int sms = 0;
   rc = current_device_state(&p.status, &sms);
   if (rc != SDPA_OK) return rc;
@@ -231,18 +248,24 @@ int sdpa_kv_append(int io_dtype, int cache_dtype, const void* q, void* q_out, co
     }
   // The rotated queries are the queries themselves, element by element, or share no element
   // with any tensor of the call; the cache shares none with any other.
-  const Span pages[2] = {span_of(k_cache, cache_bytes(a.c)), span_of(v_cache, cache_bytes(a.c))};
-  if (meet(pages[0], pages[1])) return SDPA_ERR_INVALID;
   const RopeRows kr = rope_rows(k, a.kst, B, H_kv, S, D), vr = rope_rows(v, a.vst, B, H_kv, S, D);
-  for (const Span& p : pages)
-    if (meet(p, span_of(kr)) || meet(p, span_of(vr))) return SDPA_ERR_INVALID;
+  Span qs{1, 0}, qos{1, 0};
   if (H_q > 0) {
     if (!rows_apart(a.qos, B, H_q, S, D)) return SDPA_ERR_INVALID;
     const RopeRows qr = rope_rows(q, a.qs, B, H_q, S, D), qo = rope_rows(q_out, a.qos, B, H_q, S, D);
     if ((!same_rows(qr, qo) && rows_meet(qr, qo)) || rows_meet(kr, qo) || rows_meet(vr, qo)) return SDPA_ERR_INVALID;
-    for (const Span& p : pages)
-      if (meet(p, span_of(qr)) || meet(p, span_of(qo))) return SDPA_ERR_INVALID;
+    qs = span_of(qr);
+    qos = span_of(qo);
   }
+  const size_t scales = (size_t)n_pages * H_kv * 4;
+  const Span kc = span_of(k_cache, cache_bytes(a.c)), vc = span_of(v_cache, cache_bytes(a.c)), ks = span_of(k_scale, scales),
+             vs = span_of(v_scale, scales), table = span_of(page_table, (size_t)B * max_pages * 4),
+             lens = span_of(seq_kv_lens, (size_t)B * 4), news = span_of(seq_q_lens, (size_t)B * 4),
+             freq = span_of(rot_dim ? inv_freq : nullptr, (size_t)rot_dim * 4), axis = span_of(pair_axis, (size_t)rot_dim * 2),
+             places = span_of(positions, (size_t)S * (positions_per_batch ? B : 1) * (pair_axis ? n_axes : 1) * 4);
+  if (writes_meet({kc, vc, ks, vs}, {span_of(kr), span_of(vr), qs, qos, table, lens, news, freq, axis, places}) ||
+      writes_meet({qos}, {table, lens, news, freq, axis, places}))
+    return SDPA_ERR_INVALID;
   a.q = q;
   a.q_out = q_out;
   a.k = k;
@@ -284,10 +307,11 @@ int sdpa_kv_gather(int out_dtype, int cache_dtype, const void* k_cache, const vo
   if (!k_out || !v_out) return SDPA_ERR_INVALID;
   if (misaligned(k_out, 16) || misaligned(v_out, 16)) return SDPA_ERR_ALIGN;
   const size_t bytes = (size_t)B * H_kv * S * D * 2;
-  const Span out[2] = {span_of(k_out, bytes), span_of(v_out, bytes)};
-  if (meet(out[0], out[1])) return SDPA_ERR_INVALID;
-  for (const Span& p : {span_of(k_cache, cache_bytes(a.c)), span_of(v_cache, cache_bytes(a.c))})
-    if (meet(p, out[0]) || meet(p, out[1])) return SDPA_ERR_INVALID;
+  const size_t scales = (size_t)n_pages * H_kv * 4;
+  if (writes_meet({span_of(k_out, bytes), span_of(v_out, bytes)},
+                  {span_of(k_cache, cache_bytes(a.c)), span_of(v_cache, cache_bytes(a.c)), span_of(k_scale, scales),
+                   span_of(v_scale, scales), span_of(page_table, (size_t)B * max_pages * 4), span_of(seq_kv_lens, (size_t)B * 4)}))
+    return SDPA_ERR_INVALID;
   a.k_out = k_out;
   a.v_out = v_out;
   a.B = B;

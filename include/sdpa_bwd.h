@@ -478,7 +478,7 @@ int sdpa_rope_axes(int io_dtype, const void* q, const void* k, void* q_out, void
  *               and pair_axis as sdpa_rope_axes()) an (n_axes, ...) of these. NULL: the
  *               positions in the cache.
  * q_out may be q itself (same pointer and strides) and otherwise shares no element with any
- * tensor; the buffers share none with the others (SDPA_ERR_INVALID). No two rows of a call may have
+ * tensor; the buffers and their scales share none with each other or the rest (SDPA_ERR_INVALID). No two rows of a call may have
  * the same page to write. S = 0 returns SDPA_OK without work. Returns SDPA_ERR_INVALID,
  * SDPA_ERR_UNSUPPORTED (page_size, D) or SDPA_ERR_ALIGN before anything is enqueued on `stream`.
  */
@@ -492,7 +492,8 @@ int sdpa_kv_append(int io_dtype, int cache_dtype, const void* q, void* q_out, co
 /*
  * Reads the first S (at most max_pages * page_size) positions of every batch row back as k_out, v_out:
  * contiguous (B, H_kv, S, D) of out_dtype (SDPA_DTYPE_BF16 or F16; that of a 16-bit cache), 16-byte
- * aligned, zeros at and past seq_kv_lens[b]. Codes times a power of two are exact in bf16.
+ * aligned, zeros at and past seq_kv_lens[b]. Codes times a power of two are exact in bf16. The outputs
+ * share no byte with each other or with any other tensor (SDPA_ERR_INVALID).
  */
 int sdpa_kv_gather(int out_dtype, int cache_dtype, const void* k_cache, const void* v_cache, const float* k_scale,
                    const float* v_scale, const int32_t* page_table, const int32_t* seq_kv_lens, void* k_out,
@@ -517,7 +518,9 @@ int sdpa_kv_gather(int out_dtype, int cache_dtype, const void* k_cache, const vo
  * an 8-bit cache.
  * Over an 8-bit cache the result is that of the values that the codes stand for, with no further
  * rounding of them where scales are powers of two (and, for fp16, the values fp16 numbers). Results do
- * not depend on timing. Returns as sdpa_fwd_scored(), SDPA_ERR_UNSUPPORTED for page_size and D, and
+ * not depend on timing. o, lse and the workspace share no byte with each other or any other tensor, and
+ * B * H_kv * max_pages * page_size / 16, times the 128s of a head's rows, stays below 2^31 (else
+ * SDPA_ERR_INVALID). Returns as sdpa_fwd_scored(), SDPA_ERR_UNSUPPORTED for page_size and D, and
  * SDPA_ERR_WORKSPACE.
  */
 size_t sdpa_fwd_cached_workspace_size(int B, int H_q, int H_kv, int S_q, int D, int cache_dtype, int page_size,
