@@ -259,8 +259,8 @@ __device__ __forceinline__ float cached_with_sink(const CachedParams& p, int hea
   return all;
 }
 
-cudaError_t launch_cached_rows_16(const CachedParams& p, int mt, cudaStream_t s);
-cudaError_t launch_cached_rows_8(const CachedParams& p, int mt, cudaStream_t s);
+cudaError_t launch_cached_rows_16(const CachedParams& p, int nr, cudaStream_t s);
+cudaError_t launch_cached_rows_8(const CachedParams& p, int nr, cudaStream_t s);
 cudaError_t cached_rows_16_setup();
 cudaError_t cached_rows_8_setup();
 cudaError_t launch_cached_tiles_16(const CachedParams& p, cudaStream_t s);
@@ -269,9 +269,9 @@ cudaError_t cached_tiles_16_setup();
 cudaError_t cached_tiles_8_setup();
 cudaError_t launch_cached_merge(const CachedParams& p, cudaStream_t s);
 
-// Keys of a unit of the few-rows kernel with 16 mt rows, a warp's piece.
-__host__ __device__ constexpr int cached_rows_tk(bool f8, int mt) { return f8 && mt == 1 ? 32 : 16; }
+// Keys of a unit of the few-rows kernel with 8 nr rows, a warp's piece.
+__host__ __device__ constexpr int cached_rows_tk(bool f8, int nr) { return f8 && nr <= 2 ? 32 : 16; }
 // CTAs of it that an SM holds.
-__host__ __device__ constexpr int cached_rows_ctas(int mt) { return mt == 1 ? 3 : 2; }
+__host__ __device__ constexpr int cached_rows_ctas(int nr) { return nr <= 2 ? 3 : 2; }
 
 }  // namespace sdpa

@@ -82,7 +82,7 @@ size_t cache_bytes(const KvCacheRef& c) { return (size_t)c.n_pages * c.Hkv * c.p
 // How a call over the cache is cut, from its sizes alone (not from the device it runs on, so that
 // neither the workspace nor any result depends on that).
 struct CachedPlan {
-  int tile_rows, n_rt, tk, n_ctas, n_shares, part_rows, mt;
+  int tile_rows, n_rt, tk, n_ctas, n_shares, part_rows, nr;
   size_t o_bytes, lse_bytes, bytes;
 };
 constexpr int SHARE_SMS = 152;  // SMs of a GB300
@@ -91,23 +91,23 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 CachedPlan cached_plan(long long B, int H_q, int H_kv, int S_q, int D, bool f8, long long max_keys) {
   CachedPlan c{};
   const long long R = (long long)(H_q / H_kv) * S_q;
-  // 16-row tiles of the few-rows kernel; 0: the many-rows kernel. For 17 to 32 rows of more than 64 columns that one
+  // 8-row tiles of the few-rows kernel; 0: the many-rows kernel. For 17 to 32 rows of more than 64 columns that one
   // is the faster, though its tiles are of 128: 214 us against 252 for 32 rows a head, 64 sequences of up to
   // 8,192 keys (8 bits: 234, 246), 13.4 against 16.1 over 2,000 keys of one. Of 64 columns it is not where keys are
   // many: 69 against 59 us over 131,072 keys, 136 against 131 for the batch (12.2 against 13.3 over 2,000).
-  c.mt = R <= 16 ? 1 : R <= 32 && D <= 64 ? 2 : 0;
-  c.tile_rows = c.mt ? 16 * c.mt : 128;
-  c.tk = c.mt ? cached_rows_tk(f8, c.mt) : 128;
+  c.nr = R <= 8 ? 1 : R <= 16 ? 2 : R <= 32 && D <= 64 ? 4 : 0;
+  c.tile_rows = c.nr ? 8 * c.nr : 128;
+  c.tk = c.nr ? cached_rows_tk(f8, c.nr) : 128;
   c.n_rt = (int)((R + c.tile_rows - 1) / c.tile_rows);
   // As many CTAs as the device holds at once (by their shared memory), fewer where there are
   // not that many units. A share is a CTA, or one of four warps of it.
-  const long long units = B * c.n_rt * H_kv * ((max_keys + c.tk - 1) / c.tk), warps = c.mt ? 4 : 1;
-  const long long ctas = (units + warps - 1) / warps, most = c.mt ? cached_rows_ctas(c.mt) * SHARE_SMS : SHARE_SMS;
+  const long long units = B * c.n_rt * H_kv * ((max_keys + c.tk - 1) / c.tk), warps = c.nr ? 4 : 1;
+  const long long ctas = (units + warps - 1) / warps, most = c.nr ? cached_rows_ctas(c.nr) * SHARE_SMS : SHARE_SMS;
   c.n_ctas = (int)(ctas < most ? ctas : most);
   c.n_shares = (int)(c.n_ctas * warps);
   c.part_rows = R < c.tile_rows ? (int)R : c.tile_rows;
   const size_t parts = (size_t)c.n_shares * 2 * c.part_rows;
-  const size_t notes = c.mt ? (size_t)(B * c.n_rt * H_kv) : (size_t)c.n_shares;
+  const size_t notes = c.nr ? (size_t)(B * c.n_rt * H_kv) : (size_t)c.n_shares;
   c.o_bytes = align256(parts * D * sizeof(float));
   c.lse_bytes = align256(parts * sizeof(float));
   c.bytes = c.o_bytes + c.lse_bytes + align256(notes * sizeof(int4));
@@ -199,13 +199,13 @@ int sdpa_fwd_cached(int io_dtype, int cache_dtype, const void* q, const void* k_
   while ((1 << p.tk_shift) < plan.tk) ++p.tk_shift;
   p.n_ctas = plan.n_ctas;
   p.n_shares = plan.n_shares;
-  p.share_units = plan.mt ? 8 : 1;
+  p.share_units = plan.nr ? 8 : 1;
   p.part_rows = plan.part_rows;
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.o_bytes);
   p.cuts = reinterpret_cast<int4*>(static_cast<char*>(workspace) + plan.o_bytes + plan.lse_bytes);
   nvtxRangePushA("sdpa_fwd_cached");
-  cudaError_t e = plan.mt ? (p.c.f8 ? launch_cached_rows_8(p, plan.mt, stream) : launch_cached_rows_16(p, plan.mt, stream))
+  cudaError_t e = plan.nr ? (p.c.f8 ? launch_cached_rows_8(p, plan.nr, stream) : launch_cached_rows_16(p, plan.nr, stream))
                           : (p.c.f8 ? launch_cached_tiles_8(p, stream) : launch_cached_tiles_16(p, stream));
   if (e == cudaSuccess) e = launch_cached_merge(p, stream);
   nvtxRangePop();

@@ -134,9 +134,9 @@ cudaError_t launch_merge(const CachedParams& p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_cached_rows_16(const CachedParams& p, int mt, cudaStream_t s) {
-  return p.f16 ? cached_rows::launch_type<cached_rows::F16, true>(p, mt, s)
-               : cached_rows::launch_type<cached_rows::BF16, false>(p, mt, s);
+cudaError_t launch_cached_rows_16(const CachedParams& p, int nr, cudaStream_t s) {
+  return p.f16 ? cached_rows::launch_type<cached_rows::F16, true>(p, nr, s)
+               : cached_rows::launch_type<cached_rows::BF16, false>(p, nr, s);
 }
 
 cudaError_t cached_rows_16_setup() {

@@ -3,9 +3,9 @@
 
 namespace sdpa {
 
-cudaError_t launch_cached_rows_8(const CachedParams& p, int mt, cudaStream_t s) {
-  return p.f16 ? cached_rows::launch_type<cached_rows::E4M3, true>(p, mt, s)
-               : cached_rows::launch_type<cached_rows::E4M3, false>(p, mt, s);
+cudaError_t launch_cached_rows_8(const CachedParams& p, int nr, cudaStream_t s) {
+  return p.f16 ? cached_rows::launch_type<cached_rows::E4M3, true>(p, nr, s)
+               : cached_rows::launch_type<cached_rows::E4M3, false>(p, nr, s);
 }
 
 cudaError_t cached_rows_8_setup() {
