@@ -1,5 +1,5 @@
 // cached.cuh -- attention over a paged cache: what its two kernels (sdpa_cached_rows.cuh for few
-// rows, sdpa_cached_tiles.cu for many) and the merge of their parts share.
+// rows, sdpa_cached_tiles.cuh for many) and the merge of their parts share.
 //
 //   y = scale * (q . k),  x = cap tanh(y / cap) - slope |place - j|,  place = L - Lq + i,
 //   row i sees key j < L when j <= place (causal) and (j >= place - W or j < F),

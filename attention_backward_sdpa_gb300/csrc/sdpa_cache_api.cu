@@ -1,5 +1,5 @@
 // sdpa_cache_api.cu -- host side of the cache entry points of include/sdpa_bwd.h: arguments
-// checked, then one launch (or two: the attention and the merge of its parts).
+// checked, then one launch (attention: two, the second merges the parts of what was cut).
 #include <cuda_runtime.h>
 #include <nvtx3/nvToolsExt.h>
 
@@ -302,7 +302,7 @@ int sdpa_kv_gather(int out_dtype, int cache_dtype, const void* k_cache, const vo
                      n_pages, page_size, max_pages, H_kv, D};
   int rc = fill_cache(ca, out_dtype, B, a.c);
   if (rc != SDPA_OK) return rc;
-  if (S < 0 || S > (long long)max_pages * page_size) return SDPA_ERR_INVALID;
+  if (S < 0 || S > (long long)max_pages * page_size || (long long)B * H_kv >= 1ll << 31) return SDPA_ERR_INVALID;
   if (S == 0) return SDPA_OK;  // no rows
   if (!k_out || !v_out) return SDPA_ERR_INVALID;
   if (misaligned(k_out, 16) || misaligned(v_out, 16)) return SDPA_ERR_ALIGN;

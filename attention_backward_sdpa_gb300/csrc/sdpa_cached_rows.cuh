@@ -9,9 +9,12 @@
 //     copies and waits for by itself.
 //     Rows of a piece that no query sees are filled with zeros, so that what a recycled page
 //     holds never meets a product.
-//   - Both products on m16n8k16 with the softmax in registers: 16 rows are the most that such a call
-//     has as a rule (G heads, one token), and 16 rows of P against 16 keys of V take 2 clocks where the
-//     keys' bytes take 180; a 128-row tcgen05 tile would stand empty to seven eighths.
+//   - Both products on m16n8k16 with the softmax in registers: up to 32 rows are what such a call has (G heads, one
+//     token or a few), and 16 rows of P against 16 keys of V take 2 clocks where the keys' bytes take 180; a
+//     128-row tcgen05 tile would stand empty to seven eighths. With 16-bit pages the time is then that of the reads
+//     (6.7 to 6.9 TB/s over long sequences); over codes it is a warp's chain of instructions, 740 a piece of 32 keys
+//     with 16 rows, which 12 warps an SM hide less than the reads (issue slots 48 % full at 115 us for
+//     decode_batch_8bit). Up to 8 rows have products of their own, half of them (below): 102 us.
 //   - The maximum is a lazy reference: it is raised, and O rescaled, only when some score exceeds
 //     it by 2^8; one vote a piece asks for that.
 //   - 8 bits: codes become fp16 in registers (exact), the queries are fp16 times a power of two a row (exact
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, NR>::CTAS) cached_rows
     if constexpr (NR == 1) {
       // Up to 8 rows a key/value head are the columns of the products' tiles, S^T = K Q^T and O^T += V^T P^T: the keys, and
       // the values' columns, fill the tiles' 16 rows. Against 16 rows there (below) that is half the products, scores
-      // and accumulators: 111 -> 101.5 us for decode_batch_8bit, whose time is a warp's chain of instructions.
+      // and accumulators: 111 -> 102 us for decode_batch_8bit (64 sequences of up to 8,192 keys, 4 rows a head).
       // Queries as B fragments: row g.
       uint32_t qf[KD][2];
       float back = 1.f;  // the row's score is its product times this
@@ -496,8 +499,8 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, NR>::CTAS) cached_rows
       }
     } else {
       // 16 MT rows are the tiles' rows, S = Q K^T and O += P V: P becomes an A fragment where it is. (Two tiles of 8 in
-      // the form above take 154 us where one of 16 takes 127, decode_batch_8bit's shape with 16 rows a head; of 64
-      // columns 81 against 75.)
+      // the form above take 154 us where one of 16 takes 127, the same batch with 16 rows a head; of 64 columns 81
+      // against 75.)
       constexpr int MT = NR / 2, NT = DP / 8;
       const int r0 = w.rt * L::TR;
       // Queries as A fragments, and the rows' state. Thread rows: 16 m + g and 16 m + g + 8.

@@ -108,7 +108,7 @@ def _gather(lib, io=BF16, cache=BF16, kc=KC, vc=VC, ks=None, vs=None, table=TABL
 
 
 def test_gather_refusals(lib):
-    for kw in (dict(S=65), dict(ko=None), dict(vo=None), dict(vo=K), dict(vo=K + 2 * 2 * 8 * 64 * 2 - 16), dict(ko=KC),
+    for kw in (dict(S=65), dict(B=1 << 16, Hkv=1 << 15, pages=1), dict(ko=None), dict(vo=None), dict(vo=K), dict(vo=K + 2 * 2 * 8 * 64 * 2 - 16), dict(ko=KC),
                dict(vo=VC + 16), dict(ko=TABLE), dict(vo=LENS), dict(cache=E4M3, ks=K, vs=VS), dict(cache=E4M3, ks=KS, vs=V)):
         assert _gather(lib, **kw) == INVALID, kw
     assert _gather(lib, ko=K + 8) == ALIGN and _gather(lib, vo=V + 2) == ALIGN
