@@ -3,7 +3,7 @@
 //
 // Position j of a sequence is slot j % page of page table[j / page]. The new rows of a call
 // are the last new_len positions of the sequence's length. A key is rotated in fp32 as by
-// sdpa_rope.cu and rounded once, to the cache's type.
+// sdpa_rope.cu (what becomes a code, in twice that: angle_sin_cos_2) and rounded once, to the cache's type.
 //
 // 8 bits. e4m3 has the same 4 significant bits over 2^-6 .. 448, so what a scale is good for
 // is the range, and a power of two serves as well as any: the smallest 2^e (e >= -64) that
@@ -20,9 +20,10 @@
 // heads (one, or a few that share the angles) and side (K, V), since a scale is one reduction over a page and
 // head: rows to fp32, rotated, their largest value, then the codes. Both kinds run in one launch.
 // Bound by memory: 2 bytes an element read, 1 or 2 written. For few tokens it is a chain of latencies (lengths, page,
-// rows, angles; 4.1 us for 24 tokens of 32 + 8 + 8 heads, code fetched anew 9.8). For prompts it is the instructions, 51 % of
-// the issue slots: 5 prompts of up to 1,700 tokens into 8-bit pages, 92 MB with the cache read back, take 33 us, 23
-// of them this launch (a version with eight library sines a thread in line waited for its code: 39).
+// rows, angles; 4.1 us for 24 tokens of 32 + 8 + 8 heads, code fetched anew 9.8). For prompts it is the instructions, half
+// of the issue slots: 5 prompts of up to 1,700 tokens into 8-bit pages, 92 MB with the cache read back, take 38 us, 28
+// of them this launch (33 and 23 with sines, products and sums of fp32 alone, which put a few of 3 million codes a
+// whole step off; eight library sines a thread in line waited for their code: 39).
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -105,13 +106,17 @@ struct AppendPlan {
 // The frequencies as fractions of a turn, and each pair's axis.
 struct Turns {
   uint64_t turn[64];  // D <= 128
+  SinCos2 nodes[33];
   uint8_t axis[64];
 };
-__device__ __forceinline__ void make_turns(const KvAppendArgs& a, Turns& m, int half) {
+__device__ constexpr SinCosNodes NODES = sin_cos_nodes();
+__device__ __forceinline__ void make_turns(const KvAppendArgs& a, Turns& m, int half, bool nodes) {
   for (int i = threadIdx.x; i < half; i += THREADS) {
     m.turn[i] = turn_fraction(a.freq[i]);
     m.axis[i] = a.pair_axis ? (uint8_t)min(max(a.pair_axis[i], 0), a.n_axes - 1) : (uint8_t)0;
   }
+  if (nodes)
+    for (int i = threadIdx.x; i < 33; i += THREADS) m.nodes[i] = NODES.at[i];
 }
 
 // VW 8: rot a multiple of 16, rows of 16-byte alignment; a group is eight pairs, or sixteen pass-through columns.
@@ -157,7 +162,7 @@ __device__ __forceinline__ void append_rows(const KvAppendArgs& a, const AppendP
     if constexpr (VW == 8) load(0);
   }
   if (rot > 0) {
-    make_turns(a, turns, half);
+    make_turns(a, turns, half, false);
     __syncthreads();
   }
   while (tok < pl.tokens) {
@@ -219,6 +224,22 @@ __device__ __forceinline__ void append_rows(const KvAppendArgs& a, const AppendP
       token();
       if constexpr (VW == 8) load(0);
     }
+  }
+}
+
+// turn16 for values that become codes.
+template <bool F16>
+__device__ __forceinline__ void turn16_odd(const uint4& u, const uint4& w, bool interleaved, const SinCos2 (&n)[8], float (&f)[16]) {
+  float p[8], r[8];
+  widen8<F16>(u, p);
+  widen8<F16>(w, r);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = interleaved ? (i < 4 ? p[2 * (i & 3)] : r[2 * (i & 3)]) : p[i];
+    const float y = interleaved ? (i < 4 ? p[2 * (i & 3) + 1] : r[2 * (i & 3) + 1]) : r[i];
+    const float a = dot_odd(x, n[i].ch, n[i].cl, -y, n[i].sh, n[i].sl), b = dot_odd(y, n[i].ch, n[i].cl, x, n[i].sh, n[i].sl);
+    if (interleaved) f[2 * i] = a, f[2 * i + 1] = b;
+    else f[i] = a, f[8 + i] = b;
   }
 }
 
@@ -312,19 +333,18 @@ __device__ __forceinline__ void append_page(const KvAppendArgs& a, const AppendP
   if (held) load();
   const int page = page_of(c, b, first, a.status);
   if (page < 0) return;
-  if (rot > 0) make_turns(a, turns, half);
+  if (rot > 0) make_turns(a, turns, half, true);
   // Angle j of a thread's item k is at [(8 k + j) * APART + tid] (apart so that neither side of it meets in a bank).
-  constexpr int APART = THREADS + 2;
-  float2* const angles = reinterpret_cast<float2*>(smem);
+  constexpr int APART = THREADS + 1;
+  SinCos2* const angles = reinterpret_cast<SinCos2*>(smem);
   if (rot > 0) {
     __syncthreads();
     if (held) {
 #pragma unroll 2
       for (int i = tid; i < n * half; i += THREADS) {
         const int r = i / half, pair = i - r * half, item = r * groups + pair / 8;
-        float sn, cs;
-        angle_sin_cos_near(turns.turn[pair], row_position(a, b, t0 + r, start, turns.axis[pair]), sn, cs);
-        angles[(item / THREADS * 8 + (pair & 7)) * APART + item % THREADS] = make_float2(sn * a.mult, cs * a.mult);
+        const SinCos2 n = angle_sin_cos_2(turns.turn[pair], row_position(a, b, t0 + r, start, turns.axis[pair]), turns.nodes, a.mult);
+        *reinterpret_cast<float4*>(angles + (item / THREADS * 8 + (pair & 7)) * APART + item % THREADS) = make_float4(n.sh, n.sl, n.ch, n.cl);
       }
       __syncthreads();
     }
@@ -340,13 +360,13 @@ __device__ __forceinline__ void append_page(const KvAppendArgs& a, const AppendP
       for (int k = 0; k < HELD; ++k) {
         if (tid + k * THREADS >= items) continue;
         if (turned[k]) {
-          float sn[8], cs[8];
+          SinCos2 n[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float2 v = angles[(k * 8 + j) * APART + tid];
-            sn[j] = v.x, cs[j] = v.y;
+            const float4 v = *reinterpret_cast<const float4*>(angles + (k * 8 + j) * APART + tid);
+            n[j] = SinCos2{v.x, v.y, v.z, v.w};
           }
-          turn16<F16>(u[k], w[k], a.interleaved != 0, sn, cs, f[k]);
+          turn16_odd<F16>(u[k], w[k], a.interleaved != 0, n, f[k]);
         } else {
           widen8<F16>(u[k], f[k]);
           widen8<F16>(w[k], f[k] + 8);
@@ -375,13 +395,10 @@ __device__ __forceinline__ void append_page(const KvAppendArgs& a, const AppendP
       __syncthreads();
       for (int i = tid; i < n * half; i += THREADS) {
         const int r = i / half, pair = i - r * half;
-        float sn, cs;
-        angle_sin_cos_near(turns.turn[pair], row_position(a, b, t0 + r, start, turns.axis[pair]), sn, cs);
-        sn *= a.mult;
-        cs *= a.mult;
+        const SinCos2 m = angle_sin_cos_2(turns.turn[pair], row_position(a, b, t0 + r, start, turns.axis[pair]), turns.nodes, a.mult);
         float* const p0 = smem + r * D + (a.interleaved ? 2 * pair : pair);
         float* const p1 = a.interleaved ? p0 + 1 : p0 + half;
-        const float z0 = *p0, z1 = *p1, y0 = z0 * cs - z1 * sn, y1 = z1 * cs + z0 * sn;
+        const float z0 = *p0, z1 = *p1, y0 = dot_odd(z0, m.ch, m.cl, -z1, m.sh, m.sl), y1 = dot_odd(z1, m.ch, m.cl, z0, m.sh, m.sl);
         *p0 = y0;
         *p1 = y1;
         amax = finite_max(finite_max(amax, y0), y1);
@@ -526,7 +543,7 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t s, int num_sms)
       pl.page_heads *= 2;
     pl.page_groups = ceil_div(c.Hkv, pl.page_heads);
     pl.quant_blocks = (int)(pages * pl.page_groups);
-    smem = !pl.held ? (size_t)rows * c.D * 4 : a.rot > 0 ? (size_t)items * 8 * (THREADS + 2) * sizeof(float2) : 0;
+    smem = !pl.held ? (size_t)rows * c.D * 4 : a.rot > 0 ? (size_t)items * 8 * (THREADS + 1) * sizeof(SinCos2) : 0;
   }
   pl.groups = c.D / (wide ? 16 : 2);
   pl.block_rows = THREADS / pl.groups;

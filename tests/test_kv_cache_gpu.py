@@ -3,7 +3,7 @@
 import pytest
 import torch
 
-from cache_reference import check_appended, positions_of, rotate, values
+from cache_reference import check_appended, code, positions_of, rotate, values
 
 pytestmark = pytest.mark.gpu
 
@@ -256,3 +256,34 @@ def test_captured_and_replayed(eight):
     for a, b in zip(cache, ref):
         assert a is None or torch.equal(a.view(torch.uint8), b.view(torch.uint8))
     sdpa.check_device_status()
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("P,D,rot,interleaved,mult", [(32, 128, 128, False, 1.0), (64, 128, 64, True, 1.25), (256, 64, 64, False, 1.0),
+                                                      (16, 80, 40, True, 1.0), (16, 16, 2, False, 0.8)])
+def test_codes_of_the_exact_rotation(io, P, D, rot, interleaved, mult):
+    """Codes are those of the rotation in 64 bits: a value as near to a tie as 2^-31 (|a| + |b|) may fall on either side
+    of it (sine and cosine are off by 2^-33 each, their products and sum by 2^-46), any other on its own."""
+    sdpa = _sdpa()
+    g = torch.Generator().manual_seed(P + rot)
+    B, S, Hkv = 2, 700, 3
+    per_row = -(-S // P)
+    cache = sdpa.kv_cache(B * per_row, Hkv, P, D, dtype=E4M3)
+    table = table_for(g, B, per_row, B * per_row)
+    k = torch.randn(B, Hkv, S, D, generator=g).to(io)
+    freq, where = sdpa.rope_inv_freq(rot), torch.randint(-50, 100000, (B, S), generator=g, dtype=torch.int32)
+    sdpa.kv_append(k.cuda(), k.cuda(), cache, table.cuda(), torch.tensor([S, S], dtype=torch.int32).cuda(), inv_freq=freq,
+                   mult=mult, interleaved=interleaved, positions=where.cuda())
+    x, size = rotate(k, freq.cpu(), positions_of([S] * B, [S] * B, S, rot // 2, where), float(torch.tensor(mult)), interleaved)
+    codes, scale = cache.k.float().double().cpu(), cache.k_scale.double().cpu()
+    differ = 0
+    for b in range(B):
+        pages = table[b].long()
+        got = codes[pages].transpose(0, 1).flatten(1, 2)[:, :S]
+        s = scale[pages].T.repeat_interleave(P, 1)[:, :S, None]
+        # (At position 0 nothing turns and a 16th of the 8-bit values are ties to 4 bits: exact, so no allowance.)
+        d = size[b] * 2.0 ** -31 * (where[b] != 0)[None, :, None]
+        low, high = code((x[b] - d) / s), code((x[b] + d) / s)
+        assert bool(((got == low) | (got == high)).all())
+        differ += (low != high).sum().item()
+    assert differ <= 2  # (of 10^5 values, each 2^-26 of its step from a tie or nearer: one in 10^7)
