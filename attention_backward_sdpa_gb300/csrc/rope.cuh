@@ -23,11 +23,9 @@ __device__ __forceinline__ void angle_sin_cos(uint64_t turn, int pos, float& sn,
   sincospif((float)(int32_t)(a >> 32) * 4.6566128730773926e-10f, &sn, &cs);  // 2^-31: half turns
 }
 
-// The same from the nearest quarter turn, so that the fp32 angle y is at most an eighth of a turn: its
-// rounding is a quarter as large. (What is rounded to e4m3 next falls on the other side of a tie less often.)
-// There the Taylor series is enough: |y| <= pi / 4, and what is left out is y^11 / 11! < 1.8e-9 of the sine and
-// y^12 / 12! < 1.2e-10 of the cosine. 30 instructions, where the library's call from any angle takes over twice as many
-// (and eight of them in line do not fit the instruction cache).
+// The same from the nearest quarter turn, where |y| <= pi / 4 and the Taylor series is short: what is left out is
+// y^11 / 11! < 1.8e-9 of the sine and y^12 / 12! < 1.2e-10 of the cosine. 30 instructions, where the library's call from
+// any angle takes over twice as many (and eight of them in line do not fit the instruction cache).
 __device__ __forceinline__ void angle_sin_cos_near(uint64_t turn, int pos, float& sn, float& cs) {
   const uint64_t a = turn * (uint64_t)(int64_t)pos;
   const uint32_t top = (uint32_t)(a >> 32), quarter = (top + (1u << 29)) >> 30;  // (3 rounded up: 4, as 0)
