@@ -76,6 +76,8 @@ def check_appended(before, after, rows, size, table, lens, new):
     touched = torch.zeros(p0.shape[0], P, dtype=torch.bool)
     for b, (n, t) in enumerate(zip(lens, new)):
         start = n - t
+        if t == 0:
+            continue
         for j0 in range(start // P * P, n, P):
             page = int(table[b, j0 // P])
             lo, hi = max(start - j0, 0), min(n - j0, P)
