@@ -6,7 +6,8 @@ Bounds, elementwise; P the exact weights, u half a step of the io type, A = P |V
                  bf16 2^-8 or fp16 2^-11; over codes fp16, to which these are widened]
                  + 2 e A [scores, in the numerator and the sum] + w 2^-31 sum |V| [weights below fp16's
                  smallest step: taken times 2^6 of a reference at most the row's largest, half a step 2^-25]
-                 (fp16 results below 2^-14: 2^-25 more; bf16 below 2^-126, where its step is 2^-133: 2^-134)
+                 (fp16 results below 2^-14: 2^-25 more; bf16 below 2^-126, where its step is 2^-133: 2^-134;
+                 beside a sink that far above, weights below fp32's normal numbers are 0: 2^-126 |v|max more)
   |LSE_gpu - LSE| <= e + 2^-19
   e = g (D + 16) max sum |q k| scale + g (|x|max + |LSE| + 8) + g slope distance + n 2^-24 + 2^-20
       g = 2^-23; n keys a row in the sum; 2^-20: exponentials and logarithms of a few units, in a chain of three
@@ -75,7 +76,8 @@ def reference(q, cache, table, lens, new, *, causal=True, window=-1, first=0, si
             w = (p * vscale[h // rep]).amax(1)
             small = w[:, None] * (see.double() @ (vh.abs() / vscale[h // rep][:, None])) * 2.0 ** -31
             o[b, h, :t], lse[b, h, :t] = out, L
-            bo[b, h, :t] += u * out.abs() + (u_p + 2 * e[:, None]) * A + small + (2.0 ** -25 if io == torch.float16 else 2.0 ** -134)
+            bo[b, h, :t] += u * out.abs() + (u_p + 2 * e[:, None]) * A + small + (2.0 ** -25 if io == torch.float16 else 2.0 ** -134) \
+                + 2.0 ** -126 * vh.abs().max()
             bl[b, h, :t] = e + 2.0 ** -19
     return o, lse, bo, bl
 
