@@ -54,6 +54,15 @@ struct CachedBounds {
   int n, nf, kt;   // units: nf tiles from 0, then n - nf from tile kt
 };
 
+// Units of 2^shift keys that hold the first `keys` of them, rounded up without passing 2^31 on the way:
+// a page table may have up to 2^31 - 16 positions. (Sums like a key's + 16 are kept on the other side of
+// their comparisons for the same reason.)
+__host__ __device__ constexpr int cached_units(int keys, int shift) { return keys > 0 ? ((keys - 1) >> shift) + 1 : 0; }
+static_assert(cached_units(0x7FFFFFF0, 7) == 1 << 24 && cached_units(0x7FFFFFF0, 5) == 1 << 26 &&
+                  cached_units(0x7FFFFF80, 7) == (1 << 24) - 1 && cached_units(129, 7) == 2 && cached_units(128, 7) == 1 &&
+                  cached_units(1, 7) == 1 && cached_units(0, 7) == 0,
+              "units");
+
 __device__ __forceinline__ CachedBounds cached_bounds(const CachedParams& p, int b, int rt) {
   CachedBounds s;
   s.L = cached_len(p.c, b);
@@ -67,10 +76,9 @@ __device__ __forceinline__ CachedBounds cached_bounds(const CachedParams& p, int
   s.k_lo = p.window_left >= 0 ? (int)max(0ll, (long long)place + i0 - p.window_left) : 0;
   s.n = s.nf = s.kt = 0;
   if (i0 > i1 || s.k_hi <= 0) return s;
-  const int up = (1 << p.tk_shift) - 1;
   s.kt = s.k_lo >> p.tk_shift;
-  s.nf = min((min(p.first_keys, s.k_hi) + up) >> p.tk_shift, s.kt);
-  s.n = s.nf + ((s.k_hi + up) >> p.tk_shift) - s.kt;
+  s.nf = min(cached_units(min(p.first_keys, s.k_hi), p.tk_shift), s.kt);
+  s.n = s.nf + cached_units(s.k_hi, p.tk_shift) - s.kt;
   return s;
 }
 __device__ __forceinline__ int cached_tile(const CachedBounds& s, int j) { return j < s.nf ? j : s.kt + (j - s.nf); }

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, NR>::CTAS) cached_rows
         for (int u = 0; u < L::GROUPS; ++u) {
           const int a = k0 + 16 * u, page = group_seen(a) ? cached_page(p, next_entry[u]) : -1;
           if (page >= 0) ok |= 1u << u;
-          const bool all = page >= 0 && a + 16 <= s.k_hi && (a >= s.k_lo || a + 16 <= p.first_keys);
+          const bool all = page >= 0 && a <= s.k_hi - 16 && (a >= s.k_lo || a <= p.first_keys - 16);
           const long long head = (long long)max(page, 0) * p.c.Hkv + w.kvh;
           const long long at = ((head << p.c.page_shift) + (a & (p.c.page - 1)) + copy_row) * row_bytes + copy_c * 16;
           const char* kb = static_cast<const char*>(p.c.k) + at;
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, NR>::CTAS) cached_rows
           }
         }
         constexpr uint32_t ALL = (1u << L::GROUPS) - 1u;
-        if (!(ok == ALL && k0 + L::KS - 1 <= hi_min && (k0 >= lo_max || k0 + L::KS <= p.first_keys))) {
+        if (!(ok == ALL && k0 + L::KS - 1 <= hi_min && (k0 >= lo_max || k0 <= p.first_keys - L::KS))) {
 #pragma unroll
           for (int ri = 0; ri < 2; ++ri)
 #pragma unroll
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(THREADS, Layout<CT, DP, NR>::CTAS) cached_rows
             }
         }
         constexpr uint32_t ALL = (1u << L::GROUPS) - 1u;
-        if (!(ok == ALL && k0 + L::KS - 1 <= hi_min && (k0 >= lo_max || k0 + L::KS <= p.first_keys))) {
+        if (!(ok == ALL && k0 + L::KS - 1 <= hi_min && (k0 >= lo_max || k0 <= p.first_keys - L::KS))) {
 #pragma unroll
           for (int ri = 0; ri < 2 * MT; ++ri)
 #pragma unroll

@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
             meta.lvs[st][lid] = __log2f(vs);
             meta.inv[st][lid] = __fdividef(1.f, vs);
           }
-          const bool full = there == 0xFFu && k0 + BK <= s.k_hi && (k0 >= s.k_lo || k0 + BK <= p.first_keys);
+          const bool full = there == 0xFFu && k0 <= s.k_hi - BK && (k0 >= s.k_lo || k0 <= p.first_keys - BK);
           const uint8_t* const from = staging + x * L::STAGING + rl * p.D + c * 16;
           uint8_t* const to = ring + st * L::TILE;
           if (in) {
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
           if (lid < 8)
             meta.at[side][x][lid] = page < 0 ? -1 : ((page * p.c.Hkv + w.kvh) << (p.c.page_shift - 4)) + ((a & (p.c.page - 1)) >> 4);
           const bool all = __all_sync(0xffffffffu, lid >= 8 || page >= 0);
-          if (lid == 0) meta.full[side][x] = all && k0 + BK <= s.k_hi && (k0 >= s.k_lo || k0 + BK <= p.first_keys);
+          if (lid == 0) meta.full[side][x] = all && k0 <= s.k_hi - BK && (k0 >= s.k_lo || k0 <= p.first_keys - BK);
         };
         int page = page_for(w.j0, entry_for(w.j0)), entry = entry_for(w.j0 + 1);
         int signalled = 0;  // tiles of this portion (and Q, before the first) that the others know of
