@@ -563,7 +563,7 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t s, int num_sms)
 cudaError_t launch_kv_gather(const KvGatherArgs& a, cudaStream_t s, int num_sms) {
   if (a.B == 0 || a.S == 0) return cudaSuccess;
   const int bh = a.B * a.c.Hkv, rows = GATHER / (a.c.D / 16);
-  const int across = (a.S + rows - 1) / rows;
+  const int across = (a.S - 1) / rows + 1;  // (S may be within `rows` of 2^31)
   const dim3 grid((unsigned)(across < num_sms * 64 ? across : num_sms * 64), (unsigned)(bh < 65535 ? bh : 65535));
   auto* kernel = a.c.f8 ? (a.f16 ? kv_gather_kernel<true, true> : kv_gather_kernel<true, false>)
                         : kv_gather_kernel<false, false>;
