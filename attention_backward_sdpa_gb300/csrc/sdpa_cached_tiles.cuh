@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(THREADS, 1) cached_tiles_kernel(const CachedPa
   using L = Layout<DP, F8>;
   constexpr int NS = L::NS;
   constexpr bool PF = F8 || F16;          // the products are fp16
-  constexpr float BIAS = F8 ? 6.f : 0.f;  // weights times 2^6: what fp16's smallest step loses is below 2^-30 of the largest
+  constexpr float BIAS = PF ? 6.f : 0.f;  // weights times 2^6: what fp16's smallest step loses is below 2^-30 of the largest
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if ((smem_u32(smem) & 1023u) != 0) {
