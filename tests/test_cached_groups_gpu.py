@@ -1,11 +1,12 @@
-"""Attention over a paged cache with weights far below a row's largest. Against the 64-bit reference, with the bounds of
-test_cached_attention_gpu.py."""
+"""Attention over a paged cache where 9 to 16 rows a key/value head (and 17 to 32 of up to 64 columns) share a tile of the
+few-rows kernel, at head dims up to 128 and with modified scores; and weights far below a row's largest. Against the 64-bit
+reference, with the bounds of test_cached_attention_gpu.py."""
 import math
 
 import pytest
 import torch
 
-from test_cached_attention_gpu import TYPES, check, reference
+from test_cached_attention_gpu import TYPES, case, check, reference
 from test_kv_cache_gpu import E4M3, on_gpu
 
 pytestmark = pytest.mark.gpu
@@ -14,6 +15,40 @@ pytestmark = pytest.mark.gpu
 def _sdpa():
     import attention_backward_sdpa_gb300 as pkg
     return pkg
+
+
+@pytest.mark.parametrize("io,eight", TYPES)
+@pytest.mark.parametrize("Hq,Hkv", [(9, 1), (12, 1), (30, 2), (48, 3)])
+@pytest.mark.parametrize("D", [80, 128])
+def test_many_heads_to_one(io, eight, Hq, Hkv, D):
+    case(io, eight, [400, 33, 1], 1, Hq, Hkv, 32, D, seed=Hq)
+
+
+@pytest.mark.parametrize("io,eight", TYPES)
+@pytest.mark.parametrize("Sq,group", [(2, 5), (4, 4), (5, 3), (16, 1)])
+@pytest.mark.parametrize("D", [80, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_a_few_queries_of_some_heads(io, eight, Sq, group, D, causal):
+    case(io, eight, [Sq, Sq + 1, 500, 333], Sq, 2 * group, 2, 16, D, seed=Sq, causal=causal)
+
+
+@pytest.mark.parametrize("io,eight", TYPES)
+@pytest.mark.parametrize("window,first", [(0, 1), (64, 16), (300, 37)])
+def test_windows(io, eight, window, first):
+    case(io, eight, [6, 250, 1111], 6, 4, 2, 64, 128, seed=window, window=window, first=first)
+
+
+@pytest.mark.parametrize("io,eight", TYPES)
+@pytest.mark.parametrize("Sq,D", [(1, 64), (4, 64), (4, 80), (5, 128), (6, 64), (10, 64), (50, 64), (50, 80)])
+@pytest.mark.parametrize("kw", [{"softcap": 20.0}, {"slopes": True}, {"softcap": 5.0, "slopes": True, "sink": True, "window": 50, "first": 3}])
+def test_modified_scores(io, eight, Sq, D, kw):
+    """3 rows a head, 12 and 15, 18 and 30, and 150."""
+    kw = dict(kw)
+    if "slopes" in kw:
+        kw["slopes"] = 2.0 ** (-torch.arange(1, 7).float())
+    if "sink" in kw:
+        kw["sink"] = torch.randn(6, generator=torch.Generator().manual_seed(Sq)) * 3
+    case(io, eight, [Sq, 200, 777], Sq, 6, 2, 16, D, seed=Sq + D, **kw)
 
 
 @pytest.mark.parametrize("io,eight", TYPES)
