@@ -515,7 +515,8 @@ int sdpa_kv_gather(int out_dtype, int cache_dtype, const void* k_cache, const vo
  * Elements of q and of visible keys and values must be finite, as in every call of this library;
  * what lies in the cache elsewhere has no effect. In 8 bits scales must be positive. Scores and sums
  * are fp32; a weight is rounded once to the type that it meets values in: the io type, or fp16 over
- * an 8-bit cache.
+ * an 8-bit cache. (Over a 16-bit cache with up to 16 rows a key/value head, 32 where D <= 64, it is taken
+ * to 2^-16 of itself.)
  * Over an 8-bit cache the result is that of the values that the codes stand for, with no further
  * rounding of them where scales are powers of two (and, for fp16, the values fp16 numbers). Results do
  * not depend on timing. o, lse and the workspace share no byte with each other or any other tensor, and

@@ -71,3 +71,22 @@ def test_weights_far_below_the_largest(io, eight, Sq):
     want = reference(q, cache, table, [n], [Sq], scale=1.0, causal=False)
     assert (want[2] < want[0].abs() / 8).all() and (want[0].abs() / 1024 < 64 * math.exp(-18)).all()
     check(got, want)
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("Sq,Hq,D", [(1, 2, 64), (1, 8, 128), (3, 8, 128), (4, 8, 64), (8, 8, 64), (5, 8, 48)])
+@pytest.mark.parametrize("n", [9, 40, 700])
+def test_weights_are_not_rounded_to_the_cache_s_type(io, Sq, Hq, D, n):
+    """Few rows over 16-bit pages: a weight counts as a rounded one and the rest of it, rounded too, off by u^2 of itself and
+    not by u, so that O is held to its own rounding where positive and negative values all but cancel. (Below fp16's
+    normal numbers what is left out is in the bound's term of small weights.)"""
+    g = torch.Generator().manual_seed(Sq + n)
+    P = 16
+    k, v = (torch.randn(-(-n // P), 2, P, D, generator=g).to(io) for _ in range(2))
+    q = torch.randn(1, Hq, Sq, D, generator=g).to(io)
+    table = torch.arange(-(-n // P), dtype=torch.int32)[None]
+    got = _sdpa().sdpa_fwd_cached(q.cuda(), on_gpu((k, v, None, None)), table.cuda(), torch.tensor([n], dtype=torch.int32).cuda())
+    o, lse, bo, bl = reference(q, (k, v, None, None), table, [n], [Sq])
+    size = reference(q, (k, v.abs(), None, None), table, [n], [Sq])[0]  # P |V|
+    u = 2.0 ** -8 if io == torch.bfloat16 else 2.0 ** -11
+    check(got, (o, lse, bo - (u - u * u) * size, bl))
