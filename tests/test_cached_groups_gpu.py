@@ -90,3 +90,33 @@ def test_weights_are_not_rounded_to_the_cache_s_type(io, Sq, Hq, D, n):
     size = reference(q, (k, v.abs(), None, None), table, [n], [Sq])[0]  # P |V|
     u = 2.0 ** -8 if io == torch.bfloat16 else 2.0 ** -11
     check(got, (o, lse, bo - (u - u * u) * size, bl))
+
+
+@pytest.mark.parametrize("io,eight", [(torch.bfloat16, False), (torch.float16, True)])
+@pytest.mark.parametrize("B,Sq", [(300, 1), (140, 6), (700, 17)])
+def test_more_sequences_than_a_block_has_threads(io, eight, B, Sq):
+    """Several entries a thread of the schedule (128 threads, or 640 of the many-rows kernel), a third of them without a key."""
+    g = torch.Generator().manual_seed(B)
+    lens = [int(n) * int(z) for n, z in zip(torch.randint(Sq, 90, (B,), generator=g), torch.randint(0, 3, (B,), generator=g) > 0)]
+    new = [min(Sq, n) for n in lens]
+    case(io, eight, lens, Sq, 2, 1, 16, 64, new=new, seed=B, window=40, first=2)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_more_row_tiles_than_a_block_has_threads(eight):
+    """One chunk of 83,000 rows a head in 649 tiles, behind a prefix; a few rows of it are checked by calls of their own."""
+    sdpa = _sdpa()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    S, P, D = 83_000, 256, 16
+    n = S + 100
+    cache = sdpa.kv_cache(-(-n // P), 1, P, D, dtype=E4M3 if eight else torch.bfloat16)
+    table = torch.arange(cache.k.shape[0], dtype=torch.int32, device="cuda").flip(0)[None].contiguous()
+    k, v, q = (torch.randn(1, 1, m, D, device="cuda", generator=g).bfloat16() for m in (n, n, S))
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    sdpa.kv_append(k, v, cache, table, lens)
+    o, lse = sdpa.sdpa_fwd_cached(q, cache, table, lens, window_left=500, first_keys=3)
+    sdpa.check_device_status()
+    held = type(cache)(*(None if t is None else t.cpu() for t in cache))
+    for i in (0, 1, 127, 128, 41_111, S - 130, S - 1):
+        want = reference(q[:, :, i: i + 1].cpu(), held, table.cpu(), [n - S + i + 1], [1], window=500, first=3)
+        check((o[:, :, i: i + 1], lse[:, :, i: i + 1]), want)
