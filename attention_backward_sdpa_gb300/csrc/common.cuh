@@ -230,8 +230,8 @@ __device__ __forceinline__ ModTile mod_tile(const ChainParams& p, const ModKey& 
   return m;
 }
 
-// Debug-bounds build (compiled with -DSDPA_DEBUG_BOUNDS): the kernels check
-// every raw-pointer global access (bulk copies, reductions, counters, direct
+// Debug-bounds build (compiled with -DSDPA_DEBUG_BOUNDS): the kernels of the forward
+// and the backward check every raw-pointer global access (bulk copies, reductions, counters, direct
 // stores) against the region it belongs to; an access outside it sets
 // STATUS_BOUNDS in the status word and is skipped, with no trap. In the normal
 // build the check is the constant true and compiles away.

@@ -92,9 +92,11 @@ CachedPlan cached_plan(long long B, int H_q, int H_kv, int S_q, int D, bool f8, 
   CachedPlan c{};
   const long long R = (long long)(H_q / H_kv) * S_q;
   // 8-row tiles of the few-rows kernel; 0: the many-rows kernel. For 17 to 32 rows of more than 64 columns that one
-  // is the faster, though its tiles are of 128: 214 us against 252 for 32 rows a head, 64 sequences of up to
-  // 8,192 keys (8 bits: 234, 246), 13.4 against 16.1 over 2,000 keys of one. Of 64 columns it is not where keys are
-  // many: 69 against 59 us over 131,072 keys, 136 against 131 for the batch (12.2 against 13.3 over 2,000).
+  // is the faster, though its tiles are of 128 and the codes' bytes would take 89 us: 214 us against 252 for 32 rows a
+  // head, 64 sequences of up to 8,192 keys (8 bits: 234, 246), 13.4 against 16.1 over 2,000 keys of one. Of 64
+  // columns it is not where keys are many: 69 against 61 us over 131,072 keys, 135 against 121 for the batch (8 bits: 72
+  // against 58, 144 against 120; over 2,000 keys 13.0 against 14.2). With 16 rows of 128 columns the few-rows kernel
+  // takes 199 against 222 us for the batch and 98 against 91 over 131,072 keys (8 bits: 127 against 234, 60 against 80).
   c.nr = R <= 8 ? 1 : R <= 16 ? 2 : R <= 32 && D <= 64 ? 4 : 0;
   c.tile_rows = c.nr ? 8 * c.nr : 128;
   c.tk = c.nr ? cached_rows_tk(f8, c.nr) : 128;

@@ -20,10 +20,13 @@
 // heads (one, or a few that share the angles) and side (K, V), since a scale is one reduction over a page and
 // head: rows to fp32, rotated, their largest value, then the codes. Both kinds run in one launch.
 // Bound by memory: 2 bytes an element read, 1 or 2 written. For few tokens it is a chain of latencies (lengths, page,
-// rows, angles; 4.1 us for 24 tokens of 32 + 8 + 8 heads, code fetched anew 9.8). For prompts it is the instructions, half
+// rows, angles; 4.1 us for 64 tokens of 32 + 8 + 8 heads, code fetched anew 9.8). For prompts it is the instructions, half
 // of the issue slots: 5 prompts of up to 1,700 tokens into 8-bit pages, 92 MB with the cache read back, take 38 us, 28
 // of them this launch (33 and 23 with sines, products and sums of fp32 alone, which put a few of 3 million codes a
-// whole step off; eight library sines a thread in line waited for their code: 39).
+// whole step off; eight library sines a thread in line waited for their code: 39). Into 16-bit pages prompts are bound by
+// memory: 4 of 8,192 tokens, 32 + 8 + 8 heads of 128 columns, take 120 us, 6.7 TB/s (8 bits: 222, 3.3 TB/s); 5 of 1,700
+// tokens, 16 + 4 + 4 heads, 20.9 us, 5.0 TB/s. Read back, 4 sequences of 8,192 positions take 43 us, 6.2 TB/s, from
+// 16 bits and 38, 5.3 TB/s, from 8.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -283,7 +286,8 @@ constexpr int HELD = 2;  // items of 16 columns that a thread keeps
 // A page's new rows of a few key/value heads of one side. `held`: a thread's items (16 columns of a row, in two
 // pieces of eight as a rotation pairs them) stay in registers from their loads to their codes, the sines and cosines
 // of its rows, which the heads share, in shared memory, and a head's loads are issued before the one before it is
-// reduced. That takes at most HELD items a thread (64 rows of 128 columns); larger pages, and rows whose
+// reduced. (Not all of it: three CTAs an SM leave 80 registers, and 96 bytes a thread, 176 with fp16 io, are stored to
+// local memory and loaded again.) That takes at most HELD items a thread (64 rows of 128 columns); larger pages, and rows whose
 // rotation or alignment does not go in pieces of eight, pass through shared memory in fp32.
 template <bool F16, int VW>
 __device__ __forceinline__ void append_page(const KvAppendArgs& a, const AppendPlan& pl, int block, float* smem, Turns& turns) {

@@ -456,7 +456,8 @@ int sdpa_rope_axes(int io_dtype, const void* q, const void* k, void* q_out, void
  * length, and a length outside [0, max_pages * page_size], are reported by
  * sdpa_bwd_check_device_status() (SDPA_ERR_PAGE). Nothing outside the buffers is touched: such
  * rows are not appended, read back as zeros, and invisible to the attention, which takes
- * a length past the table as the table's.
+ * a length past the table as the table's. (Rows that would be appended before position 0 are reported too: a
+ * batch row that is not in use has its seq_q_lens 0.) max_pages * page_size stays below 2^31.
  */
 
 /*
